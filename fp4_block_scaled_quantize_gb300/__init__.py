@@ -66,7 +66,9 @@ _lib = None
 EXPORTS = ("fp4_amax", "fp4_amax_many", "fp4_amax_stripes", "fp4_mxfp4_to_fp8",
            "fp4_mxfp4_to_fp8_transpose",
            "fp4_quantize", "fp4_quantize_transpose", "fp4_gemm", "fp4_gemm_quantize",
-           "fp4_fp8_gemm", "fp4_dequantize", "fp4_gemm_bf16", "fp4_mma_loop", "fp4_gemm_copies", "fp4_sf_bytes", "fp4_block_size", "fp4_status_sync",
+           "fp4_fp8_gemm", "fp4_dequantize", "fp4_gemm_bf16", "fp4_mma_loop", "fp4_gemm_copies",
+           "fp4_matvec", "fp4_kv_append", "fp4_decode_attention",
+           "fp4_decode_attention_workspace", "fp4_sf_bytes", "fp4_block_size", "fp4_status_sync",
            "fp4_status_string")
 
 
@@ -572,3 +574,7 @@ def gemm_quantize(a, b, amax_dev, p, remap=True, canonicalize_1024=False, stream
                              out.s_dec, out.row_shift, canonicalize_1024, stream),
            "fp4_gemm_quantize")
     return out
+
+
+# the serving operators (they build on the names above)
+from .serve import *  # noqa: E402,F401,F403

@@ -31,6 +31,9 @@ UNITS = {
     "gemm.cu": [],
     "gemm2.cu": [],
     "mmarate.cu": [],
+    "matvec.cu": [],
+    "append.cu": [],
+    "attention.cu": [],
 }
 
 

@@ -338,7 +338,131 @@ fp4_status gemm_shapes(const fp4_operand *A, const fp4_operand *B, int64_t M, in
 
 }  // namespace
 
+// ---------------------------------------------------------------- serving
+
+namespace {
+
+bool valid_type(int32_t t) { return t == FP4_BF16 || t == FP4_F16 || t == FP4_F32; }
+bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool whole8(int64_t a, int64_t b, int64_t c) { return a % 8 == 0 && b % 8 == 0 && c % 8 == 0; }
+
+fp4_status check_cache(const fp4_kv_cache &c) {
+  if (c.type != FP4_BF16 && c.type != FP4_F16) return FP4_ERR_INVALID_ARG;
+  if (c.pages < 0 || c.seqs < 0 || c.seq_pages < 0 || c.page_size < 1 || c.kv_heads < 1 ||
+      c.head_dim < 1)
+    return FP4_ERR_INVALID_ARG;
+  if (c.head_dim > 256) return FP4_ERR_SHAPE;
+  // positions are 32-bit
+  if ((int64_t)c.seq_pages * c.page_size > INT32_MAX) return FP4_ERR_SHAPE;
+  if (c.k_page < 0 || c.k_place < 0 || c.k_head < 0 || c.v_page < 0 || c.v_place < 0 ||
+      c.v_head < 0 || c.table_stride < 0)
+    return FP4_ERR_INVALID_ARG;
+  if (c.pages > 0 && (!c.k || !c.v)) return FP4_ERR_INVALID_ARG;
+  if (c.seqs > 0 && c.seq_pages > 0 && !c.table) return FP4_ERR_INVALID_ARG;
+  if (!aligned_to(c.k, 2) || !aligned_to(c.v, 2) || !aligned4(c.table)) return FP4_ERR_ALIGNMENT;
+  return FP4_OK;
+}
+
+}  // namespace
+
 extern "C" {
+
+fp4_status fp4_matvec(const fp4_operand *W, int32_t sf_layout, const void *x, int64_t x_stride,
+                      int32_t x_type, int64_t M, void *y, int64_t y_stride, int32_t y_type,
+                      void *stream) {
+  if (!W || !valid_format(W->format) || !valid_layout(sf_layout)) return FP4_ERR_INVALID_ARG;
+  if (!valid_type(x_type) || !valid_type(y_type)) return FP4_ERR_INVALID_ARG;
+  if (x_type == FP4_F32) return FP4_ERR_UNSUPPORTED;
+  const int64_t N = W->rows, K = W->k;
+  if (M < 0 || N < 0 || K < 0 || x_stride < 0 || y_stride < 0) return FP4_ERR_INVALID_ARG;
+  if (K % block_of(W->format) != 0 || K > INT32_MAX) return FP4_ERR_SHAPE;
+  if (M > 1 && (x_stride < K || y_stride < N)) return FP4_ERR_SHAPE;
+  if (W->row_shift && !(is_ue5m3_fmt(W->format) && sf_layout == FP4_SF_MMA))
+    return FP4_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return FP4_OK;
+  if (!y || !W->s_dec) return FP4_ERR_INVALID_ARG;
+  if (!aligned_to(y, y_type == FP4_F32 ? 4 : 2) || !aligned4(W->s_dec)) return FP4_ERR_ALIGNMENT;
+  if (K > 0) {
+    if (!W->q || !W->sf || !x) return FP4_ERR_INVALID_ARG;
+    if (!aligned16(W->q) || !aligned16(W->sf) || !aligned_to(x, 2)) return FP4_ERR_ALIGNMENT;
+  }
+  MatvecJob j{};
+  j.q = W->q;
+  j.sf = W->sf;
+  j.sd = W->s_dec;
+  j.shift = W->row_shift;
+  // remapped UE5M3 scales are E4M3 images; the tensor-core layout stores the
+  // block-32 control's codes once per 16 elements
+  j.kind = W->row_shift ? FP4_FMT_NVFP4_B16
+                        : (is_ue5m3_fmt(W->format) ? FP4_FMT_UE5M3_B16 : kernel_format(W->format));
+  j.block = W->format == FP4_FMT_UE5M3_B32 && sf_layout == FP4_SF_MMA ? 16 : block_of(W->format);
+  j.sf_mma = sf_layout == FP4_SF_MMA;
+  j.stripes = W->format == FP4_FMT_NVFP4_CTA;
+  j.M = M;
+  j.N = N;
+  j.K = K;
+  j.x = x;
+  j.xs = x_stride;
+  j.x_type = x_type;
+  j.y = y;
+  j.ys = y_stride;
+  j.y_type = y_type;
+  return launch_matvec(j, as_stream(stream));
+}
+
+fp4_status fp4_kv_append(const fp4_append_params *p, void *stream) {
+  if (!p) return FP4_ERR_INVALID_ARG;
+  const fp4_status st = check_cache(p->cache);
+  if (st != FP4_OK) return st;
+  if (p->tokens < 0 || p->rope_len < 0 || p->rot_dim < 0) return FP4_ERR_INVALID_ARG;
+  if (p->k_token < 0 || p->k_head < 0 || p->v_token < 0 || p->v_head < 0) return FP4_ERR_INVALID_ARG;
+  if (p->rot_dim % 2 != 0 || p->rot_dim > p->cache.head_dim || p->tokens > INT32_MAX)
+    return FP4_ERR_SHAPE;
+  if (p->q) {
+    if (!p->q_out || p->heads < 1 || p->q_token < 0 || p->q_head < 0 || p->qo_token < 0 ||
+        p->qo_head < 0)
+      return FP4_ERR_INVALID_ARG;
+    if (p->heads % p->cache.kv_heads != 0) return FP4_ERR_SHAPE;
+    if (!aligned_to(p->q, 2) || !aligned_to(p->q_out, 2)) return FP4_ERR_ALIGNMENT;
+  }
+  if (p->tokens == 0) return FP4_OK;
+  if (!p->k || !p->v || !p->pos || (p->rot_dim > 0 && p->rope_len > 0 && !p->rope))
+    return FP4_ERR_INVALID_ARG;
+  if (!aligned_to(p->k, 2) || !aligned_to(p->v, 2) || !aligned4(p->pos) || !aligned4(p->seq) ||
+      !aligned4(p->rope))
+    return FP4_ERR_ALIGNMENT;
+  return launch_kv_append(*p, as_stream(stream));
+}
+
+int64_t fp4_decode_attention_workspace(int32_t seqs, int32_t heads, int32_t kv_heads,
+                                       int32_t head_dim) {
+  if (seqs < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || head_dim < 1 ||
+      head_dim > 256 || head_dim % 8 != 0)
+    return -1;
+  return seqs == 0 ? 0 : decode_attention_workspace(heads, kv_heads, head_dim);
+}
+
+fp4_status fp4_decode_attention(const fp4_attention_params *p, void *stream) {
+  if (!p) return FP4_ERR_INVALID_ARG;
+  const fp4_kv_cache &c = p->cache;
+  const fp4_status st = check_cache(c);
+  if (st != FP4_OK) return st;
+  if (p->heads < 1 || p->window < 0 || p->q_seq < 0 || p->q_head < 0 || p->out_seq < 0 ||
+      p->out_head < 0)
+    return FP4_ERR_INVALID_ARG;
+  if (p->heads % c.kv_heads != 0 || c.head_dim % 8 != 0) return FP4_ERR_SHAPE;
+  if (c.seqs == 0) return FP4_OK;
+  if (!p->lengths || !p->q || !p->out) return FP4_ERR_INVALID_ARG;
+  if (!aligned4(p->lengths) || !aligned4(p->lse) || !aligned_to(p->out, 2)) return FP4_ERR_ALIGNMENT;
+  if (!aligned16(p->q) || !aligned16(c.k) || !aligned16(c.v) || p->q_seq % 8 != 0 ||
+      p->q_head % 8 != 0 || !whole8(c.k_page, c.k_place, c.k_head) ||
+      !whole8(c.v_page, c.v_place, c.v_head))
+    return FP4_ERR_ALIGNMENT;
+  const int64_t need = fp4_decode_attention_workspace(c.seqs, p->heads, c.kv_heads, c.head_dim);
+  if (need > 0 && (!p->workspace || p->workspace_bytes < need)) return FP4_ERR_INVALID_ARG;
+  if (!aligned16(p->workspace)) return FP4_ERR_ALIGNMENT;
+  return launch_decode_attention(*p, as_stream(stream));
+}
 
 fp4_status fp4_gemm(const fp4_operand *A, const fp4_operand *B, int64_t M, int64_t N, int64_t K,
                     void *D, int32_t d_is_bf16, int32_t canonicalize_1024, void *stream) {
@@ -426,6 +550,7 @@ fp4_status fp4_status_sync(void *stream) {
   if (v & kStatusTimeout) return FP4_ERR_TIMEOUT;
   if (v & kStatusNonfinite) return FP4_ERR_NONFINITE;
   if (v & kStatusScaleWindow) return FP4_ERR_SCALE_WINDOW;
+  if (v & kStatusIndex) return FP4_ERR_INVALID_ARG;
   return FP4_OK;
 }
 

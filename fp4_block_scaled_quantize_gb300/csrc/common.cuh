@@ -12,6 +12,7 @@ enum : uint32_t {
   kStatusTimeout = 1u << 0,
   kStatusNonfinite = 1u << 1,
   kStatusScaleWindow = 1u << 2,
+  kStatusIndex = 1u << 3,  // an index given on the device lies outside its table
 };
 
 // Device address of the status word on the current device (set up on first
@@ -168,5 +169,24 @@ fp4_status launch_gemm_pair(const GemmJob &j, cudaStream_t s);
 // padding); defined in gemm.cu.
 struct QoutParams;
 fp4_status qout_params(const GemmJob &j, QoutParams &o, cudaStream_t s);
+
+// Product of a 4-bit copy with 16-bit activations for few tokens; K > 0.
+struct MatvecJob {
+  const uint8_t *q, *sf;
+  const float *sd;
+  const int8_t *shift;  // nullptr: none
+  int kind;             // kUE5M3, kNVFP4 or kMXFP4: how a scale code reads
+  int block;            // elements per scale code as stored (16 or 32)
+  int sf_mma, stripes;
+  int64_t M, N, K, xs, ys;
+  const void *x;
+  void *y;
+  int x_type, y_type;
+};
+fp4_status launch_matvec(const MatvecJob &j, cudaStream_t s);
+fp4_status launch_kv_append(const fp4_append_params &p, cudaStream_t s);
+fp4_status launch_decode_attention(const fp4_attention_params &p, cudaStream_t s);
+// Bytes of partial results launch_decode_attention may write.
+int64_t decode_attention_workspace(int heads, int kv_heads, int head_dim);
 
 }  // namespace fp4

@@ -1,0 +1,313 @@
+"""Serving operators: products of 4-bit weights with a few tokens, a paged
+cache of keys and values, and attention of one new token per sequence over it.
+
+``fp4_*`` functions keep the C names and return a status code; ``matvec``,
+``kv_append`` and ``decode_attention`` check their tensors, allocate outputs
+and raise.  All of them only marshal arguments: the work is done by the
+library's CUDA kernels.  An output or workspace that a function allocates for
+a given ``stream`` belongs to that stream.
+
+Host time counts here (a call's kernels run for a few microseconds), so the
+parameter structs are packed by ``struct`` in the layout of the ctypes
+classes instead of being filled field by field.
+"""
+import ctypes
+import struct
+from contextlib import nullcontext
+
+import torch
+
+from . import (FP4_FMT_UE5M3_B16, FP4_FMT_UE5M3_B32, FP4_SF_MMA, _check, _stream, fp4_operand,
+               fp4_sf_bytes, lib, n_stripes, FP4_FMT_NVFP4_CTA)
+
+FP4_BF16, FP4_F16, FP4_F32 = 0, 1, 2
+_TYPES = {torch.bfloat16: FP4_BF16, torch.float16: FP4_F16, torch.float32: FP4_F32}
+_HALVES = (torch.bfloat16, torch.float16)
+
+
+class fp4_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_page", ctypes.c_int64),
+                ("k_place", ctypes.c_int64), ("k_head", ctypes.c_int64), ("v_page", ctypes.c_int64),
+                ("v_place", ctypes.c_int64), ("v_head", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("seqs", ctypes.c_int32), ("seq_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
+class fp4_append_params(ctypes.Structure):
+    _fields_ = [("cache", fp4_kv_cache), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k_token", ctypes.c_int64),
+                ("k_head", ctypes.c_int64), ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64),
+                ("q_token", ctypes.c_int64), ("q_head", ctypes.c_int64),
+                ("qo_token", ctypes.c_int64), ("qo_head", ctypes.c_int64), ("pos", ctypes.c_void_p),
+                ("seq", ctypes.c_void_p), ("rope", ctypes.c_void_p), ("rope_len", ctypes.c_int64),
+                ("tokens", ctypes.c_int64), ("heads", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class fp4_attention_params(ctypes.Structure):
+    _fields_ = [("cache", fp4_kv_cache), ("lengths", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("q_seq", ctypes.c_int64),
+                ("q_head", ctypes.c_int64), ("out_seq", ctypes.c_int64), ("out_head", ctypes.c_int64),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+_CACHE = "PPqqqqqqPqqiiiiii"
+_APPEND = struct.Struct("@" + _CACHE + "PPPPqqqqqqqqPPPqqiii4x")
+_ATTENTION = struct.Struct("@" + _CACHE + "PPPPqqqqPqiif4x")
+
+_entry = None
+
+
+def _lib():
+    """The library with the argument types of this module's entry points."""
+    global _entry
+    if _entry is None:
+        L = lib()
+        vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+        L.fp4_matvec.argtypes = [vp, i32, vp, i64, i32, i64, vp, i64, i32, vp]
+        L.fp4_kv_append.argtypes = [vp, vp]
+        L.fp4_decode_attention.argtypes = [vp, vp]
+        L.fp4_decode_attention_workspace.argtypes = [i32, i32, i32, i32]
+        for f in ("fp4_matvec", "fp4_kv_append", "fp4_decode_attention"):
+            getattr(L, f).restype = i32
+        L.fp4_decode_attention_workspace.restype = i64
+        _entry = L
+    return _entry
+
+
+# ------------------------------------------------------------- raw entry points
+
+def fp4_matvec(W, sf_layout, x, x_stride, x_type, M, y, y_stride, y_type, stream=None):
+    return _lib().fp4_matvec(ctypes.byref(W), sf_layout, x.data_ptr(), x_stride, x_type, M,
+                             y.data_ptr(), y_stride, y_type, _stream(stream))
+
+
+def fp4_kv_append(p, stream=None):
+    """p: an fp4_append_params, or the same bytes packed."""
+    return _lib().fp4_kv_append(p if isinstance(p, bytes) else ctypes.byref(p), _stream(stream))
+
+
+def fp4_decode_attention(p, stream=None):
+    """p: an fp4_attention_params, or the same bytes packed."""
+    return _lib().fp4_decode_attention(p if isinstance(p, bytes) else ctypes.byref(p),
+                                       _stream(stream))
+
+
+def fp4_decode_attention_workspace(seqs, heads, kv_heads, head_dim):
+    return _lib().fp4_decode_attention_workspace(seqs, heads, kv_heads, head_dim)
+
+
+# ------------------------------------------------------ allocating conveniences
+
+def _on(stream):
+    """Context in which outputs for work on `stream` are allocated."""
+    return nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _device(where, first, *rest):
+    """The one CUDA device of the tensors; it has to be the current one,
+    because that is where kernels are launched."""
+    dev = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: tensors must share one device")
+    if dev < 0:
+        raise ValueError(f"{where}: tensors must be on a CUDA device")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{where}: the tensors' device is not the current one")
+    return first.device
+
+
+def matvec(x, w, out_dtype=None, out=None, stream=None):
+    """y = x W^T for a few tokens: x [M, K] or [K] in bfloat16 or float16
+    (rows may be strided), w a Quantized copy [N, K] in either scale layout.
+    y is [M, N] (or [N]) in out_dtype -- x's dtype by default, or bfloat16,
+    float16 or float32 -- or written to `out` (rows may be strided).  The
+    activations are not quantised; see fp4_matvec in include/fp4.h."""
+    if x.dtype not in _HALVES:
+        raise ValueError("matvec: x must be bfloat16 or float16")
+    dim = x.dim()
+    if dim != 1 and dim != 2:
+        raise ValueError("matvec: x must be [K] or [M, K]")
+    q, sf, s_dec, shift = w.q, w.sf, w.s_dec, w.row_shift
+    N, K = w.rows, w.k
+    if x.shape[-1] != K:
+        raise ValueError(f"matvec: x has {x.shape[-1]} columns, the weight {K}")
+    M = x.shape[0] if dim == 2 else 1
+    if K > 1 and x.stride(-1) != 1:
+        raise ValueError("matvec: the last dimension of x must be contiguous")
+    if not (q.is_contiguous() and sf.is_contiguous() and s_dec.is_contiguous()
+            and (shift is None or shift.is_contiguous())):
+        raise ValueError("matvec: the weight copy is not contiguous")
+    if sf.numel() < fp4_sf_bytes(w.format, N, K, w.sf_layout) or \
+            s_dec.numel() < (n_stripes(N) if w.format == FP4_FMT_NVFP4_CTA else 1) or \
+            s_dec.dtype != torch.float32 or q.dtype != torch.uint8 or sf.dtype != torch.uint8:
+        raise ValueError("matvec: the weight copy's scales do not fit its format and layout")
+    if shift is not None and (w.format not in (FP4_FMT_UE5M3_B16, FP4_FMT_UE5M3_B32)
+                              or w.sf_layout != FP4_SF_MMA or shift.numel() < N
+                              or shift.dtype != torch.int8):
+        raise ValueError("matvec: row shifts belong to UE5M3 copies in the tensor-core layout")
+    device = _device("matvec", x, q, sf, s_dec, shift, out)
+    shape = (M, N) if dim == 2 else (N,)
+    if out is None:
+        dtype = x.dtype if out_dtype is None else out_dtype
+        if dtype not in _TYPES:
+            raise ValueError("matvec: out_dtype must be bfloat16, float16 or float32")
+        with _on(stream):
+            out = torch.empty(shape, dtype=dtype, device=device)
+    elif out.dtype not in _TYPES or tuple(out.shape) != shape or (N > 1 and out.stride(-1) != 1) or \
+            (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"matvec: out must be a {list(shape)} tensor with contiguous rows, in "
+                         "bfloat16, float16 or float32")
+    op = fp4_operand(q.data_ptr(), sf.data_ptr(), s_dec.data_ptr(),
+                     None if shift is None else shift.data_ptr(), w.format, N, K)
+    _check(fp4_matvec(op, w.sf_layout, x, x.stride(0) if M > 1 else K, _TYPES[x.dtype], M, out,
+                      out.stride(0) if M > 1 else N, _TYPES[out.dtype], stream), "fp4_matvec")
+    return out
+
+
+def _steps(where, name, t, sizes):
+    """Strides of the dimensions before the last of a tensor of these sizes
+    (0 along a dimension of one: it is never stepped along)."""
+    if tuple(t.shape) != sizes:
+        raise ValueError(f"{where}: {name} must be {list(sizes)}, not {list(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and sizes[-1] > 1:
+        raise ValueError(f"{where}: the last dimension of {name} must be contiguous")
+    return [0 if n == 1 else s for n, s in zip(sizes[:-1], st)]
+
+
+def _cache_fields(where, k_pages, v_pages, page_table):
+    """The fields of fp4_kv_cache, in order."""
+    dtype = k_pages.dtype
+    if dtype not in _HALVES or v_pages.dtype != dtype:
+        raise ValueError(f"{where}: keys and values must both be bfloat16 or both float16")
+    if k_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError(f"{where}: k_pages must be [pages, page_size, kv_heads, head_dim], "
+                         "page_table [seqs, pages of a sequence]")
+    if page_table.dtype != torch.int32:
+        raise ValueError(f"{where}: page_table must be int32")
+    sizes = tuple(k_pages.shape)
+    seqs, seq_pages = page_table.shape
+    if seq_pages > 1 and page_table.stride(1) != 1:
+        raise ValueError(f"{where}: the rows of page_table must be contiguous")
+    if 0 in sizes[1:]:
+        raise ValueError(f"{where}: pages without places, heads or elements")
+    return (k_pages.data_ptr(), v_pages.data_ptr(), *_steps(where, "k_pages", k_pages, sizes),
+            *_steps(where, "v_pages", v_pages, sizes), page_table.data_ptr(),
+            page_table.stride(0) if seqs > 1 else 0, sizes[0], seqs, seq_pages, sizes[1], sizes[2],
+            sizes[3], _TYPES[dtype])
+
+
+def _need_ints(where, name, t, n):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{where}: {name} must be a contiguous int32 tensor of {n}")
+
+
+def kv_append(k, v, k_pages, v_pages, page_table, pos, seq=None, q=None, rope=None,
+              interleaved=False, q_out=None, stream=None):
+    """Writes the keys k and values v [tokens, kv_heads, head_dim] of new
+    tokens into a paged cache (k_pages, v_pages [pages, page_size, kv_heads,
+    head_dim], any strides; page_table [seqs, pages of a sequence] int32) at
+    positions pos [tokens] int32 of sequences seq [tokens] int32 (default:
+    token t is the new token of sequence t).  With rope [positions, rot_dim]
+    float32 (rope_table) keys and queries q [tokens, heads, head_dim] are
+    rotated on the way.  Returns the rotated queries (q_out, new by default),
+    or None without q.  Tokens at negative positions are skipped."""
+    where = "kv_append"
+    cache = _cache_fields(where, k_pages, v_pages, page_table)
+    dtype, Hk, D = k_pages.dtype, k_pages.shape[2], k_pages.shape[3]
+    T = k.shape[0]
+    if k.dtype != dtype or v.dtype != dtype or (q is not None and q.dtype != dtype):
+        raise ValueError(f"{where}: q, k, v and the cache must share one dtype")
+    ks, vs = _steps(where, "k", k, (T, Hk, D)), _steps(where, "v", v, (T, Hk, D))
+    _need_ints(where, "pos", pos, T)
+    if seq is not None:
+        _need_ints(where, "seq", seq, T)
+    elif T > page_table.shape[0]:
+        raise ValueError(f"{where}: more tokens than sequences; give seq")
+    rot_dim = rope_len = 0
+    if rope is not None:
+        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+            raise ValueError(f"{where}: rope must be a contiguous [positions, rot_dim] float32 tensor")
+        rope_len, rot_dim = rope.shape
+    heads, qs, os_ = 0, (0, 0), (0, 0)
+    device = _device(where, k, v, k_pages, v_pages, page_table, pos, seq, q, rope, q_out)
+    if q is not None:
+        heads = q.shape[1] if q.dim() == 3 else 0
+        if heads < 1 or heads % Hk:
+            raise ValueError(f"{where}: q must be [tokens, heads, head_dim], heads a multiple of {Hk}")
+        qs = _steps(where, "q", q, (T, heads, D))
+        if q_out is None:
+            with _on(stream):
+                q_out = torch.empty((T, heads, D), dtype=dtype, device=device)
+        elif q_out.dtype != dtype:
+            raise ValueError(f"{where}: q_out must have q's dtype")
+        os_ = _steps(where, "q_out", q_out, (T, heads, D))
+    elif q_out is not None:
+        raise ValueError(f"{where}: q_out without q")
+    p = _APPEND.pack(*cache, k.data_ptr(), v.data_ptr(), q.data_ptr() if q is not None else 0,
+                     q_out.data_ptr() if q is not None else 0, *ks, *vs, *qs, *os_, pos.data_ptr(),
+                     seq.data_ptr() if seq is not None else 0,
+                     rope.data_ptr() if rope is not None else 0, rope_len, T, heads, rot_dim,
+                     1 if interleaved else 0)
+    _check(fp4_kv_append(p, stream), "fp4_kv_append")
+    return q_out
+
+
+def decode_attention(q, k_pages, v_pages, page_table, lengths, scale=None, window=0, out=None,
+                     return_lse=False, stream=None):
+    """Attention of one new token per sequence, q [seqs, heads, head_dim],
+    over a paged cache (as in kv_append) that holds lengths [seqs] int32
+    positions of each sequence, the new one among them.  scale defaults to
+    head_dim ** -0.5; window > 0 sees the newest `window` positions only.
+    Returns [seqs, heads, head_dim] in q's dtype (or `out`), and with
+    return_lse also the logarithm of each row's sum of exponentials, float32
+    [seqs, heads].  A sequence of length 0 gives zeros (and -inf)."""
+    where = "decode_attention"
+    cache = _cache_fields(where, k_pages, v_pages, page_table)
+    dtype, Hk, D = k_pages.dtype, k_pages.shape[2], k_pages.shape[3]
+    seqs = page_table.shape[0]
+    heads = q.shape[1] if q.dim() == 3 else 0
+    if q.dtype != dtype or heads < 1 or heads % Hk:
+        raise ValueError(f"{where}: q must be [seqs, heads, head_dim] in the cache's dtype, heads a "
+                         f"multiple of {Hk}")
+    shape = (seqs, heads, D)
+    qs = _steps(where, "q", q, shape)
+    _need_ints(where, "lengths", lengths, seqs)
+    if window < 0 or window > 0x7FFFFFFF:
+        raise ValueError(f"{where}: window must be >= 0")
+    device = _device(where, q, k_pages, v_pages, page_table, lengths, out)
+    need = fp4_decode_attention_workspace(seqs, heads, Hk, D)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=device)
+        elif out.dtype != dtype:
+            raise ValueError(f"{where}: out must have q's dtype")
+        lse = torch.empty((seqs, heads), dtype=torch.float32, device=device) if return_lse else None
+        work = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+    p = _ATTENTION.pack(*cache, lengths.data_ptr(), q.data_ptr(), out.data_ptr(),
+                        0 if lse is None else lse.data_ptr(), *qs, *_steps(where, "out", out, shape),
+                        0 if work is None else work.data_ptr(), max(need, 0), heads, window,
+                        D ** -0.5 if scale is None else scale)
+    _check(fp4_decode_attention(p, stream), "fp4_decode_attention")
+    return (out, lse) if return_lse else out
+
+
+def rope_table(positions, rot_dim, base=10000.0, device="cuda"):
+    """cos and sin of the rotation of each position, float32 [positions,
+    rot_dim]: cos(p base^(-2 i / rot_dim)) in column i, the sine rot_dim / 2
+    columns on (angles and functions in 64 bits, rounded once)."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rope_table: rot_dim must be even")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    angle = torch.arange(positions, dtype=torch.float64)[:, None] * base ** (-2.0 * i / rot_dim)
+    return torch.cat([torch.cos(angle), torch.sin(angle)], -1).float().to(device)
+
+
+__all__ = ["FP4_BF16", "FP4_F16", "FP4_F32", "fp4_append_params", "fp4_attention_params",
+           "fp4_decode_attention", "fp4_decode_attention_workspace", "fp4_kv_append",
+           "fp4_kv_cache", "fp4_matvec", "decode_attention", "kv_append", "matvec", "rope_table"]

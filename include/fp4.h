@@ -353,6 +353,117 @@ fp4_status fp4_mma_loop(int32_t kind, int64_t iters, void *stream);
 fp4_status fp4_gemm_copies(const fp4_operand *A, const fp4_operand *B, int64_t M, int64_t N,
                            int64_t K, void *stream);
 
+/* ---------------------------------------------------------------- serving
+ * The operators that answer with a model, token by token, on the copies
+ * above: a product with 4-bit weights and 16-bit activations for a few
+ * tokens, a paged cache of keys and values, and attention of one new token
+ * per sequence over it.  They are this library's own; no page describes
+ * them.  Strides are in elements; every sum, softmax statistic and rotation
+ * is held in binary32 and rounded once, where it is stored. */
+typedef enum { FP4_BF16 = 0, FP4_F16 = 1, FP4_F32 = 2 } fp4_type;
+
+/* Product with a 4-bit weight for few tokens:
+ *   y[m][n] = s_dec * 2^row_shift[n] *
+ *             sum_b dec(sf[n][b]) * sum_{k in block b} e2m1(q[n][k]) x[m][k]
+ * x stays in 16 bits (x_type FP4_BF16 or FP4_F16) -- it is not quantised, as
+ * the operands of fp4_gemm are.  y_type is FP4_BF16, FP4_F16 or FP4_F32.
+ * W is a row-wise copy with W->rows = N rows of W->k = K elements and scales
+ * in either layout, so one weight copy serves the GEMMs and this product:
+ * PLAIN (row_shift must be NULL) or MMA (UE5M3: with row_shift, sf holds the
+ * E4M3 images of the remap; without, UE5M3 codes).  Every format; NVFP4_CTA
+ * reads one s_dec per 128 rows.  Scale codes that no producer emits (UE5M3
+ * above 0xF7, E4M3 0x7F, E8M0 255) give unspecified values.
+ * Accuracy: x is held exactly for magnitudes down to 2^-32 of the largest in
+ * its token's 128 columns, MXFP4 block scales down to 2^-35 of the largest in
+ * a row's 128 columns; smaller ones round towards zero contribution.
+ * Shapes: any M, N >= 0; K % B == 0; K == 0 writes zeros.  The weight is read
+ * once per 16 tokens; from some hundred tokens on the GEMMs are the faster
+ * route.  x_stride >= K and y_stride >= N, when there is more than one row.
+ * Alignment: q and sf 16 bytes, x and y their element size. */
+fp4_status fp4_matvec(const fp4_operand *W, int32_t sf_layout, const void *x, int64_t x_stride,
+                      int32_t x_type, int64_t M, void *y, int64_t y_stride, int32_t y_type,
+                      void *stream);
+
+/* A paged cache of keys and values.  Position p of sequence s lies in page
+ * table[s * table_stride + p / page_size], at place p % page_size.  Keys and
+ * values are indexed [page][place][kv_head][dim] with strides of their own,
+ * so pages may hold places or heads outermost.  Table entries that no call
+ * needs are not looked at. */
+typedef struct {
+  void *k, *v;                       /* head_dim contiguous elements per head  */
+  int64_t k_page, k_place, k_head;   /* strides of k                           */
+  int64_t v_page, v_place, v_head;   /* strides of v                           */
+  const int32_t *table;              /* [seqs][seq_pages] page numbers         */
+  int64_t table_stride;
+  int64_t pages;                     /* pages in the cache                     */
+  int32_t seqs, seq_pages;           /* sequences; table entries of each       */
+  int32_t page_size;                 /* places per page, >= 1                  */
+  int32_t kv_heads, head_dim;        /* 1 <= head_dim <= 256                   */
+  int32_t type;                      /* FP4_BF16 or FP4_F16: cache, q, k, v    */
+} fp4_kv_cache;
+
+/* Appends the keys and values of `tokens` tokens to the cache and rotates
+ * keys and (if q is given) queries by their positions on the way:
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * over the first rot_dim elements of a head, pairs (i, i + rot_dim / 2), or
+ * (2i, 2i + 1) if interleaved; the rest and the values are copied.  cos and
+ * sin of position p are rope[p][0 .. rot_dim/2) and rope[p][rot_dim/2 ..
+ * rot_dim), p < rope_len.  Token t belongs to sequence seq[t] (seq NULL:
+ * sequence t, one new token of each) and has position pos[t].
+ * A token with pos < 0 is skipped: nothing is stored for it and its q_out row
+ * is zero.  A token whose sequence, position, rotation entry or page lies
+ * outside its table is treated the same, and fp4_status_sync reports
+ * FP4_ERR_INVALID_ARG.  Two tokens of one place: either may stay.
+ * q_out may be q (same strides).  rot_dim == 0: no rotation (rope may be
+ * NULL).  Shapes: rot_dim even, <= head_dim; heads % kv_heads == 0.
+ * Alignment: element size (16-byte pieces are used where all allow it). */
+typedef struct {
+  fp4_kv_cache cache;
+  const void *k, *v, *q;             /* [tokens][heads][head_dim]; q nullable  */
+  void *q_out;
+  int64_t k_token, k_head, v_token, v_head, q_token, q_head, qo_token, qo_head;
+  const int32_t *pos, *seq;          /* [tokens]; seq nullable                 */
+  const float *rope;                 /* [rope_len][rot_dim]                    */
+  int64_t rope_len;
+  int64_t tokens;
+  int32_t heads;                     /* of q                                   */
+  int32_t rot_dim, interleaved;
+} fp4_append_params;
+fp4_status fp4_kv_append(const fp4_append_params *p, void *stream);
+
+/* Attention of one new token per sequence over the cache:
+ *   out[s][h] = sum_j w_j v_j,  w = softmax_j(scale * q[s][h] . k_j)
+ * over positions j in [max(0, L - window), L) with L = lengths[s] (window 0:
+ * all); query head h reads key head h / (heads / kv_heads).  L = 0 gives
+ * zeros.  lse (nullable, [seqs][heads]) receives log sum_j exp(scale q . k_j),
+ * -inf for L = 0, so that results over parts of a cache can be joined.
+ * Positions that are not seen are never read: what lies there, NaN included,
+ * has no effect.  A length above seq_pages * page_size is cut to it, a page
+ * outside the cache is passed over, a negative length is read as 0, and
+ * fp4_status_sync reports FP4_ERR_INVALID_ARG.
+ * workspace: fp4_decode_attention_workspace() bytes, 16-byte aligned, read
+ * and written by this call only (one per call in flight).
+ * Alignment: every stride, pointer and head_dim of q, k, v in multiples of 16
+ * bytes (8 elements); out its element size. */
+typedef struct {
+  fp4_kv_cache cache;
+  const int32_t *lengths;            /* [seqs]                                 */
+  const void *q;                     /* [seqs][heads][head_dim]                */
+  void *out;
+  float *lse;
+  int64_t q_seq, q_head, out_seq, out_head;
+  void *workspace;
+  int64_t workspace_bytes;
+  int32_t heads, window;
+  float scale;
+} fp4_attention_params;
+fp4_status fp4_decode_attention(const fp4_attention_params *p, void *stream);
+
+/* Workspace of fp4_decode_attention in bytes on the current device, whatever
+ * the lengths; -1 for sizes it refuses. */
+int64_t fp4_decode_attention_workspace(int32_t seqs, int32_t heads, int32_t kv_heads,
+                                       int32_t head_dim);
+
 /* Bytes of one scale-factor output for a copy with `rows` rows and `cols`
  * elements per row; -1 for an invalid format/layout. */
 int64_t fp4_sf_bytes(int32_t format, int64_t rows, int64_t cols,
