@@ -376,9 +376,11 @@ typedef enum { FP4_BF16 = 0, FP4_F16 = 1, FP4_F32 = 2 } fp4_type;
  * Accuracy: x is held exactly for magnitudes down to 2^-32 of the largest in
  * its token's 128 columns, MXFP4 block scales down to 2^-35 of the largest in
  * a row's 128 columns; smaller ones round towards zero contribution.
- * Shapes: any M, N >= 0; K % B == 0; K == 0 writes zeros.  The weight is read
- * once per 16 tokens; from some hundred tokens on the GEMMs are the faster
- * route.  x_stride >= K and y_stride >= N, when there is more than one row.
+ * MXFP4 sums of 128 columns must stay below 2^128 before their row's largest
+ * block scale is applied: |x| up to 2^100 is safe.
+ * Shapes: any M, N >= 0; K % B == 0 and K <= 2^19; K == 0 writes zeros.  The
+ * weight is read once per 16 tokens; from some hundred tokens on the GEMMs
+ * are the faster route.  x_stride >= K and y_stride >= N, when there is more than one row.
  * Alignment: q and sf 16 bytes, x and y their element size. */
 fp4_status fp4_matvec(const fp4_operand *W, int32_t sf_layout, const void *x, int64_t x_stride,
                       int32_t x_type, int64_t M, void *y, int64_t y_stride, int32_t y_type,
