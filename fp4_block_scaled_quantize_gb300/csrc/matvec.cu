@@ -10,35 +10,40 @@
 // all but M columns of work are padding.)
 //
 // Mathematics.  E2M1 has 2 significant bits, a block scale at most 4, so
-// e2m1 * dec(sf) 2^c is exact in f16 for the constant c below (E4M3: 2^-8,
-// UE5M3: 2^-3, smallest product 2^-18 and 2^-21, largest 10.5 and 46,080).
-// E8M0 scales span more than f16: per row and 128 columns they are taken
-// relative to the largest of the four (2^13 at most, exact 36 binades down)
+// e2m1 * dec(sf) is exact in f16 for E4M3 (2^-10 .. 2,688) and times 2^-3 for
+// UE5M3 (2^-21 .. 46,080).
+// E8M0 scales span more than f16: per row and 256 columns they are taken
+// relative to the largest of the eight (2^13 at most, exact 36 binades down)
 // and the largest is applied in binary32.  A BF16 x is multiplied per token
-// and 128 columns by the power of two that puts its largest magnitude in
+// and 256 columns by the power of two that puts its largest magnitude in
 // [2^15, 2^16): 8 significant bits stay exact in f16 for 32 binades below
-// it.  Products are exact, the MMA adds 128 columns in binary32, and these
+// it.  Products are exact, the MMA adds 256 columns in binary32, and these
 // sums are multiplied by the power(s) of two and added in binary32 with
 // nearest rounding.
 //
-// Layout.  A warp takes 16 weight rows and 128 columns a step.  The order of
+// Layout.  A warp takes 16 weight rows and 256 columns a step.  The order of
 // k within an MMA is free as long as both operands share it: lane (g, t)
-// loads 16 bytes (32 weights) of rows g and g + 8 from column 32 t on --
-// a whole 16-byte load per row and no exchange between lanes -- and MMA j of
-// eight takes its weights 4 j .. 4 j + 3.  x lies in shared memory as f16,
-// each 128-column chunk with its 16-byte pieces in the order (i, t), so that
-// four lanes read 64 contiguous bytes; the token pitch is 64 mod 128 bytes,
-// so the two tokens of a quarter-warp use different banks.
+// takes columns 64 t .. 64 t + 63 of rows g and g + 8, four 16-byte pieces of
+// payload and the four scale codes over 64 columns of each row -- whole loads
+// and no exchange between lanes -- and each MMA four of its weights.  A step's payload is one
+// TMA box of 16 rows x 128 bytes in the 128-byte swizzle (rows g, g + 1 of a
+// quarter-warp then read different banks); x lies in shared memory as f16,
+// the 16-byte pieces of 256 columns in the order (piece of the lane, t), so
+// that four lanes read 64 contiguous bytes, tokens 64 mod 128 bytes apart.
 //
-// Split.  One CTA of 16 warps per SM keeps 64 KB of weight loads in flight
-// (4 steps a warp, requested before x is prepared and across tiles).  The
-// CTA holds x for its K range; SK of its warps share one row tile along K,
-// and a cluster of S CTAs splits K where x for all of it does not fit.  The
-// parts are added in shared memory (over the cluster: distributed) in a
-// fixed order.
+// Split.  One CTA of 16 warps per SM; each warp runs its own ring of 2 to 4
+// stages (payload by TMA, scale words by 4-byte cp.async, one mbarrier), so
+// that 64 KB or more of weights are in flight per SM across tiles and before
+// x is ready, and no warp waits for another inside a tile.  The CTA holds x
+// for its K range; sk of its warps share a row tile along K, and a cluster
+// of S CTAs splits K where x for all of it does not fit.  The parts are
+// added in shared memory (over the cluster: distributed) in a fixed order.
+// A row pitch that is not a multiple of 16 bytes (K / 16 odd) is no TMA
+// stride: the ring is then filled by 8-byte cp.async.
 #include <cooperative_groups.h>
 
 #include "serve.cuh"
+#include "tcgen05.cuh"
 
 namespace fp4 {
 
@@ -47,19 +52,24 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
-constexpr int kStep = 128;      // columns a step
-constexpr int kDepth = 4;       // steps in flight per warp
+constexpr int kStep = 256;             // columns a step
+constexpr int kPayload = 16 * kStep / 2;  // bytes of a stage: payload, then scale words
+constexpr int kWords = 32 * 8;
+constexpr int kMaxDepth = 4;
 constexpr int kMaxSmem = 227 * 1024;
-constexpr int kXBytes = 160 * 1024;  // above this K is split over more CTAs first
 
 struct MvParams {
+  CUtensorMap map;   // payload [N][K / 2], boxes of 16 rows x 128 bytes
   MatvecJob j;
-  int steps;         // ceil(K / 128)
+  int steps;         // ceil(K / 256)
   int tiles;         // ceil(N / 16)
   int sk, S;         // warps and CTAs that share a tile along K
   int rounds;        // row tiles a warp takes, one after the other
   int clusters;
   int mc;            // tokens a CTA takes (blockIdx.y counts them off)
+  int depth;         // stages of a warp's ring
+  int words;         // scale words can be copied whole (4-byte aligned rows)
+  uint32_t *status;
 };
 
 // 2^e as binary32, e in [-149, 127].
@@ -71,6 +81,13 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+
+// Both halves of a by the low (hi = false) or high half of s.
+__device__ __forceinline__ uint32_t hmul2_by(uint32_t a, uint32_t s, bool hi) {
+  const __half2 v = *reinterpret_cast<const __half2 *>(&s);
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), hi ? __high2half2(v) : __low2half2(v));
+  return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // The four bytes of w as four f16 pairs (E2M1 -> f16, exact).
@@ -93,105 +110,128 @@ __device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 ldg16(const uint8_t *p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0)
+               : "memory");
 }
-__device__ __forceinline__ uint2 ldg8(const uint8_t *p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0)
+               : "memory");
+}
+// The lane's arrival, when its cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// What a lane holds of one step: 32 weights of rows g and g + 8, and the
-// codes of the scales over them (first block in the low byte).
-struct Stage {
-  uint4 wa, wb;
-  uint32_t sa, sb;
-};
+// Fills a warp's stages one after the other: the payload of 16 rows x 256
+// columns and, per lane, the scale words over its 64 columns of rows g and
+// g + 8 ({a, b} at 8 * lane; a word holds the codes of 64 columns, or with
+// 32-element blocks of 128 columns).  Addresses advance by constants inside
+// a tile and are formed anew at the next.
+template <int BLOCK, bool TMA>
+struct Loader {
+  const uint8_t *sa, *sb;  // the lane's next scale words
+  int sstep;               // bytes from a step's words to the next's
+  int words_left;          // steps whose word (of a row) lies inside K
+  bool row_a, row_b;
+  int step, row0;          // of the next stage
 
-// A row tile's addresses: the lane's payload and scales at step 0.
-template <int KIND, bool K32>
-struct Rows {
-  const uint8_t *qa, *qb, *sa, *sb;
-  int64_t sstep;  // bytes from one step's scales to the next's
-
-  __device__ __forceinline__ void set(const MatvecJob &j, int64_t tile, int g, int t) {
-    int64_t ra = tile * 16 + g, rb = ra + 8;
-    if (ra >= j.N) ra = j.N - 1;  // rows past the end repeat the last; not stored
-    if (rb >= j.N) rb = j.N - 1;
-    qa = j.q + ra * (j.K / 2) + 16 * t;
-    qb = j.q + rb * (j.K / 2) + 16 * t;
-    const int64_t blocks = j.K / j.block;
-    const int first = 32 * t / j.block;  // the lane's first block of a step
+  __device__ __forceinline__ void set(const MvParams &p, int64_t tile, int s, int lane) {
+    const MatvecJob &j = p.j;
+    const int g = lane >> 2, t = lane & 3;
+    step = s;
+    row0 = (int)tile * 16;
+    const int64_t blocks = j.K / BLOCK;
+    const int per = kStep / BLOCK, first = BLOCK == 16 ? 4 * t : 2 * (t & 2);
+    const int64_t at = (int64_t)s * per + first;  // the next word's first block
+    const int64_t left = blocks - at;
+    words_left = left > 0 ? (int)((left + per - 1) / per) : 0;
+    const int64_t ra = tile * 16 + g, rb = ra + 8;
+    row_a = ra < j.N;
+    row_b = rb < j.N;
     if (j.sf_mma) {
       const int64_t c4 = (blocks + 3) >> 2;
-      const int64_t at = (first >> 2) * 512 + (first & 3);
-      sa = j.sf + (ra >> 7) * c4 * 512 + (ra & 31) * 16 + ((ra >> 5) & 3) * 4 + at;
-      sb = j.sf + (rb >> 7) * c4 * 512 + (rb & 31) * 16 + ((rb >> 5) & 3) * 4 + at;
-      sstep = kStep / j.block / 4 * 512;
+      const int64_t o = (at >> 2) * 512;
+      sa = j.sf + (ra >> 7) * c4 * 512 + (ra & 31) * 16 + ((ra >> 5) & 3) * 4 + o;
+      sb = j.sf + (rb >> 7) * c4 * 512 + (rb & 31) * 16 + ((rb >> 5) & 3) * 4 + o;
+      sstep = per / 4 * 512;
     } else {
-      sa = j.sf + ra * blocks + first;
-      sb = j.sf + rb * blocks + first;
-      sstep = kStep / j.block;
+      sa = j.sf + ra * blocks + at;
+      sb = j.sf + rb * blocks + at;
+      sstep = per;
     }
+    if (!row_a) sa = j.sf;
+    if (!row_b) sb = j.sf;
   }
 
-  // left: columns from the lane's first one to K (32 or more: all there)
-  __device__ __forceinline__ void load(Stage &s, int step, int left, bool two) const {
-    s.wa = s.wb = make_uint4(0, 0, 0, 0);
-    s.sa = s.sb = 0;
-    if (left <= 0) return;
-    const int64_t o = (int64_t)step * (kStep / 2), p = step * sstep;
-    if (K32) {
-      s.wa = ldg16(qa + o);
-      s.wb = ldg16(qb + o);
-      if (two) {
-        s.sa = __ldg(reinterpret_cast<const uint16_t *>(sa + p));
-        s.sb = __ldg(reinterpret_cast<const uint16_t *>(sb + p));
-      } else {
-        s.sa = __ldg(sa + p);
-        s.sb = __ldg(sb + p);
+  __device__ __forceinline__ void fill(const MvParams &p, uint32_t payload, uint32_t words,
+                                       uint32_t bar, int lane) {
+    const MatvecJob &j = p.j;
+    if (TMA) {
+      if (lane == 0) {
+        tc::mbar_expect_tx(bar, kPayload);  // the full box, whatever part of it lies outside
+        tc::tma_load_2d(payload, &p.map, bar, step * (kStep / 2), row0);
       }
-    } else {  // K is an odd number of 16-element blocks: rows start on 8 bytes
-      const uint2 a0 = ldg8(qa + o), b0 = ldg8(qb + o);
-      uint2 a1 = make_uint2(0, 0), b1 = make_uint2(0, 0);
-      s.sa = __ldg(sa + p);
-      s.sb = __ldg(sb + p);
-      if (left > 16) {
-        a1 = ldg8(qa + o + 8);
-        b1 = ldg8(qb + o + 8);
-        s.sa |= (uint32_t)__ldg(sa + p + 1) << 8;
-        s.sb |= (uint32_t)__ldg(sb + p + 1) << 8;
+    } else {
+      // 16 rows x 16 pieces of 8 bytes; lane: piece lane % 16 of every other row
+      const int64_t at = (int64_t)step * (kStep / 2) + (lane & 15) * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        const int64_t n = (int64_t)row0 + r;
+        const bool on = n < j.N && at < j.K / 2;
+        const int c16 = (lane & 15) >> 1;  // in the swizzled place the TMA would use
+        cp_async8(payload + r * 128 + ((c16 ^ (r & 7)) << 4) + (lane & 1) * 8,
+                  j.q + (on ? n * (j.K / 2) + at : 0), on);
       }
-      s.wa = make_uint4(a0.x, a0.y, a1.x, a1.y);
-      s.wb = make_uint4(b0.x, b0.y, b1.x, b1.y);
     }
+    const uint32_t dst = words + lane * 8;
+    if (p.words) {
+      cp_async4(dst, words_left > 0 ? sa : j.sf, row_a && words_left > 0);
+      cp_async4(dst + 4, words_left > 0 ? sb : j.sf, row_b && words_left > 0);
+    } else {  // rows of scales that start on no word (plain layout): by bytes
+      const int first = step * (kStep / BLOCK) + (BLOCK == 16 ? 4 * (lane & 3) : 2 * (lane & 2));
+      const int blocks = (int)(j.K / BLOCK);
+      uint32_t wa = 0, wb = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (first + b < blocks) {
+          if (row_a) wa |= (uint32_t)__ldg(sa + b) << (8 * b);
+          if (row_b) wb |= (uint32_t)__ldg(sb + b) << (8 * b);
+        }
+      }
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(wa), "r"(wb) : "memory");
+    }
+    cp_async_arrive(bar);
+    ++step;
+    --words_left;
+    sa += sstep;
+    sb += sstep;
   }
 };
 
-// f16 pairs (v, v) of the scales of the lane's two 16-element halves.
-template <int KIND>
-__device__ __forceinline__ void scale_pairs(uint32_t codes, bool two, int top, uint32_t *h) {
+// The f16 scales over the lane's 64 columns of one row: blocks of 16, pairs
+// {0, 1} and {2, 3} (block h in half h % 2 of h[h / 2]); blocks of 32, one pair.
+template <int KIND, int BLOCK>
+__device__ __forceinline__ void scale_pairs(uint32_t w, int top, uint32_t *h) {
   if (KIND == kMXFP4) {
     // 2^(code - top + 13): f16 exponent field 28 + code - top, subnormal below 1
-    const int e = 28 + (int)(codes & 255u) - top;
-    const uint32_t v = e >= 1 ? (uint32_t)e << 10 : (e >= -9 ? 1u << (e + 9) : 0u);
-    h[0] = h[1] = v * 0x10001u;
+    const int e0 = 28 + (int)(w & 255u) - top, e1 = 28 + (int)((w >> 8) & 255u) - top;
+    const uint32_t v0 = e0 >= 1 ? (uint32_t)e0 << 10 : (e0 >= -9 ? 1u << (e0 + 9) : 0u);
+    const uint32_t v1 = e1 >= 1 ? (uint32_t)e1 << 10 : (e1 >= -9 ? 1u << (e1 + 9) : 0u);
+    h[0] = v0 | (v1 << 16);
     return;
   }
-  uint32_t c0 = codes & 255u, c1 = two ? codes >> 8 : c0;
-  if (KIND == kNVFP4) {
-    // E4M3's fields at f16's: value 2^(7 - 15)
-    h[0] = (c0 & 127u) * (128u * 0x10001u);
-    h[1] = (c1 & 127u) * (128u * 0x10001u);
-  } else {
-    // E5M3 is the head of an f16; times 2^-3 to leave room for a product
-    h[0] = hmul2(c0 * (128u * 0x10001u), 0x30003000u);
-    h[1] = hmul2(c1 * (128u * 0x10001u), 0x30003000u);
+#pragma unroll
+  for (int i = 0; i < 32 / BLOCK; ++i) {
+    if (KIND == kNVFP4) {
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+          : "=r"(h[i])
+          : "r"(i ? w >> 16 : w));
+    } else {
+      // E5M3 is the head of an f16; times 2^-3 to leave room for a product
+      h[i] = hmul2(__byte_perm(w, 0, i ? 0x3424 : 0x1404) >> 1, 0x30003000u);
+    }
   }
 }
 
@@ -205,21 +245,19 @@ struct Is<__nv_bfloat16> {
 };
 
 // x[0 .. M) over steps [s0, s0 + n) as f16 into shared memory, and the power
-// of two taken out of each (token, step).
+// of two taken out of each (token, step); a warp per (token, step), eight
+// elements a lane.
 template <typename TX>
 __device__ void prepare_x(const MatvecJob &j, int64_t m0, int M, int s0, int n, uint8_t *xs, int pitch,
                           float *sx, int cols) {
   const TX *x = static_cast<const TX *>(j.x) + m0 * j.xs;
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (M == 1 || j.xs % 8 == 0);
-  // 16 lanes a (token, step); eight elements each
-  const int total = M * n * 16;
-  for (int i = threadIdx.x; i < (total + 31) / 32 * 32; i += kThreads) {
-    const bool on = i < total;
-    const int unit = i >> 4, piece = i & 15;
-    const int m = on ? unit / n : 0, c = on ? unit - m * n : 0;
+  const int piece = threadIdx.x & 31;
+  for (int u = threadIdx.x >> 5; u < M * n; u += kWarps) {
+    const int m = u / n, c = u - m * n;
     const int64_t k = (int64_t)(s0 + c) * kStep + piece * 8;
     uint32_t w[4] = {0, 0, 0, 0};
-    if (on && k < j.K) {  // K is a multiple of 16: a piece is inside or outside
+    if (k < j.K) {  // K is a multiple of 16: a piece is inside or outside
       const TX *p = x + m * j.xs + k;
       if (vec) {
         const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
@@ -235,8 +273,7 @@ __device__ void prepare_x(const MatvecJob &j, int64_t m0, int M, int s0, int n, 
       uint32_t top = 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) top = max(top, max(w[q] & 0x7FFFu, (w[q] >> 16) & 0x7FFFu));
-#pragma unroll
-      for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+      top = __reduce_max_sync(~0u, top);
       // exponent of the largest finite magnitude (2^133 x subnormals: 1 + mantissa bits)
       const int f = (int)(top >> 7);
       const int e = f >= 255 ? 127 : f > 0 ? f - 127 : top ? (31 - __clz((int)top)) - 133 : 0;
@@ -249,22 +286,20 @@ __device__ void prepare_x(const MatvecJob &j, int64_t m0, int M, int s0, int n, 
         w[q] = *reinterpret_cast<const uint32_t *>(&v);
       }
     }
-    if (on) {
-      // piece (t, i) = (piece / 4, piece % 4) lies at 16 (4 i + t)
-      *reinterpret_cast<uint4 *>(xs + (int64_t)m * pitch + c * 256 + ((piece & 3) * 4 + (piece >> 2)) * 16) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-      if (piece == 0) sx[c * cols + m] = pow2(ex);
-    }
+    // piece i of lane t (piece = 8 t + i) lies at 64 i + 16 t
+    *reinterpret_cast<uint4 *>(xs + m * pitch + c * 512 + (piece & 7) * 64 + (piece >> 3) * 16) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+    if (piece == 0) sx[c * cols + m] = pow2(ex);
   }
 }
 
-template <int KIND, bool K32, typename TX, int NT>
+template <int KIND, int BLOCK, bool TMA, typename TX, int NT>
 __global__ void __launch_bounds__(kThreads, 1) k_matvec(const __grid_constant__ MvParams p) {
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int kCols = 8 * NT;
   const MatvecJob &j = p.j;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int S = p.S, sk = p.sk;
+  const int S = p.S, sk = p.sk, depth = p.depth;
   const int rank = blockIdx.x % S, cluster = blockIdx.x / S;
   const int64_t m0 = (int64_t)blockIdx.y * p.mc;
   const int M = (int)min((int64_t)p.mc, j.M - m0);
@@ -272,23 +307,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_matvec(const __grid_constant__ 
   const int c0 = (int)((int64_t)p.steps * rank / S), c1 = (int)((int64_t)p.steps * (rank + 1) / S);
   const int kw = warp % sk, tw = warp / sk, group = kWarps / sk;
   const int n = c1 - c0;
-  const int s0 = c0 + n * kw / sk, s1 = c0 + n * (kw + 1) / sk;
-  const int pitch = n * 256 + 64;
+  const int s0 = c0 + n * kw / sk, ns = c0 + n * (kw + 1) / sk - s0;
+  const int pitch = n * 512 + 64;
   const int span = (p.steps + S - 1) / S;  // same on every CTA of the cluster
-  uint8_t *xs = smem;
-  float *sx = reinterpret_cast<float *>(smem + M * (span * 256 + 64));
+  uint8_t *ring = smem + warp * depth * kPayload;
+  uint8_t *word_ring = smem + kWarps * depth * kPayload + warp * depth * kWords;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kWarps * depth * (kPayload + kWords)) + warp * kMaxDepth;
+  float *sx = reinterpret_cast<float *>(smem + kWarps * depth * (kPayload + kWords) + kWarps * kMaxDepth * 8);
   float *parts = sx + span * kCols;  // [2][kWarps][16 * kCols]
-  const bool two = j.block == 16;
+  uint8_t *xs = reinterpret_cast<uint8_t *>(parts + 2 * kWarps * 16 * kCols);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(xs + p.mc * (span * 512 + 64));
+  const uint32_t ring_a = tc::smem_u32(ring), words_a = tc::smem_u32(word_ring), bars_a = tc::smem_u32(bars);
 
-  Rows<KIND, K32> rows;
-  Stage st[kDepth];
-  int64_t tile = (int64_t)cluster * group + tw;  // rounds step by clusters * group
-  const int lane_col = 32 * t;
-  const int K = (int)j.K;
-  rows.set(j, tile < p.tiles ? tile : p.tiles - 1, g, t);
-#pragma unroll
-  for (int u = 0; u < kDepth; ++u)
-    if (s0 + u < s1) rows.load(st[u], s0 + u, K - (s0 + u) * kStep - lane_col, two);
+  // the warp's own ring: 32 lanes arrive for their copies, with TMA one more
+  // arrival that also expects the box
+  if (threadIdx.x == 0) *abort_flag = 0;
+  if (lane == 0) {
+    for (int d = 0; d < depth; ++d) tc::mbar_init(bars_a + 8 * d, TMA ? 33 : 32);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  __syncwarp();
+  const int64_t tile0 = (int64_t)cluster * group + tw, hop = (int64_t)p.clusters * group;
+  const int mine = tw < group && tile0 < p.tiles ? (int)((p.tiles - 1 - tile0) / hop) + 1 : 0;  // the warp's tiles
+  int64_t ahead = (int64_t)mine * ns, flying = 0;  // stages to request, requested and not read
+  int64_t ld_tile = tile0;
+  int ld_left = ns, ld_slot = 0;
+  Loader<BLOCK, TMA> ld;
+  ld.set(p, tile0, s0, lane);
+  auto issue = [&] {
+    ld.fill(p, ring_a + ld_slot * kPayload, words_a + ld_slot * kWords, bars_a + 8 * ld_slot, lane);
+    --ahead;
+    ++flying;
+    if (++ld_slot == depth) ld_slot = 0;
+    if (--ld_left == 0) {
+      ld_left = ns;
+      ld_tile += hop;
+      ld.set(p, ld_tile, s0, lane);
+    }
+  };
+  for (int d = 0; d < depth && ahead; ++d) issue();
 
   prepare_x<TX>(j, m0, M, c0, n, xs, pitch, sx, kCols);
   __syncthreads();
@@ -297,78 +355,87 @@ __global__ void __launch_bounds__(kThreads, 1) k_matvec(const __grid_constant__ 
 #pragma unroll
   for (int b = 0; b < NT; ++b) xl[b] = xs + min(8 * b + g, M - 1) * pitch + t * 16;  // columns past M repeat
 
+  const int at0 = ((2 * t) ^ g) << 4;  // the lane's pieces of a row: at0, at0 ^ 16, then 1024 on
+  int slot = 0;
+  uint32_t phase = 0;
+  bool live = true;  // false once a wait ran out: no more loads, results void
   for (int r = 0; r < p.rounds; ++r) {
-    const int64_t next = tile + (int64_t)p.clusters * group;
     float acc[NT][4];
 #pragma unroll
     for (int b = 0; b < NT; ++b) acc[b][0] = acc[b][1] = acc[b][2] = acc[b][3] = 0.0f;
-    for (int s = s0; s < s1; s += kDepth) {
-      const bool last = s + kDepth >= s1;
-      if (last) rows.set(j, next < p.tiles ? next : p.tiles - 1, g, t);
+    int xo = (s0 - c0) * 512;
+    const float *sxl = sx + (s0 - c0) * kCols + 2 * t;
+    for (int s = r < mine && live ? ns : 0; s > 0; --s) {
+      if (!__all_sync(~0u, tc::mbar_wait_inl(bars_a + 8 * slot, phase, abort_flag, p.status))) {
+        live = false;
+        break;
+      }
+      uint2 codes = *reinterpret_cast<const uint2 *>(word_ring + slot * kWords + lane * 8);
+      const uint8_t *ra = ring + slot * kPayload + g * 128;
+      float d[NT][2][4] = {};
+      float fa = 1.0f, fb = 1.0f;
+      int topa = 0, topb = 0;
+      if (BLOCK == 32 && (t & 1)) codes.x >>= 16, codes.y >>= 16;  // the lane's half of the word
+      if (KIND == kMXFP4) {
+        topa = max((int)(codes.x & 255u), (int)((codes.x >> 8) & 255u));
+        topb = max((int)(codes.y & 255u), (int)((codes.y >> 8) & 255u));
 #pragma unroll
-      for (int u = 0; u < kDepth; ++u) {
-        if (s + u < s1) {
-          float d[NT][2][4] = {};
-          uint32_t ha[2], hb[2];
-          float fa = 1.0f, fb = 1.0f;
-          int topa = 0, topb = 0;
-          if (KIND == kMXFP4) {
-            topa = (int)st[u].sa, topb = (int)st[u].sb;
+        for (int o = 1; o < 4; o <<= 1) {
+          topa = max(topa, __shfl_xor_sync(~0u, topa, o));
+          topb = max(topb, __shfl_xor_sync(~0u, topb, o));
+        }
+        fa = pow2(topa - 140);  // 2^(top - 127) / 2^13
+        fb = pow2(topb - 140);
+      }
+      uint32_t ha[2], hb[2];
+      scale_pairs<KIND, BLOCK>(codes.x, topa, ha);
+      scale_pairs<KIND, BLOCK>(codes.y, topb, hb);
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-              topa = max(topa, __shfl_xor_sync(~0u, topa, o));
-              topb = max(topb, __shfl_xor_sync(~0u, topb, o));
-            }
-            fa = pow2(topa - 140);  // 2^(top - 127) / 2^13
-            fb = pow2(topb - 140);
-          }
-          scale_pairs<KIND>(st[u].sa, two, topa, ha);
-          scale_pairs<KIND>(st[u].sb, two, topb, hb);
-          const int xo = (s + u - c0) * 256;
+      for (int h = 0; h < 2; ++h) {  // 32 of the lane's 64 columns: a 16-byte piece of each row
+        const uint4 wa = *reinterpret_cast<const uint4 *>(ra + (at0 ^ (16 * h)));
+        const uint4 wb = *reinterpret_cast<const uint4 *>(ra + 1024 + (at0 ^ (16 * h)));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t w0 = i == 0 ? st[u].wa.x : i == 1 ? st[u].wa.y : i == 2 ? st[u].wa.z : st[u].wa.w;
-            const uint32_t w1 = i == 0 ? st[u].wb.x : i == 1 ? st[u].wb.y : i == 2 ? st[u].wb.z : st[u].wb.w;
-            uint32_t a[4], b[4];
-            decode8(w0, a);
-            decode8(w1, b);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t a[4], b[4];
+          decode8(i == 0 ? wa.x : i == 1 ? wa.y : i == 2 ? wa.z : wa.w, a);
+          decode8(i == 0 ? wb.x : i == 1 ? wb.y : i == 2 ? wb.z : wb.w, b);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              a[q] = hmul2(a[q], ha[i >> 1]);
-              b[q] = hmul2(b[q], hb[i >> 1]);
-            }
-#pragma unroll
-            for (int c = 0; c < NT; ++c) {
-              const uint4 v = *reinterpret_cast<const uint4 *>(xl[c] + xo + i * 64);
-              mma(d[c][0], a[0], b[0], a[1], b[1], v.x, v.y);
-              mma(d[c][1], a[2], b[2], a[3], b[3], v.z, v.w);
-            }
+          for (int q = 0; q < 4; ++q) {
+            a[q] = BLOCK == 16 ? hmul2_by(a[q], ha[h], i >= 2) : hmul2_by(a[q], ha[0], h);
+            b[q] = BLOCK == 16 ? hmul2_by(b[q], hb[h], i >= 2) : hmul2_by(b[q], hb[0], h);
           }
 #pragma unroll
           for (int c = 0; c < NT; ++c) {
-            const float2 f = *reinterpret_cast<const float2 *>(sx + (s + u - c0) * kCols + 8 * c + 2 * t);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float v = d[c][0][e] + d[c][1][e];
-              const float fx = e & 1 ? f.y : f.x;
-              if (KIND == kMXFP4) {
-                acc[c][e] = fmaf(v * fx, e < 2 ? fa : fb, acc[c][e]);
-              } else {
-                acc[c][e] = fmaf(v, fx, acc[c][e]);
-              }
-            }
+            const uint4 v = *reinterpret_cast<const uint4 *>(xl[c] + xo + (4 * h + i) * 64);
+            mma(d[c][0], a[0], b[0], a[1], b[1], v.x, v.y);
+            mma(d[c][1], a[2], b[2], a[3], b[3], v.z, v.w);
           }
         }
-        // request the step this stage holds next: of this tile, or of the next
-        const int ahead = last ? s0 + u : s + kDepth + u;
-        if (ahead < s1 && (!last || r + 1 < p.rounds))
-          rows.load(st[u], ahead, K - ahead * kStep - lane_col, two);
       }
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        const float2 f = *reinterpret_cast<const float2 *>(sxl + 8 * c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = d[c][0][e] + d[c][1][e];
+          const float fx = e & 1 ? f.y : f.x;
+          acc[c][e] = KIND == kMXFP4 ? fmaf(v * fx, e < 2 ? fa : fb, acc[c][e]) : fmaf(v, fx, acc[c][e]);
+        }
+      }
+      xo += 512;
+      sxl += kCols;
+      --flying;
+      if (++slot == depth) {
+        slot = 0;
+        phase ^= 1;
+      }
+      __syncwarp();  // every lane has read the stage: it can be filled again
+      if (ahead) issue();
     }
     // join the parts of the tiles of this round, in K order
-    float *mine = parts + (r & 1) * (kWarps * 16 * kCols);
+    float *share = parts + (r & 1) * (kWarps * 16 * kCols);
     {
-      float *o = mine + warp * (16 * kCols);
+      float *o = share + warp * (16 * kCols);
 #pragma unroll
       for (int c = 0; c < NT; ++c)
 #pragma unroll
@@ -387,14 +454,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_matvec(const __grid_constant__ 
     const int outs = (alone ? 1 : group) * M * 16;
     for (int i = alone ? lane : (int)threadIdx.x * S + rank; i < outs; i += alone ? 32 : kThreads * S) {
       const int row = i & 15, mt = i >> 4, m = mt % M, tg = alone ? tw : mt / M;
-      const int64_t nrow = ((int64_t)(r * p.clusters + cluster) * group + tg) * 16 + row;
+      const int64_t nrow = ((int64_t)(r * (int64_t)p.clusters + cluster) * group + tg) * 16 + row;
       if (nrow >= j.N) continue;
       float v = 0.0f;
       for (int q = 0; q < S; ++q) {
-        const float *from = S > 1 ? cg::this_cluster().map_shared_rank(mine, q) : mine;
+        const float *from = S > 1 ? cg::this_cluster().map_shared_rank(share, q) : share;
         for (int w = 0; w < sk; ++w) v += from[(tg * sk + w) * (16 * kCols) + m * 16 + row];
       }
-      const int shift = (KIND == kNVFP4 ? 8 : KIND == kMXFP4 ? 0 : 3) + (j.shift ? j.shift[nrow] : 0);
+      const int shift = (KIND == kUE5M3 ? 3 : 0) + (j.shift ? j.shift[nrow] : 0);
       v = scalbnf(v, shift) * j.sd[j.stripes ? nrow >> 7 : 0];
       const int64_t at = (m0 + m) * j.ys + nrow;
       if (j.y_type == FP4_F32)
@@ -405,15 +472,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_matvec(const __grid_constant__ 
         static_cast<__half *>(j.y)[at] = __float2half_rn(v);
     }
     if (alone) __syncwarp();
-    tile = next;
+  }
+  if (!live) {  // copies still in flight land (bounded) before the ring goes away
+    for (; flying > 0; --flying) {
+      tc::mbar_wait_drain(bars_a + 8 * slot, phase);
+      if (++slot == depth) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
   }
   if (S > 1) cg::this_cluster().sync();  // nobody leaves while its parts may be read
 }
 
 // Shared memory for M tokens over ceil(steps / S) steps, NT column tiles.
-size_t smem_bytes(int M, int steps, int S, int nt) {
+size_t smem_bytes(int M, int steps, int S, int nt, int depth) {
   const size_t span = (steps + S - 1) / S;
-  return M * (span * 256 + 64) + span * 8 * nt * 4 + 2 * kWarps * 16 * 8 * nt * 4;
+  return (size_t)kWarps * depth * (kPayload + kWords) + kWarps * kMaxDepth * 8 + span * 8 * nt * 4 +
+         2 * kWarps * 16 * 8 * nt * 4 + M * (span * 512 + 64) + 16;
+}
+
+// Payload rows as a tensor map: boxes of 16 rows x 128 bytes, swizzled; what
+// lies past the last row or column reads as zero.
+bool payload_map(CUtensorMap *m, const void *base, int64_t rows, int64_t row_bytes) {
+  return tc::make_map(m, base, rows, row_bytes, 16, kStep / 2);
 }
 
 // What a kernel may use, asked once per kernel and device: raises its shared
@@ -451,21 +533,28 @@ int resident(Kern kern, Residence *per_device, int S) {
   return n;
 }
 
-template <int KIND, bool K32, typename TX, int NT>
+template <int KIND, int BLOCK, bool TMA, typename TX, int NT>
 fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   static Residence residence[64];
-  auto kern = k_matvec<KIND, K32, TX, NT>;
+  auto kern = k_matvec<KIND, BLOCK, TMA, TX, NT>;
   MvParams p{};
   p.j = j;
   p.steps = (int)ceil_div(j.K, kStep);
   p.tiles = (int)ceil_div(j.N, 16);
   p.mc = (int)(j.M < 8 * NT ? j.M : 8 * NT);
-  // x of a CTA's tokens over its part of K: more CTAs per tile, then fewer
-  // tokens, until it fits
+  p.words = j.sf_mma || (j.K / j.block) % 4 == 0;
+  p.status = status_word();
+  if (!p.status) return FP4_ERR_CUDA;
+  if (TMA && !payload_map(&p.map, j.q, j.N, j.K / 2)) return FP4_ERR_CUDA;
+  // x of a CTA's tokens over its part of K beside rings of 3 stages or more:
+  // more CTAs per tile until it fits; then fewer stages, then fewer tokens
   p.S = 1;
-  while (p.S < 8 && smem_bytes(p.mc, p.steps, p.S, NT) > (size_t)kXBytes) p.S *= 2;
-  while (p.mc > 1 && smem_bytes(p.mc, p.steps, p.S, NT) > (size_t)kMaxSmem) p.mc = (p.mc + 1) / 2;
-  const size_t smem = smem_bytes(p.mc, p.steps, p.S, NT);
+  p.depth = 3;
+  while (p.S < 8 && smem_bytes(p.mc, p.steps, p.S, NT, p.depth) > (size_t)kMaxSmem) p.S *= 2;
+  if (smem_bytes(p.mc, p.steps, p.S, NT, 3) > (size_t)kMaxSmem) p.depth = 2;
+  while (p.mc > 1 && smem_bytes(p.mc, p.steps, p.S, NT, p.depth) > (size_t)kMaxSmem) p.mc = (p.mc + 1) / 2;
+  if (smem_bytes(p.mc, p.steps, p.S, NT, kMaxDepth) <= (size_t)kMaxSmem) p.depth = kMaxDepth;
+  const size_t smem = smem_bytes(p.mc, p.steps, p.S, NT, p.depth);
   if (smem > (size_t)kMaxSmem) return FP4_ERR_SHAPE;
   const int room = resident(kern, residence, p.S);
   if (room < 1) return FP4_ERR_CUDA;
@@ -504,22 +593,24 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   return FP4_OK;
 }
 
-template <int KIND, bool K32, typename TX>
+template <int KIND, int BLOCK, bool TMA, typename TX>
 fp4_status launch_nt(const MatvecJob &j, cudaStream_t s) {
-  return j.M <= 8 ? launch<KIND, K32, TX, 1>(j, s) : launch<KIND, K32, TX, 2>(j, s);
+  return j.M <= 8 ? launch<KIND, BLOCK, TMA, TX, 1>(j, s) : launch<KIND, BLOCK, TMA, TX, 2>(j, s);
 }
 
+// Rows of K / 2 bytes are a TMA stride when K is a multiple of 32, as it is
+// with 32-element blocks.
 template <int KIND, typename TX>
 fp4_status launch_k(const MatvecJob &j, cudaStream_t s) {
-  if constexpr (KIND == kMXFP4) return launch_nt<KIND, true, TX>(j, s);  // K is a multiple of 32
-  return j.K % 32 == 0 ? launch_nt<KIND, true, TX>(j, s) : launch_nt<KIND, false, TX>(j, s);
+  if (j.K % 32 != 0) return launch_nt<KIND, 16, false, TX>(j, s);
+  return j.block == 16 ? launch_nt<KIND, 16, true, TX>(j, s) : launch_nt<KIND, 32, true, TX>(j, s);
 }
 
 template <typename TX>
 fp4_status launch_x(const MatvecJob &j, cudaStream_t s) {
   switch (j.kind) {
-    case kMXFP4: return launch_k<kMXFP4, TX>(j, s);
-    case kNVFP4: return launch_k<kNVFP4, TX>(j, s);
+    case kMXFP4: return launch_nt<kMXFP4, 32, true, TX>(j, s);
+    case kNVFP4: return j.K % 32 != 0 ? launch_nt<kNVFP4, 16, false, TX>(j, s) : launch_nt<kNVFP4, 16, true, TX>(j, s);
     default: return launch_k<kUE5M3, TX>(j, s);
   }
 }

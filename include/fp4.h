@@ -374,9 +374,9 @@ typedef enum { FP4_BF16 = 0, FP4_F16 = 1, FP4_F32 = 2 } fp4_type;
  * reads one s_dec per 128 rows.  Scale codes that no producer emits (UE5M3
  * above 0xF7, E4M3 0x7F, E8M0 255) give unspecified values.
  * Accuracy: x is held exactly for magnitudes down to 2^-32 of the largest in
- * its token's 128 columns, MXFP4 block scales down to 2^-35 of the largest in
- * a row's 128 columns; smaller ones round towards zero contribution.
- * MXFP4 sums of 128 columns must stay below 2^128 before their row's largest
+ * its token's 256 columns, MXFP4 block scales down to 2^-35 of the largest in
+ * a row's 256 columns; smaller ones round towards zero contribution.
+ * MXFP4 sums of 256 columns must stay below 2^128 before their row's largest
  * block scale is applied: |x| up to 2^100 is safe.
  * Shapes: any M, N >= 0; K % B == 0 and K <= 2^19; K == 0 writes zeros.  The
  * weight is read once per 16 tokens; from some hundred tokens on the GEMMs
