@@ -375,7 +375,7 @@ fp4_status fp4_matvec(const fp4_operand *W, int32_t sf_layout, const void *x, in
   if (x_type == FP4_F32) return FP4_ERR_UNSUPPORTED;
   const int64_t N = W->rows, K = W->k;
   if (M < 0 || N < 0 || K < 0 || x_stride < 0 || y_stride < 0) return FP4_ERR_INVALID_ARG;
-  if (K % block_of(W->format) != 0 || K > (1 << 19) || N > (int64_t)INT32_MAX * 16)
+  if (K % block_of(W->format) != 0 || K > (1 << 19) || N > INT32_MAX - 256)
     return FP4_ERR_SHAPE;
   if (M > 1 && (x_stride < K || y_stride < N)) return FP4_ERR_SHAPE;
   if (W->row_shift && !(is_ue5m3_fmt(W->format) && sf_layout == FP4_SF_MMA))

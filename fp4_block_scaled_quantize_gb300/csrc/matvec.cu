@@ -51,24 +51,28 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kStep = 256;             // columns a step
-constexpr int kPayload = 16 * kStep / 2;  // bytes of a stage: payload, then scale words
-constexpr int kWords = 32 * 8;
+constexpr int kRows = 32;              // weight rows of a tile: two MMA row tiles
+constexpr int kPayload = kRows * kStep / 2;  // bytes of a stage: payload, then scale words
+constexpr int kWords = 512;            // 4 scale words a row, 32 rows
 constexpr int kMaxDepth = 4;
 constexpr int kMaxSmem = 227 * 1024;
 
+// Warps of a CTA: with two token tiles a warp needs more than 128 registers.
+constexpr int warps_of(int nt) { return nt == 1 ? 16 : 12; }
+
 struct MvParams {
-  CUtensorMap map;   // payload [N][K / 2], boxes of 16 rows x 128 bytes
+  CUtensorMap map;   // payload [N][K / 2], boxes of 32 or 8 rows x 128 bytes
+  CUtensorMap smap;  // scales, see Words
   MatvecJob j;
   int steps;         // ceil(K / 256)
-  int tiles;         // ceil(N / 16)
+  int tiles;         // 4 ceil(N / 128)
   int sk, S;         // warps and CTAs that share a tile along K
   int rounds;        // row tiles a warp takes, one after the other
   int clusters;
   int mc;            // tokens a CTA takes (blockIdx.y counts them off)
   int depth;         // stages of a warp's ring
-  int words;         // scale words can be copied whole (4-byte aligned rows)
+  int words;         // how scales reach shared memory: Words
   uint32_t *status;
 };
 
@@ -118,95 +122,102 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, bool on
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0)
                : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x,
+                                            int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 // The lane's arrival, when its cp.async copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Fills a warp's stages one after the other: the payload of 16 rows x 256
-// columns and, per lane, the scale words over its 64 columns of rows g and
-// g + 8 ({a, b} at 8 * lane; a word holds the codes of 64 columns, or with
-// 32-element blocks of 128 columns).  Addresses advance by constants inside
-// a tile and are formed anew at the next.
+// Scales of a stage in shared memory, and the rows of a tile.
+//   kTiled: the tensor-core layout.  512-byte tiles hold 32 lines of 16 bytes,
+//     the words of rows l, l + 32, l + 64, l + 96 of their 128 rows; so a
+//     tile of weight rows is 4 groups of 8 rows 32 apart, its payload four TMA
+//     boxes of 8 rows, and its scales 128 contiguous bytes of each 64 (or,
+//     32-element blocks, 128) columns: one box, no byte unused.  Lane (g, t)
+//     finds its four words in 16 bytes at 128 t + 16 g (t / 2 for 32-blocks).
+//   kBoxed: plain rows with a pitch of whole 16 bytes: one box of 32 rows x 16
+//     bytes (with 32-element blocks the 16 bytes that hold the step's 8);
+//     word i of a lane at 128 i + 4 lane (row g + 8 i, word t).
+//   kPieces, kBytes: plain rows of any other pitch, the same place, by 4-byte
+//     cp.async or byte loads.
+enum Words { kTiled = 0, kBoxed = 1, kPieces = 2, kBytes = 3 };
+
+// Fills a warp's stages one after the other.
 template <int BLOCK, bool TMA>
 struct Loader {
-  const uint8_t *sa, *sb;  // the lane's next scale words
-  int sstep;               // bytes from a step's words to the next's
-  int words_left;          // steps whose word (of a row) lies inside K
-  bool row_a, row_b;
-  int step, row0;          // of the next stage
+  int step, row0;        // of the next stage: row0 the tile's first row
 
-  __device__ __forceinline__ void set(const MvParams &p, int64_t tile, int s, int lane) {
-    const MatvecJob &j = p.j;
-    const int g = lane >> 2, t = lane & 3;
-    step = s;
-    row0 = (int)tile * 16;
-    const int64_t blocks = j.K / BLOCK;
-    const int per = kStep / BLOCK, first = BLOCK == 16 ? 4 * t : 2 * (t & 2);
-    const int64_t at = (int64_t)s * per + first;  // the next word's first block
-    const int64_t left = blocks - at;
-    words_left = left > 0 ? (int)((left + per - 1) / per) : 0;
-    const int64_t ra = tile * 16 + g, rb = ra + 8;
-    row_a = ra < j.N;
-    row_b = rb < j.N;
-    if (j.sf_mma) {
-      const int64_t c4 = (blocks + 3) >> 2;
-      const int64_t o = (at >> 2) * 512;
-      sa = j.sf + (ra >> 7) * c4 * 512 + (ra & 31) * 16 + ((ra >> 5) & 3) * 4 + o;
-      sb = j.sf + (rb >> 7) * c4 * 512 + (rb & 31) * 16 + ((rb >> 5) & 3) * 4 + o;
-      sstep = per / 4 * 512;
-    } else {
-      sa = j.sf + ra * blocks + at;
-      sb = j.sf + rb * blocks + at;
-      sstep = per;
-    }
-    if (!row_a) sa = j.sf;
-    if (!row_b) sb = j.sf;
+  // Tile i of 128-row group i / 4 (kTiled: its lines 8 (i % 4) ..., else its rows 32 (i % 4) ...).
+  static __device__ __forceinline__ int64_t first_row(int64_t tile, bool tiled) {
+    return (tile >> 2) * 128 + (tile & 3) * (tiled ? 8 : 32);
   }
 
   __device__ __forceinline__ void fill(const MvParams &p, uint32_t payload, uint32_t words,
                                        uint32_t bar, int lane) {
     const MatvecJob &j = p.j;
-    if (TMA) {
-      if (lane == 0) {
-        tc::mbar_expect_tx(bar, kPayload);  // the full box, whatever part of it lies outside
-        tc::tma_load_2d(payload, &p.map, bar, step * (kStep / 2), row0);
-      }
-    } else {
-      // 16 rows x 16 pieces of 8 bytes; lane: piece lane % 16 of every other row
-      const int64_t at = (int64_t)step * (kStep / 2) + (lane & 15) * 8;
+    const bool tiled = p.words == kTiled;
+    constexpr int kPer = kStep / BLOCK;  // scale bytes of a row and step
+    if (lane == 0) {
+      // full boxes count, whatever part of them lies outside
+      const uint32_t sbytes = p.words > kBoxed ? 0 : tiled ? 32 * kPer : 512;
+      const uint32_t bytes = (TMA ? kPayload : 0) + sbytes;
+      if (bytes) tc::mbar_expect_tx(bar, bytes);
+      if (TMA) {
+        if (tiled) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i)
+            tc::tma_load_2d(payload + 1024 * i, &p.map, bar, step * (kStep / 2), row0 + 32 * i);
+        } else {
+          tc::tma_load_2d(payload, &p.map, bar, step * (kStep / 2), row0);
+        }
+      }
+      if (tiled)
+        tma_load_3d(words, &p.smap, bar, (row0 & 31) * 16, step * (kPer / 4), row0 >> 7);
+      else if (p.words == kBoxed)
+        tc::tma_load_2d(words, &p.smap, bar, step * kPer & ~15, row0);
+    }
+    if (!TMA) {
+      // 16 pieces of 8 bytes a row; lane: piece lane % 16 of every other row
+      const int64_t at = (int64_t)step * (kStep / 2) + (lane & 15) * 8;
+#pragma unroll 4
+      for (int i = 0; i < kRows / 2; ++i) {
         const int r = 2 * i + (lane >> 4);
-        const int64_t n = (int64_t)row0 + r;
+        const int64_t n = (int64_t)row0 + (tiled ? 32 * (r >> 3) + (r & 7) : r);
         const bool on = n < j.N && at < j.K / 2;
         const int c16 = (lane & 15) >> 1;  // in the swizzled place the TMA would use
         cp_async8(payload + r * 128 + ((c16 ^ (r & 7)) << 4) + (lane & 1) * 8,
                   j.q + (on ? n * (j.K / 2) + at : 0), on);
       }
     }
-    const uint32_t dst = words + lane * 8;
-    if (p.words) {
-      cp_async4(dst, words_left > 0 ? sa : j.sf, row_a && words_left > 0);
-      cp_async4(dst + 4, words_left > 0 ? sb : j.sf, row_b && words_left > 0);
-    } else {  // rows of scales that start on no word (plain layout): by bytes
-      const int first = step * (kStep / BLOCK) + (BLOCK == 16 ? 4 * (lane & 3) : 2 * (lane & 2));
-      const int blocks = (int)(j.K / BLOCK);
-      uint32_t wa = 0, wb = 0;
+    if (p.words > kBoxed) {
+      const int g = lane >> 2, t = lane & 3;
+      const int blocks = (int)(j.K / BLOCK), first = step * kPer + (BLOCK == 16 ? 4 * t : 2 * (t & 2));
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (first + b < blocks) {
-          if (row_a) wa |= (uint32_t)__ldg(sa + b) << (8 * b);
-          if (row_b) wb |= (uint32_t)__ldg(sb + b) << (8 * b);
+      for (int i = 0; i < 4; ++i) {
+        const int64_t n = (int64_t)row0 + g + 8 * i;
+        const bool on = n < j.N && first < blocks;
+        const uint8_t *from = j.sf + (on ? n * blocks + first : 0);
+        const uint32_t dst = words + 128 * i + 4 * lane;
+        if (p.words == kPieces) {
+          cp_async4(dst, from, on);
+        } else {
+          uint32_t w = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (on && first + b < blocks) w |= (uint32_t)__ldg(from + b) << (8 * b);
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(w) : "memory");
         }
       }
-      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(dst), "r"(wa), "r"(wb) : "memory");
     }
-    cp_async_arrive(bar);
+    if (!TMA || p.words > kBoxed) cp_async_arrive(bar);
     ++step;
-    --words_left;
-    sa += sstep;
-    sb += sstep;
   }
 };
 
@@ -247,7 +258,7 @@ struct Is<__nv_bfloat16> {
 // x[0 .. M) over steps [s0, s0 + n) as f16 into shared memory, and the power
 // of two taken out of each (token, step); a warp per (token, step), eight
 // elements a lane.
-template <typename TX>
+template <typename TX, int kWarps>
 __device__ void prepare_x(const MatvecJob &j, int64_t m0, int M, int s0, int n, uint8_t *xs, int pitch,
                           float *sx, int cols) {
   const TX *x = static_cast<const TX *>(j.x) + m0 * j.xs;
@@ -294,8 +305,9 @@ __device__ void prepare_x(const MatvecJob &j, int64_t m0, int M, int s0, int n, 
 }
 
 template <int KIND, int BLOCK, bool TMA, typename TX, int NT>
-__global__ void __launch_bounds__(kThreads, 1) k_matvec(const __grid_constant__ MvParams p) {
+__global__ void __launch_bounds__(32 * warps_of(NT), 1) k_matvec(const __grid_constant__ MvParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int kWarps = warps_of(NT), kThreads = 32 * kWarps;
   constexpr int kCols = 8 * NT;
   const MatvecJob &j = p.j;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -314,16 +326,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_matvec(const __grid_constant__ 
   uint8_t *word_ring = smem + kWarps * depth * kPayload + warp * depth * kWords;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kWarps * depth * (kPayload + kWords)) + warp * kMaxDepth;
   float *sx = reinterpret_cast<float *>(smem + kWarps * depth * (kPayload + kWords) + kWarps * kMaxDepth * 8);
-  float *parts = sx + span * kCols;  // [2][kWarps][16 * kCols]
-  uint8_t *xs = reinterpret_cast<uint8_t *>(parts + 2 * kWarps * 16 * kCols);
+  float *parts = sx + span * kCols;  // [kWarps][kCols][kRows]
+  uint8_t *xs = reinterpret_cast<uint8_t *>(parts + kWarps * kRows * kCols);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(xs + p.mc * (span * 512 + 64));
   const uint32_t ring_a = tc::smem_u32(ring), words_a = tc::smem_u32(word_ring), bars_a = tc::smem_u32(bars);
 
-  // the warp's own ring: 32 lanes arrive for their copies, with TMA one more
-  // arrival that also expects the box
+  // the warp's own ring: one arrival that expects the boxes, and 32 lanes' for
+  // their own copies, as the stage has either or both
+  const bool boxes = TMA || p.words <= kBoxed, copies = !TMA || p.words > kBoxed;
   if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
-    for (int d = 0; d < depth; ++d) tc::mbar_init(bars_a + 8 * d, TMA ? 33 : 32);
+    for (int d = 0; d < depth; ++d) tc::mbar_init(bars_a + 8 * d, (boxes ? 1 : 0) + (copies ? 32 : 0));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -333,8 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_matvec(const __grid_constant__ 
   int64_t ahead = (int64_t)mine * ns, flying = 0;  // stages to request, requested and not read
   int64_t ld_tile = tile0;
   int ld_left = ns, ld_slot = 0;
+  const bool tiled = p.words == kTiled;
   Loader<BLOCK, TMA> ld;
-  ld.set(p, tile0, s0, lane);
+  ld.step = s0;
+  ld.row0 = (int)ld.first_row(tile0, tiled);
   auto issue = [&] {
     ld.fill(p, ring_a + ld_slot * kPayload, words_a + ld_slot * kWords, bars_a + 8 * ld_slot, lane);
     --ahead;
@@ -343,12 +358,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_matvec(const __grid_constant__ 
     if (--ld_left == 0) {
       ld_left = ns;
       ld_tile += hop;
-      ld.set(p, ld_tile, s0, lane);
+      ld.step = s0;
+      ld.row0 = (int)ld.first_row(ld_tile, tiled);
     }
   };
   for (int d = 0; d < depth && ahead; ++d) issue();
 
-  prepare_x<TX>(j, m0, M, c0, n, xs, pitch, sx, kCols);
+  prepare_x<TX, kWarps>(j, m0, M, c0, n, xs, pitch, sx, kCols);
   __syncthreads();
 
   const uint8_t *xl[NT];
@@ -360,106 +376,131 @@ __global__ void __launch_bounds__(kThreads, 1) k_matvec(const __grid_constant__ 
   uint32_t phase = 0;
   bool live = true;  // false once a wait ran out: no more loads, results void
   for (int r = 0; r < p.rounds; ++r) {
-    float acc[NT][4];
-#pragma unroll
-    for (int b = 0; b < NT; ++b) acc[b][0] = acc[b][1] = acc[b][2] = acc[b][3] = 0.0f;
+    float acc[NT][2][4] = {};
     int xo = (s0 - c0) * 512;
     const float *sxl = sx + (s0 - c0) * kCols + 2 * t;
-    for (int s = r < mine && live ? ns : 0; s > 0; --s) {
+    for (int st = s0; st < (r < mine && live ? s0 + ns : s0); ++st) {
       if (!__all_sync(~0u, tc::mbar_wait_inl(bars_a + 8 * slot, phase, abort_flag, p.status))) {
         live = false;
         break;
       }
-      uint2 codes = *reinterpret_cast<const uint2 *>(word_ring + slot * kWords + lane * 8);
+      // the whole stage into registers, so that it is filled again meanwhile
+      uint32_t codes[4];
+      const uint8_t *wl = word_ring + slot * kWords;
+      if (tiled) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(wl + (BLOCK == 16 ? t : t >> 1) * 128 + g * 16);
+        codes[0] = v.x, codes[1] = v.y, codes[2] = v.z, codes[3] = v.w;
+      } else {
+        // with 32-element blocks a box holds two steps' words
+        const int o = BLOCK == 32 && p.words == kBoxed ? (4 * g + (t >> 1) + 2 * (st & 1)) * 4 : lane * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) codes[i] = *reinterpret_cast<const uint32_t *>(wl + 128 * i + o);
+      }
+      uint4 w[2][4];
       const uint8_t *ra = ring + slot * kPayload + g * 128;
-      float d[NT][2][4] = {};
-      float fa = 1.0f, fb = 1.0f;
-      int topa = 0, topb = 0;
-      if (BLOCK == 32 && (t & 1)) codes.x >>= 16, codes.y >>= 16;  // the lane's half of the word
-      if (KIND == kMXFP4) {
-        topa = max((int)(codes.x & 255u), (int)((codes.x >> 8) & 255u));
-        topb = max((int)(codes.y & 255u), (int)((codes.y >> 8) & 255u));
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          topa = max(topa, __shfl_xor_sync(~0u, topa, o));
-          topb = max(topb, __shfl_xor_sync(~0u, topb, o));
-        }
-        fa = pow2(topa - 140);  // 2^(top - 127) / 2^13
-        fb = pow2(topb - 140);
-      }
-      uint32_t ha[2], hb[2];
-      scale_pairs<KIND, BLOCK>(codes.x, topa, ha);
-      scale_pairs<KIND, BLOCK>(codes.y, topb, hb);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {  // 32 of the lane's 64 columns: a 16-byte piece of each row
-        const uint4 wa = *reinterpret_cast<const uint4 *>(ra + (at0 ^ (16 * h)));
-        const uint4 wb = *reinterpret_cast<const uint4 *>(ra + 1024 + (at0 ^ (16 * h)));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t a[4], b[4];
-          decode8(i == 0 ? wa.x : i == 1 ? wa.y : i == 2 ? wa.z : wa.w, a);
-          decode8(i == 0 ? wb.x : i == 1 ? wb.y : i == 2 ? wb.z : wb.w, b);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            a[q] = BLOCK == 16 ? hmul2_by(a[q], ha[h], i >= 2) : hmul2_by(a[q], ha[0], h);
-            b[q] = BLOCK == 16 ? hmul2_by(b[q], hb[h], i >= 2) : hmul2_by(b[q], hb[0], h);
-          }
-#pragma unroll
-          for (int c = 0; c < NT; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(xl[c] + xo + (4 * h + i) * 64);
-            mma(d[c][0], a[0], b[0], a[1], b[1], v.x, v.y);
-            mma(d[c][1], a[2], b[2], a[3], b[3], v.z, v.w);
-          }
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        const float2 f = *reinterpret_cast<const float2 *>(sxl + 8 * c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = d[c][0][e] + d[c][1][e];
-          const float fx = e & 1 ? f.y : f.x;
-          acc[c][e] = KIND == kMXFP4 ? fmaf(v * fx, e < 2 ? fa : fb, acc[c][e]) : fmaf(v, fx, acc[c][e]);
-        }
-      }
-      xo += 512;
-      sxl += kCols;
+        for (int i = 0; i < 4; ++i)
+          w[h][i] = *reinterpret_cast<const uint4 *>(ra + 1024 * i + (at0 ^ (16 * h)));
       --flying;
       if (++slot == depth) {
         slot = 0;
         phase ^= 1;
       }
-      __syncwarp();  // every lane has read the stage: it can be filled again
+      __syncwarp();  // every lane has read the stage
       if (ahead) issue();
+      uint32_t sc[4][2];
+      float f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (BLOCK == 32 && (t & 1)) codes[i] >>= 16;  // the lane's half of the word
+        int top = 0;
+        if (KIND == kMXFP4) {
+          top = max((int)(codes[i] & 255u), (int)((codes[i] >> 8) & 255u));
+          top = max(top, __shfl_xor_sync(~0u, top, 1));
+          top = max(top, __shfl_xor_sync(~0u, top, 2));
+          f[i] = pow2(top - 140);  // 2^(top - 127) / 2^13
+        }
+        scale_pairs<KIND, BLOCK>(codes[i], top, sc[i]);
+      }
+      float d[NT][2][4] = {};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // 32 of the lane's 64 columns: a 16-byte piece of each row
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint4 v[NT];
+#pragma unroll
+          for (int c = 0; c < NT; ++c)
+            v[c] = *reinterpret_cast<const uint4 *>(xl[c] + xo + (4 * h + q) * 64);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t a[4], b[4];
+            const uint4 &wa = w[h][2 * u], &wb = w[h][2 * u + 1];
+            decode8(q == 0 ? wa.x : q == 1 ? wa.y : q == 2 ? wa.z : wa.w, a);
+            decode8(q == 0 ? wb.x : q == 1 ? wb.y : q == 2 ? wb.z : wb.w, b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a[e] = BLOCK == 16 ? hmul2_by(a[e], sc[2 * u][h], q >= 2) : hmul2_by(a[e], sc[2 * u][0], h);
+              b[e] = BLOCK == 16 ? hmul2_by(b[e], sc[2 * u + 1][h], q >= 2) : hmul2_by(b[e], sc[2 * u + 1][0], h);
+            }
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+              mma(d[c][u], a[0], b[0], a[1], b[1], v[c].x, v[c].y);
+              mma(d[c][u], a[2], b[2], a[3], b[3], v[c].z, v[c].w);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < NT; ++c) {
+        const float2 fx = *reinterpret_cast<const float2 *>(sxl + 8 * c);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = e & 1 ? fx.y : fx.x;
+            acc[c][u][e] = KIND == kMXFP4 ? fmaf(d[c][u][e] * x, f[2 * u + (e >> 1)], acc[c][u][e])
+                                          : fmaf(d[c][u][e], x, acc[c][u][e]);
+          }
+      }
+      xo += 512;
+      sxl += kCols;
     }
-    // join the parts of the tiles of this round, in K order
-    float *share = parts + (r & 1) * (kWarps * 16 * kCols);
+    // join the parts of the tiles of this round, in K order; a warp whose tile
+    // is its own joins nothing and waits for nobody
+    const bool alone = S == 1 && sk == 1;
+    auto sync = [&] {
+      if (S > 1)
+        cg::this_cluster().sync();
+      else if (alone)
+        __syncwarp();
+      else
+        __syncthreads();
+    };
+    if (r > 0) sync();  // the parts of the round before have been read
     {
-      float *o = share + warp * (16 * kCols);
+      float *o = parts + warp * (kRows * kCols);
 #pragma unroll
       for (int c = 0; c < NT; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[(8 * c + 2 * t + (e & 1)) * 16 + g + 8 * (e >> 1)] = acc[c][e];
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[(8 * c + 2 * t + (e & 1)) * kRows + g + 16 * u + 8 * (e >> 1)] = acc[c][u][e];
     }
-    if (S > 1) {
-      cg::this_cluster().sync();
-    } else if (sk > 1) {
-      __syncthreads();
-    } else {
-      __syncwarp();
-    }
-    // outputs of the round: group tiles x M tokens x 16 rows, shared by the cluster's CTAs;
-    // a warp whose tile is its own joins nothing and waits for nobody
-    const bool alone = S == 1 && sk == 1;
-    const int outs = (alone ? 1 : group) * M * 16;
+    sync();
+    // outputs of the round: group tiles x M tokens x 32 rows, shared by the cluster's CTAs
+    const int outs = (alone ? 1 : group) * M * kRows;
     for (int i = alone ? lane : (int)threadIdx.x * S + rank; i < outs; i += alone ? 32 : kThreads * S) {
-      const int row = i & 15, mt = i >> 4, m = mt % M, tg = alone ? tw : mt / M;
-      const int64_t nrow = ((int64_t)(r * (int64_t)p.clusters + cluster) * group + tg) * 16 + row;
+      const int row = i % kRows, mt = i / kRows, m = alone ? mt : mt % M, tg = alone ? tw : mt / M;
+      const int64_t tile = (r * (int64_t)p.clusters + cluster) * group + tg;
+      const int64_t nrow = ld.first_row(tile, tiled) + (tiled ? 32 * (row >> 3) + (row & 7) : row);
       if (nrow >= j.N) continue;
       float v = 0.0f;
       for (int q = 0; q < S; ++q) {
-        const float *from = S > 1 ? cg::this_cluster().map_shared_rank(share, q) : share;
-        for (int w = 0; w < sk; ++w) v += from[(tg * sk + w) * (16 * kCols) + m * 16 + row];
+        const float *from = S > 1 ? cg::this_cluster().map_shared_rank(parts, q) : parts;
+        for (int w = 0; w < sk; ++w) v += from[((tg * sk + w) * kCols + m) * kRows + row];
       }
       const int shift = (KIND == kUE5M3 ? 3 : 0) + (j.shift ? j.shift[nrow] : 0);
       v = scalbnf(v, shift) * j.sd[j.stripes ? nrow >> 7 : 0];
@@ -471,7 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_matvec(const __grid_constant__ 
       else
         static_cast<__half *>(j.y)[at] = __float2half_rn(v);
     }
-    if (alone) __syncwarp();
   }
   if (!live) {  // copies still in flight land (bounded) before the ring goes away
     for (; flying > 0; --flying) {
@@ -487,15 +527,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_matvec(const __grid_constant__ 
 
 // Shared memory for M tokens over ceil(steps / S) steps, NT column tiles.
 size_t smem_bytes(int M, int steps, int S, int nt, int depth) {
+  const int kWarps = warps_of(nt);
   const size_t span = (steps + S - 1) / S;
   return (size_t)kWarps * depth * (kPayload + kWords) + kWarps * kMaxDepth * 8 + span * 8 * nt * 4 +
-         2 * kWarps * 16 * 8 * nt * 4 + M * (span * 512 + 64) + 16;
+         kWarps * kRows * 8 * nt * 4 + M * (span * 512 + 64) + 16;
 }
 
-// Payload rows as a tensor map: boxes of 16 rows x 128 bytes, swizzled; what
-// lies past the last row or column reads as zero.
-bool payload_map(CUtensorMap *m, const void *base, int64_t rows, int64_t row_bytes) {
-  return tc::make_map(m, base, rows, row_bytes, 16, kStep / 2);
+// Bytes [z][y][x] without gaps as a tensor map (2-D for z = 0), boxes of
+// box_x x box_y; what lies past an end reads as zero.
+bool byte_map(CUtensorMap *m, const void *base, int64_t x, int64_t y, int64_t z, int box_x, int box_y,
+              bool swizzle) {
+  auto fn = tc::encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)x, (cuuint64_t)y, (cuuint64_t)z};
+  cuuint64_t strides[2] = {(cuuint64_t)x, (cuuint64_t)(x * y)};
+  cuuint32_t box[3] = {(cuuint32_t)box_x, (cuuint32_t)box_y, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, z ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // What a kernel may use, asked once per kernel and device: raises its shared
@@ -505,7 +555,7 @@ struct Residence {
   std::atomic<int> clusters[4];
 };
 template <typename Kern>
-int resident(Kern kern, Residence *per_device, int S) {
+int resident(Kern kern, Residence *per_device, int S, int kThreads) {
   constexpr int kMaxDev = 64;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return -1;
@@ -536,32 +586,37 @@ int resident(Kern kern, Residence *per_device, int S) {
 template <int KIND, int BLOCK, bool TMA, typename TX, int NT>
 fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   static Residence residence[64];
+  constexpr int kWarps = warps_of(NT), kThreads = 32 * kWarps;
   auto kern = k_matvec<KIND, BLOCK, TMA, TX, NT>;
   MvParams p{};
   p.j = j;
   p.steps = (int)ceil_div(j.K, kStep);
-  p.tiles = (int)ceil_div(j.N, 16);
+  p.tiles = (int)(4 * ceil_div(j.N, 128));
   p.mc = (int)(j.M < 8 * NT ? j.M : 8 * NT);
-  p.words = j.sf_mma || (j.K / j.block) % 4 == 0;
+  const int64_t row_words = j.K / j.block;
+  p.words = j.sf_mma ? kTiled : row_words % 16 == 0 ? kBoxed : row_words % 4 == 0 ? kPieces : kBytes;
   p.status = status_word();
   if (!p.status) return FP4_ERR_CUDA;
-  if (TMA && !payload_map(&p.map, j.q, j.N, j.K / 2)) return FP4_ERR_CUDA;
+  const bool tiled = p.words == kTiled;
+  if (TMA && !byte_map(&p.map, j.q, j.K / 2, j.N, 0, kStep / 2, tiled ? 8 : kRows, true)) return FP4_ERR_CUDA;
+  if (tiled && !byte_map(&p.smap, j.sf, 512, ceil_div(row_words, 4), ceil_div(j.N, 128), 128, kStep / BLOCK / 4, false))
+    return FP4_ERR_CUDA;
+  if (p.words == kBoxed && !byte_map(&p.smap, j.sf, row_words, j.N, 0, 16, kRows, false)) return FP4_ERR_CUDA;
   // x of a CTA's tokens over its part of K beside rings of 3 stages or more:
   // more CTAs per tile until it fits; then fewer stages, then fewer tokens
   p.S = 1;
-  p.depth = 3;
+  p.depth = 2;
   while (p.S < 8 && smem_bytes(p.mc, p.steps, p.S, NT, p.depth) > (size_t)kMaxSmem) p.S *= 2;
-  if (smem_bytes(p.mc, p.steps, p.S, NT, 3) > (size_t)kMaxSmem) p.depth = 2;
   while (p.mc > 1 && smem_bytes(p.mc, p.steps, p.S, NT, p.depth) > (size_t)kMaxSmem) p.mc = (p.mc + 1) / 2;
   if (smem_bytes(p.mc, p.steps, p.S, NT, kMaxDepth) <= (size_t)kMaxSmem) p.depth = kMaxDepth;
   const size_t smem = smem_bytes(p.mc, p.steps, p.S, NT, p.depth);
   if (smem > (size_t)kMaxSmem) return FP4_ERR_SHAPE;
-  const int room = resident(kern, residence, p.S);
+  const int room = resident(kern, residence, p.S, kThreads);
   if (room < 1) return FP4_ERR_CUDA;
   // warps per tile: the fewest steps on the busiest warp; a round costs about
   // one step more for its join, so ties go to fewer and longer ones
   int64_t cost = INT64_MAX;
-  for (int sk = 1; sk <= kWarps && (sk == 1 || p.S * sk <= p.steps); sk *= 2) {
+  for (int sk = 1; sk <= kWarps && (sk == 1 || p.S * sk <= p.steps); ++sk) {
     const int group = kWarps / sk;
     const int64_t rounds = ceil_div(p.tiles, (int64_t)room * group);
     const int64_t c = rounds * (ceil_div(p.steps, (int64_t)p.S * sk) + 1);
