@@ -58,8 +58,8 @@ constexpr int kWords = 512;            // 4 scale words a row, 32 rows
 constexpr int kMaxDepth = 4;
 constexpr int kMaxSmem = 227 * 1024;
 
-// Warps of a CTA: with two token tiles a warp needs more than 128 registers.
-constexpr int warps_of(int nt) { return nt == 1 ? 16 : 12; }
+// Most warps of a CTA: with two token tiles a warp needs more than 128 registers.
+constexpr int max_warps(int nt) { return nt == 1 ? 16 : 12; }
 
 struct MvParams {
   CUtensorMap map;   // payload [N][K / 2], boxes of 32 or 8 rows x 128 bytes
@@ -67,6 +67,7 @@ struct MvParams {
   MatvecJob j;
   int steps;         // ceil(K / 256)
   int tiles;         // 4 ceil(N / 128)
+  int warps;         // of a CTA
   int sk, S;         // warps and CTAs that share a tile along K
   int rounds;        // row tiles a warp takes, one after the other
   int clusters;
@@ -234,7 +235,7 @@ __device__ __forceinline__ void scale_pairs(uint32_t w, int top, uint32_t *h) {
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 32 / BLOCK; ++i) {
+  for (int i = 0; i < 32 / BLOCK; ++i) {  // (block 32: one pair)
     if (KIND == kNVFP4) {
       asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
           : "=r"(h[i])
@@ -258,57 +259,70 @@ struct Is<__nv_bfloat16> {
 // x[0 .. M) over steps [s0, s0 + n) as f16 into shared memory, and the power
 // of two taken out of each (token, step); a warp per (token, step), eight
 // elements a lane.
-template <typename TX, int kWarps>
+template <typename TX>
 __device__ void prepare_x(const MatvecJob &j, int64_t m0, int M, int s0, int n, uint8_t *xs, int pitch,
-                          float *sx, int cols) {
+                          float *sx, int cols, int warps) {
   const TX *x = static_cast<const TX *>(j.x) + m0 * j.xs;
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (M == 1 || j.xs % 8 == 0);
   const int piece = threadIdx.x & 31;
-  for (int u = threadIdx.x >> 5; u < M * n; u += kWarps) {
-    const int m = u / n, c = u - m * n;
-    const int64_t k = (int64_t)(s0 + c) * kStep + piece * 8;
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (k < j.K) {  // K is a multiple of 16: a piece is inside or outside
+  constexpr int kBatch = 4;  // units whose loads are requested together
+  for (int u0 = threadIdx.x >> 5; u0 < M * n; u0 += kBatch * warps) {
+    uint32_t w[kBatch][4];
+    int at[kBatch], sat[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int u = u0 + i * warps;
+      w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;
+      at[i] = -1;
+      if (u >= M * n) continue;
+      const int m = u / n, c = u - m * n;
+      // piece q of lane t (piece = 8 t + q) lies at 64 q + 16 t
+      at[i] = m * pitch + c * 512 + (piece & 7) * 64 + (piece >> 3) * 16;
+      sat[i] = c * cols + m;
+      const int64_t k = (int64_t)(s0 + c) * kStep + piece * 8;
+      if (k >= j.K) continue;  // K is a multiple of 16: a piece is inside or outside
       const TX *p = x + m * j.xs + k;
       if (vec) {
         const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
       } else {
         const uint16_t *e = reinterpret_cast<const uint16_t *>(p);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) w[q] = e[2 * q] | ((uint32_t)e[2 * q + 1] << 16);
+        for (int q = 0; q < 4; ++q) w[i][q] = e[2 * q] | ((uint32_t)e[2 * q + 1] << 16);
       }
     }
-    int ex = 0;
-    if (Is<TX>::bf16) {
-      uint32_t top = 0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) top = max(top, max(w[q] & 0x7FFFu, (w[q] >> 16) & 0x7FFFu));
-      top = __reduce_max_sync(~0u, top);
-      // exponent of the largest finite magnitude (2^133 x subnormals: 1 + mantissa bits)
-      const int f = (int)(top >> 7);
-      const int e = f >= 255 ? 127 : f > 0 ? f - 127 : top ? (31 - __clz((int)top)) - 133 : 0;
-      ex = e - 15;
-      const int h1 = -ex / 2;  // 2^-ex in two factors that binary32 holds
-      const float f1 = pow2(h1), f2 = pow2(-ex - h1);
+    for (int i = 0; i < kBatch; ++i) {
+      if (at[i] < 0) continue;  // the same for all lanes of a warp
+      int ex = 0;
+      if (Is<TX>::bf16) {
+        uint32_t top = 0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const __half2 v = __floats2half2_rn(bf16_lo(w[q]) * f1 * f2, bf16_hi(w[q]) * f1 * f2);
-        w[q] = *reinterpret_cast<const uint32_t *>(&v);
+        for (int q = 0; q < 4; ++q) top = max(top, max(w[i][q] & 0x7FFFu, (w[i][q] >> 16) & 0x7FFFu));
+        top = __reduce_max_sync(~0u, top);
+        // exponent of the largest finite magnitude (2^133 x subnormals: 1 + mantissa bits)
+        const int f = (int)(top >> 7);
+        const int e = f >= 255 ? 127 : f > 0 ? f - 127 : top ? (31 - __clz((int)top)) - 133 : 0;
+        ex = e - 15;
+        const int h1 = -ex / 2;  // 2^-ex in two factors that binary32 holds
+        const float f1 = pow2(h1), f2 = pow2(-ex - h1);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const __half2 v = __floats2half2_rn(bf16_lo(w[i][q]) * f1 * f2, bf16_hi(w[i][q]) * f1 * f2);
+          w[i][q] = *reinterpret_cast<const uint32_t *>(&v);
+        }
       }
+      *reinterpret_cast<uint4 *>(xs + at[i]) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+      if (piece == 0) sx[sat[i]] = pow2(ex);
     }
-    // piece i of lane t (piece = 8 t + i) lies at 64 i + 16 t
-    *reinterpret_cast<uint4 *>(xs + m * pitch + c * 512 + (piece & 7) * 64 + (piece >> 3) * 16) =
-        make_uint4(w[0], w[1], w[2], w[3]);
-    if (piece == 0) sx[c * cols + m] = pow2(ex);
   }
 }
 
 template <int KIND, int BLOCK, bool TMA, typename TX, int NT>
-__global__ void __launch_bounds__(32 * warps_of(NT), 1) k_matvec(const __grid_constant__ MvParams p) {
+__global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_constant__ MvParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int kWarps = warps_of(NT), kThreads = 32 * kWarps;
   constexpr int kCols = 8 * NT;
+  const int kWarps = p.warps, kThreads = 32 * p.warps;
   const MatvecJob &j = p.j;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int S = p.S, sk = p.sk, depth = p.depth;
@@ -364,7 +378,7 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) k_matvec(const __grid_co
   };
   for (int d = 0; d < depth && ahead; ++d) issue();
 
-  prepare_x<TX, kWarps>(j, m0, M, c0, n, xs, pitch, sx, kCols);
+  prepare_x<TX>(j, m0, M, c0, n, xs, pitch, sx, kCols, p.warps);
   __syncthreads();
 
   const uint8_t *xl[NT];
@@ -489,28 +503,53 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) k_matvec(const __grid_co
           for (int e = 0; e < 4; ++e)
             o[(8 * c + 2 * t + (e & 1)) * kRows + g + 16 * u + 8 * (e >> 1)] = acc[c][u][e];
     }
-    sync();
-    // outputs of the round: group tiles x M tokens x 32 rows, shared by the cluster's CTAs
-    const int outs = (alone ? 1 : group) * M * kRows;
-    for (int i = alone ? lane : (int)threadIdx.x * S + rank; i < outs; i += alone ? 32 : kThreads * S) {
-      const int row = i % kRows, mt = i / kRows, m = alone ? mt : mt % M, tg = alone ? tw : mt / M;
+    // outputs of the round: group tiles x M tokens x 32 rows, shared by the
+    // cluster's CTAs; what each is multiplied by is requested before the wait
+    const int outs = (alone ? 1 : group) * M * kRows, hops = alone ? 32 : kThreads * S;
+    int i = alone ? lane : (int)threadIdx.x * S + rank;
+    auto place = [&](int o, int &tg, int &m) {
+      const int mt = o / kRows, row = o % kRows;
+      tg = alone ? tw : mt / M;
+      m = alone ? mt : mt - tg * M;
       const int64_t tile = (r * (int64_t)p.clusters + cluster) * group + tg;
-      const int64_t nrow = ld.first_row(tile, tiled) + (tiled ? 32 * (row >> 3) + (row & 7) : row);
-      if (nrow >= j.N) continue;
-      float v = 0.0f;
-      for (int q = 0; q < S; ++q) {
-        const float *from = S > 1 ? cg::this_cluster().map_shared_rank(parts, q) : parts;
-        for (int w = 0; w < sk; ++w) v += from[((tg * sk + w) * kCols + m) * kRows + row];
+      return ld.first_row(tile, tiled) + (tiled ? 32 * (row >> 3) + (row & 7) : row);
+    };
+    auto factors = [&](int64_t n, int &shift, float &sd) {
+      shift = KIND == kUE5M3 ? 3 : 0;
+      if (n >= j.N) return;
+      if (j.shift) shift += j.shift[n];
+      sd = j.sd[j.stripes ? n >> 7 : 0];
+    };
+    int tg = 0, m = 0, shift = 0;
+    float sd = 0.0f;
+    int64_t n = j.N;
+    if (i < outs) {
+      n = place(i, tg, m);
+      factors(n, shift, sd);
+    }
+    sync();
+    while (i < outs) {
+      if (n < j.N) {
+        float v = 0.0f;
+        for (int q = 0; q < S; ++q) {
+          const float *from = S > 1 ? cg::this_cluster().map_shared_rank(parts, q) : parts;
+          from += (tg * sk * kCols + m) * kRows + i % kRows;
+          for (int w = 0; w < sk; ++w) v += from[w * kCols * kRows];
+        }
+        v = scalbnf(v, shift) * sd;
+        const int64_t at = (m0 + m) * j.ys + n;
+        if (j.y_type == FP4_F32)
+          static_cast<float *>(j.y)[at] = v;
+        else if (j.y_type == FP4_BF16)
+          static_cast<__nv_bfloat16 *>(j.y)[at] = __float2bfloat16_rn(v);
+        else
+          static_cast<__half *>(j.y)[at] = __float2half_rn(v);
       }
-      const int shift = (KIND == kUE5M3 ? 3 : 0) + (j.shift ? j.shift[nrow] : 0);
-      v = scalbnf(v, shift) * j.sd[j.stripes ? nrow >> 7 : 0];
-      const int64_t at = (m0 + m) * j.ys + nrow;
-      if (j.y_type == FP4_F32)
-        static_cast<float *>(j.y)[at] = v;
-      else if (j.y_type == FP4_BF16)
-        static_cast<__nv_bfloat16 *>(j.y)[at] = __float2bfloat16_rn(v);
-      else
-        static_cast<__half *>(j.y)[at] = __float2half_rn(v);
+      i += hops;
+      if (i < outs) {
+        n = place(i, tg, m);
+        factors(n, shift, sd);
+      }
     }
   }
   if (!live) {  // copies still in flight land (bounded) before the ring goes away
@@ -526,11 +565,10 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) k_matvec(const __grid_co
 }
 
 // Shared memory for M tokens over ceil(steps / S) steps, NT column tiles.
-size_t smem_bytes(int M, int steps, int S, int nt, int depth) {
-  const int kWarps = warps_of(nt);
+size_t smem_bytes(int M, int steps, int S, int nt, int warps, int depth) {
   const size_t span = (steps + S - 1) / S;
-  return (size_t)kWarps * depth * (kPayload + kWords) + kWarps * kMaxDepth * 8 + span * 8 * nt * 4 +
-         kWarps * kRows * 8 * nt * 4 + M * (span * 512 + 64) + 16;
+  return (size_t)warps * depth * (kPayload + kWords) + warps * kMaxDepth * 8 + span * 8 * nt * 4 +
+         warps * kRows * 8 * nt * 4 + M * (span * 512 + 64) + 16;
 }
 
 // Bytes [z][y][x] without gaps as a tensor map (2-D for z = 0), boxes of
@@ -586,7 +624,6 @@ int resident(Kern kern, Residence *per_device, int S, int kThreads) {
 template <int KIND, int BLOCK, bool TMA, typename TX, int NT>
 fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   static Residence residence[64];
-  constexpr int kWarps = warps_of(NT), kThreads = 32 * kWarps;
   auto kern = k_matvec<KIND, BLOCK, TMA, TX, NT>;
   MvParams p{};
   p.j = j;
@@ -602,22 +639,29 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   if (tiled && !byte_map(&p.smap, j.sf, 512, ceil_div(row_words, 4), ceil_div(j.N, 128), 128, kStep / BLOCK / 4, false))
     return FP4_ERR_CUDA;
   if (p.words == kBoxed && !byte_map(&p.smap, j.sf, row_words, j.N, 0, 16, kRows, false)) return FP4_ERR_CUDA;
-  // x of a CTA's tokens over its part of K beside rings of 3 stages or more:
-  // more CTAs per tile until it fits; then fewer stages, then fewer tokens
+  // x of a CTA's tokens over its part of K beside the rings: more CTAs per
+  // tile until 12 warps fit (measured, 8 tokens, 4096 x 14336: 2 CTAs of 11
+  // warps 21.5 us, 4 of 12 17.8; 16 tokens, 14336 x 4096: 1 CTA of 8 warps
+  // 29.6 us, 2 of 12 20.1), then fewer warps, then fewer tokens
+  auto fits = [&](int warps, int depth) {
+    return smem_bytes(p.mc, p.steps, p.S, NT, warps, depth) <= (size_t)kMaxSmem;
+  };
   p.S = 1;
+  while (p.S < 8 && !fits(12, 2)) p.S *= 2;
+  while (p.mc > 1 && !fits(8, 2)) p.mc = (p.mc + 1) / 2;
+  if (!fits(8, 2)) return FP4_ERR_SHAPE;
+  p.warps = max_warps(NT);
+  while (!fits(p.warps, 2)) --p.warps;
   p.depth = 2;
-  while (p.S < 8 && smem_bytes(p.mc, p.steps, p.S, NT, p.depth) > (size_t)kMaxSmem) p.S *= 2;
-  while (p.mc > 1 && smem_bytes(p.mc, p.steps, p.S, NT, p.depth) > (size_t)kMaxSmem) p.mc = (p.mc + 1) / 2;
-  if (smem_bytes(p.mc, p.steps, p.S, NT, kMaxDepth) <= (size_t)kMaxSmem) p.depth = kMaxDepth;
-  const size_t smem = smem_bytes(p.mc, p.steps, p.S, NT, p.depth);
-  if (smem > (size_t)kMaxSmem) return FP4_ERR_SHAPE;
-  const int room = resident(kern, residence, p.S, kThreads);
+  while (p.depth < kMaxDepth && fits(p.warps, p.depth + 1)) ++p.depth;
+  const size_t smem = smem_bytes(p.mc, p.steps, p.S, NT, p.warps, p.depth);
+  const int room = resident(kern, residence, p.S, 32 * max_warps(NT));
   if (room < 1) return FP4_ERR_CUDA;
   // warps per tile: the fewest steps on the busiest warp; a round costs about
   // one step more for its join, so ties go to fewer and longer ones
   int64_t cost = INT64_MAX;
-  for (int sk = 1; sk <= kWarps && (sk == 1 || p.S * sk <= p.steps); ++sk) {
-    const int group = kWarps / sk;
+  for (int sk = 1; sk <= p.warps && (sk == 1 || p.S * sk <= p.steps); ++sk) {
+    const int group = p.warps / sk;
     const int64_t rounds = ceil_div(p.tiles, (int64_t)room * group);
     const int64_t c = rounds * (ceil_div(p.steps, (int64_t)p.S * sk) + 1);
     if (c >= cost) continue;
@@ -627,7 +671,7 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
     p.clusters = (int)ceil_div(p.tiles, rounds * group);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * p.warps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
