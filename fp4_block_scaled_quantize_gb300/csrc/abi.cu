@@ -353,7 +353,7 @@ fp4_status check_cache(const fp4_kv_cache &c) {
     return FP4_ERR_INVALID_ARG;
   if (c.head_dim > 256) return FP4_ERR_SHAPE;
   // positions are 32-bit
-  if ((int64_t)c.seq_pages * c.page_size > INT32_MAX) return FP4_ERR_SHAPE;
+  if ((int64_t)c.seq_pages * c.page_size > INT32_MAX - 1024) return FP4_ERR_SHAPE;
   if (c.k_page < 0 || c.k_place < 0 || c.k_head < 0 || c.v_page < 0 || c.v_place < 0 ||
       c.v_head < 0 || c.table_stride < 0)
     return FP4_ERR_INVALID_ARG;

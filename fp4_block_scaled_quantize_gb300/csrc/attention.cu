@@ -1,9 +1,36 @@
 // attention.cu -- attention of one new token per sequence over a paged cache
 // (sm_103a):  out = sum_j w_j v_j,  w = softmax_j(scale q . k_j).
 //
-// First form: one CTA per sequence and query head; each warp walks every
-// fourth position with a running maximum and sum in binary32, the four are
-// joined in shared memory.
+// Bound: HBM, every key and value of the seen positions read once (4 D bytes
+// per position and key head); at 6.8 TB/s an SM moves 23 bytes a clock, so the
+// 2 x 8 NT MMAs per 16 positions are cheap even on the m16n8k16 path, and no
+// part of the cache needs to pass through shared memory.
+//
+// Mathematics.  Scores in binary32 (times scale log2 e), a running maximum m
+// and sum l per query head with weights 2^(s - m).  m is moved only when a
+// score passes it by more than 8 (weights stay below 2^8): most steps then
+// need no reduction over lanes and no rescaling.  A weight enters its product
+// with the values as two 16-bit parts (hi + lo, 2^-16 of it left out) and
+// the sum l as it is, so rounding weights costs no accuracy; the products are
+// summed in binary32.
+//
+// Layout.  Query heads that share a key head are the 8 columns of an MMA (NT
+// tiles of 8), positions or head elements its 16 rows:
+//   S^T = K Q^T   lane (g, t) loads 16-byte pieces 32 i + 8 t of keys g, g + 8
+//   O^T = V^T P^T lane (g, t) loads 16-byte pieces 64 i + 8 g of values
+//                 2 t, 2 t + 1, 2 t + 8, 2 t + 9 and pairs positions by byte
+//                 permutes; P^T is transposed in registers (movmatrix)
+// The order of k within an MMA is free, so both operands come from global
+// memory in whole 16-byte pieces, straight into registers: the keys of the
+// next 16 positions are requested as soon as this step's are multiplied, the
+// values likewise, and page numbers a step ahead of both.
+//
+// Split.  The 64-position tiles of all (sequence, key head, head group) rows
+// form one list that the resident CTAs share out evenly, whatever the
+// lengths; the four warps of a CTA take 16 positions of each tile.  A CTA
+// writes the rows it holds whole and leaves at most two partial rows (m, l,
+// O) in the workspace; a second, dependent launch joins those in CTA order,
+// so results repeat exactly.
 #include <cmath>
 
 #include "serve.cuh"
@@ -12,88 +39,615 @@ namespace fp4 {
 
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32, kPer = 8;  // 8 elements of a head per lane
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kTile = 16 * kWarps;   // positions of a tile
+constexpr int kPerSM = 4;            // CTAs per SM at most (workspace bound)
+constexpr float kSlack = 8.0f;       // log2 by which scores may pass the maximum in use
 
+struct AtParams {
+  fp4_attention_params p;
+  int groups;   // head groups of a key head: ceil(heads / kv_heads / (8 NT))
+  int share;    // heads / kv_heads
+  int ctas;     // CTAs of the main kernel
+  int shift;    // log2 page_size, or -1: pages of any size
+  int out16;    // rows of out allow 16-byte stores
+  float scale2; // scale * log2 e
+  float *ws;    // [ctas][2] partial rows
+  uint32_t *status;
+};
+
+// Partial row: 8 NT x DP outputs, then m, l and seen (1.0 or 0.0) per head.
+constexpr int slot_floats(int cols, int dp) { return cols * (dp + 3 + 1); }
+
+__device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1, __nv_bfloat16) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1, __half) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint4 load16(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// Two values as a pair of T, and what the pair leaves of them.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_attention(fp4_attention_params p, uint32_t *status) {
-  const fp4_kv_cache &c = p.cache;
-  const int D = c.head_dim, s = blockIdx.x, h = blockIdx.y;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int64_t hk = h / (p.heads / c.kv_heads);
-  const int64_t room = (int64_t)c.seq_pages * c.page_size;
-  int64_t len = p.lengths[s];
-  if ((len < 0 || len > room) && threadIdx.x == 0) raise_status(status, kStatusIndex);
-  len = len < 0 ? 0 : (len > room ? room : len);
-  const int64_t from = p.window && len > p.window ? len - p.window : 0;
-  float q[kPer], acc[kPer], top = -INFINITY, sum = 0.0f;
-  const T *qp = static_cast<const T *>(p.q) + s * p.q_seq + h * p.q_head;
-  for (int i = 0; i < kPer; ++i) {
-    q[i] = lane + 32 * i < D ? to_f32(qp[lane + 32 * i]) * p.scale : 0.0f;
-    acc[i] = 0.0f;
+__device__ __forceinline__ uint32_t pack(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t w) {
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+template <>
+__device__ __forceinline__ float2 unpack<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// What of a sequence is seen: positions [from, len); its tiles start at base.
+struct Span {
+  int from, len, base, tiles;
+};
+__device__ __forceinline__ Span span_of(const AtParams &a, int s) {
+  const fp4_kv_cache &c = a.p.cache;
+  const int64_t room = (int64_t)c.seq_pages * c.page_size;  // fits 32 bits
+  const int given = a.p.lengths[s];
+  Span r;
+  r.len = given < 0 ? 0 : given > room ? (int)room : given;
+  r.from = a.p.window && r.len > a.p.window ? r.len - a.p.window : 0;
+  r.base = r.from & ~15;
+  r.tiles = (r.len - r.base + kTile - 1) / kTile;
+  return r;
+}
+
+// Prefix over the sequences: the sum of rows * tiles of all, and where x
+// (which < 0: the first tile of a CTA's slice; else the start of sequence `which`) lies.
+struct Found {
+  int64_t total, start;  // start: list index of the found sequence's first tile
+  int64_t ctas;          // CTAs that share the list: no more than it has tiles
+  int seq;               // seqs: x is past the end
+};
+__device__ Found find(const AtParams &a, int rows, int64_t slice, int which, int64_t *shared) {
+  const int seqs = a.p.cache.seqs, per = (seqs + kThreads - 1) / kThreads;
+  const int s0 = threadIdx.x * per, s1 = min(s0 + per, seqs);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t sum = 0;
+  for (int s = s0; s < s1; ++s) sum += (int64_t)rows * span_of(a, s).tiles;
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(~0u, inc, o);
+    if (lane >= o) inc += v;
   }
+  if (lane == 31) shared[warp] = inc;
+  if (threadIdx.x == 0) shared[kWarps] = seqs, shared[kWarps + 1] = 0;
+  __syncthreads();
+  int64_t before = inc - sum, total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += shared[w];
+    total += shared[w];
+  }
+  const int64_t ctas = min((int64_t)a.ctas, total);
+  const int64_t x = slice < ctas ? total * slice / ctas : total;
+  if (which < 0 ? x >= before && x < before + sum : which >= s0 && which < s1) {
+    int64_t at = before;
+    for (int s = s0; s < s1; ++s) {
+      const int64_t n = (int64_t)rows * span_of(a, s).tiles;
+      if (which < 0 ? x < at + n : s == which) {
+        shared[kWarps] = s;
+        shared[kWarps + 1] = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  Found f;
+  f.total = total;
+  f.ctas = ctas;
+  f.seq = (int)shared[kWarps];
+  f.start = shared[kWarps + 1];
+  __syncthreads();
+  return f;
+}
+
+// Eight outputs of a row, rounded once.
+template <typename T>
+__device__ __forceinline__ void store8(const AtParams &a, int s, int head, int d, const float *v) {
+  T *out = static_cast<T *>(a.p.out) + s * a.p.out_seq + head * a.p.out_head + d;
+  if (a.out16) {
+    *reinterpret_cast<uint4 *>(out) = make_uint4(pack<T>(v[0], v[1]), pack<T>(v[2], v[3]),
+                                                 pack<T>(v[4], v[5]), pack<T>(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = from_f32<T>(v[i]);
+  }
+}
+
+// The parts of a row joined: `get(i, m, l, seen)` gives part i's statistics,
+// `add(i, w, v)` adds w times its eight outputs.  Writes the row's result.
+template <typename T, typename Get, typename Add>
+__device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d, int parts, Get get,
+                                       Add add) {
+  float top = -INFINITY, sum = 0.0f;
   bool any = false;
-  for (int64_t j = from + warp; j < len; j += kWarps) {
-    const int64_t page = c.table[s * c.table_stride + j / c.page_size], place = j % c.page_size;
-    if (page < 0 || page >= c.pages) {
-      if (lane == 0) raise_status(status, kStatusIndex);
+  for (int i = 0; i < parts; ++i) {
+    float m, l;
+    bool seen;
+    get(i, m, l, seen);
+    top = fmaxf(top, m);
+    any |= seen;
+  }
+  const float base = top == -INFINITY ? 0.0f : top;
+  float v[8] = {};
+  for (int i = 0; i < parts; ++i) {
+    float m, l;
+    bool seen;
+    get(i, m, l, seen);
+    const float w = ex2(m - base);
+    sum += w * l;
+    add(i, w, v);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = any ? v[i] / sum : 0.0f;
+  store8<T>(a, s, head, d, v);
+  if (a.p.lse && d == 0)
+    a.p.lse[(int64_t)s * a.p.heads + head] = any ? (base + log2f(sum)) * 0.693147180559945f : -INFINITY;
+}
+
+template <typename T, int DP, int NT, bool POW2>
+__global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
+    k_attention(const __grid_constant__ AtParams a) {
+  constexpr int kCols = 8 * NT, kKey = DP / 32, kVal = DP / 64;
+  // wide heads: keys and values take turns in the same registers
+  constexpr bool kTurns = DP > 128;
+  extern __shared__ __align__(16) float smem[];
+  __shared__ int64_t scan[kWarps + 2];
+  float *o_sh = smem;                                // [kWarps][kCols][DP + 8]
+  float *st_sh = smem + kWarps * kCols * (DP + 8);   // [3][kWarps][kCols]: m, l, seen
+  const fp4_kv_cache &c = a.p.cache;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int D = c.head_dim, rows = c.kv_heads * a.groups;
+
+  const Found f = find(a, rows, blockIdx.x, -1, scan);
+  if (blockIdx.x >= f.ctas) return;
+  int64_t at = f.total * blockIdx.x / f.ctas;
+  const int64_t end = f.total * (blockIdx.x + 1) / f.ctas;
+  int s = f.seq;
+  int64_t start = f.start;
+
+  while (at < end) {
+    const Span sp = span_of(a, s);
+    const int64_t mine = (int64_t)rows * sp.tiles;
+    if (at >= start + mine) {  // on to the next sequence
+      start += mine;
+      ++s;
       continue;
     }
-    any = true;
-    const T *k = static_cast<const T *>(c.k) + page * c.k_page + place * c.k_place + hk * c.k_head;
-    const T *v = static_cast<const T *>(c.v) + page * c.v_page + place * c.v_place + hk * c.v_head;
-    float dot = 0.0f;
-    for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i < D) dot = fmaf(q[i], to_f32(k[lane + 32 * i]), dot);
-    for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
-    const float now = fmaxf(top, dot), base = now == -INFINITY ? 0.0f : now;
-    const float fade = expf(top - base), w = expf(dot - base);
-    top = now;
-    sum = sum * fade + w;
-    for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i < D) acc[i] = fmaf(w, to_f32(v[lane + 32 * i]), acc[i] * fade);
+    const int row = (int)((at - start) / sp.tiles), tile0 = (int)(at - start - (int64_t)row * sp.tiles);
+    const int tile1 = (int)min((int64_t)sp.tiles, tile0 + (end - at));
+    const int kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
+    const int heads = min(kCols, (kvh + 1) * a.share - head0);
+    at += tile1 - tile0;
+
+    // queries: heads past the group's repeat as zero
+    uint4 q[NT][kKey];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < kKey; ++i) {
+        const int d = 32 * i + 8 * t;
+        q[n][i] = 8 * n + g < heads && d < D
+                      ? load16(static_cast<const T *>(a.p.q) + s * a.p.q_seq + (head0 + 8 * n + g) * a.p.q_head + d)
+                      : make_uint4(0, 0, 0, 0);
+      }
+
+    float m[NT][2], l[NT][2], o[NT][kVal][4][4];
+    bool seen;
+    const int32_t *table = c.table + s * c.table_stride;
+    const int stop = min(sp.len, sp.base + kTile * tile1);
+    // The pages of the 16 positions from pos on: pages of 16 or more places
+    // hold them all on one (every lane has its number); else lane i & 15 has
+    // position i's.
+    struct Where {
+      int page, place;
+    };
+    auto lookup = [&](int pos) {
+      Where w;
+      w.page = -1, w.place = 0;
+      if (POW2) {
+        if (pos < stop) w.page = __ldg(table + (pos >> a.shift));
+        w.place = pos & (c.page_size - 1);
+      } else {
+        const int i = pos + (lane & 15);
+        if (i >= sp.from && i < stop) {
+          const int e = i / c.page_size;
+          w.page = __ldg(table + e);
+          w.place = i - e * c.page_size;
+        }
+      }
+      return w;
+    };
+    // Position i of the 16: true if it is seen and its page exists.
+    auto place_of = [&](const Where &w, int pos, int i, int64_t &page, int64_t &place) {
+      int pg = w.page, pl = w.place + i;
+      if (!POW2) {
+        pg = __shfl_sync(~0u, w.page, i);
+        pl = __shfl_sync(~0u, w.place, i);
+      }
+      page = pg;
+      place = pl;
+      return pos + i >= sp.from && pos + i < stop && pg >= 0 && pg < c.pages;
+    };
+    uint4 key[2][kKey], val[4][kVal];
+    bool key_on[2], key_next[2];
+    auto load_keys = [&](const Where &w, int pos) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        int64_t page, place;
+        key_next[h] = place_of(w, pos, g + 8 * h, page, place);
+        const T *k = static_cast<const T *>(c.k) + page * c.k_page + place * c.k_place + kvh * c.k_head + 8 * t;
+#pragma unroll
+        for (int i = 0; i < kKey; ++i)
+          key[h][i] = key_next[h] && 32 * i + 8 * t < D ? load16(k + 32 * i) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto load_values = [&](const Where &w, int pos) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        int64_t page, place;
+        const bool on = place_of(w, pos, 2 * t + (h & 1) + 8 * (h >> 1), page, place);
+        const T *v = static_cast<const T *>(c.v) + page * c.v_page + place * c.v_place + kvh * c.v_head + 8 * g;
+#pragma unroll
+        for (int i = 0; i < kVal; ++i)  // what is not seen is not read: zero weights times zeros
+          val[h][i] = on && 64 * i + 8 * g < D ? load16(v + 64 * i) : make_uint4(0, 0, 0, 0);
+      }
+    };
+
+    // A value that is not finite makes lo x value a NaN where hi x value is an
+    // infinity: a warp whose sums are not finite repeats its part without lo.
+    for (bool both = true;; both = false) {
+    seen = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kVal; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[n][i][j][0] = o[n][i][j][1] = o[n][i][j][2] = o[n][i][j][3] = 0.0f;
+    }
+    int pos = sp.base + kTile * tile0 + 16 * warp;
+    Where now = lookup(pos), next = lookup(pos + kTile);
+    load_keys(now, pos);
+    if (!kTurns) load_values(now, pos);
+    for (; pos < stop; pos += kTile) {
+      key_on[0] = key_next[0];
+      key_on[1] = key_next[1];
+      // a page that is not in the cache
+      if (POW2 ? (now.page < 0 || now.page >= c.pages) && lane == 0
+               : lane < 16 && pos + lane >= sp.from && pos + lane < stop && (now.page < 0 || now.page >= c.pages))
+        raise_status(a.status, kStatusIndex);
+      float sc[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kKey; ++i) {
+          mma(sc[n], key[0][i].x, key[1][i].x, key[0][i].y, key[1][i].y, q[n][i].x, q[n][i].y, T());
+          mma(sc[n], key[0][i].z, key[1][i].z, key[0][i].w, key[1][i].w, q[n][i].z, q[n][i].w, T());
+        }
+      }
+      if (kTurns)
+        load_values(now, pos);
+      else
+        load_keys(next, pos + kTile);
+      // weights: lane (g, t) has positions g, g + 8 of heads 2 t, 2 t + 1
+      seen |= key_on[0] || key_on[1];
+      bool passed = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sc[n][e] = key_on[e >> 1] ? sc[n][e] * a.scale2 : -INFINITY;
+          passed |= sc[n][e] > m[n][e & 1] + kSlack;
+        }
+      }
+      if (__any_sync(~0u, passed)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(sc[n][e], sc[n][2 + e]);
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+            top = fmaxf(top, m[n][e]);
+            const float fade = ex2(m[n][e] - (top == -INFINITY ? 0.0f : top));
+            m[n][e] = top;
+            l[n][e] *= fade;
+#pragma unroll
+            for (int i = 0; i < kVal; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                o[n][i][j][e] *= fade;
+                o[n][i][j][2 + e] *= fade;
+              }
+          }
+      }
+      uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float base = m[n][e & 1];
+          w[e] = ex2(sc[n][e] - (base == -INFINITY ? 0.0f : base));
+          l[n][e & 1] += w[e];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t p = pack<T>(w[2 * h], w[2 * h + 1]);
+          const float2 r = unpack<T>(p);
+          hi[n][h] = transpose8x8(p);
+          lo[n][h] = transpose8x8(pack<T>(w[2 * h] - r.x, w[2 * h + 1] - r.y));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kVal; ++i) {
+        const uint32_t *v0 = reinterpret_cast<const uint32_t *>(&val[0][i]), *v1 = reinterpret_cast<const uint32_t *>(&val[1][i]);
+        const uint32_t *v2 = reinterpret_cast<const uint32_t *>(&val[2][i]), *v3 = reinterpret_cast<const uint32_t *>(&val[3][i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // rows g, g + 8: elements 2 j, 2 j + 1 of the lane's piece
+          const uint32_t a0 = __byte_perm(v0[j], v1[j], 0x5410), a1 = __byte_perm(v0[j], v1[j], 0x7632);
+          const uint32_t a2 = __byte_perm(v2[j], v3[j], 0x5410), a3 = __byte_perm(v2[j], v3[j], 0x7632);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma(o[n][i][j], a0, a1, a2, a3, hi[n][0], hi[n][1], T());
+            if (both) mma(o[n][i][j], a0, a1, a2, a3, lo[n][0], lo[n][1], T());
+          }
+        }
+      }
+      if (kTurns)
+        load_keys(next, pos + kTile);
+      else
+        load_values(next, pos + kTile);
+      now = next;
+      next = lookup(pos + 2 * kTile);
+    }
+    float worst = 0.0f;  // NaN if a sum is not finite
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < kVal; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) worst = fmaf(o[n][i][j][e], 0.0f, worst);
+    if (!both || !__any_sync(~0u, worst != 0.0f)) break;
+    }
+
+    // join the four warps
+    seen = __any_sync(~0u, seen);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = l[n][e];
+        v += __shfl_xor_sync(~0u, v, 4);
+        v += __shfl_xor_sync(~0u, v, 8);
+        v += __shfl_xor_sync(~0u, v, 16);
+        const int col = 8 * n + 2 * t + e;
+        if (g == 0) {
+          st_sh[warp * kCols + col] = m[n][e];
+          st_sh[(kWarps + warp) * kCols + col] = v;
+          st_sh[(2 * kWarps + warp) * kCols + col] = seen ? 1.0f : 0.0f;
+        }
+        float *to = o_sh + (warp * kCols + col) * (DP + 8);
+#pragma unroll
+        for (int i = 0; i < kVal; ++i) {
+          *reinterpret_cast<float4 *>(to + 64 * i + 8 * g) =
+              make_float4(o[n][i][0][e], o[n][i][0][2 + e], o[n][i][1][e], o[n][i][1][2 + e]);
+          *reinterpret_cast<float4 *>(to + 64 * i + 8 * g + 4) =
+              make_float4(o[n][i][2][e], o[n][i][2][2 + e], o[n][i][3][e], o[n][i][3][2 + e]);
+        }
+      }
+    __syncthreads();
+    const bool whole = tile0 == 0 && tile1 == sp.tiles;
+    float *slot = a.ws + (blockIdx.x * 2 + (tile0 == 0)) * (int64_t)slot_floats(kCols, DP);
+    for (int i = threadIdx.x; i < heads * (DP / 8); i += kThreads) {
+      const int col = i / (DP / 8), d = 8 * (i % (DP / 8));
+      if (d >= D) continue;
+      auto get = [&](int w, float &pm, float &pl, bool &ps) {
+        pm = st_sh[w * kCols + col];
+        pl = st_sh[(kWarps + w) * kCols + col];
+        ps = st_sh[(2 * kWarps + w) * kCols + col] != 0.0f;
+      };
+      auto add = [&](int w, float f, float *v) {
+        const float *from = o_sh + (w * kCols + col) * (DP + 8) + d;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(f, from[e], v[e]);
+      };
+      if (whole) {
+        finish<T>(a, s, head0 + col, d, kWarps, get, add);
+        continue;
+      }
+      float top = -INFINITY, sum = 0.0f, any = 0.0f, v[8] = {};
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, st_sh[w * kCols + col]);
+      for (int w = 0; w < kWarps; ++w) {
+        float pm, pl;
+        bool ps;
+        get(w, pm, pl, ps);
+        const float f = ex2(pm - (top == -INFINITY ? 0.0f : top));
+        sum = fmaf(f, pl, sum);
+        any = ps ? 1.0f : any;
+        add(w, f, v);
+      }
+      float *to = slot + col * DP + d;
+      *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      if (d == 0) {
+        float *st = slot + kCols * DP + col * 4;
+        st[0] = top;
+        st[1] = sum;
+        st[2] = any;
+      }
+    }
+    __syncthreads();
   }
-  __shared__ float tops[kWarps], sums[kWarps], accs[kWarps][32 * kPer];
-  __shared__ int anys[kWarps];
-  if (lane == 0) {
-    tops[warp] = top;
-    sums[warp] = sum;
-    anys[warp] = any;
+}
+
+// Joins the partial rows of each (sequence, head group) and writes the rows
+// of sequences that see nothing.
+template <typename T, int DP, int NT>
+__global__ void __launch_bounds__(kThreads) k_attention_join(const __grid_constant__ AtParams a) {
+  constexpr int kCols = 8 * NT;
+  __shared__ int64_t scan[kWarps + 2];
+  dependent_wait();
+  const fp4_kv_cache &c = a.p.cache;
+  const int rows = c.kv_heads * a.groups, s = blockIdx.x / rows, row = blockIdx.x - s * rows;
+  const Found f = find(a, rows, 0, s, scan);
+  const int tiles = span_of(a, s).tiles;
+  if (row == 0 && threadIdx.x == 0) {
+    const int n = a.p.lengths[s];
+    if (n < 0 || n > (int64_t)c.seq_pages * c.page_size) raise_status(a.status, kStatusIndex);
   }
-  for (int i = 0; i < kPer; ++i) accs[warp][lane + 32 * i] = acc[i];
-  __syncthreads();
-  if (warp) return;
-  float all = -INFINITY, total = 0.0f;
-  int seen = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    all = fmaxf(all, tops[w]);
-    seen |= anys[w];
+  const int kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
+  const int heads = min(kCols, (kvh + 1) * a.share - head0);
+  int first = 0, parts = 0;
+  if (tiles) {
+    const int64_t x0 = f.start + (int64_t)row * tiles, x1 = x0 + tiles - 1;
+    first = (int)(((x0 + 1) * f.ctas - 1) / f.total);  // the CTA whose share holds the tile
+    parts = (int)(((x1 + 1) * f.ctas - 1) / f.total) - first + 1;
+    if (parts == 1) return;  // written whole
   }
-  const float base = all == -INFINITY ? 0.0f : all;
-  for (int w = 0; w < kWarps; ++w) total += sums[w] * expf(tops[w] - base);
-  T *out = static_cast<T *>(p.out) + s * p.out_seq + h * p.out_head;
-  for (int i = 0; i < kPer; ++i) {
-    const int d = lane + 32 * i;
-    if (d >= D) break;
-    float v = 0.0f;
-    for (int w = 0; w < kWarps; ++w) v += accs[w][d] * expf(tops[w] - base);
-    out[d] = from_f32<T>(seen ? v / total : 0.0f);
+  for (int i = threadIdx.x; i < heads * (DP / 8); i += kThreads) {
+    const int col = i / (DP / 8), d = 8 * (i % (DP / 8));
+    if (d >= c.head_dim) continue;
+    auto slot = [&](int w) {
+      return a.ws + ((int64_t)(first + w) * 2 + (w == 0)) * slot_floats(kCols, DP);
+    };
+    finish<T>(
+        a, s, head0 + col, d, parts,
+        [&](int w, float &m, float &l, bool &seen) {
+          const float *st = slot(w) + kCols * DP + col * 4;
+          m = st[0], l = st[1], seen = st[2] != 0.0f;
+        },
+        [&](int w, float fw, float *v) {
+          const float *from = slot(w) + col * DP + d;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = fmaf(fw, from[e], v[e]);
+        });
   }
-  if (p.lse && lane == 0) p.lse[(int64_t)s * p.heads + h] = seen ? base + logf(total) : -INFINITY;
+}
+
+constexpr int dp_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256; }
+// Two tiles of 8 heads where a key head serves more than 8, but not for wide
+// heads: their queries and sums would not fit the registers.
+constexpr int nt_of(int share, int dp) { return share > 8 && dp <= 128 ? 2 : 1; }
+
+template <typename T, int DP, int NT, bool POW2>
+fp4_status launch(AtParams a, cudaStream_t s) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> occupancy[kMaxDev];
+  constexpr int cols = 8 * NT;
+  const size_t smem = (kWarps * cols * (DP + 8) + 3 * kWarps * cols) * sizeof(float);
+  auto kern = k_attention<T, DP, NT, POW2>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return FP4_ERR_CUDA;
+  int per = occupancy[dev].load(std::memory_order_acquire);
+  if (!per) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, kThreads, smem) != cudaSuccess || per < 1)
+      return FP4_ERR_CUDA;
+    occupancy[dev].store(per, std::memory_order_release);
+  }
+  const fp4_kv_cache &c = a.p.cache;
+  // no more CTAs than the table has tiles
+  const int64_t rows = (int64_t)c.seqs * c.kv_heads * a.groups;
+  const int64_t room = rows * ceil_div((int64_t)c.seq_pages * c.page_size, kTile);
+  const int64_t most = (int64_t)sm_count() * (per < kPerSM ? per : kPerSM);
+  a.ctas = (int)(room < most ? room : most);
+  if (rows > INT32_MAX) return FP4_ERR_SHAPE;
+  if (a.ctas > 0) {
+    kern<<<(unsigned)a.ctas, kThreads, smem, s>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return FP4_ERR_CUDA;
+  }
+  return launch_dependent(k_attention_join<T, DP, NT>, dim3((unsigned)rows), dim3(kThreads), 0, s, a) == cudaSuccess
+             ? FP4_OK
+             : FP4_ERR_CUDA;
+}
+
+template <typename T, int DP, int NT>
+fp4_status launch_pages(const AtParams &a, cudaStream_t s) {
+  return a.shift >= 0 ? launch<T, DP, NT, true>(a, s) : launch<T, DP, NT, false>(a, s);
+}
+
+template <typename T>
+fp4_status launch_type(const AtParams &a, int nt, cudaStream_t s) {
+  switch (dp_of(a.p.cache.head_dim)) {
+    case 64: return nt == 1 ? launch_pages<T, 64, 1>(a, s) : launch_pages<T, 64, 2>(a, s);
+    case 128: return nt == 1 ? launch_pages<T, 128, 1>(a, s) : launch_pages<T, 128, 2>(a, s);
+    case 192: return launch_pages<T, 192, 1>(a, s);
+    default: return launch_pages<T, 256, 1>(a, s);
+  }
 }
 
 }  // namespace
 
-int64_t decode_attention_workspace(int heads, int kv_heads, int head_dim) { return 0; }
+int64_t decode_attention_workspace(int heads, int kv_heads, int head_dim) {
+  const int dp = dp_of(head_dim), cols = 8 * nt_of(heads / kv_heads, dp);
+  return (int64_t)sm_count() * kPerSM * 2 * slot_floats(cols, dp) * sizeof(float);
+}
 
 fp4_status launch_decode_attention(const fp4_attention_params &p, cudaStream_t s) {
-  uint32_t *status = status_word();
-  if (!status) return FP4_ERR_CUDA;
-  const dim3 grid((unsigned)p.cache.seqs, (unsigned)p.heads);
-  if (p.cache.type == FP4_BF16)
-    k_attention<__nv_bfloat16><<<grid, kThreads, 0, s>>>(p, status);
-  else
-    k_attention<__half><<<grid, kThreads, 0, s>>>(p, status);
-  return cudaGetLastError() == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
+  AtParams a{};
+  a.p = p;
+  a.status = status_word();
+  if (!a.status) return FP4_ERR_CUDA;
+  const fp4_kv_cache &c = p.cache;
+  a.share = p.heads / c.kv_heads;
+  const int nt = nt_of(a.share, dp_of(c.head_dim));
+  a.groups = (a.share + 8 * nt - 1) / (8 * nt);
+  a.shift = -1;
+  if (c.page_size >= 16 && (c.page_size & (c.page_size - 1)) == 0)
+    for (a.shift = 4; (1 << a.shift) < c.page_size;) ++a.shift;
+  a.out16 = aligned16(p.out) && p.out_seq % 8 == 0 && p.out_head % 8 == 0;
+  a.scale2 = p.scale * 1.44269504088896f;
+  a.ws = static_cast<float *>(p.workspace);
+  return c.type == FP4_BF16 ? launch_type<__nv_bfloat16>(a, nt, s) : launch_type<__half>(a, nt, s);
 }
 
 }  // namespace fp4
