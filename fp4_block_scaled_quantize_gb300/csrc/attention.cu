@@ -40,19 +40,23 @@ namespace fp4 {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kTile = 16 * kWarps;   // positions of a tile
-constexpr int kPerSM = 4;            // CTAs per SM at most (workspace bound)
+// Groups of 16 positions a warp takes a step: what it keeps in flight.
+constexpr int units_of(int dp, int nt) { return dp <= 64 ? 2 : dp <= 128 && nt == 1 ? 1 : 1; }
+constexpr int kPerSM = 5;            // CTAs per SM at most (workspace bound)
 constexpr float kSlack = 8.0f;       // log2 by which scores may pass the maximum in use
 
 struct AtParams {
   fp4_attention_params p;
   int groups;   // head groups of a key head: ceil(heads / kv_heads / (8 NT))
   int share;    // heads / kv_heads
+  int tile;     // positions of a tile: 16 per unit and warp
   int ctas;     // CTAs of the main kernel
+  int direct;   // each takes one row, whole
   int shift;    // log2 page_size, or -1: pages of any size
   int out16;    // rows of out allow 16-byte stores
   float scale2; // scale * log2 e
   float *ws;    // [ctas][2] partial rows
+  int4 *cuts;   // [ctas] the row cut where a slice begins: sequence, row, first CTA, parts
   uint32_t *status;
 };
 
@@ -74,6 +78,11 @@ __device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Lets the join be set up while this grid runs; it waits for its completion
+// (and memory) before it reads anything.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -128,19 +137,38 @@ __device__ __forceinline__ Span span_of(const AtParams &a, int s) {
   r.len = given < 0 ? 0 : given > room ? (int)room : given;
   r.from = a.p.window && r.len > a.p.window ? r.len - a.p.window : 0;
   r.base = r.from & ~15;
-  r.tiles = (r.len - r.base + kTile - 1) / kTile;
+  r.tiles = (r.len - r.base + a.tile - 1) / a.tile;
   return r;
 }
 
-// Prefix over the sequences: the sum of rows * tiles of all, and where x
-// (which < 0: the first tile of a CTA's slice; else the start of sequence `which`) lies.
+// Prefix over the sequences: the sum of rows * tiles of all, and the sequence
+// in which a slice of the list begins.
 struct Found {
   int64_t total, start;  // start: list index of the found sequence's first tile
   int64_t ctas;          // CTAs that share the list: no more than it has tiles
-  int seq;               // seqs: x is past the end
+  int seq;
 };
-__device__ Found find(const AtParams &a, int rows, int64_t slice, int which, int64_t *shared) {
-  const int seqs = a.p.cache.seqs, per = (seqs + kThreads - 1) / kThreads;
+template <int THREADS>
+__device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *shared) {
+  constexpr int kW = THREADS / 32;
+  const int seqs = a.p.cache.seqs, per = (seqs + THREADS - 1) / THREADS;
+  if (seqs <= 32) {  // each warp by itself
+    const int lane = threadIdx.x & 31;
+    const int64_t sum = lane < seqs ? (int64_t)rows * span_of(a, lane).tiles : 0;
+    int64_t inc = sum;
+    for (int o = 1; o < seqs; o <<= 1) {
+      const int64_t v = __shfl_up_sync(~0u, inc, o);
+      if (lane >= o) inc += v;
+    }
+    Found f;
+    f.total = __shfl_sync(~0u, inc, seqs - 1);
+    f.ctas = min((int64_t)a.ctas, f.total);
+    const int64_t x = slice < f.ctas ? f.total * slice / f.ctas : f.total;
+    const uint32_t hit = __ballot_sync(~0u, x >= inc - sum && x < inc);
+    f.seq = hit ? __ffs(hit) - 1 : seqs;
+    f.start = hit ? __shfl_sync(~0u, inc - sum, f.seq) : f.total;
+    return f;
+  }
   const int s0 = threadIdx.x * per, s1 = min(s0 + per, seqs);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t sum = 0;
@@ -152,22 +180,22 @@ __device__ Found find(const AtParams &a, int rows, int64_t slice, int which, int
     if (lane >= o) inc += v;
   }
   if (lane == 31) shared[warp] = inc;
-  if (threadIdx.x == 0) shared[kWarps] = seqs, shared[kWarps + 1] = 0;
   __syncthreads();
   int64_t before = inc - sum, total = 0;
-  for (int w = 0; w < kWarps; ++w) {
+#pragma unroll
+  for (int w = 0; w < kW; ++w) {
     if (w < warp) before += shared[w];
     total += shared[w];
   }
   const int64_t ctas = min((int64_t)a.ctas, total);
   const int64_t x = slice < ctas ? total * slice / ctas : total;
-  if (which < 0 ? x >= before && x < before + sum : which >= s0 && which < s1) {
+  if (x >= before && x < before + sum) {  // one thread, if slice < ctas
     int64_t at = before;
-    for (int s = s0; s < s1; ++s) {
+    for (int s = s0;; ++s) {
       const int64_t n = (int64_t)rows * span_of(a, s).tiles;
-      if (which < 0 ? x < at + n : s == which) {
-        shared[kWarps] = s;
-        shared[kWarps + 1] = at;
+      if (x < at + n) {
+        shared[kW] = s;
+        shared[kW + 1] = at;
         break;
       }
       at += n;
@@ -177,9 +205,8 @@ __device__ Found find(const AtParams &a, int rows, int64_t slice, int which, int
   Found f;
   f.total = total;
   f.ctas = ctas;
-  f.seq = (int)shared[kWarps];
-  f.start = shared[kWarps + 1];
-  __syncthreads();
+  f.seq = slice < ctas ? (int)shared[kW] : seqs;
+  f.start = slice < ctas ? shared[kW + 1] : total;
   return f;
 }
 
@@ -230,7 +257,8 @@ __device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d
 template <typename T, int DP, int NT, bool POW2>
 __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
     k_attention(const __grid_constant__ AtParams a) {
-  constexpr int kCols = 8 * NT, kKey = DP / 32, kVal = DP / 64;
+  constexpr int kCols = 8 * NT, kKey = DP / 32, kVal = DP / 64, kUnits = units_of(DP, NT);
+  constexpr int kTile = 16 * kUnits * kWarps;
   // wide heads: keys and values take turns in the same registers
   constexpr bool kTurns = DP > 128;
   extern __shared__ __align__(16) float smem[];
@@ -241,12 +269,47 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int D = c.head_dim, rows = c.kv_heads * a.groups;
 
-  const Found f = find(a, rows, blockIdx.x, -1, scan);
-  if (blockIdx.x >= f.ctas) return;
-  int64_t at = f.total * blockIdx.x / f.ctas;
-  const int64_t end = f.total * (blockIdx.x + 1) / f.ctas;
-  int s = f.seq;
-  int64_t start = f.start;
+  int64_t at, end, start;
+  int s;
+  launch_dependents();
+  if (a.direct) {  // a CTA per row
+    s = blockIdx.x / rows;
+    start = 0;
+    const int tiles = span_of(a, s).tiles;
+    at = (int64_t)(blockIdx.x - s * rows) * tiles;
+    end = at + tiles;
+  } else {
+    const Found f = find<kThreads>(a, rows, blockIdx.x, scan);
+    s = f.seq;
+    start = f.start;
+    at = end = 0;
+    int4 cut = make_int4(0, 0, 0, 0);
+    if (blockIdx.x < f.ctas) {
+      at = f.total * blockIdx.x / f.ctas;
+      end = f.total * (blockIdx.x + 1) / f.ctas;
+      // the row begins at x0, in the slice of `first`, and ends at x1
+      const int tiles = span_of(a, s).tiles, row = (int)((at - start) / tiles);
+      const int64_t x0 = start + (int64_t)row * tiles, x1 = x0 + tiles - 1;
+      const int first = (int)(((x0 + 1) * f.ctas - 1) / f.total);
+      if (x0 < at && first == (int)blockIdx.x - 1)
+        cut = make_int4(s, row, first, (int)(((x1 + 1) * f.ctas - 1) / f.total) - first + 1);
+    }
+    if (threadIdx.x == 0) a.cuts[blockIdx.x] = cut;
+  }
+  // sequences that see nothing are in no slice: their rows are written here
+  for (int e = a.direct ? s : blockIdx.x; e < c.seqs; e += a.direct ? c.seqs : a.ctas) {
+    const int given = a.p.lengths[e];
+    if (a.direct && blockIdx.x != s * rows) break;
+    if (threadIdx.x == 0 && (given < 0 || given > (int64_t)c.seq_pages * c.page_size))
+      raise_status(a.status, kStatusIndex);
+    if (span_of(a, e).tiles) continue;
+    const float zero[8] = {};
+    for (int i = threadIdx.x; i < a.p.heads * (D / 8); i += kThreads) {
+      const int head = i / (D / 8), d = 8 * (i % (D / 8));
+      store8<T>(a, e, head, d, zero);
+      if (a.p.lse && d == 0) a.p.lse[(int64_t)e * a.p.heads + head] = -INFINITY;
+    }
+  }
 
   while (at < end) {
     const Span sp = span_of(a, s);
@@ -311,29 +374,38 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
       place = pl;
       return pos + i >= sp.from && pos + i < stop && pg >= 0 && pg < c.pages;
     };
-    uint4 key[2][kKey], val[4][kVal];
-    bool key_on[2], key_next[2];
-    auto load_keys = [&](const Where &w, int pos) {
+    uint4 key[kUnits][2][kKey], val[kUnits][4][kVal];
+    bool key_on[kUnits][2], key_next[kUnits][2];
+    Where now[kUnits], next[kUnits];
+    auto lookups = [&](Where (&w)[kUnits], int pos) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int64_t page, place;
-        key_next[h] = place_of(w, pos, g + 8 * h, page, place);
-        const T *k = static_cast<const T *>(c.k) + page * c.k_page + place * c.k_place + kvh * c.k_head + 8 * t;
-#pragma unroll
-        for (int i = 0; i < kKey; ++i)
-          key[h][i] = key_next[h] && 32 * i + 8 * t < D ? load16(k + 32 * i) : make_uint4(0, 0, 0, 0);
-      }
+      for (int u = 0; u < kUnits; ++u) w[u] = lookup(pos + 16 * u);
     };
-    auto load_values = [&](const Where &w, int pos) {
+    auto load_keys = [&](const Where (&w)[kUnits], int pos) {
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        int64_t page, place;
-        const bool on = place_of(w, pos, 2 * t + (h & 1) + 8 * (h >> 1), page, place);
-        const T *v = static_cast<const T *>(c.v) + page * c.v_page + place * c.v_place + kvh * c.v_head + 8 * g;
+      for (int u = 0; u < kUnits; ++u)
 #pragma unroll
-        for (int i = 0; i < kVal; ++i)  // what is not seen is not read: zero weights times zeros
-          val[h][i] = on && 64 * i + 8 * g < D ? load16(v + 64 * i) : make_uint4(0, 0, 0, 0);
-      }
+        for (int h = 0; h < 2; ++h) {
+          int64_t page, place;
+          const bool on = key_next[u][h] = place_of(w[u], pos + 16 * u, g + 8 * h, page, place);
+          const T *k = static_cast<const T *>(c.k) + page * c.k_page + place * c.k_place + kvh * c.k_head + 8 * t;
+#pragma unroll
+          for (int i = 0; i < kKey; ++i)
+            key[u][h][i] = on && 32 * i + 8 * t < D ? load16(k + 32 * i) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    auto load_values = [&](const Where (&w)[kUnits], int pos) {
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          int64_t page, place;
+          const bool on = place_of(w[u], pos + 16 * u, 2 * t + (h & 1) + 8 * (h >> 1), page, place);
+          const T *v = static_cast<const T *>(c.v) + page * c.v_page + place * c.v_place + kvh * c.v_head + 8 * g;
+#pragma unroll
+          for (int i = 0; i < kVal; ++i)  // what is not seen is not read: zero weights times zeros
+            val[u][h][i] = on && 64 * i + 8 * g < D ? load16(v + 64 * i) : make_uint4(0, 0, 0, 0);
+        }
     };
 
     // A value that is not finite makes lo x value a NaN where hi x value is an
@@ -349,25 +421,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[n][i][j][0] = o[n][i][j][1] = o[n][i][j][2] = o[n][i][j][3] = 0.0f;
     }
-    int pos = sp.base + kTile * tile0 + 16 * warp;
-    Where now = lookup(pos), next = lookup(pos + kTile);
+    int pos = sp.base + kTile * tile0 + 16 * kUnits * warp;
+    lookups(now, pos);
+    lookups(next, pos + kTile);
     load_keys(now, pos);
     if (!kTurns) load_values(now, pos);
     for (; pos < stop; pos += kTile) {
-      key_on[0] = key_next[0];
-      key_on[1] = key_next[1];
-      // a page that is not in the cache
-      if (POW2 ? (now.page < 0 || now.page >= c.pages) && lane == 0
-               : lane < 16 && pos + lane >= sp.from && pos + lane < stop && (now.page < 0 || now.page >= c.pages))
-        raise_status(a.status, kStatusIndex);
-      float sc[NT][4];
+      float sc[kUnits][NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+      for (int u = 0; u < kUnits; ++u) {
+        // a page that is not in the cache
+        const int first = pos + 16 * u;
+        if (POW2 ? lane == 0 && first < stop : lane < 16 && first + lane >= sp.from && first + lane < stop)
+          if (now[u].page < 0 || now[u].page >= c.pages) raise_status(a.status, kStatusIndex);
+        key_on[u][0] = key_next[u][0];
+        key_on[u][1] = key_next[u][1];
 #pragma unroll
-        for (int i = 0; i < kKey; ++i) {
-          mma(sc[n], key[0][i].x, key[1][i].x, key[0][i].y, key[1][i].y, q[n][i].x, q[n][i].y, T());
-          mma(sc[n], key[0][i].z, key[1][i].z, key[0][i].w, key[1][i].w, q[n][i].z, q[n][i].w, T());
+        for (int n = 0; n < NT; ++n) {
+          sc[u][n][0] = sc[u][n][1] = sc[u][n][2] = sc[u][n][3] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kKey; ++i) {
+            const uint4 &k0 = key[u][0][i], &k1 = key[u][1][i];
+            mma(sc[u][n], k0.x, k1.x, k0.y, k1.y, q[n][i].x, q[n][i].y, T());
+            mma(sc[u][n], k0.z, k1.z, k0.w, k1.w, q[n][i].z, q[n][i].w, T());
+          }
         }
       }
       if (kTurns)
@@ -375,26 +452,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
       else
         load_keys(next, pos + kTile);
       // weights: lane (g, t) has positions g, g + 8 of heads 2 t, 2 t + 1
-      seen |= key_on[0] || key_on[1];
       bool passed = false;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int u = 0; u < kUnits; ++u) {
+        seen |= key_on[u][0] || key_on[u][1];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sc[n][e] = key_on[e >> 1] ? sc[n][e] * a.scale2 : -INFINITY;
-          passed |= sc[n][e] > m[n][e & 1] + kSlack;
-        }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sc[u][n][e] = key_on[u][e >> 1] ? sc[u][n][e] * a.scale2 : -INFINITY;
+            passed |= sc[u][n][e] > m[n][e & 1] + kSlack;
+          }
       }
       if (__any_sync(~0u, passed)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(sc[n][e], sc[n][2 + e]);
+            float top = m[n][e];
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) top = fmaxf(top, fmaxf(sc[u][n][e], sc[u][n][2 + e]));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
-            top = fmaxf(top, m[n][e]);
             const float fade = ex2(m[n][e] - (top == -INFINITY ? 0.0f : top));
             m[n][e] = top;
             l[n][e] *= fade;
@@ -407,36 +487,41 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
               }
           }
       }
-      uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float w[4];
+      for (int u = 0; u < kUnits; ++u) {
+        uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float base = m[n][e & 1];
-          w[e] = ex2(sc[n][e] - (base == -INFINITY ? 0.0f : base));
-          l[n][e & 1] += w[e];
+        for (int n = 0; n < NT; ++n) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float base = m[n][e & 1];
+            w[e] = ex2(sc[u][n][e] - (base == -INFINITY ? 0.0f : base));
+            l[n][e & 1] += w[e];
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t p = pack<T>(w[2 * h], w[2 * h + 1]);
+            const float2 r = unpack<T>(p);
+            hi[n][h] = transpose8x8(p);
+            lo[n][h] = transpose8x8(pack<T>(w[2 * h] - r.x, w[2 * h + 1] - r.y));
+          }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t p = pack<T>(w[2 * h], w[2 * h + 1]);
-          const float2 r = unpack<T>(p);
-          hi[n][h] = transpose8x8(p);
-          lo[n][h] = transpose8x8(pack<T>(w[2 * h] - r.x, w[2 * h + 1] - r.y));
-        }
-      }
+        for (int i = 0; i < kVal; ++i) {
+          const uint32_t *v0 = reinterpret_cast<const uint32_t *>(&val[u][0][i]);
+          const uint32_t *v1 = reinterpret_cast<const uint32_t *>(&val[u][1][i]);
+          const uint32_t *v2 = reinterpret_cast<const uint32_t *>(&val[u][2][i]);
+          const uint32_t *v3 = reinterpret_cast<const uint32_t *>(&val[u][3][i]);
 #pragma unroll
-      for (int i = 0; i < kVal; ++i) {
-        const uint32_t *v0 = reinterpret_cast<const uint32_t *>(&val[0][i]), *v1 = reinterpret_cast<const uint32_t *>(&val[1][i]);
-        const uint32_t *v2 = reinterpret_cast<const uint32_t *>(&val[2][i]), *v3 = reinterpret_cast<const uint32_t *>(&val[3][i]);
+          for (int j = 0; j < 4; ++j) {  // rows g, g + 8: elements 2 j, 2 j + 1 of the lane's piece
+            const uint32_t a0 = __byte_perm(v0[j], v1[j], 0x5410), a1 = __byte_perm(v0[j], v1[j], 0x7632);
+            const uint32_t a2 = __byte_perm(v2[j], v3[j], 0x5410), a3 = __byte_perm(v2[j], v3[j], 0x7632);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {  // rows g, g + 8: elements 2 j, 2 j + 1 of the lane's piece
-          const uint32_t a0 = __byte_perm(v0[j], v1[j], 0x5410), a1 = __byte_perm(v0[j], v1[j], 0x7632);
-          const uint32_t a2 = __byte_perm(v2[j], v3[j], 0x5410), a3 = __byte_perm(v2[j], v3[j], 0x7632);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma(o[n][i][j], a0, a1, a2, a3, hi[n][0], hi[n][1], T());
-            if (both) mma(o[n][i][j], a0, a1, a2, a3, lo[n][0], lo[n][1], T());
+            for (int n = 0; n < NT; ++n) {
+              mma(o[n][i][j], a0, a1, a2, a3, hi[n][0], hi[n][1], T());
+              if (both) mma(o[n][i][j], a0, a1, a2, a3, lo[n][0], lo[n][1], T());
+            }
           }
         }
       }
@@ -444,8 +529,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
         load_keys(next, pos + kTile);
       else
         load_values(next, pos + kTile);
-      now = next;
-      next = lookup(pos + 2 * kTile);
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) now[u] = next[u];
+      lookups(next, pos + 2 * kTile);
     }
     float worst = 0.0f;  // NaN if a sum is not finite
 #pragma unroll
@@ -529,48 +615,71 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
   }
 }
 
-// Joins the partial rows of each (sequence, head group) and writes the rows
-// of sequences that see nothing.
+// Joins partial rows.  CTA c takes the row in which slice c + 1 begins, if it
+// began in slice c (so every split row has one CTA); its threads take
+// eight outputs each, in groups that walk every `groups`-th part four at a
+// time, and the first group joins the groups.
+constexpr int kJoin = 512;
 template <typename T, int DP, int NT>
-__global__ void __launch_bounds__(kThreads) k_attention_join(const __grid_constant__ AtParams a) {
-  constexpr int kCols = 8 * NT;
-  __shared__ int64_t scan[kWarps + 2];
+__global__ void __launch_bounds__(kJoin) k_attention_join(const __grid_constant__ AtParams a) {
+  constexpr int kCols = 8 * NT, kItems = kCols * DP / 8, kGroups = kJoin / kItems;
+  __shared__ float part_sh[kGroups][11][kItems];  // m, l, seen, eight outputs
   dependent_wait();
   const fp4_kv_cache &c = a.p.cache;
-  const int rows = c.kv_heads * a.groups, s = blockIdx.x / rows, row = blockIdx.x - s * rows;
-  const Found f = find(a, rows, 0, s, scan);
-  const int tiles = span_of(a, s).tiles;
-  if (row == 0 && threadIdx.x == 0) {
-    const int n = a.p.lengths[s];
-    if (n < 0 || n > (int64_t)c.seq_pages * c.page_size) raise_status(a.status, kStatusIndex);
-  }
+  const int4 cut = a.cuts[blockIdx.x + 1];
+  const int s = cut.x, row = cut.y, first = cut.z, parts = cut.w;
+  if (parts == 0) return;
   const int kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
   const int heads = min(kCols, (kvh + 1) * a.share - head0);
-  int first = 0, parts = 0;
-  if (tiles) {
-    const int64_t x0 = f.start + (int64_t)row * tiles, x1 = x0 + tiles - 1;
-    first = (int)(((x0 + 1) * f.ctas - 1) / f.total);  // the CTA whose share holds the tile
-    parts = (int)(((x1 + 1) * f.ctas - 1) / f.total) - first + 1;
-    if (parts == 1) return;  // written whole
-  }
-  for (int i = threadIdx.x; i < heads * (DP / 8); i += kThreads) {
-    const int col = i / (DP / 8), d = 8 * (i % (DP / 8));
-    if (d >= c.head_dim) continue;
-    auto slot = [&](int w) {
-      return a.ws + ((int64_t)(first + w) * 2 + (w == 0)) * slot_floats(kCols, DP);
-    };
-    finish<T>(
-        a, s, head0 + col, d, parts,
-        [&](int w, float &m, float &l, bool &seen) {
-          const float *st = slot(w) + kCols * DP + col * 4;
-          m = st[0], l = st[1], seen = st[2] != 0.0f;
-        },
-        [&](int w, float fw, float *v) {
-          const float *from = slot(w) + col * DP + d;
+  const int item = threadIdx.x % kItems, group = threadIdx.x / kItems;
+  const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
+  if (group < kGroups) {
+    float m = -INFINITY, l = 0.0f, any = 0.0f, v[8] = {};
+    constexpr int kBatch = 4;
+    for (int w0 = group; w0 < parts; w0 += kBatch * kGroups) {
+      float4 st[kBatch], lo[kBatch], hi[kBatch];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = fmaf(fw, from[e], v[e]);
-        });
+      for (int i = 0; i < kBatch; ++i) {
+        const int w = w0 + i * kGroups;
+        st[i] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+        lo[i] = hi[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (w >= parts) continue;
+        const float *slot = a.ws + ((int64_t)(first + w) * 2 + (w == 0)) * slot_floats(kCols, DP);
+        if (col < heads && d < c.head_dim) {  // what was written
+          st[i] = *reinterpret_cast<const float4 *>(slot + kCols * DP + col * 4);
+          lo[i] = *reinterpret_cast<const float4 *>(slot + col * DP + d);
+          hi[i] = *reinterpret_cast<const float4 *>(slot + col * DP + d + 4);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float now = fmaxf(m, st[i].x), base = now == -INFINITY ? 0.0f : now;
+        const float fo = ex2(m - base), fn = ex2(st[i].x - base);
+        m = now;
+        l = l * fo + st[i].y * fn;
+        any = fmaxf(any, st[i].z);
+        const float p[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = v[e] * fo + p[e] * fn;
+      }
+    }
+    part_sh[group][0][item] = m;
+    part_sh[group][1][item] = l;
+    part_sh[group][2][item] = any;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part_sh[group][3 + e][item] = v[e];
   }
+  __syncthreads();
+  if (group != 0 || col >= heads || d >= c.head_dim) return;
+  finish<T>(
+      a, s, head0 + col, d, kGroups,
+      [&](int w, float &m, float &l, bool &seen) {
+        m = part_sh[w][0][item], l = part_sh[w][1][item], seen = part_sh[w][2][item] != 0.0f;
+      },
+      [&](int w, float fw, float *v) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(fw, part_sh[w][3 + e][item], v[e]);
+      });
 }
 
 constexpr int dp_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256; }
@@ -597,15 +706,17 @@ fp4_status launch(AtParams a, cudaStream_t s) {
   const fp4_kv_cache &c = a.p.cache;
   // no more CTAs than the table has tiles
   const int64_t rows = (int64_t)c.seqs * c.kv_heads * a.groups;
-  const int64_t room = rows * ceil_div((int64_t)c.seq_pages * c.page_size, kTile);
+  const int64_t room = (int64_t)c.seq_pages * c.page_size;
   const int64_t most = (int64_t)sm_count() * (per < kPerSM ? per : kPerSM);
-  a.ctas = (int)(room < most ? room : most);
+  const int64_t tiles = rows * ceil_div(room, 16 * kWarps * units_of(DP, NT));
   if (rows > INT32_MAX) return FP4_ERR_SHAPE;
-  if (a.ctas > 0) {
-    kern<<<(unsigned)a.ctas, kThreads, smem, s>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return FP4_ERR_CUDA;
-  }
-  return launch_dependent(k_attention_join<T, DP, NT>, dim3((unsigned)rows), dim3(kThreads), 0, s, a) == cudaSuccess
+  a.tile = 16 * kWarps * units_of(DP, NT);
+  a.direct = room <= 512;
+  a.ctas = (int)(a.direct ? rows : tiles < most ? tiles : most);
+  kern<<<(unsigned)a.ctas, kThreads, smem, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return FP4_ERR_CUDA;
+  if (a.direct || a.ctas < 2) return FP4_OK;
+  return launch_dependent(k_attention_join<T, DP, NT>, dim3((unsigned)a.ctas - 1), dim3(kJoin), 0, s, a) == cudaSuccess
              ? FP4_OK
              : FP4_ERR_CUDA;
 }
@@ -629,7 +740,7 @@ fp4_status launch_type(const AtParams &a, int nt, cudaStream_t s) {
 
 int64_t decode_attention_workspace(int heads, int kv_heads, int head_dim) {
   const int dp = dp_of(head_dim), cols = 8 * nt_of(heads / kv_heads, dp);
-  return (int64_t)sm_count() * kPerSM * 2 * slot_floats(cols, dp) * sizeof(float);
+  return (int64_t)sm_count() * kPerSM * (2 * slot_floats(cols, dp) * sizeof(float) + sizeof(int4));
 }
 
 fp4_status launch_decode_attention(const fp4_attention_params &p, cudaStream_t s) {
@@ -646,7 +757,8 @@ fp4_status launch_decode_attention(const fp4_attention_params &p, cudaStream_t s
     for (a.shift = 4; (1 << a.shift) < c.page_size;) ++a.shift;
   a.out16 = aligned16(p.out) && p.out_seq % 8 == 0 && p.out_head % 8 == 0;
   a.scale2 = p.scale * 1.44269504088896f;
-  a.ws = static_cast<float *>(p.workspace);
+  a.cuts = static_cast<int4 *>(p.workspace);
+  a.ws = reinterpret_cast<float *>(a.cuts + (int64_t)sm_count() * kPerSM);
   return c.type == FP4_BF16 ? launch_type<__nv_bfloat16>(a, nt, s) : launch_type<__half>(a, nt, s);
 }
 
