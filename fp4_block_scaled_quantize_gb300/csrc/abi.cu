@@ -417,7 +417,7 @@ fp4_status fp4_kv_append(const fp4_append_params *p, void *stream) {
   if (st != FP4_OK) return st;
   if (p->tokens < 0 || p->rope_len < 0 || p->rot_dim < 0) return FP4_ERR_INVALID_ARG;
   if (p->k_token < 0 || p->k_head < 0 || p->v_token < 0 || p->v_head < 0) return FP4_ERR_INVALID_ARG;
-  if (p->rot_dim % 2 != 0 || p->rot_dim > p->cache.head_dim || p->tokens > INT32_MAX)
+  if (p->rot_dim % 2 != 0 || p->rot_dim > p->cache.head_dim || p->tokens > INT32_MAX / 2)
     return FP4_ERR_SHAPE;
   if (p->q) {
     if (!p->q_out || p->heads < 1 || p->q_token < 0 || p->q_head < 0 || p->qo_token < 0 ||

@@ -2,87 +2,275 @@
 // queries rotated by their positions on the way (sm_103a):
 //   (a, b) -> (a cos - b sin, b cos + a sin) per pair, binary32, rounded once.
 //
-// First form: one CTA per token, one thread per pair or element at a time.
+// Bound: HBM for prompts (every row read and written once, 4 bytes per
+// element; cos and sin are reused over the heads of a token), launch and three
+// dependent loads (position, page, nothing else) for a few tokens.
+//
+// Layout.  A thread owns one unit of a head -- 16 bytes, or the two 16-byte
+// pieces whose elements form pairs (i, i + rot_dim / 2) -- for one token, and
+// walks over the token's query, key and value heads with cos and sin held in
+// registers.  The rows of a CTA's tokens are spread over its threads so that
+// neighbours touch neighbouring pieces of a row.  Rows whose pointers,
+// strides or sizes are not whole 16-byte pieces go by single elements.
 #include "serve.cuh"
 
 namespace fp4 {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256, kResident = 3;  // CTAs per SM
+
+struct ApParams {
+  fp4_append_params p;
+  int units;      // units of a head
+  int lanes;      // head lanes: threads of a token / units
+  int tokens;     // tokens of a CTA at a time
+  int splits;     // CTAs that share a token's heads (few tokens)
+  uint32_t *status;
+};
+
+// Where a token at position pos goes: false if it is skipped or lies outside
+// a table.
+__device__ __forceinline__ bool locate(const fp4_append_params &p, int64_t t, int pos, uint32_t *status,
+                                       int &page, int &place) {
+  const fp4_kv_cache &c = p.cache;
+  page = 0;
+  place = 0;
+  if (pos < 0) return false;
+  const int64_t seq = p.seq ? __ldg(p.seq + t) : t;
+  bool ok = seq >= 0 && seq < c.seqs && pos < c.seq_pages * c.page_size &&
+            (p.rot_dim == 0 || pos < p.rope_len);
+  if (ok) {
+    const int e = pos / c.page_size;
+    place = pos - e * c.page_size;
+    page = __ldg(c.table + seq * c.table_stride + e);
+    ok = page >= 0 && page < c.pages;
+  }
+  if (!ok && status) raise_status(status, kStatusIndex);
+  return ok;
+}
+
+// Row r of a token: its query heads, then its key heads, then its value heads.
+template <typename T>
+__device__ __forceinline__ const T *source(const fp4_append_params &p, int64_t t, int r, int heads) {
+  if (r < heads) return static_cast<const T *>(p.q) + t * p.q_token + r * p.q_head;
+  r -= heads;
+  if (r < p.cache.kv_heads) return static_cast<const T *>(p.k) + t * p.k_token + r * p.k_head;
+  return static_cast<const T *>(p.v) + t * p.v_token + (r - p.cache.kv_heads) * p.v_head;
+}
+template <typename T>
+__device__ __forceinline__ T *target(const fp4_append_params &p, int64_t t, int r, int heads,
+                                     int page, int place) {
+  const fp4_kv_cache &c = p.cache;
+  if (r < heads) return static_cast<T *>(p.q_out) + t * p.qo_token + r * p.qo_head;
+  r -= heads;
+  if (r < c.kv_heads) return static_cast<T *>(c.k) + (int64_t)page * c.k_page + place * c.k_place + r * c.k_head;
+  return static_cast<T *>(c.v) + (int64_t)page * c.v_page + place * c.v_place + (r - c.kv_heads) * c.v_head;
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_append(fp4_append_params p, uint32_t *status) {
-  const fp4_kv_cache &c = p.cache;
-  const int D = c.head_dim, half = p.rot_dim / 2, units = D - half;  // pairs, then single elements
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-    const int pos = p.pos[t];
-    const int64_t seq = p.seq ? p.seq[t] : t;
-    bool keep = pos >= 0, bad = false;
-    int64_t page = 0;
-    if (keep) {
-      bad = seq < 0 || seq >= c.seqs || pos >= (int64_t)c.seq_pages * c.page_size ||
-            (half && pos >= p.rope_len);
-      if (!bad) {
-        page = c.table[seq * c.table_stride + pos / c.page_size];
-        bad = page < 0 || page >= c.pages;
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 get(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+  static __device__ __forceinline__ uint32_t put(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+};
+template <>
+struct Pair<__half> {
+  static __device__ __forceinline__ float2 get(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  }
+  static __device__ __forceinline__ uint32_t put(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+  }
+};
+
+__device__ __forceinline__ uint4 load16(const void *p) { return *static_cast<const uint4 *>(p); }
+
+// Pieces of eight elements turned: pairs of one element of each piece, or
+// pairs of neighbours within a piece.
+template <typename T>
+__device__ __forceinline__ void turn_halves(uint4 &x, uint4 &y, const float *co, const float *si) {
+  uint32_t *a = reinterpret_cast<uint32_t *>(&x), *b = reinterpret_cast<uint32_t *>(&y);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 u = Pair<T>::get(a[i]), v = Pair<T>::get(b[i]);
+    const float c0 = co[2 * i], c1 = co[2 * i + 1], s0 = si[2 * i], s1 = si[2 * i + 1];
+    a[i] = Pair<T>::put(u.x * c0 - v.x * s0, u.y * c1 - v.y * s1);
+    b[i] = Pair<T>::put(v.x * c0 + u.x * s0, v.y * c1 + u.y * s1);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void turn_pairs(uint4 &x, const float *co, const float *si) {
+  uint32_t *a = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 u = Pair<T>::get(a[i]);
+    a[i] = Pair<T>::put(u.x * co[i] - u.y * si[i], u.y * co[i] + u.x * si[i]);
+  }
+}
+
+// Whole 16-byte pieces, two a unit: with halves the pieces 8 u and rot_dim / 2
+// + 8 u of the rotated part, else 16 consecutive elements (the last unit may
+// hold one piece).  The rows are requested before anything is known of the
+// token's place; only their stores wait for it, and a thread's next token is
+// looked up meanwhile.
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kThreads, kResident) k_append16(const __grid_constant__ ApParams a) {
+  const fp4_append_params &p = a.p;
+  const int heads = p.q ? p.heads : 0, rows = heads + 2 * p.cache.kv_heads, D = p.cache.head_dim;
+  const int half = p.rot_dim / 2, turned = INTER ? 0 : p.rot_dim / 16;
+  const int per = a.units * a.lanes;  // threads of a token
+  const int tl = threadIdx.x / per, in = threadIdx.x - tl * per;
+  const int lane = in / a.units, unit = in - lane * a.units;
+  if (tl >= a.tokens) return;
+  const int split = blockIdx.x % a.splits;
+  const int hop = (int)(gridDim.x / a.splits) * a.tokens, tokens = (int)p.tokens;
+  const bool halves = unit < turned;
+  const int o1 = halves ? 8 * unit : 16 * unit + (INTER ? 0 : p.rot_dim - 16 * turned);
+  const int o2 = halves ? o1 + half : o1 + 8;
+  const bool two = o2 < D, rot1 = halves || (INTER && o1 < p.rot_dim), rot2 = halves || (INTER && o2 < p.rot_dim);
+  constexpr int kBatch = 3;  // rows requested together
+  const int stride = a.lanes * a.splits;
+  uint32_t *const status = in == 0 && split == 0 ? a.status : nullptr;
+  int t = (int)(blockIdx.x / a.splits) * a.tokens + tl;  // below 2^31, and so is t + hop
+  int next_pos = t < tokens ? __ldg(p.pos + t) : -1, next_place = 0, next_page = 0;
+  bool next_keep = t < tokens && locate(p, t, next_pos, status, next_page, next_place);
+  for (; t < tokens; t += hop) {
+    const int pos = next_pos, place = next_place, page = next_page;
+    const bool keep = next_keep, more = t + hop < tokens;
+    next_pos = more ? __ldg(p.pos + t + hop) : -1;
+    __align__(16) float co[8], si[8];
+    for (int r0 = split * a.lanes + lane, first = 1; r0 < rows; r0 += kBatch * stride, first = 0) {
+      uint4 x[kBatch], y[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        x[i] = y[i] = make_uint4(0, 0, 0, 0);
+        const int r = r0 + i * stride;
+        if (r >= rows) continue;
+        const T *src = source<T>(p, t, r, heads);
+        x[i] = load16(src + o1);
+        if (two) y[i] = load16(src + o2);
       }
-      if (bad && threadIdx.x == 0) raise_status(status, kStatusIndex);
-      keep = !bad;
-    }
-    const int place = keep ? pos % c.page_size : 0;
-    const float *cs = p.rope + (int64_t)(keep ? pos : 0) * p.rot_dim;
-    const int heads = p.q ? p.heads : 0, rows = heads + 2 * c.kv_heads;
-    for (int i = threadIdx.x; i < rows * units; i += kThreads) {
-      const int r = i / units, u = i % units;
-      const T *src;
-      T *dst;
-      if (r < heads) {
-        src = static_cast<const T *>(p.q) + t * p.q_token + r * p.q_head;
-        dst = static_cast<T *>(p.q_out) + t * p.qo_token + r * p.qo_head;
-      } else if (r < heads + c.kv_heads) {
-        const int64_t h = r - heads;
-        src = static_cast<const T *>(p.k) + t * p.k_token + h * p.k_head;
-        dst = static_cast<T *>(c.k) + page * c.k_page + place * c.k_place + h * c.k_head;
-      } else {
-        const int64_t h = r - heads - c.kv_heads;
-        src = static_cast<const T *>(p.v) + t * p.v_token + h * p.v_head;
-        dst = static_cast<T *>(c.v) + page * c.v_page + place * c.v_place + h * c.v_head;
-      }
-      if (!keep && r >= heads) continue;
-      const bool value = r >= heads + c.kv_heads;
-      if (u < half) {
-        const int ia = p.interleaved ? 2 * u : u, ib = p.interleaved ? 2 * u + 1 : u + half;
-        const T a = src[ia], b = src[ib];
-        if (!keep) {
-          dst[ia] = dst[ib] = from_f32<T>(0.0f);
-        } else if (value) {
-          dst[ia] = a;
-          dst[ib] = b;
-        } else {
-          const float fa = to_f32(a), fb = to_f32(b), co = cs[u], si = cs[half + u];
-          dst[ia] = from_f32<T>(fa * co - fb * si);
-          dst[ib] = from_f32<T>(fb * co + fa * si);
+      if (first) {
+        if (keep && (rot1 || rot2)) {
+          const float *cs = p.rope + (int64_t)pos * p.rot_dim + 8 * unit;
+#pragma unroll
+          for (int i = 0; i < 8; i += 4) {
+            if (i == 4 && !rot2) continue;
+            *reinterpret_cast<float4 *>(co + i) = __ldg(reinterpret_cast<const float4 *>(cs + i));
+            *reinterpret_cast<float4 *>(si + i) = __ldg(reinterpret_cast<const float4 *>(cs + half + i));
+          }
         }
-      } else {
-        const int e = half + u;
-        dst[e] = keep ? src[e] : from_f32<T>(0.0f);
+        next_keep = more && locate(p, t + hop, next_pos, status, next_page, next_place);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + i * stride;
+        if (r >= rows || (!keep && r >= heads)) continue;
+        if (!keep) {
+          x[i] = y[i] = make_uint4(0, 0, 0, 0);
+        } else if (r < heads + p.cache.kv_heads) {
+          if (halves) {
+            turn_halves<T>(x[i], y[i], co, si);
+          } else {
+            if (rot1) turn_pairs<T>(x[i], co, si);
+            if (rot2) turn_pairs<T>(y[i], co + 4, si + 4);
+          }
+        }
+        T *dst = target<T>(p, t, r, heads, page, place);
+        *reinterpret_cast<uint4 *>(dst + o1) = x[i];
+        if (two) *reinterpret_cast<uint4 *>(dst + o2) = y[i];
       }
     }
   }
 }
 
+// Single elements: any pointers, strides and sizes.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_append1(const __grid_constant__ ApParams a) {
+  const fp4_append_params &p = a.p;
+  const int D = p.cache.head_dim, half = p.rot_dim / 2, units = D - half;  // pairs, then single elements
+  const int heads = p.q ? p.heads : 0, rows = heads + 2 * p.cache.kv_heads;
+  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+    const int pos = __ldg(p.pos + t);
+    int place, page;
+    const bool keep = locate(p, t, pos, threadIdx.x == 0 ? a.status : nullptr, page, place);
+    const float *cs = p.rope + (int64_t)(keep ? pos : 0) * p.rot_dim;
+    for (int i = threadIdx.x; i < (keep ? rows : heads) * units; i += kThreads) {
+      const int r = i / units, u = i - r * units;
+      const T *src = source<T>(p, t, r, heads);
+      T *dst = target<T>(p, t, r, heads, page, place);
+      if (u < half) {
+        const int ia = p.interleaved ? 2 * u : u, ib = p.interleaved ? 2 * u + 1 : u + half;
+        const T x = src[ia], y = src[ib];
+        if (!keep) {
+          dst[ia] = dst[ib] = from_f32<T>(0.0f);
+        } else if (r >= heads + p.cache.kv_heads) {
+          dst[ia] = x;
+          dst[ib] = y;
+        } else {
+          const float fx = to_f32(x), fy = to_f32(y), co = cs[u], si = cs[half + u];
+          dst[ia] = from_f32<T>(fx * co - fy * si);
+          dst[ib] = from_f32<T>(fy * co + fx * si);
+        }
+      } else {
+        dst[half + u] = keep ? src[half + u] : from_f32<T>(0.0f);
+      }
+    }
+  }
+}
+
+bool whole16(const void *ptr, int64_t s0, int64_t s1) { return aligned16(ptr) && s0 % 8 == 0 && s1 % 8 == 0; }
+
+template <typename T>
+fp4_status launch_append(ApParams &a, cudaStream_t s) {
+  const fp4_append_params &p = a.p;
+  const fp4_kv_cache &c = p.cache;
+  const int heads = p.q ? p.heads : 0, rows = heads + 2 * c.kv_heads;
+  const bool whole = c.head_dim % 8 == 0 && p.rot_dim % (p.interleaved ? 8 : 16) == 0 &&
+                     whole16(p.k, p.k_token, p.k_head) && whole16(p.v, p.v_token, p.v_head) &&
+                     whole16(c.k, c.k_page, c.k_place) && whole16(c.v, c.v_page, c.v_place) &&
+                     c.k_head % 8 == 0 && c.v_head % 8 == 0 && aligned16(p.rope) &&
+                     (!p.q || (whole16(p.q, p.q_token, p.q_head) && whole16(p.q_out, p.qo_token, p.qo_head)));
+  const int64_t most = kResident * (int64_t)sm_count();  // CTAs resident at once
+  if (!whole) {
+    const unsigned grid = (unsigned)(p.tokens < 65535 ? p.tokens : 65535);
+    k_append1<T><<<grid, kThreads, 0, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
+  }
+  a.units = p.interleaved ? (c.head_dim + 15) / 16 : p.rot_dim / 16 + (c.head_dim - p.rot_dim + 15) / 16;  // <= 16
+  // a token's rows over the threads of a CTA, four or fewer each; what is left
+  // of the CTA takes further tokens, and where there are few tokens a token's
+  // rows go to several CTAs, one or two each
+  const int enough = (rows + 3) / 4;
+  a.lanes = 1;
+  while (a.lanes < enough && 2 * a.lanes * a.units <= kThreads) a.lanes *= 2;
+  a.tokens = kThreads / (a.units * a.lanes);
+  a.splits = 1;
+  const int64_t ctas = ceil_div(p.tokens, a.tokens);
+  while (ctas * a.splits * 2 <= most / 2 && a.lanes * a.splits < rows) a.splits *= 2;
+  const int64_t want = ctas < most / a.splits ? ctas : most / a.splits;
+  const unsigned grid = (unsigned)((want < 1 ? 1 : want) * a.splits);
+  if (p.interleaved)
+    k_append16<T, true><<<grid, kThreads, 0, s>>>(a);
+  else
+    k_append16<T, false><<<grid, kThreads, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
+}
+
 }  // namespace
 
 fp4_status launch_kv_append(const fp4_append_params &p, cudaStream_t s) {
-  uint32_t *status = status_word();
-  if (!status) return FP4_ERR_CUDA;
-  const unsigned grid = (unsigned)(p.tokens < 65535 ? p.tokens : 65535);
-  if (p.cache.type == FP4_BF16)
-    k_append<__nv_bfloat16><<<grid, kThreads, 0, s>>>(p, status);
-  else
-    k_append<__half><<<grid, kThreads, 0, s>>>(p, status);
-  return cudaGetLastError() == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
+  ApParams a{};
+  a.p = p;
+  a.status = status_word();
+  if (!a.status) return FP4_ERR_CUDA;
+  return p.cache.type == FP4_BF16 ? launch_append<__nv_bfloat16>(a, s) : launch_append<__half>(a, s);
 }
 
 }  // namespace fp4
