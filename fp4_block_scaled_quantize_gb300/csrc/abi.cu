@@ -435,12 +435,12 @@ fp4_status fp4_kv_append(const fp4_append_params *p, void *stream) {
   return launch_kv_append(*p, as_stream(stream));
 }
 
-int64_t fp4_decode_attention_workspace(int32_t seqs, int32_t heads, int32_t kv_heads,
-                                       int32_t head_dim) {
-  if (seqs < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || head_dim < 1 ||
+int64_t fp4_decode_attention_workspace(int32_t seqs, int64_t room, int32_t heads,
+                                       int32_t kv_heads, int32_t head_dim) {
+  if (seqs < 0 || room < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || head_dim < 1 ||
       head_dim > 256 || head_dim % 8 != 0)
     return -1;
-  return seqs == 0 ? 0 : decode_attention_workspace(heads, kv_heads, head_dim);
+  return seqs == 0 ? 0 : decode_attention_workspace(room, heads, kv_heads, head_dim);
 }
 
 fp4_status fp4_decode_attention(const fp4_attention_params *p, void *stream) {
@@ -459,7 +459,8 @@ fp4_status fp4_decode_attention(const fp4_attention_params *p, void *stream) {
       p->q_head % 8 != 0 || !whole8(c.k_page, c.k_place, c.k_head) ||
       !whole8(c.v_page, c.v_place, c.v_head))
     return FP4_ERR_ALIGNMENT;
-  const int64_t need = fp4_decode_attention_workspace(c.seqs, p->heads, c.kv_heads, c.head_dim);
+  const int64_t need = fp4_decode_attention_workspace(
+      c.seqs, (int64_t)c.seq_pages * c.page_size, p->heads, c.kv_heads, c.head_dim);
   if (need > 0 && (!p->workspace || p->workspace_bytes < need)) return FP4_ERR_INVALID_ARG;
   if (!aligned16(p->workspace)) return FP4_ERR_ALIGNMENT;
   return launch_decode_attention(*p, as_stream(stream));

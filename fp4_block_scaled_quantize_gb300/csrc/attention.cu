@@ -43,6 +43,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 // Groups of 16 positions a warp takes a step: what it keeps in flight.
 constexpr int units_of(int dp, int nt) { return dp <= 64 ? 2 : dp <= 128 && nt == 1 ? 1 : 1; }
 constexpr int kPerSM = 5;            // CTAs per SM at most (workspace bound)
+constexpr int kDirect = 512;         // positions up to which a CTA takes a whole row
 constexpr float kSlack = 8.0f;       // log2 by which scores may pass the maximum in use
 
 struct AtParams {
@@ -711,7 +712,7 @@ fp4_status launch(AtParams a, cudaStream_t s) {
   const int64_t tiles = rows * ceil_div(room, 16 * kWarps * units_of(DP, NT));
   if (rows > INT32_MAX) return FP4_ERR_SHAPE;
   a.tile = 16 * kWarps * units_of(DP, NT);
-  a.direct = room <= 512;
+  a.direct = room <= kDirect;
   a.ctas = (int)(a.direct ? rows : tiles < most ? tiles : most);
   kern<<<(unsigned)a.ctas, kThreads, smem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return FP4_ERR_CUDA;
@@ -738,7 +739,8 @@ fp4_status launch_type(const AtParams &a, int nt, cudaStream_t s) {
 
 }  // namespace
 
-int64_t decode_attention_workspace(int heads, int kv_heads, int head_dim) {
+int64_t decode_attention_workspace(int64_t room, int heads, int kv_heads, int head_dim) {
+  if (room <= kDirect) return 0;
   const int dp = dp_of(head_dim), cols = 8 * nt_of(heads / kv_heads, dp);
   return (int64_t)sm_count() * kPerSM * (2 * slot_floats(cols, dp) * sizeof(float) + sizeof(int4));
 }

@@ -187,6 +187,6 @@ fp4_status launch_matvec(const MatvecJob &j, cudaStream_t s);
 fp4_status launch_kv_append(const fp4_append_params &p, cudaStream_t s);
 fp4_status launch_decode_attention(const fp4_attention_params &p, cudaStream_t s);
 // Bytes of partial results launch_decode_attention may write.
-int64_t decode_attention_workspace(int heads, int kv_heads, int head_dim);
+int64_t decode_attention_workspace(int64_t room, int heads, int kv_heads, int head_dim);
 
 }  // namespace fp4

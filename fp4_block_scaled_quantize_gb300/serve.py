@@ -14,11 +14,12 @@ classes instead of being filled field by field.
 import ctypes
 import struct
 from contextlib import nullcontext
+from functools import lru_cache
 
 import torch
 
-from . import (FP4_FMT_UE5M3_B16, FP4_FMT_UE5M3_B32, FP4_SF_MMA, _check, _stream, fp4_operand,
-               fp4_sf_bytes, lib, n_stripes, FP4_FMT_NVFP4_CTA)
+from . import (FP4_FMT_NVFP4_CTA, FP4_FMT_UE5M3_B16, FP4_FMT_UE5M3_B32, FP4_SF_MMA, FP4Error,
+               _stream, fp4_sf_bytes, lib, n_stripes)
 
 FP4_BF16, FP4_F16, FP4_F32 = 0, 1, 2
 _TYPES = {torch.bfloat16: FP4_BF16, torch.float16: FP4_F16, torch.float32: FP4_F32}
@@ -55,10 +56,12 @@ class fp4_attention_params(ctypes.Structure):
 
 
 _CACHE = "PPqqqqqqPqqiiiiii"
+_OPERAND = struct.Struct("@PPPPi4xqq")
 _APPEND = struct.Struct("@" + _CACHE + "PPPPqqqqqqqqPPPqqiii4x")
 _ATTENTION = struct.Struct("@" + _CACHE + "PPPPqqqqPqiif4x")
 
 _entry = None
+_NOWHERE = nullcontext()
 
 
 def _lib():
@@ -70,7 +73,7 @@ def _lib():
         L.fp4_matvec.argtypes = [vp, i32, vp, i64, i32, i64, vp, i64, i32, vp]
         L.fp4_kv_append.argtypes = [vp, vp]
         L.fp4_decode_attention.argtypes = [vp, vp]
-        L.fp4_decode_attention_workspace.argtypes = [i32, i32, i32, i32]
+        L.fp4_decode_attention_workspace.argtypes = [i32, i64, i32, i32, i32]
         for f in ("fp4_matvec", "fp4_kv_append", "fp4_decode_attention"):
             getattr(L, f).restype = i32
         L.fp4_decode_attention_workspace.restype = i64
@@ -96,8 +99,8 @@ def fp4_decode_attention(p, stream=None):
                                        _stream(stream))
 
 
-def fp4_decode_attention_workspace(seqs, heads, kv_heads, head_dim):
-    return _lib().fp4_decode_attention_workspace(seqs, heads, kv_heads, head_dim)
+def fp4_decode_attention_workspace(seqs, room, heads, kv_heads, head_dim):
+    return _lib().fp4_decode_attention_workspace(seqs, room, heads, kv_heads, head_dim)
 
 
 # ------------------------------------------------------ allocating conveniences
@@ -108,17 +111,30 @@ def _on(stream):
 
 
 def _device(where, first, *rest):
-    """The one CUDA device of the tensors; it has to be the current one,
-    because that is where kernels are launched."""
+    """Index of the one CUDA device of the tensors; it has to be the current
+    one, because that is where kernels are launched."""
     dev = first.get_device()
     for t in rest:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{where}: tensors must share one device")
     if dev < 0:
         raise ValueError(f"{where}: tensors must be on a CUDA device")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"{where}: the tensors' device is not the current one")
-    return first.device
+    return dev
+
+
+def _handle(stream, dev):
+    """The stream's handle (of the device's current stream by default; asked
+    for directly, as a Stream object takes longer than the launch)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+@lru_cache(maxsize=1024)
+def _room(format, rows, cols, layout):
+    """(bytes of the scales, decode scales) of a copy of these sizes."""
+    return (fp4_sf_bytes(format, rows, cols, layout),
+            n_stripes(rows) if format == FP4_FMT_NVFP4_CTA else 1)
 
 
 def matvec(x, w, out_dtype=None, out=None, stream=None):
@@ -127,83 +143,99 @@ def matvec(x, w, out_dtype=None, out=None, stream=None):
     y is [M, N] (or [N]) in out_dtype -- x's dtype by default, or bfloat16,
     float16 or float32 -- or written to `out` (rows may be strided).  The
     activations are not quantised; see fp4_matvec in include/fp4.h."""
-    if x.dtype not in _HALVES:
+    q, sf, s_dec, shift, format, layout = w.q, w.sf, w.s_dec, w.row_shift, w.format, w.sf_layout
+    dtype, sizes = x.dtype, x.shape
+    if dtype not in _HALVES:
         raise ValueError("matvec: x must be bfloat16 or float16")
-    dim = x.dim()
-    if dim != 1 and dim != 2:
+    if len(sizes) == 2:
+        M = sizes[0]
+    elif len(sizes) == 1:
+        M = 1
+    else:
         raise ValueError("matvec: x must be [K] or [M, K]")
-    q, sf, s_dec, shift = w.q, w.sf, w.s_dec, w.row_shift
-    N, K = w.rows, w.k
-    if x.shape[-1] != K:
-        raise ValueError(f"matvec: x has {x.shape[-1]} columns, the weight {K}")
-    M = x.shape[0] if dim == 2 else 1
-    if K > 1 and x.stride(-1) != 1:
+    N, K = q.shape
+    K *= 2
+    if sizes[-1] != K:
+        raise ValueError(f"matvec: x has {sizes[-1]} columns, the weight {K}")
+    steps = x.stride()
+    if K > 1 and steps[-1] != 1:
         raise ValueError("matvec: the last dimension of x must be contiguous")
-    if not (q.is_contiguous() and sf.is_contiguous() and s_dec.is_contiguous()
-            and (shift is None or shift.is_contiguous())):
+    if not (q.is_contiguous() and sf.is_contiguous() and s_dec.is_contiguous()):
         raise ValueError("matvec: the weight copy is not contiguous")
-    if sf.numel() < fp4_sf_bytes(w.format, N, K, w.sf_layout) or \
-            s_dec.numel() < (n_stripes(N) if w.format == FP4_FMT_NVFP4_CTA else 1) or \
-            s_dec.dtype != torch.float32 or q.dtype != torch.uint8 or sf.dtype != torch.uint8:
+    codes, scales = _room(format, N, K, layout)
+    if sf.numel() < codes or s_dec.numel() < scales or s_dec.dtype != torch.float32 or \
+            q.dtype != torch.uint8 or sf.dtype != torch.uint8:
         raise ValueError("matvec: the weight copy's scales do not fit its format and layout")
-    if shift is not None and (w.format not in (FP4_FMT_UE5M3_B16, FP4_FMT_UE5M3_B32)
-                              or w.sf_layout != FP4_SF_MMA or shift.numel() < N
-                              or shift.dtype != torch.int8):
+    if shift is not None and (format not in (FP4_FMT_UE5M3_B16, FP4_FMT_UE5M3_B32)
+                              or layout != FP4_SF_MMA or shift.numel() < N
+                              or shift.dtype != torch.int8 or not shift.is_contiguous()):
         raise ValueError("matvec: row shifts belong to UE5M3 copies in the tensor-core layout")
-    device = _device("matvec", x, q, sf, s_dec, shift, out)
-    shape = (M, N) if dim == 2 else (N,)
+    dev = _device("matvec", x, q, sf, s_dec, shift, out)
+    shape = (M, N) if len(sizes) == 2 else (N,)
     if out is None:
-        dtype = x.dtype if out_dtype is None else out_dtype
-        if dtype not in _TYPES:
+        if out_dtype is None:
+            out_dtype = dtype
+        elif out_dtype not in _TYPES:
             raise ValueError("matvec: out_dtype must be bfloat16, float16 or float32")
-        with _on(stream):
-            out = torch.empty(shape, dtype=dtype, device=device)
-    elif out.dtype not in _TYPES or tuple(out.shape) != shape or (N > 1 and out.stride(-1) != 1) or \
-            (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError(f"matvec: out must be a {list(shape)} tensor with contiguous rows, in "
-                         "bfloat16, float16 or float32")
-    op = fp4_operand(q.data_ptr(), sf.data_ptr(), s_dec.data_ptr(),
-                     None if shift is None else shift.data_ptr(), w.format, N, K)
-    _check(fp4_matvec(op, w.sf_layout, x, x.stride(0) if M > 1 else K, _TYPES[x.dtype], M, out,
-                      out.stride(0) if M > 1 else N, _TYPES[out.dtype], stream), "fp4_matvec")
+        if stream is None:
+            out = torch.empty(shape, dtype=out_dtype, device=x.device)
+        else:
+            with _on(stream):
+                out = torch.empty(shape, dtype=out_dtype, device=x.device)
+        y_step = N
+    else:
+        if out.dtype not in _TYPES or out.shape != shape or (N > 1 and out.stride(-1) != 1) or \
+                (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"matvec: out must be a {list(shape)} tensor with contiguous rows, in "
+                             "bfloat16, float16 or float32")
+        out_dtype = out.dtype
+        y_step = out.stride(0) if M > 1 else N
+    op = _OPERAND.pack(q.data_ptr(), sf.data_ptr(), s_dec.data_ptr(),
+                       0 if shift is None else shift.data_ptr(), format, N, K)
+    code = _lib().fp4_matvec(op, layout, x.data_ptr(), steps[0] if M > 1 else K, _TYPES[dtype], M,
+                             out.data_ptr(), y_step, _TYPES[out_dtype], _handle(stream, dev))
+    if code:
+        raise FP4Error(code, "fp4_matvec")
     return out
 
 
 def _steps(where, name, t, sizes):
     """Strides of the dimensions before the last of a tensor of these sizes
     (0 along a dimension of one: it is never stepped along)."""
-    if tuple(t.shape) != sizes:
+    if t.shape != sizes:
         raise ValueError(f"{where}: {name} must be {list(sizes)}, not {list(t.shape)}")
-    st = t.stride()
-    if st[-1] != 1 and sizes[-1] > 1:
+    steps = t.stride()
+    if steps[-1] != 1 and sizes[-1] > 1:
         raise ValueError(f"{where}: the last dimension of {name} must be contiguous")
-    return [0 if n == 1 else s for n, s in zip(sizes[:-1], st)]
+    if 1 in sizes:
+        steps = [0 if n == 1 else s for n, s in zip(sizes, steps)]
+    return steps[:-1]
 
 
 def _cache_fields(where, k_pages, v_pages, page_table):
     """The fields of fp4_kv_cache, in order."""
-    dtype = k_pages.dtype
+    dtype, sizes, seqs = k_pages.dtype, k_pages.shape, page_table.shape
     if dtype not in _HALVES or v_pages.dtype != dtype:
         raise ValueError(f"{where}: keys and values must both be bfloat16 or both float16")
-    if k_pages.dim() != 4 or page_table.dim() != 2:
+    if len(sizes) != 4 or len(seqs) != 2:
         raise ValueError(f"{where}: k_pages must be [pages, page_size, kv_heads, head_dim], "
                          "page_table [seqs, pages of a sequence]")
     if page_table.dtype != torch.int32:
         raise ValueError(f"{where}: page_table must be int32")
-    sizes = tuple(k_pages.shape)
-    seqs, seq_pages = page_table.shape
-    if seq_pages > 1 and page_table.stride(1) != 1:
-        raise ValueError(f"{where}: the rows of page_table must be contiguous")
-    if 0 in sizes[1:]:
+    pages, page, heads, dim = sizes
+    if not (page and heads and dim):
         raise ValueError(f"{where}: pages without places, heads or elements")
+    seqs, wide = seqs
+    steps = page_table.stride()
+    if wide > 1 and steps[1] != 1:
+        raise ValueError(f"{where}: the rows of page_table must be contiguous")
     return (k_pages.data_ptr(), v_pages.data_ptr(), *_steps(where, "k_pages", k_pages, sizes),
             *_steps(where, "v_pages", v_pages, sizes), page_table.data_ptr(),
-            page_table.stride(0) if seqs > 1 else 0, sizes[0], seqs, seq_pages, sizes[1], sizes[2],
-            sizes[3], _TYPES[dtype])
+            steps[0] if seqs > 1 else 0, pages, seqs, wide, page, heads, dim, _TYPES[dtype])
 
 
 def _need_ints(where, name, t, n):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be a contiguous int32 tensor of {n}")
 
 
@@ -219,15 +251,16 @@ def kv_append(k, v, k_pages, v_pages, page_table, pos, seq=None, q=None, rope=No
     or None without q.  Tokens at negative positions are skipped."""
     where = "kv_append"
     cache = _cache_fields(where, k_pages, v_pages, page_table)
-    dtype, Hk, D = k_pages.dtype, k_pages.shape[2], k_pages.shape[3]
+    dtype, seqs, Hk, D = k_pages.dtype, cache[11], cache[14], cache[15]
     T = k.shape[0]
     if k.dtype != dtype or v.dtype != dtype or (q is not None and q.dtype != dtype):
         raise ValueError(f"{where}: q, k, v and the cache must share one dtype")
-    ks, vs = _steps(where, "k", k, (T, Hk, D)), _steps(where, "v", v, (T, Hk, D))
+    sizes = (T, Hk, D)
+    ks, vs = _steps(where, "k", k, sizes), _steps(where, "v", v, sizes)
     _need_ints(where, "pos", pos, T)
     if seq is not None:
         _need_ints(where, "seq", seq, T)
-    elif T > page_table.shape[0]:
+    elif T > seqs:
         raise ValueError(f"{where}: more tokens than sequences; give seq")
     rot_dim = rope_len = 0
     if rope is not None:
@@ -235,26 +268,33 @@ def kv_append(k, v, k_pages, v_pages, page_table, pos, seq=None, q=None, rope=No
             raise ValueError(f"{where}: rope must be a contiguous [positions, rot_dim] float32 tensor")
         rope_len, rot_dim = rope.shape
     heads, qs, os_ = 0, (0, 0), (0, 0)
-    device = _device(where, k, v, k_pages, v_pages, page_table, pos, seq, q, rope, q_out)
+    dev = _device(where, k, v, k_pages, v_pages, page_table, pos, seq, q, rope, q_out)
     if q is not None:
         heads = q.shape[1] if q.dim() == 3 else 0
         if heads < 1 or heads % Hk:
             raise ValueError(f"{where}: q must be [tokens, heads, head_dim], heads a multiple of {Hk}")
-        qs = _steps(where, "q", q, (T, heads, D))
+        sizes = (T, heads, D)
+        qs = _steps(where, "q", q, sizes)
         if q_out is None:
-            with _on(stream):
-                q_out = torch.empty((T, heads, D), dtype=dtype, device=device)
-        elif q_out.dtype != dtype:
-            raise ValueError(f"{where}: q_out must have q's dtype")
-        os_ = _steps(where, "q_out", q_out, (T, heads, D))
+            if stream is None:
+                q_out = torch.empty(sizes, dtype=dtype, device=q.device)
+            else:
+                with _on(stream):
+                    q_out = torch.empty(sizes, dtype=dtype, device=q.device)
+            os_ = (heads * D, D)
+        else:
+            if q_out.dtype != dtype:
+                raise ValueError(f"{where}: q_out must have q's dtype")
+            os_ = _steps(where, "q_out", q_out, sizes)
     elif q_out is not None:
         raise ValueError(f"{where}: q_out without q")
-    p = _APPEND.pack(*cache, k.data_ptr(), v.data_ptr(), q.data_ptr() if q is not None else 0,
-                     q_out.data_ptr() if q is not None else 0, *ks, *vs, *qs, *os_, pos.data_ptr(),
-                     seq.data_ptr() if seq is not None else 0,
-                     rope.data_ptr() if rope is not None else 0, rope_len, T, heads, rot_dim,
-                     1 if interleaved else 0)
-    _check(fp4_kv_append(p, stream), "fp4_kv_append")
+    p = _APPEND.pack(*cache, k.data_ptr(), v.data_ptr(), 0 if q is None else q.data_ptr(),
+                     0 if q is None else q_out.data_ptr(), *ks, *vs, *qs, *os_, pos.data_ptr(),
+                     0 if seq is None else seq.data_ptr(), 0 if rope is None else rope.data_ptr(),
+                     rope_len, T, heads, rot_dim, 1 if interleaved else 0)
+    code = _lib().fp4_kv_append(p, _handle(stream, dev))
+    if code:
+        raise FP4Error(code, "fp4_kv_append")
     return q_out
 
 
@@ -269,8 +309,7 @@ def decode_attention(q, k_pages, v_pages, page_table, lengths, scale=None, windo
     [seqs, heads].  A sequence of length 0 gives zeros (and -inf)."""
     where = "decode_attention"
     cache = _cache_fields(where, k_pages, v_pages, page_table)
-    dtype, Hk, D = k_pages.dtype, k_pages.shape[2], k_pages.shape[3]
-    seqs = page_table.shape[0]
+    dtype, seqs, Hk, D = k_pages.dtype, cache[11], cache[14], cache[15]
     heads = q.shape[1] if q.dim() == 3 else 0
     if q.dtype != dtype or heads < 1 or heads % Hk:
         raise ValueError(f"{where}: q must be [seqs, heads, head_dim] in the cache's dtype, heads a "
@@ -280,21 +319,36 @@ def decode_attention(q, k_pages, v_pages, page_table, lengths, scale=None, windo
     _need_ints(where, "lengths", lengths, seqs)
     if window < 0 or window > 0x7FFFFFFF:
         raise ValueError(f"{where}: window must be >= 0")
-    device = _device(where, q, k_pages, v_pages, page_table, lengths, out)
-    need = fp4_decode_attention_workspace(seqs, heads, Hk, D)
-    with _on(stream):
+    dev = _device(where, q, k_pages, v_pages, page_table, lengths, out)
+    need = _workspace(seqs, cache[12] * cache[13], heads, Hk, D, dev)
+    lse = work = None
+    with _on(stream) if stream is not None else _NOWHERE:
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=device)
-        elif out.dtype != dtype:
-            raise ValueError(f"{where}: out must have q's dtype")
-        lse = torch.empty((seqs, heads), dtype=torch.float32, device=device) if return_lse else None
-        work = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+            out = torch.empty(shape, dtype=dtype, device=q.device)
+            os_ = (heads * D, D)
+        else:
+            if out.dtype != dtype:
+                raise ValueError(f"{where}: out must have q's dtype")
+            os_ = _steps(where, "out", out, shape)
+        if return_lse:
+            lse = torch.empty((seqs, heads), dtype=torch.float32, device=q.device)
+        if need > 0:
+            work = torch.empty(need, dtype=torch.uint8, device=q.device)
     p = _ATTENTION.pack(*cache, lengths.data_ptr(), q.data_ptr(), out.data_ptr(),
-                        0 if lse is None else lse.data_ptr(), *qs, *_steps(where, "out", out, shape),
+                        0 if lse is None else lse.data_ptr(), *qs, *os_,
                         0 if work is None else work.data_ptr(), max(need, 0), heads, window,
                         D ** -0.5 if scale is None else scale)
-    _check(fp4_decode_attention(p, stream), "fp4_decode_attention")
+    code = _lib().fp4_decode_attention(p, _handle(stream, dev))
+    if code:
+        raise FP4Error(code, "fp4_decode_attention")
     return (out, lse) if return_lse else out
+
+
+@lru_cache(maxsize=1024)
+def _workspace(seqs, room, heads, kv_heads, head_dim, dev):
+    """fp4_decode_attention_workspace for these sizes on device `dev` (the
+    current one)."""
+    return fp4_decode_attention_workspace(seqs, room, heads, kv_heads, head_dim)
 
 
 def rope_table(positions, rot_dim, base=10000.0, device="cuda"):

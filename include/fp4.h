@@ -462,9 +462,10 @@ typedef struct {
 fp4_status fp4_decode_attention(const fp4_attention_params *p, void *stream);
 
 /* Workspace of fp4_decode_attention in bytes on the current device, whatever
- * the lengths; -1 for sizes it refuses. */
-int64_t fp4_decode_attention_workspace(int32_t seqs, int32_t heads, int32_t kv_heads,
-                                       int32_t head_dim);
+ * the lengths; room is seq_pages * page_size (short tables need none); -1 for
+ * sizes it refuses. */
+int64_t fp4_decode_attention_workspace(int32_t seqs, int64_t room, int32_t heads,
+                                       int32_t kv_heads, int32_t head_dim);
 
 /* Bytes of one scale-factor output for a copy with `rows` rows and `cols`
  * elements per row; -1 for an invalid format/layout. */

@@ -143,8 +143,9 @@ def test_attention_refusals_before_any_launch(L):
     assert call(lse=A + 2) == ALIGN and call(out=A + 1) == ALIGN
     assert call(q_seq=-8) == INVALID
     f = L.fp4_decode_attention_workspace
-    assert f(0, 4, 2, 64) == 0
-    assert f(2, 3, 2, 64) == -1 and f(2, 4, 0, 64) == -1 and f(2, 4, 2, 60) == -1 and f(-1, 4, 2, 64) == -1
+    assert f(0, 64, 4, 2, 64) == 0
+    assert f(2, 64, 3, 2, 64) == -1 and f(2, 64, 4, 0, 64) == -1 and f(2, 64, 4, 2, 60) == -1
+    assert f(-1, 64, 4, 2, 64) == -1 and f(2, -1, 4, 2, 64) == -1
 
 
 def test_python_refusals():
