@@ -13,7 +13,6 @@ classes instead of being filled field by field.
 """
 import ctypes
 import struct
-from contextlib import nullcontext
 from functools import lru_cache
 
 import torch
@@ -24,6 +23,7 @@ from . import (FP4_FMT_NVFP4_CTA, FP4_FMT_UE5M3_B16, FP4_FMT_UE5M3_B32, FP4_SF_M
 FP4_BF16, FP4_F16, FP4_F32 = 0, 1, 2
 _TYPES = {torch.bfloat16: FP4_BF16, torch.float16: FP4_F16, torch.float32: FP4_F32}
 _HALVES = (torch.bfloat16, torch.float16)
+_INT, _FLOAT = torch.int32, torch.float32
 
 
 class fp4_kv_cache(ctypes.Structure):
@@ -61,7 +61,6 @@ _APPEND = struct.Struct("@" + _CACHE + "PPPPqqqqqqqqPPPqqiii4x")
 _ATTENTION = struct.Struct("@" + _CACHE + "PPPPqqqqPqiif4x")
 
 _entry = None
-_NOWHERE = nullcontext()
 
 
 def _lib():
@@ -105,9 +104,12 @@ def fp4_decode_attention_workspace(seqs, room, heads, kv_heads, head_dim):
 
 # ------------------------------------------------------ allocating conveniences
 
-def _on(stream):
-    """Context in which outputs for work on `stream` are allocated."""
-    return nullcontext() if stream is None else torch.cuda.stream(stream)
+def _new(sizes, dtype, device, stream):
+    """A tensor for work on `stream`, which its memory then belongs to."""
+    if stream is None:
+        return torch.empty(sizes, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(sizes, dtype=dtype, device=device)
 
 
 def _device(where, first, *rest):
@@ -115,7 +117,7 @@ def _device(where, first, *rest):
     one, because that is where kernels are launched."""
     dev = first.get_device()
     for t in rest:
-        if t is not None and t.get_device() != dev:
+        if t.get_device() != dev:
             raise ValueError(f"{where}: tensors must share one device")
     if dev < 0:
         raise ValueError(f"{where}: tensors must be on a CUDA device")
@@ -170,24 +172,23 @@ def matvec(x, w, out_dtype=None, out=None, stream=None):
                               or layout != FP4_SF_MMA or shift.numel() < N
                               or shift.dtype != torch.int8 or not shift.is_contiguous()):
         raise ValueError("matvec: row shifts belong to UE5M3 copies in the tensor-core layout")
-    dev = _device("matvec", x, q, sf, s_dec, shift, out)
+    dev = _device("matvec", x, q, sf, s_dec)
+    if shift is not None:
+        _device("matvec", x, shift)
     shape = (M, N) if len(sizes) == 2 else (N,)
     if out is None:
         if out_dtype is None:
             out_dtype = dtype
         elif out_dtype not in _TYPES:
             raise ValueError("matvec: out_dtype must be bfloat16, float16 or float32")
-        if stream is None:
-            out = torch.empty(shape, dtype=out_dtype, device=x.device)
-        else:
-            with _on(stream):
-                out = torch.empty(shape, dtype=out_dtype, device=x.device)
+        out = _new(shape, out_dtype, x.device, stream)
         y_step = N
     else:
         if out.dtype not in _TYPES or out.shape != shape or (N > 1 and out.stride(-1) != 1) or \
                 (out_dtype is not None and out.dtype != out_dtype):
             raise ValueError(f"matvec: out must be a {list(shape)} tensor with contiguous rows, in "
                              "bfloat16, float16 or float32")
+        _device("matvec", x, out)
         out_dtype = out.dtype
         y_step = out.stride(0) if M > 1 else N
     op = _OPERAND.pack(q.data_ptr(), sf.data_ptr(), s_dec.data_ptr(),
@@ -200,42 +201,53 @@ def matvec(x, w, out_dtype=None, out=None, stream=None):
 
 
 def _steps(where, name, t, sizes):
-    """Strides of the dimensions before the last of a tensor of these sizes
+    """Strides of a tensor of these sizes whose last dimension is contiguous
     (0 along a dimension of one: it is never stepped along)."""
     if t.shape != sizes:
         raise ValueError(f"{where}: {name} must be {list(sizes)}, not {list(t.shape)}")
     steps = t.stride()
     if steps[-1] != 1 and sizes[-1] > 1:
         raise ValueError(f"{where}: the last dimension of {name} must be contiguous")
-    if 1 in sizes:
-        steps = [0 if n == 1 else s for n, s in zip(sizes, steps)]
-    return steps[:-1]
+    return [0 if n == 1 else s for n, s in zip(sizes, steps)]
+
+
+def _rows(where, name, t, sizes):
+    """(token, head) strides of a [tokens, heads, head_dim] tensor."""
+    if t.shape == sizes:
+        a, b, c = t.stride()
+        if c == 1 and not (a | b) & 7:
+            return a, b
+    return _steps(where, name, t, sizes)[:2]
 
 
 def _cache_fields(where, k_pages, v_pages, page_table):
     """The fields of fp4_kv_cache, in order."""
-    dtype, sizes, seqs = k_pages.dtype, k_pages.shape, page_table.shape
-    if dtype not in _HALVES or v_pages.dtype != dtype:
+    dtype, sizes, table = k_pages.dtype, k_pages.shape, page_table.shape
+    if dtype not in _HALVES or v_pages.dtype is not dtype:
         raise ValueError(f"{where}: keys and values must both be bfloat16 or both float16")
-    if len(sizes) != 4 or len(seqs) != 2:
+    if len(sizes) != 4 or len(table) != 2:
         raise ValueError(f"{where}: k_pages must be [pages, page_size, kv_heads, head_dim], "
                          "page_table [seqs, pages of a sequence]")
-    if page_table.dtype != torch.int32:
+    if page_table.dtype is not _INT:
         raise ValueError(f"{where}: page_table must be int32")
     pages, page, heads, dim = sizes
     if not (page and heads and dim):
         raise ValueError(f"{where}: pages without places, heads or elements")
-    seqs, wide = seqs
-    steps = page_table.stride()
-    if wide > 1 and steps[1] != 1:
+    seqs, wide = table
+    step, one = page_table.stride()
+    if one != 1 and wide > 1:
         raise ValueError(f"{where}: the rows of page_table must be contiguous")
-    return (k_pages.data_ptr(), v_pages.data_ptr(), *_steps(where, "k_pages", k_pages, sizes),
-            *_steps(where, "v_pages", v_pages, sizes), page_table.data_ptr(),
-            steps[0] if seqs > 1 else 0, pages, seqs, wide, page, heads, dim, _TYPES[dtype])
+    ka, kb, kc, kd = k_pages.stride()
+    va, vb, vc, vd = v_pages.stride()
+    if kd != 1 or vd != 1 or v_pages.shape != sizes or (ka | kb | kc | va | vb | vc) & 7:
+        ka, kb, kc, kd = _steps(where, "k_pages", k_pages, sizes)
+        va, vb, vc, vd = _steps(where, "v_pages", v_pages, sizes)
+    return (k_pages.data_ptr(), v_pages.data_ptr(), ka, kb, kc, va, vb, vc, page_table.data_ptr(),
+            step if seqs > 1 else 0, pages, seqs, wide, page, heads, dim, _TYPES[dtype])
 
 
 def _need_ints(where, name, t, n):
-    if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous():
+    if t.dtype is not _INT or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be a contiguous int32 tensor of {n}")
 
 
@@ -251,48 +263,52 @@ def kv_append(k, v, k_pages, v_pages, page_table, pos, seq=None, q=None, rope=No
     or None without q.  Tokens at negative positions are skipped."""
     where = "kv_append"
     cache = _cache_fields(where, k_pages, v_pages, page_table)
-    dtype, seqs, Hk, D = k_pages.dtype, cache[11], cache[14], cache[15]
-    T = k.shape[0]
-    if k.dtype != dtype or v.dtype != dtype or (q is not None and q.dtype != dtype):
+    dtype, Hk, D = k_pages.dtype, cache[14], cache[15]
+    if k.dtype is not dtype or v.dtype is not dtype:
         raise ValueError(f"{where}: q, k, v and the cache must share one dtype")
+    T = k.shape[0]
     sizes = (T, Hk, D)
-    ks, vs = _steps(where, "k", k, sizes), _steps(where, "v", v, sizes)
+    ks, kh = _rows(where, "k", k, sizes)
+    vs, vh = _rows(where, "v", v, sizes)
     _need_ints(where, "pos", pos, T)
+    extra = []
+    seq_at = rope_at = q_at = out_at = rot_dim = rope_len = heads = qs = qh = os_ = oh = 0
     if seq is not None:
         _need_ints(where, "seq", seq, T)
-    elif T > seqs:
+        extra.append(seq)
+        seq_at = seq.data_ptr()
+    elif T > cache[11]:
         raise ValueError(f"{where}: more tokens than sequences; give seq")
-    rot_dim = rope_len = 0
     if rope is not None:
-        if rope.dtype != torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+        if rope.dtype is not _FLOAT or rope.dim() != 2 or not rope.is_contiguous():
             raise ValueError(f"{where}: rope must be a contiguous [positions, rot_dim] float32 tensor")
+        extra.append(rope)
         rope_len, rot_dim = rope.shape
-    heads, qs, os_ = 0, (0, 0), (0, 0)
-    dev = _device(where, k, v, k_pages, v_pages, page_table, pos, seq, q, rope, q_out)
+        rope_at = rope.data_ptr()
     if q is not None:
         heads = q.shape[1] if q.dim() == 3 else 0
+        if q.dtype is not dtype:
+            raise ValueError(f"{where}: q, k, v and the cache must share one dtype")
         if heads < 1 or heads % Hk:
             raise ValueError(f"{where}: q must be [tokens, heads, head_dim], heads a multiple of {Hk}")
         sizes = (T, heads, D)
-        qs = _steps(where, "q", q, sizes)
+        qs, qh = _rows(where, "q", q, sizes)
         if q_out is None:
-            if stream is None:
-                q_out = torch.empty(sizes, dtype=dtype, device=q.device)
-            else:
-                with _on(stream):
-                    q_out = torch.empty(sizes, dtype=dtype, device=q.device)
-            os_ = (heads * D, D)
+            q_out = _new(sizes, dtype, q.device, stream)
+            os_, oh = heads * D, D
         else:
-            if q_out.dtype != dtype:
+            if q_out.dtype is not dtype:
                 raise ValueError(f"{where}: q_out must have q's dtype")
-            os_ = _steps(where, "q_out", q_out, sizes)
+            os_, oh = _rows(where, "q_out", q_out, sizes)
+        extra += q, q_out
+        q_at, out_at = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError(f"{where}: q_out without q")
-    p = _APPEND.pack(*cache, k.data_ptr(), v.data_ptr(), 0 if q is None else q.data_ptr(),
-                     0 if q is None else q_out.data_ptr(), *ks, *vs, *qs, *os_, pos.data_ptr(),
-                     0 if seq is None else seq.data_ptr(), 0 if rope is None else rope.data_ptr(),
-                     rope_len, T, heads, rot_dim, 1 if interleaved else 0)
-    code = _lib().fp4_kv_append(p, _handle(stream, dev))
+    dev = _device(where, k, v, k_pages, v_pages, page_table, pos, *extra)
+    code = _lib().fp4_kv_append(
+        _APPEND.pack(*cache, k.data_ptr(), v.data_ptr(), q_at, out_at, ks, kh, vs, vh, qs, qh, os_,
+                     oh, pos.data_ptr(), seq_at, rope_at, rope_len, T, heads, rot_dim,
+                     1 if interleaved else 0), _handle(stream, dev))
     if code:
         raise FP4Error(code, "fp4_kv_append")
     return q_out
@@ -311,34 +327,32 @@ def decode_attention(q, k_pages, v_pages, page_table, lengths, scale=None, windo
     cache = _cache_fields(where, k_pages, v_pages, page_table)
     dtype, seqs, Hk, D = k_pages.dtype, cache[11], cache[14], cache[15]
     heads = q.shape[1] if q.dim() == 3 else 0
-    if q.dtype != dtype or heads < 1 or heads % Hk:
+    if q.dtype is not dtype or heads < 1 or heads % Hk:
         raise ValueError(f"{where}: q must be [seqs, heads, head_dim] in the cache's dtype, heads a "
                          f"multiple of {Hk}")
-    shape = (seqs, heads, D)
-    qs = _steps(where, "q", q, shape)
+    sizes = (seqs, heads, D)
+    qs, qh = _rows(where, "q", q, sizes)
     _need_ints(where, "lengths", lengths, seqs)
     if window < 0 or window > 0x7FFFFFFF:
         raise ValueError(f"{where}: window must be >= 0")
-    dev = _device(where, q, k_pages, v_pages, page_table, lengths, out)
+    dev = _device(where, q, k_pages, v_pages, page_table, lengths)
+    device = q.device
+    if out is None:
+        out = _new(sizes, dtype, device, stream)
+        os_, oh = heads * D, D
+    else:
+        if out.dtype is not dtype:
+            raise ValueError(f"{where}: out must have q's dtype")
+        os_, oh = _rows(where, "out", out, sizes)
+        _device(where, q, out)
+    lse = _new((seqs, heads), _FLOAT, device, stream) if return_lse else None
     need = _workspace(seqs, cache[12] * cache[13], heads, Hk, D, dev)
-    lse = work = None
-    with _on(stream) if stream is not None else _NOWHERE:
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=q.device)
-            os_ = (heads * D, D)
-        else:
-            if out.dtype != dtype:
-                raise ValueError(f"{where}: out must have q's dtype")
-            os_ = _steps(where, "out", out, shape)
-        if return_lse:
-            lse = torch.empty((seqs, heads), dtype=torch.float32, device=q.device)
-        if need > 0:
-            work = torch.empty(need, dtype=torch.uint8, device=q.device)
-    p = _ATTENTION.pack(*cache, lengths.data_ptr(), q.data_ptr(), out.data_ptr(),
-                        0 if lse is None else lse.data_ptr(), *qs, *os_,
-                        0 if work is None else work.data_ptr(), max(need, 0), heads, window,
-                        D ** -0.5 if scale is None else scale)
-    code = _lib().fp4_decode_attention(p, _handle(stream, dev))
+    work = _new(need, torch.uint8, device, stream) if need > 0 else None
+    code = _lib().fp4_decode_attention(
+        _ATTENTION.pack(*cache, lengths.data_ptr(), q.data_ptr(), out.data_ptr(),
+                        lse.data_ptr() if return_lse else 0, qs, qh, os_, oh,
+                        work.data_ptr() if need > 0 else 0, need if need > 0 else 0, heads, window,
+                        D ** -0.5 if scale is None else scale), _handle(stream, dev))
     if code:
         raise FP4Error(code, "fp4_decode_attention")
     return (out, lse) if return_lse else out
