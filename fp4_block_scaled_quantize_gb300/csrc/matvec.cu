@@ -222,29 +222,23 @@ struct Loader {
   }
 };
 
-// The f16 scales over the lane's 64 columns of one row: blocks of 16, pairs
-// {0, 1} and {2, 3} (block h in half h % 2 of h[h / 2]); blocks of 32, one pair.
+// The f16 scales over 32 of the lane's 64 columns of one row, from the codes
+// at the bottom of w: two blocks of 16 (low and high half), or one of 32.
 template <int KIND, int BLOCK>
-__device__ __forceinline__ void scale_pairs(uint32_t w, int top, uint32_t *h) {
+__device__ __forceinline__ uint32_t scale_pair(uint32_t w, int top) {
   if (KIND == kMXFP4) {
     // 2^(code - top + 13): f16 exponent field 28 + code - top, subnormal below 1
-    const int e0 = 28 + (int)(w & 255u) - top, e1 = 28 + (int)((w >> 8) & 255u) - top;
-    const uint32_t v0 = e0 >= 1 ? (uint32_t)e0 << 10 : (e0 >= -9 ? 1u << (e0 + 9) : 0u);
-    const uint32_t v1 = e1 >= 1 ? (uint32_t)e1 << 10 : (e1 >= -9 ? 1u << (e1 + 9) : 0u);
-    h[0] = v0 | (v1 << 16);
-    return;
+    const int e = 28 + (int)(w & 255u) - top;
+    return (e >= 1 ? (uint32_t)e << 10 : e >= -9 ? 1u << (e + 9) : 0u) * 0x10001u;
   }
-#pragma unroll
-  for (int i = 0; i < 32 / BLOCK; ++i) {  // (block 32: one pair)
-    if (KIND == kNVFP4) {
-      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-          : "=r"(h[i])
-          : "r"(i ? w >> 16 : w));
-    } else {
-      // E5M3 is the head of an f16; times 2^-3 to leave room for a product
-      h[i] = hmul2(__byte_perm(w, 0, i ? 0x3424 : 0x1404) >> 1, 0x30003000u);
-    }
+  if (BLOCK == 32) w = __byte_perm(w, 0, 0x4400);  // the one code twice
+  if (KIND == kNVFP4) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(w));
+    return h;
   }
+  // E5M3 is the head of an f16; times 2^-3 to leave room for a product
+  return hmul2(__byte_perm(w, 0, 0x1404) >> 1, 0x30003000u);
 }
 
 template <typename TX>
@@ -256,64 +250,80 @@ struct Is<__nv_bfloat16> {
   static constexpr bool bf16 = true;
 };
 
+// Eight BF16 values times the power of two that brings the largest of the
+// warp's 256 into [2^15, 2^16), as f16; returns the exponent taken out.
+__device__ __forceinline__ int normalize(uint32_t *w) {
+  auto as2 = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162 *>(&v); };
+  const __nv_bfloat162 t = __hmax2(__hmax2(__habs2(as2(w[0])), __habs2(as2(w[1]))),
+                                   __hmax2(__habs2(as2(w[2])), __habs2(as2(w[3]))));  // (passes over NaN)
+  const uint32_t u = *reinterpret_cast<const uint32_t *>(&t);
+  const uint32_t top = __reduce_max_sync(~0u, max(u & 0xFFFFu, u >> 16));
+  // exponent of the largest finite magnitude (2^133 x subnormals: 1 + mantissa bits)
+  const int f = (int)(top >> 7);
+  const int e = f >= 255 ? 127 : f > 0 ? f - 127 : top ? (31 - __clz((int)top)) - 133 : 0;
+  const int ex = e - 15;
+  if (ex >= -127) {
+    const float s = pow2(-ex);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const __half2 v = __floats2half2_rn(bf16_lo(w[q]) * s, bf16_hi(w[q]) * s);
+      w[q] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+  } else {  // binary32 does not hold 2^-ex: two factors
+    const float s = pow2(-ex - 64), s2 = 0x1p64f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const __half2 v = __floats2half2_rn(bf16_lo(w[q]) * s * s2, bf16_hi(w[q]) * s * s2);
+      w[q] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+  }
+  return ex;
+}
+
 // x[0 .. M) over steps [s0, s0 + n) as f16 into shared memory, and the power
 // of two taken out of each (token, step); a warp per (token, step), eight
-// elements a lane.
+// elements a lane, the loads of eight tokens requested together.
 template <typename TX>
 __device__ void prepare_x(const MatvecJob &j, int64_t m0, int M, int s0, int n, uint8_t *xs, int pitch,
                           float *sx, int cols, int warps) {
   const TX *x = static_cast<const TX *>(j.x) + m0 * j.xs;
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (M == 1 || j.xs % 8 == 0);
-  const int piece = threadIdx.x & 31;
-  constexpr int kBatch = 4;  // units whose loads are requested together
-  for (int u0 = threadIdx.x >> 5; u0 < M * n; u0 += kBatch * warps) {
-    uint32_t w[kBatch][4];
-    int at[kBatch], sat[kBatch];
+  const int warp = threadIdx.x >> 5, piece = threadIdx.x & 31;
+  const int across = min(warps, n), deep = warps / across;  // warps along K, and along the tokens
+  if (warp >= across * deep) return;
+  constexpr int kBatch = 8;
+  for (int c = warp % across; c < n; c += across) {
+    const int k = (s0 + c) * kStep + piece * 8;
+    const bool in = k < (int)j.K;  // K is a multiple of 16: a piece is inside or outside
+    for (int m = warp / across; m < M; m += kBatch * deep) {
+      const TX *from = x + m * j.xs + k;
+      uint32_t w[kBatch][4];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int u = u0 + i * warps;
-      w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;
-      at[i] = -1;
-      if (u >= M * n) continue;
-      const int m = u / n, c = u - m * n;
-      // piece q of lane t (piece = 8 t + q) lies at 64 q + 16 t
-      at[i] = m * pitch + c * 512 + (piece & 7) * 64 + (piece >> 3) * 16;
-      sat[i] = c * cols + m;
-      const int64_t k = (int64_t)(s0 + c) * kStep + piece * 8;
-      if (k >= j.K) continue;  // K is a multiple of 16: a piece is inside or outside
-      const TX *p = x + m * j.xs + k;
-      if (vec) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-        w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
-      } else {
-        const uint16_t *e = reinterpret_cast<const uint16_t *>(p);
+      for (int i = 0; i < kBatch; ++i) {
+        w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;
+        if (in && m + i * deep < M) {
+          if (vec) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(from));
+            w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+          } else {
+            const uint16_t *e = reinterpret_cast<const uint16_t *>(from);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) w[i][q] = e[2 * q] | ((uint32_t)e[2 * q + 1] << 16);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (at[i] < 0) continue;  // the same for all lanes of a warp
-      int ex = 0;
-      if (Is<TX>::bf16) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) top = max(top, max(w[i][q] & 0x7FFFu, (w[i][q] >> 16) & 0x7FFFu));
-        top = __reduce_max_sync(~0u, top);
-        // exponent of the largest finite magnitude (2^133 x subnormals: 1 + mantissa bits)
-        const int f = (int)(top >> 7);
-        const int e = f >= 255 ? 127 : f > 0 ? f - 127 : top ? (31 - __clz((int)top)) - 133 : 0;
-        ex = e - 15;
-        const int h1 = -ex / 2;  // 2^-ex in two factors that binary32 holds
-        const float f1 = pow2(h1), f2 = pow2(-ex - h1);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const __half2 v = __floats2half2_rn(bf16_lo(w[i][q]) * f1 * f2, bf16_hi(w[i][q]) * f1 * f2);
-          w[i][q] = *reinterpret_cast<const uint32_t *>(&v);
+            for (int q = 0; q < 4; ++q) w[i][q] = e[2 * q] | ((uint32_t)e[2 * q + 1] << 16);
+          }
         }
+        from += deep * j.xs;
       }
-      *reinterpret_cast<uint4 *>(xs + at[i]) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
-      if (piece == 0) sx[sat[i]] = pow2(ex);
+      // piece q of lane t (piece = 8 t + q) lies at 64 q + 16 t
+      uint8_t *to = xs + m * pitch + c * 512 + (piece & 7) * 64 + (piece >> 3) * 16;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (m + i * deep >= M) break;
+        int ex = 0;
+        if (Is<TX>::bf16) ex = normalize(w[i]);
+        *reinterpret_cast<uint4 *>(to) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+        to += deep * pitch;
+        if (piece == 0) sx[c * cols + m + i * deep] = pow2(ex);
+      }
     }
   }
 }
@@ -357,7 +367,7 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
   __syncwarp();
   const int64_t tile0 = (int64_t)cluster * group + tw, hop = (int64_t)p.clusters * group;
   const int mine = tw < group && tile0 < p.tiles ? (int)((p.tiles - 1 - tile0) / hop) + 1 : 0;  // the warp's tiles
-  int64_t ahead = (int64_t)mine * ns, flying = 0;  // stages to request, requested and not read
+  int ahead = mine * ns, flying = 0;  // stages to request, requested and not read
   int64_t ld_tile = tile0;
   int ld_left = ns, ld_slot = 0;
   const bool tiled = p.words == kTiled;
@@ -398,7 +408,6 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
         live = false;
         break;
       }
-      // the whole stage into registers, so that it is filled again meanwhile
       uint32_t codes[4];
       const uint8_t *wl = word_ring + slot * kWords;
       if (tiled) {
@@ -410,53 +419,60 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
 #pragma unroll
         for (int i = 0; i < 4; ++i) codes[i] = *reinterpret_cast<const uint32_t *>(wl + 128 * i + o);
       }
-      uint4 w[2][4];
-      const uint8_t *ra = ring + slot * kPayload + g * 128;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[h][i] = *reinterpret_cast<const uint4 *>(ra + 1024 * i + (at0 ^ (16 * h)));
-      --flying;
-      if (++slot == depth) {
-        slot = 0;
-        phase ^= 1;
-      }
-      __syncwarp();  // every lane has read the stage
-      if (ahead) issue();
-      uint32_t sc[4][2];
       float f[4];
+      int top[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (BLOCK == 32 && (t & 1)) codes[i] >>= 16;  // the lane's half of the word
-        int top = 0;
         if (KIND == kMXFP4) {
-          top = max((int)(codes[i] & 255u), (int)((codes[i] >> 8) & 255u));
-          top = max(top, __shfl_xor_sync(~0u, top, 1));
-          top = max(top, __shfl_xor_sync(~0u, top, 2));
-          f[i] = pow2(top - 140);  // 2^(top - 127) / 2^13
+          top[i] = max((int)(codes[i] & 255u), (int)((codes[i] >> 8) & 255u));
+          top[i] = max(top[i], __shfl_xor_sync(~0u, top[i], 1));
+          top[i] = max(top[i], __shfl_xor_sync(~0u, top[i], 2));
+          f[i] = pow2(top[i] - 140);  // 2^(top - 127) / 2^13
         }
-        scale_pairs<KIND, BLOCK>(codes[i], top, sc[i]);
       }
       float d[NT][2][4] = {};
+      const uint8_t *ra = ring + slot * kPayload + g * 128 + at0;
+      // 32 of the lane's 64 columns at a time, a 16-byte piece of each row.
+      // Not unrolled: at twice the size the loop outgrows the instruction
+      // cache (8 tokens, 131072 x 4096: 65 us).
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        uint4 w[4];
+        uint32_t sc[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {  // 32 of the lane's 64 columns: a 16-byte piece of each row
+        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(ra + 1024 * i);
+        ra = ring + slot * kPayload + g * 128 + (at0 ^ 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sc[i] = scale_pair<KIND, BLOCK>(codes[i], top[i]);
+          codes[i] >>= BLOCK == 16 ? 16 : 8;
+        }
+        if (h) {
+          --flying;
+          if (++slot == depth) {
+            slot = 0;
+            phase ^= 1;
+          }
+          __syncwarp();  // every lane has read the stage: it is filled again meanwhile
+          if (ahead) issue();
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint4 v[NT];
 #pragma unroll
           for (int c = 0; c < NT; ++c)
-            v[c] = *reinterpret_cast<const uint4 *>(xl[c] + xo + (4 * h + q) * 64);
+            v[c] = *reinterpret_cast<const uint4 *>(xl[c] + xo + q * 64);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             uint32_t a[4], b[4];
-            const uint4 &wa = w[h][2 * u], &wb = w[h][2 * u + 1];
+            const uint4 &wa = w[2 * u], &wb = w[2 * u + 1];
             decode8(q == 0 ? wa.x : q == 1 ? wa.y : q == 2 ? wa.z : wa.w, a);
             decode8(q == 0 ? wb.x : q == 1 ? wb.y : q == 2 ? wb.z : wb.w, b);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              a[e] = BLOCK == 16 ? hmul2_by(a[e], sc[2 * u][h], q >= 2) : hmul2_by(a[e], sc[2 * u][0], h);
-              b[e] = BLOCK == 16 ? hmul2_by(b[e], sc[2 * u + 1][h], q >= 2) : hmul2_by(b[e], sc[2 * u + 1][0], h);
+              a[e] = hmul2_by(a[e], sc[2 * u], BLOCK == 16 && q >= 2);
+              b[e] = hmul2_by(b[e], sc[2 * u + 1], BLOCK == 16 && q >= 2);
             }
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
@@ -465,6 +481,7 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
             }
           }
         }
+        xo += 256;
       }
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
@@ -478,7 +495,6 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
                                           : fmaf(d[c][u][e], x, acc[c][u][e]);
           }
       }
-      xo += 512;
       sxl += kCols;
     }
     // join the parts of the tiles of this round, in K order; a warp whose tile
@@ -503,53 +519,44 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
           for (int e = 0; e < 4; ++e)
             o[(8 * c + 2 * t + (e & 1)) * kRows + g + 16 * u + 8 * (e >> 1)] = acc[c][u][e];
     }
-    // outputs of the round: group tiles x M tokens x 32 rows, shared by the
-    // cluster's CTAs; what each is multiplied by is requested before the wait
-    const int outs = (alone ? 1 : group) * M * kRows, hops = alone ? 32 : kThreads * S;
-    int i = alone ? lane : (int)threadIdx.x * S + rank;
-    auto place = [&](int o, int &tg, int &m) {
-      const int mt = o / kRows, row = o % kRows;
-      tg = alone ? tw : mt / M;
-      m = alone ? mt : mt - tg * M;
-      const int64_t tile = (r * (int64_t)p.clusters + cluster) * group + tg;
-      return ld.first_row(tile, tiled) + (tiled ? 32 * (row >> 3) + (row & 7) : row);
-    };
-    auto factors = [&](int64_t n, int &shift, float &sd) {
-      shift = KIND == kUE5M3 ? 3 : 0;
-      if (n >= j.N) return;
-      if (j.shift) shift += j.shift[n];
-      sd = j.sd[j.stripes ? n >> 7 : 0];
-    };
-    int tg = 0, m = 0, shift = 0;
+    // A warp writes 32 rows of a tile for one token at a time, a row a lane;
+    // (tile, token) pairs go around the warps of the cluster.  What a row is
+    // multiplied by is requested before the wait.
+    const int outs = alone ? M : group * M, hops = alone ? 1 : kWarps * S;
+    int shift = 0, tg = -1;
     float sd = 0.0f;
     int64_t n = j.N;
-    if (i < outs) {
-      n = place(i, tg, m);
-      factors(n, shift, sd);
-    }
+    auto row_of = [&](int to) {
+      if (to == tg) return;
+      tg = to;
+      const int64_t tile = (r * (int64_t)p.clusters + cluster) * group + tg;
+      n = ld.first_row(tile, tiled) + (tiled ? 32 * (lane >> 3) + (lane & 7) : lane);
+      if (n >= j.N) return;
+      shift = (KIND == kUE5M3 ? 3 : 0) + (j.shift ? j.shift[n] : 0);
+      sd = j.sd[j.stripes ? n >> 7 : 0];
+    };
+    int i = alone ? 0 : warp * S + rank;
+    if (i < outs) row_of(alone ? tw : i / M);
     sync();
-    while (i < outs) {
-      if (n < j.N) {
-        float v = 0.0f;
-        for (int q = 0; q < S; ++q) {
-          const float *from = S > 1 ? cg::this_cluster().map_shared_rank(parts, q) : parts;
-          from += (tg * sk * kCols + m) * kRows + i % kRows;
-          for (int w = 0; w < sk; ++w) v += from[w * kCols * kRows];
-        }
-        v = scalbnf(v, shift) * sd;
-        const int64_t at = (m0 + m) * j.ys + n;
-        if (j.y_type == FP4_F32)
-          static_cast<float *>(j.y)[at] = v;
-        else if (j.y_type == FP4_BF16)
-          static_cast<__nv_bfloat16 *>(j.y)[at] = __float2bfloat16_rn(v);
-        else
-          static_cast<__half *>(j.y)[at] = __float2half_rn(v);
+#pragma unroll 1
+    for (; i < outs; i += hops) {
+      row_of(alone ? tw : i / M);
+      if (n >= j.N) continue;
+      const int m = alone ? i : i - tg * M;
+      float v = 0.0f;
+      for (int q = 0; q < S; ++q) {
+        const float *from = S > 1 ? cg::this_cluster().map_shared_rank(parts, q) : parts;
+        from += (tg * sk * kCols + m) * kRows + lane;
+        for (int w = 0; w < sk; ++w) v += from[w * kCols * kRows];
       }
-      i += hops;
-      if (i < outs) {
-        n = place(i, tg, m);
-        factors(n, shift, sd);
-      }
+      v = v * pow2(shift >> 1) * pow2(shift - (shift >> 1)) * sd;  // the exponent in two steps: no overflow between
+      const int64_t at = (m0 + m) * j.ys + n;
+      if (j.y_type == FP4_F32)
+        static_cast<float *>(j.y)[at] = v;
+      else if (j.y_type == FP4_BF16)
+        static_cast<__nv_bfloat16 *>(j.y)[at] = __float2bfloat16_rn(v);
+      else
+        static_cast<__half *>(j.y)[at] = __float2half_rn(v);
     }
   }
   if (!live) {  // copies still in flight land (bounded) before the ring goes away
