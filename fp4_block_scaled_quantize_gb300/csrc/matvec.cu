@@ -52,21 +52,23 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kStep = 256;             // columns a step
-constexpr int kRows = 32;              // weight rows of a tile: two MMA row tiles
-constexpr int kPayload = kRows * kStep / 2;  // bytes of a stage: payload, then scale words
-constexpr int kWords = 512;            // 4 scale words a row, 32 rows
+constexpr int kWords = 512;            // scale bytes of a stage
 constexpr int kMaxDepth = 4;
 constexpr int kMaxSmem = 227 * 1024;
 
-// Most warps of a CTA: with two token tiles a warp needs more than 128 registers.
-constexpr int max_warps(int nt) { return nt == 1 ? 16 : 12; }
+constexpr int kMaxWarps = 16;
+// Weight rows of a tile: two MMA row tiles share the loads of x; with two
+// token tiles one, so that 16 warps have the registers and, beside twice the
+// x, the shared memory (32 rows and 12 warps, 16 tokens, 131072 x 4096: 103 us).
+constexpr int rows_of(int nt) { return nt == 1 ? 32 : 16; }
+constexpr int payload_of(int nt) { return rows_of(nt) * kStep / 2; }  // bytes of a stage
 
 struct MvParams {
-  CUtensorMap map;   // payload [N][K / 2], boxes of 32 or 8 rows x 128 bytes
+  CUtensorMap map;   // payload [N][K / 2], boxes of 8, 16 or 32 rows x 128 bytes
   CUtensorMap smap;  // scales, see Words
   MatvecJob j;
   int steps;         // ceil(K / 256)
-  int tiles;         // 4 ceil(N / 128)
+  int tiles;         // of all rows, N rounded up to 128
   int warps;         // of a CTA
   int sk, S;         // warps and CTAs that share a tile along K
   int rounds;        // row tiles a warp takes, one after the other
@@ -139,25 +141,29 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 // Scales of a stage in shared memory, and the rows of a tile.
 //   kTiled: the tensor-core layout.  512-byte tiles hold 32 lines of 16 bytes,
 //     the words of rows l, l + 32, l + 64, l + 96 of their 128 rows; so a
-//     tile of weight rows is 4 groups of 8 rows 32 apart, its payload four TMA
-//     boxes of 8 rows, and its scales 128 contiguous bytes of each 64 (or,
-//     32-element blocks, 128) columns: one box, no byte unused.  Lane (g, t)
-//     finds its four words in 16 bytes at 128 t + 16 g (t / 2 for 32-blocks).
-//   kBoxed: plain rows with a pitch of whole 16 bytes: one box of 32 rows x 16
-//     bytes (with 32-element blocks the 16 bytes that hold the step's 8);
+//     tile of weight rows is 4 (of 16 rows: 2) groups of 8 rows 32 apart, its
+//     payload a TMA box for each, and its scales lie in 128 contiguous bytes
+//     of each 64 (or, 32-element blocks, 128) columns: one box.  Lane (g, t)
+//     finds its words in 16 bytes at 128 t + 16 g (t / 2 for 32-blocks).
+//   kBoxed: plain rows with a pitch of whole 16 bytes: one box of the rows x
+//     16 bytes (with 32-element blocks the 16 bytes that hold the step's 8);
 //     word i of a lane at 128 i + 4 lane (row g + 8 i, word t).
 //   kPieces, kBytes: plain rows of any other pitch, the same place, by 4-byte
 //     cp.async or byte loads.
 enum Words { kTiled = 0, kBoxed = 1, kPieces = 2, kBytes = 3 };
 
 // Fills a warp's stages one after the other.
-template <int BLOCK, bool TMA>
+template <int BLOCK, bool TMA, int kRows>
 struct Loader {
+  static constexpr int kPayload = kRows * kStep / 2, kGroups = kRows / 8;
   int step, row0;        // of the next stage: row0 the tile's first row
 
-  // Tile i of 128-row group i / 4 (kTiled: its lines 8 (i % 4) ..., else its rows 32 (i % 4) ...).
+  // kTiled: tile i of a 128-row group holds lines 8 (i % 4) ... of its words 0 .. 3
+  // (16 rows: 0, 1, then 2, 3).
   static __device__ __forceinline__ int64_t first_row(int64_t tile, bool tiled) {
-    return (tile >> 2) * 128 + (tile & 3) * (tiled ? 8 : 32);
+    if (!tiled) return tile * kRows;
+    if (kRows == 32) return (tile >> 2) * 128 + (tile & 3) * 8;
+    return (tile >> 3) * 128 + ((tile >> 2) & 1) * 64 + (tile & 3) * 8;
   }
 
   __device__ __forceinline__ void fill(const MvParams &p, uint32_t payload, uint32_t words,
@@ -167,13 +173,13 @@ struct Loader {
     constexpr int kPer = kStep / BLOCK;  // scale bytes of a row and step
     if (lane == 0) {
       // full boxes count, whatever part of them lies outside
-      const uint32_t sbytes = p.words > kBoxed ? 0 : tiled ? 32 * kPer : 512;
+      const uint32_t sbytes = p.words > kBoxed ? 0 : tiled ? 32 * kPer : kRows * 16;
       const uint32_t bytes = (TMA ? kPayload : 0) + sbytes;
       if (bytes) tc::mbar_expect_tx(bar, bytes);
       if (TMA) {
         if (tiled) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < kGroups; ++i)
             tc::tma_load_2d(payload + 1024 * i, &p.map, bar, step * (kStep / 2), row0 + 32 * i);
         } else {
           tc::tma_load_2d(payload, &p.map, bar, step * (kStep / 2), row0);
@@ -201,7 +207,7 @@ struct Loader {
       const int g = lane >> 2, t = lane & 3;
       const int blocks = (int)(j.K / BLOCK), first = step * kPer + (BLOCK == 16 ? 4 * t : 2 * (t & 2));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kGroups; ++i) {
         const int64_t n = (int64_t)row0 + g + 8 * i;
         const bool on = n < j.N && first < blocks;
         const uint8_t *from = j.sf + (on ? n * blocks + first : 0);
@@ -329,9 +335,10 @@ __device__ void prepare_x(const MatvecJob &j, int64_t m0, int M, int s0, int n, 
 }
 
 template <int KIND, int BLOCK, bool TMA, typename TX, int NT>
-__global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_constant__ MvParams p) {
+__global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_constant__ MvParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int kCols = 8 * NT;
+  constexpr int kCols = 8 * NT, kRows = rows_of(NT), kPayload = payload_of(NT);
+  constexpr int kPairs = kRows / 16, kGroups = kRows / 8;  // MMA row tiles; rows of a lane
   const int kWarps = p.warps, kThreads = 32 * p.warps;
   const MatvecJob &j = p.j;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
   int64_t ld_tile = tile0;
   int ld_left = ns, ld_slot = 0;
   const bool tiled = p.words == kTiled;
-  Loader<BLOCK, TMA> ld;
+  Loader<BLOCK, TMA, kRows> ld;
   ld.step = s0;
   ld.row0 = (int)ld.first_row(tile0, tiled);
   auto issue = [&] {
@@ -400,7 +407,8 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
   uint32_t phase = 0;
   bool live = true;  // false once a wait ran out: no more loads, results void
   for (int r = 0; r < p.rounds; ++r) {
-    float acc[NT][2][4] = {};
+    float acc[NT][kPairs][4] = {};
+    const int half = kRows == 16 ? (int)((tile0 + r * hop) >> 2 & 1) * 8 : 0;  // kTiled: words 0, 1 or 2, 3
     int xo = (s0 - c0) * 512;
     const float *sxl = sx + (s0 - c0) * kCols + 2 * t;
     for (int st = s0; st < (r < mine && live ? s0 + ns : s0); ++st) {
@@ -408,21 +416,27 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
         live = false;
         break;
       }
-      uint32_t codes[4];
+      uint32_t codes[kGroups];
       const uint8_t *wl = word_ring + slot * kWords;
       if (tiled) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(wl + (BLOCK == 16 ? t : t >> 1) * 128 + g * 16);
-        codes[0] = v.x, codes[1] = v.y, codes[2] = v.z, codes[3] = v.w;
+        const uint8_t *at = wl + (BLOCK == 16 ? t : t >> 1) * 128 + g * 16;
+        if (kRows == 32) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(at);
+          codes[0] = v.x, codes[1] = v.y, codes[kGroups - 2] = v.z, codes[kGroups - 1] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2 *>(at + half);
+          codes[0] = v.x, codes[1] = v.y;
+        }
       } else {
         // with 32-element blocks a box holds two steps' words
         const int o = BLOCK == 32 && p.words == kBoxed ? (4 * g + (t >> 1) + 2 * (st & 1)) * 4 : lane * 4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) codes[i] = *reinterpret_cast<const uint32_t *>(wl + 128 * i + o);
+        for (int i = 0; i < kGroups; ++i) codes[i] = *reinterpret_cast<const uint32_t *>(wl + 128 * i + o);
       }
-      float f[4];
-      int top[4] = {0, 0, 0, 0};
+      float f[kGroups];
+      int top[kGroups] = {};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kGroups; ++i) {
         if (BLOCK == 32 && (t & 1)) codes[i] >>= 16;  // the lane's half of the word
         if (KIND == kMXFP4) {
           top[i] = max((int)(codes[i] & 255u), (int)((codes[i] >> 8) & 255u));
@@ -431,20 +445,20 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
           f[i] = pow2(top[i] - 140);  // 2^(top - 127) / 2^13
         }
       }
-      float d[NT][2][4] = {};
+      float d[NT][kPairs][4] = {};
       const uint8_t *ra = ring + slot * kPayload + g * 128 + at0;
       // 32 of the lane's 64 columns at a time, a 16-byte piece of each row.
       // Not unrolled: at twice the size the loop outgrows the instruction
       // cache (8 tokens, 131072 x 4096: 65 us).
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        uint4 w[4];
-        uint32_t sc[4];
+        uint4 w[kGroups];
+        uint32_t sc[kGroups];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(ra + 1024 * i);
+        for (int i = 0; i < kGroups; ++i) w[i] = *reinterpret_cast<const uint4 *>(ra + 1024 * i);
         ra = ring + slot * kPayload + g * 128 + (at0 ^ 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kGroups; ++i) {
           sc[i] = scale_pair<KIND, BLOCK>(codes[i], top[i]);
           codes[i] >>= BLOCK == 16 ? 16 : 8;
         }
@@ -464,7 +478,7 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
           for (int c = 0; c < NT; ++c)
             v[c] = *reinterpret_cast<const uint4 *>(xl[c] + xo + q * 64);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < kPairs; ++u) {
             uint32_t a[4], b[4];
             const uint4 &wa = w[2 * u], &wb = w[2 * u + 1];
             decode8(q == 0 ? wa.x : q == 1 ? wa.y : q == 2 ? wa.z : wa.w, a);
@@ -487,7 +501,7 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
       for (int c = 0; c < NT; ++c) {
         const float2 fx = *reinterpret_cast<const float2 *>(sxl + 8 * c);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < kPairs; ++u)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float x = e & 1 ? fx.y : fx.x;
@@ -514,15 +528,17 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
 #pragma unroll
       for (int c = 0; c < NT; ++c)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < kPairs; ++u)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             o[(8 * c + 2 * t + (e & 1)) * kRows + g + 16 * u + 8 * (e >> 1)] = acc[c][u][e];
     }
-    // A warp writes 32 rows of a tile for one token at a time, a row a lane;
-    // (tile, token) pairs go around the warps of the cluster.  What a row is
-    // multiplied by is requested before the wait.
-    const int outs = alone ? M : group * M, hops = alone ? 1 : kWarps * S;
+    // A warp writes the rows of a tile for one token (16 rows: two) at a time,
+    // a row a lane; (tile, tokens) go around the warps of the cluster.  What a
+    // row is multiplied by is requested before the wait.
+    constexpr int kTokens = 32 / kRows;
+    const int row = lane % kRows, turns = (M + kTokens - 1) / kTokens;
+    const int outs = alone ? turns : group * turns, hops = alone ? 1 : kWarps * S;
     int shift = 0, tg = -1;
     float sd = 0.0f;
     int64_t n = j.N;
@@ -530,23 +546,23 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
       if (to == tg) return;
       tg = to;
       const int64_t tile = (r * (int64_t)p.clusters + cluster) * group + tg;
-      n = ld.first_row(tile, tiled) + (tiled ? 32 * (lane >> 3) + (lane & 7) : lane);
+      n = ld.first_row(tile, tiled) + (tiled ? 32 * (row >> 3) + (row & 7) : row);
       if (n >= j.N) return;
       shift = (KIND == kUE5M3 ? 3 : 0) + (j.shift ? j.shift[n] : 0);
       sd = j.sd[j.stripes ? n >> 7 : 0];
     };
     int i = alone ? 0 : warp * S + rank;
-    if (i < outs) row_of(alone ? tw : i / M);
+    if (i < outs) row_of(alone ? tw : i / turns);
     sync();
 #pragma unroll 1
     for (; i < outs; i += hops) {
-      row_of(alone ? tw : i / M);
-      if (n >= j.N) continue;
-      const int m = alone ? i : i - tg * M;
+      row_of(alone ? tw : i / turns);
+      const int m = (alone ? i : i - tg * turns) * kTokens + lane / kRows;
+      if (n >= j.N || m >= M) continue;
       float v = 0.0f;
       for (int q = 0; q < S; ++q) {
         const float *from = S > 1 ? cg::this_cluster().map_shared_rank(parts, q) : parts;
-        from += (tg * sk * kCols + m) * kRows + lane;
+        from += (tg * sk * kCols + m) * kRows + row;
         for (int w = 0; w < sk; ++w) v += from[w * kCols * kRows];
       }
       v = v * pow2(shift >> 1) * pow2(shift - (shift >> 1)) * sd;  // the exponent in two steps: no overflow between
@@ -574,8 +590,8 @@ __global__ void __launch_bounds__(32 * max_warps(NT), 1) k_matvec(const __grid_c
 // Shared memory for M tokens over ceil(steps / S) steps, NT column tiles.
 size_t smem_bytes(int M, int steps, int S, int nt, int warps, int depth) {
   const size_t span = (steps + S - 1) / S;
-  return (size_t)warps * depth * (kPayload + kWords) + warps * kMaxDepth * 8 + span * 8 * nt * 4 +
-         warps * kRows * 8 * nt * 4 + M * (span * 512 + 64) + 16;
+  return (size_t)warps * depth * (payload_of(nt) + kWords) + warps * kMaxDepth * 8 + span * 8 * nt * 4 +
+         warps * rows_of(nt) * 8 * nt * 4 + M * (span * 512 + 64) + 16;
 }
 
 // Bytes [z][y][x] without gaps as a tensor map (2-D for z = 0), boxes of
@@ -635,17 +651,17 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   MvParams p{};
   p.j = j;
   p.steps = (int)ceil_div(j.K, kStep);
-  p.tiles = (int)(4 * ceil_div(j.N, 128));
+  p.tiles = (int)(128 / rows_of(NT) * ceil_div(j.N, 128));
   p.mc = (int)(j.M < 8 * NT ? j.M : 8 * NT);
   const int64_t row_words = j.K / j.block;
   p.words = j.sf_mma ? kTiled : row_words % 16 == 0 ? kBoxed : row_words % 4 == 0 ? kPieces : kBytes;
   p.status = status_word();
   if (!p.status) return FP4_ERR_CUDA;
   const bool tiled = p.words == kTiled;
-  if (TMA && !byte_map(&p.map, j.q, j.K / 2, j.N, 0, kStep / 2, tiled ? 8 : kRows, true)) return FP4_ERR_CUDA;
+  if (TMA && !byte_map(&p.map, j.q, j.K / 2, j.N, 0, kStep / 2, tiled ? 8 : rows_of(NT), true)) return FP4_ERR_CUDA;
   if (tiled && !byte_map(&p.smap, j.sf, 512, ceil_div(row_words, 4), ceil_div(j.N, 128), 128, kStep / BLOCK / 4, false))
     return FP4_ERR_CUDA;
-  if (p.words == kBoxed && !byte_map(&p.smap, j.sf, row_words, j.N, 0, 16, kRows, false)) return FP4_ERR_CUDA;
+  if (p.words == kBoxed && !byte_map(&p.smap, j.sf, row_words, j.N, 0, 16, rows_of(NT), false)) return FP4_ERR_CUDA;
   // x of a CTA's tokens over its part of K beside the rings: more CTAs per
   // tile until 12 warps fit (measured, 8 tokens, 4096 x 14336: 2 CTAs of 11
   // warps 21.5 us, 4 of 12 17.8; 16 tokens, 14336 x 4096: 1 CTA of 8 warps
@@ -657,12 +673,12 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   while (p.S < 8 && !fits(12, 2)) p.S *= 2;
   while (p.mc > 1 && !fits(8, 2)) p.mc = (p.mc + 1) / 2;
   if (!fits(8, 2)) return FP4_ERR_SHAPE;
-  p.warps = max_warps(NT);
+  p.warps = kMaxWarps;
   while (!fits(p.warps, 2)) --p.warps;
   p.depth = 2;
   while (p.depth < kMaxDepth && fits(p.warps, p.depth + 1)) ++p.depth;
   const size_t smem = smem_bytes(p.mc, p.steps, p.S, NT, p.warps, p.depth);
-  const int room = resident(kern, residence, p.S, 32 * max_warps(NT));
+  const int room = resident(kern, residence, p.S, 32 * kMaxWarps);
   if (room < 1) return FP4_ERR_CUDA;
   // warps per tile: the fewest steps on the busiest warp; a round costs about
   // one step more for its join, so ties go to fewer and longer ones
