@@ -76,6 +76,7 @@ struct MvParams {
   int mc;            // tokens a CTA takes (blockIdx.y counts them off)
   int depth;         // stages of a warp's ring
   int words;         // how scales reach shared memory: Words
+  int tma;           // payload by TMA: rows of whole 16 bytes
   uint32_t *status;
 };
 
@@ -151,9 +152,12 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 //   kPieces, kBytes: plain rows of any other pitch, the same place, by 4-byte
 //     cp.async or byte loads.
 enum Words { kTiled = 0, kBoxed = 1, kPieces = 2, kBytes = 3 };
+// A kernel's MODE is kTiled or kBoxed with the payload by TMA, or kAny: what
+// the parameters say.
+constexpr int kAny = 2;
 
 // Fills a warp's stages one after the other.
-template <int BLOCK, bool TMA, int kRows>
+template <int BLOCK, int MODE, int kRows>
 struct Loader {
   static constexpr int kPayload = kRows * kStep / 2, kGroups = kRows / 8;
   int step, row0;        // of the next stage: row0 the tile's first row
@@ -169,14 +173,14 @@ struct Loader {
   __device__ __forceinline__ void fill(const MvParams &p, uint32_t payload, uint32_t words,
                                        uint32_t bar, int lane) {
     const MatvecJob &j = p.j;
-    const bool tiled = p.words == kTiled;
+    const int mode = MODE == kAny ? p.words : MODE;
+    const bool tiled = mode == kTiled, tma = MODE != kAny || p.tma;
     constexpr int kPer = kStep / BLOCK;  // scale bytes of a row and step
     if (lane == 0) {
       // full boxes count, whatever part of them lies outside
-      const uint32_t sbytes = p.words > kBoxed ? 0 : tiled ? 32 * kPer : kRows * 16;
-      const uint32_t bytes = (TMA ? kPayload : 0) + sbytes;
-      if (bytes) tc::mbar_expect_tx(bar, bytes);
-      if (TMA) {
+      const uint32_t bytes = (tma ? kPayload : 0) + (mode > kBoxed ? 0 : tiled ? 32 * kPer : kRows * 16);
+      if (MODE != kAny || bytes) tc::mbar_expect_tx(bar, bytes);
+      if (tma) {
         if (tiled) {
 #pragma unroll
           for (int i = 0; i < kGroups; ++i)
@@ -187,12 +191,14 @@ struct Loader {
       }
       if (tiled)
         tma_load_3d(words, &p.smap, bar, (row0 & 31) * 16, step * (kPer / 4), row0 >> 7);
-      else if (p.words == kBoxed)
+      else if (mode == kBoxed)
         tc::tma_load_2d(words, &p.smap, bar, step * kPer & ~15, row0);
     }
-    if (!TMA) {
+    ++step;
+    if (MODE != kAny) return;
+    if (!tma) {
       // 16 pieces of 8 bytes a row; lane: piece lane % 16 of every other row
-      const int64_t at = (int64_t)step * (kStep / 2) + (lane & 15) * 8;
+      const int64_t at = (int64_t)(step - 1) * (kStep / 2) + (lane & 15) * 8;
 #pragma unroll 4
       for (int i = 0; i < kRows / 2; ++i) {
         const int r = 2 * i + (lane >> 4);
@@ -203,16 +209,16 @@ struct Loader {
                   j.q + (on ? n * (j.K / 2) + at : 0), on);
       }
     }
-    if (p.words > kBoxed) {
+    if (mode > kBoxed) {
       const int g = lane >> 2, t = lane & 3;
-      const int blocks = (int)(j.K / BLOCK), first = step * kPer + (BLOCK == 16 ? 4 * t : 2 * (t & 2));
+      const int blocks = (int)(j.K / BLOCK), first = (step - 1) * kPer + (BLOCK == 16 ? 4 * t : 2 * (t & 2));
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) {
         const int64_t n = (int64_t)row0 + g + 8 * i;
         const bool on = n < j.N && first < blocks;
         const uint8_t *from = j.sf + (on ? n * blocks + first : 0);
         const uint32_t dst = words + 128 * i + 4 * lane;
-        if (p.words == kPieces) {
+        if (mode == kPieces) {
           cp_async4(dst, from, on);
         } else {
           uint32_t w = 0;
@@ -223,8 +229,7 @@ struct Loader {
         }
       }
     }
-    if (!TMA || p.words > kBoxed) cp_async_arrive(bar);
-    ++step;
+    if (!tma || mode > kBoxed) cp_async_arrive(bar);
   }
 };
 
@@ -334,7 +339,7 @@ __device__ void prepare_x(const MatvecJob &j, int64_t m0, int M, int s0, int n, 
   }
 }
 
-template <int KIND, int BLOCK, bool TMA, typename TX, int NT>
+template <int KIND, int BLOCK, int MODE, typename TX, int NT>
 __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_constant__ MvParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int kCols = 8 * NT, kRows = rows_of(NT), kPayload = payload_of(NT);
@@ -364,7 +369,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
 
   // the warp's own ring: one arrival that expects the boxes, and 32 lanes' for
   // their own copies, as the stage has either or both
-  const bool boxes = TMA || p.words <= kBoxed, copies = !TMA || p.words > kBoxed;
+  const bool boxes = MODE != kAny || p.tma || p.words <= kBoxed, copies = MODE == kAny && (!p.tma || p.words > kBoxed);
   if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
     for (int d = 0; d < depth; ++d) tc::mbar_init(bars_a + 8 * d, (boxes ? 1 : 0) + (copies ? 32 : 0));
@@ -374,26 +379,22 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
   __syncwarp();
   const int64_t tile0 = (int64_t)cluster * group + tw, hop = (int64_t)p.clusters * group;
   const int mine = tw < group && tile0 < p.tiles ? (int)((p.tiles - 1 - tile0) / hop) + 1 : 0;  // the warp's tiles
-  int ahead = mine * ns, flying = 0;  // stages to request, requested and not read
+  int ahead = mine * ns;  // stages still to be requested
   int64_t ld_tile = tile0;
-  int ld_left = ns, ld_slot = 0;
-  const bool tiled = p.words == kTiled;
-  Loader<BLOCK, TMA, kRows> ld;
+  const bool tiled = MODE == kAny ? p.words == kTiled : MODE == kTiled;
+  Loader<BLOCK, MODE, kRows> ld;
   ld.step = s0;
   ld.row0 = (int)ld.first_row(tile0, tiled);
-  auto issue = [&] {
-    ld.fill(p, ring_a + ld_slot * kPayload, words_a + ld_slot * kWords, bars_a + 8 * ld_slot, lane);
+  auto issue = [&](int at) {
+    ld.fill(p, ring_a + at * kPayload, words_a + at * kWords, bars_a + 8 * at, lane);
     --ahead;
-    ++flying;
-    if (++ld_slot == depth) ld_slot = 0;
-    if (--ld_left == 0) {
-      ld_left = ns;
-      ld_tile += hop;
+    if (ld.step == s0 + ns) {
       ld.step = s0;
+      ld_tile += hop;
       ld.row0 = (int)ld.first_row(ld_tile, tiled);
     }
   };
-  for (int d = 0; d < depth && ahead; ++d) issue();
+  for (int d = 0; d < depth && ahead; ++d) issue(d);
 
   prepare_x<TX>(j, m0, M, c0, n, xs, pitch, sx, kCols, p.warps);
   __syncthreads();
@@ -406,6 +407,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
   int slot = 0;
   uint32_t phase = 0;
   bool live = true;  // false once a wait ran out: no more loads, results void
+  int flying = 0;    // stages in flight when it did
   for (int r = 0; r < p.rounds; ++r) {
     float acc[NT][kPairs][4] = {};
     const int half = kRows == 16 ? (int)((tile0 + r * hop) >> 2 & 1) * 8 : 0;  // kTiled: words 0, 1 or 2, 3
@@ -414,6 +416,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
     for (int st = s0; st < (r < mine && live ? s0 + ns : s0); ++st) {
       if (!__all_sync(~0u, tc::mbar_wait_inl(bars_a + 8 * slot, phase, abort_flag, p.status))) {
         live = false;
+        flying = min(depth, (mine - r - 1) * ns + s0 + ns - st);
         break;
       }
       uint32_t codes[kGroups];
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
         }
       } else {
         // with 32-element blocks a box holds two steps' words
-        const int o = BLOCK == 32 && p.words == kBoxed ? (4 * g + (t >> 1) + 2 * (st & 1)) * 4 : lane * 4;
+        const int o = BLOCK == 32 && (MODE == kBoxed || (MODE == kAny && p.words == kBoxed)) ? (4 * g + (t >> 1) + 2 * (st & 1)) * 4 : lane * 4;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) codes[i] = *reinterpret_cast<const uint32_t *>(wl + 128 * i + o);
       }
@@ -463,13 +466,12 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
           codes[i] >>= BLOCK == 16 ? 16 : 8;
         }
         if (h) {
-          --flying;
+          __syncwarp();  // every lane has read the stage: it is filled again meanwhile
+          if (ahead) issue(slot);
           if (++slot == depth) {
             slot = 0;
             phase ^= 1;
           }
-          __syncwarp();  // every lane has read the stage: it is filled again meanwhile
-          if (ahead) issue();
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -538,41 +540,47 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
     // row is multiplied by is requested before the wait.
     constexpr int kTokens = 32 / kRows;
     const int row = lane % kRows, turns = (M + kTokens - 1) / kTokens;
-    const int outs = alone ? turns : group * turns, hops = alone ? 1 : kWarps * S;
-    int shift = 0, tg = -1;
+    const int size = j.y_type == FP4_F32 ? 4 : 2;
+    int shift = 0;
     float sd = 0.0f;
     int64_t n = j.N;
     auto row_of = [&](int to) {
-      if (to == tg) return;
-      tg = to;
-      const int64_t tile = (r * (int64_t)p.clusters + cluster) * group + tg;
+      const int64_t tile = (r * (int64_t)p.clusters + cluster) * group + to;
       n = ld.first_row(tile, tiled) + (tiled ? 32 * (row >> 3) + (row & 7) : row);
       if (n >= j.N) return;
       shift = (KIND == kUE5M3 ? 3 : 0) + (j.shift ? j.shift[n] : 0);
       sd = j.sd[j.stripes ? n >> 7 : 0];
     };
-    int i = alone ? 0 : warp * S + rank;
-    if (i < outs) row_of(alone ? tw : i / turns);
+    const int outs = alone ? turns : group * turns, hops = alone ? 1 : kWarps * S;
+    int i = alone ? 0 : warp * S + rank, tg = alone ? tw : i / turns;
+    if (i < outs) row_of(tg);
     sync();
 #pragma unroll 1
-    for (; i < outs; i += hops) {
-      row_of(alone ? tw : i / turns);
+    while (i < outs) {
       const int m = (alone ? i : i - tg * turns) * kTokens + lane / kRows;
-      if (n >= j.N || m >= M) continue;
-      float v = 0.0f;
-      for (int q = 0; q < S; ++q) {
-        const float *from = S > 1 ? cg::this_cluster().map_shared_rank(parts, q) : parts;
-        from += (tg * sk * kCols + m) * kRows + row;
-        for (int w = 0; w < sk; ++w) v += from[w * kCols * kRows];
+      if (n < j.N && m < M) {
+        float v = 0.0f;
+        for (int q = 0; q < S; ++q) {
+          const float *from = S > 1 ? cg::this_cluster().map_shared_rank(parts, q) : parts;
+          from += (tg * sk * kCols + m) * kRows + row;
+          for (int w = 0; w < sk; ++w) v += from[w * kCols * kRows];
+        }
+        // the exponent in two steps: no overflow between
+        v = v * pow2(shift >> 1) * pow2(shift - (shift >> 1)) * sd;
+        uint8_t *to = static_cast<uint8_t *>(j.y) + ((m0 + m) * j.ys + n) * size;
+        if (j.y_type == FP4_F32)
+          *reinterpret_cast<float *>(to) = v;
+        else if (j.y_type == FP4_BF16)
+          *reinterpret_cast<__nv_bfloat16 *>(to) = __float2bfloat16_rn(v);
+        else
+          *reinterpret_cast<__half *>(to) = __float2half_rn(v);
       }
-      v = v * pow2(shift >> 1) * pow2(shift - (shift >> 1)) * sd;  // the exponent in two steps: no overflow between
-      const int64_t at = (m0 + m) * j.ys + n;
-      if (j.y_type == FP4_F32)
-        static_cast<float *>(j.y)[at] = v;
-      else if (j.y_type == FP4_BF16)
-        static_cast<__nv_bfloat16 *>(j.y)[at] = __float2bfloat16_rn(v);
-      else
-        static_cast<__half *>(j.y)[at] = __float2half_rn(v);
+      i += hops;
+      if (!alone && i < outs) {
+        const int next = i / turns;
+        if (next != tg) row_of(next);
+        tg = next;
+      }
     }
   }
   if (!live) {  // copies still in flight land (bounded) before the ring goes away
@@ -644,10 +652,10 @@ int resident(Kern kern, Residence *per_device, int S, int kThreads) {
   return n;
 }
 
-template <int KIND, int BLOCK, bool TMA, typename TX, int NT>
+template <int KIND, int BLOCK, int MODE, typename TX, int NT>
 fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   static Residence residence[64];
-  auto kern = k_matvec<KIND, BLOCK, TMA, TX, NT>;
+  auto kern = k_matvec<KIND, BLOCK, MODE, TX, NT>;
   MvParams p{};
   p.j = j;
   p.steps = (int)ceil_div(j.K, kStep);
@@ -658,7 +666,8 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   p.status = status_word();
   if (!p.status) return FP4_ERR_CUDA;
   const bool tiled = p.words == kTiled;
-  if (TMA && !byte_map(&p.map, j.q, j.K / 2, j.N, 0, kStep / 2, tiled ? 8 : rows_of(NT), true)) return FP4_ERR_CUDA;
+  p.tma = j.K % 32 == 0;
+  if (p.tma && !byte_map(&p.map, j.q, j.K / 2, j.N, 0, kStep / 2, tiled ? 8 : rows_of(NT), true)) return FP4_ERR_CUDA;
   if (tiled && !byte_map(&p.smap, j.sf, 512, ceil_div(row_words, 4), ceil_div(j.N, 128), 128, kStep / BLOCK / 4, false))
     return FP4_ERR_CUDA;
   if (p.words == kBoxed && !byte_map(&p.smap, j.sf, row_words, j.N, 0, 16, rows_of(NT), false)) return FP4_ERR_CUDA;
@@ -715,25 +724,28 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   return FP4_OK;
 }
 
-template <int KIND, int BLOCK, bool TMA, typename TX>
+template <int KIND, int BLOCK, int MODE, typename TX>
 fp4_status launch_nt(const MatvecJob &j, cudaStream_t s) {
-  return j.M <= 8 ? launch<KIND, BLOCK, TMA, TX, 1>(j, s) : launch<KIND, BLOCK, TMA, TX, 2>(j, s);
+  return j.M <= 8 ? launch<KIND, BLOCK, MODE, TX, 1>(j, s) : launch<KIND, BLOCK, MODE, TX, 2>(j, s);
 }
 
-// Rows of K / 2 bytes are a TMA stride when K is a multiple of 32, as it is
-// with 32-element blocks.
-template <int KIND, typename TX>
-fp4_status launch_k(const MatvecJob &j, cudaStream_t s) {
-  if (j.K % 32 != 0) return launch_nt<KIND, 16, false, TX>(j, s);
-  return j.block == 16 ? launch_nt<KIND, 16, true, TX>(j, s) : launch_nt<KIND, 32, true, TX>(j, s);
+// Rows of K / 2 payload bytes and of K / BLOCK scales that are TMA strides,
+// or the tensor-core layout, have kernels of their own.
+template <int KIND, int BLOCK, typename TX>
+fp4_status launch_mode(const MatvecJob &j, cudaStream_t s) {
+  if (j.K % 32 == 0) {
+    if (j.sf_mma) return launch_nt<KIND, BLOCK, kTiled, TX>(j, s);
+    if (j.K % (16 * BLOCK) == 0) return launch_nt<KIND, BLOCK, kBoxed, TX>(j, s);
+  }
+  return launch_nt<KIND, BLOCK, kAny, TX>(j, s);
 }
 
 template <typename TX>
 fp4_status launch_x(const MatvecJob &j, cudaStream_t s) {
   switch (j.kind) {
-    case kMXFP4: return launch_nt<kMXFP4, 32, true, TX>(j, s);
-    case kNVFP4: return j.K % 32 != 0 ? launch_nt<kNVFP4, 16, false, TX>(j, s) : launch_nt<kNVFP4, 16, true, TX>(j, s);
-    default: return launch_k<kUE5M3, TX>(j, s);
+    case kMXFP4: return launch_mode<kMXFP4, 32, TX>(j, s);
+    case kNVFP4: return launch_mode<kNVFP4, 16, TX>(j, s);
+    default: return j.block == 16 ? launch_mode<kUE5M3, 16, TX>(j, s) : launch_mode<kUE5M3, 32, TX>(j, s);
   }
 }
 
