@@ -293,7 +293,7 @@ __device__ __forceinline__ int normalize(uint32_t *w) {
 
 // x[0 .. M) over steps [s0, s0 + n) as f16 into shared memory, and the power
 // of two taken out of each (token, step); a warp per (token, step), eight
-// elements a lane, the loads of eight tokens requested together.
+// elements a lane, eight (tokens, or steps of few tokens) requested together.
 template <typename TX>
 __device__ void prepare_x(const MatvecJob &j, int64_t m0, int M, int s0, int n, uint8_t *xs, int pitch,
                           float *sx, int cols, int warps) {
@@ -303,16 +303,18 @@ __device__ void prepare_x(const MatvecJob &j, int64_t m0, int M, int s0, int n, 
   const int across = min(warps, n), deep = warps / across;  // warps along K, and along the tokens
   if (warp >= across * deep) return;
   constexpr int kBatch = 8;
-  for (int c = warp % across; c < n; c += across) {
-    const int k = (s0 + c) * kStep + piece * 8;
-    const bool in = k < (int)j.K;  // K is a multiple of 16: a piece is inside or outside
-    for (int m = warp / across; m < M; m += kBatch * deep) {
+  const bool few = M < kBatch * deep;
+  const int dm = few ? 0 : deep, dc = few ? across : 0;  // from one of a batch to the next
+  for (int c = warp % across; c < n; c += few ? kBatch * across : across) {
+    for (int m = warp / across; m < M; m += few ? deep : kBatch * deep) {
+      int k = (s0 + c) * kStep + piece * 8;
       const TX *from = x + m * j.xs + k;
       uint32_t w[kBatch][4];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0;
-        if (in && m + i * deep < M) {
+        // K is a multiple of 16: a piece is inside or outside
+        if (m + i * dm < M && c + i * dc < n && k < (int)j.K) {
           if (vec) {
             const uint4 v = __ldg(reinterpret_cast<const uint4 *>(from));
             w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
@@ -322,18 +324,19 @@ __device__ void prepare_x(const MatvecJob &j, int64_t m0, int M, int s0, int n, 
             for (int q = 0; q < 4; ++q) w[i][q] = e[2 * q] | ((uint32_t)e[2 * q + 1] << 16);
           }
         }
-        from += deep * j.xs;
+        from += dm * j.xs + dc * kStep;
+        k += dc * kStep;
       }
       // piece q of lane t (piece = 8 t + q) lies at 64 q + 16 t
       uint8_t *to = xs + m * pitch + c * 512 + (piece & 7) * 64 + (piece >> 3) * 16;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        if (m + i * deep >= M) break;
+        if (m + i * dm >= M || c + i * dc >= n) break;
         int ex = 0;
         if (Is<TX>::bf16) ex = normalize(w[i]);
         *reinterpret_cast<uint4 *>(to) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
-        to += deep * pitch;
-        if (piece == 0) sx[c * cols + m + i * deep] = pow2(ex);
+        to += dm * pitch + dc * 512;
+        if (piece == 0) sx[(c + i * dc) * cols + m + i * dm] = pow2(ex);
       }
     }
   }
@@ -671,37 +674,49 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   if (tiled && !byte_map(&p.smap, j.sf, 512, ceil_div(row_words, 4), ceil_div(j.N, 128), 128, kStep / BLOCK / 4, false))
     return FP4_ERR_CUDA;
   if (p.words == kBoxed && !byte_map(&p.smap, j.sf, row_words, j.N, 0, 16, rows_of(NT), false)) return FP4_ERR_CUDA;
-  // x of a CTA's tokens over its part of K beside the rings: more CTAs per
-  // tile until 12 warps fit (measured, 8 tokens, 4096 x 14336: 2 CTAs of 11
-  // warps 21.5 us, 4 of 12 17.8; 16 tokens, 14336 x 4096: 1 CTA of 8 warps
-  // 29.6 us, 2 of 12 20.1), then fewer warps, then fewer tokens
-  auto fits = [&](int warps, int depth) {
-    return smem_bytes(p.mc, p.steps, p.S, NT, warps, depth) <= (size_t)kMaxSmem;
+  // The split: of those that fit shared memory (x of a CTA's tokens over its
+  // part of K beside rings of two stages), the least estimated time, in steps
+  // of an SM: the steps of its warps, twice the longest warp's, the join (a
+  // store; a barrier with rings running dry; one over a cluster) and the
+  // preparation of x.  Measured with x 16 bits wide: 14336 x 4096, 8 tokens,
+  // S, sk = 1, 5: 15.2 us, 1, 4: 16.0, 2, 2: 15.9; 131072 x 4096, 16 tokens,
+  // 1, 1: 88.8, 2, 1: 99.8, 1, 4: 93.4; 4096 x 14336, 12 tokens, 4, 2: 18.8,
+  // 4, 4: 21.4, 8, 1: 25.3.  Tokens are halved until something fits.
+  int64_t best = INT64_MAX;
+  auto fits = [&](int S, int warps, int depth) {
+    return smem_bytes(p.mc, p.steps, S, NT, warps, depth) <= (size_t)kMaxSmem;
   };
-  p.S = 1;
-  while (p.S < 8 && !fits(12, 2)) p.S *= 2;
-  while (p.mc > 1 && !fits(8, 2)) p.mc = (p.mc + 1) / 2;
-  if (!fits(8, 2)) return FP4_ERR_SHAPE;
-  p.warps = kMaxWarps;
-  while (!fits(p.warps, 2)) --p.warps;
-  p.depth = 2;
-  while (p.depth < kMaxDepth && fits(p.warps, p.depth + 1)) ++p.depth;
-  const size_t smem = smem_bytes(p.mc, p.steps, p.S, NT, p.warps, p.depth);
-  const int room = resident(kern, residence, p.S, 32 * kMaxWarps);
-  if (room < 1) return FP4_ERR_CUDA;
-  // warps per tile: the fewest steps on the busiest warp; a round costs about
-  // one step more for its join, so ties go to fewer and longer ones
-  int64_t cost = INT64_MAX;
-  for (int sk = 1; sk <= p.warps && (sk == 1 || p.S * sk <= p.steps); ++sk) {
-    const int group = p.warps / sk;
-    const int64_t rounds = ceil_div(p.tiles, (int64_t)room * group);
-    const int64_t c = rounds * (ceil_div(p.steps, (int64_t)p.S * sk) + 1);
-    if (c >= cost) continue;
-    cost = c;
-    p.sk = sk;
-    p.rounds = (int)rounds;
-    p.clusters = (int)ceil_div(p.tiles, rounds * group);
+  while (best == INT64_MAX) {
+    for (int S = 1; S <= 8 && S <= p.steps; S *= 2) {
+      int warps = kMaxWarps;
+      while (warps >= 8 && !fits(S, warps, 2)) warps -= 2;
+      if (warps < 8) continue;
+      const int room = resident(kern, residence, S, 32 * kMaxWarps);
+      if (room < 1) return FP4_ERR_CUDA;
+      const int64_t span = ceil_div(p.steps, S);
+      for (int sk = 1; sk <= warps && sk <= span; ++sk) {
+        const int group = warps / sk;
+        if (sk > 1 && sk < warps && sk < span && warps / (sk + 1) == group) continue;  // a larger one keeps as many tiles
+        const int64_t rounds = ceil_div(p.tiles, (int64_t)room * group);
+        const int join = sk > 1 ? 12 : 1;
+        const int64_t cost = rounds * (group * span + 2 * ceil_div(span, sk) + join + (S > 1 ? 40 : 0)) + p.mc * span / 8;
+        if (cost >= best) continue;
+        best = cost;
+        p.S = S;
+        p.sk = sk;
+        p.warps = warps;
+        p.rounds = (int)rounds;
+        p.clusters = (int)ceil_div(p.tiles, rounds * group);
+      }
+      if (warps == kMaxWarps && S > 1) break;  // more CTAs per tile only add joins
+    }
+    if (best < INT64_MAX) break;
+    if (p.mc == 1) return FP4_ERR_SHAPE;
+    p.mc = (p.mc + 1) / 2;
   }
+  p.depth = 2;
+  while (p.depth < kMaxDepth && fits(p.S, p.warps, p.depth + 1)) ++p.depth;
+  const size_t smem = smem_bytes(p.mc, p.steps, p.S, NT, p.warps, p.depth);
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(32 * p.warps);
   cfg.dynamicSmemBytes = smem;
