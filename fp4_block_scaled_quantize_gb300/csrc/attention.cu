@@ -53,7 +53,7 @@ struct AtParams {
   int tile;     // positions of a tile: 16 per unit and warp
   int ctas;     // CTAs of the main kernel
   int direct;   // each takes one row, whole
-  int shift;    // log2 page_size, or -1: pages of any size
+  int shift;    // log2 page_size, or -1: no power of two
   int out16;    // rows of out allow 16-byte stores
   float scale2; // scale * log2 e
   float *ws;    // [ctas][2] partial rows
@@ -255,7 +255,7 @@ __device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d
     a.p.lse[(int64_t)s * a.p.heads + head] = any ? (base + log2f(sum)) * 0.693147180559945f : -INFINITY;
 }
 
-template <typename T, int DP, int NT, bool POW2>
+template <typename T, int DP, int NT, bool UNITS>
 __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
     k_attention(const __grid_constant__ AtParams a) {
   constexpr int kCols = 8 * NT, kKey = DP / 32, kVal = DP / 64, kUnits = units_of(DP, NT);
@@ -342,70 +342,96 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
     bool seen;
     const int32_t *table = c.table + s * c.table_stride;
     const int stop = min(sp.len, sp.base + kTile * tile1);
-    // The pages of the 16 positions from pos on: pages of 16 or more places
-    // hold them all on one (every lane has its number); else lane i & 15 has
-    // position i's.
+    // Where the 16 positions of a unit lie.  UNITS (pages of whole units):
+    // all on one page, the same for every lane.  Else lane i & 15 holds
+    // position i's offsets in keys and values.  Bit i of on: position i is
+    // seen and its page exists.
     struct Where {
-      int page, place;
+      int64_t k, v;
+      uint32_t on;
     };
-    auto lookup = [&](int pos) {
-      Where w;
-      w.page = -1, w.place = 0;
-      if (POW2) {
-        if (pos < stop) w.page = __ldg(table + (pos >> a.shift));
-        w.place = pos & (c.page_size - 1);
-      } else {
-        const int i = pos + (lane & 15);
-        if (i >= sp.from && i < stop) {
-          const int e = i / c.page_size;
-          w.page = __ldg(table + e);
-          w.place = i - e * c.page_size;
+    int page_next[kUnits];  // UNITS: page numbers a step ahead (their loads are not waited for)
+    auto ask = [&](int pos) {
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int first = pos + 16 * u;
+        page_next[u] = -1;
+        if (UNITS) {
+          if (first < stop) page_next[u] = __ldg(table + (a.shift >= 0 ? first >> a.shift : first / c.page_size));
+        } else {
+          const int i = first + (lane & 15);
+          if (i >= sp.from && i < stop) page_next[u] = __ldg(table + i / c.page_size);
         }
       }
-      return w;
     };
-    // Position i of the 16: true if it is seen and its page exists.
-    auto place_of = [&](const Where &w, int pos, int i, int64_t &page, int64_t &place) {
-      int pg = w.page, pl = w.place + i;
-      if (!POW2) {
-        pg = __shfl_sync(~0u, w.page, i);
-        pl = __shfl_sync(~0u, w.place, i);
-      }
-      page = pg;
-      place = pl;
-      return pos + i >= sp.from && pos + i < stop && pg >= 0 && pg < c.pages;
-    };
-    uint4 key[kUnits][2][kKey], val[kUnits][4][kVal];
-    bool key_on[kUnits][2], key_next[kUnits][2];
-    Where now[kUnits], next[kUnits];
-    auto lookups = [&](Where (&w)[kUnits], int pos) {
+    auto where = [&](Where (&w)[kUnits], int pos) {
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) w[u] = lookup(pos + 16 * u);
+      for (int u = 0; u < kUnits; ++u) {
+        const int first = pos + 16 * u;
+        const int page = page_next[u];
+        const bool ok = page >= 0 && page < c.pages;
+        if (UNITS) {
+          const int place = a.shift >= 0 ? first & (c.page_size - 1) : first % c.page_size;
+          w[u].k = (int64_t)page * c.k_page + (int64_t)place * c.k_place;
+          w[u].v = (int64_t)page * c.v_page + (int64_t)place * c.v_place;
+          w[u].on = 0xFFFFu;
+          if (first < sp.from) w[u].on &= 0xFFFFu << (sp.from - first);  // base <= from < base + 16
+          if (first + 16 > stop) w[u].on &= (1u << max(stop - first, 0)) - 1;
+          if (!ok) {
+            if (w[u].on && lane == 0) raise_status(a.status, kStatusIndex);
+            w[u].on = 0;
+          }
+        } else {
+          const int i = first + (lane & 15);
+          const bool in = i >= sp.from && i < stop;
+          if (in && !ok && lane < 16) raise_status(a.status, kStatusIndex);
+          const int place = i % c.page_size;
+          w[u].k = (int64_t)page * c.k_page + (int64_t)place * c.k_place;
+          w[u].v = (int64_t)page * c.v_page + (int64_t)place * c.v_place;
+          w[u].on = __ballot_sync(~0u, in && ok) & 0xFFFFu;
+        }
+      }
     };
-    auto load_keys = [&](const Where (&w)[kUnits], int pos) {
+    const bool exact = D == DP;  // no head element is padding
+    const T *const keys = static_cast<const T *>(c.k) + kvh * c.k_head + 8 * t;
+    const T *const values = static_cast<const T *>(c.v) + kvh * c.v_head + 8 * g;
+    uint4 key[kUnits][2][kKey], val[kUnits][4][kVal];
+    Where now[kUnits], next[kUnits];
+    // What is not seen is not read: zeros, which its zero weights then meet.
+    auto load_keys = [&](const Where (&w)[kUnits]) {
 #pragma unroll
       for (int u = 0; u < kUnits; ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          int64_t page, place;
-          const bool on = key_next[u][h] = place_of(w[u], pos + 16 * u, g + 8 * h, page, place);
-          const T *k = static_cast<const T *>(c.k) + page * c.k_page + place * c.k_place + kvh * c.k_head + 8 * t;
+          const int i = g + 8 * h;
+          const T *k = keys + (UNITS ? w[u].k + i * c.k_place : __shfl_sync(~0u, w[u].k, i));
+          if (exact && w[u].on == 0xFFFFu) {
 #pragma unroll
-          for (int i = 0; i < kKey; ++i)
-            key[u][h][i] = on && 32 * i + 8 * t < D ? load16(k + 32 * i) : make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < kKey; ++e) key[u][h][e] = load16(k + 32 * e);
+          } else {
+            const bool on = w[u].on >> i & 1;
+#pragma unroll
+            for (int e = 0; e < kKey; ++e)
+              key[u][h][e] = on && 32 * e + 8 * t < D ? load16(k + 32 * e) : make_uint4(0, 0, 0, 0);
+          }
         }
     };
-    auto load_values = [&](const Where (&w)[kUnits], int pos) {
+    auto load_values = [&](const Where (&w)[kUnits]) {
 #pragma unroll
       for (int u = 0; u < kUnits; ++u)
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          int64_t page, place;
-          const bool on = place_of(w[u], pos + 16 * u, 2 * t + (h & 1) + 8 * (h >> 1), page, place);
-          const T *v = static_cast<const T *>(c.v) + page * c.v_page + place * c.v_place + kvh * c.v_head + 8 * g;
+          const int i = 2 * t + (h & 1) + 8 * (h >> 1);
+          const T *v = values + (UNITS ? w[u].v + i * c.v_place : __shfl_sync(~0u, w[u].v, i));
+          if (exact && w[u].on == 0xFFFFu) {
 #pragma unroll
-          for (int i = 0; i < kVal; ++i)  // what is not seen is not read: zero weights times zeros
-            val[u][h][i] = on && 64 * i + 8 * g < D ? load16(v + 64 * i) : make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < kVal; ++e) val[u][h][e] = load16(v + 64 * e);
+          } else {
+            const bool on = w[u].on >> i & 1;
+#pragma unroll
+            for (int e = 0; e < kVal; ++e)
+              val[u][h][e] = on && 64 * e + 8 * g < D ? load16(v + 64 * e) : make_uint4(0, 0, 0, 0);
+          }
         }
     };
 
@@ -423,20 +449,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
         for (int j = 0; j < 4; ++j) o[n][i][j][0] = o[n][i][j][1] = o[n][i][j][2] = o[n][i][j][3] = 0.0f;
     }
     int pos = sp.base + kTile * tile0 + 16 * kUnits * warp;
-    lookups(now, pos);
-    lookups(next, pos + kTile);
-    load_keys(now, pos);
-    if (!kTurns) load_values(now, pos);
+    ask(pos);
+    where(now, pos);
+    ask(pos + kTile);
+    load_keys(now);
+    if (!kTurns) load_values(now);
     for (; pos < stop; pos += kTile) {
       float sc[kUnits][NT][4];
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        // a page that is not in the cache
-        const int first = pos + 16 * u;
-        if (POW2 ? lane == 0 && first < stop : lane < 16 && first + lane >= sp.from && first + lane < stop)
-          if (now[u].page < 0 || now[u].page >= c.pages) raise_status(a.status, kStatusIndex);
-        key_on[u][0] = key_next[u][0];
-        key_on[u][1] = key_next[u][1];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           sc[u][n][0] = sc[u][n][1] = sc[u][n][2] = sc[u][n][3] = 0.0f;
@@ -448,21 +469,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
           }
         }
       }
+      where(next, pos + kTile);
+      ask(pos + 2 * kTile);
       if (kTurns)
-        load_values(now, pos);
+        load_values(now);
       else
-        load_keys(next, pos + kTile);
+        load_keys(next);
       // weights: lane (g, t) has positions g, g + 8 of heads 2 t, 2 t + 1
+      float base[NT][2];
       bool passed = false;
 #pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          base[n][e] = m[n][e] == -INFINITY ? 0.0f : m[n][e];
+          passed |= m[n][e] == -INFINITY;
+        }
+#pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        seen |= key_on[u][0] || key_on[u][1];
+        seen |= now[u].on != 0;
+        const bool on0 = now[u].on >> g & 1, on1 = now[u].on >> (g + 8) & 1;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sc[u][n][e] = key_on[u][e >> 1] ? sc[u][n][e] * a.scale2 : -INFINITY;
-            passed |= sc[u][n][e] > m[n][e & 1] + kSlack;
+            // (log2 of the weight; -inf: not seen)
+            sc[u][n][e] = (e >> 1 ? on1 : on0) ? sc[u][n][e] * a.scale2 : -INFINITY;
+            passed |= sc[u][n][e] > base[n][e & 1] + kSlack;
           }
       }
       if (__any_sync(~0u, passed)) {
@@ -478,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
             top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
             const float fade = ex2(m[n][e] - (top == -INFINITY ? 0.0f : top));
             m[n][e] = top;
+            base[n][e] = top == -INFINITY ? 0.0f : top;
             l[n][e] *= fade;
 #pragma unroll
             for (int i = 0; i < kVal; ++i)
@@ -496,8 +530,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
           float w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float base = m[n][e & 1];
-            w[e] = ex2(sc[u][n][e] - (base == -INFINITY ? 0.0f : base));
+            w[e] = ex2(sc[u][n][e] - base[n][e & 1]);
             l[n][e & 1] += w[e];
           }
 #pragma unroll
@@ -527,12 +560,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
         }
       }
       if (kTurns)
-        load_keys(next, pos + kTile);
+        load_keys(next);
       else
-        load_values(next, pos + kTile);
+        load_values(next);
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) now[u] = next[u];
-      lookups(next, pos + 2 * kTile);
     }
     float worst = 0.0f;  // NaN if a sum is not finite
 #pragma unroll
@@ -688,13 +720,13 @@ constexpr int dp_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 1
 // heads: their queries and sums would not fit the registers.
 constexpr int nt_of(int share, int dp) { return share > 8 && dp <= 128 ? 2 : 1; }
 
-template <typename T, int DP, int NT, bool POW2>
+template <typename T, int DP, int NT, bool UNITS>
 fp4_status launch(AtParams a, cudaStream_t s) {
   constexpr int kMaxDev = 64;
   static std::atomic<int> occupancy[kMaxDev];
   constexpr int cols = 8 * NT;
   const size_t smem = (kWarps * cols * (DP + 8) + 3 * kWarps * cols) * sizeof(float);
-  auto kern = k_attention<T, DP, NT, POW2>;
+  auto kern = k_attention<T, DP, NT, UNITS>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return FP4_ERR_CUDA;
   int per = occupancy[dev].load(std::memory_order_acquire);
@@ -724,7 +756,7 @@ fp4_status launch(AtParams a, cudaStream_t s) {
 
 template <typename T, int DP, int NT>
 fp4_status launch_pages(const AtParams &a, cudaStream_t s) {
-  return a.shift >= 0 ? launch<T, DP, NT, true>(a, s) : launch<T, DP, NT, false>(a, s);
+  return a.p.cache.page_size % 16 == 0 ? launch<T, DP, NT, true>(a, s) : launch<T, DP, NT, false>(a, s);
 }
 
 template <typename T>
@@ -755,8 +787,8 @@ fp4_status launch_decode_attention(const fp4_attention_params &p, cudaStream_t s
   const int nt = nt_of(a.share, dp_of(c.head_dim));
   a.groups = (a.share + 8 * nt - 1) / (8 * nt);
   a.shift = -1;
-  if (c.page_size >= 16 && (c.page_size & (c.page_size - 1)) == 0)
-    for (a.shift = 4; (1 << a.shift) < c.page_size;) ++a.shift;
+  if ((c.page_size & (c.page_size - 1)) == 0)
+    for (a.shift = 0; (1 << a.shift) < c.page_size;) ++a.shift;
   a.out16 = aligned16(p.out) && p.out_seq % 8 == 0 && p.out_head % 8 == 0;
   a.scale2 = p.scale * 1.44269504088896f;
   a.cuts = static_cast<int4 *>(p.workspace);
