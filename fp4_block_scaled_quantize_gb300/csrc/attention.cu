@@ -25,12 +25,13 @@
 // next 16 positions are requested as soon as this step's are multiplied, the
 // values likewise, and page numbers a step ahead of both.
 //
-// Split.  The 64-position tiles of all (sequence, key head, head group) rows
-// form one list that the resident CTAs share out evenly, whatever the
-// lengths; the four warps of a CTA take 16 positions of each tile.  A CTA
-// writes the rows it holds whole and leaves at most two partial rows (m, l,
-// O) in the workspace; a second, dependent launch joins those in CTA order,
-// so results repeat exactly.
+// Split.  The tiles (16 or 32 positions) of all (sequence, key head, head
+// group) rows form one list that the warps of the resident CTAs share out
+// evenly, whatever the lengths.  A warp writes the rows it holds whole; what
+// it holds of others (at most two) is joined with the neighbours' in shared
+// memory, and a CTA leaves at most two partial rows (m, l, O) in the
+// workspace.  A second, dependent launch joins those in CTA order, so results
+// repeat exactly.
 #include <cmath>
 
 #include "serve.cuh"
@@ -50,7 +51,7 @@ struct AtParams {
   fp4_attention_params p;
   int groups;   // head groups of a key head: ceil(heads / kv_heads / (8 NT))
   int share;    // heads / kv_heads
-  int tile;     // positions of a tile: 16 per unit and warp
+  int tile;     // positions of a tile: 16 per unit
   int ctas;     // CTAs of the main kernel
   int direct;   // each takes one row, whole
   int shift;    // log2 page_size, or -1: no power of two
@@ -133,7 +134,7 @@ struct Span {
 __device__ __forceinline__ Span span_of(const AtParams &a, int s) {
   const fp4_kv_cache &c = a.p.cache;
   const int64_t room = (int64_t)c.seq_pages * c.page_size;  // fits 32 bits
-  const int given = a.p.lengths[s];
+  const int given = __ldg(a.p.lengths + s);
   Span r;
   r.len = given < 0 ? 0 : given > room ? (int)room : given;
   r.from = a.p.window && r.len > a.p.window ? r.len - a.p.window : 0;
@@ -146,7 +147,7 @@ __device__ __forceinline__ Span span_of(const AtParams &a, int s) {
 // in which a slice of the list begins.
 struct Found {
   int64_t total, start;  // start: list index of the found sequence's first tile
-  int64_t ctas;          // CTAs that share the list: no more than it has tiles
+  int64_t ctas;          // CTAs that share the list: a tile or more for each warp
   int seq;
 };
 template <int THREADS>
@@ -163,7 +164,7 @@ __device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *share
     }
     Found f;
     f.total = __shfl_sync(~0u, inc, seqs - 1);
-    f.ctas = min((int64_t)a.ctas, f.total);
+    f.ctas = min((int64_t)a.ctas, (f.total + kWarps - 1) / kWarps);
     const int64_t x = slice < f.ctas ? f.total * slice / f.ctas : f.total;
     const uint32_t hit = __ballot_sync(~0u, x >= inc - sum && x < inc);
     f.seq = hit ? __ffs(hit) - 1 : seqs;
@@ -188,7 +189,7 @@ __device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *share
     if (w < warp) before += shared[w];
     total += shared[w];
   }
-  const int64_t ctas = min((int64_t)a.ctas, total);
+  const int64_t ctas = min((int64_t)a.ctas, (total + kWarps - 1) / kWarps);
   const int64_t x = slice < ctas ? total * slice / ctas : total;
   if (x >= before && x < before + sum) {  // one thread, if slice < ctas
     int64_t at = before;
@@ -224,48 +225,58 @@ __device__ __forceinline__ void store8(const AtParams &a, int s, int head, int d
   }
 }
 
-// The parts of a row joined: `get(i, m, l, seen)` gives part i's statistics,
-// `add(i, w, v)` adds w times its eight outputs.  Writes the row's result.
-template <typename T, typename Get, typename Add>
-__device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d, int parts, Get get,
-                                       Add add) {
-  float top = -INFINITY, sum = 0.0f;
-  bool any = false;
-  for (int i = 0; i < parts; ++i) {
-    float m, l;
-    bool seen;
-    get(i, m, l, seen);
-    top = fmaxf(top, m);
-    any |= seen;
-  }
-  const float base = top == -INFINITY ? 0.0f : top;
-  float v[8] = {};
-  for (int i = 0; i < parts; ++i) {
-    float m, l;
-    bool seen;
-    get(i, m, l, seen);
-    const float w = ex2(m - base);
-    sum += w * l;
-    add(i, w, v);
-  }
+// log sum exp of a row: m + log2 l in base 2.
+__device__ __forceinline__ void store_lse(const AtParams &a, int s, int head, bool seen, float m, float l) {
+  a.p.lse[(int64_t)s * a.p.heads + head] =
+      seen ? ((m == -INFINITY ? 0.0f : m) + log2f(l)) * 0.693147180559945f : -INFINITY;
+}
+
+// Eight outputs of a row joined from parts, one for each bit of `parts`:
+// m(i), l(i) are part i's statistics, add(i, w, v) adds w times its outputs.
+struct Joined {
+  float top, sum, v[8];
+};
+template <typename M, typename L, typename Add>
+__device__ __forceinline__ Joined join(uint32_t parts, M m, L l, Add add) {
+  Joined j;
+  j.top = -INFINITY;
+  j.sum = 0.0f;
+  for (uint32_t p = parts; p; p &= p - 1) j.top = fmaxf(j.top, m(__ffs(p) - 1));
+  const float base = j.top == -INFINITY ? 0.0f : j.top;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = any ? v[i] / sum : 0.0f;
-  store8<T>(a, s, head, d, v);
-  if (a.p.lse && d == 0)
-    a.p.lse[(int64_t)s * a.p.heads + head] = any ? (base + log2f(sum)) * 0.693147180559945f : -INFINITY;
+  for (int e = 0; e < 8; ++e) j.v[e] = 0.0f;
+  for (uint32_t p = parts; p; p &= p - 1) {
+    const int i = __ffs(p) - 1;
+    const float w = ex2(m(i) - base);
+    j.sum = fmaf(w, l(i), j.sum);
+    add(i, w, j.v);
+  }
+  return j;
+}
+// Writes the result of a row that saw something (seen) or nothing.
+template <typename T>
+__device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d, Joined j, bool seen) {
+  const float w = seen ? 1.0f / j.sum : 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) j.v[e] *= w;
+  store8<T>(a, s, head, d, j.v);
+  if (a.p.lse && d == 0) store_lse(a, s, head, seen, j.top, j.sum);
 }
 
 template <typename T, int DP, int NT, bool UNITS>
 __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
     k_attention(const __grid_constant__ AtParams a) {
   constexpr int kCols = 8 * NT, kKey = DP / 32, kVal = DP / 64, kUnits = units_of(DP, NT);
-  constexpr int kTile = 16 * kUnits * kWarps;
+  constexpr int kTile = 16 * kUnits;
   // wide heads: keys and values take turns in the same registers
   constexpr bool kTurns = DP > 128;
   extern __shared__ __align__(16) float smem[];
   __shared__ int64_t scan[kWarps + 2];
-  float *o_sh = smem;                                // [kWarps][kCols][DP + 8]
-  float *st_sh = smem + kWarps * kCols * (DP + 8);   // [3][kWarps][kCols]: m, l, seen
+  // parts of rows that a warp began or ended with: [2 kWarps][kCols][DP + 8]
+  // outputs, [3][2 kWarps][kCols] m, l, seen, and whose they are
+  constexpr int kParts = 2 * kWarps;
+  float *o_sh = smem, *st_sh = smem + kParts * kCols * (DP + 8);
+  __shared__ int4 part_sh[kParts];  // sequence (-1: none), row, begins with it, ends with it
   const fp4_kv_cache &c = a.p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int D = c.head_dim, rows = c.kv_heads * a.groups;
@@ -273,6 +284,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
   int64_t at, end, start;
   int s;
   launch_dependents();
+  if (lane < 2) part_sh[2 * warp + lane] = make_int4(-1, 0, 0, 0);
+  __syncwarp();
   if (a.direct) {  // a CTA per row
     s = blockIdx.x / rows;
     start = 0;
@@ -312,6 +325,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
     }
   }
 
+  // each warp takes a quarter of the slice, row by row, by itself
+  {
+    const int64_t n = end - at;
+    end = at + n * (warp + 1) / kWarps;
+    at += n * warp / kWarps;
+  }
   while (at < end) {
     const Span sp = span_of(a, s);
     const int64_t mine = (int64_t)rows * sp.tiles;
@@ -448,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[n][i][j][0] = o[n][i][j][1] = o[n][i][j][2] = o[n][i][j][3] = 0.0f;
     }
-    int pos = sp.base + kTile * tile0 + 16 * kUnits * warp;
+    int pos = sp.base + kTile * tile0;
     ask(pos);
     where(now, pos);
     ask(pos + kTile);
@@ -457,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
     for (; pos < stop; pos += kTile) {
       float sc[kUnits][NT][4];
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
+      for (int u = 0; u < kUnits; ++u)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           sc[u][n][0] = sc[u][n][1] = sc[u][n][2] = sc[u][n][3] = 0.0f;
@@ -468,7 +487,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
             mma(sc[u][n], k0.z, k1.z, k0.w, k1.w, q[n][i].z, q[n][i].w, T());
           }
         }
-      }
       where(next, pos + kTile);
       ask(pos + 2 * kTile);
       if (kTurns)
@@ -578,23 +596,49 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
     if (!both || !__any_sync(~0u, worst != 0.0f)) break;
     }
 
-    // join the four warps
-    seen = __any_sync(~0u, seen);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float v = l[n][e];
-        v += __shfl_xor_sync(~0u, v, 4);
-        v += __shfl_xor_sync(~0u, v, 8);
-        v += __shfl_xor_sync(~0u, v, 16);
+        l[n][e] += __shfl_xor_sync(~0u, l[n][e], 4);
+        l[n][e] += __shfl_xor_sync(~0u, l[n][e], 8);
+        l[n][e] += __shfl_xor_sync(~0u, l[n][e], 16);
+      }
+    if (tile0 == 0 && tile1 == sp.tiles) {  // the whole row
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int col = 8 * n + 2 * t + e;
+          if (col >= heads) continue;
+          const float w = seen ? 1.0f / l[n][e] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < kVal; ++i) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[2 * j] = o[n][i][j][e] * w;
+              v[2 * j + 1] = o[n][i][j][2 + e] * w;
+            }
+            if (64 * i + 8 * g < D) store8<T>(a, s, head0 + col, 64 * i + 8 * g, v);
+          }
+          if (a.p.lse && g == 0) store_lse(a, s, head0 + col, seen, m[n][e], l[n][e]);
+        }
+      continue;
+    }
+    const int part = 2 * warp + (tile0 == 0);  // the warp's first row, or its last
+    if (lane == 0) part_sh[part] = make_int4(s, row, tile0 == 0, tile1 == sp.tiles);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
         const int col = 8 * n + 2 * t + e;
         if (g == 0) {
-          st_sh[warp * kCols + col] = m[n][e];
-          st_sh[(kWarps + warp) * kCols + col] = v;
-          st_sh[(2 * kWarps + warp) * kCols + col] = seen ? 1.0f : 0.0f;
+          st_sh[part * kCols + col] = m[n][e];
+          st_sh[(kParts + part) * kCols + col] = l[n][e];
+          st_sh[(2 * kParts + part) * kCols + col] = seen ? 1.0f : 0.0f;
         }
-        float *to = o_sh + (warp * kCols + col) * (DP + 8);
+        float *to = o_sh + (part * kCols + col) * (DP + 8);
 #pragma unroll
         for (int i = 0; i < kVal; ++i) {
           *reinterpret_cast<float4 *>(to + 64 * i + 8 * g) =
@@ -603,48 +647,44 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
               make_float4(o[n][i][2][e], o[n][i][2][2 + e], o[n][i][3][e], o[n][i][3][2 + e]);
         }
       }
-    __syncthreads();
-    const bool whole = tile0 == 0 && tile1 == sp.tiles;
-    float *slot = a.ws + (blockIdx.x * 2 + (tile0 == 0)) * (int64_t)slot_floats(kCols, DP);
-    for (int i = threadIdx.x; i < heads * (DP / 8); i += kThreads) {
-      const int col = i / (DP / 8), d = 8 * (i % (DP / 8));
+  }
+
+  // join the warps' parts, row by row
+  __syncthreads();
+  const int4 mine = part_sh[lane % kParts];
+  uint32_t there = __ballot_sync(~0u, mine.x >= 0) & ((1u << kParts) - 1);
+  while (there) {
+    const int i0 = __ffs(there) - 1;
+    const int s = __shfl_sync(~0u, mine.x, i0), row = __shfl_sync(~0u, mine.y, i0);
+    const bool begins = __shfl_sync(~0u, mine.z, i0);
+    const uint32_t parts = __ballot_sync(~0u, mine.x == s && mine.y == row) & there;
+    const bool whole = begins && __shfl_sync(~0u, mine.w, 31 - __clz(parts));
+    there &= ~parts;
+    const int kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
+    const int heads = min(kCols, (kvh + 1) * a.share - head0);
+    float *slot = a.ws + (blockIdx.x * 2 + begins) * (int64_t)slot_floats(kCols, DP);
+    for (int item = threadIdx.x; item < heads * (DP / 8); item += kThreads) {
+      const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
       if (d >= D) continue;
-      auto get = [&](int w, float &pm, float &pl, bool &ps) {
-        pm = st_sh[w * kCols + col];
-        pl = st_sh[(kWarps + w) * kCols + col];
-        ps = st_sh[(2 * kWarps + w) * kCols + col] != 0.0f;
-      };
-      auto add = [&](int w, float f, float *v) {
-        const float *from = o_sh + (w * kCols + col) * (DP + 8) + d;
+      const Joined j = join(
+          parts, [&](int i) { return st_sh[i * kCols + col]; },
+          [&](int i) { return st_sh[(kParts + i) * kCols + col]; },
+          [&](int i, float f, float *v) {
+            const float *from = o_sh + (i * kCols + col) * (DP + 8) + d;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(f, from[e], v[e]);
-      };
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(f, from[e], v[e]);
+          });
+      bool any = false;
+      for (uint32_t p = parts; p; p &= p - 1) any |= st_sh[(2 * kParts + __ffs(p) - 1) * kCols + col] != 0.0f;
       if (whole) {
-        finish<T>(a, s, head0 + col, d, kWarps, get, add);
+        finish<T>(a, s, head0 + col, d, j, any);
         continue;
       }
-      float top = -INFINITY, sum = 0.0f, any = 0.0f, v[8] = {};
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, st_sh[w * kCols + col]);
-      for (int w = 0; w < kWarps; ++w) {
-        float pm, pl;
-        bool ps;
-        get(w, pm, pl, ps);
-        const float f = ex2(pm - (top == -INFINITY ? 0.0f : top));
-        sum = fmaf(f, pl, sum);
-        any = ps ? 1.0f : any;
-        add(w, f, v);
-      }
-      float *to = slot + col * DP + d;
-      *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
-      if (d == 0) {
-        float *st = slot + kCols * DP + col * 4;
-        st[0] = top;
-        st[1] = sum;
-        st[2] = any;
-      }
+      float *out = slot + col * DP + d;
+      *reinterpret_cast<float4 *>(out) = make_float4(j.v[0], j.v[1], j.v[2], j.v[3]);
+      *reinterpret_cast<float4 *>(out + 4) = make_float4(j.v[4], j.v[5], j.v[6], j.v[7]);
+      if (d == 0) *reinterpret_cast<float4 *>(slot + kCols * DP + col * 4) = make_float4(j.top, j.sum, any, 0.0f);
     }
-    __syncthreads();
   }
 }
 
@@ -704,15 +744,16 @@ __global__ void __launch_bounds__(kJoin) k_attention_join(const __grid_constant_
   }
   __syncthreads();
   if (group != 0 || col >= heads || d >= c.head_dim) return;
-  finish<T>(
-      a, s, head0 + col, d, kGroups,
-      [&](int w, float &m, float &l, bool &seen) {
-        m = part_sh[w][0][item], l = part_sh[w][1][item], seen = part_sh[w][2][item] != 0.0f;
-      },
+  bool seen = false;
+  for (int w = 0; w < kGroups; ++w) seen |= part_sh[w][2][item] != 0.0f;
+  const Joined j = join(
+      (1u << kGroups) - 1, [&](int w) { return part_sh[w][0][item]; },
+      [&](int w) { return part_sh[w][1][item]; },
       [&](int w, float fw, float *v) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = fmaf(fw, part_sh[w][3 + e][item], v[e]);
       });
+  finish<T>(a, s, head0 + col, d, j, seen);
 }
 
 constexpr int dp_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256; }
@@ -725,7 +766,7 @@ fp4_status launch(AtParams a, cudaStream_t s) {
   constexpr int kMaxDev = 64;
   static std::atomic<int> occupancy[kMaxDev];
   constexpr int cols = 8 * NT;
-  const size_t smem = (kWarps * cols * (DP + 8) + 3 * kWarps * cols) * sizeof(float);
+  const size_t smem = (2 * kWarps * cols * (DP + 8) + 6 * kWarps * cols) * sizeof(float);
   auto kern = k_attention<T, DP, NT, UNITS>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return FP4_ERR_CUDA;
@@ -737,13 +778,13 @@ fp4_status launch(AtParams a, cudaStream_t s) {
     occupancy[dev].store(per, std::memory_order_release);
   }
   const fp4_kv_cache &c = a.p.cache;
+  a.tile = 16 * units_of(DP, NT);
   // no more CTAs than the table has tiles
   const int64_t rows = (int64_t)c.seqs * c.kv_heads * a.groups;
   const int64_t room = (int64_t)c.seq_pages * c.page_size;
   const int64_t most = (int64_t)sm_count() * (per < kPerSM ? per : kPerSM);
-  const int64_t tiles = rows * ceil_div(room, 16 * kWarps * units_of(DP, NT));
+  const int64_t tiles = ceil_div(rows * ceil_div(room, a.tile), kWarps);
   if (rows > INT32_MAX) return FP4_ERR_SHAPE;
-  a.tile = 16 * kWarps * units_of(DP, NT);
   a.direct = room <= kDirect;
   a.ctas = (int)(a.direct ? rows : tiles < most ? tiles : most);
   kern<<<(unsigned)a.ctas, kThreads, smem, s>>>(a);
