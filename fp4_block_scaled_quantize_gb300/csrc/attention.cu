@@ -58,7 +58,6 @@ struct AtParams {
   int out16;    // rows of out allow 16-byte stores
   float scale2; // scale * log2 e
   float *ws;    // [ctas][2] partial rows
-  int4 *cuts;   // [ctas] the row cut where a slice begins: sequence, row, first CTA, parts
   uint32_t *status;
 };
 
@@ -144,14 +143,14 @@ __device__ __forceinline__ Span span_of(const AtParams &a, int s) {
 }
 
 // Prefix over the sequences: the sum of rows * tiles of all, and the sequence
-// in which a slice of the list begins.
+// in which a slice of the list begins (or the sequence `which`).
 struct Found {
   int64_t total, start;  // start: list index of the found sequence's first tile
   int64_t ctas;          // CTAs that share the list: a tile or more for each warp
   int seq;
 };
 template <int THREADS>
-__device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *shared) {
+__device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *shared, int which = -1) {
   constexpr int kW = THREADS / 32;
   const int seqs = a.p.cache.seqs, per = (seqs + THREADS - 1) / THREADS;
   if (seqs <= 32) {  // each warp by itself
@@ -166,7 +165,7 @@ __device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *share
     f.total = __shfl_sync(~0u, inc, seqs - 1);
     f.ctas = min((int64_t)a.ctas, (f.total + kWarps - 1) / kWarps);
     const int64_t x = slice < f.ctas ? f.total * slice / f.ctas : f.total;
-    const uint32_t hit = __ballot_sync(~0u, x >= inc - sum && x < inc);
+    const uint32_t hit = __ballot_sync(~0u, which < 0 ? x >= inc - sum && x < inc : lane == which);
     f.seq = hit ? __ffs(hit) - 1 : seqs;
     f.start = hit ? __shfl_sync(~0u, inc - sum, f.seq) : f.total;
     return f;
@@ -191,11 +190,11 @@ __device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *share
   }
   const int64_t ctas = min((int64_t)a.ctas, (total + kWarps - 1) / kWarps);
   const int64_t x = slice < ctas ? total * slice / ctas : total;
-  if (x >= before && x < before + sum) {  // one thread, if slice < ctas
+  if (which < 0 ? x >= before && x < before + sum : which >= s0 && which < s1) {  // one thread, if any
     int64_t at = before;
     for (int s = s0;; ++s) {
       const int64_t n = (int64_t)rows * span_of(a, s).tiles;
-      if (x < at + n) {
+      if (which < 0 ? x < at + n : s == which) {
         shared[kW] = s;
         shared[kW + 1] = at;
         break;
@@ -207,8 +206,9 @@ __device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *share
   Found f;
   f.total = total;
   f.ctas = ctas;
-  f.seq = slice < ctas ? (int)shared[kW] : seqs;
-  f.start = slice < ctas ? shared[kW + 1] : total;
+  const bool found = which >= 0 || slice < ctas;
+  f.seq = found ? (int)shared[kW] : seqs;
+  f.start = found ? shared[kW + 1] : total;
   return f;
 }
 
@@ -297,18 +297,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
     s = f.seq;
     start = f.start;
     at = end = 0;
-    int4 cut = make_int4(0, 0, 0, 0);
     if (blockIdx.x < f.ctas) {
       at = f.total * blockIdx.x / f.ctas;
       end = f.total * (blockIdx.x + 1) / f.ctas;
-      // the row begins at x0, in the slice of `first`, and ends at x1
-      const int tiles = span_of(a, s).tiles, row = (int)((at - start) / tiles);
-      const int64_t x0 = start + (int64_t)row * tiles, x1 = x0 + tiles - 1;
-      const int first = (int)(((x0 + 1) * f.ctas - 1) / f.total);
-      if (x0 < at && first == (int)blockIdx.x - 1)
-        cut = make_int4(s, row, first, (int)(((x1 + 1) * f.ctas - 1) / f.total) - first + 1);
     }
-    if (threadIdx.x == 0) a.cuts[blockIdx.x] = cut;
   }
   // sequences that see nothing are in no slice: their rows are written here
   for (int e = a.direct ? s : blockIdx.x; e < c.seqs; e += a.direct ? c.seqs : a.ctas) {
@@ -688,72 +680,89 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
   }
 }
 
-// Joins partial rows.  CTA c takes the row in which slice c + 1 begins, if it
-// began in slice c (so every split row has one CTA); its threads take
-// eight outputs each, in groups that walk every `groups`-th part four at a
-// time, and the first group joins the groups.
-constexpr int kJoin = 512;
-template <typename T, int DP, int NT>
-__global__ void __launch_bounds__(kJoin) k_attention_join(const __grid_constant__ AtParams a) {
-  constexpr int kCols = 8 * NT, kItems = kCols * DP / 8, kGroups = kJoin / kItems;
+// Joins partial rows.  Many rows are cut into few parts each: narrow CTAs, of
+// which CTA c takes the row in which slice c + 1 begins, if it began in slice
+// c (so every cut row has one).  Few rows are cut into many: wide CTAs, one
+// for each row.  Which parts a row has follows from the lengths, before the
+// main grid is waited for.  A CTA's threads take eight outputs each, in groups
+// that walk every kGroups-th part four at a time; the first joins the groups.
+constexpr int kNarrow = 128, kWide = 1024;
+template <typename T, int DP, int NT, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constant__ AtParams a) {
+  constexpr int kCols = 8 * NT, kItems = kCols * DP / 8;
+  constexpr int kGroups = THREADS < kItems ? 1 : THREADS / kItems;
+  __shared__ int64_t scan[THREADS / 32 + 2];
   __shared__ float part_sh[kGroups][11][kItems];  // m, l, seen, eight outputs
-  dependent_wait();
   const fp4_kv_cache &c = a.p.cache;
-  const int4 cut = a.cuts[blockIdx.x + 1];
-  const int s = cut.x, row = cut.y, first = cut.z, parts = cut.w;
-  if (parts == 0) return;
+  const int rows = c.kv_heads * a.groups, slice = blockIdx.x + 1;
+  const Found f = THREADS == kNarrow ? find<THREADS>(a, rows, slice, scan)
+                                     : find<THREADS>(a, rows, 0, scan, blockIdx.x / rows);
+  int s = f.seq, row = 0, first = 0, parts = 1;
+  if (s < c.seqs && span_of(a, s).tiles) {
+    const int tiles = span_of(a, s).tiles;
+    const int64_t at = f.total * slice / f.ctas;  // narrow: list index where the slice begins
+    row = THREADS == kNarrow ? (int)((at - f.start) / tiles) : blockIdx.x - s * rows;
+    const int64_t begin = f.start + (int64_t)row * tiles;
+    first = (int)(((begin + 1) * f.ctas - 1) / f.total);  // the CTA whose slice holds the row's first tile
+    parts = (int)(((begin + tiles) * f.ctas - 1) / f.total) - first + 1;
+    if (THREADS == kNarrow && (begin == at || first != (int)blockIdx.x)) parts = 1;
+  }
+  dependent_wait();  // also where there is nothing to do: this grid ends after the main one
+  if (parts == 1) return;
   const int kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
   const int heads = min(kCols, (kvh + 1) * a.share - head0);
-  const int item = threadIdx.x % kItems, group = threadIdx.x / kItems;
-  const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
-  if (group < kGroups) {
-    float m = -INFINITY, l = 0.0f, any = 0.0f, v[8] = {};
-    constexpr int kBatch = 4;
-    for (int w0 = group; w0 < parts; w0 += kBatch * kGroups) {
-      float4 st[kBatch], lo[kBatch], hi[kBatch];
+  const int group = THREADS < kItems ? 0 : threadIdx.x / kItems;
+  for (int item = threadIdx.x % kItems; item < kItems; item += THREADS < kItems ? THREADS : kItems) {
+    const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
+    if (group < kGroups) {
+      float m = -INFINITY, l = 0.0f, any = 0.0f, v[8] = {};
+      constexpr int kBatch = 4;
+      for (int w0 = group; w0 < parts; w0 += kBatch * kGroups) {
+        float4 st[kBatch], lo[kBatch], hi[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int w = w0 + i * kGroups;
-        st[i] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-        lo[i] = hi[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (w >= parts) continue;
-        const float *slot = a.ws + ((int64_t)(first + w) * 2 + (w == 0)) * slot_floats(kCols, DP);
-        if (col < heads && d < c.head_dim) {  // what was written
-          st[i] = *reinterpret_cast<const float4 *>(slot + kCols * DP + col * 4);
-          lo[i] = *reinterpret_cast<const float4 *>(slot + col * DP + d);
-          hi[i] = *reinterpret_cast<const float4 *>(slot + col * DP + d + 4);
+        for (int i = 0; i < kBatch; ++i) {
+          const int w = w0 + i * kGroups;
+          st[i] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+          lo[i] = hi[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (w >= parts) continue;
+          const float *slot = a.ws + ((int64_t)(first + w) * 2 + (w == 0)) * slot_floats(kCols, DP);
+          if (col < heads && d < c.head_dim) {  // what was written
+            st[i] = *reinterpret_cast<const float4 *>(slot + kCols * DP + col * 4);
+            lo[i] = *reinterpret_cast<const float4 *>(slot + col * DP + d);
+            hi[i] = *reinterpret_cast<const float4 *>(slot + col * DP + d + 4);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const float now = fmaxf(m, st[i].x), base = now == -INFINITY ? 0.0f : now;
+          const float fo = ex2(m - base), fn = ex2(st[i].x - base);
+          m = now;
+          l = l * fo + st[i].y * fn;
+          any = fmaxf(any, st[i].z);
+          const float p[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = v[e] * fo + p[e] * fn;
         }
       }
+      part_sh[group][0][item] = m;
+      part_sh[group][1][item] = l;
+      part_sh[group][2][item] = any;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const float now = fmaxf(m, st[i].x), base = now == -INFINITY ? 0.0f : now;
-        const float fo = ex2(m - base), fn = ex2(st[i].x - base);
-        m = now;
-        l = l * fo + st[i].y * fn;
-        any = fmaxf(any, st[i].z);
-        const float p[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] * fo + p[e] * fn;
-      }
+      for (int e = 0; e < 8; ++e) part_sh[group][3 + e][item] = v[e];
     }
-    part_sh[group][0][item] = m;
-    part_sh[group][1][item] = l;
-    part_sh[group][2][item] = any;
+    if (kGroups > 1) __syncthreads();  // (then the loop runs once, for every thread)
+    if (group != 0 || col >= heads || d >= c.head_dim) continue;
+    bool seen = false;
+    for (int w = 0; w < kGroups; ++w) seen |= part_sh[w][2][item] != 0.0f;
+    const Joined j = join(
+        (1u << kGroups) - 1, [&](int w) { return part_sh[w][0][item]; },
+        [&](int w) { return part_sh[w][1][item]; },
+        [&](int w, float fw, float *v) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) part_sh[group][3 + e][item] = v[e];
+          for (int e = 0; e < 8; ++e) v[e] = fmaf(fw, part_sh[w][3 + e][item], v[e]);
+        });
+    finish<T>(a, s, head0 + col, d, j, seen);
   }
-  __syncthreads();
-  if (group != 0 || col >= heads || d >= c.head_dim) return;
-  bool seen = false;
-  for (int w = 0; w < kGroups; ++w) seen |= part_sh[w][2][item] != 0.0f;
-  const Joined j = join(
-      (1u << kGroups) - 1, [&](int w) { return part_sh[w][0][item]; },
-      [&](int w) { return part_sh[w][1][item]; },
-      [&](int w, float fw, float *v) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = fmaf(fw, part_sh[w][3 + e][item], v[e]);
-      });
-  finish<T>(a, s, head0 + col, d, j, seen);
 }
 
 constexpr int dp_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256; }
@@ -790,9 +799,11 @@ fp4_status launch(AtParams a, cudaStream_t s) {
   kern<<<(unsigned)a.ctas, kThreads, smem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return FP4_ERR_CUDA;
   if (a.direct || a.ctas < 2) return FP4_OK;
-  return launch_dependent(k_attention_join<T, DP, NT>, dim3((unsigned)a.ctas - 1), dim3(kJoin), 0, s, a) == cudaSuccess
-             ? FP4_OK
-             : FP4_ERR_CUDA;
+  const cudaError_t e =
+      rows * 4 <= a.ctas
+          ? launch_dependent(k_attention_join<T, DP, NT, kWide>, dim3((unsigned)rows), dim3(kWide), 0, s, a)
+          : launch_dependent(k_attention_join<T, DP, NT, kNarrow>, dim3((unsigned)a.ctas - 1), dim3(kNarrow), 0, s, a);
+  return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
 
 template <typename T, int DP, int NT>
@@ -815,7 +826,7 @@ fp4_status launch_type(const AtParams &a, int nt, cudaStream_t s) {
 int64_t decode_attention_workspace(int64_t room, int heads, int kv_heads, int head_dim) {
   if (room <= kDirect) return 0;
   const int dp = dp_of(head_dim), cols = 8 * nt_of(heads / kv_heads, dp);
-  return (int64_t)sm_count() * kPerSM * (2 * slot_floats(cols, dp) * sizeof(float) + sizeof(int4));
+  return (int64_t)sm_count() * kPerSM * 2 * slot_floats(cols, dp) * sizeof(float);
 }
 
 fp4_status launch_decode_attention(const fp4_attention_params &p, cudaStream_t s) {
@@ -832,8 +843,7 @@ fp4_status launch_decode_attention(const fp4_attention_params &p, cudaStream_t s
     for (a.shift = 0; (1 << a.shift) < c.page_size;) ++a.shift;
   a.out16 = aligned16(p.out) && p.out_seq % 8 == 0 && p.out_head % 8 == 0;
   a.scale2 = p.scale * 1.44269504088896f;
-  a.cuts = static_cast<int4 *>(p.workspace);
-  a.ws = reinterpret_cast<float *>(a.cuts + (int64_t)sm_count() * kPerSM);
+  a.ws = static_cast<float *>(p.workspace);
   return c.type == FP4_BF16 ? launch_type<__nv_bfloat16>(a, nt, s) : launch_type<__half>(a, nt, s);
 }
 
