@@ -380,10 +380,12 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   __syncwarp();
-  const int64_t tile0 = (int64_t)cluster * group + tw, hop = (int64_t)p.clusters * group;
-  const int mine = tw < group && tile0 < p.tiles ? (int)((p.tiles - 1 - tile0) / hop) + 1 : 0;  // the warp's tiles
+  // the cluster's tiles [t0, t1), `group` a round, and how many of them are the warp's
+  const int t0 = (int)((int64_t)p.tiles * cluster / p.clusters), t1 = (int)((int64_t)p.tiles * (cluster + 1) / p.clusters);
+  const int tile0 = t0 + tw;
+  const int mine = tw < group && tile0 < t1 ? (t1 - 1 - tile0) / group + 1 : 0;
   int ahead = mine * ns;  // stages still to be requested
-  int64_t ld_tile = tile0;
+  int ld_tile = tile0;
   const bool tiled = MODE == kAny ? p.words == kTiled : MODE == kTiled;
   Loader<BLOCK, MODE, kRows> ld;
   ld.step = s0;
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
     --ahead;
     if (ld.step == s0 + ns) {
       ld.step = s0;
-      ld_tile += hop;
+      ld_tile += group;
       ld.row0 = (int)ld.first_row(ld_tile, tiled);
     }
   };
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
   int flying = 0;    // stages in flight when it did
   for (int r = 0; r < p.rounds; ++r) {
     float acc[NT][kPairs][4] = {};
-    const int half = kRows == 16 ? (int)((tile0 + r * hop) >> 2 & 1) * 8 : 0;  // kTiled: words 0, 1 or 2, 3
+    const int half = kRows == 16 ? ((tile0 + r * group) >> 2 & 1) * 8 : 0;  // kTiled: words 0, 1 or 2, 3
     int xo = (s0 - c0) * 512;
     const float *sxl = sx + (s0 - c0) * kCols + 2 * t;
     for (int st = s0; st < (r < mine && live ? s0 + ns : s0); ++st) {
@@ -548,7 +550,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
     float sd = 0.0f;
     int64_t n = j.N;
     auto row_of = [&](int to) {
-      const int64_t tile = (r * (int64_t)p.clusters + cluster) * group + to;
+      const int tile = t0 + r * group + to;
+      n = j.N;
+      if (tile >= t1) return;
       n = ld.first_row(tile, tiled) + (tiled ? 32 * (row >> 3) + (row & 7) : row);
       if (n >= j.N) return;
       shift = (KIND == kUE5M3 ? 3 : 0) + (j.shift ? j.shift[n] : 0);
@@ -697,16 +701,17 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
       for (int sk = 1; sk <= warps && sk <= span; ++sk) {
         const int group = warps / sk;
         if (sk > 1 && sk < warps && sk < span && warps / (sk + 1) == group) continue;  // a larger one keeps as many tiles
-        const int64_t rounds = ceil_div(p.tiles, (int64_t)room * group);
+        const int64_t clusters = p.tiles < room ? p.tiles : room, most = ceil_div(p.tiles, clusters);
+        const int64_t rounds = ceil_div(most, group);
         const int join = sk > 1 ? 12 : 1;
-        const int64_t cost = rounds * (group * span + 2 * ceil_div(span, sk) + join + (S > 1 ? 40 : 0)) + p.mc * span / 8;
+        const int64_t cost = most * span + rounds * (2 * ceil_div(span, sk) + join + (S > 1 ? 40 : 0)) + p.mc * span / 8;
         if (cost >= best) continue;
         best = cost;
         p.S = S;
         p.sk = sk;
         p.warps = warps;
         p.rounds = (int)rounds;
-        p.clusters = (int)ceil_div(p.tiles, rounds * group);
+        p.clusters = (int)clusters;
       }
       if (warps == kMaxWarps && S > 1) break;  // more CTAs per tile only add joins
     }
