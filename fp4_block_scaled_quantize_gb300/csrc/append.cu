@@ -6,12 +6,17 @@
 // element; cos and sin are reused over the heads of a token), launch and three
 // dependent loads (position, page, nothing else) for a few tokens.
 //
-// Layout.  A thread owns one unit of a head -- 16 bytes, or the two 16-byte
-// pieces whose elements form pairs (i, i + rot_dim / 2) -- for one token, and
-// walks over the token's query, key and value heads with cos and sin held in
-// registers.  The rows of a CTA's tokens are spread over its threads so that
-// neighbours touch neighbouring pieces of a row.  Rows whose pointers,
-// strides or sizes are not whole 16-byte pieces go by single elements.
+// Layout.  A thread owns one unit of a head -- two 16-byte pieces, in the
+// rotated part the two whose elements form pairs (i, i + rot_dim / 2) -- for
+// one token, and walks over the token's query, key and value heads with cos
+// and sin held in registers; neighbours touch neighbouring pieces of a row.
+// Three rows are requested together and nothing of a token's place is waited
+// for before its stores; the next token's place is looked up meanwhile.  Rows
+// whose pointers, strides or sizes are not whole 16-byte pieces go by single
+// elements.
+// Measured: 8191 tokens, 32 + 2 x 8 heads of 128, BF16: 36.6 us (5.5 TB/s, 82%
+// of a copy's rate; 41 us with four CTAs an SM, 46 without looking ahead); one
+// token 2.7 us in a graph.
 #include "serve.cuh"
 
 namespace fp4 {

@@ -10,9 +10,9 @@
 // and sum l per query head with weights 2^(s - m).  m is moved only when a
 // score passes it by more than 8 (weights stay below 2^8): most steps then
 // need no reduction over lanes and no rescaling.  A weight enters its product
-// with the values as two 16-bit parts (hi + lo, 2^-16 of it left out) and
-// the sum l as it is, so rounding weights costs no accuracy; the products are
-// summed in binary32.
+// with the values as two 16-bit parts (hi + lo, 2^-16 of it left out; f16:
+// 2^-32 of the largest if that is more) and the sum l as it is, so rounding
+// weights costs no accuracy; the products are summed in binary32.
 //
 // Layout.  Query heads that share a key head are the 8 columns of an MMA (NT
 // tiles of 8), positions or head elements its 16 rows:
@@ -32,6 +32,10 @@
 // memory, and a CTA leaves at most two partial rows (m, l, O) in the
 // workspace.  A second, dependent launch joins those in CTA order, so results
 // repeat exactly.
+// Measured: 64 sequences of up to 16384 positions, 32 heads over 8 of 128,
+// BF16: 317 us (6.8 TB/s, a copy's rate); one of 131071: 87 us (91%), 3 us of
+// them the join; 96 windows of 1000, 16 heads of 64: 79 us (66%, the chain of
+// instructions of each 32 positions, with 12 warps an SM); one of 300: 9 us.
 #include <cmath>
 
 #include "serve.cuh"
@@ -41,10 +45,15 @@ namespace fp4 {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-// Groups of 16 positions a warp takes a step: what it keeps in flight.
+// Groups of 16 positions a warp takes a step: what it keeps in flight (heads
+// of 64, 96 windows of 1000: 82 us, with one group 88; heads of 128: 329 us,
+// with two groups and two CTAs an SM 332).
 constexpr int units_of(int dp, int nt) { return dp <= 64 ? 2 : dp <= 128 && nt == 1 ? 1 : 1; }
 constexpr int kPerSM = 5;            // CTAs per SM at most (workspace bound)
-constexpr int kDirect = 512;         // positions up to which a CTA takes a whole row
+// Positions up to which a CTA takes a whole row: no workspace and no second
+// launch (one sequence of 300: 8.9 us for 8.0 with a cut, but 5 us less on the
+// host; 16 of 512: 15.7 us for 16.9; 64 of 512: 38 us for 32).
+constexpr int kDirect = 512;
 constexpr float kSlack = 8.0f;       // log2 by which scores may pass the maximum in use
 
 struct AtParams {
@@ -79,6 +88,15 @@ __device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+template <typename T>
+struct Bf16 {
+  static constexpr bool value = false;
+};
+template <>
+struct Bf16<__nv_bfloat16> {
+  static constexpr bool value = true;
+};
+
 // Lets the join be set up while this grid runs; it waits for its completion
 // (and memory) before it reads anything.
 __device__ __forceinline__ void launch_dependents() {
@@ -100,6 +118,13 @@ __device__ __forceinline__ uint4 load16(const void *p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
+}
+
+// Weights are held 2^lift times as large: f16's smallest is 2^-24, and a long
+// context may have most of its weight in small ones.
+template <typename T>
+__device__ __forceinline__ constexpr float lift() {
+  return Bf16<T>::value ? 0.0f : 7.0f;
 }
 
 // Two values as a pair of T, and what the pair leaves of them.
@@ -226,9 +251,10 @@ __device__ __forceinline__ void store8(const AtParams &a, int s, int head, int d
 }
 
 // log sum exp of a row: m + log2 l in base 2.
+template <typename T>
 __device__ __forceinline__ void store_lse(const AtParams &a, int s, int head, bool seen, float m, float l) {
   a.p.lse[(int64_t)s * a.p.heads + head] =
-      seen ? ((m == -INFINITY ? 0.0f : m) + log2f(l)) * 0.693147180559945f : -INFINITY;
+      seen ? ((m == -INFINITY ? 0.0f : m) + log2f(l) - lift<T>()) * 0.693147180559945f : -INFINITY;
 }
 
 // Eight outputs of a row joined from parts, one for each bit of `parts`:
@@ -260,7 +286,7 @@ __device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d
 #pragma unroll
   for (int e = 0; e < 8; ++e) j.v[e] *= w;
   store8<T>(a, s, head, d, j.v);
-  if (a.p.lse && d == 0) store_lse(a, s, head, seen, j.top, j.sum);
+  if (a.p.lse && d == 0) store_lse<T>(a, s, head, seen, j.top, j.sum);
 }
 
 template <typename T, int DP, int NT, bool UNITS>
@@ -540,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
           float w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            w[e] = ex2(sc[u][n][e] - base[n][e & 1]);
+            w[e] = ex2(sc[u][n][e] - (base[n][e & 1] - lift<T>()));
             l[n][e & 1] += w[e];
           }
 #pragma unroll
@@ -614,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
             }
             if (64 * i + 8 * g < D) store8<T>(a, s, head0 + col, 64 * i + 8 * g, v);
           }
-          if (a.p.lse && g == 0) store_lse(a, s, head0 + col, seen, m[n][e], l[n][e]);
+          if (a.p.lse && g == 0) store_lse<T>(a, s, head0 + col, seen, m[n][e], l[n][e]);
         }
       continue;
     }

@@ -2,12 +2,18 @@
 // x in 16 bits (sm_103a):
 //   y[m][n] = s_dec 2^shift[n] sum_b dec(sf[n][b]) sum_{k in b} e2m1(q[n][k]) x[m][k]
 //
-// Bound: HBM, 0.5 + 1/B bytes per weight read once; at 6.8 TB/s an SM has
-// about 7 issue slots for each 32 weights, so the arithmetic is the m16n8k16
-// f16 MMA with the weight as its 16-row operand and up to 8 NT tokens as
-// columns.  (tcgen05 reads its operands from shared or tensor memory: 4-bit
-// weights would have to be decoded into it first, for a 128-row tile of which
-// all but M columns of work are padding.)
+// Bound: HBM, 0.5 + 1/B bytes per weight read once.  At 6.8 TB/s an SM has
+// 23 clocks, 90 issue slots, for every 16 x 64 weights, and two instructions a
+// pair (decode, scale) already take 32 of them; so the rest of the arithmetic
+// is the m16n8k16 f16 MMA with the weight as its 16-row operand and up to 8 NT
+// tokens as columns.  (tcgen05 reads its operands from shared or tensor
+// memory: 4-bit weights would have to be decoded into it first, for a 128-row
+// tile of which all but M columns of work are padding.)
+// Measured (131072 x 4096, NVFP4): 1 token 54.9 us (5.5 TB/s, 81% of a copy),
+// 8 tokens 61 us (73%), 16 tokens 84 us (54%): instruction issue, about 480
+// instructions for 32 x 256 weights and 8 tokens of which 304 decode, scale
+// and multiply, at half an instruction a clock and scheduler.  4096 x 14336,
+// 1 token: 13.1 us, of which 2.6 launch and set up and 1 joins.
 //
 // Mathematics.  E2M1 has 2 significant bits, a block scale at most 4, so
 // e2m1 * dec(sf) is exact in f16 for E4M3 (2^-10 .. 2,688) and times 2^-3 for
@@ -21,25 +27,26 @@
 // sums are multiplied by the power(s) of two and added in binary32 with
 // nearest rounding.
 //
-// Layout.  A warp takes 16 weight rows and 256 columns a step.  The order of
-// k within an MMA is free as long as both operands share it: lane (g, t)
-// takes columns 64 t .. 64 t + 63 of rows g and g + 8, four 16-byte pieces of
-// payload and the four scale codes over 64 columns of each row -- whole loads
-// and no exchange between lanes -- and each MMA four of its weights.  A step's payload is one
-// TMA box of 16 rows x 128 bytes in the 128-byte swizzle (rows g, g + 1 of a
-// quarter-warp then read different banks); x lies in shared memory as f16,
-// the 16-byte pieces of 256 columns in the order (piece of the lane, t), so
-// that four lanes read 64 contiguous bytes, tokens 64 mod 128 bytes apart.
+// Layout.  A warp takes 32 weight rows (16 above 8 tokens) and 256 columns a
+// step.  The order of k within an MMA is free as long as both operands share
+// it: lane (g, t) takes columns 64 t .. 64 t + 63 of rows g, g + 8, .. -- four
+// 16-byte pieces of payload and the scale codes over 64 columns of each, whole
+// loads and no exchange between lanes -- and each MMA four of its weights.  The
+// payload comes as TMA boxes of 128 bytes a row in the 128-byte swizzle (rows
+// g, g + 1 of a quarter-warp then read different banks), the scales as a box
+// of their own (Words); x lies in shared memory as f16, the 16-byte pieces of
+// 256 columns in the order (piece of the lane, t), so that four lanes read 64
+// contiguous bytes, tokens 64 mod 128 bytes apart.
 //
-// Split.  One CTA of 16 warps per SM; each warp runs its own ring of 2 to 4
-// stages (payload by TMA, scale words by 4-byte cp.async, one mbarrier), so
-// that 64 KB or more of weights are in flight per SM across tiles and before
-// x is ready, and no warp waits for another inside a tile.  The CTA holds x
-// for its K range; sk of its warps share a row tile along K, and a cluster
-// of S CTAs splits K where x for all of it does not fit.  The parts are
-// added in shared memory (over the cluster: distributed) in a fixed order.
-// A row pitch that is not a multiple of 16 bytes (K / 16 odd) is no TMA
-// stride: the ring is then filled by 8-byte cp.async.
+// Split.  One CTA of up to 16 warps per SM; each warp runs its own ring of 2
+// to 4 stages with an mbarrier each, filled by its lane 0 as soon as a stage
+// is in registers, so that 64 KB or more of weights are in flight per SM
+// across tiles and before x is ready, and no warp waits for another inside a
+// tile.  The CTA holds x for its K range; sk of its warps share a row tile
+// along K, and a cluster of S CTAs splits K where x for all of it does not
+// fit.  The parts are added in shared memory (over the cluster: distributed)
+// in a fixed order.  A row pitch that is not a multiple of 16 bytes (K / 16
+// odd) is no TMA stride: the ring is then filled by 8-byte cp.async.
 #include <cooperative_groups.h>
 
 #include "serve.cuh"
@@ -59,7 +66,8 @@ constexpr int kMaxSmem = 227 * 1024;
 constexpr int kMaxWarps = 16;
 // Weight rows of a tile: two MMA row tiles share the loads of x; with two
 // token tiles one, so that 16 warps have the registers and, beside twice the
-// x, the shared memory (32 rows and 12 warps, 16 tokens, 131072 x 4096: 103 us).
+// x, the shared memory (131072 x 4096, 16 tokens: 95 us, with 32 rows and 12
+// warps 103).
 constexpr int rows_of(int nt) { return nt == 1 ? 32 : 16; }
 constexpr int payload_of(int nt) { return rows_of(nt) * kStep / 2; }  // bytes of a stage
 
@@ -456,8 +464,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
       float d[NT][kPairs][4] = {};
       const uint8_t *ra = ring + slot * kPayload + g * 128 + at0;
       // 32 of the lane's 64 columns at a time, a 16-byte piece of each row.
-      // Not unrolled: at twice the size the loop outgrows the instruction
-      // cache (8 tokens, 131072 x 4096: 65 us).
+      // Not unrolled: at twice the size the loop outgrew the instruction cache
+      // (a third of all stalls for 16 tokens).
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         uint4 w[kGroups];
@@ -682,10 +690,10 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   // part of K beside rings of two stages), the least estimated time, in steps
   // of an SM: the steps of its warps, twice the longest warp's, the join (a
   // store; a barrier with rings running dry; one over a cluster) and the
-  // preparation of x.  Measured with x 16 bits wide: 14336 x 4096, 8 tokens,
-  // S, sk = 1, 5: 15.2 us, 1, 4: 16.0, 2, 2: 15.9; 131072 x 4096, 16 tokens,
-  // 1, 1: 88.8, 2, 1: 99.8, 1, 4: 93.4; 4096 x 14336, 12 tokens, 4, 2: 18.8,
-  // 4, 4: 21.4, 8, 1: 25.3.  Tokens are halved until something fits.
+  // preparation of x.  Measured, S, sk: 14336 x 4096, 8 tokens, 1, 4: 14.9 us,
+  // 1, 5: 15.2, 1, 16: 15.6, 2, 2: 16.1; 131072 x 4096, 16 tokens, 1, 1: 85.5,
+  // 1, 4: 92.4, 2, 1: 99.2; 4096 x 14336, 12 tokens, 4, 2: 19.0, 4, 4: 21.4,
+  // 4, 1: 20.5.  Tokens are halved until something fits.
   int64_t best = INT64_MAX;
   auto fits = [&](int S, int warps, int depth) {
     return smem_bytes(p.mc, p.steps, S, NT, warps, depth) <= (size_t)kMaxSmem;
