@@ -4,11 +4,14 @@ Each CUDA translation unit is compiled in parallel into _build/, then linked
 into fp4_block_scaled_quantize_gb300/_lib/libfp4gb300.so.  The quantizer
 units are built with -fmad=false so no multiply-add is contracted into an FMA
 (their arithmetic is specified as separately rounded binary32 operations).
+csrc/bind.c, the serving calls' short way from Python into the library,
+becomes _lib/_bind.so beside it (gcc, the running interpreter's headers).
 """
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libfp4gb300.so")
+BIND = os.path.join(LIBDIR, "_bind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC,
@@ -78,6 +82,13 @@ def build(force=False, verbose=False, extra=()):
         tmp = LIB + ".tmp"
         subprocess.run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs, check=True)
         os.replace(tmp, LIB)
+    bind = os.path.join(CSRC, "bind.c")
+    if force or _stale(BIND, [bind, LIB] + headers):
+        tmp = BIND + ".tmp"
+        subprocess.run([os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-Wall", "-shared",
+                        "-fPIC", "-I" + INCLUDE, "-I" + sysconfig.get_paths()["include"], bind, "-o",
+                        tmp, "-L" + LIBDIR, "-lfp4gb300", "-Wl,-rpath,$ORIGIN", "-lm"], check=True)
+        os.replace(tmp, BIND)
     return LIB
 
 

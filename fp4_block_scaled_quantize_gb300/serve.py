@@ -7,18 +7,23 @@ and raise.  All of them only marshal arguments: the work is done by the
 library's CUDA kernels.  An output or workspace that a function allocates for
 a given ``stream`` belongs to that stream.
 
-Host time counts here (a call's kernels run for a few microseconds), so the
-parameter structs are packed by ``struct`` in the layout of the ctypes
-classes instead of being filled field by field.
+Host time counts here (a call's kernels run for a few microseconds).  The
+ordinary call -- plain tensors that fit each other, the current stream, a new
+output -- goes through the compiled ``_lib/_bind.so``, which reads the tensors
+and fills the parameter struct; every other goes through this module, which
+packs the same structs by ``struct`` in the layout of the ctypes classes.
 """
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 import struct
 from functools import lru_cache
 
 import torch
 
-from . import (FP4_FMT_NVFP4_CTA, FP4_FMT_UE5M3_B16, FP4_FMT_UE5M3_B32, FP4_SF_MMA, FP4Error,
-               _stream, fp4_sf_bytes, lib, n_stripes)
+from . import (FP4_FMT_NVFP4_CTA, FP4_FMT_UE5M3_B16, FP4_FMT_UE5M3_B32, FP4_SF_MMA, LIB_PATH,
+               FP4Error, _stream, fp4_sf_bytes, lib, n_stripes)
 
 FP4_BF16, FP4_F16, FP4_F32 = 0, 1, 2
 _TYPES = {torch.bfloat16: FP4_BF16, torch.float16: FP4_F16, torch.float32: FP4_F32}
@@ -78,6 +83,23 @@ def _lib():
         L.fp4_decode_attention_workspace.restype = i64
         _entry = L
     return _entry
+
+
+@lru_cache(maxsize=1)
+def _bind():
+    """The compiled binding (raises OSError if it has not been built)."""
+    path = os.path.join(os.path.dirname(LIB_PATH), "_bind.so")
+    if not os.path.exists(path):
+        raise OSError(f"{path} is missing: build it with "
+                      "`python -c 'import __graft_entry__ as g; g.build()'`")
+    spec = importlib.util.spec_from_file_location(
+        "_bind", path, loader=importlib.machinery.ExtensionFileLoader("_bind", path))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.setup(torch.Tensor, (torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8,
+                           torch.int8), torch.empty, torch._C._cuda_getCurrentRawStream,
+            torch._C._cuda_getDevice, FP4Error)
+    return m
 
 
 # ------------------------------------------------------------- raw entry points
@@ -145,6 +167,10 @@ def matvec(x, w, out_dtype=None, out=None, stream=None):
     y is [M, N] (or [N]) in out_dtype -- x's dtype by default, or bfloat16,
     float16 or float32 -- or written to `out` (rows may be strided).  The
     activations are not quantised; see fp4_matvec in include/fp4.h."""
+    if out is None and stream is None:
+        y = _bind().matvec(x, w.q, w.sf, w.s_dec, w.row_shift, w.format, w.sf_layout, out_dtype)
+        if y is not NotImplemented:
+            return y
     q, sf, s_dec, shift, format, layout = w.q, w.sf, w.s_dec, w.row_shift, w.format, w.sf_layout
     dtype, sizes = x.dtype, x.shape
     if dtype not in _HALVES:
@@ -261,6 +287,10 @@ def kv_append(k, v, k_pages, v_pages, page_table, pos, seq=None, q=None, rope=No
     float32 (rope_table) keys and queries q [tokens, heads, head_dim] are
     rotated on the way.  Returns the rotated queries (q_out, new by default),
     or None without q.  Tokens at negative positions are skipped."""
+    if stream is None and q_out is None:
+        r = _bind().append(k, v, k_pages, v_pages, page_table, pos, seq, q, rope, interleaved)
+        if r is not NotImplemented:
+            return r
     where = "kv_append"
     cache = _cache_fields(where, k_pages, v_pages, page_table)
     dtype, Hk, D = k_pages.dtype, cache[14], cache[15]
@@ -323,6 +353,10 @@ def decode_attention(q, k_pages, v_pages, page_table, lengths, scale=None, windo
     Returns [seqs, heads, head_dim] in q's dtype (or `out`), and with
     return_lse also the logarithm of each row's sum of exponentials, float32
     [seqs, heads].  A sequence of length 0 gives zeros (and -inf)."""
+    if out is None and stream is None and not return_lse:
+        r = _bind().attention(q, k_pages, v_pages, page_table, lengths, scale, window)
+        if r is not NotImplemented:
+            return r
     where = "decode_attention"
     cache = _cache_fields(where, k_pages, v_pages, page_table)
     dtype, seqs, Hk, D = k_pages.dtype, cache[11], cache[14], cache[15]

@@ -213,3 +213,19 @@ def test_reference_definitions():
         y, _ = rotate(x, fq.rope_table(10, 16, device="cpu"), pos, inter)
         assert torch.allclose(y.norm(dim=-1), x.norm(dim=-1), rtol=1e-6)
         assert torch.equal(y[0], x[0])
+
+
+def test_the_binding_leaves_what_is_not_ordinary():
+    """The compiled binding takes CUDA tensors that fit each other; anything
+    else it leaves to the general way, without an exception."""
+    b = serve._bind()
+    x, p = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(3, dtype=torch.int32)
+    for args in ((), (x,) * 8, (x, x, x, x, None, 0, 0, None), (1, 2, 3, 4, 5, 6, 7, 8),
+                 (x, x, x, x, None, "a", 0, None), (torch.nn.Parameter(x), x, x, x, None, 0, 0, None),
+                 (x.to_sparse(), x, x, x, None, 0, 0, None)):
+        assert b.matvec(*args) is NotImplemented
+    for args in ((), (x, x, p, p, i[None], i, None, None, None, False), (None,) * 10):
+        assert b.append(*args) is NotImplemented
+    for args in ((), (x, p, p, i[None], i, None, 0), (None,) * 7, (x, p, p, i[None], i, "a", 2 ** 70)):
+        assert b.attention(*args) is NotImplemented

@@ -17,6 +17,7 @@ import pytest
 import torch
 
 import fp4_block_scaled_quantize_gb300 as fq
+from fp4_block_scaled_quantize_gb300 import serve
 from gpu_util import need_gpu
 from serve_ref import HALF_ULP, TINY, attention, matvec, rotate, scale_values, tile
 
@@ -529,3 +530,113 @@ def test_scale_tables_of_the_reference():
     codes = torch.arange(0x7F, dtype=torch.uint8)
     assert torch.equal(scale_values("e4m3")[:0x7F], codes.view(torch.float8_e4m3fn).double())
     assert scale_values("ue5m3")[0xF7] == 61440 and scale_values("ue5m3")[1] == 2.0 ** -17
+
+
+class General:
+    """A binding that leaves every call to the general way."""
+    matvec = append = attention = staticmethod(lambda *a: NotImplemented)
+
+
+def both_ways(monkeypatch, call):
+    """The call through the compiled binding, which has to take it, and the
+    general way."""
+    bind, taken = serve._bind(), []
+
+    class Watched:
+        def __getattr__(self, name):
+            def go(*a):
+                r = getattr(bind, name)(*a)
+                taken.append(r is not NotImplemented)
+                return r
+            return go
+
+    monkeypatch.setattr(serve, "_bind", Watched)
+    a = call()
+    assert taken == [True]
+    monkeypatch.setattr(serve, "_bind", General)
+    return a, call()
+
+
+@pytest.mark.parametrize("fmt,layout,remap", [(NV, PLAIN, True), (UE, MMA, True), (UE, MMA, False),
+                                              (MX, MMA, True), (UE32, MMA, True), (CTA, PLAIN, True)])
+@pytest.mark.parametrize("m", [None, 0, 1, 5])
+def test_binding_and_general_way_agree_on_matvec(monkeypatch, fmt, layout, remap, m):
+    w = weight(300, 512, fmt, layout, remap)
+    wide = torch.randn(m or 1, 600, generator=gen(30)).to(BF).cuda()[:m, 8:520]
+    x = wide[0] if m is None else wide
+    for dtype in (None, BF, HF, F32):
+        a, b = both_ways(monkeypatch, lambda: fq.matvec(x, w, out_dtype=dtype))
+        assert a.dtype == b.dtype and a.device == b.device and torch.equal(a, b)
+        monkeypatch.undo()
+
+
+@pytest.mark.parametrize("order", ["nhd", "hnd"])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("own_seq,with_q,rot,inter", [(True, True, 64, True), (False, True, 32, False),
+                                                      (True, False, 64, False), (False, False, 0, False)])
+def test_binding_and_general_way_agree_on_append(monkeypatch, order, dtype, own_seq, with_q, rot, inter):
+    T, page, hk, heads, dim = 6, 8, 2, 4, 64
+    table = torch.randperm(T, generator=gen(31)).view(T, 1).to(torch.int32).cuda()
+    kp, vp = cache(T, page, hk, dim, dtype, order, fill=0.0)
+    qkv = torch.randn(T, heads + 2 * hk, dim, generator=gen(32)).to(dtype).cuda()
+    pos = torch.randint(0, page, (T,), generator=gen(33)).to(torch.int32).cuda()
+    seq = torch.randperm(T, generator=gen(34)).to(torch.int32).cuda() if own_seq else None
+    rope = fq.rope_table(page, rot) if rot else None
+
+    def call():
+        kp.zero_()
+        vp.zero_()
+        q = fq.kv_append(qkv[:, heads:heads + hk], qkv[:, heads + hk:], kp, vp, table, pos, seq=seq,
+                         q=qkv[:, :heads] if with_q else None, rope=rope, interleaved=inter)
+        return q, kp.clone(), vp.clone()
+
+    (qa, ka, va), (qb, kb, vb) = both_ways(monkeypatch, call)
+    assert torch.equal(ka, kb) and torch.equal(va, vb) and ka.any() and va.any()
+    assert (qa is None and qb is None) if not with_q else torch.equal(qa, qb)
+
+
+@pytest.mark.parametrize("order", ["nhd", "hnd"])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("lengths", [[0, 1, 70], [3000], [700, 2, 0, 1500]])
+@pytest.mark.parametrize("scale,window", [(None, 0), (0.25, 0), (1, 100)])
+def test_binding_and_general_way_agree_on_attention(monkeypatch, order, dtype, lengths, scale, window):
+    kp, vp, table = pool(lengths, 16, 2, 64, dtype, order)
+    q = torch.randn(len(lengths), 3, 6, 64, generator=gen(35)).to(dtype).cuda()[:, 1]
+    ln = torch.tensor(lengths, dtype=torch.int32).cuda()
+    a, b = both_ways(monkeypatch, lambda: fq.decode_attention(q, kp, vp, table, ln, scale=scale, window=window))
+    assert torch.equal(a, b)
+
+
+def test_refusals_of_cuda_tensors():
+    """What does not fit is named the same through either way in."""
+    w = weight(64, 128, NV, PLAIN)
+    x = torch.zeros(2, 128, dtype=BF, device="cuda")
+    for bad, why in ((x.float(), "bfloat16"), (x[:, :64], "columns"), (x[None], r"\[K\]"),
+                     (x.cpu(), "device"), (x.t().contiguous().t(), "contiguous")):
+        with pytest.raises(ValueError, match=why):
+            fq.matvec(bad, w)
+    with pytest.raises(ValueError, match="out_dtype"):
+        fq.matvec(x, w, out_dtype=torch.int32)
+    short = fq.Quantized(w.q, w.sf[:-1], w.s_dec, None, w.format, w.sf_layout)
+    with pytest.raises(ValueError, match="scales"):
+        fq.matvec(x, short)
+    kp, vp, table = pool([20, 5], 16, 2, 64, BF)
+    k, q = (torch.zeros(2, h, 64, dtype=BF, device="cuda") for h in (2, 4))
+    ln = torch.tensor([20, 5], dtype=torch.int32).cuda()
+    for args, why in (((q[:, :3], kp, vp, table, ln), "multiple"), ((q[:1], kp, vp, table, ln), "q must be"),
+                      ((q, kp, vp, table, ln.long()), "int32"), ((q, kp, vp.half(), table, ln), "bfloat16"),
+                      ((q, kp, vp, table.cpu(), ln), "device"), ((q, kp, vp, table.long(), ln), "int32"),
+                      ((q.half(), kp, vp, table, ln), "dtype")):
+        with pytest.raises(ValueError, match=why):
+            fq.decode_attention(*args)
+    with pytest.raises(ValueError, match="window"):
+        fq.decode_attention(q, kp, vp, table, ln, window=-1)
+    for args, kw, why in (((k[:, :1], k, kp, vp, table, ln), {}, "k must be"),
+                          ((k, k.half(), kp, vp, table, ln), {}, "dtype"),
+                          ((k, k, kp, vp, table, ln[:1]), {}, "int32"),
+                          ((k, k, kp, vp, table[:1], ln), {}, "sequences"),
+                          ((k, k, kp, vp, table, ln), dict(q=q[:, :3]), "multiple"),
+                          ((k, k, kp, vp, table, ln), dict(rope=torch.zeros(4, 64).cuda().half()), "float32")):
+        with pytest.raises(ValueError, match=why):
+            fq.kv_append(*args, **kw)
+    assert fq.fp4_status_sync() == fq.FP4_OK
