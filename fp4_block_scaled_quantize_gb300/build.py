@@ -4,8 +4,9 @@ Each CUDA translation unit is compiled in parallel into _build/, then linked
 into fp4_block_scaled_quantize_gb300/_lib/libfp4gb300.so.  The quantizer
 units are built with -fmad=false so no multiply-add is contracted into an FMA
 (their arithmetic is specified as separately rounded binary32 operations).
-csrc/bind.c, the serving calls' short way from Python into the library,
-becomes _lib/_bind.so beside it (gcc, the running interpreter's headers).
+csrc/bind.cpp, the serving calls' short way from Python into the library,
+becomes _lib/_bind.so beside it (g++, the headers of the running interpreter
+and its torch); it compiles while the CUDA units do.
 """
 import os
 import shutil
@@ -46,6 +47,16 @@ def nvcc():
     return cand
 
 
+def cxx():
+    return os.environ.get("CXX") or shutil.which("g++") or "c++"
+
+
+def _torch():
+    """The folder of the running interpreter's torch."""
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
 def _stale(obj, deps):
     if not os.path.exists(obj):
         return True
@@ -58,7 +69,7 @@ def build(force=False, verbose=False, extra=()):
     os.makedirs(LIBDIR, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")]
     headers.append(os.path.join(INCLUDE, "fp4.h"))
-    procs, objs = [], []
+    procs, host, objs = [], [], []
     for unit, flags in UNITS.items():
         src = os.path.join(CSRC, unit)
         obj = os.path.join(BUILD, unit.replace(".cu", ".o"))
@@ -69,25 +80,31 @@ def build(force=False, verbose=False, extra=()):
                 cmd.insert(1, "-Xptxas=-v")
             procs.append((unit, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                  stderr=subprocess.STDOUT, text=True)))
+    bind, bind_obj = os.path.join(CSRC, "bind.cpp"), os.path.join(BUILD, "bind.o")
+    if force or _stale(bind_obj, [bind, os.path.join(INCLUDE, "fp4.h")]):
+        host.append(("bind.cpp", subprocess.Popen(
+            [cxx(), "-O2", "-Wall", "-std=c++17", "-fPIC", "-I" + INCLUDE,
+             "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(_torch(), "include"),
+             "-isystem", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
+             "-c", bind, "-o", bind_obj], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     failed = []
-    for unit, p in procs:
+    for unit, p in procs + host:
         out, _ = p.communicate()
         if verbose or p.returncode:
             sys.stdout.write(out)
         if p.returncode:
             failed.append(unit)
     if failed:
-        raise RuntimeError("nvcc failed for " + ", ".join(failed))
+        raise RuntimeError("compilation failed for " + ", ".join(failed))
     if force or procs or not os.path.exists(LIB) or _stale(LIB, objs):
         tmp = LIB + ".tmp"
         subprocess.run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs, check=True)
         os.replace(tmp, LIB)
-    bind = os.path.join(CSRC, "bind.c")
-    if force or _stale(BIND, [bind, LIB] + headers):
+    if force or _stale(BIND, [bind_obj, LIB]):
         tmp = BIND + ".tmp"
-        subprocess.run([os.environ.get("CC") or shutil.which("gcc") or "cc", "-O2", "-Wall", "-shared",
-                        "-fPIC", "-I" + INCLUDE, "-I" + sysconfig.get_paths()["include"], bind, "-o",
-                        tmp, "-L" + LIBDIR, "-lfp4gb300", "-Wl,-rpath,$ORIGIN", "-lm"], check=True)
+        subprocess.run([cxx(), "-shared", bind_obj, "-o", tmp, "-L" + LIBDIR, "-lfp4gb300",
+                        "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(_torch(), "lib"), "-lc10",
+                        "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], check=True)
         os.replace(tmp, BIND)
     return LIB
 

@@ -96,9 +96,7 @@ def _bind():
         "_bind", path, loader=importlib.machinery.ExtensionFileLoader("_bind", path))
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
-    m.setup(torch.Tensor, (torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8,
-                           torch.int8), torch.empty, torch._C._cuda_getCurrentRawStream,
-            torch._C._cuda_getDevice, FP4Error)
+    m.setup(FP4Error)
     return m
 
 
