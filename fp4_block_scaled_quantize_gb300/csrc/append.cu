@@ -14,9 +14,9 @@
 // for before its stores; the next token's place is looked up meanwhile.  Rows
 // whose pointers, strides or sizes are not whole 16-byte pieces go by single
 // elements.
-// Measured: 8191 tokens, 32 + 2 x 8 heads of 128, BF16: 36.6 us (5.5 TB/s, 82%
-// of a copy's rate; 41 us with four CTAs an SM, 46 without looking ahead); one
-// token 2.7 us in a graph.
+// Measured: 8191 tokens, 32 + 2 x 8 heads of 128, BF16: 34.4 us (5.9 TB/s, 87%
+// of a copy's rate; 36.6 as an ordinary launch, then 41 with four CTAs an SM
+// and 46 without looking ahead); one token 2.3 us in a graph.
 #include "serve.cuh"
 
 namespace fp4 {
@@ -42,13 +42,13 @@ __device__ __forceinline__ bool locate(const fp4_append_params &p, int64_t t, in
   page = 0;
   place = 0;
   if (pos < 0) return false;
-  const int64_t seq = p.seq ? __ldg(p.seq + t) : t;
+  const int64_t seq = p.seq ? p.seq[t] : t;
   bool ok = seq >= 0 && seq < c.seqs && pos < c.seq_pages * c.page_size &&
             (p.rot_dim == 0 || pos < p.rope_len);
   if (ok) {
     const int e = pos / c.page_size;
     place = pos - e * c.page_size;
-    page = __ldg(c.table + seq * c.table_stride + e);
+    page = c.table[seq * c.table_stride + e];
     ok = page >= 0 && page < c.pages;
   }
   if (!ok && status) raise_status(status, kStatusIndex);
@@ -142,13 +142,15 @@ __global__ void __launch_bounds__(kThreads, kResident) k_append16(const __grid_c
   constexpr int kBatch = 3;  // rows requested together
   const int stride = a.lanes * a.splits;
   uint32_t *const status = in == 0 && split == 0 ? a.status : nullptr;
+  dependent_wait();
+  launch_dependents();
   int t = (int)(blockIdx.x / a.splits) * a.tokens + tl;  // below 2^31, and so is t + hop
-  int next_pos = t < tokens ? __ldg(p.pos + t) : -1, next_place = 0, next_page = 0;
+  int next_pos = t < tokens ? p.pos[t] : -1, next_place = 0, next_page = 0;
   bool next_keep = t < tokens && locate(p, t, next_pos, status, next_page, next_place);
   for (; t < tokens; t += hop) {
     const int pos = next_pos, place = next_place, page = next_page;
     const bool keep = next_keep, more = t + hop < tokens;
-    next_pos = more ? __ldg(p.pos + t + hop) : -1;
+    next_pos = more ? p.pos[t + hop] : -1;
     __align__(16) float co[8], si[8];
     for (int r0 = split * a.lanes + lane, first = 1; r0 < rows; r0 += kBatch * stride, first = 0) {
       uint4 x[kBatch], y[kBatch];
@@ -167,8 +169,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_append16(const __grid_c
 #pragma unroll
           for (int i = 0; i < 8; i += 4) {
             if (i == 4 && !rot2) continue;
-            *reinterpret_cast<float4 *>(co + i) = __ldg(reinterpret_cast<const float4 *>(cs + i));
-            *reinterpret_cast<float4 *>(si + i) = __ldg(reinterpret_cast<const float4 *>(cs + half + i));
+            *reinterpret_cast<float4 *>(co + i) = *reinterpret_cast<const float4 *>(cs + i);
+            *reinterpret_cast<float4 *>(si + i) = *reinterpret_cast<const float4 *>(cs + half + i);
           }
         }
         next_keep = more && locate(p, t + hop, next_pos, status, next_page, next_place);
@@ -201,8 +203,10 @@ __global__ void __launch_bounds__(kThreads) k_append1(const __grid_constant__ Ap
   const fp4_append_params &p = a.p;
   const int D = p.cache.head_dim, half = p.rot_dim / 2, units = D - half;  // pairs, then single elements
   const int heads = p.q ? p.heads : 0, rows = heads + 2 * p.cache.kv_heads;
+  dependent_wait();
+  launch_dependents();
   for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-    const int pos = __ldg(p.pos + t);
+    const int pos = p.pos[t];
     int place, page;
     const bool keep = locate(p, t, pos, threadIdx.x == 0 ? a.status : nullptr, page, place);
     const float *cs = p.rope + (int64_t)(keep ? pos : 0) * p.rot_dim;
@@ -245,8 +249,7 @@ fp4_status launch_append(ApParams &a, cudaStream_t s) {
   const int64_t most = kResident * (int64_t)sm_count();  // CTAs resident at once
   if (!whole) {
     const unsigned grid = (unsigned)(p.tokens < 65535 ? p.tokens : 65535);
-    k_append1<T><<<grid, kThreads, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
+    return launch_dependent(k_append1<T>, dim3(grid), dim3(kThreads), 0, s, a) == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
   }
   a.units = p.interleaved ? (c.head_dim + 15) / 16 : p.rot_dim / 16 + (c.head_dim - p.rot_dim + 15) / 16;  // <= 16
   // a token's rows over the threads of a CTA, four or fewer each; what is left
@@ -261,11 +264,10 @@ fp4_status launch_append(ApParams &a, cudaStream_t s) {
   while (ctas * a.splits * 2 <= most / 2 && a.lanes * a.splits < rows) a.splits *= 2;
   const int64_t want = ctas < most / a.splits ? ctas : most / a.splits;
   const unsigned grid = (unsigned)((want < 1 ? 1 : want) * a.splits);
-  if (p.interleaved)
-    k_append16<T, true><<<grid, kThreads, 0, s>>>(a);
-  else
-    k_append16<T, false><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
+  return launch_dependent(p.interleaved ? k_append16<T, true> : k_append16<T, false>, dim3(grid), dim3(kThreads), 0, s,
+                          a) == cudaSuccess
+             ? FP4_OK
+             : FP4_ERR_CUDA;
 }
 
 }  // namespace

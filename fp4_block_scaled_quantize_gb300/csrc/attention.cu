@@ -35,7 +35,7 @@
 // Measured: 64 sequences of up to 16384 positions, 32 heads over 8 of 128,
 // BF16: 317 us (6.8 TB/s, a copy's rate); one of 131071: 87 us (91%), 3 us of
 // them the join; 96 windows of 1000, 16 heads of 64: 79 us (66%, the chain of
-// instructions of each 32 positions, with 12 warps an SM); one of 300: 9 us.
+// instructions of each 32 positions, with 12 warps an SM); one of 300: 8.5 us.
 #include <cmath>
 
 #include "serve.cuh"
@@ -97,11 +97,6 @@ struct Bf16<__nv_bfloat16> {
   static constexpr bool value = true;
 };
 
-// Lets the join be set up while this grid runs; it waits for its completion
-// (and memory) before it reads anything.
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -114,7 +109,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 }
 __device__ __forceinline__ uint4 load16(const void *p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -158,7 +153,7 @@ struct Span {
 __device__ __forceinline__ Span span_of(const AtParams &a, int s) {
   const fp4_kv_cache &c = a.p.cache;
   const int64_t room = (int64_t)c.seq_pages * c.page_size;  // fits 32 bits
-  const int given = __ldg(a.p.lengths + s);
+  const int given = a.p.lengths[s];
   Span r;
   r.len = given < 0 ? 0 : given > room ? (int)room : given;
   r.from = a.p.window && r.len > a.p.window ? r.len - a.p.window : 0;
@@ -309,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
 
   int64_t at, end, start;
   int s;
+  dependent_wait();
   launch_dependents();
   if (lane < 2) part_sh[2 * warp + lane] = make_int4(-1, 0, 0, 0);
   __syncwarp();
@@ -394,10 +390,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
         const int first = pos + 16 * u;
         page_next[u] = -1;
         if (UNITS) {
-          if (first < stop) page_next[u] = __ldg(table + (a.shift >= 0 ? first >> a.shift : first / c.page_size));
+          if (first < stop) page_next[u] = table[a.shift >= 0 ? first >> a.shift : first / c.page_size];
         } else {
           const int i = first + (lane & 15);
-          if (i >= sp.from && i < stop) page_next[u] = __ldg(table + i / c.page_size);
+          if (i >= sp.from && i < stop) page_next[u] = table[i / c.page_size];
         }
       }
     };
@@ -734,6 +730,7 @@ __global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constan
     if (THREADS == kNarrow && (begin == at || first != (int)blockIdx.x)) parts = 1;
   }
   dependent_wait();  // also where there is nothing to do: this grid ends after the main one
+  launch_dependents();
   if (parts == 1) return;
   const int kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
   const int heads = min(kCols, (kvh + 1) * a.share - head0);
@@ -822,9 +819,14 @@ fp4_status launch(AtParams a, cudaStream_t s) {
   if (rows > INT32_MAX) return FP4_ERR_SHAPE;
   a.direct = room <= kDirect;
   a.ctas = (int)(a.direct ? rows : tiles < most ? tiles : most);
+  // A CTA per row may start early.  Equal slices may not: their CTAs would be
+  // placed around those that still run, two on one SM and none on another
+  // (64 sequences of up to 16384: 435 us for 317).
+  if (a.direct)
+    return launch_dependent(kern, dim3((unsigned)a.ctas), dim3(kThreads), smem, s, a) == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
   kern<<<(unsigned)a.ctas, kThreads, smem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return FP4_ERR_CUDA;
-  if (a.direct || a.ctas < 2) return FP4_OK;
+  if (a.ctas < 2) return FP4_OK;
   const cudaError_t e =
       rows * 4 <= a.ctas
           ? launch_dependent(k_attention_join<T, DP, NT, kWide>, dim3((unsigned)rows), dim3(kWide), 0, s, a)

@@ -30,10 +30,17 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // reads what that kernel wrote it waits for its completion and memory
 // (dependent_wait, a no-op in a kernel launched normally).  Used for the
 // short kernels that follow a small predecessor (amax after the zeroing of
-// its outputs, the UE5M3 remap after its producer); for the producers and
-// GEMMs it measured no gain.
+// its outputs, the UE5M3 remap after its producer) and for the serving
+// kernels; for the producers and GEMMs it measured no gain.
 __device__ __forceinline__ void dependent_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// A kernel that calls this lets the next one on the stream, if it was launched
+// so, take up free multiprocessors.  It comes after the kernel's own
+// dependent_wait: what is older than this kernel is then complete for the next
+// one too, which has only this one to wait for.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,

@@ -136,3 +136,70 @@ def test_weights_that_do_not_fit_are_refused():
         FP4DecodeAttention(w, w, 3, 2, 16, 8)
     with pytest.raises(ValueError):
         FP4DecodeAttention(w, w, 4, 2, 16, 8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seqs,hidden,heads,hk,dim,start", [(1, 512, 8, 2, 64, 0), (7, 256, 4, 4, 64, 40),
+                                                            (2, 1024, 8, 1, 128, 900)])
+def test_calls_in_a_row_wait_for_each_other(seqs, hidden, heads, hk, dim, start):
+    """Steps issued back to back, each call reading what the one before it
+    wrote, give the bits of the same steps with a wait after every call; so do
+    the same steps from a CUDA graph."""
+    need_gpu()
+    g = torch.Generator().manual_seed(seqs)
+    w = [(torch.randn(s, generator=g) * 0.06).to(torch.bfloat16).cuda()
+         for s in (((heads + 2 * hk) * dim, hidden), (hidden, heads * dim))]
+    steps = 6
+    layer = FP4DecodeAttention(*w, heads, hk, dim, start + steps)
+    up = fq.quantize(w[1], fq.amax(w[1])[0], fq.params(format=fq.FP4_FMT_NVFP4_B16))
+    x0 = torch.randn(seqs, hidden, generator=g).to(torch.bfloat16).cuda()
+    cache = PagedCache(seqs, start + steps, hk, dim, page_size=16)
+    cache.reserve([start + steps] * seqs)
+    old = [torch.randn(cache.k.shape, generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+
+    def reset():
+        cache.k.copy_(old[0])
+        cache.v.copy_(old[1])
+        cache.lengths.fill_(start)
+
+    def run(wait):
+        x, kept = x0, []
+        for _ in range(steps):
+            # the layer's calls, one by one: each depends on the one before
+            pos = cache.lengths.clone()
+            qkv = fq.matvec(x, layer.w_qkv).view(seqs, heads + 2 * hk, dim)
+            wait()
+            q, k, v = qkv.split([heads, hk, hk], 1)
+            q = fq.kv_append(k, v, cache.k, cache.v, cache.table, pos, q=q, rope=layer.rope)
+            wait()
+            cache.lengths.add_(1)
+            a = fq.decode_attention(q, cache.k, cache.v, cache.table, cache.lengths)
+            wait()
+            y = fq.matvec(a.view(seqs, -1), layer.w_o)
+            wait()
+            z = fq.matvec(a.view(seqs, -1), up, out=y)  # over what was just written
+            wait()
+            x = fq.matvec(z.view(seqs, -1)[:, :hidden], layer.w_qkv)[:, :hidden]
+            wait()
+            kept += [qkv, q, a, z, x]
+        return kept
+
+    reset()
+    want = run(torch.cuda.synchronize)
+    for _ in range(10):
+        reset()
+        got = run(lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        reset()
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            got = run(lambda: None)
+    for _ in range(5):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.isfinite(t).all() for t in want)
