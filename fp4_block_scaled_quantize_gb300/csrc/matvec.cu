@@ -60,7 +60,6 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kStep = 256;             // columns a step
-constexpr int kWords = 512;            // scale bytes of a stage
 constexpr int kMaxDepth = 4;
 constexpr int kMaxSmem = 227 * 1024;
 
@@ -127,9 +126,9 @@ __device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0)
-               : "memory");
+// Four bytes, of which the first `bytes` are read and the rest zero.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, bool on) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0)
@@ -158,12 +157,16 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 //   kBoxed: plain rows with a pitch of whole 16 bytes: one box of the rows x
 //     16 bytes (with 32-element blocks the 16 bytes that hold the step's 8);
 //     word i of a lane at 128 i + 4 lane (row g + 8 i, word t).
-//   kPieces, kBytes: plain rows of any other pitch, the same place, by 4-byte
-//     cp.async or byte loads.
-enum Words { kTiled = 0, kBoxed = 1, kPieces = 2, kBytes = 3 };
+//   kPieces: plain rows of any other pitch, by 4-byte cp.async: the whole words
+//     that a row's bytes lie in, in the same places.  Where rows do not begin
+//     with words, a lane's codes are cut out of two words as they are read,
+//     and each row has one word more from 512 on.  (30000 x 2064, 1 token: 19.5
+//     us; with byte loads, which a fill waited for, 35.1.)
+enum Words { kTiled = 0, kBoxed = 1, kPieces = 2 };
 // A kernel's MODE is kTiled or kBoxed with the payload by TMA, or kAny: what
 // the parameters say.
 constexpr int kAny = 2;
+constexpr int words_of(int mode) { return mode == kAny ? 640 : 512; }  // scale bytes of a stage
 
 // Fills a warp's stages one after the other.
 template <int BLOCK, int MODE, int kRows>
@@ -206,37 +209,34 @@ struct Loader {
     ++step;
     if (MODE != kAny) return;
     if (!tma) {
-      // 16 pieces of 8 bytes a row; lane: piece lane % 16 of every other row
-      const int64_t at = (int64_t)(step - 1) * (kStep / 2) + (lane & 15) * 8;
-#pragma unroll 4
+      // 16 pieces of 8 bytes a row; lane: piece lane % 16 of every other row,
+      // in the swizzled place the TMA would use
+      const int half = (int)(j.K / 2), odd = lane >> 4, at = (step - 1) * (kStep / 2) + (lane & 15) * 8;
+      const int rows = at < half ? (int)max((int64_t)0, min(j.N - row0 - odd, (int64_t)1024)) : 0;
+      const uint8_t *from = j.q + (rows ? (int64_t)(row0 + odd) * half + at : 0);
+      const uint32_t to = payload + odd * 128 + (lane & 1) * 8;
+#pragma unroll
       for (int i = 0; i < kRows / 2; ++i) {
-        const int r = 2 * i + (lane >> 4);
-        const int64_t n = (int64_t)row0 + (tiled ? 32 * (r >> 3) + (r & 7) : r);
-        const bool on = n < j.N && at < j.K / 2;
-        const int c16 = (lane & 15) >> 1;  // in the swizzled place the TMA would use
-        cp_async8(payload + r * 128 + ((c16 ^ (r & 7)) << 4) + (lane & 1) * 8,
-                  j.q + (on ? n * (j.K / 2) + at : 0), on);
+        const int r = tiled ? 32 * (i >> 2) + 2 * (i & 3) : 2 * i;  // and `odd`
+        const bool on = r < rows;
+        cp_async8(to + 256 * i + ((((lane & 15) >> 1) ^ odd ^ (2 * (i & 3))) << 4), from + (on ? r * half : 0), on);
       }
     }
     if (mode > kBoxed) {
-      const int g = lane >> 2, t = lane & 3;
-      const int blocks = (int)(j.K / BLOCK), first = (step - 1) * kPer + (BLOCK == 16 ? 4 * t : 2 * (t & 2));
+      // offsets from the tile's first row, whose place is a multiple of 16; a
+      // row's first word may begin in the row before
+      const int blocks = (int)(j.K / BLOCK), first = (step - 1) * kPer;
+      const int64_t begin = (int64_t)row0 * blocks;
+      const int left = (int)max((int64_t)0, min(j.N * blocks - begin, (int64_t)kRows * blocks + 64));
+      const uint8_t *from = j.sf + (left ? begin : 0);
+      auto copy = [&](uint32_t dst, int at) {
+        const int bytes = min(max(left - at, 0), 4);
+        cp_async4(dst, from + (bytes ? at : 0), bytes);
+      };
+      int at = ((lane >> 2) * blocks & ~3) + first + (BLOCK == 16 ? 4 * (lane & 3) : 2 * (lane & 2));
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        const int64_t n = (int64_t)row0 + g + 8 * i;
-        const bool on = n < j.N && first < blocks;
-        const uint8_t *from = j.sf + (on ? n * blocks + first : 0);
-        const uint32_t dst = words + 128 * i + 4 * lane;
-        if (mode == kPieces) {
-          cp_async4(dst, from, on);
-        } else {
-          uint32_t w = 0;
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            if (on && first + b < blocks) w |= (uint32_t)from[b] << (8 * b);
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(w) : "memory");
-        }
-      }
+      for (int i = 0; i < kGroups; ++i, at += 8 * blocks) copy(words + 128 * i + 4 * lane, at);
+      if ((blocks & 3) && lane < kRows) copy(words + 512 + 4 * lane, (lane * blocks & ~3) + first + kPer);
     }
     if (!tma || mode > kBoxed) cp_async_arrive(bar);
   }
@@ -354,9 +354,9 @@ __device__ void prepare_x(const MatvecJob &j, int64_t m0, int M, int s0, int n, 
 template <int KIND, int BLOCK, int MODE, typename TX, int NT>
 __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_constant__ MvParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int kCols = 8 * NT, kRows = rows_of(NT), kPayload = payload_of(NT);
+  constexpr int kCols = 8 * NT, kRows = rows_of(NT), kPayload = payload_of(NT), kWords = words_of(MODE);
   constexpr int kPairs = kRows / 16, kGroups = kRows / 8;  // MMA row tiles; rows of a lane
-  const int kWarps = p.warps, kThreads = 32 * p.warps;
+  const int kWarps = p.warps;
   const MatvecJob &j = p.j;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int S = p.S, sk = p.sk, depth = p.depth;
@@ -420,6 +420,22 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
   for (int b = 0; b < NT; ++b) xl[b] = xs + min(8 * b + g, M - 1) * pitch + t * 16;  // columns past M repeat
 
   const int at0 = ((2 * t) ^ g) << 4;  // the lane's pieces of a row: at0, at0 ^ 16, then 1024 on
+  // kPieces: whether rows begin inside words, where a lane's codes begin in
+  // their first word (a tile's first row begins with one), the place of the
+  // second, and the bytes inside K
+  bool cut = false;
+  int bit = 0, next_at = 0, next_hop = 0;
+  uint32_t inside = ~0u;
+  if (MODE == kAny) {
+    const int blocks = (int)(j.K / BLOCK), own = BLOCK == 16 ? t : t >> 1;
+    const int left = blocks - (p.steps - 1) * (kStep / BLOCK) - 4 * own;
+    const bool last = own == kStep / BLOCK / 4 - 1;
+    cut = blocks & 3;
+    bit = 8 * (g * blocks & 3);
+    next_at = last ? 512 + 4 * g : 4 * lane + (BLOCK == 16 ? 4 : 8);
+    next_hop = last ? 32 : 128;
+    inside = left >= 4 ? ~0u : left > 0 ? (1u << (8 * left)) - 1 : 0u;
+  }
   int slot = 0;
   uint32_t phase = 0;
   bool live = true;  // false once a wait ran out: no more loads, results void
@@ -451,6 +467,17 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
         const int o = BLOCK == 32 && (MODE == kBoxed || (MODE == kAny && p.words == kBoxed)) ? (4 * g + (t >> 1) + 2 * (st & 1)) * 4 : lane * 4;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) codes[i] = *reinterpret_cast<const uint32_t *>(wl + 128 * i + o);
+        if (MODE == kAny && p.words == kPieces) {
+          if (cut) {
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+              codes[i] = __funnelshift_r(codes[i], *reinterpret_cast<const uint32_t *>(wl + next_at + next_hop * i), bit);
+          }
+          if (st == p.steps - 1) {  // a next row's codes would meet zeros, but may be NaN
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) codes[i] &= inside;
+          }
+        }
       }
       float f[kGroups];
       int top[kGroups] = {};
@@ -614,9 +641,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
 }
 
 // Shared memory for M tokens over ceil(steps / S) steps, NT column tiles.
-size_t smem_bytes(int M, int steps, int S, int nt, int warps, int depth) {
+size_t smem_bytes(int M, int steps, int S, int nt, int words, int warps, int depth) {
   const size_t span = (steps + S - 1) / S;
-  return (size_t)warps * depth * (payload_of(nt) + kWords) + warps * kMaxDepth * 8 + span * 8 * nt * 4 +
+  return (size_t)warps * depth * (payload_of(nt) + words) + warps * kMaxDepth * 8 + span * 8 * nt * 4 +
          warps * rows_of(nt) * 8 * nt * 4 + M * (span * 512 + 64) + 16;
 }
 
@@ -680,7 +707,7 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   p.tiles = (int)(128 / rows_of(NT) * ceil_div(j.N, 128));
   p.mc = (int)(j.M < 8 * NT ? j.M : 8 * NT);
   const int64_t row_words = j.K / j.block;
-  p.words = j.sf_mma ? kTiled : row_words % 16 == 0 ? kBoxed : row_words % 4 == 0 ? kPieces : kBytes;
+  p.words = j.sf_mma ? kTiled : row_words % 16 == 0 ? kBoxed : kPieces;
   p.status = status_word();
   if (!p.status) return FP4_ERR_CUDA;
   const bool tiled = p.words == kTiled;
@@ -699,7 +726,7 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   // 4, 1: 20.5.  Tokens are halved until something fits.
   int64_t best = INT64_MAX;
   auto fits = [&](int S, int warps, int depth) {
-    return smem_bytes(p.mc, p.steps, S, NT, warps, depth) <= (size_t)kMaxSmem;
+    return smem_bytes(p.mc, p.steps, S, NT, words_of(MODE), warps, depth) <= (size_t)kMaxSmem;
   };
   while (best == INT64_MAX) {
     for (int S = 1; S <= 8 && S <= p.steps; S *= 2) {
@@ -732,7 +759,7 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   }
   p.depth = 2;
   while (p.depth < kMaxDepth && fits(p.S, p.warps, p.depth + 1)) ++p.depth;
-  const size_t smem = smem_bytes(p.mc, p.steps, p.S, NT, p.warps, p.depth);
+  const size_t smem = smem_bytes(p.mc, p.steps, p.S, NT, words_of(MODE), p.warps, p.depth);
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(32 * p.warps);
   cfg.dynamicSmemBytes = smem;

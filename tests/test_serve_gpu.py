@@ -122,6 +122,23 @@ def test_matvec_every_code(fmt, layout):
     check_matvec(x, w, F32)
 
 
+@pytest.mark.parametrize("fmt,code", [(NV, 0x7F), (UE, 0xFF), (MX, 0xFE), (UE32, 0xFF)])
+@pytest.mark.parametrize("blocks", [1, 2, 3, 5, 17, 21, 30, 129])
+@pytest.mark.parametrize("m", [2, 11])
+def test_matvec_rows_that_begin_inside_words(fmt, code, blocks, m):
+    """Plain scales of every pitch: each row has its own codes, and a row whose
+    codes are NaN (MXFP4, which has none: 2^127) changes itself alone."""
+    n, k = 75, blocks * (32 if fmt in (MX, UE32) else 16)
+    w = random_copy(n, k, fmt, PLAIN, seed=blocks)
+    x = torch.randn(m, k, generator=gen(36)).to(HF).cuda()
+    y = check_matvec(x, w, F32)
+    w.sf.view(n, blocks)[[0, 33, n - 1]] = code
+    z = fq.matvec(x, w, out_dtype=F32)
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[[0, 33, n - 1]] = True
+    assert (fmt == MX or torch.isnan(z[:, bad]).all()) and torch.equal(z[:, ~bad], y[:, ~bad])
+
+
 def test_matvec_tall_and_long():
     """Over 65535 rows, and a row longer than any shared-memory tile."""
     w = random_copy(70001, 64, NV, PLAIN)
