@@ -440,7 +440,7 @@ int64_t fp4_decode_attention_workspace(int32_t seqs, int64_t room, int32_t heads
   if (seqs < 0 || room < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || head_dim < 1 ||
       head_dim > 256 || head_dim % 8 != 0)
     return -1;
-  return seqs == 0 ? 0 : decode_attention_workspace(room, heads, kv_heads, head_dim);
+  return seqs == 0 ? 0 : decode_attention_workspace(seqs, room, heads, kv_heads, head_dim);
 }
 
 fp4_status fp4_decode_attention(const fp4_attention_params *p, void *stream) {

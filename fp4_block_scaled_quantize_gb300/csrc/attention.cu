@@ -31,11 +31,14 @@
 // it holds of others (at most two) is joined with the neighbours' in shared
 // memory, and a CTA leaves at most two partial rows (m, l, O) in the
 // workspace.  A second, dependent launch joins those in CTA order, so results
-// repeat exactly.
+// repeat exactly.  Short rows go to clusters instead, which join in their
+// shared memory (cluster_of).
 // Measured: 64 sequences of up to 16384 positions, 32 heads over 8 of 128,
 // BF16: 317 us (6.8 TB/s, a copy's rate); one of 131071: 87 us (91%), 3 us of
 // them the join; 96 windows of 1000, 16 heads of 64: 79 us (66%, the chain of
-// instructions of each 32 positions, with 12 warps an SM); one of 300: 8.5 us.
+// instructions of each 32 positions, with 12 warps an SM); one of 300: 6.5 us (by one CTA 8.5).
+#include <cooperative_groups.h>
+
 #include <cmath>
 
 #include "serve.cuh"
@@ -44,16 +47,16 @@ namespace fp4 {
 
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 // Groups of 16 positions a warp takes a step: what it keeps in flight (heads
 // of 64, 96 windows of 1000: 82 us, with one group 88; heads of 128: 329 us,
 // with two groups and two CTAs an SM 332).
 constexpr int units_of(int dp, int nt) { return dp <= 64 ? 2 : dp <= 128 && nt == 1 ? 1 : 1; }
+constexpr int tile_of(int dp, int nt) { return 16 * units_of(dp, nt); }
 constexpr int kPerSM = 5;            // CTAs per SM at most (workspace bound)
-// Positions up to which a CTA takes a whole row: no workspace and no second
-// launch (one sequence of 300: 8.9 us for 8.0 with a cut, but 5 us less on the
-// host; 16 of 512: 15.7 us for 16.9; 64 of 512: 38 us for 32).
-constexpr int kDirect = 512;
+constexpr int kCluster = 8;          // CTAs that take a row between them, at most
 constexpr float kSlack = 8.0f;       // log2 by which scores may pass the maximum in use
 
 struct AtParams {
@@ -62,7 +65,7 @@ struct AtParams {
   int share;    // heads / kv_heads
   int tile;     // positions of a tile: 16 per unit
   int ctas;     // CTAs of the main kernel
-  int direct;   // each takes one row, whole
+  int direct;   // CTAs (a cluster) that take a row between them, or 0: equal slices
   int shift;    // log2 page_size, or -1: no power of two
   int out16;    // rows of out allow 16-byte stores
   float scale2; // scale * log2 e
@@ -70,7 +73,8 @@ struct AtParams {
   uint32_t *status;
 };
 
-// Partial row: 8 NT x DP outputs, then m, l and seen (1.0 or 0.0) per head.
+// Partial row: 8 NT x DP outputs, then m, l, seen (1.0 or 0.0) and whether
+// there is one (clusters) per head.
 constexpr int slot_floats(int cols, int dp) { return cols * (dp + 3 + 1); }
 
 __device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -284,8 +288,11 @@ __device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d
   if (a.p.lse && d == 0) store_lse<T>(a, s, head, seen, j.top, j.sum);
 }
 
+// CTAs an SM holds at least, by the kernel's launch bounds.
+constexpr int per_sm(int dp, int nt) { return nt == 1 && dp <= 128 ? 3 : 2; }
+
 template <typename T, int DP, int NT, bool UNITS>
-__global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
     k_attention(const __grid_constant__ AtParams a) {
   constexpr int kCols = 8 * NT, kKey = DP / 32, kVal = DP / 64, kUnits = units_of(DP, NT);
   constexpr int kTile = 16 * kUnits;
@@ -297,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
   // outputs, [3][2 kWarps][kCols] m, l, seen, and whose they are
   constexpr int kParts = 2 * kWarps;
   float *o_sh = smem, *st_sh = smem + kParts * kCols * (DP + 8);
+  float *const part = st_sh + 3 * kParts * kCols;  // clusters: the CTA's partial row
   __shared__ int4 part_sh[kParts];  // sequence (-1: none), row, begins with it, ends with it
   const fp4_kv_cache &c = a.p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -308,12 +316,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
   launch_dependents();
   if (lane < 2) part_sh[2 * warp + lane] = make_int4(-1, 0, 0, 0);
   __syncwarp();
-  if (a.direct) {  // a CTA per row
-    s = blockIdx.x / rows;
+  const int rank = a.direct ? blockIdx.x % a.direct : 0, mine_row = a.direct ? blockIdx.x / a.direct : 0;
+  if (a.direct) {
+    s = mine_row / rows;
     start = 0;
     const int tiles = span_of(a, s).tiles;
-    at = (int64_t)(blockIdx.x - s * rows) * tiles;
-    end = at + tiles;
+    at = (int64_t)(mine_row - s * rows) * tiles;
+    end = at + (int64_t)tiles * (rank + 1) / a.direct;
+    at += (int64_t)tiles * rank / a.direct;
   } else {
     const Found f = find<kThreads>(a, rows, blockIdx.x, scan);
     s = f.seq;
@@ -327,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
   // sequences that see nothing are in no slice: their rows are written here
   for (int e = a.direct ? s : blockIdx.x; e < c.seqs; e += a.direct ? c.seqs : a.ctas) {
     const int given = a.p.lengths[e];
-    if (a.direct && blockIdx.x != s * rows) break;
+    if (a.direct && (rank || mine_row != s * rows)) break;
     if (threadIdx.x == 0 && (given < 0 || given > (int64_t)c.seq_pages * c.page_size))
       raise_status(a.status, kStatusIndex);
     if (span_of(a, e).tiles) continue;
@@ -640,19 +650,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
         }
       continue;
     }
-    const int part = 2 * warp + (tile0 == 0);  // the warp's first row, or its last
-    if (lane == 0) part_sh[part] = make_int4(s, row, tile0 == 0, tile1 == sp.tiles);
+    const int at_part = 2 * warp + (tile0 == 0);  // the warp's first row, or its last
+    if (lane == 0) part_sh[at_part] = make_int4(s, row, tile0 == 0, tile1 == sp.tiles);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int col = 8 * n + 2 * t + e;
         if (g == 0) {
-          st_sh[part * kCols + col] = m[n][e];
-          st_sh[(kParts + part) * kCols + col] = l[n][e];
-          st_sh[(2 * kParts + part) * kCols + col] = seen ? 1.0f : 0.0f;
+          st_sh[at_part * kCols + col] = m[n][e];
+          st_sh[(kParts + at_part) * kCols + col] = l[n][e];
+          st_sh[(2 * kParts + at_part) * kCols + col] = seen ? 1.0f : 0.0f;
         }
-        float *to = o_sh + (part * kCols + col) * (DP + 8);
+        float *to = o_sh + (at_part * kCols + col) * (DP + 8);
 #pragma unroll
         for (int i = 0; i < kVal; ++i) {
           *reinterpret_cast<float4 *>(to + 64 * i + 8 * g) =
@@ -667,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
   __syncthreads();
   const int4 mine = part_sh[lane % kParts];
   uint32_t there = __ballot_sync(~0u, mine.x >= 0) & ((1u << kParts) - 1);
+  bool partial = false;
   while (there) {
     const int i0 = __ffs(there) - 1;
     const int s = __shfl_sync(~0u, mine.x, i0), row = __shfl_sync(~0u, mine.y, i0);
@@ -676,7 +687,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
     there &= ~parts;
     const int kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
     const int heads = min(kCols, (kvh + 1) * a.share - head0);
-    float *slot = a.ws + (blockIdx.x * 2 + begins) * (int64_t)slot_floats(kCols, DP);
+    float *slot = a.direct ? part : a.ws + (blockIdx.x * 2 + begins) * (int64_t)slot_floats(kCols, DP);
+    partial = !whole;
     for (int item = threadIdx.x; item < heads * (DP / 8); item += kThreads) {
       const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
       if (d >= D) continue;
@@ -697,9 +709,53 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && DP <= 128 ? 3 : 2)
       float *out = slot + col * DP + d;
       *reinterpret_cast<float4 *>(out) = make_float4(j.v[0], j.v[1], j.v[2], j.v[3]);
       *reinterpret_cast<float4 *>(out + 4) = make_float4(j.v[4], j.v[5], j.v[6], j.v[7]);
-      if (d == 0) *reinterpret_cast<float4 *>(slot + kCols * DP + col * 4) = make_float4(j.top, j.sum, any, 0.0f);
+      if (d == 0) *reinterpret_cast<float4 *>(slot + kCols * DP + col * 4) = make_float4(j.top, j.sum, any, 1.0f);
     }
   }
+  if (a.direct < 2) return;
+
+  // join the cluster's partial rows, an output piece a thread, in CTA order
+  if (!partial)
+    for (int i = threadIdx.x; i < slot_floats(kCols, DP); i += kThreads)
+      part[i] = i >= kCols * DP && i % 4 == 0 ? -INFINITY : 0.0f;
+  cg::this_cluster().sync();
+  const int row = mine_row - s * rows, kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
+  const int heads = min(kCols, (kvh + 1) * a.share - head0);
+  for (int item = threadIdx.x * a.direct + rank; item < heads * (DP / 8); item += kThreads * a.direct) {
+    const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
+    if (d >= D) continue;
+    float4 st[kCluster], lo[kCluster], hi[kCluster];
+    float there = 0.0f, any = 0.0f;
+    Joined j = {};
+    j.top = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < kCluster; ++q) {
+      st[q] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+      lo[q] = hi[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (q >= a.direct) continue;
+      const float *from = cg::this_cluster().map_shared_rank(part, q);
+      st[q] = *reinterpret_cast<const float4 *>(from + kCols * DP + col * 4);
+      lo[q] = *reinterpret_cast<const float4 *>(from + col * DP + d);
+      hi[q] = *reinterpret_cast<const float4 *>(from + col * DP + d + 4);
+    }
+#pragma unroll
+    for (int q = 0; q < kCluster; ++q) {
+      j.top = fmaxf(j.top, st[q].x);
+      any = fmaxf(any, st[q].z);
+      there = fmaxf(there, st[q].w);
+    }
+    const float base = j.top == -INFINITY ? 0.0f : j.top;
+#pragma unroll
+    for (int q = 0; q < kCluster; ++q) {
+      const float w = ex2(st[q].x - base);
+      j.sum = fmaf(w, st[q].y, j.sum);
+      const float v[8] = {lo[q].x, lo[q].y, lo[q].z, lo[q].w, hi[q].x, hi[q].y, hi[q].z, hi[q].w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) j.v[e] = fmaf(w, v[e], j.v[e]);
+    }
+    if (there != 0.0f) finish<T>(a, s, head0 + col, d, j, any != 0.0f);
+  }
+  cg::this_cluster().sync();  // nobody leaves while its part may be read
 }
 
 // Joins partial rows.  Many rows are cut into few parts each: narrow CTAs, of
@@ -793,37 +849,64 @@ constexpr int dp_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 1
 // heads: their queries and sums would not fit the registers.
 constexpr int nt_of(int share, int dp) { return share > 8 && dp <= 128 ? 2 : 1; }
 
+// CTAs (a cluster) that take a row of up to `reach` positions between them,
+// joined in their shared memory: no workspace and no second launch.  0: equal
+// slices.  As many as leave a warp two tiles (one, if each has an SM to
+// itself) and are resident at once (7/8: clusters leave some places empty).  A row longer than the others keeps its
+// CTAs to itself, so slices take over where they are as fast for equal rows.
+// Measured, 32 heads over 8 of 128, us as clusters of 1, 2, 4, 8 / as slices:
+//   1 sequence    of  200:  7.7,  7.1,  6.5,  6.2 /  7.1   (1000, 8: 8.0 / 8.6; 2000, 8: 10.9 / 10.6)
+//   8 sequences   of  500: 15.1, 11.2, 10.8,   -  / 14.0   (1000, 4: 14.2 / 16.3; 2000, 4: 20.8 / 20.8)
+//   16 sequences  of  500: 15.7, 14.0,   -     -  / 16.2   (1000, 2: 20.6 / 20.9; 128, 1: 7.4, 2: 8.8)
+//   50 sequences  of  200: 13.7,   -     -     -  / 17.4   (500, 1: 23.1 / 27.2)
+// Rows that fill the GPU more than once are left to slices earlier (64
+// sequences of 512: 32 us, a CTA per row 38).
+int cluster_of(int64_t rows, int64_t reach, int dp, int nt) {
+  const int64_t sms = sm_count(), fit = sms * per_sm(dp, nt);
+  int n = 1;
+  while (n < kCluster && rows * 2 * n <= fit * 7 / 8 &&
+         (rows * 2 * n <= sms ? n : 2 * n) * kWarps * tile_of(dp, nt) < reach)
+    n *= 2;
+  const int64_t most = rows > fit ? 128 : n == kCluster ? 2048 : 384 * n;
+  return reach <= most ? n : 0;
+}
+
 template <typename T, int DP, int NT, bool UNITS>
 fp4_status launch(AtParams a, cudaStream_t s) {
   constexpr int kMaxDev = 64;
   static std::atomic<int> occupancy[kMaxDev];
   constexpr int cols = 8 * NT;
-  const size_t smem = (2 * kWarps * cols * (DP + 8) + 6 * kWarps * cols) * sizeof(float);
+  constexpr size_t smem = (2 * kWarps * cols * (DP + 8) + 6 * kWarps * cols) * sizeof(float);
+  constexpr size_t part = slot_floats(cols, DP) * sizeof(float);
   auto kern = k_attention<T, DP, NT, UNITS>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return FP4_ERR_CUDA;
   int per = occupancy[dev].load(std::memory_order_acquire);
   if (!per) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(smem + part)) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, kThreads, smem) != cudaSuccess || per < 1)
       return FP4_ERR_CUDA;
     occupancy[dev].store(per, std::memory_order_release);
   }
   const fp4_kv_cache &c = a.p.cache;
-  a.tile = 16 * units_of(DP, NT);
+  a.tile = tile_of(DP, NT);
   // no more CTAs than the table has tiles
   const int64_t rows = (int64_t)c.seqs * c.kv_heads * a.groups;
   const int64_t room = (int64_t)c.seq_pages * c.page_size;
   const int64_t most = (int64_t)sm_count() * (per < kPerSM ? per : kPerSM);
   const int64_t tiles = ceil_div(rows * ceil_div(room, a.tile), kWarps);
   if (rows > INT32_MAX) return FP4_ERR_SHAPE;
-  a.direct = room <= kDirect;
-  a.ctas = (int)(a.direct ? rows : tiles < most ? tiles : most);
-  // A CTA per row may start early.  Equal slices may not: their CTAs would be
+  a.direct = cluster_of(rows, a.p.window && a.p.window < room - 15 ? a.p.window + 15 : room, DP, NT);
+  a.ctas = (int)(a.direct ? rows * a.direct : tiles < most ? tiles : most);
+  // Rows of their own may start early.  Equal slices may not: their CTAs would be
   // placed around those that still run, two on one SM and none on another
   // (64 sequences of up to 16384: 435 us for 317).
-  if (a.direct)
-    return launch_dependent(kern, dim3((unsigned)a.ctas), dim3(kThreads), smem, s, a) == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
+  if (a.direct) {
+    const size_t bytes = smem + (a.direct > 1 ? part : 0);
+    return launch_dependent_clusters(kern, a.direct, dim3((unsigned)a.ctas), dim3(kThreads), bytes, s, a) == cudaSuccess
+               ? FP4_OK
+               : FP4_ERR_CUDA;
+  }
   kern<<<(unsigned)a.ctas, kThreads, smem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return FP4_ERR_CUDA;
   if (a.ctas < 2) return FP4_OK;
@@ -851,9 +934,9 @@ fp4_status launch_type(const AtParams &a, int nt, cudaStream_t s) {
 
 }  // namespace
 
-int64_t decode_attention_workspace(int64_t room, int heads, int kv_heads, int head_dim) {
-  if (room <= kDirect) return 0;
-  const int dp = dp_of(head_dim), cols = 8 * nt_of(heads / kv_heads, dp);
+int64_t decode_attention_workspace(int64_t seqs, int64_t room, int heads, int kv_heads, int head_dim) {
+  const int dp = dp_of(head_dim), nt = nt_of(heads / kv_heads, dp), cols = 8 * nt;
+  if (cluster_of(seqs * kv_heads * ceil_div(heads / kv_heads, cols), room, dp, nt)) return 0;
   return (int64_t)sm_count() * kPerSM * 2 * slot_floats(cols, dp) * sizeof(float);
 }
 

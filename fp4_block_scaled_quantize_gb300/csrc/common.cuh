@@ -42,20 +42,30 @@ __device__ __forceinline__ void dependent_wait() {
 __device__ __forceinline__ void launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// In clusters of `cluster` CTAs along x, if that is more than one.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                                    cudaStream_t s, Args... args) {
+inline cudaError_t launch_dependent_clusters(void (*kern)(KArgs...), int cluster, dim3 grid,
+                                             dim3 block, size_t smem, cudaStream_t s,
+                                             Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                    cudaStream_t s, Args... args) {
+  return launch_dependent_clusters(kern, 1, grid, block, smem, s, args...);
 }
 
 inline bool aligned16(const void *p) {
@@ -194,6 +204,6 @@ fp4_status launch_matvec(const MatvecJob &j, cudaStream_t s);
 fp4_status launch_kv_append(const fp4_append_params &p, cudaStream_t s);
 fp4_status launch_decode_attention(const fp4_attention_params &p, cudaStream_t s);
 // Bytes of partial results launch_decode_attention may write.
-int64_t decode_attention_workspace(int64_t room, int heads, int kv_heads, int head_dim);
+int64_t decode_attention_workspace(int64_t seqs, int64_t room, int heads, int kv_heads, int head_dim);
 
 }  // namespace fp4

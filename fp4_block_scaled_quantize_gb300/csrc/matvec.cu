@@ -760,26 +760,14 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
   p.depth = 2;
   while (p.depth < kMaxDepth && fits(p.S, p.warps, p.depth + 1)) ++p.depth;
   const size_t smem = smem_bytes(p.mc, p.steps, p.S, NT, words_of(MODE), p.warps, p.depth);
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(32 * p.warps);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)p.S;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.S > 1 ? 2 : 1;
   const int64_t most = (int64_t)p.mc * 65535;  // tokens a launch takes
   const size_t xe = 2, ye = j.y_type == FP4_F32 ? 4 : 2;
   for (int64_t m = 0; m < j.M; m += most) {
     p.j.M = j.M - m < most ? j.M - m : most;
     p.j.x = static_cast<const uint8_t *>(j.x) + m * j.xs * xe;
     p.j.y = static_cast<uint8_t *>(j.y) + m * j.ys * ye;
-    cfg.gridDim = dim3((unsigned)(p.clusters * p.S), (unsigned)ceil_div(p.j.M, p.mc));
-    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return FP4_ERR_CUDA;
+    const dim3 grid((unsigned)(p.clusters * p.S), (unsigned)ceil_div(p.j.M, p.mc));
+    if (launch_dependent_clusters(kern, p.S, grid, dim3(32 * p.warps), smem, s, p) != cudaSuccess) return FP4_ERR_CUDA;
   }
   return FP4_OK;
 }

@@ -422,6 +422,26 @@ def test_attention_lengths(lengths, heads, hk, dim, dtype):
     assert all(torch.equal(a, fq.decode_attention(q, kp, vp, table, ln)) for _ in range(3))
 
 
+@pytest.mark.parametrize("seqs,heads,hk,dim,dtype", [(1, 4, 1, 128, BF), (3, 8, 2, 64, HF), (24, 8, 2, 128, HF),
+                                                     (70, 6, 2, 80, BF), (5, 24, 2, 128, BF), (9, 4, 4, 256, HF),
+                                                     (260, 4, 2, 64, BF)])
+@pytest.mark.parametrize("longest", [20, 130, 300, 700, 1400, 2100])
+@pytest.mark.parametrize("window", [0, 77])
+def test_attention_rows_shared_out(seqs, heads, hk, dim, dtype, longest, window):
+    """Rows taken by one CTA, by a cluster or by equal slices, as their number
+    and the room of the table say; empty, short and full ones side by side."""
+    if seqs * longest > 60000:
+        longest = 60000 // seqs
+    g = gen(37)
+    lengths = [(0, 1, 17, longest, longest // 2)[i % 5] if i % 3 else int(torch.randint(0, longest + 1, (1,), generator=g))
+               for i in range(seqs)]
+    lengths[0] = longest
+    kp, vp, table = pool(lengths, 16, hk, dim, dtype)
+    q = torch.randn(seqs, heads, dim, generator=gen(38)).to(dtype).cuda()
+    check_attention(q, kp, vp, table, torch.tensor(lengths, dtype=torch.int32).cuda(), window=window)
+    assert fq.fp4_status_sync() == fq.FP4_OK
+
+
 def test_attention_scores_of_all_sizes():
     """A late position that outweighs all others, scores of thousands, equal
     scores, a negative scale, and a row whose scores are all minus infinity."""
