@@ -6,17 +6,19 @@
 // element; cos and sin are reused over the heads of a token), launch and three
 // dependent loads (position, page, nothing else) for a few tokens.
 //
-// Layout.  A thread owns one unit of a head -- two 16-byte pieces, in the
+// Layout.  A thread owns one unit of a head -- two pieces of 16 bytes, in the
 // rotated part the two whose elements form pairs (i, i + rot_dim / 2) -- for
 // one token, and walks over the token's query, key and value heads with cos
 // and sin held in registers; neighbours touch neighbouring pieces of a row.
 // Three rows are requested together and nothing of a token's place is waited
 // for before its stores; the next token's place is looked up meanwhile.  Rows
-// whose pointers, strides or sizes are not whole 16-byte pieces go by single
+// whose pointers, strides or sizes are not whole pieces of 16 bytes (half of
+// an odd number of eights rotated, say) go by pieces of 8, the rest by single
 // elements.
 // Measured: 8191 tokens, 32 + 2 x 8 heads of 128, BF16: 34.4 us (5.9 TB/s, 87%
 // of a copy's rate; 36.6 as an ordinary launch, then 41 with four CTAs an SM
-// and 46 without looking ahead); one token 2.3 us in a graph.
+// and 46 without looking ahead); one token 2.3 us in a graph.  8000 tokens, 48
+// heads of 80 with 40 rotated: 42 us by pieces of 8 bytes, 98 by elements.
 #include "serve.cuh"
 
 namespace fp4 {
@@ -94,41 +96,41 @@ struct Pair<__half> {
   }
 };
 
-__device__ __forceinline__ uint4 load16(const void *p) { return *static_cast<const uint4 *>(p); }
 
 // Pieces of eight elements turned: pairs of one element of each piece, or
 // pairs of neighbours within a piece.
-template <typename T>
-__device__ __forceinline__ void turn_halves(uint4 &x, uint4 &y, const float *co, const float *si) {
+template <typename T, typename V>
+__device__ __forceinline__ void turn_halves(V &x, V &y, const float *co, const float *si) {
   uint32_t *a = reinterpret_cast<uint32_t *>(&x), *b = reinterpret_cast<uint32_t *>(&y);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < (int)sizeof(V) / 4; ++i) {
     const float2 u = Pair<T>::get(a[i]), v = Pair<T>::get(b[i]);
     const float c0 = co[2 * i], c1 = co[2 * i + 1], s0 = si[2 * i], s1 = si[2 * i + 1];
     a[i] = Pair<T>::put(u.x * c0 - v.x * s0, u.y * c1 - v.y * s1);
     b[i] = Pair<T>::put(v.x * c0 + u.x * s0, v.y * c1 + u.y * s1);
   }
 }
-template <typename T>
-__device__ __forceinline__ void turn_pairs(uint4 &x, const float *co, const float *si) {
+template <typename T, typename V>
+__device__ __forceinline__ void turn_pairs(V &x, const float *co, const float *si) {
   uint32_t *a = reinterpret_cast<uint32_t *>(&x);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < (int)sizeof(V) / 4; ++i) {
     const float2 u = Pair<T>::get(a[i]);
     a[i] = Pair<T>::put(u.x * co[i] - u.y * si[i], u.y * co[i] + u.x * si[i]);
   }
 }
 
-// Whole 16-byte pieces, two a unit: with halves the pieces 8 u and rot_dim / 2
-// + 8 u of the rotated part, else 16 consecutive elements (the last unit may
-// hold one piece).  The rows are requested before anything is known of the
+// Whole pieces V of P elements (16 or 8 bytes), two a unit: with halves the
+// pieces P u and rot_dim / 2 + P u of the rotated part, else 2 P consecutive
+// elements (the last unit may hold one piece).  The rows are requested before anything is known of the
 // token's place; only their stores wait for it, and a thread's next token is
 // looked up meanwhile.
-template <typename T, bool INTER>
-__global__ void __launch_bounds__(kThreads, kResident) k_append16(const __grid_constant__ ApParams a) {
+template <typename T, bool INTER, typename V>
+__global__ void __launch_bounds__(kThreads, kResident) k_append_pieces(const __grid_constant__ ApParams a) {
+  constexpr int P = sizeof(V) / 2;
   const fp4_append_params &p = a.p;
   const int heads = p.q ? p.heads : 0, rows = heads + 2 * p.cache.kv_heads, D = p.cache.head_dim;
-  const int half = p.rot_dim / 2, turned = INTER ? 0 : p.rot_dim / 16;
+  const int half = p.rot_dim / 2, turned = INTER ? 0 : p.rot_dim / (2 * P);
   const int per = a.units * a.lanes;  // threads of a token
   const int tl = threadIdx.x / per, in = threadIdx.x - tl * per;
   const int lane = in / a.units, unit = in - lane * a.units;
@@ -136,8 +138,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_append16(const __grid_c
   const int split = blockIdx.x % a.splits;
   const int hop = (int)(gridDim.x / a.splits) * a.tokens, tokens = (int)p.tokens;
   const bool halves = unit < turned;
-  const int o1 = halves ? 8 * unit : 16 * unit + (INTER ? 0 : p.rot_dim - 16 * turned);
-  const int o2 = halves ? o1 + half : o1 + 8;
+  const int o1 = halves ? P * unit : 2 * P * unit + (INTER ? 0 : p.rot_dim - 2 * P * turned);
+  const int o2 = halves ? o1 + half : o1 + P;
   const bool two = o2 < D, rot1 = halves || (INTER && o1 < p.rot_dim), rot2 = halves || (INTER && o2 < p.rot_dim);
   constexpr int kBatch = 3;  // rows requested together
   const int stride = a.lanes * a.splits;
@@ -151,23 +153,23 @@ __global__ void __launch_bounds__(kThreads, kResident) k_append16(const __grid_c
     const int pos = next_pos, place = next_place, page = next_page;
     const bool keep = next_keep, more = t + hop < tokens;
     next_pos = more ? p.pos[t + hop] : -1;
-    __align__(16) float co[8], si[8];
+    __align__(16) float co[P], si[P];
     for (int r0 = split * a.lanes + lane, first = 1; r0 < rows; r0 += kBatch * stride, first = 0) {
-      uint4 x[kBatch], y[kBatch];
+      V x[kBatch], y[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        x[i] = y[i] = make_uint4(0, 0, 0, 0);
+        x[i] = y[i] = V{};
         const int r = r0 + i * stride;
         if (r >= rows) continue;
         const T *src = source<T>(p, t, r, heads);
-        x[i] = load16(src + o1);
-        if (two) y[i] = load16(src + o2);
+        x[i] = *reinterpret_cast<const V *>(src + o1);
+        if (two) y[i] = *reinterpret_cast<const V *>(src + o2);
       }
       if (first) {
         if (keep && (rot1 || rot2)) {
-          const float *cs = p.rope + (int64_t)pos * p.rot_dim + 8 * unit;
+          const float *cs = p.rope + (int64_t)pos * p.rot_dim + P * unit;
 #pragma unroll
-          for (int i = 0; i < 8; i += 4) {
+          for (int i = 0; i < P; i += 4) {
             if (i == 4 && !rot2) continue;
             *reinterpret_cast<float4 *>(co + i) = *reinterpret_cast<const float4 *>(cs + i);
             *reinterpret_cast<float4 *>(si + i) = *reinterpret_cast<const float4 *>(cs + half + i);
@@ -180,18 +182,18 @@ __global__ void __launch_bounds__(kThreads, kResident) k_append16(const __grid_c
         const int r = r0 + i * stride;
         if (r >= rows || (!keep && r >= heads)) continue;
         if (!keep) {
-          x[i] = y[i] = make_uint4(0, 0, 0, 0);
+          x[i] = y[i] = V{};
         } else if (r < heads + p.cache.kv_heads) {
           if (halves) {
             turn_halves<T>(x[i], y[i], co, si);
           } else {
             if (rot1) turn_pairs<T>(x[i], co, si);
-            if (rot2) turn_pairs<T>(y[i], co + 4, si + 4);
+            if (rot2) turn_pairs<T>(y[i], co + P / 2, si + P / 2);
           }
         }
         T *dst = target<T>(p, t, r, heads, page, place);
-        *reinterpret_cast<uint4 *>(dst + o1) = x[i];
-        if (two) *reinterpret_cast<uint4 *>(dst + o2) = y[i];
+        *reinterpret_cast<V *>(dst + o1) = x[i];
+        if (two) *reinterpret_cast<V *>(dst + o2) = y[i];
       }
     }
   }
@@ -234,24 +236,27 @@ __global__ void __launch_bounds__(kThreads) k_append1(const __grid_constant__ Ap
   }
 }
 
-bool whole16(const void *ptr, int64_t s0, int64_t s1) { return aligned16(ptr) && s0 % 8 == 0 && s1 % 8 == 0; }
+// Whether rows at this address, so many elements apart, are whole pieces of P.
+bool whole(int P, const void *ptr, int64_t s0, int64_t s1) {
+  return reinterpret_cast<uintptr_t>(ptr) % (2 * P) == 0 && s0 % P == 0 && s1 % P == 0;
+}
+bool whole(int P, const fp4_append_params &p) {
+  const fp4_kv_cache &c = p.cache;
+  return c.head_dim % P == 0 && p.rot_dim % (p.interleaved ? 8 : 2 * P) == 0 && whole(P, p.k, p.k_token, p.k_head) &&
+         whole(P, p.v, p.v_token, p.v_head) && whole(P, c.k, c.k_page, c.k_place) && whole(P, c.v, c.v_page, c.v_place) &&
+         c.k_head % P == 0 && c.v_head % P == 0 && aligned16(p.rope) &&
+         (!p.q || (whole(P, p.q, p.q_token, p.q_head) && whole(P, p.q_out, p.qo_token, p.qo_head)));
+}
 
-template <typename T>
-fp4_status launch_append(ApParams &a, cudaStream_t s) {
+template <typename T, typename V>
+fp4_status launch_pieces(ApParams &a, cudaStream_t s) {
+  constexpr int P = sizeof(V) / 2;
   const fp4_append_params &p = a.p;
   const fp4_kv_cache &c = p.cache;
-  const int heads = p.q ? p.heads : 0, rows = heads + 2 * c.kv_heads;
-  const bool whole = c.head_dim % 8 == 0 && p.rot_dim % (p.interleaved ? 8 : 16) == 0 &&
-                     whole16(p.k, p.k_token, p.k_head) && whole16(p.v, p.v_token, p.v_head) &&
-                     whole16(c.k, c.k_page, c.k_place) && whole16(c.v, c.v_page, c.v_place) &&
-                     c.k_head % 8 == 0 && c.v_head % 8 == 0 && aligned16(p.rope) &&
-                     (!p.q || (whole16(p.q, p.q_token, p.q_head) && whole16(p.q_out, p.qo_token, p.qo_head)));
+  const int rows = (p.q ? p.heads : 0) + 2 * c.kv_heads;
   const int64_t most = kResident * (int64_t)sm_count();  // CTAs resident at once
-  if (!whole) {
-    const unsigned grid = (unsigned)(p.tokens < 65535 ? p.tokens : 65535);
-    return launch_dependent(k_append1<T>, dim3(grid), dim3(kThreads), 0, s, a) == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
-  }
-  a.units = p.interleaved ? (c.head_dim + 15) / 16 : p.rot_dim / 16 + (c.head_dim - p.rot_dim + 15) / 16;  // <= 16
+  const int turned = p.interleaved ? 0 : p.rot_dim / (2 * P);
+  a.units = turned + (c.head_dim - 2 * P * turned + 2 * P - 1) / (2 * P);  // <= 32
   // a token's rows over the threads of a CTA, four or fewer each; what is left
   // of the CTA takes further tokens, and where there are few tokens a token's
   // rows go to several CTAs, one or two each
@@ -263,11 +268,18 @@ fp4_status launch_append(ApParams &a, cudaStream_t s) {
   const int64_t ctas = ceil_div(p.tokens, a.tokens);
   while (ctas * a.splits * 2 <= most / 2 && a.lanes * a.splits < rows) a.splits *= 2;
   const int64_t want = ctas < most / a.splits ? ctas : most / a.splits;
-  const unsigned grid = (unsigned)((want < 1 ? 1 : want) * a.splits);
-  return launch_dependent(p.interleaved ? k_append16<T, true> : k_append16<T, false>, dim3(grid), dim3(kThreads), 0, s,
-                          a) == cudaSuccess
-             ? FP4_OK
-             : FP4_ERR_CUDA;
+  const dim3 grid((unsigned)((want < 1 ? 1 : want) * a.splits));
+  const auto kern = p.interleaved ? k_append_pieces<T, true, V> : k_append_pieces<T, false, V>;
+  return launch_dependent(kern, grid, dim3(kThreads), 0, s, a) == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
+}
+
+template <typename T>
+fp4_status launch_append(ApParams &a, cudaStream_t s) {
+  const fp4_append_params &p = a.p;
+  if (whole(8, p)) return launch_pieces<T, uint4>(a, s);
+  if (whole(4, p)) return launch_pieces<T, uint2>(a, s);
+  const unsigned grid = (unsigned)(p.tokens < 65535 ? p.tokens : 65535);
+  return launch_dependent(k_append1<T>, dim3(grid), dim3(kThreads), 0, s, a) == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
 
 }  // namespace

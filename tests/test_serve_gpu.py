@@ -302,6 +302,23 @@ def test_append_shapes(dtype, order, heads, hk, dim, rot, page, inter):
     assert fq.fp4_status_sync() == fq.FP4_OK
 
 
+@pytest.mark.parametrize("dim,rot,inter,pad", [(80, 40, False, 0), (12, 8, False, 0), (20, 16, True, 0), (20, 0, False, 4),
+                                               (64, 64, False, 4), (64, 32, True, 12), (252, 248, False, 0), (4, 0, False, 0)])
+@pytest.mark.parametrize("T", [1, 50, 2500])
+def test_append_pieces_of_eight_bytes(dim, rot, inter, pad, T):
+    """Rows that are whole pieces of 4 elements but not of 8, by size or by
+    stride."""
+    heads, hk, page = 6, 2, 16
+    pages = T // page + 2
+    table = torch.randperm(pages, generator=gen(40))[None].to(torch.int32).cuda()
+    kp, vp = (t[..., :dim] for t in cache(pages, page, hk, dim + pad, BF))
+    qkv = torch.randn(T, heads + 2 * hk, dim + pad, generator=gen(41)).to(BF).cuda()[..., :dim]
+    pos = torch.randperm(T, generator=gen(42)).to(torch.int32).cuda()
+    check_append(qkv[:, heads:heads + hk], qkv[:, heads + hk:], kp, vp, table, pos,
+                 torch.zeros(T, dtype=torch.int32).cuda(), qkv[:, :heads], fq.rope_table(T, rot) if rot else None, inter)
+    assert fq.fp4_status_sync() == fq.FP4_OK
+
+
 @pytest.mark.parametrize("T", [1, 2, 200, 3001])
 def test_append_token_counts_and_decode_form(T):
     page, hk, dim, heads = 16, 2, 128, 8
