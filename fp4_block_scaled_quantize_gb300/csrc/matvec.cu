@@ -717,13 +717,13 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
     return FP4_ERR_CUDA;
   if (p.words == kBoxed && !byte_map(&p.smap, j.sf, row_words, j.N, 0, 16, rows_of(NT), false)) return FP4_ERR_CUDA;
   // The split: of those that fit shared memory (x of a CTA's tokens over its
-  // part of K beside rings of two stages), the least estimated time, in steps
-  // of an SM: the steps of its warps, twice the longest warp's, the join (a
-  // store; a barrier with rings running dry; one over a cluster) and the
-  // preparation of x.  Measured, S, sk: 14336 x 4096, 8 tokens, 1, 4: 14.9 us,
-  // 1, 5: 15.2, 1, 16: 15.6, 2, 2: 16.1; 131072 x 4096, 16 tokens, 1, 1: 85.5,
-  // 1, 4: 92.4, 2, 1: 99.2; 4096 x 14336, 12 tokens, 4, 2: 19.0, 4, 4: 21.4,
-  // 4, 1: 20.5.  Tokens are halved until something fits.
+  // part of K beside rings of two stages), the least estimated time, in units
+  // of 30 ns: the steps of an SM, those of the longest warp one after the
+  // other, the preparation of x, and each round's join (over warps; over a
+  // cluster, by barriers that grow with it; rings run dry between rounds).  The weights are a fit to 50
+  // sizes (1 .. 24 tokens, 141 .. 32768 rows, 256 .. 15040 columns) with every
+  // split that fits: the choice takes 3% longer than the best on average, 12%
+  // at worst.  Tokens are halved until something fits.
   int64_t best = INT64_MAX;
   auto fits = [&](int S, int warps, int depth) {
     return smem_bytes(p.mc, p.steps, S, NT, words_of(MODE), warps, depth) <= (size_t)kMaxSmem;
@@ -736,13 +736,15 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
       const int room = resident(kern, residence, S, 32 * kMaxWarps);
       if (room < 1) return FP4_ERR_CUDA;
       const int64_t span = ceil_div(p.steps, S);
+      const int64_t clusters = p.tiles < room ? p.tiles : room, most = ceil_div(p.tiles, clusters);
+      const int64_t waves = ceil_div(clusters * ceil_div(j.M, p.mc), room);
       for (int sk = 1; sk <= warps && sk <= span; ++sk) {
         const int group = warps / sk;
         if (sk > 1 && sk < warps && sk < span && warps / (sk + 1) == group) continue;  // a larger one keeps as many tiles
-        const int64_t clusters = p.tiles < room ? p.tiles : room, most = ceil_div(p.tiles, clusters);
         const int64_t rounds = ceil_div(most, group);
-        const int join = sk > 1 ? 12 : 1;
-        const int64_t cost = most * span + rounds * (2 * ceil_div(span, sk) + join + (S > 1 ? 40 : 0)) + p.mc * span / 8;
+        const int join = (sk > 1 ? 10 + sk : 0) + (S > 1 ? 8 + 20 * S : 0), dry = sk > 1 || S > 1 ? 40 : 0;
+        const int64_t cost = waves * (rows_of(NT) / 4 * most * span + 4 * most + p.mc * span / 2 +
+                                      rounds * (22 * ceil_div(span, sk) + join) + (rounds - 1) * dry);
         if (cost >= best) continue;
         best = cost;
         p.S = S;
@@ -750,8 +752,11 @@ fp4_status launch(const MatvecJob &j, cudaStream_t s) {
         p.warps = warps;
         p.rounds = (int)rounds;
         p.clusters = (int)clusters;
+        // small calls: half the warps start sooner (148 x 576, 1 token: 4.0 us
+        // for 4.3), and with two rounds of tokens two CTAs fit an SM (5957 x 448,
+        // 24 tokens: 7.7 us for 11.2); large ones want them all for x and the join
+        if (most * sk <= 8 && p.mc * span <= 32) p.warps = 8;
       }
-      if (warps == kMaxWarps && S > 1) break;  // more CTAs per tile only add joins
     }
     if (best < INT64_MAX) break;
     if (p.mc == 1) return FP4_ERR_SHAPE;
