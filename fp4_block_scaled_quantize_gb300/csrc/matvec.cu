@@ -9,8 +9,8 @@
 // tokens as columns.  (tcgen05 reads its operands from shared or tensor
 // memory: 4-bit weights would have to be decoded into it first, for a 128-row
 // tile of which all but M columns of work are padding.)
-// Measured (131072 x 4096, NVFP4): 1 token 54.9 us (5.5 TB/s, 81% of a copy),
-// 8 tokens 61 us (73%), 16 tokens 84 us (54%): instruction issue, about 480
+// Measured (131072 x 4096, NVFP4): 1 token 53.4 us (5.7 TB/s, 84% of a copy),
+// 8 tokens 59.7 us (75%), 16 tokens 81 us (57%): instruction issue, about 480
 // instructions for 32 x 256 weights and 8 tokens of which 304 decode, scale
 // and multiply, at half an instruction a clock and scheduler.  4096 x 14336,
 // 1 token: 11.3 us behind another of its kind (a dependent launch: barriers and
