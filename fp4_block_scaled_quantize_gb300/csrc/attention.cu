@@ -34,9 +34,10 @@
 // repeat exactly.  Short rows go to clusters instead, which join in their
 // shared memory (cluster_of).
 // Measured: 64 sequences of up to 16384 positions, 32 heads over 8 of 128,
-// BF16: 317 us (6.8 TB/s, a copy's rate); one of 131071: 87 us (91%), 3 us of
-// them the join; 96 windows of 1000, 16 heads of 64: 79 us (66%, the chain of
-// instructions of each 32 positions, with 12 warps an SM); one of 300: 6.5 us (by one CTA 8.5).
+// BF16: 315 us (6.8 TB/s, a copy's rate); one of 131071: 87 us (91%), 3 us of
+// them the join; 96 windows of 1000, 16 heads of 64: 76 us (69%, the chain of
+// instructions of each 32 positions, with 12 warps an SM); one of 300: 6.3 us
+// (by one CTA 8.5).
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -278,6 +279,40 @@ __device__ __forceinline__ Joined join(uint32_t parts, M m, L l, Add add) {
   }
   return j;
 }
+// The same of parts held side by side: get(q, st, lo, hi) reads part q (m, l,
+// seen, 1 and the outputs) if there is one.  All are requested together.
+struct Whole {
+  Joined j;
+  bool seen, there;
+};
+template <int N, typename Get>
+__device__ __forceinline__ Whole join_all(Get get) {
+  float4 st[N], lo[N], hi[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    st[q] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    lo[q] = hi[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    get(q, st[q], lo[q], hi[q]);
+  }
+  Whole r = {};
+  r.j.top = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    r.j.top = fmaxf(r.j.top, st[q].x);
+    r.seen |= st[q].z != 0.0f;
+    r.there |= st[q].w != 0.0f;
+  }
+  const float base = r.j.top == -INFINITY ? 0.0f : r.j.top;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const float w = ex2(st[q].x - base);
+    r.j.sum = fmaf(w, st[q].y, r.j.sum);
+    const float v[8] = {lo[q].x, lo[q].y, lo[q].z, lo[q].w, hi[q].x, hi[q].y, hi[q].z, hi[q].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.j.v[e] = fmaf(w, v[e], r.j.v[e]);
+  }
+  return r;
+}
 // Writes the result of a row that saw something (seen) or nothing.
 template <typename T>
 __device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d, Joined j, bool seen) {
@@ -301,10 +336,11 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
   extern __shared__ __align__(16) float smem[];
   __shared__ int64_t scan[kWarps + 2];
   // parts of rows that a warp began or ended with: [2 kWarps][kCols][DP + 8]
-  // outputs, [3][2 kWarps][kCols] m, l, seen, and whose they are
+  // outputs, [2 kWarps][kCols] m, l, seen, 1, and whose they are
   constexpr int kParts = 2 * kWarps;
-  float *o_sh = smem, *st_sh = smem + kParts * kCols * (DP + 8);
-  float *const part = st_sh + 3 * kParts * kCols;  // clusters: the CTA's partial row
+  float *const o_sh = smem;
+  float4 *const st_sh = reinterpret_cast<float4 *>(smem + kParts * kCols * (DP + 8));
+  float *const part = reinterpret_cast<float *>(st_sh + kParts * kCols);  // clusters: the CTA's partial row
   __shared__ int4 part_sh[kParts];  // sequence (-1: none), row, begins with it, ends with it
   const fp4_kv_cache &c = a.p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -657,11 +693,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int col = 8 * n + 2 * t + e;
-        if (g == 0) {
-          st_sh[at_part * kCols + col] = m[n][e];
-          st_sh[(kParts + at_part) * kCols + col] = l[n][e];
-          st_sh[(2 * kParts + at_part) * kCols + col] = seen ? 1.0f : 0.0f;
-        }
+        if (g == 0) st_sh[at_part * kCols + col] = make_float4(m[n][e], l[n][e], seen ? 1.0f : 0.0f, 1.0f);
         float *to = o_sh + (at_part * kCols + col) * (DP + 8);
 #pragma unroll
         for (int i = 0; i < kVal; ++i) {
@@ -692,24 +724,23 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
     for (int item = threadIdx.x; item < heads * (DP / 8); item += kThreads) {
       const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
       if (d >= D) continue;
-      const Joined j = join(
-          parts, [&](int i) { return st_sh[i * kCols + col]; },
-          [&](int i) { return st_sh[(kParts + i) * kCols + col]; },
-          [&](int i, float f, float *v) {
-            const float *from = o_sh + (i * kCols + col) * (DP + 8) + d;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(f, from[e], v[e]);
-          });
-      bool any = false;
-      for (uint32_t p = parts; p; p &= p - 1) any |= st_sh[(2 * kParts + __ffs(p) - 1) * kCols + col] != 0.0f;
+      const Whole r = join_all<kParts>([&](int q, float4 &st, float4 &lo, float4 &hi) {
+        if (!(parts >> q & 1)) return;
+        const float *from = o_sh + (q * kCols + col) * (DP + 8) + d;
+        st = st_sh[q * kCols + col];
+        lo = *reinterpret_cast<const float4 *>(from);
+        hi = *reinterpret_cast<const float4 *>(from + 4);
+      });
       if (whole) {
-        finish<T>(a, s, head0 + col, d, j, any);
+        finish<T>(a, s, head0 + col, d, r.j, r.seen);
         continue;
       }
+      const float *v = r.j.v;
       float *out = slot + col * DP + d;
-      *reinterpret_cast<float4 *>(out) = make_float4(j.v[0], j.v[1], j.v[2], j.v[3]);
-      *reinterpret_cast<float4 *>(out + 4) = make_float4(j.v[4], j.v[5], j.v[6], j.v[7]);
-      if (d == 0) *reinterpret_cast<float4 *>(slot + kCols * DP + col * 4) = make_float4(j.top, j.sum, any, 1.0f);
+      *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4 *>(out + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      if (d == 0)
+        *reinterpret_cast<float4 *>(slot + kCols * DP + col * 4) = make_float4(r.j.top, r.j.sum, r.seen ? 1.0f : 0.0f, 1.0f);
     }
   }
   if (a.direct < 2) return;
@@ -724,36 +755,14 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
   for (int item = threadIdx.x * a.direct + rank; item < heads * (DP / 8); item += kThreads * a.direct) {
     const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
     if (d >= D) continue;
-    float4 st[kCluster], lo[kCluster], hi[kCluster];
-    float there = 0.0f, any = 0.0f;
-    Joined j = {};
-    j.top = -INFINITY;
-#pragma unroll
-    for (int q = 0; q < kCluster; ++q) {
-      st[q] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-      lo[q] = hi[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (q >= a.direct) continue;
+    const Whole r = join_all<kCluster>([&](int q, float4 &st, float4 &lo, float4 &hi) {
+      if (q >= a.direct) return;
       const float *from = cg::this_cluster().map_shared_rank(part, q);
-      st[q] = *reinterpret_cast<const float4 *>(from + kCols * DP + col * 4);
-      lo[q] = *reinterpret_cast<const float4 *>(from + col * DP + d);
-      hi[q] = *reinterpret_cast<const float4 *>(from + col * DP + d + 4);
-    }
-#pragma unroll
-    for (int q = 0; q < kCluster; ++q) {
-      j.top = fmaxf(j.top, st[q].x);
-      any = fmaxf(any, st[q].z);
-      there = fmaxf(there, st[q].w);
-    }
-    const float base = j.top == -INFINITY ? 0.0f : j.top;
-#pragma unroll
-    for (int q = 0; q < kCluster; ++q) {
-      const float w = ex2(st[q].x - base);
-      j.sum = fmaf(w, st[q].y, j.sum);
-      const float v[8] = {lo[q].x, lo[q].y, lo[q].z, lo[q].w, hi[q].x, hi[q].y, hi[q].z, hi[q].w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) j.v[e] = fmaf(w, v[e], j.v[e]);
-    }
-    if (there != 0.0f) finish<T>(a, s, head0 + col, d, j, any != 0.0f);
+      st = *reinterpret_cast<const float4 *>(from + kCols * DP + col * 4);
+      lo = *reinterpret_cast<const float4 *>(from + col * DP + d);
+      hi = *reinterpret_cast<const float4 *>(from + col * DP + d + 4);
+    });
+    if (r.there) finish<T>(a, s, head0 + col, d, r.j, r.seen);
   }
   cg::this_cluster().sync();  // nobody leaves while its part may be read
 }
@@ -876,7 +885,7 @@ fp4_status launch(AtParams a, cudaStream_t s) {
   constexpr int kMaxDev = 64;
   static std::atomic<int> occupancy[kMaxDev];
   constexpr int cols = 8 * NT;
-  constexpr size_t smem = (2 * kWarps * cols * (DP + 8) + 6 * kWarps * cols) * sizeof(float);
+  constexpr size_t smem = (2 * kWarps * cols * (DP + 8) + 8 * kWarps * cols) * sizeof(float);
   constexpr size_t part = slot_floats(cols, DP) * sizeof(float);
   auto kern = k_attention<T, DP, NT, UNITS>;
   int dev = 0;
