@@ -35,7 +35,7 @@
 // shared memory (cluster_of).
 // Measured: 64 sequences of up to 16384 positions, 32 heads over 8 of 128,
 // BF16: 315 us (6.8 TB/s, a copy's rate); one of 131071: 87 us (91%), 3 us of
-// them the join; 96 windows of 1000, 16 heads of 64: 76 us (69%, the chain of
+// them the join; 96 windows of 1000, 16 heads of 64: 75 - 83 us (63 - 69%, the chain of
 // instructions of each 32 positions, with 12 warps an SM); one of 300: 6.3 us
 // (by one CTA 8.5).
 #include <cooperative_groups.h>
