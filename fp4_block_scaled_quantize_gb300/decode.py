@@ -22,8 +22,9 @@ from . import (FP4_FMT_UE5M3_B16, FP4_SF_MMA, Quantized, amax, decode_attention,
 class PagedCache:
     """Keys and values of up to `seqs` sequences in `pages` pages of
     `page_size` places.  Pages are taken from a list on the host by
-    ``reserve`` and given back by ``release``; ``table`` [seqs, max_pages] and
-    ``lengths`` [seqs] (int32) live on the device."""
+    ``reserve`` and given back by ``release``; ``table`` [seqs, max_pages]
+    (-1 where a sequence has no page), ``room`` [seqs] (the positions its pages
+    hold) and ``lengths`` [seqs], all int32, live on the device."""
 
     def __init__(self, seqs, max_len, kv_heads, head_dim, pages=None, page_size=64,
                  dtype=torch.bfloat16, device="cuda"):
@@ -34,7 +35,8 @@ class PagedCache:
         shape = (pages, page_size, kv_heads, head_dim)
         self.k = torch.empty(shape, dtype=dtype, device=device)
         self.v = torch.empty(shape, dtype=dtype, device=device)
-        self.table = torch.zeros((seqs, wide), dtype=torch.int32, device=device)
+        self.table = torch.full((seqs, wide), -1, dtype=torch.int32, device=device)
+        self.room = torch.zeros(seqs, dtype=torch.int32, device=device)
         self.lengths = torch.zeros(seqs, dtype=torch.int32, device=device)
         self.page_size, self.max_len = page_size, max_len
         self._free = list(range(pages - 1, -1, -1))
@@ -57,11 +59,15 @@ class PagedCache:
             at = len(self._owned[s])
             self._owned[s] += new
             self.table[s, at:at + n] = torch.tensor(new, dtype=torch.int32)
+            self.room[s] = (at + n) * self.page_size
 
     def release(self, seq):
-        """Gives the pages of a sequence back and sets its length to zero."""
+        """Gives the pages of a sequence back, takes them out of the table and
+        sets its length to zero."""
         self._free += reversed(self._owned[seq])
         self._owned[seq] = []
+        self.table[seq] = -1
+        self.room[seq] = 0
         self.lengths[seq] = 0
 
 
@@ -101,15 +107,21 @@ class FP4DecodeAttention(torch.nn.Module):
 
     def forward(self, x, cache, pos=None):
         """One new token of every sequence: x [seqs, hidden] at positions pos
-        (default: the cache's lengths), which the cache must have pages for.
-        Returns [seqs, hidden] and advances the cache's lengths."""
+        (default: the cache's lengths).  Returns [seqs, hidden] and advances the
+        cache's lengths.  Where a sequence has no page for its position, or the
+        rotation ends before it, nothing is stored, its length stays (at most
+        the room of its pages), its row of the result means nothing and
+        fp4_status_sync reports FP4_ERR_INVALID_ARG."""
         n = x.shape[0]
-        pos = cache.lengths.clone() if pos is None else pos
+        pos = cache.lengths if pos is None else pos
+        after = pos + 1
         qkv = matvec(x, self.w_qkv).view(n, self.heads + 2 * self.kv_heads, self.head_dim)
         q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)
         q = kv_append(k, v, cache.k, cache.v, cache.table, pos, q=q, rope=self.rope,
                       interleaved=self.interleaved)
-        torch.add(pos, 1, out=cache.lengths)
+        torch.minimum(after, cache.room, out=cache.lengths)
+        if cache.table.shape[1] * cache.page_size > self.rope.shape[0]:
+            cache.lengths.clamp_(max=self.rope.shape[0])
         a = decode_attention(q, cache.k, cache.v, cache.table, cache.lengths, window=self.window)
         return matvec(a.view(n, -1), self.w_o)
 

@@ -1,0 +1,95 @@
+"""The decoding layer's cache where not every slot takes part in a step: pages
+given back, slots without pages, sequences past their pages."""
+import pytest
+import torch
+
+import fp4_block_scaled_quantize_gb300 as fq
+from fp4_block_scaled_quantize_gb300.decode import FP4DecodeAttention, PagedCache
+from gpu_util import need_gpu
+
+H, HK, D, HIDDEN, PAGE = 8, 2, 64, 256, 8
+
+
+def named(cache):
+    """The pages that each row of the table names."""
+    return [[p for p in row if p >= 0] for row in cache.table.tolist()]
+
+
+def test_no_two_rows_name_one_page():
+    c = PagedCache(4, 40, 2, 8, pages=7, page_size=16, device="cpu")
+    assert named(c) == [[], [], [], []]
+    c.reserve([32, 0, 16, 0])
+    c.release(0)
+    assert named(c)[0] == [] and int(c.lengths[0]) == 0
+    c.reserve([0, 40, 16, 40])
+    assert named(c) == c._owned
+    pages = sum(named(c), [])
+    assert len(pages) == len(set(pages)) == 7
+    c.release(1)
+    c.reserve([1, 0, 33, 40])
+    assert named(c) == c._owned and len(set(sum(named(c), []))) == 7
+
+
+def layer_of(seed=5, max_len=64, **kw):
+    g = torch.Generator().manual_seed(seed)
+    w = [(torch.randn(s, generator=g) * 0.06).to(torch.bfloat16).cuda()
+         for s in (((H + 2 * HK) * D, HIDDEN), (HIDDEN, H * D))]
+    return FP4DecodeAttention(*w, H, HK, D, max_len, **kw), g
+
+
+def filled(cache, g):
+    for t in (cache.k, cache.v):
+        t.copy_(torch.randn(t.shape, generator=g).to(t.dtype))
+    return cache
+
+
+@pytest.mark.gpu
+def test_slots_without_a_page_touch_nobody_elses():
+    """A step with an unreserved, a released and an outgrown slot: reported,
+    nothing written for them, their lengths unchanged, the live sequences as
+    in a step that leaves those slots out."""
+    need_gpu()
+    layer, g = layer_of()
+    cache = filled(PagedCache(5, 64, HK, D, page_size=PAGE), g)
+    cache.reserve([20, 0, 24, 0, 8])
+    cache.release(2)
+    cache.reserve([20, 0, 0, 40, 8])  # takes the pages of the released slot
+    lengths = torch.tensor([5, 0, 0, 17, 8], dtype=torch.int32)  # the last one is full
+    x = torch.randn(5, HIDDEN, generator=g).to(torch.bfloat16).cuda()
+    k0, v0 = cache.k.clone(), cache.v.clone()
+    skip = torch.tensor([5, -1, -1, 17, -1], dtype=torch.int32).cuda()
+    cache.lengths.copy_(lengths)
+    want = layer(x, cache, skip)
+    assert fq.fp4_status_sync() == fq.FP4_OK
+    want_k, want_v = cache.k.clone(), cache.v.clone()
+    cache.k.copy_(k0)
+    cache.v.copy_(v0)
+    cache.lengths.copy_(lengths)
+    got = layer(x, cache)
+    assert fq.fp4_status_sync() == fq.FP4_ERR_INVALID_ARG
+    assert torch.equal(cache.k, want_k) and torch.equal(cache.v, want_v)
+    changed = (cache.k != k0).flatten(2).any(-1).nonzero().tolist()
+    assert sorted(changed) == sorted([[cache._owned[0][0], 5], [cache._owned[3][2], 1]])
+    assert torch.equal(got[[0, 3]], want[[0, 3]])
+    assert cache.lengths.tolist() == [6, 0, 0, 18, 8]
+    # the full one goes on once it has pages
+    cache.reserve([20, 0, 0, 40, 9])
+    layer(x, cache, torch.tensor([-1, -1, -1, -1, 8], dtype=torch.int32).cuda())
+    assert fq.fp4_status_sync() == fq.FP4_OK and int(cache.lengths[4]) == 9
+
+
+@pytest.mark.gpu
+def test_positions_past_the_rotation_table_do_not_count():
+    """A table of rotations shorter than the pages: a position past it is
+    reported and the length stays."""
+    need_gpu()
+    layer, g = layer_of(max_len=10)
+    cache = filled(PagedCache(2, 16, HK, D, page_size=PAGE), g)
+    cache.reserve([16, 16])
+    cache.lengths.copy_(torch.tensor([10, 3], dtype=torch.int32))
+    x = torch.randn(2, HIDDEN, generator=g).to(torch.bfloat16).cuda()
+    k0 = cache.k.clone()
+    layer(x, cache)
+    assert fq.fp4_status_sync() == fq.FP4_ERR_INVALID_ARG
+    assert cache.lengths.tolist() == [10, 4]
+    assert (cache.k != k0).flatten(2).any(-1).sum() == 1
