@@ -108,10 +108,11 @@ class FP4DecodeAttention(torch.nn.Module):
     def forward(self, x, cache, pos=None):
         """One new token of every sequence: x [seqs, hidden] at positions pos
         (default: the cache's lengths).  Returns [seqs, hidden] and advances the
-        cache's lengths.  Where a sequence has no page for its position, or the
-        rotation ends before it, nothing is stored, its length stays (at most
-        the room of its pages), its row of the result means nothing and
-        fp4_status_sync reports FP4_ERR_INVALID_ARG."""
+        cache's lengths.  A sequence at position -1 is left out of the step: it
+        keeps its length, and its row of the result is zero.  Where a sequence
+        has no page for its position, or the rotation ends before it, nothing is
+        stored, its length stays (at most the room of its pages), its row of the
+        result means nothing and fp4_status_sync reports FP4_ERR_INVALID_ARG."""
         n = x.shape[0]
         pos = cache.lengths if pos is None else pos
         after = pos + 1
@@ -119,10 +120,14 @@ class FP4DecodeAttention(torch.nn.Module):
         q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)
         q = kv_append(k, v, cache.k, cache.v, cache.table, pos, q=q, rope=self.rope,
                       interleaved=self.interleaved)
-        torch.minimum(after, cache.room, out=cache.lengths)
+        given = pos is not cache.lengths
+        seen = torch.minimum(after, cache.room, out=None if given else cache.lengths)
         if cache.table.shape[1] * cache.page_size > self.rope.shape[0]:
-            cache.lengths.clamp_(max=self.rope.shape[0])
-        a = decode_attention(q, cache.k, cache.v, cache.table, cache.lengths, window=self.window)
+            seen.clamp_(max=self.rope.shape[0])
+        if given:  # what is left out sees nothing and keeps its length
+            seen.clamp_(min=0)
+            cache.lengths.copy_(torch.where(pos < 0, cache.lengths, seen))
+        a = decode_attention(q, cache.k, cache.v, cache.table, seen, window=self.window)
         return matvec(a.view(n, -1), self.w_o)
 
     def prefill(self, x, cache, seq, pos):

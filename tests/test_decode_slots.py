@@ -1,11 +1,12 @@
 """The decoding layer's cache where not every slot takes part in a step: pages
-given back, slots without pages, sequences past their pages."""
+given back, slots without pages, sequences past their pages, paused ones."""
 import pytest
 import torch
 
 import fp4_block_scaled_quantize_gb300 as fq
 from fp4_block_scaled_quantize_gb300.decode import FP4DecodeAttention, PagedCache
 from gpu_util import need_gpu
+from test_decode import reference
 
 H, HK, D, HIDDEN, PAGE = 8, 2, 64, 256, 8
 
@@ -93,3 +94,36 @@ def test_positions_past_the_rotation_table_do_not_count():
     assert fq.fp4_status_sync() == fq.FP4_ERR_INVALID_ARG
     assert cache.lengths.tolist() == [10, 4]
     assert (cache.k != k0).flatten(2).any(-1).sum() == 1
+
+
+@pytest.mark.gpu
+def test_a_paused_sequence_goes_on_where_it_was():
+    """A sequence left out of some steps (position -1) keeps its length and
+    its history: its outputs are the bits of the same tokens without a pause,
+    and what the 64-bit definition gives (tolerance as for a conversation)."""
+    need_gpu()
+    layer, g = layer_of()
+    steps, pause = 14, range(5, 9)
+    xs = torch.randn(steps, 3, HIDDEN, generator=g).to(torch.bfloat16).cuda()
+    cache = PagedCache(3, 32, HK, D, page_size=PAGE)
+    cache.reserve([32] * 3)
+    kept = []
+    for i in range(steps):
+        if i in pause:
+            pos = cache.lengths.clone()
+            pos[1] = -1
+            y = layer(xs[i], cache, pos)
+            assert (y[1] == 0).all() and int(cache.lengths[1]) == pause[0]
+        else:
+            y = layer(xs[i], cache)
+            kept.append(y[1])
+    assert cache.lengths.tolist() == [steps, steps - len(pause), steps]
+    assert fq.fp4_status_sync() == fq.FP4_OK
+    mine = [i for i in range(steps) if i not in pause]
+    other = PagedCache(3, 32, HK, D, page_size=PAGE)
+    other.reserve([32] * 3)
+    alone = [layer(xs[i], other)[1] for i in mine]
+    assert all(torch.equal(a, b) for a, b in zip(kept, alone))
+    want = reference(layer, xs[mine][:, 1:2], [0])
+    rms = want.pow(2).mean().sqrt()
+    assert ((torch.stack(kept).cpu().double() - want[:, 0]).abs() <= 2.0 ** -4 * rms).all()
