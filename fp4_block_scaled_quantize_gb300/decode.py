@@ -113,8 +113,12 @@ class FP4DecodeAttention(torch.nn.Module):
         has no page for its position, or the rotation ends before it, nothing is
         stored, its length stays (at most the room of its pages), its row of the
         result means nothing and fp4_status_sync reports FP4_ERR_INVALID_ARG."""
-        n = x.shape[0]
+        n = cache.lengths.shape[0]
+        if x.dim() != 2 or x.shape[0] != n:
+            raise ValueError(f"FP4DecodeAttention: x must be [{n}, hidden], a token of every sequence of the cache")
         pos = cache.lengths if pos is None else pos
+        if pos.shape != (n,) or pos.dtype != torch.int32 or pos.device != cache.lengths.device:
+            raise ValueError(f"FP4DecodeAttention: pos must be {n} int32 positions beside the cache")
         after = pos + 1
         qkv = matvec(x, self.w_qkv).view(n, self.heads + 2 * self.kv_heads, self.head_dim)
         q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)

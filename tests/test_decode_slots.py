@@ -127,3 +127,20 @@ def test_a_paused_sequence_goes_on_where_it_was():
     want = reference(layer, xs[mine][:, 1:2], [0])
     rms = want.pow(2).mean().sqrt()
     assert ((torch.stack(kept).cpu().double() - want[:, 0]).abs() <= 2.0 ** -4 * rms).all()
+
+
+@pytest.mark.gpu
+def test_a_step_of_another_size_is_refused_and_changes_nothing():
+    need_gpu()
+    layer, g = layer_of()
+    cache = filled(PagedCache(3, 32, HK, D, page_size=PAGE), g)
+    cache.reserve([32] * 3)
+    cache.lengths.fill_(4)
+    k0 = cache.k.clone()
+    x = torch.randn(4, HIDDEN, generator=g).to(torch.bfloat16).cuda()
+    ints = torch.full((4,), 4, dtype=torch.int32, device="cuda")
+    for bad in ((x[:2], cache, ints[:2]), (x[:2], cache), (x, cache, ints), (x[:3], cache, ints[:2]),
+                (x[:3], cache, ints[:3].long()), (x[:3], cache, ints[:3].cpu()), (x[0], cache)):
+        with pytest.raises(ValueError):
+            layer(*bad)
+        assert cache.lengths.tolist() == [4] * 3 and torch.equal(cache.k, k0)
