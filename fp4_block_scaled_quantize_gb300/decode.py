@@ -73,8 +73,8 @@ class PagedCache:
 
 class FP4DecodeAttention(torch.nn.Module):
     """Attention layer for decoding: heads query heads over kv_heads key heads
-    of head_dim, rotated over rot_dim elements (default: all) by positions up
-    to max_len.  w_qkv [(heads + 2 kv_heads) head_dim, hidden] and w_o [hidden,
+    of head_dim, rotated over rot_dim elements (default: all; 0: none) by
+    positions up to max_len.  w_qkv [(heads + 2 kv_heads) head_dim, hidden] and w_o [hidden,
     heads head_dim] are bfloat16 weights, quantised once, or Quantized
     copies."""
 
@@ -90,8 +90,9 @@ class FP4DecodeAttention(torch.nn.Module):
             raise ValueError("FP4DecodeAttention: the weights do not fit the heads")
         self.heads, self.kv_heads, self.head_dim = heads, kv_heads, head_dim
         self.window, self.interleaved = window, interleaved
-        self.register_buffer("rope", rope_table(max_len, rot_dim or head_dim, base, self.w_qkv.q.device),
-                             persistent=False)
+        rot_dim = head_dim if rot_dim is None else rot_dim
+        rope = rope_table(max_len, rot_dim, base, self.w_qkv.q.device) if rot_dim else None
+        self.register_buffer("rope", rope, persistent=False)
 
     @staticmethod
     def quantized(w, p):
@@ -126,7 +127,7 @@ class FP4DecodeAttention(torch.nn.Module):
                       interleaved=self.interleaved)
         given = pos is not cache.lengths
         seen = torch.minimum(after, cache.room, out=None if given else cache.lengths)
-        if cache.table.shape[1] * cache.page_size > self.rope.shape[0]:
+        if self.rope is not None and cache.table.shape[1] * cache.page_size > self.rope.shape[0]:
             seen.clamp_(max=self.rope.shape[0])
         if given:  # what is left out sees nothing and keeps its length
             seen.clamp_(min=0)

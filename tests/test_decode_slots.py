@@ -144,3 +144,24 @@ def test_a_step_of_another_size_is_refused_and_changes_nothing():
         with pytest.raises(ValueError):
             layer(*bad)
         assert cache.lengths.tolist() == [4] * 3 and torch.equal(cache.k, k0)
+
+
+@pytest.mark.gpu
+def test_no_rotation():
+    """rot_dim 0 rotates nothing: the step of a table of ones and zeros."""
+    need_gpu()
+    ys = []
+    for rot in (0, D):
+        layer, g = layer_of(rot_dim=rot)
+        if rot:
+            layer.rope[:, :D // 2] = 1
+            layer.rope[:, D // 2:] = 0
+        cache = PagedCache(2, 32, HK, D, page_size=PAGE)
+        cache.reserve([32] * 2)
+        xs = torch.randn(6, 2, HIDDEN, generator=g).to(torch.bfloat16).cuda()
+        ys.append([layer(x, cache) for x in xs])
+        seq = torch.zeros(4, dtype=torch.int32, device="cuda")
+        layer.prefill(xs[:2].reshape(4, -1), cache, seq, torch.arange(4, dtype=torch.int32).cuda())
+        ys[-1].append(cache.k[cache._owned[0][0], :4].clone())
+    assert fq.fp4_status_sync() == fq.FP4_OK
+    assert all(torch.equal(a, b) for a, b in zip(*ys))
