@@ -515,7 +515,14 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
     };
 
     // A value that is not finite makes lo x value a NaN where hi x value is an
-    // infinity: a warp whose sums are not finite repeats its part without lo.
+    // infinity: a warp with a sum that is not finite repeats its part without
+    // lo, and takes from that pass what was not finite in the first.
+    const int at_part = 2 * warp + (tile0 == 0);  // the warp's first row, or its last
+    // the place of this row's part, outputs 64 i + 8 g ... of column 8 n + 2 t + e
+    auto part_at = [&](int n, int e, int i) {
+      int place = (at_part * kCols + 2 * t) * (DP + 8) + 8 * g;
+      return reinterpret_cast<float4 *>(o_sh + place + (8 * n + e) * (DP + 8) + 64 * i);
+    };
     for (bool both = true;; both = false) {
     seen = false;
 #pragma unroll
@@ -611,6 +618,9 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
             w[e] = ex2(sc[u][n][e] - (base[n][e & 1] - lift<T>()));
             l[n][e & 1] += w[e];
           }
+          if (!Bf16<T>::value && !both)  // a weight that f16 would round to zero still meets an infinity
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = w[e] > 0.0f ? fmaxf(w[e], 0x1p-24f) : w[e];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t p = pack<T>(w[2 * h], w[2 * h + 1]);
@@ -653,7 +663,31 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) worst = fmaf(o[n][i][j][e], 0.0f, worst);
-    if (!both || !__any_sync(~0u, worst != 0.0f)) break;
+    if (__builtin_expect(both && !__any_sync(~0u, worst != 0.0f), 1)) break;
+    // a lane's own values, so nothing has to be waited for
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < kVal; ++i) {
+          float4 *const at = part_at(n, e, i);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float *const v[4] = {&o[n][i][2 * h][e], &o[n][i][2 * h][2 + e], &o[n][i][2 * h + 1][e],
+                                 &o[n][i][2 * h + 1][2 + e]};
+            if (both) {
+              at[h] = make_float4(*v[0], *v[1], *v[2], *v[3]);
+            } else {
+              const float4 first = at[h];
+              if (isfinite(first.x)) *v[0] = first.x;
+              if (isfinite(first.y)) *v[1] = first.y;
+              if (isfinite(first.z)) *v[2] = first.z;
+              if (isfinite(first.w)) *v[3] = first.w;
+            }
+          }
+        }
+    if (!both) break;
     }
 
 #pragma unroll
@@ -686,7 +720,6 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
         }
       continue;
     }
-    const int at_part = 2 * warp + (tile0 == 0);  // the warp's first row, or its last
     if (lane == 0) part_sh[at_part] = make_int4(s, row, tile0 == 0, tile1 == sp.tiles);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -694,13 +727,10 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
       for (int e = 0; e < 2; ++e) {
         const int col = 8 * n + 2 * t + e;
         if (g == 0) st_sh[at_part * kCols + col] = make_float4(m[n][e], l[n][e], seen ? 1.0f : 0.0f, 1.0f);
-        float *to = o_sh + (at_part * kCols + col) * (DP + 8);
 #pragma unroll
         for (int i = 0; i < kVal; ++i) {
-          *reinterpret_cast<float4 *>(to + 64 * i + 8 * g) =
-              make_float4(o[n][i][0][e], o[n][i][0][2 + e], o[n][i][1][e], o[n][i][1][2 + e]);
-          *reinterpret_cast<float4 *>(to + 64 * i + 8 * g + 4) =
-              make_float4(o[n][i][2][e], o[n][i][2][2 + e], o[n][i][3][e], o[n][i][3][2 + e]);
+          part_at(n, e, i)[0] = make_float4(o[n][i][0][e], o[n][i][0][2 + e], o[n][i][1][e], o[n][i][1][2 + e]);
+          part_at(n, e, i)[1] = make_float4(o[n][i][2][e], o[n][i][2][2 + e], o[n][i][3][e], o[n][i][3][2 + e]);
         }
       }
   }

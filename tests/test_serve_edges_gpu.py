@@ -1,0 +1,76 @@
+"""The serving operators on values and layouts at the edge of what they take:
+values that are not finite beside finite ones."""
+import pytest
+import torch
+
+import fp4_block_scaled_quantize_gb300 as fq
+from gpu_util import need_gpu
+from serve_ref import HALF_ULP, TINY, attention
+from test_serve_gpu import BF, HF, close, gen, pool
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    need_gpu()
+    for _ in range(2):
+        fq.fp4_status_sync()
+    yield
+
+
+# ------------------------------------------------- values that are not finite
+
+def check_partly_finite(q, kp, vp, table, lengths):
+    """Elements whose 64-bit value is finite lie within the operator's usual
+    tolerance; the others are the same infinity or NaN."""
+    D = q.shape[-1]
+    want, wv, _, mag = attention(q, kp, vp, table, lengths, D ** -0.5, 0)
+    got = fq.decode_attention(q, kp, vp, table, lengths).cpu().double()
+    fine = torch.isfinite(want)
+    assert not fine.all() and fine.any()
+    d = (D / 16 + 8) * 2.0 ** -23 * mag
+    sums = (lengths.cpu().double()[:, None] / 16 + 32) * 2.0 ** -23
+    tol = (4 * d + 2.0 ** -14 + sums)[..., None] * wv + 2 * HALF_ULP[q.dtype] * want.abs() + 2 * TINY[q.dtype]
+    close(got[fine], want[fine], tol[fine], "finite elements")
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    odd = torch.isinf(want)
+    assert torch.equal(got[odd], want[odd])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("heads,hk,dim,page", [(8, 2, 128, 16), (4, 4, 64, 16), (16, 1, 64, 8), (32, 2, 128, 16),
+                                               (6, 2, 192, 16), (8, 1, 256, 24), (10, 2, 80, 16)])
+@pytest.mark.parametrize("lengths", [[21], [100, 90], [1000, 3], [9000, 5000]])
+def test_attention_values_not_finite_leave_the_others_their_accuracy(dtype, heads, hk, dim, page, lengths):
+    kp, vp, table = pool(lengths, page, hk, dim, dtype)
+    q = torch.randn(len(lengths), heads, dim, generator=gen(50)).to(dtype).cuda()
+    at = lambda s, p: (int(table[s, p // page]), p % page)  # noqa: E731
+    last = lengths[0] - 1
+    vp[at(0, 3)][0, 5] = float("inf")
+    vp[at(0, last)][0, dim - 1] = float("-inf")
+    vp[at(0, 7)][hk - 1, 9] = float("nan")
+    vp[at(0, 2)][0, 17], vp[at(0, last // 2)][0, 17] = float("inf"), float("-inf")
+    check_partly_finite(q, kp, vp, table, torch.tensor(lengths, dtype=torch.int32).cuda())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_attention_a_query_head_that_is_not_finite_is_alone(dtype):
+    kp, vp, table = pool([60, 700], 16, 2, 128, dtype)
+    q = torch.randn(2, 8, 128, generator=gen(51)).to(dtype).cuda()
+    ln = torch.tensor([60, 700], dtype=torch.int32).cuda()
+    q[1, 2, 77] = float("nan")
+    check_partly_finite(q, kp, vp, table, ln)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("away", [10.0, 30.0, 60.0])
+def test_attention_small_weight_of_an_infinite_value(dtype, away):
+    """A weight of e^-away is no zero: its infinity is the result."""
+    kp, vp, table = pool([50], 16, 1, 64, dtype)
+    kp[table[0, :4].long()] = 0
+    q = torch.zeros(1, 2, 64, dtype=dtype, device="cuda")
+    q[..., 0] = 8
+    kp[table[0, 1], 4, 0, 0] = -away  # score 8 x -away / 8
+    vp[table[0, 1], 4, 0, 6] = float("-inf")
+    check_partly_finite(q, kp, vp, table, torch.tensor([50], dtype=torch.int32).cuda())
