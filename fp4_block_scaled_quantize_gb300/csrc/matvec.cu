@@ -421,20 +421,26 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
 
   const int at0 = ((2 * t) ^ g) << 4;  // the lane's pieces of a row: at0, at0 ^ 16, then 1024 on
   // kPieces: whether rows begin inside words, where a lane's codes begin in
-  // their first word (a tile's first row begins with one), the place of the
-  // second, and the bytes inside K
+  // their first word (a tile's first row begins with one) and the place of the
+  // second
   bool cut = false;
   int bit = 0, next_at = 0, next_hop = 0;
+  // not kBoxed: where K ends inside a word, the bytes of the lane's word in the
+  // last step that are inside (what follows is a next row's or padding: it
+  // would meet zeros, but may be NaN, or the largest MXFP4 scale of a row)
   uint32_t inside = ~0u;
-  if (MODE == kAny) {
-    const int blocks = (int)(j.K / BLOCK), own = BLOCK == 16 ? t : t >> 1;
+  const int blocks = (int)(j.K / BLOCK), own = BLOCK == 16 ? t : t >> 1;
+  if (MODE != kBoxed) {
     const int left = blocks - (p.steps - 1) * (kStep / BLOCK) - 4 * own;
+    inside = left >= 4 ? ~0u : left > 0 ? (1u << (8 * left)) - 1 : 0u;
+  }
+  const int edge = blocks & 3 ? p.steps - 1 : -1;
+  if (MODE == kAny) {
     const bool last = own == kStep / BLOCK / 4 - 1;
     cut = blocks & 3;
     bit = 8 * (g * blocks & 3);
     next_at = last ? 512 + 4 * g : 4 * lane + (BLOCK == 16 ? 4 : 8);
     next_hop = last ? 32 : 128;
-    inside = left >= 4 ? ~0u : left > 0 ? (1u << (8 * left)) - 1 : 0u;
   }
   int slot = 0;
   uint32_t phase = 0;
@@ -467,17 +473,15 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
         const int o = BLOCK == 32 && (MODE == kBoxed || (MODE == kAny && p.words == kBoxed)) ? (4 * g + (t >> 1) + 2 * (st & 1)) * 4 : lane * 4;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) codes[i] = *reinterpret_cast<const uint32_t *>(wl + 128 * i + o);
-        if (MODE == kAny && p.words == kPieces) {
-          if (cut) {
+        if (MODE == kAny && p.words == kPieces && cut) {
 #pragma unroll
-            for (int i = 0; i < kGroups; ++i)
-              codes[i] = __funnelshift_r(codes[i], *reinterpret_cast<const uint32_t *>(wl + next_at + next_hop * i), bit);
-          }
-          if (st == p.steps - 1) {  // a next row's codes would meet zeros, but may be NaN
-#pragma unroll
-            for (int i = 0; i < kGroups; ++i) codes[i] &= inside;
-          }
+          for (int i = 0; i < kGroups; ++i)
+            codes[i] = __funnelshift_r(codes[i], *reinterpret_cast<const uint32_t *>(wl + next_at + next_hop * i), bit);
         }
+      }
+      if (MODE != kBoxed && __builtin_expect(st == edge, 0)) {
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) codes[i] &= inside;
       }
       float f[kGroups];
       int top[kGroups] = {};

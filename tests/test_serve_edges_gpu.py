@@ -1,12 +1,12 @@
 """The serving operators on values and layouts at the edge of what they take:
-values that are not finite beside finite ones."""
+values that are not finite beside finite ones, scale bytes outside a weight."""
 import pytest
 import torch
 
 import fp4_block_scaled_quantize_gb300 as fq
 from gpu_util import need_gpu
 from serve_ref import HALF_ULP, TINY, attention
-from test_serve_gpu import BF, HF, close, gen, pool
+from test_serve_gpu import BF, F32, HF, MMA, MX, NV, UE, UE32, close, gen, pool, random_copy
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +74,26 @@ def test_attention_small_weight_of_an_infinite_value(dtype, away):
     kp[table[0, 1], 4, 0, 0] = -away  # score 8 x -away / 8
     vp[table[0, 1], 4, 0, 6] = float("-inf")
     check_partly_finite(q, kp, vp, table, torch.tensor([50], dtype=torch.int32).cuda())
+
+
+# ------------------------------------------------ scale bytes outside a weight
+
+@pytest.mark.parametrize("fmt", [NV, UE, MX, UE32])
+@pytest.mark.parametrize("blocks", [1, 2, 3, 5, 7, 18, 33, 65])
+@pytest.mark.parametrize("m", [1, 11])
+def test_matvec_padding_of_the_tiled_scales_has_no_effect(fmt, blocks, m):
+    """The tiled layout's bytes past a row's end and past the last row may hold
+    anything."""
+    block = 32 if fmt in (MX, UE32) else 16
+    n, k = 75, blocks * block
+    w = random_copy(n, k, fmt, MMA, seed=blocks)
+    x = torch.randn(m, k, generator=gen(52)).to(BF).cuda()
+    y = fq.matvec(x, w, out_dtype=F32)
+    cols = k // (16 if fmt == UE32 else block)
+    view = w.sf.view(1, -(-cols // 4), 32, 4, 4).permute(0, 3, 2, 1, 4)  # [tile row, word, line, tile column, byte]
+    inside = torch.zeros(128, -(-cols // 4) * 4, dtype=torch.bool, device="cuda")
+    inside[:n, :cols] = True
+    inside = inside.view(1, 4, 32, -1, 4)
+    for code in (0xFF, 0x7F, 0xFE, 0x80):
+        view[~inside] = code
+        assert torch.equal(fq.matvec(x, w, out_dtype=F32), y), code
