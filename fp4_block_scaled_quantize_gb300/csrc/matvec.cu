@@ -492,7 +492,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
           top[i] = max((int)(codes[i] & 255u), (int)((codes[i] >> 8) & 255u));
           top[i] = max(top[i], __shfl_xor_sync(~0u, top[i], 1));
           top[i] = max(top[i], __shfl_xor_sync(~0u, top[i], 2));
-          f[i] = pow2(top[i] - 140);  // 2^(top - 127) / 2^13
+          // 2^(top - 127) / 2^13; 255 is NaN
+          f[i] = top[i] == 255 ? __uint_as_float(0x7FC00000u) : pow2(top[i] - 140);
         }
       }
       float d[NT][kPairs][4] = {};

@@ -372,8 +372,8 @@ typedef enum { FP4_BF16 = 0, FP4_F16 = 1, FP4_F32 = 2 } fp4_type;
  * PLAIN (row_shift must be NULL) or MMA (UE5M3: with row_shift, sf holds the
  * E4M3 images of the remap; without, UE5M3 codes).  Every format; NVFP4_CTA
  * reads one s_dec per 128 rows.  Padding bytes of the MMA layout have no effect.
- * Scale codes that no producer emits (UE5M3
- * above 0xF7, E4M3 0x7F, E8M0 255) give unspecified values.
+ * A row with a NaN scale code (UE5M3 0xFF, E4M3 0x7F, E8M0 255) is NaN; UE5M3
+ * 0xF8 .. 0xFE, which no producer emits, give unspecified values.
  * Accuracy: x is held exactly for magnitudes down to 2^-32 of the largest in
  * its token's 256 columns, MXFP4 block scales down to 2^-35 of the largest in
  * a row's 256 columns; smaller ones round towards zero contribution.

@@ -6,7 +6,7 @@ import torch
 import fp4_block_scaled_quantize_gb300 as fq
 from gpu_util import need_gpu
 from serve_ref import HALF_ULP, TINY, attention
-from test_serve_gpu import BF, F32, HF, MMA, MX, NV, UE, UE32, close, gen, pool, random_copy
+from test_serve_gpu import BF, F32, HF, MMA, MX, NV, PLAIN, UE, UE32, close, gen, pool, random_copy
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +97,23 @@ def test_matvec_padding_of_the_tiled_scales_has_no_effect(fmt, blocks, m):
     for code in (0xFF, 0x7F, 0xFE, 0x80):
         view[~inside] = code
         assert torch.equal(fq.matvec(x, w, out_dtype=F32), y), code
+
+
+@pytest.mark.parametrize("layout", [PLAIN, MMA])
+@pytest.mark.parametrize("m", [1, 5, 16])
+@pytest.mark.parametrize("k", [96, 512, 1024])
+def test_matvec_e8m0_nan_is_nan(layout, m, k):
+    """E8M0 255 is NaN: the rows that hold one are NaN, no other changes."""
+    n = 200
+    w = random_copy(n, k, MX, layout, seed=k)
+    x = torch.randn(m, k, generator=gen(53)).to(HF).cuda()
+    y = fq.matvec(x, w, out_dtype=F32)
+    cols, rows = k // 32, [0, 31, 77, n - 1]
+    for i, r in enumerate(rows):
+        c = (i * 5) % cols
+        at = r * cols + c if layout == PLAIN else (r // 128 * -(-cols // 4) + c // 4) * 512 + r % 32 * 16 + r % 128 // 32 * 4 + c % 4
+        w.sf[at] = 255
+    z = fq.matvec(x, w, out_dtype=F32)
+    bad = torch.zeros(n, dtype=torch.bool, device="cuda")
+    bad[rows] = True
+    assert torch.isnan(z[:, bad]).all() and torch.equal(z[:, ~bad], y[:, ~bad])
