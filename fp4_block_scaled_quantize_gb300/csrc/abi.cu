@@ -548,7 +548,9 @@ fp4_status fp4_status_sync(void *stream) {
   if (!w) return FP4_ERR_CUDA;
   uint32_t v = 0;
   if (cudaMemcpy(&v, w, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return FP4_ERR_CUDA;
-  if (v && cudaMemset(w, 0, sizeof v) != cudaSuccess) return FP4_ERR_CUDA;
+  // a bad index beside another condition waits for the next call
+  const uint32_t rest = v & ~kStatusIndex ? v & kStatusIndex : 0u;
+  if (v && cudaMemcpy(w, &rest, sizeof rest, cudaMemcpyHostToDevice) != cudaSuccess) return FP4_ERR_CUDA;
   if (v & kStatusTimeout) return FP4_ERR_TIMEOUT;
   if (v & kStatusNonfinite) return FP4_ERR_NONFINITE;
   if (v & kStatusScaleWindow) return FP4_ERR_SCALE_WINDOW;

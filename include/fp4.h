@@ -478,7 +478,9 @@ int32_t fp4_block_size(int32_t format);
 
 /* Waits for `stream`, then returns and clears the device status word of the
  * current device (FP4_OK if no device condition was raised).  Calls that
- * overlap on the device share one status word. */
+ * overlap on the device share one status word.  Of several conditions the
+ * gravest is returned; a bad index of the serving calls beside another one
+ * stays in the word and is returned by the next call. */
 fp4_status fp4_status_sync(void *stream);
 
 /* Static description of a status code. */

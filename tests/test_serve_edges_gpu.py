@@ -1,12 +1,13 @@
 """The serving operators on values and layouts at the edge of what they take:
-values that are not finite beside finite ones, scale bytes outside a weight."""
+values that are not finite beside finite ones, scale bytes outside a weight,
+several conditions in one status word."""
 import pytest
 import torch
 
 import fp4_block_scaled_quantize_gb300 as fq
 from gpu_util import need_gpu
 from serve_ref import HALF_ULP, TINY, attention
-from test_serve_gpu import BF, F32, HF, MMA, MX, NV, PLAIN, UE, UE32, close, gen, pool, random_copy
+from test_serve_gpu import BF, F32, HF, MMA, MX, NV, PLAIN, UE, UE32, cache, close, gen, pool, random_copy
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +118,22 @@ def test_matvec_e8m0_nan_is_nan(layout, m, k):
     bad = torch.zeros(n, dtype=torch.bool, device="cuda")
     bad[rows] = True
     assert torch.isnan(z[:, bad]).all() and torch.equal(z[:, ~bad], y[:, ~bad])
+
+
+# ------------------------------------------------------------- the status word
+
+def test_a_bad_index_is_not_lost_beside_another_condition():
+    kp, vp = cache(2, 4, 1, 64, BF)
+    k = torch.zeros(1, 1, 64, dtype=BF, device="cuda")
+    ints = lambda *a: torch.tensor(a, dtype=torch.int32).cuda()  # noqa: E731
+
+    def bad_index():
+        fq.kv_append(k, k, kp, vp, ints(9)[None], ints(0))
+
+    bad_index()
+    fq.amax(torch.full((16, 64), float("nan"), dtype=BF, device="cuda"))
+    assert fq.fp4_status_sync() == fq.FP4_ERR_NONFINITE
+    assert fq.fp4_status_sync() == fq.FP4_ERR_INVALID_ARG
+    assert fq.fp4_status_sync() == fq.FP4_OK
+    bad_index()
+    assert fq.fp4_status_sync() == fq.FP4_ERR_INVALID_ARG and fq.fp4_status_sync() == fq.FP4_OK
