@@ -57,6 +57,19 @@ def _torch():
     return os.path.dirname(torch.__file__)
 
 
+def _made_for():
+    """What the binding's object depends on beside its sources."""
+    import torch
+    return f"{sys.implementation.cache_tag} torch {torch.__version__} {_torch()}"
+
+
+def _read(path):
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
 def _stale(obj, deps):
     if not os.path.exists(obj):
         return True
@@ -80,16 +93,18 @@ def build(force=False, verbose=False, extra=()):
                 cmd.insert(1, "-Xptxas=-v")
             procs.append((unit, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                  stderr=subprocess.STDOUT, text=True)))
-    bind, bind_obj = os.path.join(CSRC, "bind.cpp"), os.path.join(BUILD, "bind.o")
-    if force or _stale(bind_obj, [bind, os.path.join(INCLUDE, "fp4.h")]):
-        try:
+    bind, bind_obj, bind_for = (os.path.join(CSRC, "bind.cpp"), os.path.join(BUILD, "bind.o"),
+                                os.path.join(BUILD, "bind.for"))
+    try:
+        made_for = _made_for()
+        if force or _stale(bind_obj, [bind, os.path.join(INCLUDE, "fp4.h")]) or _read(bind_for) != made_for:
             host.append(("bind.cpp", subprocess.Popen(
                 [cxx(), "-O2", "-Wall", "-std=c++17", "-fPIC", "-I" + INCLUDE,
                  "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(_torch(), "include"),
                  "-isystem", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
                  "-c", bind, "-o", bind_obj], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-        except (ImportError, OSError) as e:  # no torch, no compiler
-            unbound.append(f"bind.cpp ({e})")
+    except (ImportError, OSError) as e:  # no torch, no compiler
+        unbound.append(f"bind.cpp ({e})")
 
     def wait(started):
         bad = []
@@ -119,6 +134,8 @@ def build(force=False, verbose=False, extra=()):
                         "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(_torch(), "lib"), "-lc10",
                         "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], check=True)
         os.replace(tmp, BIND)
+        with open(bind_for, "w") as f:
+            f.write(made_for)
     return LIB
 
 

@@ -1,4 +1,4 @@
-"""The build: what one part's failure leaves of the others."""
+"""The build: what one part's failure leaves of the others, and what is made again."""
 import os
 
 import pytest
@@ -26,3 +26,19 @@ def test_a_binding_that_does_not_compile_leaves_the_library(elsewhere, monkeypat
     with pytest.raises(RuntimeError, match="bind.cpp"):
         fbuild.build()
     assert os.path.exists(fbuild.LIB) and not os.path.exists(fbuild.BIND)
+
+
+def test_the_binding_is_made_again_for_another_torch(elsewhere, monkeypatch):
+    """It is compiled against torch's C++ headers: another torch, or another
+    interpreter, means another binding."""
+    import torch
+    fbuild.build()
+    first = os.stat(fbuild.BIND).st_mtime_ns
+    fbuild.build()
+    assert os.stat(fbuild.BIND).st_mtime_ns == first
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".another")
+    fbuild.build()
+    second = os.stat(fbuild.BIND).st_mtime_ns
+    assert second > first
+    fbuild.build()
+    assert os.stat(fbuild.BIND).st_mtime_ns == second
