@@ -71,6 +71,24 @@ class PagedCache:
         self.lengths[seq] = 0
 
 
+_PARTS = ("q", "sf", "s_dec", "row_shift")
+
+
+def _weight(name):
+    """A Quantized copy whose parts are buffers of the module, so that they
+    are saved, loaded and moved with it."""
+    def get(self):
+        b = self._buffers
+        return Quantized(*(b[f"{name}_{part}"] for part in _PARTS), *self._forms[name])
+
+    def put(self, w):
+        for part in _PARTS:
+            self.register_buffer(f"{name}_{part}", getattr(w, part))
+        self._forms[name] = (w.format, w.sf_layout)
+
+    return property(get, put)
+
+
 class FP4DecodeAttention(torch.nn.Module):
     """Attention layer for decoding: heads query heads over kv_heads key heads
     of head_dim, rotated over rot_dim elements (default: all; 0: none) by
@@ -78,12 +96,15 @@ class FP4DecodeAttention(torch.nn.Module):
     heads head_dim] are bfloat16 weights, quantised once, or Quantized
     copies."""
 
+    w_qkv, w_o = _weight("w_qkv"), _weight("w_o")
+
     def __init__(self, w_qkv, w_o, heads, kv_heads, head_dim, max_len, rot_dim=None, base=10000.0,
                  window=0, interleaved=False, format=FP4_FMT_UE5M3_B16):
         super().__init__()
         if heads % kv_heads:
             raise ValueError("FP4DecodeAttention: heads must be a multiple of kv_heads")
         p = params(format=format, block2d=True, sf_layout=FP4_SF_MMA)  # as a linear layer's weight
+        self._forms = {}
         self.w_qkv, self.w_o = (w if isinstance(w, Quantized) else self.quantized(w, p)
                                 for w in (w_qkv, w_o))
         if self.w_qkv.rows != (heads + 2 * kv_heads) * head_dim or self.w_o.k != heads * head_dim:
@@ -93,6 +114,13 @@ class FP4DecodeAttention(torch.nn.Module):
         rot_dim = head_dim if rot_dim is None else rot_dim
         rope = rope_table(max_len, rot_dim, base, self.w_qkv.q.device) if rot_dim else None
         self.register_buffer("rope", rope, persistent=False)
+
+    def get_extra_state(self):
+        """Format and scale layout of the two weights."""
+        return torch.tensor([self._forms["w_qkv"], self._forms["w_o"]])
+
+    def set_extra_state(self, state):
+        self._forms = dict(zip(("w_qkv", "w_o"), map(tuple, state.tolist())))
 
     @staticmethod
     def quantized(w, p):
