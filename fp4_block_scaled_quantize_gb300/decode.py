@@ -39,6 +39,7 @@ class PagedCache:
         self.room = torch.zeros(seqs, dtype=torch.int32, device=device)
         self.lengths = torch.zeros(seqs, dtype=torch.int32, device=device)
         self.page_size, self.max_len = page_size, max_len
+        self.places = wide * page_size  # that a sequence's row of the table can name
         self._free = list(range(pages - 1, -1, -1))
         self._owned = [[] for _ in range(seqs)]
 
@@ -142,21 +143,20 @@ class FP4DecodeAttention(torch.nn.Module):
         has no page for its position, or the rotation ends before it, nothing is
         stored, its length stays (at most the room of its pages), its row of the
         result means nothing and fp4_status_sync reports FP4_ERR_INVALID_ARG."""
-        n = cache.lengths.shape[0]
+        n, rope, given = len(cache._owned), self.rope, pos is not None
         if x.dim() != 2 or x.shape[0] != n:
             raise ValueError(f"FP4DecodeAttention: x must be [{n}, hidden], a token of every sequence of the cache")
-        pos = cache.lengths if pos is None else pos
-        if pos.shape != (n,) or pos.dtype != torch.int32 or pos.device != cache.lengths.device:
+        if not given:
+            pos = cache.lengths
+        elif pos.shape != (n,) or pos.dtype != torch.int32 or pos.device != cache.lengths.device:
             raise ValueError(f"FP4DecodeAttention: pos must be {n} int32 positions beside the cache")
         after = pos + 1
         qkv = matvec(x, self.w_qkv).view(n, self.heads + 2 * self.kv_heads, self.head_dim)
         q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)
-        q = kv_append(k, v, cache.k, cache.v, cache.table, pos, q=q, rope=self.rope,
-                      interleaved=self.interleaved)
-        given = pos is not cache.lengths
+        q = kv_append(k, v, cache.k, cache.v, cache.table, pos, q=q, rope=rope, interleaved=self.interleaved)
         seen = torch.minimum(after, cache.room, out=None if given else cache.lengths)
-        if self.rope is not None and cache.table.shape[1] * cache.page_size > self.rope.shape[0]:
-            seen.clamp_(max=self.rope.shape[0])
+        if rope is not None and cache.places > rope.shape[0]:
+            seen.clamp_(max=rope.shape[0])
         if given:  # what is left out sees nothing and keeps its length
             seen.clamp_(min=0)
             cache.lengths.copy_(torch.where(pos < 0, cache.lengths, seen))
