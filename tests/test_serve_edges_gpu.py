@@ -1,6 +1,6 @@
 """The serving operators on values and layouts at the edge of what they take:
 values that are not finite beside finite ones, scale bytes outside a weight,
-several conditions in one status word."""
+several conditions in one status word, slices of attention in a chain."""
 import pytest
 import torch
 
@@ -137,3 +137,67 @@ def test_a_bad_index_is_not_lost_beside_another_condition():
     assert fq.fp4_status_sync() == fq.FP4_OK
     bad_index()
     assert fq.fp4_status_sync() == fq.FP4_ERR_INVALID_ARG and fq.fp4_status_sync() == fq.FP4_OK
+
+
+# ----------------------------------------------------------- slices in a chain
+
+@pytest.mark.parametrize("seqs,heads,hk,dim,longest", [(1, 8, 2, 128, 9000), (40, 8, 4, 64, 2500), (6, 16, 8, 128, 4000)])
+def test_attention_by_slices_in_a_chain(seqs, heads, hk, dim, longest):
+    """Steps of product, append, attention by slices (a second launch joins the
+    rows, wide for few of them and narrow for many) and product, lengths
+    changing in between, back to back and from a graph: the bits of the same
+    steps with a wait after every call."""
+    page, hidden, steps = 16, heads * dim, 5
+    wide = -(-(longest + steps) // page)
+    assert fq.fp4_decode_attention_workspace(seqs, wide * page, heads, hk, dim) > 0
+    kp, vp = cache(seqs * wide, page, hk, dim, BF)
+    table = torch.randperm(seqs * wide, generator=gen(60)).view(seqs, wide).to(torch.int32).cuda()
+    start = torch.randint(1, longest, (seqs,), generator=gen(61), dtype=torch.int32)
+    start[0] = longest
+    start = start.cuda()
+    w = [random_copy(n, k, NV, MMA, seed=n) for n, k in (((heads + 2 * hk) * dim, hidden), (hidden, hidden))]
+    x0 = torch.randn(seqs, hidden, generator=gen(62)).to(BF).cuda()
+    rope = fq.rope_table(longest + steps, dim)
+    old, lengths = (kp.clone(), vp.clone()), start.clone()
+
+    def reset():
+        kp.copy_(old[0])
+        vp.copy_(old[1])
+        lengths.copy_(start)
+
+    def run(wait):
+        x, kept = x0, []
+        for _ in range(steps):
+            qkv = fq.matvec(x, w[0]).view(seqs, heads + 2 * hk, dim)
+            wait()
+            q, k, v = (qkv * qkv.abs().amax().reciprocal()).split([heads, hk, hk], 1)
+            q = fq.kv_append(k, v, kp, vp, table, lengths, q=q, rope=rope)
+            wait()
+            lengths.add_(1)
+            a = fq.decode_attention(q, kp, vp, table, lengths)
+            wait()
+            y = fq.matvec(a.view(seqs, -1), w[1])
+            wait()
+            x = y * y.abs().amax().reciprocal()
+            kept += [q, a, y]
+        return kept
+
+    reset()
+    want = run(torch.cuda.synchronize)
+    assert all(torch.isfinite(t).all() for t in want)
+    for _ in range(5):
+        reset()
+        got = run(lambda: None)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        reset()
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            got = run(lambda: None)
+    for _ in range(3):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert fq.fp4_status_sync() == fq.FP4_OK
