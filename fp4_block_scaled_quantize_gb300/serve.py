@@ -284,7 +284,8 @@ def kv_append(k, v, k_pages, v_pages, page_table, pos, seq=None, q=None, rope=No
     token t is the new token of sequence t).  With rope [positions, rot_dim]
     float32 (rope_table) keys and queries q [tokens, heads, head_dim] are
     rotated on the way.  Returns the rotated queries (q_out, new by default),
-    or None without q.  Tokens at negative positions are skipped."""
+    or None without q.  Tokens at negative positions are skipped; no two tokens
+    of a call may have the same place (it would hold parts of both)."""
     if stream is None and q_out is None:
         r = _bind().append(k, v, k_pages, v_pages, page_table, pos, seq, q, rope, interleaved)
         if r is not NotImplemented:

@@ -416,7 +416,8 @@ typedef struct {
  * A token with pos < 0 is skipped: nothing is stored for it and its q_out row
  * is zero.  A token whose sequence, position, rotation entry or page lies
  * outside its table is treated the same, and fp4_status_sync reports
- * FP4_ERR_INVALID_ARG.  Two tokens of one place: either may stay.
+ * FP4_ERR_INVALID_ARG.  Two tokens of one place in one call: what stays there
+ * is unspecified, and may be parts of both.
  * q_out may be q (same strides).  rot_dim == 0: no rotation (rope may be
  * NULL).  Shapes: rot_dim even, <= head_dim; heads % kv_heads == 0.
  * Alignment: element size (16-byte pieces are used where all allow it). */
