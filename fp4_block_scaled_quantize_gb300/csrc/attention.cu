@@ -54,8 +54,8 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 // Groups of 16 positions a warp takes a step: what it keeps in flight (heads
 // of 64, 96 windows of 1000: 82 us, with one group 88; heads of 128: 329 us,
 // with two groups and two CTAs an SM 332).
-constexpr int units_of(int dp, int nt) { return dp <= 64 ? 2 : dp <= 128 && nt == 1 ? 1 : 1; }
-constexpr int tile_of(int dp, int nt) { return 16 * units_of(dp, nt); }
+constexpr int units_of(int dp) { return dp <= 64 ? 2 : 1; }
+constexpr int tile_of(int dp) { return 16 * units_of(dp); }
 constexpr int kPerSM = 5;            // CTAs per SM at most (workspace bound)
 constexpr int kCluster = 8;          // CTAs that take a row between them, at most
 constexpr float kSlack = 8.0f;       // log2 by which scores may pass the maximum in use
@@ -329,7 +329,7 @@ constexpr int per_sm(int dp, int nt) { return nt == 1 && dp <= 128 ? 3 : 2; }
 template <typename T, int DP, int NT, bool UNITS>
 __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
     k_attention(const __grid_constant__ AtParams a) {
-  constexpr int kCols = 8 * NT, kKey = DP / 32, kVal = DP / 64, kUnits = units_of(DP, NT);
+  constexpr int kCols = 8 * NT, kKey = DP / 32, kVal = DP / 64, kUnits = units_of(DP);
   constexpr int kTile = 16 * kUnits;
   // wide heads: keys and values take turns in the same registers
   constexpr bool kTurns = DP > 128;
@@ -904,7 +904,7 @@ int cluster_of(int64_t rows, int64_t reach, int dp, int nt) {
   const int64_t sms = sm_count(), fit = sms * per_sm(dp, nt);
   int n = 1;
   while (n < kCluster && rows * 2 * n <= fit * 7 / 8 &&
-         (rows * 2 * n <= sms ? n : 2 * n) * kWarps * tile_of(dp, nt) < reach)
+         (rows * 2 * n <= sms ? n : 2 * n) * kWarps * tile_of(dp) < reach)
     n *= 2;
   const int64_t most = rows > fit ? 128 : n == kCluster ? 2048 : 384 * n;
   return reach <= most ? n : 0;
@@ -928,7 +928,7 @@ fp4_status launch(AtParams a, cudaStream_t s) {
     occupancy[dev].store(per, std::memory_order_release);
   }
   const fp4_kv_cache &c = a.p.cache;
-  a.tile = tile_of(DP, NT);
+  a.tile = tile_of(DP);
   // no more CTAs than the table has tiles
   const int64_t rows = (int64_t)c.seqs * c.kv_heads * a.groups;
   const int64_t room = (int64_t)c.seq_pages * c.page_size;

@@ -163,8 +163,9 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 //     and each row has one word more from 512 on.  (30000 x 2064, 1 token: 19.5
 //     us; with byte loads, which a fill waited for, 35.1.)
 enum Words { kTiled = 0, kBoxed = 1, kPieces = 2 };
-// A kernel's MODE is kTiled or kBoxed with the payload by TMA, or kAny: what
-// the parameters say.
+// A kernel's MODE is kTiled or kBoxed with the payload by TMA, or kAny: tiled
+// scales with the payload by copies, or pieces with either, as the parameters
+// say.
 constexpr int kAny = 2;
 constexpr int words_of(int mode) { return mode == kAny ? 640 : 512; }  // scale bytes of a stage
 
@@ -185,15 +186,14 @@ struct Loader {
   __device__ __forceinline__ void fill(const MvParams &p, uint32_t payload, uint32_t words,
                                        uint32_t bar, int lane) {
     const MatvecJob &j = p.j;
-    const int mode = MODE == kAny ? p.words : MODE;
-    const bool tiled = mode == kTiled, tma = MODE != kAny || p.tma;
+    const bool tiled = (MODE == kAny ? p.words : MODE) == kTiled, tma = MODE != kAny || p.tma;
     constexpr int kPer = kStep / BLOCK;  // scale bytes of a row and step
     if (lane == 0) {
       // full boxes count, whatever part of them lies outside
-      const uint32_t bytes = (tma ? kPayload : 0) + (mode > kBoxed ? 0 : tiled ? 32 * kPer : kRows * 16);
+      const uint32_t bytes = (tma ? kPayload : 0) + (MODE == kBoxed ? kRows * 16 : tiled ? 32 * kPer : 0);
       if (MODE != kAny || bytes) tc::mbar_expect_tx(bar, bytes);
       if (tma) {
-        if (tiled) {
+        if (MODE == kTiled) {
 #pragma unroll
           for (int i = 0; i < kGroups; ++i)
             tc::tma_load_2d(payload + 1024 * i, &p.map, bar, step * (kStep / 2), row0 + 32 * i);
@@ -203,7 +203,7 @@ struct Loader {
       }
       if (tiled)
         tma_load_3d(words, &p.smap, bar, (row0 & 31) * 16, step * (kPer / 4), row0 >> 7);
-      else if (mode == kBoxed)
+      else if (MODE == kBoxed)
         tc::tma_load_2d(words, &p.smap, bar, step * kPer & ~15, row0);
     }
     ++step;
@@ -222,7 +222,7 @@ struct Loader {
         cp_async8(to + 256 * i + ((((lane & 15) >> 1) ^ odd ^ (2 * (i & 3))) << 4), from + (on ? r * half : 0), on);
       }
     }
-    if (mode > kBoxed) {
+    if (!tiled) {
       // offsets from the tile's first row, whose place is a multiple of 16; a
       // row's first word may begin in the row before
       const int blocks = (int)(j.K / BLOCK), first = (step - 1) * kPer;
@@ -238,7 +238,7 @@ struct Loader {
       for (int i = 0; i < kGroups; ++i, at += 8 * blocks) copy(words + 128 * i + 4 * lane, at);
       if ((blocks & 3) && lane < kRows) copy(words + 512 + 4 * lane, (lane * blocks & ~3) + first + kPer);
     }
-    if (!tma || mode > kBoxed) cp_async_arrive(bar);
+    cp_async_arrive(bar);
   }
 };
 
@@ -379,12 +379,12 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
   volatile int *abort_flag = reinterpret_cast<volatile int *>(xs + p.mc * (span * 512 + 64));
   const uint32_t ring_a = tc::smem_u32(ring), words_a = tc::smem_u32(word_ring), bars_a = tc::smem_u32(bars);
 
-  // the warp's own ring: one arrival that expects the boxes, and 32 lanes' for
-  // their own copies, as the stage has either or both
-  const bool boxes = MODE != kAny || p.tma || p.words <= kBoxed, copies = MODE == kAny && (!p.tma || p.words > kBoxed);
+  // the warp's own ring: one arrival that expects the boxes of a stage, if it
+  // has any, and in kAny 32 lanes' for their own copies
+  const bool boxes = MODE != kAny || p.tma || p.words == kTiled;
   if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
-    for (int d = 0; d < depth; ++d) tc::mbar_init(bars_a + 8 * d, (boxes ? 1 : 0) + (copies ? 32 : 0));
+    for (int d = 0; d < depth; ++d) tc::mbar_init(bars_a + 8 * d, (boxes ? 1 : 0) + (MODE == kAny ? 32 : 0));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -470,10 +470,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
         }
       } else {
         // with 32-element blocks a box holds two steps' words
-        const int o = BLOCK == 32 && (MODE == kBoxed || (MODE == kAny && p.words == kBoxed)) ? (4 * g + (t >> 1) + 2 * (st & 1)) * 4 : lane * 4;
+        const int o = BLOCK == 32 && MODE == kBoxed ? (4 * g + (t >> 1) + 2 * (st & 1)) * 4 : lane * 4;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) codes[i] = *reinterpret_cast<const uint32_t *>(wl + 128 * i + o);
-        if (MODE == kAny && p.words == kPieces && cut) {
+        if (MODE == kAny && cut) {
 #pragma unroll
           for (int i = 0; i < kGroups; ++i)
             codes[i] = __funnelshift_r(codes[i], *reinterpret_cast<const uint32_t *>(wl + next_at + next_hop * i), bit);
