@@ -448,6 +448,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
   int flying = 0;    // stages in flight when it did
   for (int r = 0; r < p.rounds; ++r) {
     float acc[NT][kPairs][4] = {};
+    int largest[kGroups] = {};  // E8M0 codes of the rows
     const int half = kRows == 16 ? ((tile0 + r * group) >> 2 & 1) * 8 : 0;  // kTiled: words 0, 1 or 2, 3
     int xo = (s0 - c0) * 512;
     const float *sxl = sx + (s0 - c0) * kCols + 2 * t;
@@ -492,8 +493,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
           top[i] = max((int)(codes[i] & 255u), (int)((codes[i] >> 8) & 255u));
           top[i] = max(top[i], __shfl_xor_sync(~0u, top[i], 1));
           top[i] = max(top[i], __shfl_xor_sync(~0u, top[i], 2));
-          // 2^(top - 127) / 2^13; 255 is NaN
-          f[i] = top[i] == 255 ? __uint_as_float(0x7FC00000u) : pow2(top[i] - 140);
+          f[i] = pow2(top[i] - 140);  // 2^(top - 127) / 2^13
+          largest[i] = max(largest[i], top[i]);
         }
       }
       float d[NT][kPairs][4] = {};
@@ -560,6 +561,15 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) k_matvec(const __grid_const
           }
       }
       sxl += kCols;
+    }
+    if (KIND == kMXFP4) {  // 255 is NaN
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i)
+        if (largest[i] == 255) {
+#pragma unroll
+          for (int c = 0; c < NT; ++c)
+            acc[c][i >> 1][2 * (i & 1)] = acc[c][i >> 1][2 * (i & 1) + 1] = __uint_as_float(0x7FC00000u);
+        }
     }
     // join the parts of the tiles of this round, in K order; a warp whose tile
     // is its own joins nothing and waits for nobody
