@@ -6,8 +6,8 @@ import torch
 
 import fp4_block_scaled_quantize_gb300 as fq
 from gpu_util import need_gpu
-from serve_ref import HALF_ULP, TINY, attention
-from test_serve_gpu import BF, F32, HF, MMA, MX, NV, PLAIN, UE, UE32, cache, close, gen, pool, random_copy
+from serve_ref import HALF_ULP, TINY, attention, tile
+from test_serve_gpu import BF, F32, HF, MMA, MX, NV, PLAIN, UE, UE32, cache, check_matvec, close, gen, pool, random_copy
 
 pytestmark = pytest.mark.gpu
 
@@ -98,6 +98,21 @@ def test_matvec_padding_of_the_tiled_scales_has_no_effect(fmt, blocks, m):
     for code in (0xFF, 0x7F, 0xFE, 0x80):
         view[~inside] = code
         assert torch.equal(fq.matvec(x, w, out_dtype=F32), y), code
+
+
+@pytest.mark.parametrize("layout", [PLAIN, MMA])
+@pytest.mark.parametrize("m", [1, 9])
+def test_matvec_e8m0_codes_of_every_size(layout, m):
+    """Rows whose codes span 30 binades each, from 2^-107 to 2^103."""
+    n, k = 181, 1152
+    w = random_copy(n, k, MX, PLAIN, seed=70)
+    codes = 20 + torch.arange(n)[:, None] + torch.randint(0, 31, (n, k // 32), generator=gen(71))
+    codes = codes.to(torch.uint8)
+    sf = tile(codes) if layout == MMA else codes.contiguous().view(-1)
+    w = fq.Quantized(w.q, sf.cuda(), w.s_dec, None, MX, layout)
+    x = torch.randn(m, k, generator=gen(72)).cuda()
+    check_matvec(x.to(BF), w, F32)
+    check_matvec(x.to(HF), w, F32)
 
 
 @pytest.mark.parametrize("layout", [PLAIN, MMA])
