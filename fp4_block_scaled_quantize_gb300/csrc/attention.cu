@@ -1,8 +1,8 @@
 // attention.cu -- attention of one new token per sequence over a paged cache
 // (sm_103a):  out = sum_j w_j v_j,  w = softmax_j(scale q . k_j).
 //
-// Bound: HBM, every key and value of the seen positions read once (4 D bytes
-// per position and key head); at 6.8 TB/s an SM moves 23 bytes a clock, so the
+// Bound: HBM, every key and value of the seen positions read once for each 8 NT
+// query heads that share them (4 D bytes per position and key head); at 6.8 TB/s an SM moves 23 bytes a clock, so the
 // 2 x 8 NT MMAs per 16 positions are cheap even on the m16n8k16 path, and no
 // part of the cache needs to pass through shared memory.
 //
@@ -12,7 +12,9 @@
 // need no reduction over lanes and no rescaling.  A weight enters its product
 // with the values as two 16-bit parts (hi + lo, 2^-16 of it left out; f16:
 // 2^-32 of the largest if that is more) and the sum l as it is, so rounding
-// weights costs no accuracy; the products are summed in binary32.
+// weights costs no accuracy; the products are summed in binary32.  A warp that
+// meets a value that is not finite goes over its part again with hi alone, for
+// the sums that are not finite; the others keep the first pass.
 //
 // Layout.  Query heads that share a key head are the 8 columns of an MMA (NT
 // tiles of 8), positions or head elements its 16 rows:
@@ -34,10 +36,11 @@
 // repeat exactly.  Short rows go to clusters instead, which join in their
 // shared memory (cluster_of).
 // Measured: 64 sequences of up to 16384 positions, 32 heads over 8 of 128,
-// BF16: 315 us (6.8 TB/s, a copy's rate); one of 131071: 87 us (91%), 3 us of
-// them the join; 96 windows of 1000, 16 heads of 64: 75 - 83 us (63 - 69%, the chain of
-// instructions of each 32 positions, with 12 warps an SM); one of 300: 6.3 us
-// (by one CTA 8.5).
+// BF16: 313 - 324 us (97 - 101% of a copy's rate); one of 131071: 87 us (91%),
+// 3 us of them the join; 96 windows of 1000, 16 heads of 64: 76 - 84 us (62 -
+// 68%: loads a step ahead in registers, which 12 warps an SM do not cover; a
+// quarter of the issue slots is used); one of 300: 6.3 us in a graph (by one CTA
+// 8.5).
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -51,9 +54,9 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-// Groups of 16 positions a warp takes a step: what it keeps in flight (heads
-// of 64, 96 windows of 1000: 82 us, with one group 88; heads of 128: 329 us,
-// with two groups and two CTAs an SM 332).
+// Groups of 16 positions a warp takes a step: what it keeps in flight.  When
+// this was chosen, heads of 64, 96 windows of 1000: 82 us, with one group 88;
+// heads of 128, 64 sequences: 329 us, with two groups and two CTAs an SM 332.
 constexpr int units_of(int dp) { return dp <= 64 ? 2 : 1; }
 constexpr int tile_of(int dp) { return 16 * units_of(dp); }
 constexpr int kPerSM = 5;            // CTAs per SM at most (workspace bound)
@@ -800,8 +803,9 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
 // Joins partial rows.  Many rows are cut into few parts each: narrow CTAs, of
 // which CTA c takes the row in which slice c + 1 begins, if it began in slice
 // c (so every cut row has one).  Few rows are cut into many: wide CTAs, one
-// for each row.  Which parts a row has follows from the lengths, before the
-// main grid is waited for.  A CTA's threads take eight outputs each, in groups
+// for each row.  Which parts a row has follows from the lengths, which are read
+// before the main grid is waited for: that grid is an ordinary launch, so what
+// came before it on the stream is complete.  A CTA's threads take eight outputs each, in groups
 // that walk every kGroups-th part four at a time; the first joins the groups.
 constexpr int kNarrow = 128, kWide = 1024;
 template <typename T, int DP, int NT, int THREADS>
@@ -885,7 +889,10 @@ __global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constan
 
 constexpr int dp_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256; }
 // Two tiles of 8 heads where a key head serves more than 8, but not for wide
-// heads: their queries and sums would not fit the registers.
+// heads: their queries and sums would not fit the registers.  Further heads are
+// rows of their own, which read the same keys and values again, in part from
+// L2 (32 sequences of 4000, one key head: of 256, 8 heads 31.6 us, 16 heads
+// 42.6; of 128, 16 heads 23.2, 32 heads 29.9).
 constexpr int nt_of(int share, int dp) { return share > 8 && dp <= 128 ? 2 : 1; }
 
 // CTAs (a cluster) that take a row of up to `reach` positions between them,

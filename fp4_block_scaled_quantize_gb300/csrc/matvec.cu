@@ -6,11 +6,11 @@
 // 23 clocks, 90 issue slots, for every 16 x 64 weights, and two instructions a
 // pair (decode, scale) already take 32 of them; so the rest of the arithmetic
 // is the m16n8k16 f16 MMA with the weight as its 16-row operand and up to 8 NT
-// tokens as columns.  (tcgen05 reads its operands from shared or tensor
-// memory: 4-bit weights would have to be decoded into it first, for a 128-row
-// tile of which all but M columns of work are padding.)
-// Measured (131072 x 4096, NVFP4): 1 token 53.4 us (5.7 TB/s, 84% of a copy),
-// 8 tokens 59.7 us (75%), 16 tokens 81 us (57%): instruction issue, about 480
+// tokens as columns.  (tcgen05 multiplies 4-bit weights as they lie only with
+// activations of at most 8 bits: 16-bit ones would have to be split into parts,
+// or the weights decoded into shared or tensor memory first.)
+// Measured (131072 x 4096, NVFP4): 1 token 52.2 us (5.8 TB/s, 85% of a copy),
+// 8 tokens 58.9 us (76%), 16 tokens 81 us (57%): instruction issue, about 480
 // instructions for 32 x 256 weights and 8 tokens of which 304 decode, scale
 // and multiply, at half an instruction a clock and scheduler.  4096 x 14336,
 // 1 token: 11.3 us behind another of its kind (a dependent launch: barriers and
@@ -66,8 +66,8 @@ constexpr int kMaxSmem = 227 * 1024;
 constexpr int kMaxWarps = 16;
 // Weight rows of a tile: two MMA row tiles share the loads of x; with two
 // token tiles one, so that 16 warps have the registers and, beside twice the
-// x, the shared memory (131072 x 4096, 16 tokens: 95 us, with 32 rows and 12
-// warps 103).
+// x, the shared memory (131072 x 4096, 16 tokens, when this was chosen: 95 us,
+// with 32 rows and 12 warps 103; 81 now).
 constexpr int rows_of(int nt) { return nt == 1 ? 32 : 16; }
 constexpr int payload_of(int nt) { return rows_of(nt) * kStep / 2; }  // bytes of a stage
 
@@ -160,7 +160,7 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 //   kPieces: plain rows of any other pitch, by 4-byte cp.async: the whole words
 //     that a row's bytes lie in, in the same places.  Where rows do not begin
 //     with words, a lane's codes are cut out of two words as they are read,
-//     and each row has one word more from 512 on.  (30000 x 2064, 1 token: 19.5
+//     and each row has one word more from 512 on.  (30000 x 2064, 1 token: 18.2
 //     us; with byte loads, which a fill waited for, 35.1.)
 enum Words { kTiled = 0, kBoxed = 1, kPieces = 2 };
 // A kernel's MODE is kTiled or kBoxed with the payload by TMA, or kAny: tiled

@@ -10,7 +10,8 @@ to the layer's output through the serving operators.
 table and the lengths on the device; ``FP4DecodeAttention`` holds the two
 weights as the FP4 copies that training's GEMMs read (tensor-core scale
 layout, 2D tiles), so a weight trained with ``FP4Linear`` serves as it was
-trained.  A step allocates nothing but its outputs and waits for nothing, so
+trained.  A step waits for nothing on the host and allocates its results, the
+tensors between the calls and attention's workspace from torch's pool alone, so
 it can be captured in a CUDA graph once the pages it needs are reserved.
 """
 import torch
