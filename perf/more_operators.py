@@ -230,7 +230,7 @@ def prepare(case, seed):
             j = torch.arange(b, device=dev)
             look = pos[:, None] // b * b + j
             s["look_pos"] = torch.where(look <= pos[:, None], look, -1).to(torch.int32).view(-1)
-            s["look_seq"] = torch.arange(t, device=dev, dtype=torch.int32)[:, None].expand(t, b).reshape(-1)
+            s["look_seq"] = torch.arange(t, device=dev, dtype=torch.int32)[:, None].repeat(1, b).view(-1)
             # only the last pages of each sequence are at hand: earlier ones hold nothing that is looked at
             s["table"] = torch.randperm(2 * n, generator=gen, device=dev)[:n, None].expand(n, -(-last // page)).to(torch.int32).contiguous()
             count = 2 * n
