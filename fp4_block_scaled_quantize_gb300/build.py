@@ -39,6 +39,9 @@ UNITS = {
     "matvec.cu": [],
     "append.cu": [],
     "attention.cu": [],
+    "attention8.cu": [],
+    "append8.cu": [],
+    "plan.cu": [],
 }
 
 

@@ -363,6 +363,63 @@ fp4_status check_cache(const fp4_kv_cache &c) {
   return FP4_OK;
 }
 
+bool whole16(int64_t a, int64_t b, int64_t c) { return a % 16 == 0 && b % 16 == 0 && c % 16 == 0; }
+
+// A cache in 8 bits: its codes and scales.
+fp4_status check_scales(const fp4_kv_cache &c, const fp4_kv_scales &s) {
+  if (s.block < 1 || s.k_page < 0 || s.k_block < 0 || s.k_head < 0 || s.v_page < 0 || s.v_block < 0 || s.v_head < 0)
+    return FP4_ERR_INVALID_ARG;
+  if (c.page_size % s.block != 0 || c.head_dim % 16 != 0) return FP4_ERR_SHAPE;
+  if (c.pages > 0 && (!s.k_sf || !s.v_sf)) return FP4_ERR_INVALID_ARG;
+  if (!aligned16(c.k) || !aligned16(c.v) || !whole16(c.k_page, c.k_place, c.k_head) ||
+      !whole16(c.v_page, c.v_place, c.v_head))
+    return FP4_ERR_ALIGNMENT;
+  return FP4_OK;
+}
+
+fp4_status check_append(const fp4_append_params &a) {
+  const fp4_append_params *const p = &a;
+  const fp4_status st = check_cache(p->cache);
+  if (st != FP4_OK) return st;
+  if (p->tokens < 0 || p->rope_len < 0 || p->rot_dim < 0) return FP4_ERR_INVALID_ARG;
+  if (p->k_token < 0 || p->k_head < 0 || p->v_token < 0 || p->v_head < 0) return FP4_ERR_INVALID_ARG;
+  if (p->rot_dim % 2 != 0 || p->rot_dim > p->cache.head_dim || p->tokens > INT32_MAX / 2)
+    return FP4_ERR_SHAPE;
+  if (p->q) {
+    if (!p->q_out || p->heads < 1 || p->q_token < 0 || p->q_head < 0 || p->qo_token < 0 ||
+        p->qo_head < 0)
+      return FP4_ERR_INVALID_ARG;
+    if (p->heads % p->cache.kv_heads != 0) return FP4_ERR_SHAPE;
+    if (!aligned_to(p->q, 2) || !aligned_to(p->q_out, 2)) return FP4_ERR_ALIGNMENT;
+  }
+  if (p->tokens == 0) return FP4_OK;
+  if (!p->k || !p->v || !p->pos || (p->rot_dim > 0 && p->rope_len > 0 && !p->rope))
+    return FP4_ERR_INVALID_ARG;
+  if (!aligned_to(p->k, 2) || !aligned_to(p->v, 2) || !aligned4(p->pos) || !aligned4(p->seq) ||
+      !aligned4(p->rope))
+    return FP4_ERR_ALIGNMENT;
+  return FP4_OK;
+}
+
+fp4_status check_attention(const fp4_attention_params &a) {
+  const fp4_attention_params *const p = &a;
+  const fp4_kv_cache &c = p->cache;
+  const fp4_status st = check_cache(c);
+  if (st != FP4_OK) return st;
+  if (p->heads < 1 || p->window < 0 || p->sinks < 0 || p->q_seq < 0 || p->q_head < 0 || p->out_seq < 0 ||
+      p->out_head < 0)
+    return FP4_ERR_INVALID_ARG;
+  if (p->heads % c.kv_heads != 0 || c.head_dim % 8 != 0) return FP4_ERR_SHAPE;
+  if (c.seqs == 0) return FP4_OK;
+  if (!p->lengths || !p->q || !p->out) return FP4_ERR_INVALID_ARG;
+  if (!aligned4(p->lengths) || !aligned4(p->lse) || !aligned_to(p->out, 2)) return FP4_ERR_ALIGNMENT;
+  if (!aligned16(p->q) || !aligned16(c.k) || !aligned16(c.v) || p->q_seq % 8 != 0 ||
+      p->q_head % 8 != 0 || !whole8(c.k_page, c.k_place, c.k_head) ||
+      !whole8(c.v_page, c.v_place, c.v_head))
+    return FP4_ERR_ALIGNMENT;
+  return aligned16(p->workspace) ? FP4_OK : FP4_ERR_ALIGNMENT;
+}
+
 }  // namespace
 
 extern "C" {
@@ -413,26 +470,54 @@ fp4_status fp4_matvec(const fp4_operand *W, int32_t sf_layout, const void *x, in
 
 fp4_status fp4_kv_append(const fp4_append_params *p, void *stream) {
   if (!p) return FP4_ERR_INVALID_ARG;
-  const fp4_status st = check_cache(p->cache);
-  if (st != FP4_OK) return st;
-  if (p->tokens < 0 || p->rope_len < 0 || p->rot_dim < 0) return FP4_ERR_INVALID_ARG;
-  if (p->k_token < 0 || p->k_head < 0 || p->v_token < 0 || p->v_head < 0) return FP4_ERR_INVALID_ARG;
-  if (p->rot_dim % 2 != 0 || p->rot_dim > p->cache.head_dim || p->tokens > INT32_MAX / 2)
-    return FP4_ERR_SHAPE;
-  if (p->q) {
-    if (!p->q_out || p->heads < 1 || p->q_token < 0 || p->q_head < 0 || p->qo_token < 0 ||
-        p->qo_head < 0)
-      return FP4_ERR_INVALID_ARG;
-    if (p->heads % p->cache.kv_heads != 0) return FP4_ERR_SHAPE;
-    if (!aligned_to(p->q, 2) || !aligned_to(p->q_out, 2)) return FP4_ERR_ALIGNMENT;
-  }
-  if (p->tokens == 0) return FP4_OK;
-  if (!p->k || !p->v || !p->pos || (p->rot_dim > 0 && p->rope_len > 0 && !p->rope))
-    return FP4_ERR_INVALID_ARG;
-  if (!aligned_to(p->k, 2) || !aligned_to(p->v, 2) || !aligned4(p->pos) || !aligned4(p->seq) ||
-      !aligned4(p->rope))
-    return FP4_ERR_ALIGNMENT;
+  const fp4_status st = check_append(*p);
+  if (st != FP4_OK || p->tokens == 0) return st;
   return launch_kv_append(*p, as_stream(stream));
+}
+
+fp4_status fp4_kv_append8(const fp4_append8_params *p, void *stream) {
+  if (!p) return FP4_ERR_INVALID_ARG;
+  fp4_status st = check_append(p->base);
+  if (st != FP4_OK) return st;
+  st = check_scales(p->base.cache, p->scales);
+  if (st != FP4_OK || p->base.tokens == 0) return st;
+  return launch_kv_append8(*p, as_stream(stream));
+}
+
+fp4_status fp4_kv_read(const fp4_read_params *p, void *stream) {
+  if (!p) return FP4_ERR_INVALID_ARG;
+  fp4_status st = check_cache(p->cache);
+  if (st != FP4_OK) return st;
+  const fp4_kv_cache &c = p->cache;
+  if (p->scales.k_sf || p->scales.v_sf) {
+    st = check_scales(c, p->scales);
+    if (st != FP4_OK) return st;
+  }
+  if (p->tokens < 0 || p->k_token < 0 || p->k_out_head < 0 || p->v_token < 0 || p->v_out_head < 0)
+    return FP4_ERR_INVALID_ARG;
+  if (c.head_dim % 8 != 0 || p->tokens > INT32_MAX / 2) return FP4_ERR_SHAPE;
+  if (p->tokens == 0) return FP4_OK;
+  if (!p->k_out || !p->v_out || !p->pos) return FP4_ERR_INVALID_ARG;
+  if (!aligned16(c.k) || !aligned16(c.v) || !aligned16(p->k_out) || !aligned16(p->v_out) || !aligned4(p->pos) ||
+      !aligned4(p->seq) || !whole8(c.k_page, c.k_place, c.k_head) || !whole8(c.v_page, c.v_place, c.v_head) ||
+      !whole8(p->k_token, p->k_out_head, 0) || !whole8(p->v_token, p->v_out_head, 0))
+    return FP4_ERR_ALIGNMENT;
+  return launch_kv_read(*p, as_stream(stream));
+}
+
+fp4_status fp4_page_plan(const fp4_plan_params *p, void *stream) {
+  if (!p || p->seqs < 0 || p->seq_pages < 0 || p->page_size < 1 || p->pool_pages < 0 || p->table_stride < 0)
+    return FP4_ERR_INVALID_ARG;
+  if ((int64_t)p->seq_pages * p->page_size > INT32_MAX - 1024 || p->pool_pages > INT32_MAX - 2 ||
+      p->tokens > INT32_MAX / 2)
+    return FP4_ERR_SHAPE;
+  if (!p->pool || (p->seqs > 0 && (!p->new_tokens || !p->lengths || !p->room)) ||
+      (p->seqs > 0 && p->seq_pages > 0 && !p->table))
+    return FP4_ERR_INVALID_ARG;
+  if (!aligned4(p->new_tokens) || !aligned4(p->lengths) || !aligned4(p->room) || !aligned4(p->table) ||
+      !aligned4(p->pool) || !aligned4(p->offsets) || !aligned4(p->seq) || !aligned4(p->pos) || !aligned_to(p->slot, 8))
+    return FP4_ERR_ALIGNMENT;
+  return launch_page_plan(*p, as_stream(stream));
 }
 
 int64_t fp4_decode_attention_workspace(int32_t seqs, int64_t room, int32_t heads,
@@ -443,27 +528,36 @@ int64_t fp4_decode_attention_workspace(int32_t seqs, int64_t room, int32_t heads
   return seqs == 0 ? 0 : decode_attention_workspace(seqs, room, heads, kv_heads, head_dim);
 }
 
+int64_t fp4_decode_attention8_workspace(int32_t seqs, int64_t room, int32_t heads,
+                                        int32_t kv_heads, int32_t head_dim) {
+  if (seqs < 0 || room < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || head_dim < 1 ||
+      head_dim > 256 || head_dim % 16 != 0)
+    return -1;
+  return seqs == 0 ? 0 : decode_attention8_workspace(seqs, room, heads, kv_heads, head_dim);
+}
+
 fp4_status fp4_decode_attention(const fp4_attention_params *p, void *stream) {
   if (!p) return FP4_ERR_INVALID_ARG;
   const fp4_kv_cache &c = p->cache;
-  const fp4_status st = check_cache(c);
-  if (st != FP4_OK) return st;
-  if (p->heads < 1 || p->window < 0 || p->q_seq < 0 || p->q_head < 0 || p->out_seq < 0 ||
-      p->out_head < 0)
-    return FP4_ERR_INVALID_ARG;
-  if (p->heads % c.kv_heads != 0 || c.head_dim % 8 != 0) return FP4_ERR_SHAPE;
-  if (c.seqs == 0) return FP4_OK;
-  if (!p->lengths || !p->q || !p->out) return FP4_ERR_INVALID_ARG;
-  if (!aligned4(p->lengths) || !aligned4(p->lse) || !aligned_to(p->out, 2)) return FP4_ERR_ALIGNMENT;
-  if (!aligned16(p->q) || !aligned16(c.k) || !aligned16(c.v) || p->q_seq % 8 != 0 ||
-      p->q_head % 8 != 0 || !whole8(c.k_page, c.k_place, c.k_head) ||
-      !whole8(c.v_page, c.v_place, c.v_head))
-    return FP4_ERR_ALIGNMENT;
+  const fp4_status st = check_attention(*p);
+  if (st != FP4_OK || c.seqs == 0) return st;
   const int64_t need = fp4_decode_attention_workspace(
       c.seqs, (int64_t)c.seq_pages * c.page_size, p->heads, c.kv_heads, c.head_dim);
   if (need > 0 && (!p->workspace || p->workspace_bytes < need)) return FP4_ERR_INVALID_ARG;
-  if (!aligned16(p->workspace)) return FP4_ERR_ALIGNMENT;
   return launch_decode_attention(*p, as_stream(stream));
+}
+
+fp4_status fp4_decode_attention8(const fp4_attention8_params *p, void *stream) {
+  if (!p) return FP4_ERR_INVALID_ARG;
+  const fp4_kv_cache &c = p->base.cache;
+  fp4_status st = check_attention(p->base);
+  if (st != FP4_OK) return st;
+  st = check_scales(c, p->scales);
+  if (st != FP4_OK || c.seqs == 0) return st;
+  const int64_t need = fp4_decode_attention8_workspace(
+      c.seqs, (int64_t)c.seq_pages * c.page_size, p->base.heads, c.kv_heads, c.head_dim);
+  if (need > 0 && (!p->base.workspace || p->base.workspace_bytes < need)) return FP4_ERR_INVALID_ARG;
+  return launch_decode_attention8(*p, as_stream(stream));
 }
 
 fp4_status fp4_gemm(const fp4_operand *A, const fp4_operand *B, int64_t M, int64_t N, int64_t K,

@@ -1,0 +1,391 @@
+// attention.cuh -- what the attention kernels over a paged cache share
+// (attention.cu: keys and values of 16 bits, attention8.cu: of 8): which
+// positions are seen, the list of tiles that warps share out, the tensor-core
+// and packing helpers, and the joins of partial rows.
+#pragma once
+#include <cmath>
+
+#include "serve.cuh"
+
+namespace fp4 {
+
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kPerSM = 5;            // CTAs per SM at most (workspace bound)
+constexpr int kCluster = 8;          // CTAs that take a row between them, at most
+constexpr float kSlack = 8.0f;       // log2 by which scores may pass the maximum in use
+
+struct AtParams {
+  fp4_attention_params p;
+  int groups;   // head groups of a key head: ceil(heads / kv_heads / (8 NT))
+  int share;    // heads / kv_heads
+  int tile;     // positions of a tile: 16 per unit
+  int ctas;     // CTAs of the main kernel
+  int direct;   // CTAs (a cluster) that take a row between them, or 0: equal slices
+  int shift;    // log2 page_size, or -1: no power of two
+  int out16;    // rows of out allow 16-byte stores
+  float scale2; // scale * log2 e
+  float *ws;    // [ctas][2] partial rows
+  uint32_t *status;
+};
+
+// Partial row: 8 NT x DP outputs, then m, l, seen (1.0 or 0.0) and whether
+// there is one (clusters) per head.
+constexpr int slot_floats(int cols, int dp) { return cols * (dp + 3 + 1); }
+
+__device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1, __nv_bfloat16) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1, __half) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <typename T>
+struct Bf16 {
+  static constexpr bool value = false;
+};
+template <>
+struct Bf16<__nv_bfloat16> {
+  static constexpr bool value = true;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint4 load16(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// Weights are held 2^lift times as large: f16's smallest is 2^-24, and a long
+// context may have most of its weight in small ones.
+template <typename T>
+__device__ __forceinline__ constexpr float lift() {
+  return Bf16<T>::value ? 0.0f : 7.0f;
+}
+
+// Two values as a pair of T, and what the pair leaves of them.
+template <typename T>
+__device__ __forceinline__ uint32_t pack(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t w) {
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+template <>
+__device__ __forceinline__ float2 unpack<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// What of a sequence is seen: positions [0, sinks) and [from, len), apart from
+// each other (sinks is 0 where they meet).  Its tiles are those of the first
+// positions, then those of the others, which start at base.
+struct Span {
+  int from, len, base, sinks, first, tiles;  // first: tiles of the first positions
+  // the seen positions [lo, hi) of tile i and the position where it starts
+  __device__ __forceinline__ int start(int i, int tile, int &lo, int &hi) const {
+    const bool early = i < first;
+    lo = early ? 0 : from;
+    hi = early ? sinks : len;
+    return early ? i * tile : base + (i - first) * tile;
+  }
+};
+__device__ __forceinline__ Span span_of(const AtParams &a, int s) {
+  const fp4_kv_cache &c = a.p.cache;
+  const int64_t room = (int64_t)c.seq_pages * c.page_size;  // fits 32 bits
+  const int given = a.p.lengths[s];
+  Span r;
+  r.len = given < 0 ? 0 : given > room ? (int)room : given;
+  r.from = a.p.window && r.len > a.p.window ? r.len - a.p.window : 0;
+  r.sinks = a.p.sinks;
+  if (r.from <= r.sinks) r.from = r.sinks = 0;
+  r.base = r.from & ~15;
+  r.first = (r.sinks + a.tile - 1) / a.tile;
+  r.tiles = r.first + (r.len - r.base + a.tile - 1) / a.tile;
+  return r;
+}
+
+// Prefix over the sequences: the sum of rows * tiles of all, and the sequence
+// in which a slice of the list begins (or the sequence `which`).
+struct Found {
+  int64_t total, start;  // start: list index of the found sequence's first tile
+  int64_t ctas;          // CTAs that share the list: a tile or more for each warp
+  int seq;
+};
+template <int THREADS>
+__device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *shared, int which = -1) {
+  constexpr int kW = THREADS / 32;
+  const int seqs = a.p.cache.seqs, per = (seqs + THREADS - 1) / THREADS;
+  if (seqs <= 32) {  // each warp by itself
+    const int lane = threadIdx.x & 31;
+    const int64_t sum = lane < seqs ? (int64_t)rows * span_of(a, lane).tiles : 0;
+    int64_t inc = sum;
+    for (int o = 1; o < seqs; o <<= 1) {
+      const int64_t v = __shfl_up_sync(~0u, inc, o);
+      if (lane >= o) inc += v;
+    }
+    Found f;
+    f.total = __shfl_sync(~0u, inc, seqs - 1);
+    f.ctas = min((int64_t)a.ctas, (f.total + kWarps - 1) / kWarps);
+    const int64_t x = slice < f.ctas ? f.total * slice / f.ctas : f.total;
+    const uint32_t hit = __ballot_sync(~0u, which < 0 ? x >= inc - sum && x < inc : lane == which);
+    f.seq = hit ? __ffs(hit) - 1 : seqs;
+    f.start = hit ? __shfl_sync(~0u, inc - sum, f.seq) : f.total;
+    return f;
+  }
+  const int s0 = threadIdx.x * per, s1 = min(s0 + per, seqs);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t sum = 0;
+  for (int s = s0; s < s1; ++s) sum += (int64_t)rows * span_of(a, s).tiles;
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(~0u, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) shared[warp] = inc;
+  __syncthreads();
+  int64_t before = inc - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kW; ++w) {
+    if (w < warp) before += shared[w];
+    total += shared[w];
+  }
+  const int64_t ctas = min((int64_t)a.ctas, (total + kWarps - 1) / kWarps);
+  const int64_t x = slice < ctas ? total * slice / ctas : total;
+  if (which < 0 ? x >= before && x < before + sum : which >= s0 && which < s1) {  // one thread, if any
+    int64_t at = before;
+    for (int s = s0;; ++s) {
+      const int64_t n = (int64_t)rows * span_of(a, s).tiles;
+      if (which < 0 ? x < at + n : s == which) {
+        shared[kW] = s;
+        shared[kW + 1] = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  Found f;
+  f.total = total;
+  f.ctas = ctas;
+  const bool found = which >= 0 || slice < ctas;
+  f.seq = found ? (int)shared[kW] : seqs;
+  f.start = found ? shared[kW + 1] : total;
+  return f;
+}
+
+// Eight outputs of a row, rounded once.
+template <typename T>
+__device__ __forceinline__ void store8(const AtParams &a, int s, int head, int d, const float *v) {
+  T *out = static_cast<T *>(a.p.out) + s * a.p.out_seq + head * a.p.out_head + d;
+  if (a.out16) {
+    *reinterpret_cast<uint4 *>(out) = make_uint4(pack<T>(v[0], v[1]), pack<T>(v[2], v[3]),
+                                                 pack<T>(v[4], v[5]), pack<T>(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = from_f32<T>(v[i]);
+  }
+}
+
+// log sum exp of a row: m + log2 l in base 2.
+template <typename T>
+__device__ __forceinline__ void store_lse(const AtParams &a, int s, int head, bool seen, float m, float l) {
+  a.p.lse[(int64_t)s * a.p.heads + head] =
+      seen ? ((m == -INFINITY ? 0.0f : m) + log2f(l) - lift<T>()) * 0.693147180559945f : -INFINITY;
+}
+
+// Eight outputs of a row joined from parts, one for each bit of `parts`:
+// m(i), l(i) are part i's statistics, add(i, w, v) adds w times its outputs.
+struct Joined {
+  float top, sum, v[8];
+};
+template <typename M, typename L, typename Add>
+__device__ __forceinline__ Joined join(uint32_t parts, M m, L l, Add add) {
+  Joined j;
+  j.top = -INFINITY;
+  j.sum = 0.0f;
+  for (uint32_t p = parts; p; p &= p - 1) j.top = fmaxf(j.top, m(__ffs(p) - 1));
+  const float base = j.top == -INFINITY ? 0.0f : j.top;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) j.v[e] = 0.0f;
+  for (uint32_t p = parts; p; p &= p - 1) {
+    const int i = __ffs(p) - 1;
+    const float w = ex2(m(i) - base);
+    j.sum = fmaf(w, l(i), j.sum);
+    add(i, w, j.v);
+  }
+  return j;
+}
+// The same of parts held side by side: get(q, st, lo, hi) reads part q (m, l,
+// seen, 1 and the outputs) if there is one.  All are requested together.
+struct Whole {
+  Joined j;
+  bool seen, there;
+};
+template <int N, typename Get>
+__device__ __forceinline__ Whole join_all(Get get) {
+  float4 st[N], lo[N], hi[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    st[q] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    lo[q] = hi[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    get(q, st[q], lo[q], hi[q]);
+  }
+  Whole r = {};
+  r.j.top = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    r.j.top = fmaxf(r.j.top, st[q].x);
+    r.seen |= st[q].z != 0.0f;
+    r.there |= st[q].w != 0.0f;
+  }
+  const float base = r.j.top == -INFINITY ? 0.0f : r.j.top;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const float w = ex2(st[q].x - base);
+    r.j.sum = fmaf(w, st[q].y, r.j.sum);
+    const float v[8] = {lo[q].x, lo[q].y, lo[q].z, lo[q].w, hi[q].x, hi[q].y, hi[q].z, hi[q].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.j.v[e] = fmaf(w, v[e], r.j.v[e]);
+  }
+  return r;
+}
+// Writes the result of a row that saw something (seen) or nothing.
+template <typename T>
+__device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d, Joined j, bool seen) {
+  const float w = seen ? 1.0f / j.sum : 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) j.v[e] *= w;
+  store8<T>(a, s, head, d, j.v);
+  if (a.p.lse && d == 0) store_lse<T>(a, s, head, seen, j.top, j.sum);
+}
+
+// Joins partial rows.  Many rows are cut into few parts each: narrow CTAs, of
+// which CTA c takes the row in which slice c + 1 begins, if it began in slice
+// c (so every cut row has one).  Few rows are cut into many: wide CTAs, one
+// for each row.  Which parts a row has follows from the lengths, which are read
+// before the main grid is waited for: that grid is an ordinary launch, so what
+// came before it on the stream is complete.  A CTA's threads take eight outputs each, in groups
+// that walk every kGroups-th part four at a time; the first joins the groups.
+constexpr int kNarrow = 128, kWide = 1024;
+template <typename T, int DP, int NT, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constant__ AtParams a) {
+  constexpr int kCols = 8 * NT, kItems = kCols * DP / 8;
+  constexpr int kGroups = THREADS < kItems ? 1 : THREADS / kItems;
+  __shared__ int64_t scan[THREADS / 32 + 2];
+  __shared__ float part_sh[kGroups][11][kItems];  // m, l, seen, eight outputs
+  const fp4_kv_cache &c = a.p.cache;
+  const int rows = c.kv_heads * a.groups, slice = blockIdx.x + 1;
+  const Found f = THREADS == kNarrow ? find<THREADS>(a, rows, slice, scan)
+                                     : find<THREADS>(a, rows, 0, scan, blockIdx.x / rows);
+  int s = f.seq, row = 0, first = 0, parts = 1;
+  if (s < c.seqs && span_of(a, s).tiles) {
+    const int tiles = span_of(a, s).tiles;
+    const int64_t at = f.total * slice / f.ctas;  // narrow: list index where the slice begins
+    row = THREADS == kNarrow ? (int)((at - f.start) / tiles) : blockIdx.x - s * rows;
+    const int64_t begin = f.start + (int64_t)row * tiles;
+    first = (int)(((begin + 1) * f.ctas - 1) / f.total);  // the CTA whose slice holds the row's first tile
+    parts = (int)(((begin + tiles) * f.ctas - 1) / f.total) - first + 1;
+    if (THREADS == kNarrow && (begin == at || first != (int)blockIdx.x)) parts = 1;
+  }
+  dependent_wait();  // also where there is nothing to do: this grid ends after the main one
+  launch_dependents();
+  if (parts == 1) return;
+  const int kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
+  const int heads = min(kCols, (kvh + 1) * a.share - head0);
+  const int group = THREADS < kItems ? 0 : threadIdx.x / kItems;
+  for (int item = threadIdx.x % kItems; item < kItems; item += THREADS < kItems ? THREADS : kItems) {
+    const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
+    if (group < kGroups) {
+      float m = -INFINITY, l = 0.0f, any = 0.0f, v[8] = {};
+      constexpr int kBatch = 4;
+      for (int w0 = group; w0 < parts; w0 += kBatch * kGroups) {
+        float4 st[kBatch], lo[kBatch], hi[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int w = w0 + i * kGroups;
+          st[i] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+          lo[i] = hi[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (w >= parts) continue;
+          const float *slot = a.ws + ((int64_t)(first + w) * 2 + (w == 0)) * slot_floats(kCols, DP);
+          if (col < heads && d < c.head_dim) {  // what was written
+            st[i] = *reinterpret_cast<const float4 *>(slot + kCols * DP + col * 4);
+            lo[i] = *reinterpret_cast<const float4 *>(slot + col * DP + d);
+            hi[i] = *reinterpret_cast<const float4 *>(slot + col * DP + d + 4);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const float now = fmaxf(m, st[i].x), base = now == -INFINITY ? 0.0f : now;
+          const float fo = ex2(m - base), fn = ex2(st[i].x - base);
+          m = now;
+          l = l * fo + st[i].y * fn;
+          any = fmaxf(any, st[i].z);
+          const float p[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = v[e] * fo + p[e] * fn;
+        }
+      }
+      part_sh[group][0][item] = m;
+      part_sh[group][1][item] = l;
+      part_sh[group][2][item] = any;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part_sh[group][3 + e][item] = v[e];
+    }
+    if (kGroups > 1) __syncthreads();  // (then the loop runs once, for every thread)
+    if (group != 0 || col >= heads || d >= c.head_dim) continue;
+    bool seen = false;
+    for (int w = 0; w < kGroups; ++w) seen |= part_sh[w][2][item] != 0.0f;
+    const Joined j = join(
+        (1u << kGroups) - 1, [&](int w) { return part_sh[w][0][item]; },
+        [&](int w) { return part_sh[w][1][item]; },
+        [&](int w, float fw, float *v) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = fmaf(fw, part_sh[w][3 + e][item], v[e]);
+        });
+    finish<T>(a, s, head0 + col, d, j, seen);
+  }
+}
+
+constexpr int dp_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : d <= 192 ? 192 : 256; }
+// Two tiles of 8 heads where a key head serves more than 8, but not for wide
+// heads: their queries and sums would not fit the registers.  Further heads are
+// rows of their own, which read the same keys and values again, in part from
+// L2 (32 sequences of 4000, one key head: of 256, 8 heads 31.6 us, 16 heads
+// 42.6; of 128, 16 heads 23.2, 32 heads 29.9).
+constexpr int nt_of(int share, int dp) { return share > 8 && dp <= 128 ? 2 : 1; }
+
+}  // namespace
+
+}  // namespace fp4

@@ -1,0 +1,694 @@
+// attention8.cu -- attention of one new token per sequence over a paged cache
+// of E4M3 codes with a power-of-two scale for each block of tokens and head
+// (sm_103a):  out = sum_j w_j 2^ev_j cv_j,  w = softmax_j(scale q . 2^ek_j ck_j).
+//
+// Bound: HBM, 2 D bytes per position and key head, half of what 16 bits move,
+// so twice the positions per time: at 6.8 TB/s an SM has 178 clocks for 16
+// positions of a head of 128, in which they take ~230 instructions of a warp.
+//
+// Mathematics.  Codes become f16 exactly (one conversion a pair) and meet the
+// queries, held in f16 times a power of two per head (exact down to 2^-38 of
+// the head's largest element, 2^-31 for BF16's eight bits), in MMAs that sum in
+// binary32.  A score is that sum times two powers of two and scale log2 e.  The
+// values' scales go into the weights: with s_j the score in base 2 the sum l
+// takes 2^(s_j - m), the product with the codes 2^(s_j + ev_j - mo), each with a
+// running maximum of its own, so whatever the scales are, the terms that make
+// the result are held to full precision; 2^(mo - m) is applied at the end.  Both
+// maxima are moved only when passed by more than 8.  A weight enters its
+// product as two f16 parts (2^-22 of it left out, or 2^-32 of the largest).
+//
+// Loads.  Asynchronous 16-byte copies into a ring of shared memory that each
+// warp fills for itself, kStages - 1 tiles ahead, across the rows of its slice.
+// A lane reads back what it copied itself, so no barrier is needed; scales are
+// requested with the copies and put beside them a step later.
+//
+// Layout, split and joins are those of attention.cu:
+//   S^T = K Q^T   lane (g, t) copies pieces 64 i + 16 t of keys g, g + 8
+//   O^T = V^T P^T lane (g, t) copies pieces 128 i + 16 g (or 8 g) of values
+//                 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+#include <cooperative_groups.h>
+
+#include "attention.cuh"
+
+namespace fp4 {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+struct At8Params {
+  AtParams a;
+  fp4_kv_scales s;
+  int block_shift;  // log2 of the block, or -1: no power of two
+};
+
+constexpr int kStages = 4;
+constexpr int kBlocks = 2;  // CTAs an SM holds at least
+constexpr float kLift = 7.0f;  // weights are held 2^7 times as large (f16's smallest is 2^-24)
+
+// Groups of 16 positions a step.
+constexpr int units8(int dp) { return dp <= 64 ? 2 : 1; }
+
+// The ring of a warp, a stage: keys, values, then per unit 32 floats (the keys'
+// scales, the values' exponents) and the mask of what is seen.
+constexpr int info_bytes = 40 * 4;
+constexpr int unit_bytes(int dp) { return 32 * dp + info_bytes; }
+constexpr int ring_bytes(int dp) { return kStages * units8(dp) * unit_bytes(dp); }
+constexpr int part_bytes(int cols, int dp) { return cols * (dp + 8) * 4; }
+
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t to, const void *from, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(on ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t shared_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// Four E4M3 codes as two pairs of f16.
+__device__ __forceinline__ void halves(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// A slice of the list of tiles, walked row by row.
+struct Cursor {
+  int64_t at, end, start;  // start: list index of sequence s's first tile
+  Span sp;
+  int s, row, kvh, tile, tile1;
+  bool live;
+  __device__ __forceinline__ void begin(const AtParams &a, int s0, int64_t start0, int64_t at0, int64_t end0) {
+    s = s0, start = start0, at = at0, end = end0;
+    row = tile = tile1 = 0;
+    live = at < end;
+    sp = live ? span_of(a, s) : Span{};
+  }
+  // on to the next row of the slice; false (and not live) at its end
+  __device__ __forceinline__ bool next_row(const AtParams &a, int rows) {
+    live = at < end;
+    if (!live) return false;
+    while (at >= start + (int64_t)rows * sp.tiles) {
+      start += (int64_t)rows * sp.tiles;
+      sp = span_of(a, ++s);
+    }
+    row = (int)((at - start) / sp.tiles);
+    tile = (int)(at - start - (int64_t)row * sp.tiles);
+    tile1 = (int)min((int64_t)sp.tiles, tile + (end - at));
+    at += tile1 - tile;
+    kvh = row / a.groups;
+    return true;
+  }
+};
+
+template <typename T, int DP, int NT, bool UNITS>
+__global__ void __launch_bounds__(kThreads, kBlocks) k_attention8(const __grid_constant__ At8Params b) {
+  constexpr int kCols = 8 * NT, kKey = DP / 64, kV16 = DP / 128, kV8 = DP / 64 % 2, kWords = DP / 32;
+  constexpr int kUnits = units8(DP), kTile = 16 * kUnits, kParts = 2 * kWarps;
+  const AtParams &a = b.a;
+  extern __shared__ __align__(16) char smem8[];
+  __shared__ int64_t scan[kWarps + 2];
+  __shared__ int4 part_sh[kParts];  // sequence (-1: none), row, begins with it, ends with it
+  const fp4_kv_cache &c = a.p.cache;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int D = c.head_dim, rows = c.kv_heads * a.groups;
+  // the warps' rings; outputs of rows that a warp ended (a row that it began
+  // last and did not end takes the place of its ring); their m, l, seen, 1; the
+  // partial row of a CTA of a cluster
+  char *const ring = smem8 + warp * ring_bytes(DP);
+  char *const ended = smem8 + kWarps * ring_bytes(DP);
+  float4 *const st_sh = reinterpret_cast<float4 *>(ended + kWarps * part_bytes(kCols, DP));
+  float *const part = reinterpret_cast<float *>(st_sh + kParts * kCols);
+  auto part_of = [&](int p) {
+    return reinterpret_cast<float *>(p & 1 ? smem8 + (p >> 1) * ring_bytes(DP) : ended + (p >> 1) * part_bytes(kCols, DP));
+  };
+
+  int64_t at, end, start;
+  int s;
+  dependent_wait();
+  launch_dependents();
+  if (lane < 2) part_sh[2 * warp + lane] = make_int4(-1, 0, 0, 0);
+  __syncwarp();
+  const int rank = a.direct ? blockIdx.x % a.direct : 0, mine_row = a.direct ? blockIdx.x / a.direct : 0;
+  if (a.direct) {
+    s = mine_row / rows;
+    start = 0;
+    const int tiles = span_of(a, s).tiles;
+    at = (int64_t)(mine_row - s * rows) * tiles;
+    end = at + (int64_t)tiles * (rank + 1) / a.direct;
+    at += (int64_t)tiles * rank / a.direct;
+  } else {
+    const Found f = find<kThreads>(a, rows, blockIdx.x, scan);
+    s = f.seq;
+    start = f.start;
+    at = end = 0;
+    if (blockIdx.x < f.ctas) {
+      at = f.total * blockIdx.x / f.ctas;
+      end = f.total * (blockIdx.x + 1) / f.ctas;
+    }
+  }
+  // sequences that see nothing are in no slice: their rows are written here
+  for (int e = a.direct ? s : blockIdx.x; e < c.seqs; e += a.direct ? c.seqs : a.ctas) {
+    const int given = a.p.lengths[e];
+    if (a.direct && (rank || mine_row != s * rows)) break;
+    if (threadIdx.x == 0 && (given < 0 || given > (int64_t)c.seq_pages * c.page_size))
+      raise_status(a.status, kStatusIndex);
+    if (span_of(a, e).tiles) continue;
+    const float zero[8] = {};
+    for (int i = threadIdx.x; i < a.p.heads * (D / 8); i += kThreads) {
+      const int head = i / (D / 8), d = 8 * (i % (D / 8));
+      store8<T>(a, e, head, d, zero);
+      if (a.p.lse && d == 0) a.p.lse[(int64_t)e * a.p.heads + head] = -INFINITY;
+    }
+  }
+
+  // each warp takes a quarter of the slice by itself
+  Cursor use, put;  // the row that is worked on, the row whose tiles are copied
+  {
+    const int64_t n = end - at;
+    end = at + n * (warp + 1) / kWarps;
+    at += n * warp / kWarps;
+    use.begin(a, s, start, at, end);
+    put = use;
+  }
+
+  // page numbers a step ahead of the copies (their loads are not waited for).
+  // UNITS (pages of whole units): one for a unit, else lane i & 15 has that of
+  // position i.
+  auto ask = [&](int (&page)[kUnits]) {
+    int lo, hi;
+    const int pos = put.sp.start(put.tile, kTile, lo, hi);
+    const int32_t *table = c.table + put.s * c.table_stride;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int i = pos + 16 * u + (UNITS ? 0 : lane & 15);
+      page[u] = -1;
+      if (put.live && i < hi && (UNITS || i >= lo)) page[u] = table[a.shift >= 0 ? i >> a.shift : i / c.page_size];
+    }
+  };
+  // Copies the tile at `put` into a stage and requests its scales: lanes 0 - 15
+  // those of the keys of 16 positions, lanes 16 - 31 those of the values.
+  const char *const nothing = static_cast<const char *>(a.p.q);  // an address for copies of no bytes
+  auto copy = [&](int stage, const int (&pages)[kUnits], uint32_t (&code)[kUnits], uint32_t (&on)[kUnits]) {
+    int lo, hi;
+    const int pos = put.sp.start(put.tile, kTile, lo, hi);
+    const char *const keys = static_cast<const char *>(c.k) + put.kvh * c.k_head + 16 * t;
+    const char *const values = static_cast<const char *>(c.v) + put.kvh * c.v_head;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const uint32_t to = shared_at(ring) + (stage * kUnits + u) * unit_bytes(DP);
+      const int first = pos + 16 * u, page = pages[u], i = first + (lane & 15);
+      const bool ok = page >= 0 && page < c.pages, in = put.live && i >= lo && i < hi;
+      if (in && !ok && lane < 16) raise_status(a.status, kStatusIndex);
+      on[u] = __ballot_sync(~0u, in && ok) & 0xFFFFu;
+      const int place0 = a.shift >= 0 ? (UNITS ? first : i) & (c.page_size - 1) : (UNITS ? first : i) % c.page_size;
+      const int place = UNITS ? place0 + (lane & 15) : place0;
+      code[u] = 0;
+      if (in && ok) {
+        const int blk = b.block_shift >= 0 ? place >> b.block_shift : place / b.s.block;
+        code[u] = lane < 16 ? b.s.k_sf[(int64_t)page * b.s.k_page + blk * b.s.k_block + put.kvh * b.s.k_head]
+                            : b.s.v_sf[(int64_t)page * b.s.v_page + blk * b.s.v_block + put.kvh * b.s.v_head];
+      }
+      const int64_t k0 = (int64_t)page * c.k_page + (int64_t)place0 * c.k_place;
+      const int64_t v0 = (int64_t)page * c.v_page + (int64_t)place0 * c.v_place;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = g + 8 * h;
+        const char *k = keys + (UNITS ? k0 + j * c.k_place : __shfl_sync(~0u, k0, j));
+        const bool there = on[u] >> j & 1;
+#pragma unroll
+        for (int e = 0; e < kKey; ++e) {
+          const bool yes = there && 64 * e + 16 * t < D;
+          copy16(to + (h * kKey + e) * 512 + 16 * lane, yes ? k + 64 * e : nothing, yes);
+        }
+      }
+      const uint32_t tv = to + 16 * DP;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int j = 2 * t + (h & 1) + 8 * (h >> 1);
+        const char *v = values + (UNITS ? v0 + j * c.v_place : __shfl_sync(~0u, v0, j));
+        const bool there = on[u] >> j & 1;
+#pragma unroll
+        for (int e = 0; e < kV16; ++e) {
+          const bool yes = there && 128 * e + 16 * g < D;
+          copy16(tv + (h * kV16 + e) * 512 + 16 * lane, yes ? v + 128 * e + 16 * g : nothing, yes);
+        }
+        if (kV8) {
+          const bool yes = there && 128 * kV16 + 8 * g < D;
+          copy8(tv + 4 * kV16 * 512 + h * 256 + 8 * lane, yes ? v + 128 * kV16 + 8 * g : nothing, yes);
+        }
+      }
+    }
+    copies_commit();
+  };
+  // Puts the scales of a copied stage beside it.
+  auto settle = [&](int stage, const uint32_t (&code)[kUnits], const uint32_t (&on)[kUnits]) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      float *info = reinterpret_cast<float *>(ring + (stage * kUnits + u) * unit_bytes(DP) + 32 * DP);
+      const float e = code[u] == 255 ? NAN : (float)((int)code[u] - 127);
+      const float v = __uint_as_float(code[u] ? code[u] << 23 : 0x00400000u);
+      info[lane] = lane < 16 ? (code[u] == 255 ? NAN : v) : e;
+      if (lane == 0) info[32] = __uint_as_float(on[u]);
+    }
+  };
+  auto advance = [&] {
+    if (put.live && ++put.tile >= put.tile1) put.next_row(a, rows);
+  };
+
+  int page_next[kUnits];
+  {
+    int page[kStages - 1][kUnits];
+    uint32_t code[kStages - 1][kUnits], on[kStages - 1][kUnits];
+    put.next_row(a, rows);
+    Cursor ahead = put;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      ask(page[i]);
+      advance();
+    }
+    ask(page_next);
+    const Cursor later = put;
+    put = ahead;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      copy(i, page[i], code[i], on[i]);
+      advance();
+    }
+    put = later;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) settle(i, code[i], on[i]);
+  }
+
+  int stage = 0;
+  while (use.next_row(a, rows)) {
+    const int head0 = use.kvh * a.share + (use.row - use.kvh * a.groups) * kCols;
+    const int heads = min(kCols, (use.kvh + 1) * a.share - head0), tile0 = use.tile;
+
+    // queries, times a power of two per head; heads past the group's repeat as zero
+    uint32_t q[NT][kKey][8];
+    float qs[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      uint4 raw[kKey][2];
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kKey; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int d = 64 * i + 16 * t + 8 * h;
+          raw[i][h] = 8 * n + g < heads && d < D
+                          ? load16(static_cast<const T *>(a.p.q) + use.s * a.p.q_seq + (head0 + 8 * n + g) * a.p.q_head + d)
+                          : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {raw[i][h].x, raw[i][h].y, raw[i][h].z, raw[i][h].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 v = unpack<T>(w[j]);
+            top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+          }
+        }
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      // 2^e times the largest is at least 2^14 and below 2^15
+      const int e = top > 0.0f ? min(14 + 127 - (int)(__float_as_uint(top) >> 23), 126) : 0;
+      const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+      const float back = a.scale2 * __uint_as_float((uint32_t)(127 - e) << 23);
+      qs[n][0] = __shfl_sync(~0u, back, 8 * t);
+      qs[n][1] = __shfl_sync(~0u, back, 8 * t + 4);
+#pragma unroll
+      for (int i = 0; i < kKey; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t w[4] = {raw[i][h].x, raw[i][h].y, raw[i][h].z, raw[i][h].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 v = unpack<T>(w[j]);
+            q[n][i][4 * h + j] = pack<__half>(v.x * f, v.y * f);
+          }
+        }
+    }
+
+    float m[NT][2], mo[NT][2], l[NT][2], o[NT][2 * kWords][4];
+    bool seen = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = mo[n][0] = mo[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2 * kWords; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
+    }
+
+    for (; use.tile < use.tile1; ++use.tile) {
+      copies_wait<kStages - 2>();
+      __syncwarp();  // the scales that other lanes put there
+      uint32_t code_next[kUnits], on_next[kUnits];
+      const int free = stage == 0 ? kStages - 1 : stage - 1;
+      copy(free, page_next, code_next, on_next);
+      advance();
+      ask(page_next);
+
+      const char *const here = ring + stage * kUnits * unit_bytes(DP);
+      float sc[kUnits][NT][4], so[kUnits][NT][4];
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const uint4 *kp = reinterpret_cast<const uint4 *>(here + u * unit_bytes(DP)) + lane;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sc[u][n][0] = sc[u][n][1] = sc[u][n][2] = sc[u][n][3] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kKey; ++i) {
+          const uint4 k0 = kp[32 * i], k1 = kp[32 * (kKey + i)];
+          const uint32_t x[4] = {k0.x, k0.y, k0.z, k0.w}, y[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t x0, x1, y0, y1;
+            halves(x[j], x0, x1);
+            halves(y[j], y0, y1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma(sc[u][n], x0, y0, x1, y1, q[n][i][2 * j], q[n][i][2 * j + 1], __half());
+          }
+        }
+      }
+      // scores: lane (g, t) has positions g, g + 8 of heads 2 t, 2 t + 1
+      bool passed = false;
+      float base[NT][2], baseo[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          base[n][e] = m[n][e] == -INFINITY ? 0.0f : m[n][e];
+          baseo[n][e] = mo[n][e] == -INFINITY ? 0.0f : mo[n][e];
+          passed |= m[n][e] == -INFINITY || mo[n][e] == -INFINITY;
+        }
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const float *info = reinterpret_cast<const float *>(here + u * unit_bytes(DP) + 32 * DP);
+        const uint32_t on = __float_as_uint(info[32]);
+        const float ks[2] = {info[g], info[g + 8]}, ve[2] = {info[16 + g], info[24 + g]};
+        seen |= on != 0;
+        const bool on0 = on >> g & 1, on1 = on >> (g + 8) & 1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sc[u][n][e] = (e >> 1 ? on1 : on0) ? sc[u][n][e] * qs[n][e & 1] * ks[e >> 1] : -INFINITY;
+            so[u][n][e] = sc[u][n][e] + ve[e >> 1];
+            passed |= sc[u][n][e] > base[n][e & 1] + kSlack || so[u][n][e] > baseo[n][e & 1] + kSlack;
+          }
+      }
+      if (__any_sync(~0u, passed)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = m[n][e], topo = mo[n][e];
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+              top = fmaxf(top, fmaxf(sc[u][n][e], sc[u][n][2 + e]));
+              topo = fmaxf(topo, fmaxf(so[u][n][e], so[u][n][2 + e]));
+            }
+#pragma unroll
+            for (int x = 4; x <= 16; x <<= 1) {
+              top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+              topo = fmaxf(topo, __shfl_xor_sync(~0u, topo, x));
+            }
+            base[n][e] = top == -INFINITY ? 0.0f : top;
+            baseo[n][e] = topo == -INFINITY ? 0.0f : topo;
+            l[n][e] *= ex2(m[n][e] - base[n][e]);
+            const float fade = ex2(mo[n][e] - baseo[n][e]);
+            m[n][e] = top;
+            mo[n][e] = topo;
+#pragma unroll
+            for (int i = 0; i < 2 * kWords; ++i) {
+              o[n][i][e] *= fade;
+              o[n][i][2 + e] *= fade;
+            }
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            l[n][e & 1] += ex2(sc[u][n][e] - base[n][e & 1]);
+            w[e] = ex2(so[u][n][e] - (baseo[n][e & 1] - kLift));
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t p = pack<__half>(w[2 * h], w[2 * h + 1]);
+            const float2 r = unpack<__half>(p);
+            hi[n][h] = transpose8x8(p);
+            lo[n][h] = transpose8x8(pack<__half>(w[2 * h] - r.x, w[2 * h + 1] - r.y));
+          }
+        }
+        const char *vp = here + u * unit_bytes(DP) + 16 * DP;
+#pragma unroll
+        for (int i = 0; i < kV16 + kV8; ++i) {
+          uint32_t v[4][4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            if (i < kV16) {
+              const uint4 w = *reinterpret_cast<const uint4 *>(vp + (h * kV16 + i) * 512 + 16 * lane);
+              v[h][0] = w.x, v[h][1] = w.y, v[h][2] = w.z, v[h][3] = w.w;
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2 *>(vp + 4 * kV16 * 512 + h * 256 + 8 * lane);
+              v[h][0] = w.x, v[h][1] = w.y;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < (i < kV16 ? 4 : 2); ++j)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {  // rows g, g + 8: elements 2 p, 2 p + 1 of the word
+              uint32_t a0, a1, a2, a3;
+              halves(__byte_perm(v[0][j], v[1][j], p ? 0x7362 : 0x5140), a0, a1);
+              halves(__byte_perm(v[2][j], v[3][j], p ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                float *d = o[n][2 * (4 * i + j) + p];
+                mma(d, a0, a1, a2, a3, hi[n][0], hi[n][1], __half());
+                mma(d, a0, a1, a2, a3, lo[n][0], lo[n][1], __half());
+              }
+            }
+        }
+      }
+      settle(free, code_next, on_next);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    }
+
+    // the row's outputs relative to m, 2^lift<T>() times, as l
+    const bool whole = tile0 == 0 && use.tile1 == use.sp.tiles;
+    const int at_part = 2 * warp + (tile0 == 0);  // the warp's first row, or its last
+    if (!whole && lane == 0) part_sh[at_part] = make_int4(use.s, use.row, tile0 == 0, use.tile1 == use.sp.tiles);
+    float *const outs = part_of(at_part);
+    if (!whole && tile0 == 0) {  // every lane is done with the ring
+      copies_wait<0>();
+      __syncwarp();
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[n][e] * exp2f(lift<T>());
+        sum += __shfl_xor_sync(~0u, sum, 4);
+        sum += __shfl_xor_sync(~0u, sum, 8);
+        sum += __shfl_xor_sync(~0u, sum, 16);
+        const int col = 8 * n + 2 * t + e;
+        if (col >= heads) continue;
+        // (no maximum: nothing seen, or sums that are NaN already)
+        float w = m[n][e] == -INFINITY || mo[n][e] == -INFINITY ? 1.0f : ex2(mo[n][e] - m[n][e] - (kLift - lift<T>()));
+        if (whole) w = seen ? w / sum : 0.0f;
+#pragma unroll
+        for (int x = 0; x < kWords / 2; ++x) {
+          const int d = x < 2 * kV16 ? 128 * (x / 2) + 16 * g + 8 * (x % 2) : 128 * kV16 + 8 * g;
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[2 * j] = o[n][4 * x + j][e] * w;
+            v[2 * j + 1] = o[n][4 * x + j][2 + e] * w;
+          }
+          if (!whole) {
+            float4 *to = reinterpret_cast<float4 *>(outs + col * (DP + 8) + d);
+            to[0] = make_float4(v[0], v[1], v[2], v[3]);
+            to[1] = make_float4(v[4], v[5], v[6], v[7]);
+          } else if (d < D) {
+            store8<T>(a, use.s, head0 + col, d, v);
+          }
+        }
+        if (g == 0) {
+          if (!whole)
+            st_sh[at_part * kCols + col] = make_float4(m[n][e], sum, seen ? 1.0f : 0.0f, 1.0f);
+          else if (a.p.lse)
+            store_lse<T>(a, use.s, head0 + col, seen, m[n][e], sum);
+        }
+      }
+  }
+
+  // join the warps' parts, row by row
+  copies_wait<0>();
+  __syncthreads();
+  const int4 mine = part_sh[lane % kParts];
+  uint32_t there = __ballot_sync(~0u, mine.x >= 0) & ((1u << kParts) - 1);
+  bool partial = false;
+  while (there) {
+    const int i0 = __ffs(there) - 1;
+    const int s = __shfl_sync(~0u, mine.x, i0), row = __shfl_sync(~0u, mine.y, i0);
+    const bool begins = __shfl_sync(~0u, mine.z, i0);
+    const uint32_t parts = __ballot_sync(~0u, mine.x == s && mine.y == row) & there;
+    const bool whole = begins && __shfl_sync(~0u, mine.w, 31 - __clz(parts));
+    there &= ~parts;
+    const int kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
+    const int heads = min(kCols, (kvh + 1) * a.share - head0);
+    float *slot = a.direct ? part : a.ws + (blockIdx.x * 2 + begins) * (int64_t)slot_floats(kCols, DP);
+    partial = !whole;
+    for (int item = threadIdx.x; item < heads * (DP / 8); item += kThreads) {
+      const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
+      if (d >= D) continue;
+      const Whole r = join_all<kParts>([&](int q, float4 &st, float4 &lo, float4 &hi) {
+        if (!(parts >> q & 1)) return;
+        const float *from = part_of(q) + col * (DP + 8) + d;
+        st = st_sh[q * kCols + col];
+        lo = *reinterpret_cast<const float4 *>(from);
+        hi = *reinterpret_cast<const float4 *>(from + 4);
+      });
+      if (whole) {
+        finish<T>(a, s, head0 + col, d, r.j, r.seen);
+        continue;
+      }
+      const float *v = r.j.v;
+      float *out = slot + col * DP + d;
+      *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4 *>(out + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      if (d == 0)
+        *reinterpret_cast<float4 *>(slot + kCols * DP + col * 4) = make_float4(r.j.top, r.j.sum, r.seen ? 1.0f : 0.0f, 1.0f);
+    }
+  }
+  if (a.direct < 2) return;
+
+  // join the cluster's partial rows, an output piece a thread, in CTA order
+  if (!partial)
+    for (int i = threadIdx.x; i < slot_floats(kCols, DP); i += kThreads)
+      part[i] = i >= kCols * DP && i % 4 == 0 ? -INFINITY : 0.0f;
+  cg::this_cluster().sync();
+  const int row = mine_row - s * rows, kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
+  const int heads = min(kCols, (kvh + 1) * a.share - head0);
+  for (int item = threadIdx.x * a.direct + rank; item < heads * (DP / 8); item += kThreads * a.direct) {
+    const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
+    if (d >= D) continue;
+    const Whole r = join_all<kCluster>([&](int q, float4 &st, float4 &lo, float4 &hi) {
+      if (q >= a.direct) return;
+      const float *from = cg::this_cluster().map_shared_rank(part, q);
+      st = *reinterpret_cast<const float4 *>(from + kCols * DP + col * 4);
+      lo = *reinterpret_cast<const float4 *>(from + col * DP + d);
+      hi = *reinterpret_cast<const float4 *>(from + col * DP + d + 4);
+    });
+    if (r.there) finish<T>(a, s, head0 + col, d, r.j, r.seen);
+  }
+  cg::this_cluster().sync();  // nobody leaves while its part may be read
+}
+
+// CTAs (a cluster) that take a row of up to `reach` positions between them, as
+// in attention.cu; 0: equal slices.
+int cluster_of(int64_t rows, int64_t reach, int dp) {
+  const int64_t sms = sm_count(), fit = sms * kBlocks;
+  int n = 1;
+  while (n < kCluster && rows * 2 * n <= fit * 7 / 8 &&
+         (rows * 2 * n <= sms ? n : 2 * n) * kWarps * 16 * units8(dp) < reach)
+    n *= 2;
+  const int64_t most = rows > fit ? 128 : n == kCluster ? 2048 : 384 * n;
+  return reach <= most ? n : 0;
+}
+
+template <typename T, int DP, int NT, bool UNITS>
+fp4_status launch(At8Params b, cudaStream_t s) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> occupancy[kMaxDev];
+  constexpr int cols = 8 * NT;
+  constexpr size_t smem = kWarps * (ring_bytes(DP) + part_bytes(cols, DP)) + 2 * kWarps * cols * sizeof(float4);
+  constexpr size_t part = slot_floats(cols, DP) * sizeof(float);
+  static_assert(ring_bytes(DP) >= part_bytes(cols, DP), "a part takes the place of a ring");
+  auto kern = k_attention8<T, DP, NT, UNITS>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return FP4_ERR_CUDA;
+  int per = occupancy[dev].load(std::memory_order_acquire);
+  if (!per) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(smem + part)) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, kThreads, smem) != cudaSuccess || per < 1)
+      return FP4_ERR_CUDA;
+    occupancy[dev].store(per, std::memory_order_release);
+  }
+  AtParams &a = b.a;
+  const fp4_kv_cache &c = a.p.cache;
+  a.tile = 16 * units8(DP);
+  const int64_t rows = (int64_t)c.seqs * c.kv_heads * a.groups;
+  const int64_t room = (int64_t)c.seq_pages * c.page_size;
+  const int64_t most = (int64_t)sm_count() * (per < kPerSM ? per : kPerSM);
+  const int64_t tiles = ceil_div(rows * ceil_div(room, a.tile), kWarps);  // no more CTAs than the table has tiles
+  if (rows > INT32_MAX) return FP4_ERR_SHAPE;
+  const int64_t reach = (int64_t)a.p.window + 15 + ceil_div(a.p.sinks, a.tile) * a.tile;
+  a.direct = cluster_of(rows, a.p.window && reach < room ? reach : room, DP);
+  a.ctas = (int)(a.direct ? rows * a.direct : tiles < most ? tiles : most);
+  if (a.direct) {
+    const size_t bytes = smem + (a.direct > 1 ? part : 0);
+    return launch_dependent_clusters(kern, a.direct, dim3((unsigned)a.ctas), dim3(kThreads), bytes, s, b) == cudaSuccess
+               ? FP4_OK
+               : FP4_ERR_CUDA;
+  }
+  kern<<<(unsigned)a.ctas, kThreads, smem, s>>>(b);  // (an ordinary launch, as in attention.cu)
+  if (cudaGetLastError() != cudaSuccess) return FP4_ERR_CUDA;
+  if (a.ctas < 2) return FP4_OK;
+  const cudaError_t e =
+      rows * 4 <= a.ctas
+          ? launch_dependent(k_attention_join<T, DP, NT, kWide>, dim3((unsigned)rows), dim3(kWide), 0, s, a)
+          : launch_dependent(k_attention_join<T, DP, NT, kNarrow>, dim3((unsigned)a.ctas - 1), dim3(kNarrow), 0, s, a);
+  return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
+}
+
+template <typename T, int DP, int NT>
+fp4_status launch_pages(const At8Params &b, cudaStream_t s) {
+  return b.a.p.cache.page_size % 16 == 0 ? launch<T, DP, NT, true>(b, s) : launch<T, DP, NT, false>(b, s);
+}
+
+template <typename T>
+fp4_status launch_type(const At8Params &b, int nt, cudaStream_t s) {
+  switch (dp_of(b.a.p.cache.head_dim)) {
+    case 64: return nt == 1 ? launch_pages<T, 64, 1>(b, s) : launch_pages<T, 64, 2>(b, s);
+    case 128: return nt == 1 ? launch_pages<T, 128, 1>(b, s) : launch_pages<T, 128, 2>(b, s);
+    case 192: return launch_pages<T, 192, 1>(b, s);
+    default: return launch_pages<T, 256, 1>(b, s);
+  }
+}
+
+}  // namespace
+
+int64_t decode_attention8_workspace(int64_t seqs, int64_t room, int heads, int kv_heads, int head_dim) {
+  const int dp = dp_of(head_dim), nt = nt_of(heads / kv_heads, dp), cols = 8 * nt;
+  if (cluster_of(seqs * kv_heads * ceil_div(heads / kv_heads, cols), room, dp)) return 0;
+  return (int64_t)sm_count() * kPerSM * 2 * slot_floats(cols, dp) * sizeof(float);
+}
+
+fp4_status launch_decode_attention8(const fp4_attention8_params &p, cudaStream_t s) {
+  At8Params b{};
+  AtParams &a = b.a;
+  a.p = p.base;
+  b.s = p.scales;
+  a.status = status_word();
+  if (!a.status) return FP4_ERR_CUDA;
+  const fp4_kv_cache &c = a.p.cache;
+  a.share = a.p.heads / c.kv_heads;
+  const int nt = nt_of(a.share, dp_of(c.head_dim));
+  a.groups = (a.share + 8 * nt - 1) / (8 * nt);
+  a.shift = log2_or(c.page_size, -1);
+  b.block_shift = log2_or(b.s.block, -1);
+  a.out16 = aligned16(a.p.out) && a.p.out_seq % 8 == 0 && a.p.out_head % 8 == 0;
+  a.scale2 = a.p.scale * 1.44269504088896f;
+  a.ws = static_cast<float *>(a.p.workspace);
+  return c.type == FP4_BF16 ? launch_type<__nv_bfloat16>(b, nt, s) : launch_type<__half>(b, nt, s);
+}
+
+}  // namespace fp4

@@ -29,6 +29,14 @@ __device__ __forceinline__ float from_f32<float>(float v) {
   return v;
 }
 
+// log2 of a power of two, else `other`.
+inline int log2_or(int v, int other) {
+  if (v < 1 || (v & (v - 1)) != 0) return other;
+  int e = 0;
+  while (1 << e < v) ++e;
+  return e;
+}
+
 // Multiprocessors of the current device (asked once per device).
 inline int sm_count() {
   constexpr int kMaxDev = 64;

@@ -1,9 +1,10 @@
 """Serving operators: products of 4-bit weights with a few tokens, a paged
-cache of keys and values, and attention of one new token per sequence over it.
+cache of keys and values in 16 or in 8 bits, its page tables, and attention of
+one new token per sequence over it.
 
 ``fp4_*`` functions keep the C names and return a status code; ``matvec``,
-``kv_append`` and ``decode_attention`` check their tensors, allocate outputs
-and raise.  All of them only marshal arguments: the work is done by the
+``kv_append``, ``kv_read``, ``page_plan`` and ``decode_attention`` check their
+tensors, allocate outputs and raise.  All of them only marshal arguments: the work is done by the
 library's CUDA kernels.  An output or workspace that a function allocates for
 a given ``stream`` belongs to that stream.
 
@@ -18,6 +19,7 @@ import importlib.machinery
 import importlib.util
 import os
 import struct
+from collections import namedtuple
 from functools import lru_cache
 
 import torch
@@ -29,6 +31,7 @@ FP4_BF16, FP4_F16, FP4_F32 = 0, 1, 2
 _TYPES = {torch.bfloat16: FP4_BF16, torch.float16: FP4_F16, torch.float32: FP4_F32}
 _HALVES = (torch.bfloat16, torch.float16)
 _INT, _FLOAT = torch.int32, torch.float32
+E4M3 = torch.float8_e4m3fn
 
 
 class fp4_kv_cache(ctypes.Structure):
@@ -57,13 +60,46 @@ class fp4_attention_params(ctypes.Structure):
                 ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("q_seq", ctypes.c_int64),
                 ("q_head", ctypes.c_int64), ("out_seq", ctypes.c_int64), ("out_head", ctypes.c_int64),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
-                ("heads", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
+                ("heads", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("sinks", ctypes.c_int32)]
+
+
+class fp4_kv_scales(ctypes.Structure):
+    _fields_ = [("k_sf", ctypes.c_void_p), ("v_sf", ctypes.c_void_p), ("k_page", ctypes.c_int64),
+                ("k_block", ctypes.c_int64), ("k_head", ctypes.c_int64), ("v_page", ctypes.c_int64),
+                ("v_block", ctypes.c_int64), ("v_head", ctypes.c_int64), ("block", ctypes.c_int32)]
+
+
+class fp4_append8_params(ctypes.Structure):
+    _fields_ = [("base", fp4_append_params), ("scales", fp4_kv_scales)]
+
+
+class fp4_attention8_params(ctypes.Structure):
+    _fields_ = [("base", fp4_attention_params), ("scales", fp4_kv_scales)]
+
+
+class fp4_read_params(ctypes.Structure):
+    _fields_ = [("cache", fp4_kv_cache), ("scales", fp4_kv_scales), ("k_out", ctypes.c_void_p),
+                ("v_out", ctypes.c_void_p), ("k_token", ctypes.c_int64), ("k_out_head", ctypes.c_int64),
+                ("v_token", ctypes.c_int64), ("v_out_head", ctypes.c_int64), ("pos", ctypes.c_void_p),
+                ("seq", ctypes.c_void_p), ("tokens", ctypes.c_int64)]
+
+
+class fp4_plan_params(ctypes.Structure):
+    _fields_ = [("new_tokens", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("room", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("pool", ctypes.c_void_p),
+                ("pool_pages", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("seq", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p), ("slot", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+                ("seqs", ctypes.c_int32), ("seq_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
 
 
 _CACHE = "PPqqqqqqPqqiiiiii"
 _OPERAND = struct.Struct("@PPPPi4xqq")
 _APPEND = struct.Struct("@" + _CACHE + "PPPPqqqqqqqqPPPqqiii4x")
-_ATTENTION = struct.Struct("@" + _CACHE + "PPPPqqqqPqiif4x")
+_ATTENTION = struct.Struct("@" + _CACHE + "PPPPqqqqPqiifi")
+_SCALES = struct.Struct("@PPqqqqqqi4x")
+_READ = struct.Struct("@" + _CACHE + "PPqqqqqqi4xPPqqqqPPq")
+_PLAN = struct.Struct("@PPPPqPqPPPPqiii4x")
 
 _entry = None
 
@@ -78,9 +114,13 @@ def _lib():
         L.fp4_kv_append.argtypes = [vp, vp]
         L.fp4_decode_attention.argtypes = [vp, vp]
         L.fp4_decode_attention_workspace.argtypes = [i32, i64, i32, i32, i32]
-        for f in ("fp4_matvec", "fp4_kv_append", "fp4_decode_attention"):
+        L.fp4_decode_attention8_workspace.argtypes = [i32, i64, i32, i32, i32]
+        for f in ("fp4_kv_append8", "fp4_decode_attention8", "fp4_kv_read", "fp4_page_plan"):
+            getattr(L, f).argtypes = [vp, vp]
+        for f in ("fp4_matvec", "fp4_kv_append", "fp4_decode_attention", "fp4_kv_append8",
+                  "fp4_decode_attention8", "fp4_kv_read", "fp4_page_plan"):
             getattr(L, f).restype = i32
-        L.fp4_decode_attention_workspace.restype = i64
+        L.fp4_decode_attention_workspace.restype = L.fp4_decode_attention8_workspace.restype = i64
         _entry = L
     return _entry
 
@@ -120,6 +160,34 @@ def fp4_decode_attention(p, stream=None):
 
 def fp4_decode_attention_workspace(seqs, room, heads, kv_heads, head_dim):
     return _lib().fp4_decode_attention_workspace(seqs, room, heads, kv_heads, head_dim)
+
+
+def _call(name, p, stream):
+    return getattr(_lib(), name)(p if isinstance(p, bytes) else ctypes.byref(p), _stream(stream))
+
+
+def fp4_kv_append8(p, stream=None):
+    """p: an fp4_append8_params, or the same bytes packed."""
+    return _call("fp4_kv_append8", p, stream)
+
+
+def fp4_decode_attention8(p, stream=None):
+    """p: an fp4_attention8_params, or the same bytes packed."""
+    return _call("fp4_decode_attention8", p, stream)
+
+
+def fp4_decode_attention8_workspace(seqs, room, heads, kv_heads, head_dim):
+    return _lib().fp4_decode_attention8_workspace(seqs, room, heads, kv_heads, head_dim)
+
+
+def fp4_kv_read(p, stream=None):
+    """p: an fp4_read_params, or the same bytes packed."""
+    return _call("fp4_kv_read", p, stream)
+
+
+def fp4_page_plan(p, stream=None):
+    """p: an fp4_plan_params, or the same bytes packed."""
+    return _call("fp4_page_plan", p, stream)
 
 
 # ------------------------------------------------------ allocating conveniences
@@ -244,11 +312,16 @@ def _rows(where, name, t, sizes):
     return _steps(where, name, t, sizes)[:2]
 
 
-def _cache_fields(where, k_pages, v_pages, page_table):
-    """The fields of fp4_kv_cache, in order."""
+def _cache_fields(where, k_pages, v_pages, page_table, row_type=None):
+    """The fields of fp4_kv_cache, in order.  row_type: the type of the rows
+    beside a cache of E4M3 codes."""
     dtype, sizes, table = k_pages.dtype, k_pages.shape, page_table.shape
-    if dtype not in _HALVES or v_pages.dtype is not dtype:
-        raise ValueError(f"{where}: keys and values must both be bfloat16 or both float16")
+    codes = row_type is not None and dtype is E4M3
+    if (dtype not in _HALVES and not codes) or v_pages.dtype is not dtype:
+        raise ValueError(f"{where}: keys and values must both be bfloat16 or both float16"
+                         + (", or both float8_e4m3fn" if row_type is not None else ""))
+    if codes and row_type not in _HALVES:
+        raise ValueError(f"{where}: beside a cache in 8 bits, rows must be bfloat16 or float16")
     if len(sizes) != 4 or len(table) != 2:
         raise ValueError(f"{where}: k_pages must be [pages, page_size, kv_heads, head_dim], "
                          "page_table [seqs, pages of a sequence]")
@@ -263,11 +336,29 @@ def _cache_fields(where, k_pages, v_pages, page_table):
         raise ValueError(f"{where}: the rows of page_table must be contiguous")
     ka, kb, kc, kd = k_pages.stride()
     va, vb, vc, vd = v_pages.stride()
-    if kd != 1 or vd != 1 or v_pages.shape != sizes or (ka | kb | kc | va | vb | vc) & 7:
+    if kd != 1 or vd != 1 or v_pages.shape != sizes or (ka | kb | kc | va | vb | vc) & 15:
         ka, kb, kc, kd = _steps(where, "k_pages", k_pages, sizes)
         va, vb, vc, vd = _steps(where, "v_pages", v_pages, sizes)
     return (k_pages.data_ptr(), v_pages.data_ptr(), ka, kb, kc, va, vb, vc, page_table.data_ptr(),
-            step if seqs > 1 else 0, pages, seqs, wide, page, heads, dim, _TYPES[dtype])
+            step if seqs > 1 else 0, pages, seqs, wide, page, heads, dim, _TYPES[row_type if codes else dtype])
+
+
+def _scale_fields(where, k_pages, k_scale, v_scale):
+    """(fields of fp4_kv_scales in order, the tensors) of a cache in 8 bits; (None, []) of one in 16."""
+    if k_pages.dtype is not E4M3:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError(f"{where}: k_scale and v_scale belong to a cache of float8_e4m3fn")
+        return None, []
+    if k_scale is None or v_scale is None:
+        raise ValueError(f"{where}: a cache of float8_e4m3fn needs k_scale and v_scale")
+    pages, page, heads, _ = k_pages.shape
+    blocks = k_scale.shape[1] if k_scale.dim() == 3 else 0
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.dtype is not torch.uint8 or blocks < 1 or page % blocks or t.shape != (pages, blocks, heads):
+            raise ValueError(f"{where}: {name} must be uint8 [{pages}, blocks of a page, {heads}], the blocks equal "
+                             f"parts of {page} places")
+    steps = [[0 if n == 1 else s for n, s in zip(t.shape, t.stride())] for t in (k_scale, v_scale)]
+    return (k_scale.data_ptr(), v_scale.data_ptr(), *steps[0], *steps[1], page // blocks), [k_scale, v_scale]
 
 
 def _need_ints(where, name, t, n):
@@ -276,7 +367,7 @@ def _need_ints(where, name, t, n):
 
 
 def kv_append(k, v, k_pages, v_pages, page_table, pos, seq=None, q=None, rope=None,
-              interleaved=False, q_out=None, stream=None):
+              interleaved=False, q_out=None, stream=None, k_scale=None, v_scale=None):
     """Writes the keys k and values v [tokens, kv_heads, head_dim] of new
     tokens into a paged cache (k_pages, v_pages [pages, page_size, kv_heads,
     head_dim], any strides; page_table [seqs, pages of a sequence] int32) at
@@ -285,14 +376,23 @@ def kv_append(k, v, k_pages, v_pages, page_table, pos, seq=None, q=None, rope=No
     float32 (rope_table) keys and queries q [tokens, heads, head_dim] are
     rotated on the way.  Returns the rotated queries (q_out, new by default),
     or None without q.  Tokens at negative positions are skipped; no two tokens
-    of a call may have the same place (it would hold parts of both)."""
+    of a call may have the same place (it would hold parts of both).
+
+    A cache in 8 bits is of float8_e4m3fn, with k_scale and v_scale [pages,
+    blocks of a page, kv_heads] uint8: a power of two (2^(code - 127)) for each
+    block of places and head.  Values are rounded once, to the codes; where a
+    new token needs a larger scale the block's earlier codes are rounded anew,
+    and a call that writes a block's first place begins it (see fp4_kv_append8
+    in include/fp4.h).  A call's tokens of one block stand side by side, in the
+    order of their positions."""
     if stream is None and q_out is None:
-        r = _bind().append(k, v, k_pages, v_pages, page_table, pos, seq, q, rope, interleaved)
+        r = _bind().append(k, v, k_pages, v_pages, page_table, pos, seq, q, rope, interleaved, k_scale, v_scale)
         if r is not NotImplemented:
             return r
     where = "kv_append"
-    cache = _cache_fields(where, k_pages, v_pages, page_table)
-    dtype, Hk, D = k_pages.dtype, cache[14], cache[15]
+    cache = _cache_fields(where, k_pages, v_pages, page_table, k.dtype)
+    scales, extra = _scale_fields(where, k_pages, k_scale, v_scale)
+    dtype, Hk, D = k.dtype if scales else k_pages.dtype, cache[14], cache[15]
     if k.dtype is not dtype or v.dtype is not dtype:
         raise ValueError(f"{where}: q, k, v and the cache must share one dtype")
     T = k.shape[0]
@@ -300,7 +400,6 @@ def kv_append(k, v, k_pages, v_pages, page_table, pos, seq=None, q=None, rope=No
     ks, kh = _rows(where, "k", k, sizes)
     vs, vh = _rows(where, "v", v, sizes)
     _need_ints(where, "pos", pos, T)
-    extra = []
     seq_at = rope_at = q_at = out_at = rot_dim = rope_len = heads = qs = qh = os_ = oh = 0
     if seq is not None:
         _need_ints(where, "seq", seq, T)
@@ -334,31 +433,125 @@ def kv_append(k, v, k_pages, v_pages, page_table, pos, seq=None, q=None, rope=No
     elif q_out is not None:
         raise ValueError(f"{where}: q_out without q")
     dev = _device(where, k, v, k_pages, v_pages, page_table, pos, *extra)
-    code = _lib().fp4_kv_append(
-        _APPEND.pack(*cache, k.data_ptr(), v.data_ptr(), q_at, out_at, ks, kh, vs, vh, qs, qh, os_,
-                     oh, pos.data_ptr(), seq_at, rope_at, rope_len, T, heads, rot_dim,
-                     1 if interleaved else 0), _handle(stream, dev))
+    p = _APPEND.pack(*cache, k.data_ptr(), v.data_ptr(), q_at, out_at, ks, kh, vs, vh, qs, qh, os_, oh,
+                     pos.data_ptr(), seq_at, rope_at, rope_len, T, heads, rot_dim, 1 if interleaved else 0)
+    entry = "fp4_kv_append8" if scales else "fp4_kv_append"
+    code = getattr(_lib(), entry)(p + _SCALES.pack(*scales) if scales else p, _handle(stream, dev))
     if code:
-        raise FP4Error(code, "fp4_kv_append")
+        raise FP4Error(code, entry)
     return q_out
 
 
+def kv_read(k_pages, v_pages, page_table, pos, seq=None, k_scale=None, v_scale=None, dtype=None, stream=None):
+    """(keys, values) [tokens, kv_heads, head_dim] of tokens at positions pos
+    [tokens] int32 of sequences seq [tokens] int32 (default: token t of sequence
+    t), read back from a paged cache as kv_append stored them: the rows of a
+    16-bit cache, in its dtype, or the values that the codes of an 8-bit one
+    stand for, in bfloat16 (by default) or float16.  Negative positions give
+    zeros."""
+    if stream is None:
+        r = _bind().read(k_pages, v_pages, page_table, pos, seq, k_scale, v_scale, dtype)
+        if r is not NotImplemented:
+            return r
+    where = "kv_read"
+    codes = k_pages.dtype is E4M3
+    if dtype is None:
+        dtype = torch.bfloat16 if codes else k_pages.dtype
+    cache = _cache_fields(where, k_pages, v_pages, page_table, dtype)
+    scales, extra = _scale_fields(where, k_pages, k_scale, v_scale)
+    if not codes and dtype is not k_pages.dtype:
+        raise ValueError(f"{where}: a 16-bit cache is read in its own dtype")
+    T = pos.shape[0] if pos.dim() == 1 else -1
+    _need_ints(where, "pos", pos, T)
+    if seq is not None:
+        _need_ints(where, "seq", seq, T)
+        extra.append(seq)
+    elif T > cache[11]:
+        raise ValueError(f"{where}: more tokens than sequences; give seq")
+    dev = _device(where, k_pages, v_pages, page_table, pos, *extra)
+    H, D = cache[14], cache[15]
+    k, v = (_new((T, H, D), dtype, k_pages.device, stream) for _ in range(2))
+    code = _lib().fp4_kv_read(
+        _READ.pack(*cache, *(scales or (0,) * 9), k.data_ptr(), v.data_ptr(), H * D, D, H * D, D, pos.data_ptr(),
+                   0 if seq is None else seq.data_ptr(), T), _handle(stream, dev))
+    if code:
+        raise FP4Error(code, "fp4_kv_read")
+    return k, v
+
+
+def page_pool(pages, device="cuda"):
+    """A pool of free pages for page_plan, int32 [2 + pages]: how many are
+    free, a word of page_plan's own, the stack of page numbers (0 on top)."""
+    head = torch.tensor([pages, 0], dtype=torch.int32)
+    return torch.cat([head, torch.arange(pages - 1, -1, -1, dtype=torch.int32)]).to(device)
+
+
+Plan = namedtuple("Plan", "seq pos slot offsets")
+
+
+def page_plan(new, lengths, page_table, room, pool, page_size, tokens=None, stream=None):
+    """Pages and places for new tokens, worked out on the GPU: new [seqs] int32
+    tokens more (or, negative, fewer) of each sequence, whose state is lengths
+    [seqs] (positions held), room [seqs] (positions its pages hold), page_table
+    [seqs, pages of a sequence] (-1: no page) and the free pages pool
+    (page_pool), all int32 and brought up to date in place.  With tokens, the
+    size of the batch, returns Plan(seq, pos, slot, offsets): sequence, position
+    (int32) and place page * page_size + place (int64) of each new token, -1
+    behind the last, and offsets [seqs + 1] int32 of the sequences in the batch;
+    kv_append takes seq and pos as they are.  A sequence that cannot have its
+    pages or places stays as it is, its tokens have position -1, and
+    fp4_status_sync reports FP4_ERR_INVALID_ARG."""
+    if stream is None:
+        r = _bind().plan(new, lengths, page_table, room, pool, page_size, tokens)
+        if r is not NotImplemented:
+            return r if r is None else Plan(*r)
+    where = "page_plan"
+    if page_table.dtype is not _INT or page_table.dim() != 2:
+        raise ValueError(f"{where}: page_table must be int32 [seqs, pages of a sequence]")
+    seqs, wide = page_table.shape
+    step, one = page_table.stride()
+    if one != 1 and wide > 1:
+        raise ValueError(f"{where}: the rows of page_table must be contiguous")
+    for name, t in (("new", new), ("lengths", lengths), ("room", room)):
+        _need_ints(where, name, t, seqs)
+    if pool.dim() != 1 or pool.shape[0] < 2:
+        raise ValueError(f"{where}: pool must be int32 [2 + pages]")
+    _need_ints(where, "pool", pool, pool.shape[0])
+    if page_size < 1 or page_size > 0x7FFFFFFF or (tokens is not None and tokens < 0):
+        raise ValueError(f"{where}: page_size must be positive, tokens not negative")
+    dev = _device(where, page_table, new, lengths, room, pool)
+    made = None
+    if tokens is not None:
+        sizes = ((tokens, _INT), (tokens, _INT), (tokens, torch.int64), (seqs + 1, _INT))
+        made = Plan(*(_new((n,), dtype, pool.device, stream) for n, dtype in sizes))
+    seq, pos, slot, offsets = (0,) * 4 if made is None else (t.data_ptr() for t in made)
+    code = _lib().fp4_page_plan(
+        _PLAN.pack(new.data_ptr(), lengths.data_ptr(), room.data_ptr(), page_table.data_ptr(),
+                   step if seqs > 1 else 0, pool.data_ptr(), pool.shape[0] - 2, offsets, seq, pos, slot,
+                   -1 if tokens is None else tokens, seqs, wide, page_size), _handle(stream, dev))
+    if code:
+        raise FP4Error(code, "fp4_page_plan")
+    return made
+
+
 def decode_attention(q, k_pages, v_pages, page_table, lengths, scale=None, window=0, out=None,
-                     return_lse=False, stream=None):
+                     return_lse=False, stream=None, sinks=0, k_scale=None, v_scale=None):
     """Attention of one new token per sequence, q [seqs, heads, head_dim],
-    over a paged cache (as in kv_append) that holds lengths [seqs] int32
-    positions of each sequence, the new one among them.  scale defaults to
-    head_dim ** -0.5; window > 0 sees the newest `window` positions only.
+    over a paged cache (as in kv_append, in 16 or in 8 bits) that holds lengths
+    [seqs] int32 positions of each sequence, the new one among them.  scale
+    defaults to head_dim ** -0.5; window > 0 sees the newest `window` positions
+    and the first `sinks` only.
     Returns [seqs, heads, head_dim] in q's dtype (or `out`), and with
     return_lse also the logarithm of each row's sum of exponentials, float32
     [seqs, heads].  A sequence of length 0 gives zeros (and -inf)."""
     if out is None and stream is None and not return_lse:
-        r = _bind().attention(q, k_pages, v_pages, page_table, lengths, scale, window)
+        r = _bind().attention(q, k_pages, v_pages, page_table, lengths, scale, window, sinks, k_scale, v_scale)
         if r is not NotImplemented:
             return r
     where = "decode_attention"
-    cache = _cache_fields(where, k_pages, v_pages, page_table)
-    dtype, seqs, Hk, D = k_pages.dtype, cache[11], cache[14], cache[15]
+    cache = _cache_fields(where, k_pages, v_pages, page_table, q.dtype)
+    scales, extra = _scale_fields(where, k_pages, k_scale, v_scale)
+    dtype, seqs, Hk, D = q.dtype if scales else k_pages.dtype, cache[11], cache[14], cache[15]
     heads = q.shape[1] if q.dim() == 3 else 0
     if q.dtype is not dtype or heads < 1 or heads % Hk:
         raise ValueError(f"{where}: q must be [seqs, heads, head_dim] in the cache's dtype, heads a "
@@ -368,7 +561,9 @@ def decode_attention(q, k_pages, v_pages, page_table, lengths, scale=None, windo
     _need_ints(where, "lengths", lengths, seqs)
     if window < 0 or window > 0x7FFFFFFF:
         raise ValueError(f"{where}: window must be >= 0")
-    dev = _device(where, q, k_pages, v_pages, page_table, lengths)
+    if sinks < 0 or sinks > 0x7FFFFFFF:
+        raise ValueError(f"{where}: sinks must be >= 0")
+    dev = _device(where, q, k_pages, v_pages, page_table, lengths, *extra)
     device = q.device
     if out is None:
         out = _new(sizes, dtype, device, stream)
@@ -379,23 +574,25 @@ def decode_attention(q, k_pages, v_pages, page_table, lengths, scale=None, windo
         os_, oh = _rows(where, "out", out, sizes)
         _device(where, q, out)
     lse = _new((seqs, heads), _FLOAT, device, stream) if return_lse else None
-    need = _workspace(seqs, cache[12] * cache[13], heads, Hk, D, dev)
+    need = _workspace(seqs, cache[12] * cache[13], heads, Hk, D, dev, bool(scales))
     work = _new(need, torch.uint8, device, stream) if need > 0 else None
-    code = _lib().fp4_decode_attention(
-        _ATTENTION.pack(*cache, lengths.data_ptr(), q.data_ptr(), out.data_ptr(),
+    p = _ATTENTION.pack(*cache, lengths.data_ptr(), q.data_ptr(), out.data_ptr(),
                         lse.data_ptr() if return_lse else 0, qs, qh, os_, oh,
                         work.data_ptr() if need > 0 else 0, need if need > 0 else 0, heads, window,
-                        D ** -0.5 if scale is None else scale), _handle(stream, dev))
+                        D ** -0.5 if scale is None else scale, sinks)
+    entry = "fp4_decode_attention8" if scales else "fp4_decode_attention"
+    code = getattr(_lib(), entry)(p + _SCALES.pack(*scales) if scales else p, _handle(stream, dev))
     if code:
-        raise FP4Error(code, "fp4_decode_attention")
+        raise FP4Error(code, entry)
     return (out, lse) if return_lse else out
 
 
 @lru_cache(maxsize=1024)
-def _workspace(seqs, room, heads, kv_heads, head_dim, dev):
-    """fp4_decode_attention_workspace for these sizes on device `dev` (the
-    current one)."""
-    return fp4_decode_attention_workspace(seqs, room, heads, kv_heads, head_dim)
+def _workspace(seqs, room, heads, kv_heads, head_dim, dev, codes):
+    """Workspace of attention over a cache in 16 bits, or of codes in 8, for
+    these sizes on device `dev` (the current one)."""
+    f = fp4_decode_attention8_workspace if codes else fp4_decode_attention_workspace
+    return f(seqs, room, heads, kv_heads, head_dim)
 
 
 def rope_table(positions, rot_dim, base=10000.0, device="cuda"):
@@ -409,6 +606,10 @@ def rope_table(positions, rot_dim, base=10000.0, device="cuda"):
     return torch.cat([torch.cos(angle), torch.sin(angle)], -1).float().to(device)
 
 
-__all__ = ["FP4_BF16", "FP4_F16", "FP4_F32", "fp4_append_params", "fp4_attention_params",
-           "fp4_decode_attention", "fp4_decode_attention_workspace", "fp4_kv_append",
-           "fp4_kv_cache", "fp4_matvec", "decode_attention", "kv_append", "matvec", "rope_table"]
+__all__ = ["FP4_BF16", "FP4_F16", "FP4_F32", "Plan", "fp4_append8_params", "fp4_append_params",
+           "fp4_attention8_params", "fp4_attention_params", "fp4_decode_attention",
+           "fp4_decode_attention8", "fp4_decode_attention8_workspace",
+           "fp4_decode_attention_workspace", "fp4_kv_append", "fp4_kv_append8", "fp4_kv_cache",
+           "fp4_kv_read", "fp4_kv_scales", "fp4_matvec", "fp4_page_plan", "fp4_plan_params",
+           "fp4_read_params", "decode_attention", "kv_append", "kv_read", "matvec", "page_plan",
+           "page_pool", "rope_table"]

@@ -438,7 +438,8 @@ fp4_status fp4_kv_append(const fp4_append_params *p, void *stream);
 /* Attention of one new token per sequence over the cache:
  *   out[s][h] = sum_j w_j v_j,  w = softmax_j(scale * q[s][h] . k_j)
  * over positions j in [max(0, L - window), L) with L = lengths[s] (window 0:
- * all); query head h reads key head h / (heads / kv_heads).  L = 0 gives
+ * all) and, with a window, the first `sinks` positions, which stay visible
+ * (each position once); query head h reads key head h / (heads / kv_heads).  L = 0 gives
  * zeros.  lse (nullable, [seqs][heads]) receives log sum_j exp(scale q . k_j),
  * -inf for L = 0, so that results over parts of a cache can be joined.
  * Positions that are not seen are never read: what lies there, NaN included,
@@ -460,6 +461,7 @@ typedef struct {
   int64_t workspace_bytes;
   int32_t heads, window;
   float scale;
+  int32_t sinks;                     /* first positions always seen; 0: none   */
 } fp4_attention_params;
 fp4_status fp4_decode_attention(const fp4_attention_params *p, void *stream);
 
@@ -468,6 +470,116 @@ fp4_status fp4_decode_attention(const fp4_attention_params *p, void *stream);
  * sizes it refuses. */
 int64_t fp4_decode_attention_workspace(int32_t seqs, int64_t room, int32_t heads,
                                        int32_t kv_heads, int32_t head_dim);
+
+/* --- The cache in 8 bits.  fp4_kv_cache with type the type of q, k, v and out,
+ * its k and v E4M3 codes (a byte an element; strides in elements), and scales:
+ * E8M0 codes, one for each block of `block` places of a page and head,
+ *   value = e4m3(code) * 2^(scale code - 127),
+ * block b of a page holding places [b * block, (b + 1) * block).  block divides
+ * page_size.  Codes 0x7F and 0xFF are NaN, and so is a scale code of 255.
+ * head_dim is a multiple of 16; pointers and strides of k and v are multiples
+ * of 16. */
+typedef struct {
+  uint8_t *k_sf, *v_sf;              /* [page][block][kv_head]                 */
+  int64_t k_page, k_block, k_head;   /* strides of k_sf                        */
+  int64_t v_page, v_block, v_head;   /* strides of v_sf                        */
+  int32_t block;                     /* places that share a scale              */
+} fp4_kv_scales;
+
+/* fp4_kv_append to a cache in 8 bits.  Keys are rotated in binary32 and rounded
+ * once, to their codes; queries as there.  For each block of places and head,
+ * with x the new values of this call:
+ *   need = smallest E8M0 value with max |x| <= 448 need (not finite x left out),
+ *   scale' = need                if the call writes the block's first place,
+ *            max(scale, need)    otherwise,
+ *   code  = nearest-even E4M3 code of x / scale' (not finite: NaN),
+ * and where the scale of a block that is not begun rises, the codes of its other
+ * places are rounded anew, code' = E4M3(code * scale / scale'), so that they
+ * stand for what they stood for (exactly, but for those that fall below 2^-6 of
+ * the new unit).  What the other places of a block hold that a call begins
+ * means nothing afterwards.  Scales only rise within a block.
+ * The tokens of one call that go into one block stand side by side, at
+ * consecutive positions; where they do not, or a place comes twice, what the
+ * block holds afterwards is unspecified.
+ * Shapes as fp4_kv_append, head_dim % 16 == 0. */
+typedef struct {
+  fp4_append_params base;
+  fp4_kv_scales scales;
+} fp4_append8_params;
+fp4_status fp4_kv_append8(const fp4_append8_params *p, void *stream);
+
+/* fp4_decode_attention over a cache in 8 bits: keys and values are what codes
+ * and scales stand for.  Queries are held exactly for magnitudes down to 2^-31
+ * of the largest in their head, softmax weights times their values' scales to
+ * 2^-32 of a row's largest.  A NaN code among the keys makes the rows that
+ * see it NaN, one among the values its own element, a query that is not finite
+ * its head (and lse NaN).
+ * workspace: fp4_decode_attention8_workspace() bytes. */
+typedef struct {
+  fp4_attention_params base;
+  fp4_kv_scales scales;
+} fp4_attention8_params;
+fp4_status fp4_decode_attention8(const fp4_attention8_params *p, void *stream);
+int64_t fp4_decode_attention8_workspace(int32_t seqs, int64_t room, int32_t heads,
+                                        int32_t kv_heads, int32_t head_dim);
+
+/* Reads the keys and values of `tokens` tokens back from a cache, as they are
+ * stored (keys rotated): k_out[t][h], v_out[t][h] of the cache's type.  Token t
+ * belongs to sequence seq[t] (NULL: sequence t), at position pos[t].  With
+ * scales.k_sf NULL the cache is of 16 bits and rows are copied; else of 8, and
+ * values are code times scale, rounded once.  A negative position gives a row
+ * of zeros; one outside the table, or on a page outside the cache, too, and
+ * fp4_status_sync reports FP4_ERR_INVALID_ARG.
+ * Shapes: head_dim % 8 == 0 (8 bits: 16).  Alignment: pointers and strides in
+ * multiples of 16 bytes (8 elements). */
+typedef struct {
+  fp4_kv_cache cache;
+  fp4_kv_scales scales;
+  void *k_out, *v_out;               /* [tokens][kv_heads][head_dim]           */
+  int64_t k_token, k_out_head, v_token, v_out_head;
+  const int32_t *pos, *seq;          /* [tokens]; seq nullable                 */
+  int64_t tokens;
+} fp4_read_params;
+fp4_status fp4_kv_read(const fp4_read_params *p, void *stream);
+
+/* Pages and places for new tokens, from what sequences hold and are to get.
+ * State, read and written:
+ *   lengths[s]   positions that sequence s holds,
+ *   room[s]      positions that its pages hold, a multiple of page_size,
+ *   table[s][e]  its page numbers, e < room[s] / page_size,
+ *   pool         [0] how many pages are free, [1] a word of this call's own (0
+ *                between calls), [2 + i] the free pages, a stack of pool_pages.
+ * new_tokens[s] = n >= 0: n tokens more.  Pages for lengths[s] + n positions that
+ * room[s] does not cover come from the top of the stack, in the order of the
+ * sequences and of their positions.  n < 0: -n tokens fewer (at most all);
+ * pages that hold no position any more go back and leave -1 in the table.  What
+ * goes back in a call is given out by later ones, and giving back what a call
+ * took leaves the stack as it was.
+ * A sequence whose tokens would pass its row of the table, or the token maps,
+ * or whose pages (with those of the sequences before it) are more than are free,
+ * gets none: it stays as it is, its tokens have position and slot -1, and
+ * fp4_status_sync reports FP4_ERR_INVALID_ARG.
+ * Maps (each nullable), the new tokens of all sequences (n > 0) in a row:
+ *   offsets[s]   the first of sequence s; offsets[seqs]: how many,
+ *   seq[t], pos[t], slot[t]  sequence, position and place (page * page_size +
+ *                place in it) of token t < tokens; -1 behind the last.
+ * fp4_kv_append takes seq and pos as they are.  tokens < 0: no limit, no maps
+ * but offsets.  One call at a time may use a pool.
+ * Alignment: 4 bytes, slot 8. */
+typedef struct {
+  const int32_t *new_tokens;         /* [seqs]                                 */
+  int32_t *lengths, *room;           /* [seqs]                                 */
+  int32_t *table;                    /* [seqs][seq_pages]                      */
+  int64_t table_stride;
+  int32_t *pool;                     /* [2 + pool_pages]                       */
+  int64_t pool_pages;
+  int32_t *offsets;                  /* [seqs + 1]                             */
+  int32_t *seq, *pos;                /* [tokens]                               */
+  int64_t *slot;                     /* [tokens]                               */
+  int64_t tokens;
+  int32_t seqs, seq_pages, page_size;
+} fp4_plan_params;
+fp4_status fp4_page_plan(const fp4_plan_params *p, void *stream);
 
 /* Bytes of one scale-factor output for a copy with `rows` rows and `cols`
  * elements per row; -1 for an invalid format/layout. */
