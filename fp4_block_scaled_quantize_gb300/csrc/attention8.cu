@@ -42,8 +42,9 @@ struct At8Params {
   int block_shift;  // log2 of the block, or -1: no power of two
 };
 
-constexpr int kStages = 4;
-constexpr int kBlocks = 2;  // CTAs an SM holds at least
+constexpr int kStages = 3;
+// CTAs an SM holds at least, by the kernel's launch bounds.
+constexpr int per_sm8(int dp, int nt) { return nt == 1 && dp <= 128 ? 3 : 2; }
 constexpr float kLift = 7.0f;  // weights are held 2^7 times as large (f16's smallest is 2^-24)
 
 // Groups of 16 positions a step.
@@ -76,43 +77,22 @@ __device__ __forceinline__ void halves(uint32_t w, uint32_t &lo, uint32_t &hi) {
       : "r"(w));
 }
 
-// A slice of the list of tiles, walked row by row.
-struct Cursor {
-  int64_t at, end, start;  // start: list index of sequence s's first tile
-  Span sp;
-  int s, row, kvh, tile, tile1;
-  bool live;
-  __device__ __forceinline__ void begin(const AtParams &a, int s0, int64_t start0, int64_t at0, int64_t end0) {
-    s = s0, start = start0, at = at0, end = end0;
-    row = tile = tile1 = 0;
-    live = at < end;
-    sp = live ? span_of(a, s) : Span{};
-  }
-  // on to the next row of the slice; false (and not live) at its end
-  __device__ __forceinline__ bool next_row(const AtParams &a, int rows) {
-    live = at < end;
-    if (!live) return false;
-    while (at >= start + (int64_t)rows * sp.tiles) {
-      start += (int64_t)rows * sp.tiles;
-      sp = span_of(a, ++s);
-    }
-    row = (int)((at - start) / sp.tiles);
-    tile = (int)(at - start - (int64_t)row * sp.tiles);
-    tile1 = (int)min((int64_t)sp.tiles, tile + (end - at));
-    at += tile1 - tile;
-    kvh = row / a.groups;
-    return true;
-  }
+// What a warp has to know of a row that it works on: sequence, row, tiles of it
+// in the slice, and whether it begins (1) and ends (2) there.
+struct Row {
+  int s, row, tiles, ends;
 };
+constexpr int kQueue = 8;  // rows between the copies and the work: kStages + 1 at most
 
 template <typename T, int DP, int NT, bool UNITS>
-__global__ void __launch_bounds__(kThreads, kBlocks) k_attention8(const __grid_constant__ At8Params b) {
+__global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const __grid_constant__ At8Params b) {
   constexpr int kCols = 8 * NT, kKey = DP / 64, kV16 = DP / 128, kV8 = DP / 64 % 2, kWords = DP / 32;
   constexpr int kUnits = units8(DP), kTile = 16 * kUnits, kParts = 2 * kWarps;
   const AtParams &a = b.a;
   extern __shared__ __align__(16) char smem8[];
   __shared__ int64_t scan[kWarps + 2];
   __shared__ int4 part_sh[kParts];  // sequence (-1: none), row, begins with it, ends with it
+  __shared__ Row queue_sh[kWarps][kQueue];
   const fp4_kv_cache &c = a.p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int D = c.head_dim, rows = c.kv_heads * a.groups;
@@ -167,79 +147,165 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_attention8(const __grid_c
   }
 
   // each warp takes a quarter of the slice by itself
-  Cursor use, put;  // the row that is worked on, the row whose tiles are copied
   {
     const int64_t n = end - at;
     end = at + n * (warp + 1) / kWarps;
     at += n * warp / kWarps;
-    use.begin(a, s, start, at, end);
-    put = use;
   }
+  Row *const queue = queue_sh[warp];
+  // The tile that is copied next: position pos, tile `tile` of a row of which the
+  // slice has those before tile1; where the row's keys, values (a lane's first
+  // pieces), scales and page numbers are.
+  bool live = at < end;
+  Span sp = live ? span_of(a, s) : Span{};
+  int tile = 0, tile1 = 0, pos = 0, entered = 0;
+  const int32_t *table = c.table;
+  const char *keys = nullptr, *values = nullptr;
+  const uint8_t *codes = nullptr;
+  auto enter = [&] {  // on to the next row of the slice
+    live = at < end;
+    if (!live) return;
+    while (at >= start + (int64_t)rows * sp.tiles) {
+      start += (int64_t)rows * sp.tiles;
+      sp = span_of(a, ++s);
+    }
+    const int row = (int)((at - start) / sp.tiles), kvh = row / a.groups;
+    tile = (int)(at - start - (int64_t)row * sp.tiles);
+    tile1 = (int)min((int64_t)sp.tiles, tile + (end - at));
+    at += tile1 - tile;
+    if (lane == 0)
+      queue[entered % kQueue] = Row{s, row, tile1 - tile, (tile == 0 ? 1 : 0) | (tile1 == sp.tiles ? 2 : 0)};
+    ++entered;
+    int lo, hi;
+    pos = sp.start(tile, kTile, lo, hi);
+    table = c.table + s * c.table_stride;
+    keys = static_cast<const char *>(c.k) + kvh * c.k_head;
+    values = static_cast<const char *>(c.v) + kvh * c.v_head;
+    if (UNITS) {  // (lanes behind the head's end copy nothing: an address inside it)
+      keys += g * c.k_place + (16 * t < D ? 16 * t : 0);
+      values += 2 * t * c.v_place + ((kV16 ? 16 : 8) * g < D ? (kV16 ? 16 : 8) * g : 0);
+    }
+    codes = lane < 16 ? b.s.k_sf + kvh * b.s.k_head : b.s.v_sf + kvh * b.s.v_head;
+  };
+  auto advance = [&] {
+    if (!live) return;
+    if (++tile < tile1)
+      pos = tile == sp.first ? sp.base : pos + kTile;
+    else
+      enter();
+  };
+  const int64_t sf_page = lane < 16 ? b.s.k_page : b.s.v_page, sf_block = lane < 16 ? b.s.k_block : b.s.v_block;
 
   // page numbers a step ahead of the copies (their loads are not waited for).
   // UNITS (pages of whole units): one for a unit, else lane i & 15 has that of
   // position i.
   auto ask = [&](int (&page)[kUnits]) {
-    int lo, hi;
-    const int pos = put.sp.start(put.tile, kTile, lo, hi);
-    const int32_t *table = c.table + put.s * c.table_stride;
+    const int lo = tile < sp.first ? 0 : sp.from, hi = live ? tile < sp.first ? sp.sinks : sp.len : 0;
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
       const int i = pos + 16 * u + (UNITS ? 0 : lane & 15);
       page[u] = -1;
-      if (put.live && i < hi && (UNITS || i >= lo)) page[u] = table[a.shift >= 0 ? i >> a.shift : i / c.page_size];
+      if (i < hi && (UNITS || i >= lo)) page[u] = table[a.shift >= 0 ? i >> a.shift : i / c.page_size];
     }
   };
-  // Copies the tile at `put` into a stage and requests its scales: lanes 0 - 15
+  // Copies the next tile into a stage and requests its scales: lanes 0 - 15
   // those of the keys of 16 positions, lanes 16 - 31 those of the values.
-  const char *const nothing = static_cast<const char *>(a.p.q);  // an address for copies of no bytes
   auto copy = [&](int stage, const int (&pages)[kUnits], uint32_t (&code)[kUnits], uint32_t (&on)[kUnits]) {
-    int lo, hi;
-    const int pos = put.sp.start(put.tile, kTile, lo, hi);
-    const char *const keys = static_cast<const char *>(c.k) + put.kvh * c.k_head + 16 * t;
-    const char *const values = static_cast<const char *>(c.v) + put.kvh * c.v_head;
+    const int lo = tile < sp.first ? 0 : sp.from, hi = live ? tile < sp.first ? sp.sinks : sp.len : 0;
+    const uint32_t to0 = shared_at(ring) + stage * kUnits * unit_bytes(DP);
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
-      const uint32_t to = shared_at(ring) + (stage * kUnits + u) * unit_bytes(DP);
-      const int first = pos + 16 * u, page = pages[u], i = first + (lane & 15);
-      const bool ok = page >= 0 && page < c.pages, in = put.live && i >= lo && i < hi;
+      const uint32_t to = to0 + u * unit_bytes(DP) + 16 * lane, tv = to + 16 * DP;
+      const int first = pos + 16 * u, i = first + (lane & 15);
+      int page = pages[u];
+      const bool in = i >= lo && i < hi, ok = page >= 0 && page < c.pages;
       if (in && !ok && lane < 16) raise_status(a.status, kStatusIndex);
       on[u] = __ballot_sync(~0u, in && ok) & 0xFFFFu;
+      if (on[u] == 0 && UNITS) {  // nothing is seen: zeros
+#pragma unroll
+        for (int e = 0; e < 2 * kKey + 4 * kV16; ++e)
+          *reinterpret_cast<uint4 *>(ring + (stage * kUnits + u) * unit_bytes(DP) + e * 512 + 16 * lane) = make_uint4(0, 0, 0, 0);
+        if (kV8)
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            *reinterpret_cast<uint2 *>(ring + (stage * kUnits + u) * unit_bytes(DP) + 16 * DP + 4 * kV16 * 512 + h * 256 +
+                                       8 * lane) = make_uint2(0, 0);
+        code[u] = 0;
+        continue;
+      }
       const int place0 = a.shift >= 0 ? (UNITS ? first : i) & (c.page_size - 1) : (UNITS ? first : i) % c.page_size;
       const int place = UNITS ? place0 + (lane & 15) : place0;
       code[u] = 0;
       if (in && ok) {
         const int blk = b.block_shift >= 0 ? place >> b.block_shift : place / b.s.block;
-        code[u] = lane < 16 ? b.s.k_sf[(int64_t)page * b.s.k_page + blk * b.s.k_block + put.kvh * b.s.k_head]
-                            : b.s.v_sf[(int64_t)page * b.s.v_page + blk * b.s.v_block + put.kvh * b.s.v_head];
+        code[u] = codes[page * sf_page + blk * sf_block];
       }
-      const int64_t k0 = (int64_t)page * c.k_page + (int64_t)place0 * c.k_place;
-      const int64_t v0 = (int64_t)page * c.v_page + (int64_t)place0 * c.v_place;
+      if (UNITS) {
+        // every place of the unit is one of its page, so every address is inside the cache
+        const char *const k = keys + (int64_t)page * c.k_page + (int64_t)place0 * c.k_place;
+        const char *const v = values + (int64_t)page * c.v_page + (int64_t)place0 * c.v_place;
+        const bool all = on[u] == 0xFFFFu && D == DP;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = g + 8 * h;
-        const char *k = keys + (UNITS ? k0 + j * c.k_place : __shfl_sync(~0u, k0, j));
-        const bool there = on[u] >> j & 1;
+        for (int h = 0; h < 2; ++h) {
+          const char *const row = k + (h ? 8 * c.k_place : 0);
+          const bool there = on[u] >> (g + 8 * h) & 1;
 #pragma unroll
-        for (int e = 0; e < kKey; ++e) {
-          const bool yes = there && 64 * e + 16 * t < D;
-          copy16(to + (h * kKey + e) * 512 + 16 * lane, yes ? k + 64 * e : nothing, yes);
+          for (int e = 0; e < kKey; ++e)
+            if (all)
+              copy16(to + (h * kKey + e) * 512, row + 64 * e, true);
+            else if (64 * e + 16 * t < D)
+              copy16(to + (h * kKey + e) * 512, row + 64 * e, there);
+            else
+              copy16(to + (h * kKey + e) * 512, k, false);
         }
-      }
-      const uint32_t tv = to + 16 * DP;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int j = 2 * t + (h & 1) + 8 * (h >> 1);
-        const char *v = values + (UNITS ? v0 + j * c.v_place : __shfl_sync(~0u, v0, j));
-        const bool there = on[u] >> j & 1;
+        for (int h = 0; h < 4; ++h) {
+          const char *const row = v + ((h & 1) + 8 * (h >> 1)) * c.v_place;
+          const bool there = on[u] >> (2 * t + (h & 1) + 8 * (h >> 1)) & 1;
 #pragma unroll
-        for (int e = 0; e < kV16; ++e) {
-          const bool yes = there && 128 * e + 16 * g < D;
-          copy16(tv + (h * kV16 + e) * 512 + 16 * lane, yes ? v + 128 * e + 16 * g : nothing, yes);
+          for (int e = 0; e < kV16; ++e)
+            if (all)
+              copy16(tv + (h * kV16 + e) * 512, row + 128 * e, true);
+            else if (128 * e + 16 * g < D)
+              copy16(tv + (h * kV16 + e) * 512, row + 128 * e, there);
+            else
+              copy16(tv + (h * kV16 + e) * 512, v, false);
+          if (kV8) {
+            const bool yes = 128 * kV16 + 8 * g < D;
+            // (the lane's pieces of 16 bytes lie at 16 g, this one at 8 g)
+            const char *const at8 = row + (kV16 ? 128 * kV16 - 8 * g : 0);
+            copy8(tv - 8 * lane + 4 * kV16 * 512 + h * 256, yes ? at8 : v, yes && (all || there));
+          }
         }
-        if (kV8) {
-          const bool yes = there && 128 * kV16 + 8 * g < D;
-          copy8(tv + 4 * kV16 * 512 + h * 256 + 8 * lane, yes ? v + 128 * kV16 + 8 * g : nothing, yes);
+      } else {
+        const int64_t k0 = (int64_t)page * c.k_page + (int64_t)place0 * c.k_place;
+        const int64_t v0 = (int64_t)page * c.v_page + (int64_t)place0 * c.v_place;
+        const char *const nothing = static_cast<const char *>(a.p.q);  // an address for copies of no bytes
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int j = g + 8 * h;
+          const char *k = keys + __shfl_sync(~0u, k0, j) + 16 * t;
+          const bool there = on[u] >> j & 1;
+#pragma unroll
+          for (int e = 0; e < kKey; ++e) {
+            const bool yes = there && 64 * e + 16 * t < D;
+            copy16(to + (h * kKey + e) * 512, yes ? k + 64 * e : nothing, yes);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int j = 2 * t + (h & 1) + 8 * (h >> 1);
+          const char *v = values + __shfl_sync(~0u, v0, j);
+          const bool there = on[u] >> j & 1;
+#pragma unroll
+          for (int e = 0; e < kV16; ++e) {
+            const bool yes = there && 128 * e + 16 * g < D;
+            copy16(tv + (h * kV16 + e) * 512, yes ? v + 128 * e + 16 * g : nothing, yes);
+          }
+          if (kV8) {
+            const bool yes = there && 128 * kV16 + 8 * g < D;
+            copy8(tv - 8 * lane + 4 * kV16 * 512 + h * 256, yes ? v + 128 * kV16 + 8 * g : nothing, yes);
+          }
         }
       }
     }
@@ -256,38 +322,32 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_attention8(const __grid_c
       if (lane == 0) info[32] = __uint_as_float(on[u]);
     }
   };
-  auto advance = [&] {
-    if (put.live && ++put.tile >= put.tile1) put.next_row(a, rows);
-  };
 
   int page_next[kUnits];
   {
     int page[kStages - 1][kUnits];
     uint32_t code[kStages - 1][kUnits], on[kStages - 1][kUnits];
-    put.next_row(a, rows);
-    Cursor ahead = put;
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      ask(page[i]);
-      advance();
-    }
+    enter();
     ask(page_next);
-    const Cursor later = put;
-    put = ahead;
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      copy(i, page[i], code[i], on[i]);
+    for (int n = 0; n < kStages - 1; ++n) {
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) page[n][u] = page_next[u];
+      copy(n, page[n], code[n], on[n]);
       advance();
+      ask(page_next);
     }
-    put = later;
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) settle(i, code[i], on[i]);
+    for (int n = 0; n < kStages - 1; ++n) settle(n, code[n], on[n]);
   }
 
   int stage = 0;
-  while (use.next_row(a, rows)) {
-    const int head0 = use.kvh * a.share + (use.row - use.kvh * a.groups) * kCols;
-    const int heads = min(kCols, (use.kvh + 1) * a.share - head0), tile0 = use.tile;
+  for (int done = 0; done < entered; ++done) {
+    __syncwarp();
+    const Row mine = queue[done % kQueue];
+    const int kvh = mine.row / a.groups, head0 = kvh * a.share + (mine.row - kvh * a.groups) * kCols;
+    const int heads = min(kCols, (kvh + 1) * a.share - head0);
+    const bool begins = mine.ends & 1;
 
     // queries, times a power of two per head; heads past the group's repeat as zero
     uint32_t q[NT][kKey][8];
@@ -302,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_attention8(const __grid_c
         for (int h = 0; h < 2; ++h) {
           const int d = 64 * i + 16 * t + 8 * h;
           raw[i][h] = 8 * n + g < heads && d < D
-                          ? load16(static_cast<const T *>(a.p.q) + use.s * a.p.q_seq + (head0 + 8 * n + g) * a.p.q_head + d)
+                          ? load16(static_cast<const T *>(a.p.q) + mine.s * a.p.q_seq + (head0 + 8 * n + g) * a.p.q_head + d)
                           : make_uint4(0, 0, 0, 0);
           const uint32_t w[4] = {raw[i][h].x, raw[i][h].y, raw[i][h].z, raw[i][h].w};
 #pragma unroll
@@ -342,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_attention8(const __grid_c
       for (int i = 0; i < 2 * kWords; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
     }
 
-    for (; use.tile < use.tile1; ++use.tile) {
+    for (int left = mine.tiles; left > 0; --left) {
       copies_wait<kStages - 2>();
       __syncwarp();  // the scales that other lanes put there
       uint32_t code_next[kUnits], on_next[kUnits];
@@ -482,11 +542,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_attention8(const __grid_c
     }
 
     // the row's outputs relative to m, 2^lift<T>() times, as l
-    const bool whole = tile0 == 0 && use.tile1 == use.sp.tiles;
-    const int at_part = 2 * warp + (tile0 == 0);  // the warp's first row, or its last
-    if (!whole && lane == 0) part_sh[at_part] = make_int4(use.s, use.row, tile0 == 0, use.tile1 == use.sp.tiles);
+    const bool whole = mine.ends == 3;
+    const int at_part = 2 * warp + begins;  // the warp's first row, or its last
+    if (!whole && lane == 0) part_sh[at_part] = make_int4(mine.s, mine.row, begins, mine.ends >> 1);
     float *const outs = part_of(at_part);
-    if (!whole && tile0 == 0) {  // every lane is done with the ring
+    if (!whole && begins) {  // every lane is done with the ring
       copies_wait<0>();
       __syncwarp();
     }
@@ -517,14 +577,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_attention8(const __grid_c
             to[0] = make_float4(v[0], v[1], v[2], v[3]);
             to[1] = make_float4(v[4], v[5], v[6], v[7]);
           } else if (d < D) {
-            store8<T>(a, use.s, head0 + col, d, v);
+            store8<T>(a, mine.s, head0 + col, d, v);
           }
         }
         if (g == 0) {
           if (!whole)
             st_sh[at_part * kCols + col] = make_float4(m[n][e], sum, seen ? 1.0f : 0.0f, 1.0f);
           else if (a.p.lse)
-            store_lse<T>(a, use.s, head0 + col, seen, m[n][e], sum);
+            store_lse<T>(a, mine.s, head0 + col, seen, m[n][e], sum);
         }
       }
   }
@@ -594,8 +654,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) k_attention8(const __grid_c
 
 // CTAs (a cluster) that take a row of up to `reach` positions between them, as
 // in attention.cu; 0: equal slices.
-int cluster_of(int64_t rows, int64_t reach, int dp) {
-  const int64_t sms = sm_count(), fit = sms * kBlocks;
+int cluster_of(int64_t rows, int64_t reach, int dp, int nt) {
+  const int64_t sms = sm_count(), fit = sms * per_sm8(dp, nt);
   int n = 1;
   while (n < kCluster && rows * 2 * n <= fit * 7 / 8 &&
          (rows * 2 * n <= sms ? n : 2 * n) * kWarps * 16 * units8(dp) < reach)
@@ -631,7 +691,7 @@ fp4_status launch(At8Params b, cudaStream_t s) {
   const int64_t tiles = ceil_div(rows * ceil_div(room, a.tile), kWarps);  // no more CTAs than the table has tiles
   if (rows > INT32_MAX) return FP4_ERR_SHAPE;
   const int64_t reach = (int64_t)a.p.window + 15 + ceil_div(a.p.sinks, a.tile) * a.tile;
-  a.direct = cluster_of(rows, a.p.window && reach < room ? reach : room, DP);
+  a.direct = cluster_of(rows, a.p.window && reach < room ? reach : room, DP, NT);
   a.ctas = (int)(a.direct ? rows * a.direct : tiles < most ? tiles : most);
   if (a.direct) {
     const size_t bytes = smem + (a.direct > 1 ? part : 0);
@@ -668,7 +728,7 @@ fp4_status launch_type(const At8Params &b, int nt, cudaStream_t s) {
 
 int64_t decode_attention8_workspace(int64_t seqs, int64_t room, int heads, int kv_heads, int head_dim) {
   const int dp = dp_of(head_dim), nt = nt_of(heads / kv_heads, dp), cols = 8 * nt;
-  if (cluster_of(seqs * kv_heads * ceil_div(heads / kv_heads, cols), room, dp)) return 0;
+  if (cluster_of(seqs * kv_heads * ceil_div(heads / kv_heads, cols), room, dp, nt)) return 0;
   return (int64_t)sm_count() * kPerSM * 2 * slot_floats(cols, dp) * sizeof(float);
 }
 
