@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
     end = at + n * (warp + 1) / kWarps;
     at += n * warp / kWarps;
   }
+  bool bad = false;  // a page outside the cache was met: reported at the end, not in the loop's way
   while (at < end) {
     const Span sp = span_of(a, s);
     const int64_t mine = (int64_t)rows * sp.tiles;
@@ -196,13 +197,13 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
           if (first < lo) w[u].on &= 0xFFFFu << (lo - first);  // base <= from < base + 16
           if (first + 16 > hi) w[u].on &= (1u << max(hi - first, 0)) - 1;
           if (!ok) {
-            if (w[u].on && lane == 0) raise_status(a.status, kStatusIndex);
+            bad |= w[u].on != 0;
             w[u].on = 0;
           }
         } else {
           const int i = first + (lane & 15);
           const bool in = i >= lo && i < hi;
-          if (in && !ok && lane < 16) raise_status(a.status, kStatusIndex);
+          bad |= in && !ok;
           const int place = i % c.page_size;
           w[u].k = (int64_t)page * c.k_page + (int64_t)place * c.k_place;
           w[u].v = (int64_t)page * c.v_page + (int64_t)place * c.v_place;
@@ -473,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
       }
   }
 
+  if (bad) raise_status(a.status, kStatusIndex);
   // join the warps' parts, row by row
   __syncthreads();
   const int4 mine = part_sh[lane % kParts];

@@ -18,13 +18,12 @@
 // product as two f16 parts (2^-22 of it left out, or 2^-32 of the largest).
 //
 // Loads.  Asynchronous 16-byte copies into a ring of shared memory that each
-// warp fills for itself, kStages - 1 tiles ahead, across the rows of its slice.
-// A lane reads back what it copied itself, so no barrier is needed; scales are
-// requested with the copies and put beside them a step later.
+// warp fills for itself, kStages - 1 tiles ahead, across the rows of its slice;
+// scales are requested with the copies and put beside them a step later.
 //
 // Layout, split and joins are those of attention.cu:
-//   S^T = K Q^T   lane (g, t) copies pieces 64 i + 16 t of keys g, g + 8
-//   O^T = V^T P^T lane (g, t) copies pieces 128 i + 16 g (or 8 g) of values
+//   S^T = K Q^T   lane (g, t) reads pieces 64 i + 16 t of keys g, g + 8
+//   O^T = V^T P^T lane (g, t) reads pieces 128 i + 16 g (or 8 g) of values
 //                 2 t, 2 t + 1, 2 t + 8, 2 t + 9
 #include <cooperative_groups.h>
 
@@ -36,15 +35,36 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+// i / d for 0 <= i < 2^31 by a multiplication: with 2^(l - 1) < d <= 2^l and m =
+// ceil(2^(31 + l) / d), which is below 2^32 for d > 1, m d exceeds 2^(31 + l)
+// by less than d <= 2^l, so i m / 2^(31 + l) exceeds i / d by less than 1 / d.
+struct Divisor {
+  uint32_t m;
+  int shift;  // l - 1; -1: d = 1
+};
+inline Divisor divisor(int d) {
+  int l = 0;
+  while (((int64_t)1 << l) < d) ++l;
+  if (l == 0) return {0, -1};
+  return {(uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d), l - 1};
+}
+__device__ __forceinline__ int over(int i, const Divisor &d) {
+  return d.shift < 0 ? i : (int)(__umulhi((uint32_t)i, d.m) >> d.shift);
+}
+
 struct At8Params {
   AtParams a;
   fp4_kv_scales s;
-  int block_shift;  // log2 of the block, or -1: no power of two
+  Divisor page, block;
+  int64_t k_step, v_step;  // from a lane's row to its next
+  // strides in 32 bits (pages of whole units only)
+  int k_page, k_place, v_page, v_place, ks_page, ks_block, vs_page, vs_block;
 };
 
 constexpr int kStages = 3;
 // CTAs an SM holds at least, by the kernel's launch bounds.
 constexpr int per_sm8(int dp, int nt) { return nt == 1 && dp <= 128 ? 3 : 2; }
+constexpr float kNone = -3e38f;  // a running maximum before there is a score
 constexpr float kLift = 7.0f;  // weights are held 2^7 times as large (f16's smallest is 2^-24)
 
 // Groups of 16 positions a step.
@@ -60,8 +80,8 @@ constexpr int part_bytes(int cols, int dp) { return cols * (dp + 8) * 4; }
 __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t to, const void *from, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(on ? 8 : 0) : "memory");
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -69,6 +89,50 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ uint32_t shared_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// A stage's keys and values lie there by rows (positions) of DP bytes, in chunks
+// of 16.  Eight neighbouring lanes copy 128 consecutive bytes of a row (DP 64: two
+// rows of 64): where a lane copied the pieces that it reads itself, 4 rows to
+// eight lanes, the copies ran at 2.5 TB/s.  Chunks change places so that both the
+// copies and the reads meet all banks:
+//   keys    chunk c of row r at c ^ 4 (r & 1)           read by rows g, chunks t
+//   values  chunk c of row r at c ^ 2 ((r / 2) & 3)     read by rows 2 t, chunks g
+// (rows of 192 bytes shift by half the banks by themselves; their last four
+// chunks, and the values of DP 64, change places within four, and the latter's
+// rows r and r + 4 share 128 bytes).
+template <int DP>
+struct Layout {
+  static constexpr int kLanes = DP <= 64 ? 4 : DP <= 128 ? 8 : 16;  // of a row
+  static constexpr int kRows = 32 / kLanes, kSteps = 16 / kRows;    // rows of a copy, copies of 16
+  static __device__ __forceinline__ int row(int lane) {  // of a lane's keys and values in the first copy
+    return DP == 64 ? (lane >> 3) + (lane & 4) : lane / kLanes;
+  }
+  static __device__ __forceinline__ int chunk(int lane) { return lane % kLanes; }
+  // where copy j puts the chunk
+  static __device__ __forceinline__ int key(int lane, int j) {
+    const int r = row(lane) + kRows * j, c = chunk(lane);
+    return r * DP + 16 * (DP % 128 == 0 ? c ^ 4 * (r & 1) : c);
+  }
+  static __device__ __forceinline__ int value(int lane, int j) {
+    const int r = row(lane) + kRows * j, c = chunk(lane);
+    if (DP == 64) return 128 * ((r & 3) | (r >> 3) << 2) + 64 * (r >> 2 & 1) + 16 * (c ^ (r & 2));
+    return r * DP + 16 * (DP == 192 && c >= 8 ? c ^ (r & 2) : c ^ 2 * (r >> 1 & 3));
+  }
+  // where lane (g, t) finds piece i of key g (g + 8: 8 DP on)
+  static __device__ __forceinline__ int key_at(int g, int t, int i) {
+    return g * DP + 16 * (DP % 128 == 0 ? (4 * i + t) ^ 4 * (g & 1) : 4 * i + t);
+  }
+  // where it finds its piece of 16 bytes, i, of value 2 t + (h & 1) + 8 (h / 2)
+  static __device__ __forceinline__ int value_at(int g, int t, int h, int i) {
+    return (2 * t + (h & 1) + 8 * (h >> 1)) * DP + 128 * i + 16 * (g ^ 2 * t);
+  }
+  // and that of 8 bytes behind them
+  static __device__ __forceinline__ int value8_at(int g, int t, int h) {
+    const int in = 16 * (g >> 1 ^ 2 * (t & 1)) + 8 * (g & 1);
+    return DP == 64 ? 256 * (t & 1) + 128 * (h & 1) + 512 * (h >> 1) + 64 * (t >> 1) + in
+                    : (2 * t + (h & 1) + 8 * (h >> 1)) * DP + 128 + in;
+  }
+};
 
 // Four E4M3 codes as two pairs of f16.
 __device__ __forceinline__ void halves(uint32_t w, uint32_t &lo, uint32_t &hi) {
@@ -84,10 +148,12 @@ struct Row {
 };
 constexpr int kQueue = 8;  // rows between the copies and the work: kStages + 1 at most
 
+// UNITS: pages of whole units of 16 places, strides below 2^31.
 template <typename T, int DP, int NT, bool UNITS>
 __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const __grid_constant__ At8Params b) {
   constexpr int kCols = 8 * NT, kKey = DP / 64, kV16 = DP / 128, kV8 = DP / 64 % 2, kWords = DP / 32;
   constexpr int kUnits = units8(DP), kTile = 16 * kUnits, kParts = 2 * kWarps;
+  constexpr int kRows = Layout<DP>::kRows, kSteps = Layout<DP>::kSteps;
   const AtParams &a = b.a;
   extern __shared__ __align__(16) char smem8[];
   __shared__ int64_t scan[kWarps + 2];
@@ -156,7 +222,10 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
   // The tile that is copied next: position pos, tile `tile` of a row of which the
   // slice has those before tile1; where the row's keys, values (a lane's first
   // pieces), scales and page numbers are.
-  bool live = at < end;
+  // bad: a page outside the cache was met, reported at the end (a branch to it in
+  // the loop makes loads in flight be waited for: 64 sequences of up to 16384 took
+  // 233 us for 173).
+  bool live = at < end, bad = false;
   Span sp = live ? span_of(a, s) : Span{};
   int tile = 0, tile1 = 0, pos = 0, entered = 0;
   const int32_t *table = c.table;
@@ -182,8 +251,9 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
     keys = static_cast<const char *>(c.k) + kvh * c.k_head;
     values = static_cast<const char *>(c.v) + kvh * c.v_head;
     if (UNITS) {  // (lanes behind the head's end copy nothing: an address inside it)
-      keys += g * c.k_place + (16 * t < D ? 16 * t : 0);
-      values += 2 * t * c.v_place + ((kV16 ? 16 : 8) * g < D ? (kV16 ? 16 : 8) * g : 0);
+      const int in = 16 * Layout<DP>::chunk(lane) < D ? 16 * Layout<DP>::chunk(lane) : 0;
+      keys += Layout<DP>::row(lane) * c.k_place + in;
+      values += Layout<DP>::row(lane) * c.v_place + in;
     }
     codes = lane < 16 ? b.s.k_sf + kvh * b.s.k_head : b.s.v_sf + kvh * b.s.v_head;
   };
@@ -194,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
     else
       enter();
   };
-  const int64_t sf_page = lane < 16 ? b.s.k_page : b.s.v_page, sf_block = lane < 16 ? b.s.k_block : b.s.v_block;
+  const int sf_page = lane < 16 ? b.ks_page : b.vs_page, sf_block = lane < 16 ? b.ks_block : b.vs_block;
 
   // page numbers a step ahead of the copies (their loads are not waited for).
   // UNITS (pages of whole units): one for a unit, else lane i & 15 has that of
@@ -205,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
     for (int u = 0; u < kUnits; ++u) {
       const int i = pos + 16 * u + (UNITS ? 0 : lane & 15);
       page[u] = -1;
-      if (i < hi && (UNITS || i >= lo)) page[u] = table[a.shift >= 0 ? i >> a.shift : i / c.page_size];
+      if (i < hi && (UNITS || i >= lo)) page[u] = table[over(i, b.page)];
     }
   };
   // Copies the next tile into a stage and requests its scales: lanes 0 - 15
@@ -215,97 +285,61 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
     const uint32_t to0 = shared_at(ring) + stage * kUnits * unit_bytes(DP);
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
-      const uint32_t to = to0 + u * unit_bytes(DP) + 16 * lane, tv = to + 16 * DP;
+      const uint32_t to = to0 + u * unit_bytes(DP), tv = to + 16 * DP;
       const int first = pos + 16 * u, i = first + (lane & 15);
       int page = pages[u];
       const bool in = i >= lo && i < hi, ok = page >= 0 && page < c.pages;
-      if (in && !ok && lane < 16) raise_status(a.status, kStatusIndex);
+      bad |= in && !ok;
       on[u] = __ballot_sync(~0u, in && ok) & 0xFFFFu;
       if (on[u] == 0 && UNITS) {  // nothing is seen: zeros
 #pragma unroll
-        for (int e = 0; e < 2 * kKey + 4 * kV16; ++e)
+        for (int e = 0; e < DP / 16; ++e)
           *reinterpret_cast<uint4 *>(ring + (stage * kUnits + u) * unit_bytes(DP) + e * 512 + 16 * lane) = make_uint4(0, 0, 0, 0);
-        if (kV8)
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            *reinterpret_cast<uint2 *>(ring + (stage * kUnits + u) * unit_bytes(DP) + 16 * DP + 4 * kV16 * 512 + h * 256 +
-                                       8 * lane) = make_uint2(0, 0);
         code[u] = 0;
         continue;
       }
-      const int place0 = a.shift >= 0 ? (UNITS ? first : i) & (c.page_size - 1) : (UNITS ? first : i) % c.page_size;
+      const int place0 = (UNITS ? first : i) - over(UNITS ? first : i, b.page) * c.page_size;
       const int place = UNITS ? place0 + (lane & 15) : place0;
       code[u] = 0;
       if (in && ok) {
-        const int blk = b.block_shift >= 0 ? place >> b.block_shift : place / b.s.block;
-        code[u] = codes[page * sf_page + blk * sf_block];
+        const int blk = over(place, b.block);
+        code[u] = UNITS ? codes[(int64_t)page * sf_page + (int64_t)blk * sf_block]
+                        : codes[page * (lane < 16 ? b.s.k_page : b.s.v_page) + blk * (lane < 16 ? b.s.k_block : b.s.v_block)];
       }
       if (UNITS) {
         // every place of the unit is one of its page, so every address is inside the cache
-        const char *const k = keys + (int64_t)page * c.k_page + (int64_t)place0 * c.k_place;
-        const char *const v = values + (int64_t)page * c.v_page + (int64_t)place0 * c.v_place;
-        const bool all = on[u] == 0xFFFFu && D == DP;
+        const char *const k = keys + (int64_t)page * b.k_page + (int64_t)place0 * b.k_place;
+        const char *const v = values + (int64_t)page * b.v_page + (int64_t)place0 * b.v_place;
+        if (on[u] == 0xFFFFu && D == DP) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const char *const row = k + (h ? 8 * c.k_place : 0);
-          const bool there = on[u] >> (g + 8 * h) & 1;
+          for (int j = 0; j < kSteps; ++j)
+            if (DP != 192 || Layout<DP>::chunk(lane) < 12) copy16(to + Layout<DP>::key(lane, j), k + j * b.k_step);
 #pragma unroll
-          for (int e = 0; e < kKey; ++e)
-            if (all)
-              copy16(to + (h * kKey + e) * 512, row + 64 * e, true);
-            else if (64 * e + 16 * t < D)
-              copy16(to + (h * kKey + e) * 512, row + 64 * e, there);
-            else
-              copy16(to + (h * kKey + e) * 512, k, false);
-        }
+          for (int j = 0; j < kSteps; ++j)
+            if (DP != 192 || Layout<DP>::chunk(lane) < 12) copy16(tv + Layout<DP>::value(lane, j), v + j * b.v_step);
+        } else {
+          const bool inside = 16 * Layout<DP>::chunk(lane) < D;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const char *const row = v + ((h & 1) + 8 * (h >> 1)) * c.v_place;
-          const bool there = on[u] >> (2 * t + (h & 1) + 8 * (h >> 1)) & 1;
-#pragma unroll
-          for (int e = 0; e < kV16; ++e)
-            if (all)
-              copy16(tv + (h * kV16 + e) * 512, row + 128 * e, true);
-            else if (128 * e + 16 * g < D)
-              copy16(tv + (h * kV16 + e) * 512, row + 128 * e, there);
-            else
-              copy16(tv + (h * kV16 + e) * 512, v, false);
-          if (kV8) {
-            const bool yes = 128 * kV16 + 8 * g < D;
-            // (the lane's pieces of 16 bytes lie at 16 g, this one at 8 g)
-            const char *const at8 = row + (kV16 ? 128 * kV16 - 8 * g : 0);
-            copy8(tv - 8 * lane + 4 * kV16 * 512 + h * 256, yes ? at8 : v, yes && (all || there));
+          for (int j = 0; j < kSteps; ++j) {
+            const bool yes = inside && (on[u] >> (Layout<DP>::row(lane) + kRows * j) & 1);
+            if (DP == 192 && Layout<DP>::chunk(lane) >= 12) continue;
+            copy16(to + Layout<DP>::key(lane, j), k + j * b.k_step, yes);
+            copy16(tv + Layout<DP>::value(lane, j), v + j * b.v_step, yes);
           }
         }
       } else {
         const int64_t k0 = (int64_t)page * c.k_page + (int64_t)place0 * c.k_place;
         const int64_t v0 = (int64_t)page * c.v_page + (int64_t)place0 * c.v_place;
         const char *const nothing = static_cast<const char *>(a.p.q);  // an address for copies of no bytes
+        const int in = 16 * Layout<DP>::chunk(lane);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int j = g + 8 * h;
-          const char *k = keys + __shfl_sync(~0u, k0, j) + 16 * t;
-          const bool there = on[u] >> j & 1;
-#pragma unroll
-          for (int e = 0; e < kKey; ++e) {
-            const bool yes = there && 64 * e + 16 * t < D;
-            copy16(to + (h * kKey + e) * 512, yes ? k + 64 * e : nothing, yes);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int j = 2 * t + (h & 1) + 8 * (h >> 1);
-          const char *v = values + __shfl_sync(~0u, v0, j);
-          const bool there = on[u] >> j & 1;
-#pragma unroll
-          for (int e = 0; e < kV16; ++e) {
-            const bool yes = there && 128 * e + 16 * g < D;
-            copy16(tv + (h * kV16 + e) * 512, yes ? v + 128 * e + 16 * g : nothing, yes);
-          }
-          if (kV8) {
-            const bool yes = there && 128 * kV16 + 8 * g < D;
-            copy8(tv - 8 * lane + 4 * kV16 * 512 + h * 256, yes ? v + 128 * kV16 + 8 * g : nothing, yes);
-          }
+        for (int j = 0; j < kSteps; ++j) {
+          const int row = Layout<DP>::row(lane) + kRows * j;
+          const char *const k = keys + __shfl_sync(~0u, k0, row) + in, *const v = values + __shfl_sync(~0u, v0, row) + in;
+          const bool yes = in < D && (on[u] >> row & 1);
+          if (DP == 192 && Layout<DP>::chunk(lane) >= 12) continue;
+          copy16(to + Layout<DP>::key(lane, j), yes ? k : nothing, yes);
+          copy16(tv + Layout<DP>::value(lane, j), yes ? v : nothing, yes);
         }
       }
     }
@@ -396,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
     bool seen = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      m[n][0] = m[n][1] = mo[n][0] = mo[n][1] = -INFINITY;
+      m[n][0] = m[n][1] = mo[n][0] = mo[n][1] = kNone;
       l[n][0] = l[n][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < 2 * kWords; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
@@ -415,12 +449,13 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
       float sc[kUnits][NT][4], so[kUnits][NT][4];
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const uint4 *kp = reinterpret_cast<const uint4 *>(here + u * unit_bytes(DP)) + lane;
+        const char *const kp = here + u * unit_bytes(DP);
 #pragma unroll
         for (int n = 0; n < NT; ++n) sc[u][n][0] = sc[u][n][1] = sc[u][n][2] = sc[u][n][3] = 0.0f;
 #pragma unroll
         for (int i = 0; i < kKey; ++i) {
-          const uint4 k0 = kp[32 * i], k1 = kp[32 * (kKey + i)];
+          const uint4 k0 = *reinterpret_cast<const uint4 *>(kp + Layout<DP>::key_at(g, t, i));
+          const uint4 k1 = *reinterpret_cast<const uint4 *>(kp + Layout<DP>::key_at(g, t, i) + 8 * DP);
           const uint32_t x[4] = {k0.x, k0.y, k0.z, k0.w}, y[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -434,15 +469,6 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
       }
       // scores: lane (g, t) has positions g, g + 8 of heads 2 t, 2 t + 1
       bool passed = false;
-      float base[NT][2], baseo[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          base[n][e] = m[n][e] == -INFINITY ? 0.0f : m[n][e];
-          baseo[n][e] = mo[n][e] == -INFINITY ? 0.0f : mo[n][e];
-          passed |= m[n][e] == -INFINITY || mo[n][e] == -INFINITY;
-        }
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
         const float *info = reinterpret_cast<const float *>(here + u * unit_bytes(DP) + 32 * DP);
@@ -451,13 +477,15 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
         seen |= on != 0;
         const bool on0 = on >> g & 1, on1 = on >> (g + 8) & 1;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+          const float qk[4] = {qs[n][0] * ks[0], qs[n][1] * ks[0], qs[n][0] * ks[1], qs[n][1] * ks[1]};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sc[u][n][e] = (e >> 1 ? on1 : on0) ? sc[u][n][e] * qs[n][e & 1] * ks[e >> 1] : -INFINITY;
+            sc[u][n][e] = (e >> 1 ? on1 : on0) ? sc[u][n][e] * qk[e] : -INFINITY;
             so[u][n][e] = sc[u][n][e] + ve[e >> 1];
-            passed |= sc[u][n][e] > base[n][e & 1] + kSlack || so[u][n][e] > baseo[n][e & 1] + kSlack;
+            passed |= sc[u][n][e] > m[n][e & 1] + kSlack || so[u][n][e] > mo[n][e & 1] + kSlack;
           }
+        }
       }
       if (__any_sync(~0u, passed)) {
 #pragma unroll
@@ -475,10 +503,8 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
               top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
               topo = fmaxf(topo, __shfl_xor_sync(~0u, topo, x));
             }
-            base[n][e] = top == -INFINITY ? 0.0f : top;
-            baseo[n][e] = topo == -INFINITY ? 0.0f : topo;
-            l[n][e] *= ex2(m[n][e] - base[n][e]);
-            const float fade = ex2(mo[n][e] - baseo[n][e]);
+            l[n][e] *= ex2(m[n][e] - top);
+            const float fade = ex2(mo[n][e] - topo);
             m[n][e] = top;
             mo[n][e] = topo;
 #pragma unroll
@@ -496,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
           float w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            l[n][e & 1] += ex2(sc[u][n][e] - base[n][e & 1]);
-            w[e] = ex2(so[u][n][e] - (baseo[n][e & 1] - kLift));
+            l[n][e & 1] += ex2(sc[u][n][e] - m[n][e & 1]);
+            w[e] = ex2(so[u][n][e] - (mo[n][e & 1] - kLift));
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -514,10 +540,10 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             if (i < kV16) {
-              const uint4 w = *reinterpret_cast<const uint4 *>(vp + (h * kV16 + i) * 512 + 16 * lane);
+              const uint4 w = *reinterpret_cast<const uint4 *>(vp + Layout<DP>::value_at(g, t, h, i));
               v[h][0] = w.x, v[h][1] = w.y, v[h][2] = w.z, v[h][3] = w.w;
             } else {
-              const uint2 w = *reinterpret_cast<const uint2 *>(vp + 4 * kV16 * 512 + h * 256 + 8 * lane);
+              const uint2 w = *reinterpret_cast<const uint2 *>(vp + Layout<DP>::value8_at(g, t, h));
               v[h][0] = w.x, v[h][1] = w.y;
             }
           }
@@ -561,7 +587,8 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
         const int col = 8 * n + 2 * t + e;
         if (col >= heads) continue;
         // (no maximum: nothing seen, or sums that are NaN already)
-        float w = m[n][e] == -INFINITY || mo[n][e] == -INFINITY ? 1.0f : ex2(mo[n][e] - m[n][e] - (kLift - lift<T>()));
+        if (m[n][e] == kNone) m[n][e] = -INFINITY;
+        float w = m[n][e] == -INFINITY || mo[n][e] == kNone ? 1.0f : ex2(mo[n][e] - m[n][e] - (kLift - lift<T>()));
         if (whole) w = seen ? w / sum : 0.0f;
 #pragma unroll
         for (int x = 0; x < kWords / 2; ++x) {
@@ -589,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
       }
   }
 
+  if (bad) raise_status(a.status, kStatusIndex);
   // join the warps' parts, row by row
   copies_wait<0>();
   __syncthreads();
@@ -685,6 +713,8 @@ fp4_status launch(At8Params b, cudaStream_t s) {
   AtParams &a = b.a;
   const fp4_kv_cache &c = a.p.cache;
   a.tile = 16 * units8(DP);
+  b.k_step = Layout<DP>::kRows * c.k_place;
+  b.v_step = Layout<DP>::kRows * c.v_place;
   const int64_t rows = (int64_t)c.seqs * c.kv_heads * a.groups;
   const int64_t room = (int64_t)c.seq_pages * c.page_size;
   const int64_t most = (int64_t)sm_count() * (per < kPerSM ? per : kPerSM);
@@ -711,7 +741,9 @@ fp4_status launch(At8Params b, cudaStream_t s) {
 
 template <typename T, int DP, int NT>
 fp4_status launch_pages(const At8Params &b, cudaStream_t s) {
-  return b.a.p.cache.page_size % 16 == 0 ? launch<T, DP, NT, true>(b, s) : launch<T, DP, NT, false>(b, s);
+  const fp4_kv_cache &c = b.a.p.cache;
+  const int64_t far = c.k_page | c.k_place | c.v_page | c.v_place | b.s.k_page | b.s.k_block | b.s.v_page | b.s.v_block;
+  return c.page_size % 16 == 0 && far <= INT32_MAX ? launch<T, DP, NT, true>(b, s) : launch<T, DP, NT, false>(b, s);
 }
 
 template <typename T>
@@ -744,7 +776,10 @@ fp4_status launch_decode_attention8(const fp4_attention8_params &p, cudaStream_t
   const int nt = nt_of(a.share, dp_of(c.head_dim));
   a.groups = (a.share + 8 * nt - 1) / (8 * nt);
   a.shift = log2_or(c.page_size, -1);
-  b.block_shift = log2_or(b.s.block, -1);
+  b.page = divisor(c.page_size);
+  b.block = divisor(b.s.block);
+  b.k_page = (int)c.k_page, b.k_place = (int)c.k_place, b.v_page = (int)c.v_page, b.v_place = (int)c.v_place;
+  b.ks_page = (int)b.s.k_page, b.ks_block = (int)b.s.k_block, b.vs_page = (int)b.s.v_page, b.vs_block = (int)b.s.v_block;
   a.out16 = aligned16(a.p.out) && a.p.out_seq % 8 == 0 && a.p.out_head % 8 == 0;
   a.scale2 = a.p.scale * 1.44269504088896f;
   a.ws = static_cast<float *>(a.p.workspace);
