@@ -578,6 +578,8 @@ fp4_status launch(AtParams a, cudaStream_t s) {
   }
   const fp4_kv_cache &c = a.p.cache;
   a.tile = tile_of(DP);
+  a.least = kWarps;
+  a.bundle = 1;
   // no more CTAs than the table has tiles
   const int64_t rows = (int64_t)c.seqs * c.kv_heads * a.groups;
   const int64_t room = (int64_t)c.seq_pages * c.page_size;

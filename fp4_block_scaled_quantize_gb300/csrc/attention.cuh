@@ -21,7 +21,9 @@ struct AtParams {
   int groups;   // head groups of a key head: ceil(heads / kv_heads / (8 NT))
   int share;    // heads / kv_heads
   int tile;     // positions of a tile: 16 per unit
-  int ctas;     // CTAs of the main kernel
+  int ctas;     // slices of the list of tiles: one for a CTA of the main kernel, or more
+  int least;    // tiles of a slice, at least
+  int bundle;   // rows whose tiles are one item of the list, worked on side by side
   int direct;   // CTAs (a cluster) that take a row between them, or 0: equal slices
   int shift;    // log2 page_size, or -1: no power of two
   int out16;    // rows of out allow 16-byte stores
@@ -139,7 +141,7 @@ __device__ __forceinline__ Span span_of(const AtParams &a, int s) {
 // in which a slice of the list begins (or the sequence `which`).
 struct Found {
   int64_t total, start;  // start: list index of the found sequence's first tile
-  int64_t ctas;          // CTAs that share the list: a tile or more for each warp
+  int64_t ctas;          // slices that share the list
   int seq;
 };
 template <int THREADS>
@@ -156,7 +158,7 @@ __device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *share
     }
     Found f;
     f.total = __shfl_sync(~0u, inc, seqs - 1);
-    f.ctas = min((int64_t)a.ctas, (f.total + kWarps - 1) / kWarps);
+    f.ctas = min((int64_t)a.ctas, (f.total + a.least - 1) / a.least);
     const int64_t x = slice < f.ctas ? f.total * slice / f.ctas : f.total;
     const uint32_t hit = __ballot_sync(~0u, which < 0 ? x >= inc - sum && x < inc : lane == which);
     f.seq = hit ? __ffs(hit) - 1 : seqs;
@@ -181,7 +183,7 @@ __device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *share
     if (w < warp) before += shared[w];
     total += shared[w];
   }
-  const int64_t ctas = min((int64_t)a.ctas, (total + kWarps - 1) / kWarps);
+  const int64_t ctas = min((int64_t)a.ctas, (total + a.least - 1) / a.least);
   const int64_t x = slice < ctas ? total * slice / ctas : total;
   if (which < 0 ? x >= before && x < before + sum : which >= s0 && which < s1) {  // one thread, if any
     int64_t at = before;
@@ -297,7 +299,8 @@ __device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d
 // for each row.  Which parts a row has follows from the lengths, which are read
 // before the main grid is waited for: that grid is an ordinary launch, so what
 // came before it on the stream is complete.  A CTA's threads take eight outputs each, in groups
-// that walk every kGroups-th part four at a time; the first joins the groups.
+// that walk every kGroups-th part four at a time; the first joins the groups.  The
+// rows of a bundle have a CTA each.
 constexpr int kNarrow = 128, kWide = 1024;
 template <typename T, int DP, int NT, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constant__ AtParams a) {
@@ -306,22 +309,24 @@ __global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constan
   __shared__ int64_t scan[THREADS / 32 + 2];
   __shared__ float part_sh[kGroups][11][kItems];  // m, l, seen, eight outputs
   const fp4_kv_cache &c = a.p.cache;
-  const int rows = c.kv_heads * a.groups, slice = blockIdx.x + 1;
+  const int rows = c.kv_heads * a.groups / a.bundle, index = blockIdx.x / a.bundle, member = blockIdx.x % a.bundle;
+  const int slice = index + 1;
   const Found f = THREADS == kNarrow ? find<THREADS>(a, rows, slice, scan)
-                                     : find<THREADS>(a, rows, 0, scan, blockIdx.x / rows);
+                                     : find<THREADS>(a, rows, 0, scan, index / rows);
   int s = f.seq, row = 0, first = 0, parts = 1;
   if (s < c.seqs && span_of(a, s).tiles) {
     const int tiles = span_of(a, s).tiles;
     const int64_t at = f.total * slice / f.ctas;  // narrow: list index where the slice begins
-    row = THREADS == kNarrow ? (int)((at - f.start) / tiles) : blockIdx.x - s * rows;
+    row = THREADS == kNarrow ? (int)((at - f.start) / tiles) : index - s * rows;
     const int64_t begin = f.start + (int64_t)row * tiles;
     first = (int)(((begin + 1) * f.ctas - 1) / f.total);  // the CTA whose slice holds the row's first tile
     parts = (int)(((begin + tiles) * f.ctas - 1) / f.total) - first + 1;
-    if (THREADS == kNarrow && (begin == at || first != (int)blockIdx.x)) parts = 1;
+    if (THREADS == kNarrow && (begin == at || first != index)) parts = 1;
   }
   dependent_wait();  // also where there is nothing to do: this grid ends after the main one
   launch_dependents();
   if (parts == 1) return;
+  row = row * a.bundle + member;
   const int kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
   const int heads = min(kCols, (kvh + 1) * a.share - head0);
   const int group = THREADS < kItems ? 0 : threadIdx.x / kItems;
@@ -338,7 +343,8 @@ __global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constan
           st[i] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
           lo[i] = hi[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           if (w >= parts) continue;
-          const float *slot = a.ws + ((int64_t)(first + w) * 2 + (w == 0)) * slot_floats(kCols, DP);
+          const float *slot =
+              a.ws + (((int64_t)(first + w) * 2 + (w == 0)) * a.bundle + member) * slot_floats(kCols, DP);
           if (col < heads && d < c.head_dim) {  // what was written
             st[i] = *reinterpret_cast<const float4 *>(slot + kCols * DP + col * 4);
             lo[i] = *reinterpret_cast<const float4 *>(slot + col * DP + d);

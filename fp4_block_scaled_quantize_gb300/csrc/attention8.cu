@@ -61,14 +61,15 @@ struct At8Params {
   int k_page, k_place, v_page, v_place, ks_page, ks_block, vs_page, vs_block;
 };
 
-constexpr int kStages = 3;
+constexpr int kStages = 2;
+constexpr int kPerSM8 = 2;  // CTAs an SM holds at most (workspace bound)
 // CTAs an SM holds at least, by the kernel's launch bounds.
-constexpr int per_sm8(int dp, int nt) { return nt == 1 && dp <= 128 ? 3 : 2; }
+constexpr int per_sm8(int dp, int nt) { return dp <= 128 ? 2 : 1; }
 constexpr float kNone = -3e38f;  // a running maximum before there is a score
 constexpr float kLift = 7.0f;  // weights are held 2^7 times as large (f16's smallest is 2^-24)
 
 // Groups of 16 positions a step.
-constexpr int units8(int dp) { return dp <= 64 ? 2 : 1; }
+constexpr int units8(int dp) { return dp <= 64 ? 4 : dp <= 128 ? 2 : 1; }
 
 // The ring of a warp, a stage: keys, values, then per unit 32 floats (the keys'
 // scales, the values' exponents) and the mask of what is seen.
@@ -152,33 +153,28 @@ constexpr int kQueue = 8;  // rows between the copies and the work: kStages + 1 
 template <typename T, int DP, int NT, bool UNITS>
 __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const __grid_constant__ At8Params b) {
   constexpr int kCols = 8 * NT, kKey = DP / 64, kV16 = DP / 128, kV8 = DP / 64 % 2, kWords = DP / 32;
-  constexpr int kUnits = units8(DP), kTile = 16 * kUnits, kParts = 2 * kWarps;
+  constexpr int kUnits = units8(DP), kTile = 16 * kUnits;
   constexpr int kRows = Layout<DP>::kRows, kSteps = Layout<DP>::kSteps;
   const AtParams &a = b.a;
   extern __shared__ __align__(16) char smem8[];
   __shared__ int64_t scan[kWarps + 2];
-  __shared__ int4 part_sh[kParts];  // sequence (-1: none), row, begins with it, ends with it
+  __shared__ int part_sh[kWarps];  // clusters: whether a warp has a part of the row, and if it begins and ends (1, 2) there
   __shared__ Row queue_sh[kWarps][kQueue];
   const fp4_kv_cache &c = a.p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int D = c.head_dim, rows = c.kv_heads * a.groups;
-  // the warps' rings; outputs of rows that a warp ended (a row that it began
-  // last and did not end takes the place of its ring); their m, l, seen, 1; the
-  // partial row of a CTA of a cluster
+  const int D = c.head_dim, rows = c.kv_heads * a.groups / a.bundle;  // of the list, `bundle` rows in one
+  // the warps' rings; m, l, seen, 1 of partial rows (clusters: their outputs take
+  // the place of the rings); the partial row of a CTA of a cluster
   char *const ring = smem8 + warp * ring_bytes(DP);
-  char *const ended = smem8 + kWarps * ring_bytes(DP);
-  float4 *const st_sh = reinterpret_cast<float4 *>(ended + kWarps * part_bytes(kCols, DP));
-  float *const part = reinterpret_cast<float *>(st_sh + kParts * kCols);
-  auto part_of = [&](int p) {
-    return reinterpret_cast<float *>(p & 1 ? smem8 + (p >> 1) * ring_bytes(DP) : ended + (p >> 1) * part_bytes(kCols, DP));
-  };
+  float4 *const st_sh = reinterpret_cast<float4 *>(smem8 + kWarps * ring_bytes(DP));
+  float *const part = reinterpret_cast<float *>(st_sh + kWarps * kCols);
+  auto part_of = [&](int p) { return reinterpret_cast<float *>(smem8 + p * ring_bytes(DP)); };
 
   int64_t at, end, start;
   int s;
   dependent_wait();
   launch_dependents();
-  if (lane < 2) part_sh[2 * warp + lane] = make_int4(-1, 0, 0, 0);
-  __syncwarp();
+  if (lane == 0) part_sh[warp] = -1;
   const int rank = a.direct ? blockIdx.x % a.direct : 0, mine_row = a.direct ? blockIdx.x / a.direct : 0;
   if (a.direct) {
     s = mine_row / rows;
@@ -188,17 +184,20 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
     end = at + (int64_t)tiles * (rank + 1) / a.direct;
     at += (int64_t)tiles * rank / a.direct;
   } else {
-    const Found f = find<kThreads>(a, rows, blockIdx.x, scan);
+    // warps of a bundle share a slice
+    const int subs = kWarps / a.bundle;
+    const int64_t first = (int64_t)blockIdx.x * subs, slice = first + warp / a.bundle;
+    const Found f = find<kThreads>(a, rows, first, scan);
     s = f.seq;
     start = f.start;
     at = end = 0;
-    if (blockIdx.x < f.ctas) {
-      at = f.total * blockIdx.x / f.ctas;
-      end = f.total * (blockIdx.x + 1) / f.ctas;
+    if (slice < f.ctas) {
+      at = f.total * slice / f.ctas;
+      end = f.total * (slice + 1) / f.ctas;
     }
   }
   // sequences that see nothing are in no slice: their rows are written here
-  for (int e = a.direct ? s : blockIdx.x; e < c.seqs; e += a.direct ? c.seqs : a.ctas) {
+  for (int e = a.direct ? s : blockIdx.x; e < c.seqs; e += a.direct ? c.seqs : gridDim.x) {
     const int given = a.p.lengths[e];
     if (a.direct && (rank || mine_row != s * rows)) break;
     if (threadIdx.x == 0 && (given < 0 || given > (int64_t)c.seq_pages * c.page_size))
@@ -212,8 +211,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
     }
   }
 
-  // each warp takes a quarter of the slice by itself
-  {
+  if (a.direct) {  // a quarter of the CTA's tiles for each warp
     const int64_t n = end - at;
     end = at + n * (warp + 1) / kWarps;
     at += n * warp / kWarps;
@@ -238,8 +236,8 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
       start += (int64_t)rows * sp.tiles;
       sp = span_of(a, ++s);
     }
-    const int row = (int)((at - start) / sp.tiles), kvh = row / a.groups;
-    tile = (int)(at - start - (int64_t)row * sp.tiles);
+    const int item = (int)((at - start) / sp.tiles), row = item * a.bundle + warp % a.bundle, kvh = row / a.groups;
+    tile = (int)(at - start - (int64_t)item * sp.tiles);
     tile1 = (int)min((int64_t)sp.tiles, tile + (end - at));
     at += tile1 - tile;
     if (lane == 0)
@@ -381,7 +379,6 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
     const Row mine = queue[done % kQueue];
     const int kvh = mine.row / a.groups, head0 = kvh * a.share + (mine.row - kvh * a.groups) * kCols;
     const int heads = min(kCols, (kvh + 1) * a.share - head0);
-    const bool begins = mine.ends & 1;
 
     // queries, times a power of two per head; heads past the group's repeat as zero
     uint32_t q[NT][kKey][8];
@@ -567,14 +564,20 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
       stage = stage == kStages - 1 ? 0 : stage + 1;
     }
 
-    // the row's outputs relative to m, 2^lift<T>() times, as l
+    // the row's outputs relative to m, 2^lift<T>() times, as l: the result, or a
+    // partial row for the join (clusters: in this warp's ring, which is done with)
     const bool whole = mine.ends == 3;
-    const int at_part = 2 * warp + begins;  // the warp's first row, or its last
-    if (!whole && lane == 0) part_sh[at_part] = make_int4(mine.s, mine.row, begins, mine.ends >> 1);
-    float *const outs = part_of(at_part);
-    if (!whole && begins) {  // every lane is done with the ring
+    const int pitch = a.direct ? DP + 8 : DP;
+    float *outs = part_of(warp);
+    float4 *stats = st_sh + warp * kCols;
+    if (!whole && a.direct) {
+      if (lane == 0) part_sh[warp] = mine.ends;
       copies_wait<0>();
       __syncwarp();
+    } else if (!whole) {
+      const int64_t slice = (int64_t)blockIdx.x * (kWarps / a.bundle) + warp / a.bundle;
+      outs = a.ws + ((slice * 2 + (mine.ends & 1)) * a.bundle + warp % a.bundle) * slot_floats(kCols, DP);
+      stats = reinterpret_cast<float4 *>(outs + kCols * DP);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -600,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
             v[2 * j + 1] = o[n][4 * x + j][2 + e] * w;
           }
           if (!whole) {
-            float4 *to = reinterpret_cast<float4 *>(outs + col * (DP + 8) + d);
+            float4 *to = reinterpret_cast<float4 *>(outs + col * pitch + d);
             to[0] = make_float4(v[0], v[1], v[2], v[3]);
             to[1] = make_float4(v[4], v[5], v[6], v[7]);
           } else if (d < D) {
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
         }
         if (g == 0) {
           if (!whole)
-            st_sh[at_part * kCols + col] = make_float4(m[n][e], sum, seen ? 1.0f : 0.0f, 1.0f);
+            stats[col] = make_float4(m[n][e], sum, seen ? 1.0f : 0.0f, 1.0f);
           else if (a.p.lse)
             store_lse<T>(a, mine.s, head0 + col, seen, m[n][e], sum);
         }
@@ -617,45 +620,38 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
   }
 
   if (bad) raise_status(a.status, kStatusIndex);
-  // join the warps' parts, row by row
+  if (!a.direct) return;
+
+  // join the warps' parts of the row
   copies_wait<0>();
   __syncthreads();
-  const int4 mine = part_sh[lane % kParts];
-  uint32_t there = __ballot_sync(~0u, mine.x >= 0) & ((1u << kParts) - 1);
-  bool partial = false;
-  while (there) {
-    const int i0 = __ffs(there) - 1;
-    const int s = __shfl_sync(~0u, mine.x, i0), row = __shfl_sync(~0u, mine.y, i0);
-    const bool begins = __shfl_sync(~0u, mine.z, i0);
-    const uint32_t parts = __ballot_sync(~0u, mine.x == s && mine.y == row) & there;
-    const bool whole = begins && __shfl_sync(~0u, mine.w, 31 - __clz(parts));
-    there &= ~parts;
-    const int kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
-    const int heads = min(kCols, (kvh + 1) * a.share - head0);
-    float *slot = a.direct ? part : a.ws + (blockIdx.x * 2 + begins) * (int64_t)slot_floats(kCols, DP);
-    partial = !whole;
+  const int row = mine_row - s * rows, kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
+  const int heads = min(kCols, (kvh + 1) * a.share - head0);
+  const int have = part_sh[lane % kWarps];
+  const uint32_t parts = __ballot_sync(~0u, have >= 0) & ((1u << kWarps) - 1);
+  const bool partial = parts != 0 && a.direct > 1;
+  if (parts)
     for (int item = threadIdx.x; item < heads * (DP / 8); item += kThreads) {
       const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
       if (d >= D) continue;
-      const Whole r = join_all<kParts>([&](int q, float4 &st, float4 &lo, float4 &hi) {
+      const Whole r = join_all<kWarps>([&](int q, float4 &st, float4 &lo, float4 &hi) {
         if (!(parts >> q & 1)) return;
         const float *from = part_of(q) + col * (DP + 8) + d;
         st = st_sh[q * kCols + col];
         lo = *reinterpret_cast<const float4 *>(from);
         hi = *reinterpret_cast<const float4 *>(from + 4);
       });
-      if (whole) {
+      if (a.direct == 1) {
         finish<T>(a, s, head0 + col, d, r.j, r.seen);
         continue;
       }
       const float *v = r.j.v;
-      float *out = slot + col * DP + d;
+      float *out = part + col * DP + d;
       *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
       *reinterpret_cast<float4 *>(out + 4) = make_float4(v[4], v[5], v[6], v[7]);
       if (d == 0)
-        *reinterpret_cast<float4 *>(slot + kCols * DP + col * 4) = make_float4(r.j.top, r.j.sum, r.seen ? 1.0f : 0.0f, 1.0f);
+        *reinterpret_cast<float4 *>(part + kCols * DP + col * 4) = make_float4(r.j.top, r.j.sum, r.seen ? 1.0f : 0.0f, 1.0f);
     }
-  }
   if (a.direct < 2) return;
 
   // join the cluster's partial rows, an output piece a thread, in CTA order
@@ -663,8 +659,6 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
     for (int i = threadIdx.x; i < slot_floats(kCols, DP); i += kThreads)
       part[i] = i >= kCols * DP && i % 4 == 0 ? -INFINITY : 0.0f;
   cg::this_cluster().sync();
-  const int row = mine_row - s * rows, kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
-  const int heads = min(kCols, (kvh + 1) * a.share - head0);
   for (int item = threadIdx.x * a.direct + rank; item < heads * (DP / 8); item += kThreads * a.direct) {
     const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
     if (d >= D) continue;
@@ -697,7 +691,7 @@ fp4_status launch(At8Params b, cudaStream_t s) {
   constexpr int kMaxDev = 64;
   static std::atomic<int> occupancy[kMaxDev];
   constexpr int cols = 8 * NT;
-  constexpr size_t smem = kWarps * (ring_bytes(DP) + part_bytes(cols, DP)) + 2 * kWarps * cols * sizeof(float4);
+  constexpr size_t smem = kWarps * (ring_bytes(DP) + cols * sizeof(float4));
   constexpr size_t part = slot_floats(cols, DP) * sizeof(float);
   static_assert(ring_bytes(DP) >= part_bytes(cols, DP), "a part takes the place of a ring");
   auto kern = k_attention8<T, DP, NT, UNITS>;
@@ -717,25 +711,31 @@ fp4_status launch(At8Params b, cudaStream_t s) {
   b.v_step = Layout<DP>::kRows * c.v_place;
   const int64_t rows = (int64_t)c.seqs * c.kv_heads * a.groups;
   const int64_t room = (int64_t)c.seq_pages * c.page_size;
-  const int64_t most = (int64_t)sm_count() * (per < kPerSM ? per : kPerSM);
-  const int64_t tiles = ceil_div(rows * ceil_div(room, a.tile), kWarps);  // no more CTAs than the table has tiles
+  const int64_t most = (int64_t)sm_count() * (per < kPerSM8 ? per : kPerSM8);
   if (rows > INT32_MAX) return FP4_ERR_SHAPE;
   const int64_t reach = (int64_t)a.p.window + 15 + ceil_div(a.p.sinks, a.tile) * a.tile;
   a.direct = cluster_of(rows, a.p.window && reach < room ? reach : room, DP, NT);
-  a.ctas = (int)(a.direct ? rows * a.direct : tiles < most ? tiles : most);
+  const int each = c.kv_heads * a.groups;
+  a.bundle = a.direct ? 1 : each % kWarps == 0 ? kWarps : each % 2 == 0 ? 2 : 1;
+  a.least = 4;
+  const int subs = kWarps / a.bundle;
+  const int64_t want = ceil_div(rows / a.bundle * ceil_div(room, a.tile), subs);  // no more than the table has tiles
+  const int64_t grid = a.direct ? rows * a.direct : want < most ? want : most;
+  a.ctas = (int)grid * subs;
   if (a.direct) {
     const size_t bytes = smem + (a.direct > 1 ? part : 0);
-    return launch_dependent_clusters(kern, a.direct, dim3((unsigned)a.ctas), dim3(kThreads), bytes, s, b) == cudaSuccess
+    return launch_dependent_clusters(kern, a.direct, dim3((unsigned)grid), dim3(kThreads), bytes, s, b) == cudaSuccess
                ? FP4_OK
                : FP4_ERR_CUDA;
   }
-  kern<<<(unsigned)a.ctas, kThreads, smem, s>>>(b);  // (an ordinary launch, as in attention.cu)
+  kern<<<(unsigned)grid, kThreads, smem, s>>>(b);  // (an ordinary launch, as in attention.cu)
   if (cudaGetLastError() != cudaSuccess) return FP4_ERR_CUDA;
   if (a.ctas < 2) return FP4_OK;
   const cudaError_t e =
-      rows * 4 <= a.ctas
+      rows * 4 <= (int64_t)a.ctas * a.bundle
           ? launch_dependent(k_attention_join<T, DP, NT, kWide>, dim3((unsigned)rows), dim3(kWide), 0, s, a)
-          : launch_dependent(k_attention_join<T, DP, NT, kNarrow>, dim3((unsigned)a.ctas - 1), dim3(kNarrow), 0, s, a);
+          : launch_dependent(k_attention_join<T, DP, NT, kNarrow>, dim3((unsigned)((a.ctas - 1) * a.bundle)), dim3(kNarrow), 0,
+                             s, a);
   return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
 
@@ -761,7 +761,7 @@ fp4_status launch_type(const At8Params &b, int nt, cudaStream_t s) {
 int64_t decode_attention8_workspace(int64_t seqs, int64_t room, int heads, int kv_heads, int head_dim) {
   const int dp = dp_of(head_dim), nt = nt_of(heads / kv_heads, dp), cols = 8 * nt;
   if (cluster_of(seqs * kv_heads * ceil_div(heads / kv_heads, cols), room, dp, nt)) return 0;
-  return (int64_t)sm_count() * kPerSM * 2 * slot_floats(cols, dp) * sizeof(float);
+  return (int64_t)sm_count() * kPerSM8 * kWarps * 2 * slot_floats(cols, dp) * sizeof(float);
 }
 
 fp4_status launch_decode_attention8(const fp4_attention8_params &p, cudaStream_t s) {
