@@ -11,12 +11,11 @@
 // values, 2 and 2 of queries), launch and dependent loads (position, page,
 // scale) for a few tokens.
 //
-// Layout.  A warp takes the tokens of one block and one key or value head: lanes
-// hold units of 16 elements (two pieces of 8, in the rotated part those whose
-// elements form pairs) of 32 / units rows at a time.  It goes over its rows
-// twice, for the largest magnitude and for the codes; the second time they come
-// from L1.  Warps look for blocks in windows of up to 32 tokens, of which each
-// lane locates one.  The queries' rows are shared out to the CTAs behind those.
+// Layout.  Lanes hold units of 16 elements (two pieces of 8, in the rotated part
+// those whose elements form pairs) of 32 / units rows; a team of warps takes the
+// tokens of one block and one key or value head.  Teams look for blocks in windows
+// of up to 32 tokens, of which each lane locates one.  The queries' rows are taken
+// by CTAs of their own, every so many.
 #include "serve.cuh"
 
 namespace fp4 {
@@ -24,25 +23,29 @@ namespace fp4 {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kResident = 2;  // CTAs an SM holds at least
 
 struct Ap8Params {
   fp4_append_params p;
   fp4_kv_scales s;
   int units;     // units of 16 elements of a head
-  int window;    // tokens that a warp looks at together
+  int team;      // warps that take a run together
+  int window;    // tokens that a team looks at together
+  int chunks;    // parts of the heads, each a team's
+  Divisor page, block;
   int kv_ctas;   // CTAs for keys and values; further ones for queries
   uint32_t *status;
 };
 
 // Where a token at position pos of a sequence lies: false if it is skipped or
 // outside a table.
-__device__ __forceinline__ bool locate8(const fp4_kv_cache &c, int64_t seq, int pos, int64_t limit, uint32_t *status,
-                                        int &page, int &place) {
+__device__ __forceinline__ bool locate8(const fp4_kv_cache &c, const Divisor &by, int64_t seq, int pos, int64_t limit,
+                                        uint32_t *status, int &page, int &place) {
   page = place = 0;
   if (pos < 0) return false;
   bool ok = seq >= 0 && seq < c.seqs && pos < c.seq_pages * c.page_size && pos < limit;
   if (ok) {
-    const int e = pos / c.page_size;
+    const int e = over(pos, by);
     place = pos - e * c.page_size;
     page = c.table[seq * c.table_stride + e];
     ok = page >= 0 && page < c.pages;
@@ -72,6 +75,12 @@ struct Two<__half> {
   }
 };
 
+// Four E4M3 codes as two pairs of f16.
+__device__ __forceinline__ void halves(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 // Two values as E4M3 codes (nearest-even; not finite: NaN), the first low.
 __device__ __forceinline__ uint32_t codes2(float a, float b) {
   uint16_t r;
@@ -95,59 +104,59 @@ __device__ __forceinline__ int code_for(float top) {
   return e > 0 ? e : 0;  // (a subnormal top has e <= 0 too)
 }
 
-// Where the two pieces of a unit lie, and what turns them.
+// How rows are read: whole pieces, pairs (i, i + rot_dim / 2) or neighbours; or
+// any pointers, strides and rot_dim.
+enum Kind { kHalves, kPairs, kAny };
+
+// Where the two pieces of a unit lie, and which of them are turned.
 struct Unit {
   int o1, o2;
-  bool halves, turn1, turn2;
+  bool turn1, turn2;
 };
+template <int KIND>
 __device__ __forceinline__ Unit unit_at(const fp4_append_params &p, int u) {
   Unit r;
-  const int turned = p.interleaved ? 0 : p.rot_dim / 16;
-  r.halves = u < turned;
-  r.o1 = r.halves ? 8 * u : 16 * u;  // 16 u = rot_dim + 16 (u - turned)
-  r.o2 = r.halves ? r.o1 + p.rot_dim / 2 : r.o1 + 8;
-  r.turn1 = r.halves || (p.interleaved && r.o1 < p.rot_dim);
-  r.turn2 = r.halves || (p.interleaved && r.o2 < p.rot_dim);
+  const bool halves = KIND == kHalves && u < p.rot_dim / 16;
+  r.o1 = halves ? 8 * u : 16 * u;  // behind the rotated part 16 u = rot_dim + 16 (u - rot_dim / 16)
+  r.o2 = halves ? r.o1 + p.rot_dim / 2 : r.o1 + 8;
+  r.turn1 = halves || (KIND == kPairs && r.o1 < p.rot_dim);
+  r.turn2 = halves || (KIND == kPairs && r.o2 < p.rot_dim);
   return r;
 }
 struct Turn {
   float co[8], si[8];
 };
 // cos and sin of a unit at a position.
-__device__ __forceinline__ void load_turn(const fp4_append_params &p, const Unit &u, int pos, Turn &r) {
-  if (!u.turn1 && !u.turn2) return;
-  const float *cs = p.rope + (int64_t)pos * p.rot_dim + (u.halves ? u.o1 : u.o1 / 2);
+template <int KIND>
+__device__ __forceinline__ void load_turn(const fp4_append_params &p, const Unit &u, bool key, int pos, Turn &r) {
+  if (!key || !u.turn1) return;
+  const float *cs = p.rope + (int64_t)pos * p.rot_dim + (KIND == kHalves ? u.o1 : u.o1 / 2);
 #pragma unroll
   for (int i = 0; i < 8; i += 4) {
-    if (i == 4 && !u.turn2) continue;
-    *reinterpret_cast<float4 *>(r.co + i) = *reinterpret_cast<const float4 *>(cs + i);
-    *reinterpret_cast<float4 *>(r.si + i) = *reinterpret_cast<const float4 *>(cs + p.rot_dim / 2 + i);
+    if (i == 4 && KIND == kPairs && !u.turn2) continue;
+    const float4 co = *reinterpret_cast<const float4 *>(cs + i);
+    const float4 si = *reinterpret_cast<const float4 *>(cs + p.rot_dim / 2 + i);
+    r.co[i] = co.x, r.co[i + 1] = co.y, r.co[i + 2] = co.z, r.co[i + 3] = co.w;
+    r.si[i] = si.x, r.si[i + 1] = si.y, r.si[i + 2] = si.z, r.si[i + 3] = si.w;
   }
 }
 // A unit's 16 values, turned.
-template <typename T>
-__device__ __forceinline__ void turn_unit(const Unit &u, uint4 a, uint4 b, const Turn &r, float (&x)[16]) {
+template <typename T, int KIND>
+__device__ __forceinline__ void turn_unit(bool key, const Unit &u, uint4 a, uint4 b, const Turn &r, float (&x)[16]) {
   const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 va = Two<T>::get(wa[i]), vb = Two<T>::get(wb[i]);
     x[2 * i] = va.x, x[2 * i + 1] = va.y, x[8 + 2 * i] = vb.x, x[8 + 2 * i + 1] = vb.y;
   }
-  if (u.halves) {
+  if (!key || !u.turn1) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = x[i], w = x[8 + i];
-      x[i] = v * r.co[i] - w * r.si[i];
-      x[8 + i] = w * r.co[i] + v * r.si[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < 4 ? u.turn1 : u.turn2) {
-        const float v = x[2 * i], w = x[2 * i + 1];
-        x[2 * i] = v * r.co[i] - w * r.si[i];
-        x[2 * i + 1] = w * r.co[i] + v * r.si[i];
-      }
+  for (int i = 0; i < 8; ++i) {
+    const int j = KIND == kHalves ? i : 2 * i, k = KIND == kHalves ? 8 + i : 2 * i + 1;
+    if (KIND == kPairs && i >= 4 && !u.turn2) continue;
+    const float v = x[j], w = x[k];
+    x[j] = v * r.co[i] - w * r.si[i];
+    x[k] = w * r.co[i] + v * r.si[i];
   }
 }
 // The same without whole pieces: 16 consecutive elements, any pointers and
@@ -169,138 +178,226 @@ __device__ __forceinline__ void turn_any(const fp4_append_params &p, const T *sr
   }
 }
 
-// Keys and values.  Item i of a warp: window i / (2 kv_heads), head i % (2
-// kv_heads) of the keys, then of the values.
-template <typename T, bool WHOLE>
-__device__ __forceinline__ void store_blocks(const Ap8Params &a) {
+// Keys and values.  Item i of a team of warps: window i / chunks, of its 2 kv_heads
+// heads (keys', then values') the chunk i % chunks.  The tokens of a window fall
+// into runs, each of one block, at consecutive places; a run may go on behind the
+// window.  Either the team takes one run after the other, its groups of lanes a
+// token each, or each group takes a run of its own.  A group holds kHold rows at a
+// time; of longer runs all but the last are loaded again for their codes.
+constexpr int kHold = 1;
+template <typename T, int KIND>
+__device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
   const fp4_append_params &p = a.p;
   const fp4_kv_cache &c = p.cache;
-  const int lane = threadIdx.x & 31, block = a.s.block, Hk = c.kv_heads;
-  const int rows = 32 / a.units, my_row = lane / a.units, my_unit = lane - my_row * a.units;
-  const bool busy = my_row < rows;
+  __shared__ float top_sh[2][kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = a.s.block, Hk = c.kv_heads;
+  const int groups = 32 / a.units, my_group = lane / a.units, my_unit = lane - my_group * a.units;
+  const int teams = kWarps / a.team, team = warp / a.team, mate = warp % a.team;
+  const int all = groups * a.team, my_all = mate * groups + my_group;  // the team's groups
+  int parity = 0;
   const int64_t limit = p.rot_dim ? p.rope_len : INT64_MAX;
-  const int64_t windows = (p.tokens + a.window - 1) / a.window, items = windows * 2 * Hk;
-  const Unit unit = unit_at(p, my_unit);
-  for (int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); item < items; item += (int64_t)a.kv_ctas * kWarps) {
-    const int64_t t0 = item / (2 * Hk) * a.window;
-    const int hv = (int)(item % (2 * Hk)), head = hv < Hk ? hv : hv - Hk;
-    const bool key = hv < Hk;
-    // token t0 + lane: its place, and whether it goes on with the block of the one before
+  const int64_t windows = (p.tokens + a.window - 1) / a.window, items = windows * a.chunks;
+  const Unit unit = unit_at<KIND>(p, my_unit);
+  for (int64_t item = (int64_t)cta * teams + team; item < items; item += (int64_t)a.kv_ctas * teams) {
+    const int64_t t0 = item / a.chunks * a.window;
+    const int chunk = (int)(item % a.chunks), hv0 = 2 * Hk * chunk / a.chunks, hv1 = 2 * Hk * (chunk + 1) / a.chunks;
+    // whether token t goes on with the block of the one before
     auto joins = [&](int64_t t) {
-      if (t < 1 || t >= p.tokens) return false;
+      if (!p.seq || t < 1 || t >= p.tokens) return false;
       const int pos = p.pos[t], last = p.pos[t - 1];
-      return pos > 0 && pos % block != 0 && pos == last + 1 && (p.seq ? p.seq[t] == p.seq[t - 1] : false);
+      const bool same = p.seq[t] == p.seq[t - 1];
+      return pos > 0 && pos == last + 1 && same && pos != over(pos, a.block) * block;
     };
     const int64_t mine = t0 + lane;
     const bool in = lane < a.window && mine < p.tokens;
     const int my_pos = in ? p.pos[mine] : -1;
     const int my_seq = in ? (p.seq ? p.seq[mine] : (int)mine) : 0;
-    int my_page, my_place;
-    const bool keep = locate8(c, my_seq, my_pos, limit, hv == 0 ? a.status : nullptr, my_page, my_place);
-    uint32_t leaders = __ballot_sync(~0u, keep && !joins(mine));
-    uint8_t *const sf0 = key ? a.s.k_sf : a.s.v_sf;
-    const int64_t sf_page = key ? a.s.k_page : a.s.v_page, sf_block = key ? a.s.k_block : a.s.v_block;
-    const int64_t sf_head = key ? a.s.k_head : a.s.v_head;
-    const int64_t my_sf = (int64_t)my_page * sf_page + (my_place / block) * sf_block + head * sf_head;
-    const int my_old = keep ? sf0[my_sf] : 0;
-    while (leaders) {
-      const int L = __ffs(leaders) - 1;
-      leaders &= leaders - 1;
+    const bool my_join = in && joins(mine);
+    const bool ranged = my_pos >= 0 && my_seq >= 0 && my_seq < c.seqs && my_pos < c.seq_pages * c.page_size && my_pos < limit;
+    if (my_pos >= 0 && !ranged && chunk == 0 && mate == 0) raise_status(a.status, kStatusIndex);
+    const int my_entry = over(max(my_pos, 0), a.page), my_place = my_pos - my_entry * c.page_size;
+    int my_page = -1;
+    if (ranged) my_page = c.table[my_seq * c.table_stride + my_entry];
+    const uint32_t joined = __ballot_sync(~0u, ranged && my_join), leaders = __ballot_sync(~0u, ranged && !my_join);
+    const int count = __popc(leaders);
+    // steps of a run after the other, and of runs side by side, with a run's own
+    // latencies as three steps
+    const int length = count ? (__popc(joined) + count - 1) / count + 1 : 1;
+    const bool apart = !p.seq || (count > 1 && (count + all - 1) / all * (length + 3) < count * ((length + all - 1) / all + 3));
+    for (int base = 0; base < count; base += apart ? all : 1) {
+      const int which = base + (apart ? my_all : 0);
+      const bool active = my_group < groups && which < count;
+      uint32_t rest = leaders;
+      for (int i = 0; i < (active ? which : base); ++i) rest &= rest - 1;
+      const int L = __ffs(rest) - 1;
       const int64_t t = t0 + L;
-      const int pos0 = __shfl_sync(~0u, my_pos, L), page = __shfl_sync(~0u, my_page, L);
-      const int place0 = __shfl_sync(~0u, my_place, L), old = __shfl_sync(~0u, my_old, L);
-      uint8_t *const sf = sf0 + __shfl_sync(~0u, my_sf, L);
-      const int begin = place0 % block, room = block - begin;
-      int n = 1;  // tokens of the block from here on (positions behind a table's end are not in them)
-      for (int base = 1; base < room; base += 32) {
-        const int i = base + lane;
-        const uint32_t on = __ballot_sync(~0u, i < room && joins(t + i) && pos0 + i < limit);
-        const int more = on == ~0u ? 32 : __ffs(~on) - 1;
-        n += more;
-        if (more < 32) break;
+      const int pos0 = __shfl_sync(~0u, my_pos, L), place0 = __shfl_sync(~0u, my_place, L);
+      const int blk = over(place0, a.block), begin = place0 - blk * block;
+      const uint32_t on = L < 31 ? joined >> (L + 1) : 0;
+      int n = __ffs(~on);  // tokens of the run in the window
+      const int most = (int)min((int64_t)(block - begin), limit - pos0);
+      if (!apart) {
+        if (L + n == a.window)  // it may go on behind
+          for (;; n += 32) {
+            const uint32_t more = __ballot_sync(~0u, n + lane < most && joins(t + n + lane));
+            if (more != ~0u) {
+              n += __ffs(~more) - 1;
+              break;
+            }
+          }
+      } else {
+        while (active && L + n >= a.window && n < most && joins(t + n)) ++n;
       }
-      const T *const src = (key ? static_cast<const T *>(p.k) + t * p.k_token + head * p.k_head
-                                : static_cast<const T *>(p.v) + t * p.v_token + head * p.v_head);
-      const int64_t step = key ? p.k_token : p.v_token;
-      uint8_t *const dst = static_cast<uint8_t *>(key ? c.k : c.v) + (int64_t)page * (key ? c.k_page : c.v_page) +
-                           head * (key ? c.k_head : c.v_head);
-      const int64_t place = key ? c.k_place : c.v_place;
-      Unit u = unit;
-      if (!key) u.turn1 = u.turn2 = u.halves = false;
-      auto values = [&](int r, float (&x)[16]) {
-        const T *row = src + r * step;
-        if (WHOLE) {
-          Turn turn;
-          load_turn(p, u, pos0 + r, turn);
-          const uint4 v = *reinterpret_cast<const uint4 *>(row + unit.o1), w = *reinterpret_cast<const uint4 *>(row + unit.o2);
-          turn_unit<T>(u, v, w, turn, x);
-        } else {
-          turn_any(p, row, my_unit, pos0 + r, key, x);
+      const int page = __shfl_sync(~0u, my_page, L);
+      const bool there = page >= 0 && page < c.pages;
+      if (active && !there && my_unit == 0) raise_status(a.status, kStatusIndex);
+      const int r0 = apart ? 0 : my_all, hop = apart ? 1 : all, rows = active && there ? n : 0;
+      int steps = (n + kHold * hop - 1) / (kHold * hop);
+      if (apart) steps = __reduce_max_sync(~0u, active ? steps : 1);
+      // kHold rows from r on; behind the last row, and for lanes without one, a row
+      // that is there again, which changes no largest.  Runs of one step: the next
+      // head's are requested before this one's are done with, and the heads share
+      // their cosines and sines.
+      uint4 v[kHold], w[kHold];
+      Turn turn[kHold];
+      auto ask = [&](int hv, int r, bool turns) {
+        const bool key = hv < Hk;
+        const int head = key ? hv : hv - Hk;
+        const T *const src = key ? static_cast<const T *>(p.k) + t * p.k_token + head * p.k_head
+                                 : static_cast<const T *>(p.v) + t * p.v_token + head * p.v_head;
+        const int64_t step = key ? p.k_token : p.v_token;
+#pragma unroll
+        for (int h = 0; h < kHold; ++h) {
+          if (KIND == kAny) continue;
+          const int q = max(min(r + h * hop, rows - 1), 0);
+          v[h] = *reinterpret_cast<const uint4 *>(src + q * step + unit.o1);
+          w[h] = *reinterpret_cast<const uint4 *>(src + q * step + unit.o2);
+          if (turns) load_turn<KIND>(p, unit, key, pos0 + q, turn[h]);
         }
       };
-      float top = 0.0f;
-      for (int r = my_row; r < n && busy; r += rows) {
-        float x[16];
-        values(r, x);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float v = fabsf(x[i]);
-          if (v <= 3.4028235e38f) top = fmaxf(top, v);
-        }
-      }
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
-      const bool fresh = begin == 0;
-      const int need = code_for(top), code = fresh || need > old ? need : old;
-      const float f = e8m0_inverse(code < 255 ? code : 254);
-      for (int r = my_row; r < n && busy; r += rows) {
-        float x[16];
-        values(r, x);
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = codes2(or_nan(x[2 * i]) * f, or_nan(x[2 * i + 1]) * f);
-        uint8_t *to = dst + (place0 + r) * place;
-        const int o1 = WHOLE ? unit.o1 : 16 * my_unit, o2 = WHOLE ? unit.o2 : o1 + 8;
-        *reinterpret_cast<uint2 *>(to + o1) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-        *reinterpret_cast<uint2 *>(to + o2) = make_uint2(w[4] | w[5] << 16, w[6] | w[7] << 16);
-      }
-      if (!fresh && code > old) {  // the block's other places, in the new unit
-        const float down = e8m0_inverse(127 + min(code - old, 100));
-        for (int r = my_row; r < block - n && busy; r += rows) {
-          const int q = place0 - begin + (r < begin ? r : r + n);
-          uint4 *at = reinterpret_cast<uint4 *>(dst + q * place + 16 * my_unit);
-          uint4 v = *at;
-          uint32_t *w = reinterpret_cast<uint32_t *>(&v);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t lo, hi;
-            asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-                : "=r"(lo), "=r"(hi)
-                : "r"(w[i]));
-            const float2 x = Two<__half>::get(lo), y = Two<__half>::get(hi);
-            w[i] = codes2(x.x * down, x.y * down) | codes2(y.x * down, y.y * down) << 16;
+      const bool single = steps == 1;
+      if (single) ask(hv0, r0, true);
+      for (int hv = hv0; hv < hv1; ++hv) {
+        const bool key = hv < Hk;
+        const int head = key ? hv : hv - Hk;
+        const T *const src = key ? static_cast<const T *>(p.k) + t * p.k_token + head * p.k_head
+                                 : static_cast<const T *>(p.v) + t * p.v_token + head * p.v_head;
+        const int64_t step = key ? p.k_token : p.v_token, place = key ? c.k_place : c.v_place;
+        uint8_t *const dst = static_cast<uint8_t *>(key ? c.k : c.v) + (int64_t)page * (key ? c.k_page : c.v_page) +
+                             head * (key ? c.k_head : c.v_head) + place0 * place;
+        uint8_t *const sf = (key ? a.s.k_sf : a.s.v_sf) + head * (key ? a.s.k_head : a.s.v_head) +
+                            (int64_t)page * (key ? a.s.k_page : a.s.v_page) + blk * (key ? a.s.k_block : a.s.v_block);
+        const int old = rows ? *sf : 0;
+        float x[kHold][16];
+        auto over_team = [&](float top) {
+          if (apart) {
+            const float own = top;
+            for (int o = 1; o < a.units; ++o) {
+              const int from = my_unit + o < a.units ? lane + o : lane + o - a.units;
+              top = fmaxf(top, __shfl_sync(~0u, own, from & 31));
+            }
+            return top;
           }
-          *at = v;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+          if (a.team > 1) {
+            if (lane == 0) top_sh[parity][warp] = top;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * a.team) : "memory");
+            for (int o = 0; o < a.team; ++o) top = fmaxf(top, top_sh[parity][team * a.team + o]);
+            parity ^= 1;
+          }
+          return top;
+        };
+        auto take = [&](int r, bool infinite) {
+#pragma unroll
+          for (int h = 0; h < kHold; ++h) {
+            const int q = max(min(r + h * hop, rows - 1), 0);
+            if (KIND == kAny)
+              turn_any(p, src + q * step, my_unit, pos0 + q, key, x[h]);
+            else
+              turn_unit<T, KIND>(key, unit, v[h], w[h], turn[h], x[h]);
+            if (infinite)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[h][e] = or_nan(x[h][e]);
+          }
+        };
+        // the largest; where that is an infinity, once more without infinities
+        float top;
+        bool infinite = false;
+        for (;; infinite = true) {
+          float more = 0.0f;
+          top = 0.0f;
+          for (int i = 0; i < steps; ++i) {
+            if (!single) ask(hv, r0 + i * kHold * hop, true);
+            take(r0 + i * kHold * hop, infinite);
+#pragma unroll
+            for (int h = 0; h < kHold; ++h)
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {  // (of a number and a NaN: the number)
+                top = fmaxf(top, fabsf(x[h][e]));
+                more = fmaxf(more, fabsf(x[h][e + 1]));
+              }
+          }
+          top = over_team(fmaxf(top, more));
+          if (infinite || !(apart ? __any_sync(~0u, isinf(top)) : isinf(top))) break;
         }
+        if (single && hv + 1 < hv1) ask(hv + 1, r0, false);
+        const int need = code_for(top), code = begin == 0 || need > old ? need : old;
+        const float f = e8m0_inverse(code < 255 ? code : 254);
+        for (int i = steps - 1;;) {
+#pragma unroll
+          for (int h = 0; h < kHold; ++h) {
+            const int r = r0 + (i * kHold + h) * hop;
+            if (r >= rows) continue;
+            uint32_t z[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = codes2(x[h][2 * e] * f, x[h][2 * e + 1] * f);
+            uint8_t *to = dst + r * place;
+            const int o1 = KIND != kAny ? unit.o1 : 16 * my_unit, o2 = KIND != kAny ? unit.o2 : o1 + 8;
+            *reinterpret_cast<uint2 *>(to + o1) = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
+            *reinterpret_cast<uint2 *>(to + o2) = make_uint2(z[4] | z[5] << 16, z[6] | z[7] << 16);
+          }
+          if (i-- == 0) break;
+          ask(hv, r0 + i * kHold * hop, true);
+          take(r0 + i * kHold * hop, infinite);
+        }
+        if (rows && begin != 0 && code > old) {  // the block's other places, in the new unit
+          const float down = e8m0_inverse(127 + min(code - old, 100));
+#pragma unroll 4
+          for (int r = r0; r < block - n; r += hop) {
+            const int q = (r < begin ? r : r + n) - begin;
+            uint4 *at = reinterpret_cast<uint4 *>(dst + q * place + 16 * my_unit);
+            const uint4 o = *at;
+            uint32_t z[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t lo, hi;
+              halves(z[e], lo, hi);
+              const float2 x = Two<__half>::get(lo), y = Two<__half>::get(hi);
+              z[e] = codes2(x.x * down, x.y * down) | codes2(y.x * down, y.y * down) << 16;
+            }
+            *at = make_uint4(z[0], z[1], z[2], z[3]);
+          }
+        }
+        if (rows && my_unit == 0 && (apart || my_all == 0) && code != old) *sf = (uint8_t)code;
       }
-      if (lane == 0 && code != old) *sf = (uint8_t)code;
     }
   }
 }
 
 // Queries: a warp takes up to 4 * (32 / units) heads of a token at a time.
 constexpr int kBatch = 4;
-template <typename T, bool WHOLE>
-__device__ __forceinline__ void turn_queries(const Ap8Params &a) {
+template <typename T, int KIND>
+__device__ __forceinline__ void turn_queries(const Ap8Params &a, int cta) {
   const fp4_append_params &p = a.p;
   const fp4_kv_cache &c = p.cache;
   const int lane = threadIdx.x & 31;
   const int rows = 32 / a.units, my_row = lane / a.units, my_unit = lane - my_row * a.units;
   const int64_t limit = p.rot_dim ? p.rope_len : INT64_MAX;
   const int parts = (p.heads + kBatch * rows - 1) / (kBatch * rows);
-  const Unit u = unit_at(p, my_unit);
+  const Unit u = unit_at<KIND>(p, my_unit);
   const int64_t ctas = gridDim.x - a.kv_ctas;
-  for (int64_t item = ((int64_t)blockIdx.x - a.kv_ctas) * kWarps + (threadIdx.x >> 5); item < p.tokens * parts;
+  for (int64_t item = (int64_t)cta * kWarps + (threadIdx.x >> 5); item < p.tokens * parts;
        item += ctas * kWarps) {
     const int64_t t = item / parts;
     const int h0 = (int)(item - t * parts) * kBatch * rows;
@@ -308,7 +405,7 @@ __device__ __forceinline__ void turn_queries(const Ap8Params &a) {
     T *const dst = static_cast<T *>(p.q_out) + t * p.qo_token;
     const int pos = p.pos[t];
     int page, place;
-    if (WHOLE) {
+    if (KIND != kAny) {
       uint4 v[kBatch], w[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
@@ -318,9 +415,9 @@ __device__ __forceinline__ void turn_queries(const Ap8Params &a) {
         v[i] = *reinterpret_cast<const uint4 *>(src + h * p.q_head + u.o1);
         w[i] = *reinterpret_cast<const uint4 *>(src + h * p.q_head + u.o2);
       }
-      const bool keep = locate8(c, p.seq ? p.seq[t] : t, pos, limit, nullptr, page, place);
+      const bool keep = locate8(c, a.page, p.seq ? p.seq[t] : t, pos, limit, nullptr, page, place);
       Turn turn;
-      if (keep) load_turn(p, u, pos, turn);
+      load_turn<KIND>(p, u, keep, pos, turn);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int h = h0 + i * rows + my_row;
@@ -332,13 +429,13 @@ __device__ __forceinline__ void turn_queries(const Ap8Params &a) {
           continue;
         }
         float x[16];
-        turn_unit<T>(u, v[i], w[i], turn, x);
+        turn_unit<T, KIND>(true, u, v[i], w[i], turn, x);
         *at1 = make_uint4(Two<T>::put(x[0], x[1]), Two<T>::put(x[2], x[3]), Two<T>::put(x[4], x[5]), Two<T>::put(x[6], x[7]));
         *at2 = make_uint4(Two<T>::put(x[8], x[9]), Two<T>::put(x[10], x[11]), Two<T>::put(x[12], x[13]),
                           Two<T>::put(x[14], x[15]));
       }
     } else {  // by pairs, then single elements
-      const bool keep = locate8(c, p.seq ? p.seq[t] : t, pos, limit, nullptr, page, place);
+      const bool keep = locate8(c, a.page, p.seq ? p.seq[t] : t, pos, limit, nullptr, page, place);
       const int half = p.rot_dim / 2, per = c.head_dim - half, heads = min(kBatch * rows, p.heads - h0);
       const float *cs = p.rope + (int64_t)(keep ? pos : 0) * p.rot_dim;
       for (int i = lane; i < heads * per; i += 32) {
@@ -358,14 +455,16 @@ __device__ __forceinline__ void turn_queries(const Ap8Params &a) {
   }
 }
 
-template <typename T, bool WHOLE>
-__global__ void __launch_bounds__(kThreads) k_append8(const __grid_constant__ Ap8Params a) {
+template <typename T, int KIND>
+__global__ void __launch_bounds__(kThreads, kResident) k_append8(const __grid_constant__ Ap8Params a) {
   dependent_wait();
   launch_dependents();
-  if (blockIdx.x < a.kv_ctas)
-    store_blocks<T, WHOLE>(a);
+  // CTAs for keys and values, and for queries, in turn
+  const int before = (int)((int64_t)blockIdx.x * a.kv_ctas / gridDim.x);
+  if (before != (int)(((int64_t)blockIdx.x + 1) * a.kv_ctas / gridDim.x))
+    store_blocks<T, KIND>(a, before);
   else
-    turn_queries<T, WHOLE>(a);
+    turn_queries<T, KIND>(a, blockIdx.x - before);
 }
 
 bool whole8(const void *ptr, int64_t s0, int64_t s1) { return aligned16(ptr) && s0 % 8 == 0 && s1 % 8 == 0; }
@@ -378,14 +477,27 @@ fp4_status launch_append(Ap8Params &a, cudaStream_t s) {
                      (!p.q || (whole8(p.q, p.q_token, p.q_head) && whole8(p.q_out, p.qo_token, p.qo_head)));
   a.units = p.cache.head_dim / 16;
   const int heads = 2 * p.cache.kv_heads, rows = 32 / a.units;
-  const int64_t most = 8 * (int64_t)sm_count();  // CTAs resident at once, about
+  const int64_t most = kResident * (int64_t)sm_count(), grid_most = 1 << 20;
+  // as many warps as hold a block's rows, if runs may be as long; as many tokens
+  // as these have groups of lanes, or more; the heads in as few parts as leave one
+  // for every warp, of windows in which a run begins
+  const int64_t run = !p.seq ? 1 : p.tokens < a.s.block ? p.tokens : a.s.block, warps = most * kWarps;
+  a.team = 1;
+  while (a.team < kWarps && a.team * rows * kHold < run) a.team *= 2;
   a.window = 1;
-  while (a.window < 32 && ceil_div(p.tokens, a.window) * heads > most * kWarps) a.window *= 2;
-  const int64_t kv = ceil_div(ceil_div(p.tokens, a.window) * heads, kWarps);
-  a.kv_ctas = (int)(kv < most ? kv : most);
+  while (a.window < 32 && ((2 * a.window <= rows * a.team && 2 * a.window <= p.tokens) ||
+                           ceil_div(p.tokens, a.window) * heads * a.team > warps))
+    a.window *= 2;
+  const int64_t full = ceil_div(p.tokens, a.window > run ? a.window : run);
+  a.chunks = heads;
+  while (a.chunks > 1 && full * (a.chunks / 2) * a.team >= warps) a.chunks = (a.chunks + 1) / 2;
+  a.page = divisor(p.cache.page_size);
+  a.block = divisor(a.s.block);
+  const int64_t kv = ceil_div(ceil_div(p.tokens, a.window) * a.chunks * a.team, kWarps);
+  a.kv_ctas = (int)(kv < grid_most ? kv : grid_most);
   const int64_t qn = p.q ? ceil_div(p.tokens * ceil_div(p.heads, kBatch * rows), kWarps) : 0;
-  const unsigned grid = (unsigned)(a.kv_ctas + (qn < most ? qn : most));
-  const auto kern = whole ? k_append8<T, true> : k_append8<T, false>;
+  const unsigned grid = (unsigned)(a.kv_ctas + (qn < grid_most ? qn : grid_most));
+  const auto kern = !whole ? k_append8<T, kAny> : p.interleaved ? k_append8<T, kPairs> : k_append8<T, kHalves>;
   return launch_dependent(kern, dim3(grid), dim3(kThreads), 0, s, a) == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
 
@@ -393,63 +505,75 @@ fp4_status launch_append(Ap8Params &a, cudaStream_t s) {
 
 struct RdParams {
   fp4_read_params p;
-  int pieces;    // 16-byte pieces of a stored head
-  int tokens;    // tokens of a CTA at a time
+  Divisor page, block, piece;  // piece: by the pieces of a head
+  int pieces;                  // of 16 stored bytes, of a head
+  int per;                     // of a token, its keys and values
+  int tokens;                  // of a CTA at a time
   uint32_t *status;
 };
+constexpr int readers(bool codes) { return codes ? 6 : 8; }  // CTAs an SM holds
 
 // A thread takes a piece of 16 stored bytes: codes become 16 elements, 16-bit
-// elements are copied.  Neighbours take neighbouring pieces of a token's heads.
+// elements are copied.  Neighbours take neighbouring pieces of a token's heads; a
+// CTA's next tokens are looked up before this one's pieces are waited for.
 template <typename T, bool CODES>
-__global__ void __launch_bounds__(kThreads) k_read(const __grid_constant__ RdParams a) {
+__global__ void __launch_bounds__(kThreads, readers(CODES)) k_read(const __grid_constant__ RdParams a) {
   const fp4_read_params &p = a.p;
   const fp4_kv_cache &c = p.cache;
   constexpr int kEach = CODES ? 16 : 8;
   dependent_wait();
   launch_dependents();
-  const int per = 2 * c.kv_heads * a.pieces;  // of a token: its keys, its values
   const int width = kThreads / a.tokens, tl = threadIdx.x / width, in = threadIdx.x - tl * width;
   if (tl >= a.tokens) return;
-  for (int64_t t = (int64_t)blockIdx.x * a.tokens + tl; t < p.tokens; t += (int64_t)gridDim.x * a.tokens) {
-    int page, place;
-    const bool keep = locate8(c, p.seq ? p.seq[t] : t, p.pos[t], INT64_MAX, in == 0 ? a.status : nullptr, page, place);
-    for (int i = in; i < per; i += width) {
-      const int row = i / a.pieces, d = (i - row * a.pieces) * kEach;
+  const int hop = gridDim.x * a.tokens, tokens = (int)p.tokens;  // (below 2^30)
+  int page = 0, place = 0;
+  auto look = [&](int t) {
+    return t < tokens && locate8(c, a.page, p.seq ? p.seq[t] : t, p.pos[t], INT64_MAX, in == 0 ? a.status : nullptr, page, place);
+  };
+  int t = blockIdx.x * a.tokens + tl;
+  bool keep = look(t);
+  for (; t < tokens; t += hop) {
+    const bool here = keep;
+    const int my_page = page, my_place = place;
+    for (int i = in; i < a.per; i += width) {
+      const int row = over(i, a.piece), d = (i - row * a.pieces) * kEach;
       const bool key = row < c.kv_heads;
       const int head = key ? row : row - c.kv_heads;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      int code = 127;
+      if (here) {
+        const int64_t at = my_page * (key ? c.k_page : c.v_page) + my_place * (key ? c.k_place : c.v_place) +
+                           head * (key ? c.k_head : c.v_head) + d;
+        v = *reinterpret_cast<const uint4 *>(static_cast<const char *>(key ? c.k : c.v) + at * (CODES ? 1 : 2));
+        if (CODES) {
+          const fp4_kv_scales &f = p.scales;
+          code = (key ? f.k_sf : f.v_sf)[my_page * (key ? f.k_page : f.v_page) +
+                                         over(my_place, a.block) * (key ? f.k_block : f.v_block) +
+                                         head * (key ? f.k_head : f.v_head)];
+        }
+      }
+      if (i == in) keep = look(t + hop);
       T *out = key ? static_cast<T *>(p.k_out) + t * p.k_token + head * p.k_out_head + d
                    : static_cast<T *>(p.v_out) + t * p.v_token + head * p.v_out_head + d;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (keep) {
-        const int64_t at = key ? (int64_t)page * c.k_page + place * c.k_place + head * c.k_head + d
-                               : (int64_t)page * c.v_page + place * c.v_place + head * c.v_head + d;
-        v = *reinterpret_cast<const uint4 *>(static_cast<const char *>(key ? c.k : c.v) + at * (CODES ? 1 : 2));
-      }
       if (!CODES) {
         *reinterpret_cast<uint4 *>(out) = v;
         continue;
       }
-      float f = 0.0f;
-      if (keep) {
-        const int b = place / p.scales.block;
-        const int code = key ? p.scales.k_sf[(int64_t)page * p.scales.k_page + b * p.scales.k_block + head * p.scales.k_head]
-                             : p.scales.v_sf[(int64_t)page * p.scales.v_page + b * p.scales.v_block + head * p.scales.v_head];
-        f = code == 255 ? NAN : e8m0_value(code);
-      }
+      const float f = code == 255 ? NAN : e8m0_value(code);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t r[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t lo, hi;
-        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-            : "=r"(lo), "=r"(hi)
-            : "r"(w[j]));
-        const float2 x = Two<__half>::get(lo), y = Two<__half>::get(hi);
-        r[2 * j] = Two<T>::put(x.x * f, x.y * f);
-        r[2 * j + 1] = Two<T>::put(y.x * f, y.y * f);
+      for (int j = 0; j < 2; ++j) {
+        uint32_t r[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t lo, hi;
+          halves(w[2 * j + e], lo, hi);
+          const float2 x = Two<__half>::get(lo), y = Two<__half>::get(hi);
+          r[2 * e] = Two<T>::put(x.x * f, x.y * f);
+          r[2 * e + 1] = Two<T>::put(y.x * f, y.y * f);
+        }
+        reinterpret_cast<uint4 *>(out)[j] = make_uint4(r[0], r[1], r[2], r[3]);
       }
-      reinterpret_cast<uint4 *>(out)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-      reinterpret_cast<uint4 *>(out)[1] = make_uint4(r[4], r[5], r[6], r[7]);
     }
   }
 }
@@ -459,10 +583,14 @@ fp4_status launch_read(RdParams &a, cudaStream_t s) {
   const fp4_read_params &p = a.p;
   const bool codes = p.scales.k_sf != nullptr;
   a.pieces = p.cache.head_dim / (codes ? 16 : 8);
-  const int per = 2 * p.cache.kv_heads * a.pieces;
+  if (2 * (int64_t)p.cache.kv_heads * a.pieces > INT32_MAX) return FP4_ERR_SHAPE;
+  a.per = 2 * p.cache.kv_heads * a.pieces;
   a.tokens = 1;
-  while (a.tokens < 32 && kThreads / (2 * a.tokens) >= per) a.tokens *= 2;
-  const int64_t most = 8 * (int64_t)sm_count(), want = ceil_div(p.tokens, a.tokens);
+  while (a.tokens < 32 && kThreads / (2 * a.tokens) >= a.per) a.tokens *= 2;
+  a.page = divisor(p.cache.page_size);
+  a.block = divisor(codes ? p.scales.block : 1);
+  a.piece = divisor(a.pieces);
+  const int64_t most = readers(codes) * (int64_t)sm_count(), want = ceil_div(p.tokens, a.tokens);
   const auto kern = codes ? k_read<T, true> : k_read<T, false>;
   return launch_dependent(kern, dim3((unsigned)(want < most ? want : most)), dim3(kThreads), 0, s, a) == cudaSuccess
              ? FP4_OK

@@ -1,16 +1,20 @@
 // plan.cu -- pages and places for new tokens, from what sequences hold and are
 // to get (sm_103a): block tables, slot maps, and the pool of free pages.
 //
-// Bound: latency (a launch, two dependent loads, two scans over the sequences,
-// a look-up), and for prompts the 16 bytes written a token.
+// Bound: latency (a launch, two dependent loads, scans over the sequences, a
+// look-up), and for prompts the 16 bytes written a token.
 //
 // Layout.  Every CTA scans all sequences, a run of them a thread: the new
-// tokens' offsets, then the pages that each gets.  It then writes its share of
-// the granted table entries and of the token maps, finding sequences by
-// bisection in the threads' sums and a walk within a thread's run.  Page numbers
-// of new entries come from the stack, not from the table, so no CTA waits for
-// another; the last one to finish (counted in the pool's second word) writes the
-// state that the others read: lengths, rooms, the stack and what goes back.
+// tokens' offsets, the pages that each gets, those that each gives back.  It then
+// writes its share of the table entries, the token maps and the pages that go
+// back, finding sequences by bisection in the threads' sums and a walk within a
+// thread's run (up to 512 sequences: none, and what is known of them is in shared
+// memory).  Page numbers of new entries come from the stack, not from the table,
+// so no CTA waits for another; the last one to finish (counted in the pool's
+// second word) writes the state that the others read: lengths, rooms, how many
+// are free, and, where the call also gives out pages from those places of the
+// stack, what goes back.
+// Measured in a graph: see the table of the serving operators' measurements.
 #include "serve.cuh"
 
 namespace fp4 {
@@ -22,26 +26,31 @@ constexpr int kTokens = 4;  // consecutive tokens of a thread
 
 struct PlanParams {
   fp4_plan_params p;
+  Divisor page;
+  int limit;  // positions that a row of the table can name
+  bool wide;  // maps allow stores of whole groups of tokens
   uint32_t *status;
 };
 
-// What becomes of sequence s whose new tokens begin at `first` in the maps.
+// What becomes of a sequence whose new tokens begin at `first` in the maps.
 struct Change {
-  int64_t length, after;
-  int n, held, want;
+  int n, length, held, want;
+  int64_t after;
   bool fits;
-  __device__ __forceinline__ int64_t grows() const { return fits && n >= 0 && want > held ? want - held : 0; }
-  __device__ __forceinline__ int64_t gives() const { return n < 0 && held > want ? held - want : 0; }
+  __device__ __forceinline__ int grows() const { return fits && n >= 0 && want > held ? want - held : 0; }
+  __device__ __forceinline__ int gives() const { return n < 0 && held > want ? held - want : 0; }
+  __device__ __forceinline__ int adds() const { return max(n, 0); }
+  // with `upto` pages granted up to and with it, of `free`
+  __device__ __forceinline__ bool granted(int64_t upto, int64_t free) const {
+    return n < 0 || (fits && (grows() == 0 || upto <= free));
+  }
 };
-__device__ __forceinline__ Change change_of(const fp4_plan_params &p, int s, int64_t first) {
+__device__ __forceinline__ Change change_of(const PlanParams &a, int n, int length, int held, int64_t first) {
   Change c;
-  c.n = p.new_tokens[s];
-  c.length = max(p.lengths[s], 0);
-  c.held = min(max(p.room[s], 0) / p.page_size, p.seq_pages);
-  c.after = max(c.length + c.n, (int64_t)0);
-  const int64_t want = (c.after + p.page_size - 1) / p.page_size;
-  c.fits = want <= p.seq_pages && (p.tokens < 0 || first + max(c.n, 0) <= p.tokens);
-  c.want = (int)min(want, (int64_t)p.seq_pages);
+  c.n = n, c.length = length, c.held = held;
+  c.after = max((int64_t)length + n, (int64_t)0);
+  c.fits = c.after <= a.limit && (a.p.tokens < 0 || first + max(n, 0) <= a.p.tokens);
+  c.want = c.after > a.limit ? a.p.seq_pages : c.after > 0 ? over((int)c.after - 1, a.page) + 1 : 0;
   return c;
 }
 
@@ -57,8 +66,13 @@ __device__ __forceinline__ int64_t scan(int64_t v, int64_t *sums, int64_t *warps
   }
   if (lane == 31) warps[warp] = inc;
   __syncthreads();
-  int64_t before = inc - v;
-  for (int w = 0; w < warp; ++w) before += warps[w];
+  int64_t w = lane < kW ? warps[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < kW; o <<= 1) {
+    const int64_t x = __shfl_up_sync(~0u, w, o);
+    if (lane >= o) w += x;
+  }
+  const int64_t before = inc - v + (warp ? __shfl_sync(~0u, w, warp - 1) : 0);
   sums[threadIdx.x] = before;
   if (threadIdx.x == kThreads - 1) sums[kThreads] = before + v;
   __syncthreads();
@@ -77,83 +91,149 @@ __device__ __forceinline__ int thread_of(const int64_t *sums, int64_t x) {
 
 __global__ void __launch_bounds__(kThreads) k_plan(const __grid_constant__ PlanParams a) {
   __shared__ int64_t add_sh[kThreads + 1], grow_sh[kThreads + 1], give_sh[kThreads + 1], warps[kW];
-  __shared__ int last_sh;
+  __shared__ int n_sh[kThreads], length_sh[kThreads], held_sh[kThreads], last_sh, taken_sh;
   const fp4_plan_params &p = a.p;
   const int per = (p.seqs + kThreads - 1) / kThreads;
   const int s0 = min((int)threadIdx.x * per, p.seqs), s1 = min(s0 + per, p.seqs);
   dependent_wait();
   launch_dependents();
   const int64_t free = min((int64_t)max(p.pool[0], 0), p.pool_pages);
+  auto load = [&](int s, int64_t first) {
+    return change_of(a, p.new_tokens[s], max(p.lengths[s], 0), min(over(max(p.room[s], 0), a.page), p.seq_pages), first);
+  };
   int64_t add = 0;
-  for (int s = s0; s < s1; ++s) add += max(p.new_tokens[s], 0);
-  const int64_t add0 = scan(add, add_sh, warps);
-  int64_t grow = 0, at = add0;
+  bool back_too = false;
   for (int s = s0; s < s1; ++s) {
-    const Change c = change_of(p, s, at);
+    const Change c = load(s, 0);
+    if (s == s0) n_sh[threadIdx.x] = c.n, length_sh[threadIdx.x] = c.length, held_sh[threadIdx.x] = c.held;
+    add += c.adds();
+    back_too |= c.n < 0;
+  }
+  if (threadIdx.x == 0) taken_sh = 0;
+  // sequence s, the first of thread th's run if there is one a thread
+  auto change = [&](int s, int64_t first) {
+    return per == 1 ? change_of(a, n_sh[s], length_sh[s], held_sh[s], first) : load(s, first);
+  };
+  const int64_t add0 = scan(add, add_sh, warps);
+  int64_t grow = 0, give = 0, at = add0;
+  for (int s = s0; s < s1; ++s) {
+    const Change c = change(s, at);
     grow += c.grows();
-    at += max(c.n, 0);
+    give += c.gives();
+    at += c.adds();
   }
   const int64_t grow0 = scan(grow, grow_sh, warps);
-  // sequence s with `upto` pages granted up to and with it: whether it gets them
-  auto granted = [&](const Change &c, int64_t upto) { return c.n < 0 || (c.fits && (c.grows() == 0 || upto <= free)); };
+  back_too = __syncthreads_or(back_too);
+  const int64_t give0 = back_too ? scan(give, give_sh, warps) : 0;
+  const int64_t step = (int64_t)gridDim.x * kThreads, me = (int64_t)blockIdx.x * kThreads + threadIdx.x;
 
   // table entries: page j of those to be granted
   const int64_t pages = min(grow_sh[kThreads], free);
-  const int64_t step = (int64_t)gridDim.x * kThreads, me = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   for (int64_t j = me; j < pages; j += step) {
     const int th = thread_of(grow_sh, j);
     int64_t g = grow_sh[th], t = add_sh[th];
     for (int s = th * per;; ++s) {
-      const Change c = change_of(p, s, t);
+      const Change c = change(s, t);
       if (j < g + c.grows()) {
         if (g + c.grows() <= free) p.table[s * p.table_stride + c.held + (j - g)] = p.pool[2 + free - 1 - j];
         break;
       }
       g += c.grows();
-      t += max(c.n, 0);
+      t += c.adds();
     }
   }
 
   // token maps
   const int64_t total = add_sh[kThreads];
   for (int64_t t0 = me * kTokens; t0 < p.tokens; t0 += step * kTokens) {
-    int s = -1;
+    int s = -1, known = -1, page = 0;
     int64_t begin = 0, end = 0, g = 0;  // the tokens of sequence s; pages granted before it
     Change c{};
     bool ok = false;
-    for (int64_t t = t0; t < min(t0 + kTokens, p.tokens); ++t) {
-      int seq = -1, pos = -1;
-      int64_t slot = -1;
-      if (t < total) {
+    int seq[kTokens], pos[kTokens];
+    int64_t slot[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      const int64_t t = t0 + i;
+      seq[i] = pos[i] = -1;
+      slot[i] = -1;
+      if (t >= total) continue;
+      if (s < 0 || t >= end) {
         if (s < 0) {
           const int th = thread_of(add_sh, t);
           s = th * per;
           begin = add_sh[th];
           g = grow_sh[th];
-          c = change_of(p, s, begin);
-          end = begin + max(c.n, 0);
-          ok = granted(c, g + c.grows());
-        }
-        while (t >= end) {
+        } else {
           g += c.grows();
           begin = end;
-          c = change_of(p, ++s, begin);
-          end = begin + max(c.n, 0);
-          ok = granted(c, g + c.grows());
+          ++s;
         }
-        seq = s;
-        if (ok) {
-          pos = (int)(c.length + (t - begin));
-          const int e = pos / p.page_size;
-          const int page = e < c.held ? p.table[s * p.table_stride + e] : p.pool[2 + free - 1 - (g + e - c.held)];
-          slot = (int64_t)page * p.page_size + (pos - e * p.page_size);
+        c = change(s, begin);
+        while (t >= (end = begin + c.adds())) {
+          g += c.grows();
+          begin = end;
+          c = change(++s, begin);
         }
+        ok = c.granted(g + c.grows(), free);
+        known = -1;
       }
-      if (p.seq) p.seq[t] = seq;
-      if (p.pos) p.pos[t] = pos;
-      if (p.slot) p.slot[t] = slot;
+      seq[i] = s;
+      if (!ok) continue;
+      pos[i] = c.length + (int)(t - begin);
+      const int e = over(pos[i], a.page);
+      if (e != known) page = e < c.held ? p.table[s * p.table_stride + e] : p.pool[2 + free - 1 - (g + e - c.held)];
+      known = e;
+      slot[i] = (int64_t)page * p.page_size + (pos[i] - e * p.page_size);
+    }
+    if (a.wide && t0 + kTokens <= p.tokens) {
+      *reinterpret_cast<int4 *>(p.seq + t0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+      *reinterpret_cast<int4 *>(p.pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      *reinterpret_cast<longlong2 *>(p.slot + t0) = make_longlong2(slot[0], slot[1]);
+      *reinterpret_cast<longlong2 *>(p.slot + t0 + 2) = make_longlong2(slot[2], slot[3]);
+      continue;
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      if (t0 + i >= p.tokens) break;
+      if (p.seq) p.seq[t0 + i] = seq[i];
+      if (p.pos) p.pos[t0 + i] = pos[i];
+      if (p.slot) p.slot[t0 + i] = slot[i];
     }
   }
+
+  // how many pages are given out: those up to the last sequence that gets any
+  at = add0;
+  int64_t g = grow0, taken = 0;
+  for (int s = s0; s < s1; ++s) {
+    const Change c = change(s, at);
+    g += c.grows();
+    if (c.grows() && c.granted(g, free)) taken = g;
+    at += c.adds();
+  }
+  if (taken) atomicMax(&taken_sh, (int)taken);
+  __syncthreads();
+  taken = taken_sh;
+  const int64_t left = free - taken, back = back_too ? give_sh[kThreads] : 0;
+  const int64_t fit = min(back, p.pool_pages - left);  // (more than the pool's pages: what is left over is lost)
+  // pages that go back, as if the last had gone first
+  auto give_back = [&](int64_t from, int64_t stride) {
+    for (int64_t j = from; j < back; j += stride) {
+      const int th = thread_of(give_sh, j);
+      int64_t f = give_sh[th];
+      for (int s = th * per;; ++s) {
+        const Change c = change(s, 0);
+        if (j < f + c.gives()) {
+          int32_t *entry = p.table + s * p.table_stride + c.want + (j - f);
+          if (back - 1 - j < fit) p.pool[2 + left + (back - 1 - j)] = *entry;
+          *entry = -1;
+          break;
+        }
+        f += c.gives();
+      }
+    }
+  };
+  if (taken == 0) give_back(me, step);  // onto places of the stack that nobody reads
 
   // the last CTA writes the state
   if (gridDim.x > 1) {
@@ -166,52 +246,23 @@ __global__ void __launch_bounds__(kThreads) k_plan(const __grid_constant__ PlanP
   } else {
     __syncthreads();
   }
-  int64_t give = 0, taken = 0;
-  at = add0;
-  int64_t g = grow0;
-  for (int s = s0; s < s1; ++s) {
-    const Change c = change_of(p, s, at);
-    g += c.grows();
-    if (granted(c, g)) taken = c.grows() ? g : taken;  // the last one granted: pages up to it
-    else raise_status(a.status, kStatusIndex);
-    give += c.gives();
-    at += max(c.n, 0);
+  if (taken != 0) {
+    give_back(threadIdx.x, kThreads);
+    if (per > 1) __syncthreads();  // lengths and rooms are read there
   }
-  const int64_t give0 = scan(give, give_sh, warps);
-  // pages granted: those of the last sequence that got any
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) taken = max(taken, __shfl_xor_sync(~0u, taken, o));
-  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = taken;
-  __syncthreads();
-  for (int w = 0; w < kW; ++w) taken = max(taken, warps[w]);
-  const int64_t left = free - taken, back = give_sh[kThreads];
-  const int64_t fit = min(back, p.pool_pages - left);  // (more than the pool's pages: what is left over is lost)
-  for (int64_t j = threadIdx.x; j < back; j += kThreads) {
-    const int th = thread_of(give_sh, j);
-    int64_t f = give_sh[th];
-    for (int s = th * per;; ++s) {
-      const Change c = change_of(p, s, 0);
-      if (j < f + c.gives()) {
-        int32_t *entry = p.table + s * p.table_stride + c.want + (j - f);
-        if (back - 1 - j < fit) p.pool[2 + left + (back - 1 - j)] = *entry;
-        *entry = -1;
-        break;
-      }
-      f += c.gives();
-    }
-  }
-  __syncthreads();  // lengths and rooms are read above
   at = add0;
   g = grow0;
   for (int s = s0; s < s1; ++s) {
-    const Change c = change_of(p, s, at);
+    const Change c = change(s, at);
     g += c.grows();
-    const bool ok = granted(c, g);
     if (p.offsets) p.offsets[s] = (int32_t)min(at, (int64_t)INT32_MAX);
-    at += max(c.n, 0);
-    if (!ok) continue;
+    at += c.adds();
+    if (!c.granted(g, free)) {
+      raise_status(a.status, kStatusIndex);
+      continue;
+    }
     p.lengths[s] = (int32_t)c.after;
-    p.room[s] = (int32_t)((c.n < 0 ? min(c.held, c.want) : c.held + c.grows()) * p.page_size);
+    p.room[s] = (c.n < 0 ? min(c.held, c.want) : c.held + c.grows()) * p.page_size;
   }
   if (threadIdx.x == 0) {
     if (p.offsets) p.offsets[p.seqs] = (int32_t)min(add_sh[kThreads], (int64_t)INT32_MAX);
@@ -226,9 +277,15 @@ __global__ void __launch_bounds__(kThreads) k_plan(const __grid_constant__ PlanP
 fp4_status launch_page_plan(const fp4_plan_params &p, cudaStream_t s) {
   PlanParams a{};
   a.p = p;
+  a.page = divisor(p.page_size);
+  a.limit = p.seq_pages * p.page_size;
+  a.wide = p.seq && p.pos && p.slot && aligned16(p.seq) && aligned16(p.pos) && aligned16(p.slot);
   a.status = status_word();
   if (!a.status) return FP4_ERR_CUDA;
-  const int64_t want = ceil_div(p.tokens > 0 ? p.tokens : 1, kThreads * kTokens), most = sm_count();
+  // CTAs for the tokens, or for pages that may go back
+  const int64_t tokens = ceil_div(p.tokens > 0 ? p.tokens : 1, kThreads * kTokens);
+  const int64_t pages = ceil_div(p.pool_pages, 4 * kThreads);
+  const int64_t want = p.tokens >= 0 ? tokens : pages < 16 ? (pages > 1 ? pages : 1) : 16, most = sm_count();
   return launch_dependent(k_plan, dim3((unsigned)(want < most ? want : most)), dim3(kThreads), 0, s, a) == cudaSuccess
              ? FP4_OK
              : FP4_ERR_CUDA;

@@ -29,6 +29,23 @@ __device__ __forceinline__ float from_f32<float>(float v) {
   return v;
 }
 
+// i / d for 0 <= i < 2^31 by a multiplication: with 2^(l - 1) < d <= 2^l and m =
+// ceil(2^(31 + l) / d), which is below 2^32 for d > 1, m d exceeds 2^(31 + l)
+// by less than d <= 2^l, so i m / 2^(31 + l) exceeds i / d by less than 1 / d.
+struct Divisor {
+  uint32_t m;
+  int shift;  // l - 1; -1: d = 1
+};
+inline Divisor divisor(int d) {
+  int l = 0;
+  while (((int64_t)1 << l) < d) ++l;
+  if (l == 0) return {0, -1};
+  return {(uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d), l - 1};
+}
+__device__ __forceinline__ int over(int i, const Divisor &d) {
+  return d.shift < 0 ? i : (int)(__umulhi((uint32_t)i, d.m) >> d.shift);
+}
+
 // log2 of a power of two, else `other`.
 inline int log2_or(int v, int other) {
   if (v < 1 || (v & (v - 1)) != 0) return other;
