@@ -588,6 +588,7 @@ fp4_status launch(AtParams a, cudaStream_t s) {
   if (rows > INT32_MAX) return FP4_ERR_SHAPE;
   const int64_t reach = (int64_t)a.p.window + 15 + ceil_div(a.p.sinks, a.tile) * a.tile;
   a.direct = cluster_of(rows, a.p.window && reach < room ? reach : room, DP, NT);
+  if (!a.direct && !a.ws) return FP4_ERR_INVALID_ARG;  // (where rows of `room` have CTAs of their own, shorter ones do)
   a.ctas = (int)(a.direct ? rows * a.direct : tiles < most ? tiles : most);
   // Rows of their own may start early.  Equal slices may not: their CTAs would be
   // placed around those that still run, two on one SM and none on another

@@ -696,8 +696,13 @@ fp4_status launch(At8Params b, cudaStream_t s) {
   const int64_t room = (int64_t)c.seq_pages * c.page_size;
   const int64_t most = (int64_t)sm_count() * (per < kPerSM8 ? per : kPerSM8);
   if (rows > INT32_MAX) return FP4_ERR_SHAPE;
+  // by what a window and the first positions reach, but by slices only where the
+  // workspace, which knows the table's room alone, has been asked for
   const int64_t reach = (int64_t)a.p.window + 15 + ceil_div(a.p.sinks, a.tile) * a.tile;
-  a.direct = cluster_of(rows, a.p.window && reach < room ? reach : room, DP, NT);
+  const int by_room = cluster_of(rows, room, DP, NT);
+  a.direct = a.p.window && reach < room ? cluster_of(rows, reach, DP, NT) : by_room;
+  if (!a.direct) a.direct = by_room;
+  if (!a.direct && !a.ws) return FP4_ERR_INVALID_ARG;
   const int each = c.kv_heads * a.groups;
   a.bundle = a.direct ? 1 : each % kWarps == 0 ? kWarps : each % 2 == 0 ? 2 : 1;
   a.least = 4;

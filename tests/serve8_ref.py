@@ -157,7 +157,7 @@ class Pages:
                     self.table[s][held + e] = self.free[len(self.free) - 1 - (pages - grow + e)]
                     given.append(self.table[s][held + e])
                 self.lengths[s], self.room[s] = after, (held + grow) * P
-            for j in range(n):
+            for j in range(n if tokens is not None else 0):
                 seq.append(s)
                 pos.append(L + j if ok else -1)
                 slot.append(self.table[s][(L + j) // P] * P + (L + j) % P if ok else -1)
