@@ -11,6 +11,12 @@
 // values, 2 and 2 of queries), launch and dependent loads (position, page,
 // scale) for a few tokens.
 //
+// Measured in a graph: 192 tokens of 192 sequences, 16 + 2 x 16 heads of 64 in
+// blocks of 8 4.1 us, one token 3.7; 8191 prompt tokens of 32 + 2 x 8 heads of 128
+// in blocks of 64 57 us (3.2 TB/s, 48% of a copy's rate; without queries 33: some
+// 900 instructions of a warp a head and 64 tokens, 16 warps an SM); reading 100003
+// tokens back 119 us (5.1 TB/s, 76%), 300 2.3 us.
+//
 // Layout.  Lanes hold units of 16 elements (two pieces of 8, in the rotated part
 // those whose elements form pairs) of 32 / units rows; a team of warps takes the
 // tokens of one block and one key or value head.  Teams look for blocks in windows
@@ -183,9 +189,10 @@ __device__ __forceinline__ void turn_any(const fp4_append_params &p, const T *sr
 // into runs, each of one block, at consecutive places; a run may go on behind the
 // window.  Either the team takes one run after the other, its groups of lanes a
 // token each, or each group takes a run of its own.  A group holds kHold rows at a
-// time; of longer runs all but the last are loaded again for their codes.
-constexpr int kHold = 1;
-template <typename T, int KIND>
+// time (more than one costs registers: 192 tokens of 192 sequences take 5.4 us with
+// two, 4.0 with one); of longer runs all but the last are loaded again for their
+// codes.
+template <typename T, int KIND, int kHold>
 __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
   const fp4_append_params &p = a.p;
   const fp4_kv_cache &c = p.cache;
@@ -256,11 +263,11 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
       if (apart) steps = __reduce_max_sync(~0u, active ? steps : 1);
       // kHold rows from r on; behind the last row, and for lanes without one, a row
       // that is there again, which changes no largest.  Runs of one step: the next
-      // head's are requested before this one's are done with, and the heads share
-      // their cosines and sines.
+      // head's are requested before this one's are done with (two or four heads
+      // ahead measured the same), and the heads share their cosines and sines.
       uint4 v[kHold], w[kHold];
       Turn turn[kHold];
-      auto ask = [&](int hv, int r, bool turns) {
+      auto ask = [&](int hv, int r) {
         const bool key = hv < Hk;
         const int head = key ? hv : hv - Hk;
         const T *const src = key ? static_cast<const T *>(p.k) + t * p.k_token + head * p.k_head
@@ -272,11 +279,18 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
           const int q = max(min(r + h * hop, rows - 1), 0);
           v[h] = *reinterpret_cast<const uint4 *>(src + q * step + unit.o1);
           w[h] = *reinterpret_cast<const uint4 *>(src + q * step + unit.o2);
-          if (turns) load_turn<KIND>(p, unit, key, pos0 + q, turn[h]);
         }
       };
+      auto ask_turns = [&](bool key, int r) {
+#pragma unroll
+        for (int h = 0; h < kHold; ++h)
+          if (KIND != kAny) load_turn<KIND>(p, unit, key, pos0 + max(min(r + h * hop, rows - 1), 0), turn[h]);
+      };
       const bool single = steps == 1;
-      if (single) ask(hv0, r0, true);
+      if (single) {
+        ask(hv0, r0);
+        ask_turns(hv0 < Hk, r0);
+      }
       for (int hv = hv0; hv < hv1; ++hv) {
         const bool key = hv < Hk;
         const int head = key ? hv : hv - Hk;
@@ -328,7 +342,10 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
           float more = 0.0f;
           top = 0.0f;
           for (int i = 0; i < steps; ++i) {
-            if (!single) ask(hv, r0 + i * kHold * hop, true);
+            if (!single) {
+              ask(hv, r0 + i * kHold * hop);
+              ask_turns(key, r0 + i * kHold * hop);
+            }
             take(r0 + i * kHold * hop, infinite);
 #pragma unroll
             for (int h = 0; h < kHold; ++h)
@@ -341,7 +358,7 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
           top = over_team(fmaxf(top, more));
           if (infinite || !(apart ? __any_sync(~0u, isinf(top)) : isinf(top))) break;
         }
-        if (single && hv + 1 < hv1) ask(hv + 1, r0, false);
+        if (single && hv + 1 < hv1) ask(hv + 1, r0);
         const int need = code_for(top), code = begin == 0 || need > old ? need : old;
         const float f = e8m0_inverse(code < 255 ? code : 254);
         for (int i = steps - 1;;) {
@@ -358,7 +375,8 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
             *reinterpret_cast<uint2 *>(to + o2) = make_uint2(z[4] | z[5] << 16, z[6] | z[7] << 16);
           }
           if (i-- == 0) break;
-          ask(hv, r0 + i * kHold * hop, true);
+          ask(hv, r0 + i * kHold * hop);
+          ask_turns(key, r0 + i * kHold * hop);
           take(r0 + i * kHold * hop, infinite);
         }
         if (rows && begin != 0 && code > old) {  // the block's other places, in the new unit
@@ -455,14 +473,14 @@ __device__ __forceinline__ void turn_queries(const Ap8Params &a, int cta) {
   }
 }
 
-template <typename T, int KIND>
+template <typename T, int KIND, int HOLD>
 __global__ void __launch_bounds__(kThreads, kResident) k_append8(const __grid_constant__ Ap8Params a) {
   dependent_wait();
   launch_dependents();
   // CTAs for keys and values, and for queries, in turn
   const int before = (int)((int64_t)blockIdx.x * a.kv_ctas / gridDim.x);
   if (before != (int)(((int64_t)blockIdx.x + 1) * a.kv_ctas / gridDim.x))
-    store_blocks<T, KIND>(a, before);
+    store_blocks<T, KIND, HOLD>(a, before);
   else
     turn_queries<T, KIND>(a, blockIdx.x - before);
 }
@@ -482,8 +500,9 @@ fp4_status launch_append(Ap8Params &a, cudaStream_t s) {
   // as these have groups of lanes, or more; the heads in as few parts as leave one
   // for every warp, of windows in which a run begins
   const int64_t run = !p.seq ? 1 : p.tokens < a.s.block ? p.tokens : a.s.block, warps = most * kWarps;
+  const bool two = run > kWarps * rows;
   a.team = 1;
-  while (a.team < kWarps && a.team * rows * kHold < run) a.team *= 2;
+  while (a.team < kWarps && a.team * rows * (two ? 2 : 1) < run) a.team *= 2;
   a.window = 1;
   while (a.window < 32 && ((2 * a.window <= rows * a.team && 2 * a.window <= p.tokens) ||
                            ceil_div(p.tokens, a.window) * heads * a.team > warps))
@@ -497,7 +516,10 @@ fp4_status launch_append(Ap8Params &a, cudaStream_t s) {
   a.kv_ctas = (int)(kv < grid_most ? kv : grid_most);
   const int64_t qn = p.q ? ceil_div(p.tokens * ceil_div(p.heads, kBatch * rows), kWarps) : 0;
   const unsigned grid = (unsigned)(a.kv_ctas + (qn < grid_most ? qn : grid_most));
-  const auto kern = !whole ? k_append8<T, kAny> : p.interleaved ? k_append8<T, kPairs> : k_append8<T, kHalves>;
+  const auto kern = !whole          ? k_append8<T, kAny, 1>
+                    : p.interleaved ? (two ? k_append8<T, kPairs, 2> : k_append8<T, kPairs, 1>)
+                    : two           ? k_append8<T, kHalves, 2>
+                                    : k_append8<T, kHalves, 1>;
   return launch_dependent(kern, dim3(grid), dim3(kThreads), 0, s, a) == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
 
