@@ -39,8 +39,8 @@
 // BF16: 313 - 324 us (97 - 101% of a copy's rate); one of 131071: 87 us (91%),
 // 3 us of them the join; 96 windows of 1000, 16 heads of 64: 76 - 84 us (62 -
 // 68%: loads a step ahead in registers, which 12 warps an SM do not cover; a
-// quarter of the issue slots is used); one of 300: 6.3 us in a graph (by one CTA
-// 8.5).
+// quarter of the issue slots is used), with 4 first positions before each 80; one
+// of 300: 6.3 us in a graph (by one CTA 8.5).
 #include <cooperative_groups.h>
 
 #include "attention.cuh"

@@ -3,8 +3,9 @@
 // (sm_103a):  out = sum_j w_j 2^ev_j cv_j,  w = softmax_j(scale q . 2^ek_j ck_j).
 //
 // Bound: HBM, 2 D bytes per position and key head, half of what 16 bits move,
-// so twice the positions per time: at 6.8 TB/s an SM has 178 clocks for 16
-// positions of a head of 128, in which they take ~230 instructions of a warp.
+// so twice the positions per time: at 6.8 TB/s an SM has 190 clocks for 16
+// positions of a head of 128, which take ~320 instructions of a warp, 40% of its
+// issue slots.
 //
 // Mathematics.  Codes become f16 exactly (one conversion a pair) and meet the
 // queries, held in f16 times a power of two per head (exact down to 2^-38 of
@@ -21,7 +22,23 @@
 // warp fills for itself, kStages - 1 tiles ahead, across the rows of its slice;
 // scales are requested with the copies and put beside them a step later.
 //
-// Layout, split and joins are those of attention.cu:
+// Split.  Short rows go to clusters, as in attention.cu.  Otherwise the warps of
+// the resident CTAs share the list of all tiles out evenly; warps of a CTA take
+// `bundle` (4, 2 or 1) neighbouring key heads over the same positions.  In a page
+// with heads innermost a head's row of 128 bytes lies between others': copies
+// alone reach 6.1 TB/s of rows that one warp takes by itself, 7.1 where two or
+// more neighbours are in flight together.  What a warp has of a row that others
+// share goes to the workspace, for the join of attention.cuh in a second,
+// dependent launch, in slice order, so results repeat exactly.
+// Measured in a graph, 32 heads over 8 of 128, BF16: 64 sequences of up to 16384
+// positions 180 - 187 us (85 - 88% of a copy's rate; copies alone 190, the work
+// alone on a tile that stays 142); one of 131071 57 us, of 16000 21 (6.5 TB/s
+// between them; some 16 us are launch, search, last tiles and join); one of 300
+// 6.9; 40 windows of 4096 with 20 first positions 67.  Heads of 64 (16, 64
+// sequences of 16384) 430 us for 317 at a copy's rate: as many instructions a
+// position as heads of 128, half the bytes; of 256 334.
+//
+// Layout is that of attention.cu:
 //   S^T = K Q^T   lane (g, t) reads pieces 64 i + 16 t of keys g, g + 8
 //   O^T = V^T P^T lane (g, t) reads pieces 128 i + 16 g (or 8 g) of values
 //                 2 t, 2 t + 1, 2 t + 8, 2 t + 9
@@ -44,10 +61,13 @@ struct At8Params {
   int k_page, k_place, v_page, v_place, ks_page, ks_block, vs_page, vs_block;
 };
 
-constexpr int kStages = 2;
-constexpr int kPerSM8 = 2;  // CTAs an SM holds at most (workspace bound)
+constexpr int kStages = 2;  // 3 - 6: slower, by up to a tenth
+// CTAs an SM holds at most (workspace bound).  3 (160 registers): 177 us for 183
+// with 64 sequences of up to 16384, but 76 for 67 with 40 windows of 4096, 60 for
+// 57 with one of 131071.
+constexpr int kPerSM8 = 2;
 // CTAs an SM holds at least, by the kernel's launch bounds.
-constexpr int per_sm8(int dp, int nt) { return dp <= 128 ? 2 : 1; }
+constexpr int per_sm8(int dp) { return dp <= 128 ? 2 : 1; }
 constexpr float kNone = -3e38f;  // a running maximum before there is a score
 constexpr float kLift = 7.0f;  // weights are held 2^7 times as large (f16's smallest is 2^-24)
 
@@ -134,7 +154,7 @@ constexpr int kQueue = 8;  // rows between the copies and the work: kStages + 1 
 
 // UNITS: pages of whole units of 16 places, strides below 2^31.
 template <typename T, int DP, int NT, bool UNITS>
-__global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const __grid_constant__ At8Params b) {
+__global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __grid_constant__ At8Params b) {
   constexpr int kCols = 8 * NT, kKey = DP / 64, kV16 = DP / 128, kV8 = DP / 64 % 2, kWords = DP / 32;
   constexpr int kUnits = units8(DP), kTile = 16 * kUnits;
   constexpr int kRows = Layout<DP>::kRows, kSteps = Layout<DP>::kSteps;
@@ -660,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP, NT)) k_attention8(const 
 // CTAs (a cluster) that take a row of up to `reach` positions between them, as
 // in attention.cu; 0: equal slices.
 int cluster_of(int64_t rows, int64_t reach, int dp, int nt) {
-  const int64_t sms = sm_count(), fit = sms * per_sm8(dp, nt);
+  const int64_t sms = sm_count(), fit = sms * per_sm8(dp);
   int n = 1;
   while (n < kCluster && rows * 2 * n <= fit * 7 / 8 &&
          (rows * 2 * n <= sms ? n : 2 * n) * kWarps * 16 * units8(dp) < reach)

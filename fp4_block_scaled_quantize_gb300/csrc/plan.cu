@@ -14,7 +14,9 @@
 // second word) writes the state that the others read: lengths, rooms, how many
 // are free, and, where the call also gives out pages from those places of the
 // stack, what goes back.
-// Measured in a graph: see the table of the serving operators' measurements.
+// Measured in a graph, two calls, pages given back and taken again: 256 sequences
+// by a token 12.6 us; 96 prompts of 250000 tokens in all 15.6.  One CTA's scans
+// take some 4 us of each: barriers and dependent loads, 27% of issue slots.
 #include "serve.cuh"
 
 namespace fp4 {
