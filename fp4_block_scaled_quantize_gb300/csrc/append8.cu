@@ -529,73 +529,82 @@ struct RdParams {
   fp4_read_params p;
   Divisor page, block, piece;  // piece: by the pieces of a head
   int pieces;                  // of 16 stored bytes, of a head
-  int per;                     // of a token, its keys and values
+  int parts;                   // CTAs of the same tokens: keys', then values'
   int tokens;                  // of a CTA at a time
+  bool wide;                   // rows of results begin at multiples of 32 bytes
   uint32_t *status;
 };
-constexpr int readers(bool codes) { return codes ? 6 : 8; }  // CTAs an SM holds
+constexpr int kReaders = 8;  // CTAs an SM holds
 
-// A thread takes a piece of 16 stored bytes: codes become 16 elements, 16-bit
-// elements are copied.  Neighbours take neighbouring pieces of a token's heads; a
-// CTA's next tokens are looked up before this one's pieces are waited for.
+__device__ __forceinline__ void store32(void *to, const uint4 &a, const uint4 &b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
+// A thread has a piece of 16 stored bytes, always the same of keys or of values, of
+// one token after the other: codes become 16 elements, 16-bit elements are copied.
+// Neighbours have neighbouring pieces; the next token is looked up before this
+// one's piece is waited for.  Warps cover the latency, not pieces ahead: 100003
+// tokens take 98 us with 8 CTAs an SM, 101 with 6; two pieces at a time and 6 CTAs
+// 114, four and 4 148.  Stores of 32 bytes: with two of 16 123 became 136.
 template <typename T, bool CODES>
-__global__ void __launch_bounds__(kThreads, readers(CODES)) k_read(const __grid_constant__ RdParams a) {
+__global__ void __launch_bounds__(kThreads, kReaders) k_read(const __grid_constant__ RdParams a) {
   const fp4_read_params &p = a.p;
   const fp4_kv_cache &c = p.cache;
   constexpr int kEach = CODES ? 16 : 8;
   dependent_wait();
   launch_dependents();
-  const int width = kThreads / a.tokens, tl = threadIdx.x / width, in = threadIdx.x - tl * width;
-  if (tl >= a.tokens) return;
-  const int hop = gridDim.x * a.tokens, tokens = (int)p.tokens;  // (below 2^30)
+  const int group = blockIdx.x / a.parts, part = blockIdx.x - group * a.parts;
+  const bool key = part < a.parts / 2;
+  const int width = kThreads / a.tokens, tl = threadIdx.x / width;
+  const int i = (key ? part : part - a.parts / 2) * width + threadIdx.x - tl * width;
+  const int head = over(i, a.piece), d = (i - head * a.pieces) * kEach;
+  if (tl >= a.tokens || head >= c.kv_heads) return;
+  const int hop = gridDim.x / a.parts * a.tokens, tokens = (int)p.tokens;  // (below 2^30)
+  const int64_t in_page = key ? c.k_page : c.v_page, in_place = key ? c.k_place : c.v_place;
+  const int64_t sf_page = key ? p.scales.k_page : p.scales.v_page, sf_block = key ? p.scales.k_block : p.scales.v_block;
+  const int64_t out_token = key ? p.k_token : p.v_token;
+  const char *const from = static_cast<const char *>(key ? c.k : c.v) + (head * (key ? c.k_head : c.v_head) + d) * (CODES ? 1 : 2);
+  const uint8_t *const sf = CODES ? (key ? p.scales.k_sf : p.scales.v_sf) + head * (key ? p.scales.k_head : p.scales.v_head) : nullptr;
+  T *const to = static_cast<T *>(key ? p.k_out : p.v_out) + head * (key ? p.k_out_head : p.v_out_head) + d;
   int page = 0, place = 0;
   auto look = [&](int t) {
-    return t < tokens && locate8(c, a.page, p.seq ? p.seq[t] : t, p.pos[t], INT64_MAX, in == 0 ? a.status : nullptr, page, place);
+    return t < tokens && locate8(c, a.page, p.seq ? p.seq[t] : t, p.pos[t], INT64_MAX, i == 0 && key ? a.status : nullptr,
+                                 page, place);
   };
-  int t = blockIdx.x * a.tokens + tl;
-  bool keep = look(t);
+  int t = group * a.tokens + tl;
+  bool there = look(t);
   for (; t < tokens; t += hop) {
-    const bool here = keep;
-    const int my_page = page, my_place = place;
-    for (int i = in; i < a.per; i += width) {
-      const int row = over(i, a.piece), d = (i - row * a.pieces) * kEach;
-      const bool key = row < c.kv_heads;
-      const int head = key ? row : row - c.kv_heads;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      int code = 127;
-      if (here) {
-        const int64_t at = my_page * (key ? c.k_page : c.v_page) + my_place * (key ? c.k_place : c.v_place) +
-                           head * (key ? c.k_head : c.v_head) + d;
-        v = *reinterpret_cast<const uint4 *>(static_cast<const char *>(key ? c.k : c.v) + at * (CODES ? 1 : 2));
-        if (CODES) {
-          const fp4_kv_scales &f = p.scales;
-          code = (key ? f.k_sf : f.v_sf)[my_page * (key ? f.k_page : f.v_page) +
-                                         over(my_place, a.block) * (key ? f.k_block : f.v_block) +
-                                         head * (key ? f.k_head : f.v_head)];
-        }
-      }
-      if (i == in) keep = look(t + hop);
-      T *out = key ? static_cast<T *>(p.k_out) + t * p.k_token + head * p.k_out_head + d
-                   : static_cast<T *>(p.v_out) + t * p.v_token + head * p.v_out_head + d;
-      if (!CODES) {
-        *reinterpret_cast<uint4 *>(out) = v;
-        continue;
-      }
-      const float f = code == 255 ? NAN : e8m0_value(code);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint4 v = make_uint4(0, 0, 0, 0);
+    int code = 127;
+    if (there) {
+      v = *reinterpret_cast<const uint4 *>(from + (page * in_page + place * in_place) * (CODES ? 1 : 2));
+      if (CODES) code = sf[page * sf_page + over(place, a.block) * sf_block];
+    }
+    there = look(t + hop);
+    T *const out = to + t * out_token;
+    if (!CODES) {
+      *reinterpret_cast<uint4 *>(out) = v;
+      continue;
+    }
+    const float f = code == 255 ? NAN : e8m0_value(code);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t r[8];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t r[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t lo, hi;
-          halves(w[2 * j + e], lo, hi);
-          const float2 x = Two<__half>::get(lo), y = Two<__half>::get(hi);
-          r[2 * e] = Two<T>::put(x.x * f, x.y * f);
-          r[2 * e + 1] = Two<T>::put(y.x * f, y.y * f);
-        }
-        reinterpret_cast<uint4 *>(out)[j] = make_uint4(r[0], r[1], r[2], r[3]);
-      }
+    for (int e = 0; e < 4; ++e) {
+      uint32_t lo, hi;
+      halves(w[e], lo, hi);
+      const float2 x = Two<__half>::get(lo), y = Two<__half>::get(hi);
+      r[2 * e] = Two<T>::put(x.x * f, x.y * f);
+      r[2 * e + 1] = Two<T>::put(y.x * f, y.y * f);
+    }
+    const uint4 r0 = make_uint4(r[0], r[1], r[2], r[3]), r1 = make_uint4(r[4], r[5], r[6], r[7]);
+    if (a.wide) {
+      store32(out, r0, r1);
+    } else {
+      reinterpret_cast<uint4 *>(out)[0] = r0;
+      reinterpret_cast<uint4 *>(out)[1] = r1;
     }
   }
 }
@@ -605,16 +614,23 @@ fp4_status launch_read(RdParams &a, cudaStream_t s) {
   const fp4_read_params &p = a.p;
   const bool codes = p.scales.k_sf != nullptr;
   a.pieces = p.cache.head_dim / (codes ? 16 : 8);
-  if (2 * (int64_t)p.cache.kv_heads * a.pieces > INT32_MAX) return FP4_ERR_SHAPE;
-  a.per = 2 * p.cache.kv_heads * a.pieces;
+  if (2 * (int64_t)p.cache.kv_heads * a.pieces > INT32_MAX / 2) return FP4_ERR_SHAPE;
+  const int per = p.cache.kv_heads * a.pieces;  // pieces of a token's keys
   a.tokens = 1;
-  while (a.tokens < 32 && kThreads / (2 * a.tokens) >= a.per) a.tokens *= 2;
+  while (a.tokens < 32 && kThreads / (2 * a.tokens) >= per) a.tokens *= 2;
+  a.parts = 2 * (int)ceil_div(per, kThreads / a.tokens);
   a.page = divisor(p.cache.page_size);
   a.block = divisor(codes ? p.scales.block : 1);
   a.piece = divisor(a.pieces);
-  const int64_t most = readers(codes) * (int64_t)sm_count(), want = ceil_div(p.tokens, a.tokens);
+  auto whole32 = [](const void *to, int64_t token, int64_t head) {
+    return reinterpret_cast<uintptr_t>(to) % 32 == 0 && token % 16 == 0 && head % 16 == 0;
+  };
+  a.wide = whole32(p.k_out, p.k_token, p.k_out_head) && whole32(p.v_out, p.v_token, p.v_out_head);
+  // as many groups of CTAs as fit, or fewer that have equally many tokens
+  const int64_t most = ceil_div(kReaders * (int64_t)sm_count(), a.parts), want = ceil_div(p.tokens, a.tokens);
+  const int64_t groups = want ? ceil_div(want, ceil_div(want, most)) : 0;
   const auto kern = codes ? k_read<T, true> : k_read<T, false>;
-  return launch_dependent(kern, dim3((unsigned)(want < most ? want : most)), dim3(kThreads), 0, s, a) == cudaSuccess
+  return launch_dependent(kern, dim3((unsigned)(groups * a.parts)), dim3(kThreads), 0, s, a) == cudaSuccess
              ? FP4_OK
              : FP4_ERR_CUDA;
 }
