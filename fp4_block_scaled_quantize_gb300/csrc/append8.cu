@@ -110,8 +110,8 @@ __device__ __forceinline__ int code_for(float top) {
   return e > 0 ? e : 0;  // (a subnormal top has e <= 0 too)
 }
 
-// How rows are read: whole pieces, pairs (i, i + rot_dim / 2) or neighbours; or
-// any pointers, strides and rot_dim.
+// How rows are read: whole pieces, pairs (i, i + rot_dim / 2) or neighbours, with
+// strides of rows and heads in 32 bits; or any pointers, strides and rot_dim.
 enum Kind { kHalves, kPairs, kAny };
 
 // Where the two pieces of a unit lie, and which of them are turned.
@@ -196,7 +196,8 @@ template <typename T, int KIND, int kHold>
 __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
   const fp4_append_params &p = a.p;
   const fp4_kv_cache &c = p.cache;
-  __shared__ float top_sh[2][kWarps];
+  using Step = typename std::conditional<KIND == kAny, int64_t, int>::type;
+  __shared__ unsigned top_sh[2][kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, block = a.s.block, Hk = c.kv_heads;
   const int groups = 32 / a.units, my_group = lane / a.units, my_unit = lane - my_group * a.units;
   const int teams = kWarps / a.team, team = warp / a.team, mate = warp % a.team;
@@ -267,18 +268,44 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
       // ahead measured the same), and the heads share their cosines and sines.
       uint4 v[kHold], w[kHold];
       Turn turn[kHold];
-      auto ask = [&](int hv, int r) {
+      // the head whose rows are asked for next, and the one that is stored: where
+      // token t's row, its scale and the steps to other rows and heads are
+      const T *src = nullptr;
+      Step src_row = 0, src_head = 0;
+      int ahead[kHold];
+#pragma unroll
+      for (int h = 0; h < kHold; ++h) ahead[h] = max(min(r0 + h * hop, rows - 1), 0);
+      uint8_t *dst = nullptr, *sf = nullptr;
+      Step dst_row = 0, dst_head = 0, sf_head = 0;
+      auto read_from = [&](int hv) {
         const bool key = hv < Hk;
         const int head = key ? hv : hv - Hk;
-        const T *const src = key ? static_cast<const T *>(p.k) + t * p.k_token + head * p.k_head
-                                 : static_cast<const T *>(p.v) + t * p.v_token + head * p.v_head;
-        const int64_t step = key ? p.k_token : p.v_token;
+        src_row = (Step)(key ? p.k_token : p.v_token);
+        src_head = (Step)(key ? p.k_head : p.v_head);
+        src = static_cast<const T *>(key ? p.k : p.v) + t * src_row + (int64_t)head * src_head;
+      };
+      auto store_to = [&](int hv) {
+        const bool key = hv < Hk;
+        const int head = key ? hv : hv - Hk;
+        dst_row = (Step)(key ? c.k_place : c.v_place);
+        dst_head = (Step)(key ? c.k_head : c.v_head);
+        sf_head = (Step)(key ? a.s.k_head : a.s.v_head);
+        dst = static_cast<uint8_t *>(key ? c.k : c.v) + (int64_t)page * (key ? c.k_page : c.v_page) +
+              (int64_t)head * dst_head + (int64_t)place0 * dst_row;
+        sf = (key ? a.s.k_sf : a.s.v_sf) + (int64_t)head * sf_head + (int64_t)page * (key ? a.s.k_page : a.s.v_page) +
+             blk * (key ? a.s.k_block : a.s.v_block);
+      };
+      auto next_read = [&](int hv) {
+        if (hv == Hk) read_from(hv);
+        else src += src_head;
+      };
+      auto ask = [&](int r) {
 #pragma unroll
         for (int h = 0; h < kHold; ++h) {
           if (KIND == kAny) continue;
-          const int q = max(min(r + h * hop, rows - 1), 0);
-          v[h] = *reinterpret_cast<const uint4 *>(src + q * step + unit.o1);
-          w[h] = *reinterpret_cast<const uint4 *>(src + q * step + unit.o2);
+          const T *const row = src + (int64_t)(r == r0 ? ahead[h] : max(min(r + h * hop, rows - 1), 0)) * src_row;
+          v[h] = *reinterpret_cast<const uint4 *>(row + unit.o1);
+          w[h] = *reinterpret_cast<const uint4 *>(row + unit.o2);
         }
       };
       auto ask_turns = [&](bool key, int r) {
@@ -287,20 +314,15 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
           if (KIND != kAny) load_turn<KIND>(p, unit, key, pos0 + max(min(r + h * hop, rows - 1), 0), turn[h]);
       };
       const bool single = steps == 1;
+      read_from(hv0);
+      store_to(hv0);
       if (single) {
-        ask(hv0, r0);
+        ask(r0);
         ask_turns(hv0 < Hk, r0);
       }
       for (int hv = hv0; hv < hv1; ++hv) {
         const bool key = hv < Hk;
-        const int head = key ? hv : hv - Hk;
-        const T *const src = key ? static_cast<const T *>(p.k) + t * p.k_token + head * p.k_head
-                                 : static_cast<const T *>(p.v) + t * p.v_token + head * p.v_head;
-        const int64_t step = key ? p.k_token : p.v_token, place = key ? c.k_place : c.v_place;
-        uint8_t *const dst = static_cast<uint8_t *>(key ? c.k : c.v) + (int64_t)page * (key ? c.k_page : c.v_page) +
-                             head * (key ? c.k_head : c.v_head) + place0 * place;
-        uint8_t *const sf = (key ? a.s.k_sf : a.s.v_sf) + head * (key ? a.s.k_head : a.s.v_head) +
-                            (int64_t)page * (key ? a.s.k_page : a.s.v_page) + blk * (key ? a.s.k_block : a.s.v_block);
+        if (hv == Hk && hv != hv0) store_to(hv);
         const int old = rows ? *sf : 0;
         float x[kHold][16];
         auto over_team = [&](float top) {
@@ -312,22 +334,22 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
             }
             return top;
           }
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+          // (numbers that are not negative are ordered as their bits are)
+          unsigned bits = __reduce_max_sync(~0u, __float_as_uint(top));
           if (a.team > 1) {
-            if (lane == 0) top_sh[parity][warp] = top;
+            if (lane == 0) top_sh[parity][warp] = bits;
             asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * a.team) : "memory");
-            for (int o = 0; o < a.team; ++o) top = fmaxf(top, top_sh[parity][team * a.team + o]);
+            bits = __reduce_max_sync(~0u, top_sh[parity][team * a.team + (lane & (a.team - 1))]);
             parity ^= 1;
           }
-          return top;
+          return __uint_as_float(bits);
         };
         auto take = [&](int r, bool infinite) {
 #pragma unroll
           for (int h = 0; h < kHold; ++h) {
             const int q = max(min(r + h * hop, rows - 1), 0);
             if (KIND == kAny)
-              turn_any(p, src + q * step, my_unit, pos0 + q, key, x[h]);
+              turn_any(p, src + (int64_t)q * src_row, my_unit, pos0 + q, key, x[h]);
             else
               turn_unit<T, KIND>(key, unit, v[h], w[h], turn[h], x[h]);
             if (infinite)
@@ -343,7 +365,7 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
           top = 0.0f;
           for (int i = 0; i < steps; ++i) {
             if (!single) {
-              ask(hv, r0 + i * kHold * hop);
+              ask(r0 + i * kHold * hop);
               ask_turns(key, r0 + i * kHold * hop);
             }
             take(r0 + i * kHold * hop, infinite);
@@ -358,7 +380,10 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
           top = over_team(fmaxf(top, more));
           if (infinite || !(apart ? __any_sync(~0u, isinf(top)) : isinf(top))) break;
         }
-        if (single && hv + 1 < hv1) ask(hv + 1, r0);
+        if (single && hv + 1 < hv1) {
+          next_read(hv + 1);
+          ask(r0);
+        }
         const int need = code_for(top), code = begin == 0 || need > old ? need : old;
         const float f = e8m0_inverse(code < 255 ? code : 254);
         for (int i = steps - 1;;) {
@@ -369,13 +394,13 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
             uint32_t z[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[e] = codes2(x[h][2 * e] * f, x[h][2 * e + 1] * f);
-            uint8_t *to = dst + r * place;
+            uint8_t *to = dst + (int64_t)r * dst_row;
             const int o1 = KIND != kAny ? unit.o1 : 16 * my_unit, o2 = KIND != kAny ? unit.o2 : o1 + 8;
             *reinterpret_cast<uint2 *>(to + o1) = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
             *reinterpret_cast<uint2 *>(to + o2) = make_uint2(z[4] | z[5] << 16, z[6] | z[7] << 16);
           }
           if (i-- == 0) break;
-          ask(hv, r0 + i * kHold * hop);
+          ask(r0 + i * kHold * hop);
           ask_turns(key, r0 + i * kHold * hop);
           take(r0 + i * kHold * hop, infinite);
         }
@@ -384,7 +409,7 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
 #pragma unroll 4
           for (int r = r0; r < block - n; r += hop) {
             const int q = (r < begin ? r : r + n) - begin;
-            uint4 *at = reinterpret_cast<uint4 *>(dst + q * place + 16 * my_unit);
+            uint4 *at = reinterpret_cast<uint4 *>(dst + (int64_t)q * dst_row + 16 * my_unit);
             const uint4 o = *at;
             uint32_t z[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
@@ -398,6 +423,9 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
           }
         }
         if (rows && my_unit == 0 && (apart || my_all == 0) && code != old) *sf = (uint8_t)code;
+        dst += dst_head;
+        sf += sf_head;
+        if (!single) next_read(hv + 1);
       }
     }
   }
@@ -490,9 +518,13 @@ bool whole8(const void *ptr, int64_t s0, int64_t s1) { return aligned16(ptr) && 
 template <typename T>
 fp4_status launch_append(Ap8Params &a, cudaStream_t s) {
   const fp4_append_params &p = a.p;
-  const bool whole = p.rot_dim % (p.interleaved ? 8 : 16) == 0 && whole8(p.k, p.k_token, p.k_head) &&
-                     whole8(p.v, p.v_token, p.v_head) && aligned16(p.rope) &&
-                     (!p.q || (whole8(p.q, p.q_token, p.q_head) && whole8(p.q_out, p.qo_token, p.qo_head)));
+  const int64_t steps[] = {p.k_token, p.k_head, p.v_token, p.v_head, p.cache.k_place, p.cache.k_head, p.cache.v_place,
+                           p.cache.v_head, a.s.k_head, a.s.v_head};
+  bool whole = true;
+  for (int64_t step : steps) whole = whole && step <= INT32_MAX;
+  whole = whole && p.rot_dim % (p.interleaved ? 8 : 16) == 0 && whole8(p.k, p.k_token, p.k_head) &&
+          whole8(p.v, p.v_token, p.v_head) && aligned16(p.rope) &&
+          (!p.q || (whole8(p.q, p.q_token, p.q_head) && whole8(p.q_out, p.qo_token, p.qo_head)));
   a.units = p.cache.head_dim / 16;
   const int heads = 2 * p.cache.kv_heads, rows = 32 / a.units;
   const int64_t most = kResident * (int64_t)sm_count(), grid_most = 1 << 20;
