@@ -344,7 +344,7 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
           }
           return __uint_as_float(bits);
         };
-        auto take = [&](int r, bool infinite) {
+        auto take = [&](int r) {
 #pragma unroll
           for (int h = 0; h < kHold; ++h) {
             const int q = max(min(r + h * hop, rows - 1), 0);
@@ -352,33 +352,51 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
               turn_any(p, src + (int64_t)q * src_row, my_unit, pos0 + q, key, x[h]);
             else
               turn_unit<T, KIND>(key, unit, v[h], w[h], turn[h], x[h]);
-            if (infinite)
-#pragma unroll
-              for (int e = 0; e < 16; ++e) x[h][e] = or_nan(x[h][e]);
           }
+        };
+        auto leave_out = [&] {
+#pragma unroll
+          for (int h = 0; h < kHold; ++h)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[h][e] = or_nan(x[h][e]);
+        };
+        auto largest = [&](float &top, float &more) {  // (of a number and a NaN: the number)
+#pragma unroll
+          for (int h = 0; h < kHold; ++h)
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              top = fmaxf(top, fabsf(x[h][e]));
+              more = fmaxf(more, fabsf(x[h][e + 1]));
+            }
         };
         // the largest; where that is an infinity, once more without infinities
         float top;
         bool infinite = false;
-        for (;; infinite = true) {
-          float more = 0.0f;
-          top = 0.0f;
-          for (int i = 0; i < steps; ++i) {
-            if (!single) {
+        if (single) {
+          float more = top = 0.0f;
+          take(r0);
+          largest(top, more);
+          top = over_team(fmaxf(top, more));
+          infinite = apart ? __any_sync(~0u, isinf(top)) : isinf(top);
+          if (infinite) {
+            more = top = 0.0f;
+            leave_out();
+            largest(top, more);
+            top = over_team(fmaxf(top, more));
+          }
+        } else {
+          for (;; infinite = true) {
+            float more = top = 0.0f;
+            for (int i = 0; i < steps; ++i) {
               ask(r0 + i * kHold * hop);
               ask_turns(key, r0 + i * kHold * hop);
+              take(r0 + i * kHold * hop);
+              if (infinite) leave_out();
+              largest(top, more);
             }
-            take(r0 + i * kHold * hop, infinite);
-#pragma unroll
-            for (int h = 0; h < kHold; ++h)
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {  // (of a number and a NaN: the number)
-                top = fmaxf(top, fabsf(x[h][e]));
-                more = fmaxf(more, fabsf(x[h][e + 1]));
-              }
+            top = over_team(fmaxf(top, more));
+            if (infinite || !(apart ? __any_sync(~0u, isinf(top)) : isinf(top))) break;
           }
-          top = over_team(fmaxf(top, more));
-          if (infinite || !(apart ? __any_sync(~0u, isinf(top)) : isinf(top))) break;
         }
         if (single && hv + 1 < hv1) {
           next_read(hv + 1);
@@ -402,7 +420,8 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
           if (i-- == 0) break;
           ask(r0 + i * kHold * hop);
           ask_turns(key, r0 + i * kHold * hop);
-          take(r0 + i * kHold * hop, infinite);
+          take(r0 + i * kHold * hop);
+          if (infinite) leave_out();
         }
         if (rows && begin != 0 && code > old) {  // the block's other places, in the new unit
           const float down = e8m0_inverse(127 + min(code - old, 100));
@@ -566,7 +585,7 @@ struct RdParams {
   bool wide;                   // rows of results begin at multiples of 32 bytes
   uint32_t *status;
 };
-constexpr int kReaders = 8;  // CTAs an SM holds
+constexpr int kReadThreads = 256, kReaders = 8;  // CTAs an SM holds
 
 __device__ __forceinline__ void store32(void *to, const uint4 &a, const uint4 &b) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(a.x), "r"(a.y), "r"(a.z),
@@ -581,7 +600,7 @@ __device__ __forceinline__ void store32(void *to, const uint4 &a, const uint4 &b
 // tokens take 98 us with 8 CTAs an SM, 101 with 6; two pieces at a time and 6 CTAs
 // 114, four and 4 148.  Stores of 32 bytes: with two of 16 123 became 136.
 template <typename T, bool CODES>
-__global__ void __launch_bounds__(kThreads, kReaders) k_read(const __grid_constant__ RdParams a) {
+__global__ void __launch_bounds__(kReadThreads, kReaders) k_read(const __grid_constant__ RdParams a) {
   const fp4_read_params &p = a.p;
   const fp4_kv_cache &c = p.cache;
   constexpr int kEach = CODES ? 16 : 8;
@@ -589,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, kReaders) k_read(const __grid_consta
   launch_dependents();
   const int group = blockIdx.x / a.parts, part = blockIdx.x - group * a.parts;
   const bool key = part < a.parts / 2;
-  const int width = kThreads / a.tokens, tl = threadIdx.x / width;
+  const int width = kReadThreads / a.tokens, tl = threadIdx.x / width;
   const int i = (key ? part : part - a.parts / 2) * width + threadIdx.x - tl * width;
   const int head = over(i, a.piece), d = (i - head * a.pieces) * kEach;
   if (tl >= a.tokens || head >= c.kv_heads) return;
@@ -649,8 +668,8 @@ fp4_status launch_read(RdParams &a, cudaStream_t s) {
   if (2 * (int64_t)p.cache.kv_heads * a.pieces > INT32_MAX / 2) return FP4_ERR_SHAPE;
   const int per = p.cache.kv_heads * a.pieces;  // pieces of a token's keys
   a.tokens = 1;
-  while (a.tokens < 32 && kThreads / (2 * a.tokens) >= per) a.tokens *= 2;
-  a.parts = 2 * (int)ceil_div(per, kThreads / a.tokens);
+  while (a.tokens < 32 && kReadThreads / (2 * a.tokens) >= per) a.tokens *= 2;
+  a.parts = 2 * (int)ceil_div(per, kReadThreads / a.tokens);
   a.page = divisor(p.cache.page_size);
   a.block = divisor(codes ? p.scales.block : 1);
   a.piece = divisor(a.pieces);
@@ -662,7 +681,7 @@ fp4_status launch_read(RdParams &a, cudaStream_t s) {
   const int64_t most = ceil_div(kReaders * (int64_t)sm_count(), a.parts), want = ceil_div(p.tokens, a.tokens);
   const int64_t groups = want ? ceil_div(want, ceil_div(want, most)) : 0;
   const auto kern = codes ? k_read<T, true> : k_read<T, false>;
-  return launch_dependent(kern, dim3((unsigned)(groups * a.parts)), dim3(kThreads), 0, s, a) == cudaSuccess
+  return launch_dependent(kern, dim3((unsigned)(groups * a.parts)), dim3(kReadThreads), 0, s, a) == cudaSuccess
              ? FP4_OK
              : FP4_ERR_CUDA;
 }
