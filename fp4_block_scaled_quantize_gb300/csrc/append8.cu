@@ -12,10 +12,15 @@
 // scale) for a few tokens.
 //
 // Measured in a graph: 192 tokens of 192 sequences, 16 + 2 x 16 heads of 64 in
-// blocks of 8 4.1 us, one token 3.7; 8191 prompt tokens of 32 + 2 x 8 heads of 128
-// in blocks of 64 57 us (3.2 TB/s, 48% of a copy's rate; without queries 33: some
-// 900 instructions of a warp a head and 64 tokens, 16 warps an SM); reading 100003
-// tokens back 119 us (5.1 TB/s, 76%), 300 2.3 us.
+// blocks of 8 4.0 us, one token 3.6; 8191 prompt tokens of 32 + 2 x 8 heads of 128
+// in blocks of 64 50.5 us (3.7 TB/s, 54% of a copy's rate; without queries 27: some
+// 700 instructions of a warp a head and 64 tokens, 16 warps an SM); reading 100003
+// tokens back 97.5 us (6.3 TB/s, 93%), 300 2.1 us.
+//
+// A rotated key is rounded to binary32 before it is rounded to its code: about one
+// code in a million is the other neighbour of a number that lies within 2^-20 of
+// the middle of two.  Rotations whose binary32 result is rounded to odd wherever a
+// middle is near have none of these, and took 59.8 us for 50.8.
 //
 // Layout.  Lanes hold units of 16 elements (two pieces of 8, in the rotated part
 // those whose elements form pairs) of 32 / units rows; a team of warps takes the
