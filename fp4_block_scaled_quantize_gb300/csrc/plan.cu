@@ -4,19 +4,21 @@
 // Bound: latency (a launch, two dependent loads, scans over the sequences, a
 // look-up), and for prompts the 16 bytes written a token.
 //
-// Layout.  Every CTA scans all sequences, a run of them a thread: the new
-// tokens' offsets, the pages that each gets, those that each gives back.  It then
-// writes its share of the table entries, the token maps and the pages that go
-// back, finding sequences by bisection in the threads' sums and a walk within a
-// thread's run (up to 512 sequences: none, and what is known of them is in shared
-// memory).  Page numbers of new entries come from the stack, not from the table,
-// so no CTA waits for another; the last one to finish (counted in the pool's
-// second word) writes the state that the others read: lengths, rooms, how many
-// are free, and, where the call also gives out pages from those places of the
-// stack, what goes back.
+// Layout.  Where no sequence gets or loses more than kFew tokens (decoding), one
+// CTA scans the sequences and a thread does all of a sequence's work.  Else every
+// CTA scans all sequences, a run of them a thread: the new tokens' offsets, the
+// pages that each gets, those that each gives back.  It then writes its share of
+// the table entries, the token maps and the pages that go back, finding sequences
+// by bisection in the threads' sums and a walk within a thread's run (up to 512
+// sequences: none, and what is known of them is in shared memory).  Page numbers of
+// new entries come from the stack, not from the table, so no CTA waits for another;
+// the last one (counted in the pool's second word) writes the state that the others
+// read: lengths, rooms, how many are free, and, where the call also gives out pages
+// from those places of the stack, what goes back.
 // Measured in a graph, two calls, pages given back and taken again: 256 sequences
-// by a token 12.6 us; 96 prompts of 250000 tokens in all 15.6.  One CTA's scans
-// take some 4 us of each: barriers and dependent loads, 27% of issue slots.
+// by a token 6.7 us (by bisection, with the state written by the last CTA to
+// finish, 12.6); 96 prompts of 250000 tokens in all 15.0.  Two empty launches take
+// 1.2, with the loads 1.9, with the scans 3.6.
 #include "serve.cuh"
 
 namespace fp4 {
@@ -25,6 +27,10 @@ namespace {
 
 constexpr int kThreads = 512, kW = kThreads / 32;
 constexpr int kTokens = 4;  // consecutive tokens of a thread
+// Where no sequence gets or loses more than kFew tokens (and each has a thread),
+// its thread does all of its work: no look-ups, and one CTA writes everything but
+// the maps' ends.
+constexpr int kFew = 4;
 
 struct PlanParams {
   fp4_plan_params p;
@@ -91,32 +97,112 @@ __device__ __forceinline__ int thread_of(const int64_t *sums, int64_t x) {
   return lo;
 }
 
+// The whole call by one CTA, a thread a sequence.
+__device__ __forceinline__ void plan_few(const PlanParams &a, const Change &c, int64_t add0, int64_t total, int64_t free,
+                                         int64_t *sums, int64_t *warps, int *taken_sh) {
+  const fp4_plan_params &p = a.p;
+  const int s = threadIdx.x;
+  const bool mine = s < p.seqs;
+  const int grows = mine ? c.grows() : 0, gives = mine ? c.gives() : 0;
+  const bool back_too = __syncthreads_or(gives > 0);
+  const int64_t grow0 = scan(grows, sums, warps);
+  const bool ok = mine && c.granted(grow0 + grows, free);
+  if (ok && grows) atomicMax(taken_sh, (int)(grow0 + grows));
+  const int32_t *const stack = p.pool + 2 + free - 1 - grow0;  // downwards, the pages that the sequence gets
+  int32_t *const row = p.table + s * p.table_stride;
+  for (int i = 0; ok && i < grows; ++i) row[c.held + i] = stack[-i];
+  if (mine && p.tokens >= 0)
+#pragma unroll
+    for (int i = 0; i < kFew; ++i) {
+      const int64_t t = add0 + i;
+      if (i >= c.n || t >= p.tokens) break;
+      const int pos = c.length + i, e = ok ? over(pos, a.page) : 0;
+      if (p.seq) p.seq[t] = s;
+      if (p.pos) p.pos[t] = ok ? pos : -1;
+      if (p.slot)
+        p.slot[t] = ok ? (int64_t)(e < c.held ? row[e] : stack[c.held - e]) * p.page_size + (pos - e * p.page_size) : -1;
+    }
+  __syncthreads();  // what goes back may lie on places that were read above
+  const int64_t taken = *taken_sh, left = free - taken;
+  int64_t fit = 0, back = 0;
+  if (back_too) {
+    const int64_t give0 = scan(gives, sums, warps);
+    back = sums[kThreads];
+    fit = min(back, p.pool_pages - left);  // (more than the pool's pages: what is left over is lost)
+    for (int i = 0; i < gives; ++i) {
+      const int64_t at = back - 1 - (give0 + i);
+      if (at < fit) p.pool[2 + left + at] = row[c.want + i];
+      row[c.want + i] = -1;
+    }
+  }
+  if (mine && p.offsets) p.offsets[s] = (int32_t)min(add0, (int64_t)INT32_MAX);
+  if (mine && !ok) raise_status(a.status, kStatusIndex);
+  if (ok) {
+    p.lengths[s] = (int32_t)c.after;
+    p.room[s] = (c.n < 0 ? min(c.held, c.want) : c.held + grows) * p.page_size;
+  }
+  if (threadIdx.x == 0) {
+    if (p.offsets) p.offsets[p.seqs] = (int32_t)min(total, (int64_t)INT32_MAX);
+    if (back > fit) raise_status(a.status, kStatusIndex);
+    p.pool[0] = (int32_t)(left + fit);
+  }
+}
+
 __global__ void __launch_bounds__(kThreads) k_plan(const __grid_constant__ PlanParams a) {
   __shared__ int64_t add_sh[kThreads + 1], grow_sh[kThreads + 1], give_sh[kThreads + 1], warps[kW];
-  __shared__ int n_sh[kThreads], length_sh[kThreads], held_sh[kThreads], last_sh, taken_sh;
+  __shared__ int n_sh[kThreads], length_sh[kThreads], held_sh[kThreads], last_sh, taken_sh, free_sh;
   const fp4_plan_params &p = a.p;
   const int per = (p.seqs + kThreads - 1) / kThreads;
   const int s0 = min((int)threadIdx.x * per, p.seqs), s1 = min(s0 + per, p.seqs);
   dependent_wait();
   launch_dependents();
-  const int64_t free = min((int64_t)max(p.pool[0], 0), p.pool_pages);
   auto load = [&](int s, int64_t first) {
     return change_of(a, p.new_tokens[s], max(p.lengths[s], 0), min(over(max(p.room[s], 0), a.page), p.seq_pages), first);
   };
   int64_t add = 0;
-  bool back_too = false;
+  bool back_too = false, few = per == 1;
   for (int s = s0; s < s1; ++s) {
     const Change c = load(s, 0);
     if (s == s0) n_sh[threadIdx.x] = c.n, length_sh[threadIdx.x] = c.length, held_sh[threadIdx.x] = c.held;
     add += c.adds();
     back_too |= c.n < 0;
+    few &= c.n <= kFew && c.n >= -kFew;
   }
-  if (threadIdx.x == 0) taken_sh = 0;
+  if (threadIdx.x == 0) {
+    taken_sh = 0;
+    free_sh = (int)min((int64_t)max(p.pool[0], 0), p.pool_pages);
+  }
   // sequence s, the first of thread th's run if there is one a thread
   auto change = [&](int s, int64_t first) {
     return per == 1 ? change_of(a, n_sh[s], length_sh[s], held_sh[s], first) : load(s, first);
   };
-  const int64_t add0 = scan(add, add_sh, warps);
+  few = __syncthreads_and(few);
+  const int64_t add0 = scan(add, add_sh, warps), free = free_sh;
+  const int64_t step = (int64_t)gridDim.x * kThreads, me = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (few) {
+    const int64_t total = add_sh[kThreads];
+    for (int64_t t = total + me; t < p.tokens; t += step) {
+      if (p.seq) p.seq[t] = -1;
+      if (p.pos) p.pos[t] = -1;
+      if (p.slot) p.slot[t] = -1;
+    }
+    // (the others have read what they go by: nothing but new_tokens)
+    if (blockIdx.x == 0) {
+      Change c{};
+      if (threadIdx.x < p.seqs) c = change(threadIdx.x, add0);
+      plan_few(a, c, add0, total, free, grow_sh, warps, &taken_sh);
+    }
+    return;
+  }
+  // One thread a sequence: everything that is read of the state has been read, so
+  // the CTA that comes last may write it while others still work.
+  const bool early = per == 1 && gridDim.x > 1;
+  unsigned *const tickets = reinterpret_cast<unsigned *>(p.pool + 1);
+  if (early && threadIdx.x == 0) {
+    __threadfence();
+    last_sh = (atomicAdd(tickets, 1u) & 0xFFFFu) == gridDim.x - 1;
+    __threadfence();
+  }
   int64_t grow = 0, give = 0, at = add0;
   for (int s = s0; s < s1; ++s) {
     const Change c = change(s, at);
@@ -127,7 +213,6 @@ __global__ void __launch_bounds__(kThreads) k_plan(const __grid_constant__ PlanP
   const int64_t grow0 = scan(grow, grow_sh, warps);
   back_too = __syncthreads_or(back_too);
   const int64_t give0 = back_too ? scan(give, give_sh, warps) : 0;
-  const int64_t step = (int64_t)gridDim.x * kThreads, me = (int64_t)blockIdx.x * kThreads + threadIdx.x;
 
   // table entries: page j of those to be granted
   const int64_t pages = min(grow_sh[kThreads], free);
@@ -237,16 +322,19 @@ __global__ void __launch_bounds__(kThreads) k_plan(const __grid_constant__ PlanP
   };
   if (taken == 0) give_back(me, step);  // onto places of the stack that nobody reads
 
-  // the last CTA writes the state
-  if (gridDim.x > 1) {
+  // the last CTA writes the state: the last to have read it, or, where pages go back
+  // onto places of the stack that others read, or the state is read all along, the
+  // last to come here
+  if (gridDim.x > 1 && (!early || (taken != 0 && back != 0))) {
     __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) last_sh = atomicAdd(reinterpret_cast<unsigned *>(p.pool + 1), 1u) == gridDim.x - 1;
+    if (threadIdx.x == 0) last_sh = atomicAdd(tickets, 1u << 16) >> 16 == gridDim.x - 1;
     __syncthreads();
     if (!last_sh) return;
     __threadfence();
   } else {
     __syncthreads();
+    if (early && !last_sh) return;
   }
   if (taken != 0) {
     give_back(threadIdx.x, kThreads);
