@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
     for (int item = threadIdx.x; item < heads * (DP / 8); item += kThreads) {
       const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
       if (d >= D) continue;
-      const Whole r = join_all<kParts>([&](int q, float4 &st, float4 &lo, float4 &hi) {
+      const Whole r = join_all<kParts, false>([&](int q, float4 &st, float4 &lo, float4 &hi) {
         if (!(parts >> q & 1)) return;
         const float *from = o_sh + (q * kCols + col) * (DP + 8) + d;
         st = st_sh[q * kCols + col];
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
         hi = *reinterpret_cast<const float4 *>(from + 4);
       });
       if (whole) {
-        finish<T>(a, s, head0 + col, d, r.j, r.seen);
+        finish<T, false>(a, s, head0 + col, d, r.j, r.seen);
         continue;
       }
       const float *v = r.j.v;
@@ -525,14 +525,14 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
   for (int item = threadIdx.x * a.direct + rank; item < heads * (DP / 8); item += kThreads * a.direct) {
     const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
     if (d >= D) continue;
-    const Whole r = join_all<kCluster>([&](int q, float4 &st, float4 &lo, float4 &hi) {
+    const Whole r = join_all<kCluster, false>([&](int q, float4 &st, float4 &lo, float4 &hi) {
       if (q >= a.direct) return;
       const float *from = cg::this_cluster().map_shared_rank(part, q);
       st = *reinterpret_cast<const float4 *>(from + kCols * DP + col * 4);
       lo = *reinterpret_cast<const float4 *>(from + col * DP + d);
       hi = *reinterpret_cast<const float4 *>(from + col * DP + d + 4);
     });
-    if (r.there) finish<T>(a, s, head0 + col, d, r.j, r.seen);
+    if (r.there) finish<T, false>(a, s, head0 + col, d, r.j, r.seen);
   }
   cg::this_cluster().sync();  // nobody leaves while its part may be read
 }
@@ -604,8 +604,8 @@ fp4_status launch(AtParams a, cudaStream_t s) {
   if (a.ctas < 2) return FP4_OK;
   const cudaError_t e =
       rows * 4 <= a.ctas
-          ? launch_dependent(k_attention_join<T, DP, NT, kWide>, dim3((unsigned)rows), dim3(kWide), 0, s, a)
-          : launch_dependent(k_attention_join<T, DP, NT, kNarrow>, dim3((unsigned)a.ctas - 1), dim3(kNarrow), 0, s, a);
+          ? launch_dependent(k_attention_join<T, DP, NT, kWide, false>, dim3((unsigned)rows), dim3(kWide), 0, s, a)
+          : launch_dependent(k_attention_join<T, DP, NT, kNarrow, false>, dim3((unsigned)a.ctas - 1), dim3(kNarrow), 0, s, a);
   return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
 

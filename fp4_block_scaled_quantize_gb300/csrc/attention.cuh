@@ -32,8 +32,11 @@ struct AtParams {
   uint32_t *status;
 };
 
-// Partial row: 8 NT x DP outputs, then m, l, seen (1.0 or 0.0) and whether
-// there is one (clusters) per head.
+// Partial row: 8 NT x DP outputs relative to m, then m, l, seen (1.0 or 0.0) and
+// whether there is one (clusters) per head.  Over codes the outputs are relative
+// to a maximum of their own, mo (of scores with the values' exponents), which may
+// lie as far from m as the exponents of binary32 reach: m, l, kThere or kSeen, mo.
+constexpr float kThere = 1.0f, kSeen = 2.0f;
 constexpr int slot_floats(int cols, int dp) { return cols * (dp + 3 + 1); }
 
 __device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -227,68 +230,80 @@ __device__ __forceinline__ void store_lse(const AtParams &a, int s, int head, bo
       seen ? ((m == -INFINITY ? 0.0f : m) + log2f(l) - lift<T>()) * 0.693147180559945f : -INFINITY;
 }
 
-// Eight outputs of a row joined from parts, one for each bit of `parts`:
-// m(i), l(i) are part i's statistics, add(i, w, v) adds w times its outputs.
+// v 2^x in two steps: x alone may pass binary32's exponents where the result does not.
+__device__ __forceinline__ float shifted(float v, float half) { return v * half * half; }
+
+// Eight outputs of a row joined from parts, one for each bit of `parts`: m(i),
+// l(i) are part i's statistics, mo(i) what its outputs are relative to (CODES;
+// else m), add(i, w, v) adds w times its outputs.
 struct Joined {
-  float top, sum, v[8];
+  float top, topo, sum, v[8];
 };
-template <typename M, typename L, typename Add>
-__device__ __forceinline__ Joined join(uint32_t parts, M m, L l, Add add) {
+template <bool CODES, typename M, typename Mo, typename L, typename Add>
+__device__ __forceinline__ Joined join(uint32_t parts, M m, Mo mo, L l, Add add) {
   Joined j;
-  j.top = -INFINITY;
+  j.top = j.topo = -INFINITY;
   j.sum = 0.0f;
-  for (uint32_t p = parts; p; p &= p - 1) j.top = fmaxf(j.top, m(__ffs(p) - 1));
-  const float base = j.top == -INFINITY ? 0.0f : j.top;
+  for (uint32_t p = parts; p; p &= p - 1) {
+    j.top = fmaxf(j.top, m(__ffs(p) - 1));
+    if (CODES) j.topo = fmaxf(j.topo, mo(__ffs(p) - 1));
+  }
+  const float base = j.top == -INFINITY ? 0.0f : j.top, baseo = j.topo == -INFINITY ? 0.0f : j.topo;
 #pragma unroll
   for (int e = 0; e < 8; ++e) j.v[e] = 0.0f;
   for (uint32_t p = parts; p; p &= p - 1) {
     const int i = __ffs(p) - 1;
     const float w = ex2(m(i) - base);
     j.sum = fmaf(w, l(i), j.sum);
-    add(i, w, j.v);
+    add(i, CODES ? ex2(mo(i) - baseo) : w, j.v);
   }
   return j;
 }
-// The same of parts held side by side: get(q, st, lo, hi) reads part q (m, l,
-// seen, 1 and the outputs) if there is one.  All are requested together.
+// The same of parts held side by side: get(q, st, lo, hi) reads part q (its
+// statistics and the outputs) if there is one.  All are requested together.
 struct Whole {
   Joined j;
   bool seen, there;
 };
-template <int N, typename Get>
+template <int N, bool CODES, typename Get>
 __device__ __forceinline__ Whole join_all(Get get) {
   float4 st[N], lo[N], hi[N];
 #pragma unroll
   for (int q = 0; q < N; ++q) {
-    st[q] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    st[q] = make_float4(-INFINITY, 0.0f, 0.0f, CODES ? -INFINITY : 0.0f);
     lo[q] = hi[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     get(q, st[q], lo[q], hi[q]);
   }
   Whole r = {};
-  r.j.top = -INFINITY;
+  r.j.top = r.j.topo = -INFINITY;
 #pragma unroll
   for (int q = 0; q < N; ++q) {
     r.j.top = fmaxf(r.j.top, st[q].x);
-    r.seen |= st[q].z != 0.0f;
-    r.there |= st[q].w != 0.0f;
+    if (CODES) r.j.topo = fmaxf(r.j.topo, st[q].w);
+    r.seen |= CODES ? st[q].z == kSeen : st[q].z != 0.0f;
+    r.there |= (CODES ? st[q].z : st[q].w) != 0.0f;
   }
-  const float base = r.j.top == -INFINITY ? 0.0f : r.j.top;
+  const float base = r.j.top == -INFINITY ? 0.0f : r.j.top, baseo = r.j.topo == -INFINITY ? 0.0f : r.j.topo;
 #pragma unroll
   for (int q = 0; q < N; ++q) {
-    const float w = ex2(st[q].x - base);
+    const float w = ex2(st[q].x - base), wo = CODES ? ex2(st[q].w - baseo) : w;
     r.j.sum = fmaf(w, st[q].y, r.j.sum);
     const float v[8] = {lo[q].x, lo[q].y, lo[q].z, lo[q].w, hi[q].x, hi[q].y, hi[q].z, hi[q].w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r.j.v[e] = fmaf(w, v[e], r.j.v[e]);
+    for (int e = 0; e < 8; ++e) r.j.v[e] = fmaf(wo, v[e], r.j.v[e]);
   }
   return r;
 }
+// sqrt 2^(topo - top), or 1 where there is no weight at all.
+__device__ __forceinline__ float half_shift(float top, float topo) {
+  return top == -INFINITY || topo == -INFINITY ? 1.0f : ex2(0.5f * (topo - top));
+}
 // Writes the result of a row that saw something (seen) or nothing.
-template <typename T>
+template <typename T, bool CODES>
 __device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d, Joined j, bool seen) {
-  const float w = seen ? 1.0f / j.sum : 0.0f;
+  const float w = seen ? 1.0f / j.sum : 0.0f, half = CODES ? half_shift(j.top, j.topo) : 1.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) j.v[e] *= w;
+  for (int e = 0; e < 8; ++e) j.v[e] = CODES ? shifted(j.v[e] * w, half) : j.v[e] * w;
   store8<T>(a, s, head, d, j.v);
   if (a.p.lse && d == 0) store_lse<T>(a, s, head, seen, j.top, j.sum);
 }
@@ -299,15 +314,19 @@ __device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d
 // for each row.  Which parts a row has follows from the lengths, which are read
 // before the main grid is waited for: that grid is an ordinary launch, so what
 // came before it on the stream is complete.  A CTA's threads take eight outputs each, in groups
-// that walk every kGroups-th part four at a time; the first joins the groups.  The
-// rows of a bundle have a CTA each.
-constexpr int kNarrow = 128, kWide = 1024;
-template <typename T, int DP, int NT, int THREADS>
+// that walk every kGroups-th part some at a time; the first joins the groups.  The
+// rows of a bundle have a CTA each.  Over codes, where a part has one number more,
+// wide CTAs have half the threads (one sequence of 131071: 56.7 us with 6 parts at
+// a time, 57.7 with 4; 1024 threads 57.8 with 2, 59.0 with 4 and spills), and narrow
+// ones take two at a time (40 windows of 4096: 66.1 us, with 4 67.1, with 8 69.3).
+constexpr int kNarrow = 128, kWide = 1024, kWide8 = 512;
+template <typename T, int DP, int NT, int THREADS, bool CODES>
 __global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constant__ AtParams a) {
   constexpr int kCols = 8 * NT, kItems = kCols * DP / 8;
   constexpr int kGroups = THREADS < kItems ? 1 : THREADS / kItems;
   __shared__ int64_t scan[THREADS / 32 + 2];
-  __shared__ float part_sh[kGroups][11][kItems];  // m, l, seen, eight outputs
+  constexpr int kStats = CODES ? 4 : 3, kBatch = !CODES ? 4 : THREADS == kNarrow ? 2 : 6;  // parts at a time
+  __shared__ float part_sh[kGroups][kStats + 8][kItems];  // m, l, seen, mo (CODES); eight outputs
   const fp4_kv_cache &c = a.p.cache;
   const int rows = c.kv_heads * a.groups / a.bundle, index = blockIdx.x / a.bundle, member = blockIdx.x % a.bundle;
   const int slice = index + 1;
@@ -333,14 +352,13 @@ __global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constan
   for (int item = threadIdx.x % kItems; item < kItems; item += THREADS < kItems ? THREADS : kItems) {
     const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
     if (group < kGroups) {
-      float m = -INFINITY, l = 0.0f, any = 0.0f, v[8] = {};
-      constexpr int kBatch = 4;
+      float m = -INFINITY, mo = -INFINITY, l = 0.0f, any = 0.0f, v[8] = {};
       for (int w0 = group; w0 < parts; w0 += kBatch * kGroups) {
         float4 st[kBatch], lo[kBatch], hi[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           const int w = w0 + i * kGroups;
-          st[i] = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+          st[i] = make_float4(-INFINITY, 0.0f, 0.0f, CODES ? -INFINITY : 0.0f);
           lo[i] = hi[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           if (w >= parts) continue;
           const float *slot =
@@ -351,36 +369,58 @@ __global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constan
             hi[i] = *reinterpret_cast<const float4 *>(slot + col * DP + d + 4);
           }
         }
+        if constexpr (CODES) {  // what was joined before moves once for the batch
+          float now = m, nowo = mo;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const float now = fmaxf(m, st[i].x), base = now == -INFINITY ? 0.0f : now;
-          const float fo = ex2(m - base), fn = ex2(st[i].x - base);
+          for (int i = 0; i < kBatch; ++i) now = fmaxf(now, st[i].x), nowo = fmaxf(nowo, st[i].w);
+          const float base = now == -INFINITY ? 0.0f : now, baseo = nowo == -INFINITY ? 0.0f : nowo, fade = ex2(mo - baseo);
+          l *= ex2(m - base);
           m = now;
-          l = l * fo + st[i].y * fn;
-          any = fmaxf(any, st[i].z);
-          const float p[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+          mo = nowo;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = v[e] * fo + p[e] * fn;
+          for (int e = 0; e < 8; ++e) v[e] *= fade;
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const float w = ex2(st[i].w - baseo);
+            l = fmaf(ex2(st[i].x - base), st[i].y, l);
+            any = fmaxf(any, st[i].z);
+            const float p[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(w, p[e], v[e]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const float now = fmaxf(m, st[i].x), base = now == -INFINITY ? 0.0f : now;
+            const float fo = ex2(m - base), fn = ex2(st[i].x - base);
+            m = now;
+            l = l * fo + st[i].y * fn;
+            any = fmaxf(any, st[i].z);
+            const float p[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * fo + p[e] * fn;
+          }
         }
       }
       part_sh[group][0][item] = m;
       part_sh[group][1][item] = l;
       part_sh[group][2][item] = any;
+      if (CODES) part_sh[group][kStats - 1][item] = mo;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) part_sh[group][3 + e][item] = v[e];
+      for (int e = 0; e < 8; ++e) part_sh[group][kStats + e][item] = v[e];
     }
     if (kGroups > 1) __syncthreads();  // (then the loop runs once, for every thread)
     if (group != 0 || col >= heads || d >= c.head_dim) continue;
     bool seen = false;
-    for (int w = 0; w < kGroups; ++w) seen |= part_sh[w][2][item] != 0.0f;
-    const Joined j = join(
+    for (int w = 0; w < kGroups; ++w) seen |= CODES ? part_sh[w][2][item] == kSeen : part_sh[w][2][item] != 0.0f;
+    const Joined j = join<CODES>(
         (1u << kGroups) - 1, [&](int w) { return part_sh[w][0][item]; },
-        [&](int w) { return part_sh[w][1][item]; },
+        [&](int w) { return part_sh[w][kStats - 1][item]; }, [&](int w) { return part_sh[w][1][item]; },
         [&](int w, float fw, float *v) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = fmaf(fw, part_sh[w][3 + e][item], v[e]);
+          for (int e = 0; e < 8; ++e) v[e] = fmaf(fw, part_sh[w][kStats + e][item], v[e]);
         });
-    finish<T>(a, s, head0 + col, d, j, seen);
+    finish<T, CODES>(a, s, head0 + col, d, j, seen);
   }
 }
 

@@ -14,8 +14,10 @@
 // values' scales go into the weights: with s_j the score in base 2 the sum l
 // takes 2^(s_j - m), the product with the codes 2^(s_j + ev_j - mo), each with a
 // running maximum of its own, so whatever the scales are, the terms that make
-// the result are held to full precision; 2^(mo - m) is applied at the end.  Both
-// maxima are moved only when passed by more than 8.  A weight enters its
+// the result are held to full precision; 2^(mo - m), which may pass binary32's
+// exponents where the result does not, is applied at the very end, in two steps,
+// and parts of a row are joined before it.  Both maxima are moved only when
+// passed by more than 8.  A weight enters its
 // product as two f16 parts (2^-22 of it left out, or 2^-32 of the largest).
 //
 // Loads.  Asynchronous 16-byte copies into a ring of shared memory that each
@@ -567,8 +569,9 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
       stage = stage == kStages - 1 ? 0 : stage + 1;
     }
 
-    // the row's outputs relative to m, 2^lift<T>() times, as l: the result, or a
-    // partial row for the join (clusters: in this warp's ring, which is done with)
+    // the row's outputs relative to mo, sums relative to m, both 2^lift<T>() times:
+    // the result, or a partial row for the join (clusters: in this warp's ring,
+    // which is done with)
     const bool whole = mine.ends == 3;
     const int pitch = a.direct ? DP + 8 : DP;
     float *outs = part_of(warp);
@@ -594,7 +597,9 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
         if (col >= heads) continue;
         // (no maximum: nothing seen, or sums that are NaN already)
         if (m[n][e] == kNone) m[n][e] = -INFINITY;
-        float w = m[n][e] == -INFINITY || mo[n][e] == kNone ? 1.0f : ex2(mo[n][e] - m[n][e] - (kLift - lift<T>()));
+        if (mo[n][e] == kNone) mo[n][e] = -INFINITY;
+        float w = exp2f(lift<T>() - kLift);
+        const float half = whole ? half_shift(m[n][e], mo[n][e]) : 1.0f;
         if (whole) w = seen ? w / sum : 0.0f;
 #pragma unroll
         for (int x = 0; x < kWords / 2; ++x) {
@@ -602,8 +607,8 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
           float v[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            v[2 * j] = o[n][4 * x + j][e] * w;
-            v[2 * j + 1] = o[n][4 * x + j][2 + e] * w;
+            v[2 * j] = shifted(o[n][4 * x + j][e] * w, half);
+            v[2 * j + 1] = shifted(o[n][4 * x + j][2 + e] * w, half);
           }
           if (!whole) {
             float4 *to = reinterpret_cast<float4 *>(outs + col * pitch + d);
@@ -615,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
         }
         if (g == 0) {
           if (!whole)
-            stats[col] = make_float4(m[n][e], sum, seen ? 1.0f : 0.0f, 1.0f);
+            stats[col] = make_float4(m[n][e], sum, seen ? kSeen : kThere, mo[n][e]);
           else if (a.p.lse)
             store_lse<T>(a, mine.s, head0 + col, seen, m[n][e], sum);
         }
@@ -637,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
     for (int item = threadIdx.x; item < heads * (DP / 8); item += kThreads) {
       const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
       if (d >= D) continue;
-      const Whole r = join_all<kWarps>([&](int q, float4 &st, float4 &lo, float4 &hi) {
+      const Whole r = join_all<kWarps, true>([&](int q, float4 &st, float4 &lo, float4 &hi) {
         if (!(parts >> q & 1)) return;
         const float *from = part_of(q) + col * (DP + 8) + d;
         st = st_sh[q * kCols + col];
@@ -645,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
         hi = *reinterpret_cast<const float4 *>(from + 4);
       });
       if (a.direct == 1) {
-        finish<T>(a, s, head0 + col, d, r.j, r.seen);
+        finish<T, true>(a, s, head0 + col, d, r.j, r.seen);
         continue;
       }
       const float *v = r.j.v;
@@ -653,26 +658,27 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
       *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
       *reinterpret_cast<float4 *>(out + 4) = make_float4(v[4], v[5], v[6], v[7]);
       if (d == 0)
-        *reinterpret_cast<float4 *>(part + kCols * DP + col * 4) = make_float4(r.j.top, r.j.sum, r.seen ? 1.0f : 0.0f, 1.0f);
+        *reinterpret_cast<float4 *>(part + kCols * DP + col * 4) =
+            make_float4(r.j.top, r.j.sum, r.seen ? kSeen : kThere, r.j.topo);
     }
   if (a.direct < 2) return;
 
   // join the cluster's partial rows, an output piece a thread, in CTA order
   if (!partial)
     for (int i = threadIdx.x; i < slot_floats(kCols, DP); i += kThreads)
-      part[i] = i >= kCols * DP && i % 4 == 0 ? -INFINITY : 0.0f;
+      part[i] = i >= kCols * DP && (i % 4 == 0 || i % 4 == 3) ? -INFINITY : 0.0f;
   cg::this_cluster().sync();
   for (int item = threadIdx.x * a.direct + rank; item < heads * (DP / 8); item += kThreads * a.direct) {
     const int col = item / (DP / 8), d = 8 * (item % (DP / 8));
     if (d >= D) continue;
-    const Whole r = join_all<kCluster>([&](int q, float4 &st, float4 &lo, float4 &hi) {
+    const Whole r = join_all<kCluster, true>([&](int q, float4 &st, float4 &lo, float4 &hi) {
       if (q >= a.direct) return;
       const float *from = cg::this_cluster().map_shared_rank(part, q);
       st = *reinterpret_cast<const float4 *>(from + kCols * DP + col * 4);
       lo = *reinterpret_cast<const float4 *>(from + col * DP + d);
       hi = *reinterpret_cast<const float4 *>(from + col * DP + d + 4);
     });
-    if (r.there) finish<T>(a, s, head0 + col, d, r.j, r.seen);
+    if (r.there) finish<T, true>(a, s, head0 + col, d, r.j, r.seen);
   }
   cg::this_cluster().sync();  // nobody leaves while its part may be read
 }
@@ -741,8 +747,8 @@ fp4_status launch(At8Params b, cudaStream_t s) {
   if (a.ctas < 2) return FP4_OK;
   const cudaError_t e =
       rows * 4 <= (int64_t)a.ctas * a.bundle
-          ? launch_dependent(k_attention_join<T, DP, NT, kWide>, dim3((unsigned)rows), dim3(kWide), 0, s, a)
-          : launch_dependent(k_attention_join<T, DP, NT, kNarrow>, dim3((unsigned)((a.ctas - 1) * a.bundle)), dim3(kNarrow), 0,
+          ? launch_dependent(k_attention_join<T, DP, NT, kWide8, true>, dim3((unsigned)rows), dim3(kWide8), 0, s, a)
+          : launch_dependent(k_attention_join<T, DP, NT, kNarrow, true>, dim3((unsigned)((a.ctas - 1) * a.bundle)), dim3(kNarrow), 0,
                              s, a);
   return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }
