@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(DP, NT))
             }
             if (64 * i + 8 * g < D) store8<T>(a, s, head0 + col, 64 * i + 8 * g, v);
           }
-          if (a.p.lse && g == 0) store_lse<T>(a, s, head0 + col, seen, m[n][e], l[n][e]);
+          if (a.p.lse && g == 0) store_lse<T, false>(a, s, head0 + col, seen, m[n][e], l[n][e]);
         }
       continue;
     }

@@ -223,9 +223,12 @@ __device__ __forceinline__ void store8(const AtParams &a, int s, int head, int d
   }
 }
 
-// log sum exp of a row: m + log2 l in base 2.
-template <typename T>
+// log sum exp of a row: m + log2 l in base 2.  Scores that are all -inf have the
+// sum 0 and give -inf; over codes, which are finite, it is the query that is not,
+// and that is NaN.
+template <typename T, bool CODES>
 __device__ __forceinline__ void store_lse(const AtParams &a, int s, int head, bool seen, float m, float l) {
+  if (CODES && l == 0.0f) l = NAN;
   a.p.lse[(int64_t)s * a.p.heads + head] =
       seen ? ((m == -INFINITY ? 0.0f : m) + log2f(l) - lift<T>()) * 0.693147180559945f : -INFINITY;
 }
@@ -305,7 +308,7 @@ __device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d
 #pragma unroll
   for (int e = 0; e < 8; ++e) j.v[e] = CODES ? shifted(j.v[e] * w, half) : j.v[e] * w;
   store8<T>(a, s, head, d, j.v);
-  if (a.p.lse && d == 0) store_lse<T>(a, s, head, seen, j.top, j.sum);
+  if (a.p.lse && d == 0) store_lse<T, CODES>(a, s, head, seen, j.top, j.sum);
 }
 
 // Joins partial rows.  Many rows are cut into few parts each: narrow CTAs, of

@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
           if (!whole)
             stats[col] = make_float4(m[n][e], sum, seen ? kSeen : kThere, mo[n][e]);
           else if (a.p.lse)
-            store_lse<T>(a, mine.s, head0 + col, seen, m[n][e], sum);
+            store_lse<T, true>(a, mine.s, head0 + col, seen, m[n][e], sum);
         }
       }
   }

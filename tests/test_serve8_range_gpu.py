@@ -1,6 +1,8 @@
 """Attention over a cache in 8 bits where the values' scales lie at the ends of
 E8M0, and so far apart that a result is made of weights that binary32 does not
-hold: tolerances are those of test_serve8_gpu.py."""
+hold, and where queries are infinite: tolerances are those of test_serve8_gpu.py."""
+import math
+
 import pytest
 import torch
 
@@ -72,3 +74,23 @@ def test_large_units_behind_small_weights(n, dtype):
     check_attention(q, cache, table, ints([n]), scale=1.0)
     cache[3][half:] = 0  # the second half next to nothing: the first one's is the result
     check_attention(q, cache, table, ints([n]), scale=1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("lengths,H,Hk", [([1, 0, 5], 4, 2)] + ROWS)
+def test_infinite_queries_over_keys_of_one_sign(lengths, H, Hk, sign, dtype):
+    """Every score of the head is the same infinity: the head and its lse are NaN,
+    whichever it is; the others keep their accuracy (not their bits: a head whose
+    maximum moves takes the warp's others along, an exponential's rounding, which
+    check_attention's tolerance counts)."""
+    cache, table, q, ln = rows_of(lengths, H, Hk, 64, 13)
+    q = q.to(dtype)
+    cache[0].view(torch.uint8)[..., 3] = 0x38
+    q[:, :, 3] = 0.0
+    q[:, 1, 3] = sign * math.inf
+    check_attention(q, cache, table, ln)
+    got, got_lse = fq.decode_attention(q, cache[0], cache[1], table, ln, k_scale=cache[2], v_scale=cache[3], return_lse=True)
+    there = ln > 0
+    assert torch.isnan(got[there, 1]).all() and torch.isnan(got_lse[there, 1]).all()
+    assert not got[~there].any() and (got_lse[~there] == -math.inf).all()
