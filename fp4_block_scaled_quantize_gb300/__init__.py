@@ -69,8 +69,8 @@ EXPORTS = ("fp4_amax", "fp4_amax_many", "fp4_amax_stripes", "fp4_mxfp4_to_fp8",
            "fp4_fp8_gemm", "fp4_dequantize", "fp4_gemm_bf16", "fp4_mma_loop", "fp4_gemm_copies",
            "fp4_matvec", "fp4_kv_append", "fp4_decode_attention",
            "fp4_decode_attention_workspace", "fp4_kv_append8", "fp4_decode_attention8",
-           "fp4_decode_attention8_workspace", "fp4_kv_read", "fp4_page_plan", "fp4_sf_bytes", "fp4_block_size", "fp4_status_sync",
-           "fp4_status_string")
+           "fp4_decode_attention8_workspace", "fp4_kv_read", "fp4_page_plan", "fp4_page_plan_within",
+           "fp4_sf_bytes", "fp4_block_size", "fp4_status_sync", "fp4_status_string")
 
 
 def lib():

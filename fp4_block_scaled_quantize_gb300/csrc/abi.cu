@@ -505,8 +505,10 @@ fp4_status fp4_kv_read(const fp4_read_params *p, void *stream) {
   return launch_kv_read(*p, as_stream(stream));
 }
 
-fp4_status fp4_page_plan(const fp4_plan_params *p, void *stream) {
-  if (!p || p->seqs < 0 || p->seq_pages < 0 || p->page_size < 1 || p->pool_pages < 0 || p->table_stride < 0)
+fp4_status fp4_page_plan(const fp4_plan_params *p, void *stream) { return fp4_page_plan_within(p, INT64_MAX, stream); }
+
+fp4_status fp4_page_plan_within(const fp4_plan_params *p, int64_t max_len, void *stream) {
+  if (!p || max_len < 0 || p->seqs < 0 || p->seq_pages < 0 || p->page_size < 1 || p->pool_pages < 0 || p->table_stride < 0)
     return FP4_ERR_INVALID_ARG;
   if ((int64_t)p->seq_pages * p->page_size > INT32_MAX - 1024 || p->pool_pages > INT32_MAX - 2 ||
       p->tokens > INT32_MAX / 2)
@@ -517,7 +519,7 @@ fp4_status fp4_page_plan(const fp4_plan_params *p, void *stream) {
   if (!aligned4(p->new_tokens) || !aligned4(p->lengths) || !aligned4(p->room) || !aligned4(p->table) ||
       !aligned4(p->pool) || !aligned4(p->offsets) || !aligned4(p->seq) || !aligned4(p->pos) || !aligned_to(p->slot, 8))
     return FP4_ERR_ALIGNMENT;
-  return launch_page_plan(*p, as_stream(stream));
+  return launch_page_plan(*p, max_len, as_stream(stream));
 }
 
 int64_t fp4_decode_attention_workspace(int32_t seqs, int64_t room, int32_t heads,

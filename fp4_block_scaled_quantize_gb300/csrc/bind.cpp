@@ -334,17 +334,18 @@ PyObject *bind_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// plan(new, lengths, page_table, room, pool, page_size, tokens or None)
+// plan(new, lengths, page_table, room, pool, page_size, tokens or None, max_len or None)
 PyObject *bind_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Tensor fresh, lengths, table, room, pool;
-  if (n != 7 || !fresh.read(a[0]) || !lengths.read(a[1]) || !table.read(a[2]) || !room.read(a[3]) || !pool.read(a[4]))
+  if (n != 8 || !fresh.read(a[0]) || !lengths.read(a[1]) || !table.read(a[2]) || !room.read(a[3]) || !pool.read(a[4]))
     return general();
   const long page = PyLong_AsLong(a[5]);
   const long tokens = PyErr_Occurred() ? -1 : a[6] == Py_None ? -1 : PyLong_AsLong(a[6]);
+  const int64_t most = PyErr_Occurred() ? -1 : a[7] == Py_None ? INT64_MAX : PyLong_AsLong(a[7]);
   if (PyErr_Occurred()) return general();
   if (table.type != c10::kInt || table.dims != 2 || !table.rows_whole() || table.size[0] > INT32_MAX ||
-      table.size[1] > INT32_MAX || page < 1 || page > INT32_MAX || (a[6] != Py_None && tokens < 0))
+      table.size[1] > INT32_MAX || page < 1 || page > INT32_MAX || (a[6] != Py_None && tokens < 0) || most < 0)
     return general();
   const int64_t S = table.size[0];
   if (!fresh.ints(S) || !lengths.ints(S) || !room.ints(S) || pool.dims != 1 || !pool.ints(pool.size[0]) ||
@@ -363,12 +364,12 @@ PyObject *bind_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
   p.tokens = tokens;
   p.seqs = static_cast<int32_t>(S), p.seq_pages = static_cast<int32_t>(table.size[1]);
   p.page_size = static_cast<int32_t>(page);
-  if (tokens < 0) return finish(fp4_page_plan(&p, stream), "fp4_page_plan", at::Tensor());
+  if (tokens < 0) return finish(fp4_page_plan_within(&p, most, stream), "fp4_page_plan", at::Tensor());
   const at::Tensor made[4] = {make(table, c10::kInt, {tokens}), make(table, c10::kInt, {tokens}),
                               make(table, c10::kLong, {tokens}), make(table, c10::kInt, {S + 1})};
   p.seq = static_cast<int32_t *>(made[0].data_ptr()), p.pos = static_cast<int32_t *>(made[1].data_ptr());
   p.slot = static_cast<int64_t *>(made[2].data_ptr()), p.offsets = static_cast<int32_t *>(made[3].data_ptr());
-  return finish_all(fp4_page_plan(&p, stream), "fp4_page_plan", made, 4);
+  return finish_all(fp4_page_plan_within(&p, most, stream), "fp4_page_plan", made, 4);
   END_HANDLE_TH_ERRORS
 }
 

@@ -206,7 +206,7 @@ fp4_status launch_decode_attention(const fp4_attention_params &p, cudaStream_t s
 fp4_status launch_kv_append8(const fp4_append8_params &p, cudaStream_t s);
 fp4_status launch_kv_read(const fp4_read_params &p, cudaStream_t s);
 fp4_status launch_decode_attention8(const fp4_attention8_params &p, cudaStream_t s);
-fp4_status launch_page_plan(const fp4_plan_params &p, cudaStream_t s);
+fp4_status launch_page_plan(const fp4_plan_params &p, int64_t max_len, cudaStream_t s);
 // Bytes of partial results launch_decode_attention may write.
 int64_t decode_attention_workspace(int64_t seqs, int64_t room, int heads, int kv_heads, int head_dim);
 int64_t decode_attention8_workspace(int64_t seqs, int64_t room, int heads, int kv_heads, int head_dim);

@@ -36,6 +36,7 @@ struct PlanParams {
   fp4_plan_params p;
   Divisor page;
   int limit;  // positions that a row of the table can name
+  int most;   // that a sequence may grow to
   bool wide;  // maps allow stores of whole groups of tokens
   uint32_t *status;
 };
@@ -57,7 +58,7 @@ __device__ __forceinline__ Change change_of(const PlanParams &a, int n, int leng
   Change c;
   c.n = n, c.length = length, c.held = held;
   c.after = max((int64_t)length + n, (int64_t)0);
-  c.fits = c.after <= a.limit && (a.p.tokens < 0 || first + max(n, 0) <= a.p.tokens);
+  c.fits = c.after <= (n > 0 ? a.most : a.limit) && (a.p.tokens < 0 || first + max(n, 0) <= a.p.tokens);
   c.want = c.after > a.limit ? a.p.seq_pages : c.after > 0 ? over((int)c.after - 1, a.page) + 1 : 0;
   return c;
 }
@@ -364,11 +365,12 @@ __global__ void __launch_bounds__(kThreads) k_plan(const __grid_constant__ PlanP
 
 }  // namespace
 
-fp4_status launch_page_plan(const fp4_plan_params &p, cudaStream_t s) {
+fp4_status launch_page_plan(const fp4_plan_params &p, int64_t max_len, cudaStream_t s) {
   PlanParams a{};
   a.p = p;
   a.page = divisor(p.page_size);
   a.limit = p.seq_pages * p.page_size;
+  a.most = max_len < a.limit ? (int)max_len : a.limit;
   a.wide = p.seq && p.pos && p.slot && aligned16(p.seq) && aligned16(p.pos) && aligned16(p.slot);
   a.status = status_word();
   if (!a.status) return FP4_ERR_CUDA;

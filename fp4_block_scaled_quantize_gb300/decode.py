@@ -99,16 +99,19 @@ class PagedCache:
     def plan(self, new, tokens=None):
         """On the device: new [seqs] int32 tokens more (or, negative, fewer) of
         each sequence, with the pages that takes or frees; lengths, room and
-        table are brought up to date (see page_plan).  With tokens returns the
-        Plan of a batch of that size, whose seq and pos prefill takes."""
+        table are brought up to date (see page_plan).  A sequence for which there
+        are too few pages, or that would grow past max_len, stays as it is.  With
+        tokens returns the Plan of a batch of that size, whose seq and pos prefill
+        takes."""
         if self.pool is None:
             raise ValueError("PagedCache.plan: the pages of this cache are handed out on the host (on_device=True)")
-        return page_plan(new, self.lengths, self.table, self.room, self.pool, self.page_size, tokens)
+        return page_plan(new, self.lengths, self.table, self.room, self.pool, self.page_size, tokens,
+                         max_len=self.max_len)
 
     def step(self, new=None):
         """One token more of each sequence, or of those with new [seqs] int32 1
         (0: none): positions [seqs] for the layer's forward, -1 where there is
-        no token or no page for it."""
+        no token, no page for it, or where it would be past max_len."""
         before = self.lengths.clone()
         self.plan(torch.ones_like(before) if new is None else new)
         return torch.where(self.lengths > before, before, -1)

@@ -117,8 +117,9 @@ def _lib():
         L.fp4_decode_attention8_workspace.argtypes = [i32, i64, i32, i32, i32]
         for f in ("fp4_kv_append8", "fp4_decode_attention8", "fp4_kv_read", "fp4_page_plan"):
             getattr(L, f).argtypes = [vp, vp]
+        L.fp4_page_plan_within.argtypes = [vp, i64, vp]
         for f in ("fp4_matvec", "fp4_kv_append", "fp4_decode_attention", "fp4_kv_append8",
-                  "fp4_decode_attention8", "fp4_kv_read", "fp4_page_plan"):
+                  "fp4_decode_attention8", "fp4_kv_read", "fp4_page_plan", "fp4_page_plan_within"):
             getattr(L, f).restype = i32
         L.fp4_decode_attention_workspace.restype = L.fp4_decode_attention8_workspace.restype = i64
         _entry = L
@@ -188,6 +189,11 @@ def fp4_kv_read(p, stream=None):
 def fp4_page_plan(p, stream=None):
     """p: an fp4_plan_params, or the same bytes packed."""
     return _call("fp4_page_plan", p, stream)
+
+
+def fp4_page_plan_within(p, max_len, stream=None):
+    """p: an fp4_plan_params, or the same bytes packed."""
+    return _lib().fp4_page_plan_within(p if isinstance(p, bytes) else ctypes.byref(p), max_len, _stream(stream))
 
 
 # ------------------------------------------------------ allocating conveniences
@@ -489,7 +495,7 @@ def page_pool(pages, device="cuda"):
 Plan = namedtuple("Plan", "seq pos slot offsets")
 
 
-def page_plan(new, lengths, page_table, room, pool, page_size, tokens=None, stream=None):
+def page_plan(new, lengths, page_table, room, pool, page_size, tokens=None, stream=None, max_len=None):
     """Pages and places for new tokens, worked out on the GPU: new [seqs] int32
     tokens more (or, negative, fewer) of each sequence, whose state is lengths
     [seqs] (positions held), room [seqs] (positions its pages hold), page_table
@@ -499,10 +505,11 @@ def page_plan(new, lengths, page_table, room, pool, page_size, tokens=None, stre
     (int32) and place page * page_size + place (int64) of each new token, -1
     behind the last, and offsets [seqs + 1] int32 of the sequences in the batch;
     kv_append takes seq and pos as they are.  A sequence that cannot have its
-    pages or places stays as it is, its tokens have position -1, and
+    pages or places, or that would grow past max_len positions (default: what its
+    row of page_table can name), stays as it is, its tokens have position -1, and
     fp4_status_sync reports FP4_ERR_INVALID_ARG."""
     if stream is None:
-        r = _bind().plan(new, lengths, page_table, room, pool, page_size, tokens)
+        r = _bind().plan(new, lengths, page_table, room, pool, page_size, tokens, max_len)
         if r is not NotImplemented:
             return r if r is None else Plan(*r)
     where = "page_plan"
@@ -519,16 +526,19 @@ def page_plan(new, lengths, page_table, room, pool, page_size, tokens=None, stre
     _need_ints(where, "pool", pool, pool.shape[0])
     if page_size < 1 or page_size > 0x7FFFFFFF or (tokens is not None and tokens < 0):
         raise ValueError(f"{where}: page_size must be positive, tokens not negative")
+    if max_len is not None and max_len < 0:
+        raise ValueError(f"{where}: max_len must not be negative")
     dev = _device(where, page_table, new, lengths, room, pool)
     made = None
     if tokens is not None:
         sizes = ((tokens, _INT), (tokens, _INT), (tokens, torch.int64), (seqs + 1, _INT))
         made = Plan(*(_new((n,), dtype, pool.device, stream) for n, dtype in sizes))
     seq, pos, slot, offsets = (0,) * 4 if made is None else (t.data_ptr() for t in made)
-    code = _lib().fp4_page_plan(
+    code = _lib().fp4_page_plan_within(
         _PLAN.pack(new.data_ptr(), lengths.data_ptr(), room.data_ptr(), page_table.data_ptr(),
                    step if seqs > 1 else 0, pool.data_ptr(), pool.shape[0] - 2, offsets, seq, pos, slot,
-                   -1 if tokens is None else tokens, seqs, wide, page_size), _handle(stream, dev))
+                   -1 if tokens is None else tokens, seqs, wide, page_size),
+        0x7FFFFFFFFFFFFFFF if max_len is None else max_len, _handle(stream, dev))
     if code:
         raise FP4Error(code, "fp4_page_plan")
     return made
@@ -610,6 +620,6 @@ __all__ = ["FP4_BF16", "FP4_F16", "FP4_F32", "Plan", "fp4_append8_params", "fp4_
            "fp4_attention8_params", "fp4_attention_params", "fp4_decode_attention",
            "fp4_decode_attention8", "fp4_decode_attention8_workspace",
            "fp4_decode_attention_workspace", "fp4_kv_append", "fp4_kv_append8", "fp4_kv_cache",
-           "fp4_kv_read", "fp4_kv_scales", "fp4_matvec", "fp4_page_plan", "fp4_plan_params",
+           "fp4_kv_read", "fp4_kv_scales", "fp4_matvec", "fp4_page_plan", "fp4_page_plan_within", "fp4_plan_params",
            "fp4_read_params", "decode_attention", "kv_append", "kv_read", "matvec", "page_plan",
            "page_pool", "rope_table"]

@@ -581,6 +581,11 @@ typedef struct {
 } fp4_plan_params;
 fp4_status fp4_page_plan(const fp4_plan_params *p, void *stream);
 
+/* The same for sequences of at most max_len positions, where that is less than
+ * their rows of the table can name: a sequence whose new tokens would pass it
+ * gets none, as above. */
+fp4_status fp4_page_plan_within(const fp4_plan_params *p, int64_t max_len, void *stream);
+
 /* Bytes of one scale-factor output for a copy with `rows` rows and `cols`
  * elements per row; -1 for an invalid format/layout. */
 int64_t fp4_sf_bytes(int32_t format, int64_t rows, int64_t cols,
