@@ -12,8 +12,8 @@
 // scale) for a few tokens.
 //
 // Measured in a graph: 192 tokens of 192 sequences, 16 + 2 x 16 heads of 64 in
-// blocks of 8 4.0 us, one token 3.6; 8191 prompt tokens of 32 + 2 x 8 heads of 128
-// in blocks of 64 50.5 us (3.7 TB/s, 54% of a copy's rate; without queries 27: some
+// blocks of 8 4.1 us, one token 3.6; 8191 prompt tokens of 32 + 2 x 8 heads of 128
+// in blocks of 64 51.1 us (3.6 TB/s, 54% of a copy's rate; without queries 27: some
 // 700 instructions of a warp a head and 64 tokens, 16 warps an SM); reading 100003
 // tokens back 97.5 us (6.3 TB/s, 93%), 300 2.1 us.
 //
@@ -21,6 +21,14 @@
 // code in a million is the other neighbour of a number that lies within 2^-20 of
 // the middle of two.  Rotations whose binary32 result is rounded to odd wherever a
 // middle is near have none of these, and took 59.8 us for 50.8.
+//
+// Order.  A block whose tokens stand apart in the call would be written by teams
+// that know nothing of each other.  CTAs of their own look for that and report it:
+// of each 256 tokens those that go on with a block without the token before them
+// (none in whole prompts) into a table in shared memory, which every token of the
+// call is then looked up in, beside the work of the others.  They come first in the
+// grid: 8191 prompt tokens 51.1 us (50.5 without, 51.6 last), 8000 single tokens
+// 57.5 (56.5, 67.6), 192 of them 4.4 (4.35).
 //
 // Layout.  Lanes hold units of 16 elements (two pieces of 8, in the rotated part
 // those whose elements form pairs) of 32 / units rows; a team of warps takes the
@@ -44,7 +52,9 @@ struct Ap8Params {
   int window;    // tokens that a team looks at together
   int chunks;    // parts of the heads, each a team's
   Divisor page, block;
-  int kv_ctas;   // CTAs for keys and values; further ones for queries
+  int kv_ctas;   // CTAs for keys and values; further ones for queries: `ctas` of both
+  int ctas;
+  int checks;    // CTAs before those, for the order of the tokens
   uint32_t *status;
 };
 
@@ -455,6 +465,63 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
   }
 }
 
+// Whether tokens of one block stand apart.  Any two runs of a block have one that
+// begins inside it: for each of those, is there a token of its block that is not
+// part of the run?  (a token of the same distance in position and index behind it
+// is, or is behind a run of its own)
+constexpr int kSlots = 4 * kThreads;
+__device__ __forceinline__ void check_order(const Ap8Params &a, int cta) {
+  const fp4_append_params &p = a.p;
+  const fp4_kv_cache &c = p.cache;
+  __shared__ int4 begun[kThreads];  // sequence, first position of the block, position - index, index
+  __shared__ int slot[kSlots];      // which of those, by a hash of the first two; -1: none
+  const int block = a.s.block, tokens = (int)p.tokens;
+  auto hash = [](int seq, int first) {
+    return (int)(((uint32_t)seq * 0x9E3779B1u + (uint32_t)first * 0x85EBCA77u) >> 22) & (kSlots - 1);
+  };
+  bool apart = false;
+  for (int base = cta * kThreads; base < tokens; base += a.checks * kThreads) {
+    const int t = base + threadIdx.x;
+    int4 mine = make_int4(0, 0, 0, t);
+    bool inside = false;
+    if (t < tokens) {
+      const int pos = p.pos[t], seq = p.seq[t];
+      const int first = over(max(pos, 0), a.block) * block;
+      inside = pos > first && seq >= 0 && seq < c.seqs && pos < c.seq_pages * c.page_size &&
+               !(t > 0 && p.seq[t - 1] == seq && p.pos[t - 1] == pos - 1);
+      mine = make_int4(seq, first, pos - t, t);
+    }
+    if (!__syncthreads_or(inside)) continue;
+    for (int i = threadIdx.x; i < kSlots; i += kThreads) slot[i] = -1;
+    begun[threadIdx.x] = mine;
+    __syncthreads();
+    if (inside)  // (a slot in four is taken at most, so there is a free one)
+      for (int h = hash(mine.x, mine.y);; h = (h + 1) & (kSlots - 1)) {
+        const int other = atomicCAS(&slot[h], -1, threadIdx.x);
+        if (other < 0) break;
+        if (begun[other].x == mine.x && begun[other].y == mine.y) {
+          apart = true;
+          break;
+        }
+      }
+    __syncthreads();
+#pragma unroll 4
+    for (int j = threadIdx.x; j < tokens; j += kThreads) {
+      const int pos = p.pos[j], seq = p.seq[j];
+      if (pos < 0) continue;
+      const int first = over(pos, a.block) * block;
+      for (int h = hash(seq, first), i; (i = slot[h]) >= 0; h = (h + 1) & (kSlots - 1)) {
+        const int4 e = begun[i];
+        if (e.x != seq || e.y != first) continue;
+        apart |= j < e.w || pos - j != e.z;
+        break;
+      }
+    }
+    __syncthreads();
+  }
+  if (__syncthreads_or(apart) && threadIdx.x == 0) raise_status(a.status, kStatusIndex);
+}
+
 // Queries: a warp takes up to 4 * (32 / units) heads of a token at a time.
 constexpr int kBatch = 4;
 template <typename T, int KIND>
@@ -466,7 +533,7 @@ __device__ __forceinline__ void turn_queries(const Ap8Params &a, int cta) {
   const int64_t limit = p.rot_dim ? p.rope_len : INT64_MAX;
   const int parts = (p.heads + kBatch * rows - 1) / (kBatch * rows);
   const Unit u = unit_at<KIND>(p, my_unit);
-  const int64_t ctas = gridDim.x - a.kv_ctas;
+  const int64_t ctas = a.ctas - a.kv_ctas;
   for (int64_t item = (int64_t)cta * kWarps + (threadIdx.x >> 5); item < p.tokens * parts;
        item += ctas * kWarps) {
     const int64_t t = item / parts;
@@ -529,12 +596,17 @@ template <typename T, int KIND, int HOLD>
 __global__ void __launch_bounds__(kThreads, kResident) k_append8(const __grid_constant__ Ap8Params a) {
   dependent_wait();
   launch_dependents();
+  const int cta = (int)blockIdx.x - a.checks;
+  if (cta < 0) {
+    check_order(a, blockIdx.x);
+    return;
+  }
   // CTAs for keys and values, and for queries, in turn
-  const int before = (int)((int64_t)blockIdx.x * a.kv_ctas / gridDim.x);
-  if (before != (int)(((int64_t)blockIdx.x + 1) * a.kv_ctas / gridDim.x))
+  const int before = (int)((int64_t)cta * a.kv_ctas / a.ctas);
+  if (before != (int)(((int64_t)cta + 1) * a.kv_ctas / a.ctas))
     store_blocks<T, KIND, HOLD>(a, before);
   else
-    turn_queries<T, KIND>(a, blockIdx.x - before);
+    turn_queries<T, KIND>(a, cta - before);
 }
 
 bool whole8(const void *ptr, int64_t s0, int64_t s1) { return aligned16(ptr) && s0 % 8 == 0 && s1 % 8 == 0; }
@@ -571,7 +643,11 @@ fp4_status launch_append(Ap8Params &a, cudaStream_t s) {
   const int64_t kv = ceil_div(ceil_div(p.tokens, a.window) * a.chunks * a.team, kWarps);
   a.kv_ctas = (int)(kv < grid_most ? kv : grid_most);
   const int64_t qn = p.q ? ceil_div(p.tokens * ceil_div(p.heads, kBatch * rows), kWarps) : 0;
-  const unsigned grid = (unsigned)(a.kv_ctas + (qn < grid_most ? qn : grid_most));
+  a.ctas = a.kv_ctas + (int)(qn < grid_most ? qn : grid_most);
+  // (without seq every token has a sequence, and so a block, of its own)
+  const int64_t looks = p.seq && a.s.block > 1 && p.tokens > 1 ? ceil_div(p.tokens, kThreads) : 0;
+  a.checks = (int)(looks < most ? looks : most);
+  const unsigned grid = (unsigned)(a.checks + a.ctas);
   const auto kern = !whole          ? k_append8<T, kAny, 1>
                     : p.interleaved ? (two ? k_append8<T, kPairs, 2> : k_append8<T, kPairs, 1>)
                     : two           ? k_append8<T, kHalves, 2>

@@ -389,8 +389,10 @@ def kv_append(k, v, k_pages, v_pages, page_table, pos, seq=None, q=None, rope=No
     block of places and head.  Values are rounded once, to the codes; where a
     new token needs a larger scale the block's earlier codes are rounded anew,
     and a call that writes a block's first place begins it (see fp4_kv_append8
-    in include/fp4.h).  A call's tokens of one block stand side by side, in the
-    order of their positions."""
+    in include/fp4.h).  Unlike in 16 bits, a call's tokens of one block stand side
+    by side, in the order of their positions (as page_plan lays them out);
+    where they do not, what the block holds means nothing and fp4_status_sync
+    reports FP4_ERR_INVALID_ARG."""
     if stream is None and q_out is None:
         r = _bind().append(k, v, k_pages, v_pages, page_table, pos, seq, q, rope, interleaved, k_scale, v_scale)
         if r is not NotImplemented:

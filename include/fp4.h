@@ -499,8 +499,10 @@ typedef struct {
  * the new unit).  What the other places of a block hold that a call begins
  * means nothing afterwards.  Scales only rise within a block.
  * The tokens of one call that go into one block stand side by side, at
- * consecutive positions; where they do not, or a place comes twice, what the
- * block holds afterwards is unspecified.
+ * consecutive positions (as fp4_page_plan lays them out); where they stand apart
+ * or in another order, what the block holds afterwards is unspecified, and
+ * fp4_status_sync reports FP4_ERR_INVALID_ARG.  So it is where a place comes
+ * twice, which is reported unless it is a block's first.
  * Shapes as fp4_kv_append, head_dim % 16 == 0. */
 typedef struct {
   fp4_append_params base;
