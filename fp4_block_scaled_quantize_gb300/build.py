@@ -39,6 +39,7 @@ UNITS = {
     "matvec.cu": [],
     "append.cu": [],
     "attention.cu": [],
+    "attention_sinks.cu": [],
     "attention8.cu": [],
     "append8.cu": [],
     "plan.cu": [],

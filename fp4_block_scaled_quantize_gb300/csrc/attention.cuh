@@ -1,5 +1,5 @@
 // attention.cuh -- what the attention kernels over a paged cache share
-// (attention.cu: keys and values of 16 bits, attention8.cu: of 8): which
+// (attention16.cuh: keys and values of 16 bits, attention8.cu: of 8): which
 // positions are seen, the list of tiles that warps share out, the tensor-core
 // and packing helpers, and the joins of partial rows.
 #pragma once
@@ -113,7 +113,7 @@ __device__ __forceinline__ float2 unpack<__half>(uint32_t w) {
 }
 
 // What of a sequence is seen: positions [0, sinks) and [from, len), apart from
-// each other (sinks is 0 where they meet).  Its tiles are those of the first
+// each other (sinks is 0 where they meet, and without SINKS).  Its tiles are those of the first
 // positions, then those of the others, which start at base.
 struct Span {
   int from, len, base, sinks, first, tiles;  // first: tiles of the first positions
@@ -125,6 +125,7 @@ struct Span {
     return early ? i * tile : base + (i - first) * tile;
   }
 };
+template <bool SINKS>
 __device__ __forceinline__ Span span_of(const AtParams &a, int s) {
   const fp4_kv_cache &c = a.p.cache;
   const int64_t room = (int64_t)c.seq_pages * c.page_size;  // fits 32 bits
@@ -132,10 +133,10 @@ __device__ __forceinline__ Span span_of(const AtParams &a, int s) {
   Span r;
   r.len = given < 0 ? 0 : given > room ? (int)room : given;
   r.from = a.p.window && r.len > a.p.window ? r.len - a.p.window : 0;
-  r.sinks = a.p.sinks;
-  if (r.from <= r.sinks) r.from = r.sinks = 0;
+  r.sinks = SINKS ? a.p.sinks : 0;
+  if (SINKS && r.from <= r.sinks) r.from = r.sinks = 0;
   r.base = r.from & ~15;
-  r.first = (r.sinks + a.tile - 1) / a.tile;
+  r.first = SINKS ? (r.sinks + a.tile - 1) / a.tile : 0;
   r.tiles = r.first + (r.len - r.base + a.tile - 1) / a.tile;
   return r;
 }
@@ -147,13 +148,13 @@ struct Found {
   int64_t ctas;          // slices that share the list
   int seq;
 };
-template <int THREADS>
+template <int THREADS, bool SINKS>
 __device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *shared, int which = -1) {
   constexpr int kW = THREADS / 32;
   const int seqs = a.p.cache.seqs, per = (seqs + THREADS - 1) / THREADS;
   if (seqs <= 32) {  // each warp by itself
     const int lane = threadIdx.x & 31;
-    const int64_t sum = lane < seqs ? (int64_t)rows * span_of(a, lane).tiles : 0;
+    const int64_t sum = lane < seqs ? (int64_t)rows * span_of<SINKS>(a, lane).tiles : 0;
     int64_t inc = sum;
     for (int o = 1; o < seqs; o <<= 1) {
       const int64_t v = __shfl_up_sync(~0u, inc, o);
@@ -171,7 +172,7 @@ __device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *share
   const int s0 = threadIdx.x * per, s1 = min(s0 + per, seqs);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t sum = 0;
-  for (int s = s0; s < s1; ++s) sum += (int64_t)rows * span_of(a, s).tiles;
+  for (int s = s0; s < s1; ++s) sum += (int64_t)rows * span_of<SINKS>(a, s).tiles;
   int64_t inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -191,7 +192,7 @@ __device__ Found find(const AtParams &a, int rows, int64_t slice, int64_t *share
   if (which < 0 ? x >= before && x < before + sum : which >= s0 && which < s1) {  // one thread, if any
     int64_t at = before;
     for (int s = s0;; ++s) {
-      const int64_t n = (int64_t)rows * span_of(a, s).tiles;
+      const int64_t n = (int64_t)rows * span_of<SINKS>(a, s).tiles;
       if (which < 0 ? x < at + n : s == which) {
         shared[kW] = s;
         shared[kW + 1] = at;
@@ -323,7 +324,7 @@ __device__ __forceinline__ void finish(const AtParams &a, int s, int head, int d
 // a time, 57.7 with 4; 1024 threads 57.8 with 2, 59.0 with 4 and spills), and narrow
 // ones take two at a time (40 windows of 4096: 66.1 us, with 4 67.1, with 8 69.3).
 constexpr int kNarrow = 128, kWide = 1024, kWide8 = 512;
-template <typename T, int DP, int NT, int THREADS, bool CODES>
+template <typename T, int DP, int NT, int THREADS, bool SINKS, bool CODES>
 __global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constant__ AtParams a) {
   constexpr int kCols = 8 * NT, kItems = kCols * DP / 8;
   constexpr int kGroups = THREADS < kItems ? 1 : THREADS / kItems;
@@ -331,13 +332,14 @@ __global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constan
   constexpr int kStats = CODES ? 4 : 3, kBatch = !CODES ? 4 : THREADS == kNarrow ? 2 : 6;  // parts at a time
   __shared__ float part_sh[kGroups][kStats + 8][kItems];  // m, l, seen, mo (CODES); eight outputs
   const fp4_kv_cache &c = a.p.cache;
-  const int rows = c.kv_heads * a.groups / a.bundle, index = blockIdx.x / a.bundle, member = blockIdx.x % a.bundle;
+  const int bundle = CODES ? a.bundle : 1;
+  const int rows = c.kv_heads * a.groups / bundle, index = blockIdx.x / bundle, member = blockIdx.x % bundle;
   const int slice = index + 1;
-  const Found f = THREADS == kNarrow ? find<THREADS>(a, rows, slice, scan)
-                                     : find<THREADS>(a, rows, 0, scan, index / rows);
+  const Found f = THREADS == kNarrow ? find<THREADS, SINKS>(a, rows, slice, scan)
+                                     : find<THREADS, SINKS>(a, rows, 0, scan, index / rows);
   int s = f.seq, row = 0, first = 0, parts = 1;
-  if (s < c.seqs && span_of(a, s).tiles) {
-    const int tiles = span_of(a, s).tiles;
+  if (s < c.seqs && span_of<SINKS>(a, s).tiles) {
+    const int tiles = span_of<SINKS>(a, s).tiles;
     const int64_t at = f.total * slice / f.ctas;  // narrow: list index where the slice begins
     row = THREADS == kNarrow ? (int)((at - f.start) / tiles) : index - s * rows;
     const int64_t begin = f.start + (int64_t)row * tiles;
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constan
   dependent_wait();  // also where there is nothing to do: this grid ends after the main one
   launch_dependents();
   if (parts == 1) return;
-  row = row * a.bundle + member;
+  row = row * bundle + member;
   const int kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
   const int heads = min(kCols, (kvh + 1) * a.share - head0);
   const int group = THREADS < kItems ? 0 : threadIdx.x / kItems;
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(THREADS) k_attention_join(const __grid_constan
           lo[i] = hi[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           if (w >= parts) continue;
           const float *slot =
-              a.ws + (((int64_t)(first + w) * 2 + (w == 0)) * a.bundle + member) * slot_floats(kCols, DP);
+              a.ws + (((int64_t)(first + w) * 2 + (w == 0)) * bundle + member) * slot_floats(kCols, DP);
           if (col < heads && d < c.head_dim) {  // what was written
             st[i] = *reinterpret_cast<const float4 *>(slot + kCols * DP + col * 4);
             lo[i] = *reinterpret_cast<const float4 *>(slot + col * DP + d);

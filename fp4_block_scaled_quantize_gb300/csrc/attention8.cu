@@ -24,7 +24,7 @@
 // warp fills for itself, kStages - 1 tiles ahead, across the rows of its slice;
 // scales are requested with the copies and put beside them a step later.
 //
-// Split.  Short rows go to clusters, as in attention.cu.  Otherwise the warps of
+// Split.  Short rows go to clusters, as in attention16.cuh.  Otherwise the warps of
 // the resident CTAs share the list of all tiles out evenly; warps of a CTA take
 // `bundle` (4, 2 or 1) neighbouring key heads over the same positions.  In a page
 // with heads innermost a head's row of 128 bytes lies between others': copies
@@ -40,7 +40,7 @@
 // sequences of 16384) 430 us for 317 at a copy's rate: as many instructions a
 // position as heads of 128, half the bytes; of 256 334.
 //
-// Layout is that of attention.cu:
+// Layout is that of attention16.cuh:
 //   S^T = K Q^T   lane (g, t) reads pieces 64 i + 16 t of keys g, g + 8
 //   O^T = V^T P^T lane (g, t) reads pieces 128 i + 16 g (or 8 g) of values
 //                 2 t, 2 t + 1, 2 t + 8, 2 t + 9
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
   if (a.direct) {
     s = mine_row / rows;
     start = 0;
-    const int tiles = span_of(a, s).tiles;
+    const int tiles = span_of<true>(a, s).tiles;
     at = (int64_t)(mine_row - s * rows) * tiles;
     end = at + (int64_t)tiles * (rank + 1) / a.direct;
     at += (int64_t)tiles * rank / a.direct;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
     // warps of a bundle share a slice
     const int subs = kWarps / a.bundle;
     const int64_t first = (int64_t)blockIdx.x * subs, slice = first + warp / a.bundle;
-    const Found f = find<kThreads>(a, rows, first, scan);
+    const Found f = find<kThreads, true>(a, rows, first, scan);
     s = f.seq;
     start = f.start;
     at = end = 0;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
     if (a.direct && (rank || mine_row != s * rows)) break;
     if (threadIdx.x == 0 && (given < 0 || given > (int64_t)c.seq_pages * c.page_size))
       raise_status(a.status, kStatusIndex);
-    if (span_of(a, e).tiles) continue;
+    if (span_of<true>(a, e).tiles) continue;
     const float zero[8] = {};
     for (int i = threadIdx.x; i < a.p.heads * (D / 8); i += kThreads) {
       const int head = i / (D / 8), d = 8 * (i % (D / 8));
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
   // the loop makes loads in flight be waited for: 64 sequences of up to 16384 took
   // 233 us for 173).
   bool live = at < end, bad = false;
-  Span sp = live ? span_of(a, s) : Span{};
+  Span sp = live ? span_of<true>(a, s) : Span{};
   int tile = 0, tile1 = 0, pos = 0, entered = 0;
   const int32_t *table = c.table;
   const char *keys = nullptr, *values = nullptr;
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
     if (!live) return;
     while (at >= start + (int64_t)rows * sp.tiles) {
       start += (int64_t)rows * sp.tiles;
-      sp = span_of(a, ++s);
+      sp = span_of<true>(a, ++s);
     }
     const int item = (int)((at - start) / sp.tiles), row = item * a.bundle + warp % a.bundle, kvh = row / a.groups;
     tile = (int)(at - start - (int64_t)item * sp.tiles);
@@ -742,13 +742,13 @@ fp4_status launch(At8Params b, cudaStream_t s) {
                ? FP4_OK
                : FP4_ERR_CUDA;
   }
-  kern<<<(unsigned)grid, kThreads, smem, s>>>(b);  // (an ordinary launch, as in attention.cu)
+  kern<<<(unsigned)grid, kThreads, smem, s>>>(b);  // (an ordinary launch, as in attention16.cuh)
   if (cudaGetLastError() != cudaSuccess) return FP4_ERR_CUDA;
   if (a.ctas < 2) return FP4_OK;
   const cudaError_t e =
       rows * 4 <= (int64_t)a.ctas * a.bundle
-          ? launch_dependent(k_attention_join<T, DP, NT, kWide8, true>, dim3((unsigned)rows), dim3(kWide8), 0, s, a)
-          : launch_dependent(k_attention_join<T, DP, NT, kNarrow, true>, dim3((unsigned)((a.ctas - 1) * a.bundle)), dim3(kNarrow), 0,
+          ? launch_dependent(k_attention_join<T, DP, NT, kWide8, true, true>, dim3((unsigned)rows), dim3(kWide8), 0, s, a)
+          : launch_dependent(k_attention_join<T, DP, NT, kNarrow, true, true>, dim3((unsigned)((a.ctas - 1) * a.bundle)), dim3(kNarrow), 0,
                              s, a);
   return e == cudaSuccess ? FP4_OK : FP4_ERR_CUDA;
 }

@@ -203,6 +203,7 @@ struct MatvecJob {
 fp4_status launch_matvec(const MatvecJob &j, cudaStream_t s);
 fp4_status launch_kv_append(const fp4_append_params &p, cudaStream_t s);
 fp4_status launch_decode_attention(const fp4_attention_params &p, cudaStream_t s);
+fp4_status launch_decode_attention_sinks(const fp4_attention_params &p, cudaStream_t s);
 fp4_status launch_kv_append8(const fp4_append8_params &p, cudaStream_t s);
 fp4_status launch_kv_read(const fp4_read_params &p, cudaStream_t s);
 fp4_status launch_decode_attention8(const fp4_attention8_params &p, cudaStream_t s);

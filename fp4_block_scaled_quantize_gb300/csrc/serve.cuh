@@ -1,4 +1,4 @@
-// serve.cuh -- what the serving kernels (matvec.cu, append.cu, attention.cu)
+// serve.cuh -- what the serving kernels (matvec.cu, append.cu, attention16.cuh)
 // share: 16-bit element types, conversions and launch geometry.
 #pragma once
 #include <cuda_bf16.h>
