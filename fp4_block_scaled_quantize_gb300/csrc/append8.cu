@@ -75,33 +75,6 @@ __device__ __forceinline__ bool locate8(const fp4_kv_cache &c, const Divisor &by
   return ok;
 }
 
-template <typename T>
-struct Two;
-template <>
-struct Two<__nv_bfloat16> {
-  static __device__ __forceinline__ float2 get(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
-  static __device__ __forceinline__ uint32_t put(float a, float b) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
-  }
-};
-template <>
-struct Two<__half> {
-  static __device__ __forceinline__ float2 get(uint32_t w) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-  }
-  static __device__ __forceinline__ uint32_t put(float a, float b) {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
-  }
-};
-
-// Four E4M3 codes as two pairs of f16.
-__device__ __forceinline__ void halves(uint32_t w, uint32_t &lo, uint32_t &hi) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
 // Two values as E4M3 codes (nearest-even; not finite: NaN), the first low.
 __device__ __forceinline__ uint32_t codes2(float a, float b) {
   uint16_t r;
@@ -167,7 +140,7 @@ __device__ __forceinline__ void turn_unit(bool key, const Unit &u, uint4 a, uint
   const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 va = Two<T>::get(wa[i]), vb = Two<T>::get(wb[i]);
+    const float2 va = unpack<T>(wa[i]), vb = unpack<T>(wb[i]);
     x[2 * i] = va.x, x[2 * i + 1] = va.y, x[8 + 2 * i] = vb.x, x[8 + 2 * i + 1] = vb.y;
   }
   if (!key || !u.turn1) return;
@@ -449,8 +422,8 @@ __device__ __forceinline__ void store_blocks(const Ap8Params &a, int cta) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t lo, hi;
-              halves(z[e], lo, hi);
-              const float2 x = Two<__half>::get(lo), y = Two<__half>::get(hi);
+              e4m3_halves(z[e], lo, hi);
+              const float2 x = unpack<__half>(lo), y = unpack<__half>(hi);
               z[e] = codes2(x.x * down, x.y * down) | codes2(y.x * down, y.y * down) << 16;
             }
             *at = make_uint4(z[0], z[1], z[2], z[3]);
@@ -567,9 +540,9 @@ __device__ __forceinline__ void turn_queries(const Ap8Params &a, int cta) {
         }
         float x[16];
         turn_unit<T, KIND>(true, u, v[i], w[i], turn, x);
-        *at1 = make_uint4(Two<T>::put(x[0], x[1]), Two<T>::put(x[2], x[3]), Two<T>::put(x[4], x[5]), Two<T>::put(x[6], x[7]));
-        *at2 = make_uint4(Two<T>::put(x[8], x[9]), Two<T>::put(x[10], x[11]), Two<T>::put(x[12], x[13]),
-                          Two<T>::put(x[14], x[15]));
+        *at1 = make_uint4(pack<T>(x[0], x[1]), pack<T>(x[2], x[3]), pack<T>(x[4], x[5]), pack<T>(x[6], x[7]));
+        *at2 = make_uint4(pack<T>(x[8], x[9]), pack<T>(x[10], x[11]), pack<T>(x[12], x[13]),
+                          pack<T>(x[14], x[15]));
       }
     } else {  // by pairs, then single elements
       const bool keep = locate8(c, a.page, p.seq ? p.seq[t] : t, pos, limit, nullptr, page, place);
@@ -726,10 +699,10 @@ __global__ void __launch_bounds__(kReadThreads, kReaders) k_read(const __grid_co
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       uint32_t lo, hi;
-      halves(w[e], lo, hi);
-      const float2 x = Two<__half>::get(lo), y = Two<__half>::get(hi);
-      r[2 * e] = Two<T>::put(x.x * f, x.y * f);
-      r[2 * e + 1] = Two<T>::put(y.x * f, y.y * f);
+      e4m3_halves(w[e], lo, hi);
+      const float2 x = unpack<__half>(lo), y = unpack<__half>(hi);
+      r[2 * e] = pack<T>(x.x * f, x.y * f);
+      r[2 * e + 1] = pack<T>(y.x * f, y.y * f);
     }
     const uint4 r0 = make_uint4(r[0], r[1], r[2], r[3]), r1 = make_uint4(r[4], r[5], r[6], r[7]);
     if (a.wide) {

@@ -25,7 +25,7 @@ struct AtParams {
   int least;    // tiles of a slice, at least
   int bundle;   // rows whose tiles are one item of the list, worked on side by side
   int direct;   // CTAs (a cluster) that take a row between them, or 0: equal slices
-  int shift;    // log2 page_size, or -1: no power of two
+  int shift;    // log2 page_size, or -1: no power of two (16 bits)
   int out16;    // rows of out allow 16-byte stores
   float scale2; // scale * log2 e
   float *ws;    // [ctas][2] partial rows
@@ -86,30 +86,6 @@ __device__ __forceinline__ uint4 load16(const void *p) {
 template <typename T>
 __device__ __forceinline__ constexpr float lift() {
   return Bf16<T>::value ? 0.0f : 7.0f;
-}
-
-// Two values as a pair of T, and what the pair leaves of them.
-template <typename T>
-__device__ __forceinline__ uint32_t pack(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-template <>
-__device__ __forceinline__ uint32_t pack<__half>(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-template <typename T>
-__device__ __forceinline__ float2 unpack(uint32_t w);
-template <>
-__device__ __forceinline__ float2 unpack<__nv_bfloat16>(uint32_t w) {
-  return make_float2(bf16_lo(w), bf16_hi(w));
-}
-template <>
-__device__ __forceinline__ float2 unpack<__half>(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
 // What of a sequence is seen: positions [0, sinks) and [from, len), apart from

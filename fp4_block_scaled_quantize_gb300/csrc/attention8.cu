@@ -140,13 +140,6 @@ struct Layout {
   }
 };
 
-// Four E4M3 codes as two pairs of f16.
-__device__ __forceinline__ void halves(uint32_t w, uint32_t &lo, uint32_t &hi) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-
 // What a warp has to know of a row that it works on: sequence, row, tiles of it
 // in the slice, and whether it begins (1) and ends (2) there.
 struct Row {
@@ -163,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
   const AtParams &a = b.a;
   extern __shared__ __align__(16) char smem8[];
   __shared__ int64_t scan[kWarps + 2];
-  __shared__ int part_sh[kWarps];  // clusters: whether a warp has a part of the row, and if it begins and ends (1, 2) there
+  __shared__ bool part_sh[kWarps];  // clusters: whether a warp has a part of the row
   __shared__ Row queue_sh[kWarps][kQueue];
   const fp4_kv_cache &c = a.p.cache;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -179,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
   int s;
   dependent_wait();
   launch_dependents();
-  if (lane == 0) part_sh[warp] = -1;
+  if (lane == 0) part_sh[warp] = false;
   const int rank = a.direct ? blockIdx.x % a.direct : 0, mine_row = a.direct ? blockIdx.x / a.direct : 0;
   if (a.direct) {
     s = mine_row / rows;
@@ -462,8 +455,8 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t x0, x1, y0, y1;
-            halves(x[j], x0, x1);
-            halves(y[j], y0, y1);
+            e4m3_halves(x[j], x0, x1);
+            e4m3_halves(y[j], y0, y1);
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma(sc[u][n], x0, y0, x1, y1, q[n][i][2 * j], q[n][i][2 * j + 1], __half());
           }
@@ -554,8 +547,8 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
 #pragma unroll
             for (int p = 0; p < 2; ++p) {  // rows g, g + 8: elements 2 p, 2 p + 1 of the word
               uint32_t a0, a1, a2, a3;
-              halves(__byte_perm(v[0][j], v[1][j], p ? 0x7362 : 0x5140), a0, a1);
-              halves(__byte_perm(v[2][j], v[3][j], p ? 0x7362 : 0x5140), a2, a3);
+              e4m3_halves(__byte_perm(v[0][j], v[1][j], p ? 0x7362 : 0x5140), a0, a1);
+              e4m3_halves(__byte_perm(v[2][j], v[3][j], p ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
                 float *d = o[n][2 * (4 * i + j) + p];
@@ -577,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
     float *outs = part_of(warp);
     float4 *stats = st_sh + warp * kCols;
     if (!whole && a.direct) {
-      if (lane == 0) part_sh[warp] = mine.ends;
+      if (lane == 0) part_sh[warp] = true;
       copies_wait<0>();
       __syncwarp();
     } else if (!whole) {
@@ -635,8 +628,7 @@ __global__ void __launch_bounds__(kThreads, per_sm8(DP)) k_attention8(const __gr
   __syncthreads();
   const int row = mine_row - s * rows, kvh = row / a.groups, head0 = kvh * a.share + (row - kvh * a.groups) * kCols;
   const int heads = min(kCols, (kvh + 1) * a.share - head0);
-  const int have = part_sh[lane % kWarps];
-  const uint32_t parts = __ballot_sync(~0u, have >= 0) & ((1u << kWarps) - 1);
+  const uint32_t parts = __ballot_sync(~0u, part_sh[lane % kWarps]) & ((1u << kWarps) - 1);
   const bool partial = parts != 0 && a.direct > 1;
   if (parts)
     for (int item = threadIdx.x; item < heads * (DP / 8); item += kThreads) {
@@ -789,7 +781,6 @@ fp4_status launch_decode_attention8(const fp4_attention8_params &p, cudaStream_t
   a.share = a.p.heads / c.kv_heads;
   const int nt = nt_of(a.share, dp_of(c.head_dim));
   a.groups = (a.share + 8 * nt - 1) / (8 * nt);
-  a.shift = log2_or(c.page_size, -1);
   b.page = divisor(c.page_size);
   b.block = divisor(b.s.block);
   b.k_page = (int)c.k_page, b.k_place = (int)c.k_place, b.v_page = (int)c.v_page, b.v_place = (int)c.v_place;
