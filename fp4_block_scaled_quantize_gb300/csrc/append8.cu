@@ -14,8 +14,11 @@
 // Measured in a graph: 192 tokens of 192 sequences, 16 + 2 x 16 heads of 64 in
 // blocks of 8 4.1 us, one token 3.6; 8191 prompt tokens of 32 + 2 x 8 heads of 128
 // in blocks of 64 51.1 us (3.6 TB/s, 54% of a copy's rate; without queries 27: some
-// 700 instructions of a warp a head and 64 tokens, 16 warps an SM); reading 100003
-// tokens back 97.5 us (6.3 TB/s, 93%), 300 2.1 us.
+// 700 instructions of a warp a head and 64 tokens, 16 warps an SM by 128 registers, of
+// which the forms that hold two rows spill 120 - 128 bytes); rows whose rotated part
+// is not whole pieces go element by element (8000 tokens, heads of 80 with 40 rotated
+// 283 us, with 32 or 80 49); reading 100003 tokens back 97.5 us (6.3 TB/s, 93%), 300
+// 2.1 us.
 //
 // A rotated key is rounded to binary32 before it is rounded to its code: about one
 // code in a million is the other neighbour of a number that lies within 2^-20 of

@@ -33,12 +33,14 @@
 // share goes to the workspace, for the join of attention.cuh in a second,
 // dependent launch, in slice order, so results repeat exactly.
 // Measured in a graph, 32 heads over 8 of 128, BF16: 64 sequences of up to 16384
-// positions 180 - 187 us (85 - 88% of a copy's rate; copies alone 190, the work
-// alone on a tile that stays 142); one of 131071 57 us, of 16000 21 (6.5 TB/s
-// between them; some 16 us are launch, search, last tiles and join); one of 300
-// 6.9; 40 windows of 4096 with 20 first positions 67.  Heads of 64 (16, 64
-// sequences of 16384) 430 us for 317 at a copy's rate: as many instructions a
-// position as heads of 128, half the bytes; of 256 334.
+// positions 179 - 182 us (87 - 89% of a copy's rate; the kernel's copies without its
+// work 174; pages of 24 183, of 8 188, of 20 in blocks of 4 192); one of 131071 57
+// us (copies 56), of 65000 38, of 16000 20, so that some 15 us do not grow with the
+// length, with or without the work; one of 300 7.0; 40 windows of 4096 with 20 first
+// positions 65 - 67 (copies 63).  Heads of 64 (16, 64 sequences of 16384) 433 us for
+// 317 at a copy's rate: as many instructions a position as heads of 128, half the
+// bytes; of 256 333.  Query heads that need a second pass over a key head (32
+// sequences of 4000): of 256, 8 heads 25.3, 16 heads 28.1.
 //
 // Layout is that of attention16.cuh:
 //   S^T = K Q^T   lane (g, t) reads pieces 64 i + 16 t of keys g, g + 8

@@ -16,7 +16,7 @@
 // read: lengths, rooms, how many are free, and, where the call also gives out pages
 // from those places of the stack, what goes back.
 // Measured in a graph, two calls, pages given back and taken again: 256 sequences
-// by a token 6.7 us (by bisection, with the state written by the last CTA to
+// by a token 6.8 us (by bisection, with the state written by the last CTA to
 // finish, 12.6); 96 prompts of 250000 tokens in all 15.0.  Two empty launches take
 // 1.2, with the loads 1.9, with the scans 3.6.
 #include "serve.cuh"

@@ -448,6 +448,9 @@ fp4_status fp4_kv_append(const fp4_append_params *p, void *stream);
  * fp4_status_sync reports FP4_ERR_INVALID_ARG.
  * workspace: fp4_decode_attention_workspace() bytes, 16-byte aligned, read
  * and written by this call only (one per call in flight).
+ * Set the struct to zero before it is filled: `sinks` lies where it had padding
+ * before there were first positions, so what a caller built without it leaves
+ * there is read as their number by calls with a window.
  * Alignment: every stride, pointer and head_dim of q, k, v in multiples of 16
  * bytes (8 elements); out its element size. */
 typedef struct {
