@@ -540,7 +540,7 @@ def page_plan(new, lengths, page_table, room, pool, page_size, tokens=None, stre
         _PLAN.pack(new.data_ptr(), lengths.data_ptr(), room.data_ptr(), page_table.data_ptr(),
                    step if seqs > 1 else 0, pool.data_ptr(), pool.shape[0] - 2, offsets, seq, pos, slot,
                    -1 if tokens is None else tokens, seqs, wide, page_size),
-        0x7FFFFFFFFFFFFFFF if max_len is None else max_len, _handle(stream, dev))
+        0x7FFFFFFFFFFFFFFF if max_len is None else min(max_len, 0x7FFFFFFFFFFFFFFF), _handle(stream, dev))
     if code:
         raise FP4Error(code, "fp4_page_plan")
     return made

@@ -114,3 +114,21 @@ def test_a_cache_keeps_its_max_len(dtype):
     y = layer(x[:2], cache, pos)
     assert pos.tolist() == [1, -1] and cache.lengths.tolist() == [2, 100] and not y[1].any()
     assert fq.fp4_status_sync() == fq.FP4_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("most,given", [(10, [0, 9]), (2 ** 64 + 5, [12, 9])])
+def test_the_general_way(most, given):
+    """Another stream; a limit that no integer of the library holds is none."""
+    need_gpu()
+    fq.fp4_status_sync()
+    st = ints([0, 0]), torch.full((2, 4), -1, dtype=I32, device="cuda"), ints([0, 0])
+    pool, new = fq.page_pool(8), ints([12, 9])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for stream in (s, None):
+        got = fq.page_plan(new, *st, pool, 4, tokens=21, max_len=most, stream=stream)
+        torch.cuda.synchronize()
+        assert st[0].tolist() == given and got.pos.tolist() == list(range(12)) * bool(given[0]) + [-1] * 12 * (not given[0]) + list(range(9))
+        assert (fq.fp4_status_sync() == fq.FP4_OK) == (given[0] == 12)
+        fq.page_plan(ints([-12, -9]), *st, pool, 4)
