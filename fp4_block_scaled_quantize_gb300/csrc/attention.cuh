@@ -89,8 +89,8 @@ __device__ __forceinline__ constexpr float lift() {
 }
 
 // What of a sequence is seen: positions [0, sinks) and [from, len), apart from
-// each other (sinks is 0 where they meet, and without SINKS).  Its tiles are those of the first
-// positions, then those of the others, which start at base.
+// each other (sinks is 0 where they meet, and without SINKS).  Its tiles are those
+// of the first positions, then those of the others, which start at base.
 struct Span {
   int from, len, base, sinks, first, tiles;  // first: tiles of the first positions
   // the seen positions [lo, hi) of tile i and the position where it starts
